@@ -1,0 +1,635 @@
+"""The token operators as they are measured: the norm and rotary position of
+queries and keys, attention over documents, and the gated scan.
+
+A network that predicts Gaussians works on ragged batches of tokens, one
+document per scene; these are its mixing operators, at the sizes such networks
+have in training (long packed batches, forward and backward) and in serving
+(one new token per request).  ``run`` computes them in their plain form, or
+calls the framework where ``own`` is true; ``exact`` computes them in 64 bits.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+LIMIT = 1 << 28          # scores held at a time by the plain form
+
+
+# ---------------------------------------------------------------------------
+# Cases
+# ---------------------------------------------------------------------------
+def _qk(name, way, rows, heads_q, heads_k, dim, rotary, interleaved, dtype, far):
+    """way: "fwd" or "train" (forward and backward)."""
+    return {"name": name, "op": "qk", "way": way, "rows": rows, "heads_q": heads_q,
+            "heads_k": heads_k, "dim": dim, "rotary": rotary, "interleaved": interleaved,
+            "dtype": dtype, "far": far}
+
+
+def _attention(name, way, docs, tokens, heads_q, heads_k, dim, dtype, causal=True, prefix=False,
+               slopes=False, softcap=0.0):
+    """way: "step" (one query token per document over its cached keys), "fwd"
+    or "train"; tokens: keys of all documents together."""
+    return {"name": name, "op": "attention", "way": way, "docs": docs, "tokens": tokens,
+            "heads_q": heads_q, "heads_k": heads_k, "dim": dim, "dtype": dtype,
+            "causal": causal, "prefix": prefix, "slopes": slopes, "softcap": softcap}
+
+
+def _scan(name, way, docs, tokens, channels, dtype, coupled):
+    """way: "step" (one token per document), "fwd" or "train"."""
+    return {"name": name, "op": "scan", "way": way, "docs": docs, "tokens": tokens,
+            "channels": channels, "dtype": dtype, "coupled": coupled}
+
+
+def listed():
+    return [
+        # eight requests, one new token each, positions deep in a long context
+        _qk("qk_step", "fwd", 8, 16, 4, 128, 128, False, "bf16", 65536),
+        # a packed training batch, or a long prompt
+        _qk("qk_fwd_16k", "fwd", 16384, 16, 4, 128, 128, False, "bf16", 16384),
+        # training in the framework's own type, part of the head rotated, an odd batch
+        _qk("qk_train_part", "train", 6007, 12, 12, 96, 64, True, "fp32", 8192),
+        # few requests with long caches: one token each, split over the keys
+        _attention("attn_step_long", "step", 4, 120001, 16, 4, 128, "bf16", softcap=30.0),
+        # many requests with caches of many lengths
+        _attention("attn_step_many", "step", 64, 100003, 8, 8, 64, "fp16", slopes=True),
+        # scenes of many sizes packed into one small batch, every token sees its scene
+        _attention("attn_fwd_docs", "fwd", 24, 3001, 8, 8, 64, "bf16", causal=False),
+        # one long causal document: the largest forward
+        _attention("attn_fwd_long", "fwd", 1, 16384, 16, 4, 128, "bf16"),
+        # a training batch with prefixes seen whole and a distance bias
+        _attention("attn_train_prefix", "train", 6, 4099, 8, 2, 64, "fp16", prefix=True,
+                   slopes=True),
+        # the largest training pass: two long documents, capped scores
+        _attention("attn_train_long", "train", 2, 16384, 16, 4, 128, "bf16", softcap=30.0),
+        # thirty-two requests, one token each, the state carried on
+        _scan("scan_step", "step", 32, 32, 2048, "bf16", True),
+        # one very long sequence
+        _scan("scan_fwd_long", "fwd", 1, 65536, 2048, "bf16", True),
+        # a training batch in the framework's own type
+        _scan("scan_train", "train", 12, 20011, 1024, "fp32", False),
+    ]
+
+
+def _spread(rng, lo, hi):
+    """A whole number of [lo, hi], spread over its logarithm."""
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 1)))))))
+
+
+def draw(rng):
+    op = rng.choice(("qk", "attention", "attention", "scan"))
+    if op == "qk":
+        heads_k = rng.choice((1, 2, 4, 8))
+        dim = rng.choice((64, 96, 128))
+        return _nameless(_qk("", rng.choice(("fwd", "train")), _spread(rng, 1, 16384),
+                             heads_k * rng.choice((1, 2, 4)), heads_k, dim,
+                             rng.choice((dim, dim // 2)), rng.random() < 0.5,
+                             rng.choice(("fp32", "bf16", "fp16")),
+                             _spread(rng, 1024, 65536)))
+    if op == "scan":
+        way = rng.choice(("step", "fwd", "train"))
+        docs = _spread(rng, 1, 64)
+        tokens = docs if way == "step" else max(docs, _spread(rng, 64, 32768))
+        return _nameless(_scan("", way, docs, tokens, 8 * _spread(rng, 8, 256),
+                               rng.choice(("fp32", "bf16", "fp16")), rng.random() < 0.5))
+    way = rng.choice(("step", "fwd", "train"))
+    heads_k = rng.choice((1, 2, 4))
+    docs = _spread(rng, 1, 64 if way == "step" else 32)
+    tokens = max(docs, _spread(rng, 64, 120000 if way == "step" else 8192))
+    causal = way == "step" or rng.random() < 0.7
+    return _nameless(_attention("", way, docs, tokens, heads_k * rng.choice((1, 2, 4)), heads_k,
+                                rng.choice((64, 96, 128)), rng.choice(("bf16", "fp16")), causal,
+                                causal and way != "step" and rng.random() < 0.5,
+                                rng.random() < 0.5, rng.choice((0.0, 30.0))))
+
+
+def _nameless(case):
+    del case["name"]
+    return case
+
+
+def _lengths(docs, tokens):
+    """Lengths of the documents: uneven, at least 1, tokens in all."""
+    if tokens == docs:
+        return [1] * docs
+    rng = random.Random(docs * 1000003 + tokens)
+    w = [0.2 + rng.random() ** 2 for _ in range(docs)]
+    free, total = tokens - docs, sum(w)
+    n = [1 + int(free * x / total) for x in w]
+    n[0] += tokens - sum(n)
+    return n
+
+
+def _prefix(case, lengths):
+    return [n // 4 for n in lengths] if case["prefix"] else [0] * len(lengths)
+
+
+def work(case):
+    size = 4 if case["dtype"] == "fp32" else 2
+    if case["op"] == "qk":
+        n = case["rows"] * (case["heads_q"] + case["heads_k"]) * case["dim"]
+        # forward: x in, y out; training: dy in and dx out as well
+        return {"bytes": n * size * (4 if case["way"] == "train" else 2) + 4 * case["rows"],
+                "flops": n * (25 if case["way"] == "train" else 10)}
+    if case["op"] == "scan":
+        n = case["tokens"] * case["channels"]
+        states = 2 * case["docs"] * case["channels"] * 4
+        # forward: gate and x in, y out; training: dy in, both gradients out as well
+        return {"bytes": n * size * (6 if case["way"] == "train" else 3) +
+                states * (2 if case["way"] == "train" else 1),
+                "flops": n * (25 if case["way"] == "train" else 10)}
+    lengths = _lengths(case["docs"], case["tokens"])
+    hq, hk, dim = case["heads_q"], case["heads_k"], case["dim"]
+    if case["way"] == "step":
+        return {"bytes": (2 * case["tokens"] * hk + 2 * case["docs"] * hq) * dim * size,
+                "flops": 4 * case["tokens"] * hq * dim}
+    pairs = 0
+    for n, p in zip(lengths, _prefix(case, lengths)):
+        # row i sees keys up to i, and the prefix
+        pairs += n * (n + 1) // 2 + p * (p - 1) // 2 if case["causal"] else n * n
+    elements = case["tokens"] * dim * (2 * hq + 2 * hk)      # q, k, v in, o out
+    if case["way"] == "train":
+        elements += case["tokens"] * dim * (2 * hq + 2 * hk)  # do in, dq, dk, dv out
+        return {"bytes": elements * size, "flops": 14 * pairs * hq * dim}
+    return {"bytes": elements * size, "flops": 4 * pairs * hq * dim}
+
+
+# ---------------------------------------------------------------------------
+# What a program has in hand
+# ---------------------------------------------------------------------------
+def prepare(case, seed):
+    state = {"case": dict(case)}
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    {"qk": _prepare_qk, "attention": _prepare_attention,
+     "scan": _prepare_scan}[case["op"]](state, case, gen)
+    if own:
+        {"qk": _plan_qk, "attention": _plan_attention, "scan": _plan_scan}[case["op"]](state, case)
+    return state
+
+
+def _normal(gen, dtype, *shape):
+    return torch.randn(shape, generator=gen, device="cuda", dtype=torch.float32).to(TYPES[dtype])
+
+
+def _ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def _starts(lengths):
+    out, at = [], 0
+    for n in lengths:
+        out.append(at)
+        at += n
+    return out
+
+
+def _prepare_qk(state, case, gen):
+    rows, hq, hk, dim = case["rows"], case["heads_q"], case["heads_k"], case["dim"]
+    # queries and keys are columns of one projection that holds the values too
+    fused = _normal(gen, case["dtype"], rows, hq + 2 * hk, dim)
+    state["q"], state["k"] = fused[:, :hq], fused[:, hq:hq + hk]
+    state["positions"] = torch.randint(0, case["far"], (rows,), generator=gen, device="cuda",
+                                       dtype=torch.int32)
+    half = case["rotary"] // 2
+    # base 10000, stretched fourfold for a context longer than it was made for
+    freq = 10000.0 ** (-torch.arange(half, dtype=torch.float64) / half) / 4.0
+    state["inv_freq"] = freq.to(torch.float32).cuda()
+    state["wq"] = 1.0 + 0.1 * torch.randn(dim, generator=gen, device="cuda")
+    state["wk"] = 1.0 + 0.1 * torch.randn(dim, generator=gen, device="cuda")
+    state["eps"], state["amplitude"] = 1e-6, 1.1
+    if case["way"] == "train":
+        state["dq_out"] = _normal(gen, case["dtype"], rows, hq, dim)
+        state["dk_out"] = _normal(gen, case["dtype"], rows, hk, dim)
+
+
+def _prepare_attention(state, case, gen):
+    hq, hk, dim, dtype = case["heads_q"], case["heads_k"], case["dim"], case["dtype"]
+    lengths = _lengths(case["docs"], case["tokens"])
+    state["k_lens"] = lengths
+    state["prefixes"] = _prefix(case, lengths)
+    if case["way"] == "step":
+        # a cache with room for the longest request in every slot
+        room = (max(lengths) + 255) // 256 * 256
+        state["q_lens"] = [1] * len(lengths)
+        state["k_starts"] = [i * room for i in range(len(lengths))]
+        state["q"] = _normal(gen, dtype, len(lengths), hq, dim)
+        state["k"] = _normal(gen, dtype, len(lengths) * room, hk, dim)
+        state["v"] = _normal(gen, dtype, len(lengths) * room, hk, dim)
+    else:
+        state["q_lens"] = lengths
+        state["k_starts"] = _starts(lengths)
+        fused = _normal(gen, dtype, case["tokens"], hq + 2 * hk, dim)
+        state["q"], state["k"], state["v"] = (fused[:, :hq], fused[:, hq:hq + hk],
+                                              fused[:, hq + hk:])
+    state["q_starts"] = _starts(state["q_lens"])
+    state["scale"] = 1.0 / math.sqrt(dim)
+    state["slopes"] = None
+    if case["slopes"]:
+        state["slopes"] = 2.0 ** (-8.0 * (torch.arange(hq, device="cuda", dtype=torch.float32) + 1)
+                                  / hq)
+    if case["way"] == "train":
+        state["do"] = _normal(gen, dtype, case["tokens"], hq, dim)
+
+
+def _prepare_scan(state, case, gen):
+    tokens, channels, docs = case["tokens"], case["channels"], case["docs"]
+    state["lens"] = _lengths(docs, tokens)
+    state["starts"] = _starts(state["lens"])
+    # gate and input are the halves of one projection; gates mostly open,
+    # memories of a few to some hundred tokens
+    fused = torch.randn((tokens, 2 * channels), generator=gen, device="cuda")
+    fused[:, :channels] = fused[:, :channels] * 1.5 + 2.5
+    fused = fused.to(TYPES[case["dtype"]])
+    state["gate"], state["x"] = fused[:, :channels], fused[:, channels:]
+    state["state"] = torch.randn((docs, channels), generator=gen, device="cuda")
+    if case["way"] == "train":
+        state["dy"] = _normal(gen, case["dtype"], tokens, channels)
+        state["dstate"] = torch.randn((docs, channels), generator=gen, device="cuda")
+
+
+# ---------------------------------------------------------------------------
+# The framework's plans: outputs, workspaces and descriptions kept by a program
+# ---------------------------------------------------------------------------
+def _space(size):
+    """A 256-byte aligned workspace of size bytes."""
+    return torch.empty((max(size, 256),), dtype=torch.uint8, device="cuda")
+
+
+def _plan_qk(state, case):
+    from differentiable_rasterization_amd import raster
+    s = state
+    s["cfg"] = raster.qk_config(s["q"].dtype, case["heads_q"], case["heads_k"], case["dim"],
+                                rotary_dim=case["rotary"], interleaved=case["interleaved"],
+                                norm=True, eps=s["eps"], amplitude=s["amplitude"])
+    dense = lambda t: torch.empty(t.shape, dtype=t.dtype, device="cuda")
+    s["out"] = [dense(s["q"]), dense(s["k"])]
+    s["in_heads"] = [raster.heads(s["q"]), raster.heads(s["k"])]
+    s["out_heads"] = [raster.heads(t) for t in s["out"]]
+    if case["way"] == "train":
+        s["grads"] = [dense(s["q"]), dense(s["k"]), torch.empty_like(s["wq"]),
+                      torch.empty_like(s["wk"])]
+        s["grad_heads"] = [raster.heads(t) for t in s["grads"][:2]]
+        s["dout_heads"] = [raster.heads(s["dq_out"]), raster.heads(s["dk_out"])]
+        s["ws_bytes"] = raster.gs_qk_norm_rope_bwd_workspace_size(s["cfg"], case["rows"])
+        s["ws"] = _space(s["ws_bytes"])
+
+
+def _plan_attention(state, case):
+    from differentiable_rasterization_amd import raster
+    s = state
+    s["cfg"] = raster.attention_config(s["q"].dtype, case["heads_q"], case["heads_k"],
+                                       case["dim"], s["scale"], causal=case["causal"],
+                                       softcap=case["softcap"], slopes=s["slopes"])
+    s["docs"] = raster.documents(_ints(s["q_starts"]), _ints(s["q_lens"]),
+                                 _ints(s["k_starts"]), _ints(s["k_lens"]),
+                                 prefix=_ints(s["prefixes"]) if case["prefix"] else None,
+                                 max_q_len=max(s["q_lens"]), max_k_len=max(s["k_lens"]))
+    s["rows"] = (s["q"].shape[0], s["k"].shape[0])
+    dense = lambda t: torch.empty(t.shape, dtype=t.dtype, device="cuda")
+    s["o"] = dense(s["q"])
+    s["qkvo"] = [raster.heads(t) for t in (s["q"], s["k"], s["v"], s["o"])]
+    s["lse"] = torch.empty((case["heads_q"], s["q"].shape[0]), device="cuda")
+    size = raster.gs_attention_fwd_workspace_size(s["cfg"], s["docs"], *s["rows"])
+    if case["way"] == "train":
+        s["grads"] = [dense(s["q"]), dense(s["k"]), dense(s["v"])]
+        s["grad_heads"] = [raster.heads(t) for t in s["grads"]]
+        s["do_heads"] = raster.heads(s["do"])
+        size = max(size, raster.gs_attention_bwd_workspace_size(s["cfg"], s["docs"], *s["rows"]))
+    s["ws"], s["ws_bytes"] = _space(size), size
+
+
+def _plan_scan(state, case):
+    from differentiable_rasterization_amd import raster
+    s = state
+    s["cfg"] = raster.scan_config(s["x"].dtype, case["channels"], coupled=case["coupled"])
+    s["docs"] = raster.documents(_ints(s["starts"]), _ints(s["lens"]), max_q_len=max(s["lens"]))
+    dense = lambda t: torch.empty(t.shape, dtype=t.dtype, device="cuda")
+    s["out"] = [dense(s["x"]), torch.empty_like(s["state"])]
+    s["io"] = [raster.rows(t) for t in (s["gate"], s["x"], s["out"][0])]
+    size = raster.gs_gated_scan_fwd_workspace_size(s["cfg"], s["docs"], case["tokens"])
+    s["saved"] = None
+    if case["way"] == "train":
+        s["saved"] = _space(raster.gs_gated_scan_saved_size(s["cfg"], s["docs"], case["tokens"]))
+        s["grads"] = [dense(s["gate"]), dense(s["x"]), torch.empty_like(s["state"])]
+        s["grad_rows"] = [raster.rows(t) for t in (s["dy"], s["grads"][0], s["grads"][1])]
+        size = max(size, raster.gs_gated_scan_bwd_workspace_size(s["cfg"], s["docs"],
+                                                                 case["tokens"]))
+    s["ws"], s["ws_bytes"] = _space(size), size
+
+
+# ---------------------------------------------------------------------------
+# One pass
+# ---------------------------------------------------------------------------
+def run(state):
+    op = state["case"]["op"]
+    if own:
+        return {"qk": _own_qk, "attention": _own_attention, "scan": _own_scan}[op](state)
+    return {"qk": _plain_qk, "attention": _plain_attention, "scan": _plain_scan}[op](state)
+
+
+def _own_qk(s):
+    from differentiable_rasterization_amd import raster
+    rows = s["case"]["rows"]
+    raster.gs_qk_norm_rope_fwd(s["cfg"], rows, s["positions"], s["inv_freq"], s["wq"], s["wk"],
+                               *s["in_heads"], *s["out_heads"])
+    if s["case"]["way"] == "fwd":
+        return s["out"]
+    raster.gs_qk_norm_rope_bwd(s["cfg"], rows, s["positions"], s["inv_freq"], s["wq"], s["wk"],
+                               *s["in_heads"], *s["dout_heads"], *s["grad_heads"], s["grads"][2],
+                               s["grads"][3], s["ws"], s["ws_bytes"])
+    return s["out"] + s["grads"]
+
+
+def _own_attention(s):
+    from differentiable_rasterization_amd import raster
+    train = s["case"]["way"] == "train"
+    raster.gs_attention_fwd(s["cfg"], s["docs"], *s["rows"], *s["qkvo"],
+                            s["lse"] if s["case"]["way"] != "step" else None, s["ws"],
+                            s["ws_bytes"])
+    if s["case"]["way"] == "step":
+        return s["o"]
+    if not train:
+        return [s["o"], s["lse"]]
+    raster.gs_attention_bwd(s["cfg"], s["docs"], *s["rows"], *s["qkvo"], s["lse"], s["do_heads"],
+                            *s["grad_heads"], s["ws"], s["ws_bytes"])
+    return [s["o"], s["lse"]] + s["grads"]
+
+
+def _own_scan(s):
+    from differentiable_rasterization_amd import raster
+    rows = s["case"]["tokens"]
+    raster.gs_gated_scan_fwd(s["cfg"], s["docs"], rows, s["io"][0], s["io"][1], s["state"],
+                             s["io"][2], s["out"][1], s["saved"], s["ws"], s["ws_bytes"])
+    if s["case"]["way"] != "train":
+        return s["out"]
+    raster.gs_gated_scan_bwd(s["cfg"], s["docs"], rows, s["io"][0], s["io"][1], s["state"],
+                             s["saved"], s["grad_rows"][0], s["dstate"], s["grad_rows"][1],
+                             s["grad_rows"][2], s["grads"][2], s["ws"], s["ws_bytes"])
+    return s["out"] + s["grads"]
+
+
+# ---------------------------------------------------------------------------
+# The plain forms, in 32 bits
+# ---------------------------------------------------------------------------
+def _pairs(x, interleaved):
+    half = x.shape[-1] // 2
+    return (x[..., 0::2], x[..., 1::2]) if interleaved else (x[..., :half], x[..., half:])
+
+
+def _joined(a, b, interleaved):
+    return torch.stack((a, b), -1).flatten(-2) if interleaved else torch.cat((a, b), -1)
+
+
+def _turned(x, cos, sin, rotary, interleaved):
+    a, b = _pairs(x[..., :rotary], interleaved)
+    y = _joined(a * cos - b * sin, b * cos + a * sin, interleaved)
+    return torch.cat((y, x[..., rotary:]), -1)
+
+
+def _plain_qk(s):
+    c = s["case"]
+    # the angle alone is formed in 64 bits: in 32 its rounding at far positions
+    # would be the whole error
+    angle = s["positions"].double()[:, None, None] * s["inv_freq"].double()
+    angle = torch.remainder(angle, 2.0 * math.pi).float()
+    cos, sin = torch.cos(angle) * s["amplitude"], torch.sin(angle) * s["amplitude"]
+    outs, grads, sums = [], [], []
+    for x, w, dy in ((s["q"], s["wq"], s.get("dq_out")), (s["k"], s["wk"], s.get("dk_out"))):
+        x32 = x.float()
+        r = torch.rsqrt((x32 * x32).mean(-1, keepdim=True) + s["eps"])
+        outs.append(_turned(x32 * r * w, cos, sin, c["rotary"], c["interleaved"]).to(x.dtype))
+        if dy is not None:
+            dn = _turned(dy.float(), cos, -sin, c["rotary"], c["interleaved"])
+            sums.append((dn * x32 * r).sum((0, 1)))
+            g = dn * w
+            dx = r * (g - x32 * (r * r) * (g * x32).mean(-1, keepdim=True))
+            grads.append(dx.to(x.dtype))
+    return outs + grads + sums
+
+
+def _bias(s, heads, i, lq, lk):
+    """(seen, distance bias) of query rows i of a document: [lq, lk], [heads, lq, lk]."""
+    c = s["case"]
+    rows = (torch.arange(lq, device="cuda") + (lk - lq))[:, None]
+    cols = torch.arange(lk, device="cuda")[None, :]
+    seen = None
+    if c["causal"]:
+        seen = (cols <= rows) | (cols < s["prefixes"][i])
+    bias = None
+    if s["slopes"] is not None:
+        bias = -s["slopes"][heads][:, None, None] * (rows - cols).abs().float()
+    return seen, bias
+
+
+def _plain_attention(s):
+    c = s["case"]
+    group = c["heads_q"] // c["heads_k"]
+    o = torch.empty(s["q"].shape, dtype=s["q"].dtype, device="cuda")
+    lse = torch.empty((c["heads_q"], s["q"].shape[0]), device="cuda")
+    train = c["way"] == "train"
+    if train:
+        grads = [torch.empty(s[t].shape, dtype=s[t].dtype, device="cuda") for t in "qkv"]
+    for i, (q0, lq, k0, lk) in enumerate(zip(s["q_starts"], s["q_lens"], s["k_starts"],
+                                             s["k_lens"])):
+        step = c["heads_k"] if c["heads_q"] * lq * lk <= LIMIT else 1
+        for h in range(0, c["heads_k"], step):
+            hk, hq = slice(h, h + step), slice(h * group, (h + step) * group)
+            to = lambda t, a, n, hs: t[a:a + n, hs].float().permute(1, 0, 2).contiguous()
+            q = to(s["q"], q0, lq, hq)
+            k = to(s["k"], k0, lk, hk).repeat_interleave(group, 0)
+            v = to(s["v"], k0, lk, hk).repeat_interleave(group, 0)
+            score = torch.matmul(q, k.transpose(1, 2).contiguous()) * s["scale"]
+            slope = None
+            if c["softcap"]:
+                t = torch.tanh(score / c["softcap"])
+                score = t * c["softcap"]
+                slope = 1.0 - t * t
+            seen, bias = _bias(s, hq, i, lq, lk)
+            if bias is not None:
+                score = score + bias
+            if seen is not None:
+                score = torch.where(seen, score, float("-inf"))
+            top = score.amax(-1, keepdim=True)
+            p = torch.exp(score - top)
+            total = p.sum(-1, keepdim=True)
+            p = p / total
+            out = torch.matmul(p, v)
+            o[q0:q0 + lq, hq] = out.permute(1, 0, 2).to(o.dtype)
+            lse[hq, q0:q0 + lq] = (top + torch.log(total))[..., 0]
+            if not train:
+                continue
+            do = to(s["do"], q0, lq, hq)
+            dv = torch.matmul(p.transpose(1, 2).contiguous(), do)
+            dp = torch.matmul(do, v.transpose(1, 2).contiguous())
+            ds = p * (dp - (do * out).sum(-1, keepdim=True)) * s["scale"]
+            if slope is not None:
+                ds = ds * slope
+            dq = torch.matmul(ds, k)
+            dk = torch.matmul(ds.transpose(1, 2).contiguous(), q)
+            shared = lambda t: t.reshape(step, group, lk, -1).sum(1).permute(1, 0, 2)
+            grads[0][q0:q0 + lq, hq] = dq.permute(1, 0, 2).to(o.dtype)
+            grads[1][k0:k0 + lk, hk] = shared(dk).to(o.dtype)
+            grads[2][k0:k0 + lk, hk] = shared(dv).to(o.dtype)
+    if c["way"] == "step":
+        return o
+    return [o, lse] + (grads if train else [])
+
+
+def _composed(a, b):
+    """h_t = a_t h_{t-1} + b_t from h = 0 along the first dimension, by doubling."""
+    a, b = a.clone(), b.clone()
+    step, n = 1, a.shape[0]
+    while step < n:
+        b = torch.cat((b[:step], b[step:] + a[step:] * b[:-step]))
+        a = torch.cat((a[:step], a[step:] * a[:-step]))
+        step *= 2
+    return b
+
+
+def _plain_scan(s):
+    c = s["case"]
+    x, f = s["x"].float(), s["gate"].float()
+    a, z = torch.sigmoid(f), torch.sigmoid(-f)
+    u = z * x if c["coupled"] else x.clone()
+    first = torch.tensor(s["starts"], device="cuda")
+    last = first + torch.tensor(s["lens"], device="cuda") - 1
+    # a document's first step takes its state in, and nothing of the one before
+    u[first] += a[first] * s["state"]
+    carry = a.clone()
+    carry[first] = 0.0
+    h = _composed(carry, u)
+    out = [h.to(s["x"].dtype), h[last].clone()]
+    if c["way"] != "train":
+        return out
+    before = torch.cat((h[:1], h[:-1]))
+    before[first] = s["state"]
+    g = s["dy"].float()
+    g[last] += s["dstate"]
+    back = torch.cat((carry[1:], carry[:1] * 0.0))
+    g = _composed(back.flip(0), g.flip(0)).flip(0)
+    dx = g * z if c["coupled"] else g
+    df = g * (before - x if c["coupled"] else before) * a * z
+    return out + [df.to(s["x"].dtype), dx.to(s["x"].dtype), a[first] * g[first]]
+
+
+# ---------------------------------------------------------------------------
+# From the definitions, in 64 bits
+# ---------------------------------------------------------------------------
+def exact(case, seed):
+    state = prepare(case, seed)
+    return {"qk": _exact_qk, "attention": _exact_attention, "scan": _exact_scan}[case["op"]](state)
+
+
+def _exact_qk(s):
+    c = s["case"]
+    pairs = c["rotary"] // 2
+    # the turned pairs as complex numbers
+    turn = torch.polar(torch.full((c["rows"], 1, pairs), s["amplitude"], dtype=torch.float64,
+                                  device="cuda"),
+                       torch.remainder(s["positions"].double()[:, None, None] *
+                                       s["inv_freq"].double(), 2.0 * math.pi))
+    if c["interleaved"]:
+        order = torch.arange(c["rotary"], device="cuda").reshape(pairs, 2)
+    else:
+        order = torch.arange(c["rotary"], device="cuda").reshape(2, pairs).T
+    outs, grads, sums = [], [], []
+    for x, w, dy in ((s["q"], s["wq"], s.get("dq_out")), (s["k"], s["wk"], s.get("dk_out"))):
+        x64 = x.double().requires_grad_(dy is not None)
+        w64 = w.double().requires_grad_(dy is not None)
+        n = x64 / torch.sqrt(x64.pow(2).sum(-1, keepdim=True) / c["dim"] + s["eps"]) * w64
+        z = torch.view_as_complex(n[..., order].contiguous()) * turn
+        y = n.clone()
+        y[..., order.flatten()] = torch.view_as_real(z).flatten(-2)
+        outs.append(y.detach())
+        if dy is not None:
+            gx, gw = torch.autograd.grad(y, (x64, w64), dy.double())
+            grads.append(gx)
+            sums.append(gw)
+    return outs + grads + sums
+
+
+def _exact_attention(s):
+    c = s["case"]
+    train = c["way"] == "train"
+    group = c["heads_q"] // c["heads_k"]
+    o = torch.zeros(s["q"].shape, dtype=torch.float64, device="cuda")
+    lse = torch.zeros((c["heads_q"], s["q"].shape[0]), dtype=torch.float64, device="cuda")
+    grads = [torch.zeros(s[t].shape, dtype=torch.float64, device="cuda") for t in "qkv"]
+    for i in range(len(s["q_lens"])):
+        rq = slice(s["q_starts"][i], s["q_starts"][i] + s["q_lens"][i])
+        rk = slice(s["k_starts"][i], s["k_starts"][i] + s["k_lens"][i])
+        at = torch.arange(s["q_lens"][i], device="cuda") + s["k_lens"][i] - s["q_lens"][i]
+        away = at[:, None] - torch.arange(s["k_lens"][i], device="cuda")[None, :]
+        hidden = away < 0
+        if s["prefixes"][i]:
+            hidden[:, :s["prefixes"][i]] = False
+        for h in range(c["heads_q"]):
+            q, k, v = (s["q"][rq, h].double(), s["k"][rk, h // group].double(),
+                       s["v"][rk, h // group].double())
+            if train:
+                q, k, v = (t.requires_grad_() for t in (q, k, v))
+            x = (q @ k.T) * s["scale"]
+            if c["softcap"]:
+                x = c["softcap"] * torch.tanh(x / c["softcap"])
+            if s["slopes"] is not None:
+                x = x - float(s["slopes"][h]) * away.abs().double()
+            if c["causal"]:
+                x = x.masked_fill(hidden, float("-inf"))
+            y = torch.logsumexp(x, -1)
+            out = torch.exp(x - y[:, None]) @ v
+            o[rq, h], lse[h, rq] = out.detach(), y.detach()
+            if train:
+                g = torch.autograd.grad(out, (q, k, v), s["do"][rq, h].double())
+                grads[0][rq, h] = g[0]
+                grads[1][rk, h // group] += g[1]
+                grads[2][rk, h // group] += g[2]
+    if c["way"] == "step":
+        return o
+    return [o, lse] + (grads if train else [])
+
+
+def _exact_scan(s):
+    c = s["case"]
+    lens = torch.tensor(s["lens"], device="cuda")
+    starts = torch.tensor(s["starts"], device="cuda")
+    longest, rows = max(s["lens"]), c["tokens"]
+    f, x = s["gate"].double(), s["x"].double()
+    a = 1.0 / (1.0 + torch.exp(-f))
+    z = 1.0 / (1.0 + torch.exp(f))
+    y = torch.zeros_like(x)
+    before = torch.zeros_like(x)
+    h = s["state"].double()
+    # all documents step together; one that has ended keeps its state
+    one = len(s["lens"]) == 1
+    for t in range(longest):
+        if one:
+            i = t
+            before[i] = h[0]
+            h = (a[i] * h[0] + (z[i] * x[i] if c["coupled"] else x[i]))[None]
+            y[i] = h[0]
+            continue
+        on = lens > t
+        i = (starts + t)[on]
+        prev = h[on]
+        before[i] = prev
+        now = a[i] * prev + (z[i] * x[i] if c["coupled"] else x[i])
+        h[on] = now
+        y[i] = now
+    out = [y, h]
+    if c["way"] != "train":
+        return out
+    g = torch.zeros_like(x)
+    dy = s["dy"].double()
+    back = s["dstate"].double()
+    for t in range(longest - 1, -1, -1):
+        on = lens > t
+        i = (starts + t)[on]
+        now = dy[i] + back[on]
+        g[i] = now
+        back[on] = a[i] * now
+    dx = g * z if c["coupled"] else g
+    df = g * (before - x if c["coupled"] else before) * a * z
+    return out + [df, dx, back]
