@@ -365,8 +365,8 @@ def _own_scan(s):
                              s["io"][2], s["out"][1], s["saved"], s["ws"], s["ws_bytes"])
     if s["case"]["way"] != "train":
         return s["out"]
-    raster.gs_gated_scan_bwd(s["cfg"], s["docs"], rows, s["io"][0], s["io"][1], s["state"],
-                             s["saved"], s["grad_rows"][0], s["dstate"], s["grad_rows"][1],
+    raster.gs_gated_scan_bwd(s["cfg"], s["docs"], rows, s["io"][0], s["io"][1], s["saved"],
+                             s["grad_rows"][0], s["dstate"], s["grad_rows"][1],
                              s["grad_rows"][2], s["grads"][2], s["ws"], s["ws_bytes"])
     return s["out"] + s["grads"]
 
