@@ -506,7 +506,7 @@ def _plain_scan(s):
         return out
     before = torch.cat((h[:1], h[:-1]))
     before[first] = s["state"]
-    g = s["dy"].float()
+    g = s["dy"].float().clone()
     g[last] += s["dstate"]
     back = torch.cat((carry[1:], carry[:1] * 0.0))
     g = _composed(back.flip(0), g.flip(0)).flip(0)
