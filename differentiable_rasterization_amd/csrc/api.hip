@@ -75,6 +75,41 @@ hipError_t gs_launch_densify(int64_t N, int nplanes, const float* const* in_plan
                              const float* dL_dmeans, const float* opacities, float clone_fraction,
                              float min_opacity, float* const* out_planes, int64_t* num_out,
                              void* workspace, hipStream_t s);
+size_t gs_qk_bwd_workspace_bytes(const gs_qk_config& cfg, int64_t rows);
+hipError_t gs_launch_qk_fwd(const gs_qk_config& cfg, int64_t rows, const int32_t* positions,
+                            const float* inv_freq, const float* wq, const float* wk,
+                            const gs_heads& q, const gs_heads& k, const gs_heads& qo,
+                            const gs_heads& ko, hipStream_t s);
+hipError_t gs_launch_qk_bwd(const gs_qk_config& cfg, int64_t rows, const int32_t* positions,
+                            const float* inv_freq, const float* wq, const float* wk,
+                            const gs_heads& q, const gs_heads& k, const gs_heads& dqo,
+                            const gs_heads& dko, const gs_heads& dq, const gs_heads& dk,
+                            float* dwq, float* dwk, void* workspace, hipStream_t s);
+size_t gs_attention_fwd_bytes(const gs_attention_config& cfg, const gs_documents& d,
+                              int64_t rows_q, int64_t rows_k);
+size_t gs_attention_bwd_bytes(const gs_attention_config& cfg, const gs_documents& d,
+                              int64_t rows_q, int64_t rows_k);
+hipError_t gs_launch_attention_fwd(const gs_attention_config& cfg, const gs_documents& d,
+                                   int64_t rows_q, int64_t rows_k, const gs_heads& q,
+                                   const gs_heads& k, const gs_heads& v, const gs_heads& out,
+                                   float* lse, void* workspace, hipStream_t s);
+hipError_t gs_launch_attention_bwd(const gs_attention_config& cfg, const gs_documents& d,
+                                   int64_t rows_q, int64_t rows_k, const gs_heads& q,
+                                   const gs_heads& k, const gs_heads& v, const gs_heads& out,
+                                   const float* lse, const gs_heads& dout, const gs_heads& dq,
+                                   const gs_heads& dk, const gs_heads& dv, void* workspace,
+                                   hipStream_t s);
+size_t gs_gated_scan_bytes(const gs_scan_config& cfg, const gs_documents& d, int64_t rows);
+size_t gs_gated_saved_bytes(const gs_scan_config& cfg, const gs_documents& d, int64_t rows);
+hipError_t gs_launch_gated_fwd(const gs_scan_config& cfg, const gs_documents& d, int64_t rows,
+                              const gs_rows& gate, const gs_rows& x, const float* state_in,
+                              const gs_rows& y, float* state_out, float* saved, void* workspace,
+                              hipStream_t s);
+hipError_t gs_launch_gated_bwd(const gs_scan_config& cfg, const gs_documents& d, int64_t rows,
+                              const gs_rows& gate, const gs_rows& x, const float* saved,
+                              const gs_rows& dy, const float* dstate_out, const gs_rows& dgate,
+                              const gs_rows& dx, float* dstate_in, void* workspace,
+                              hipStream_t s);
 }
 
 namespace {
@@ -1045,6 +1080,332 @@ gs_status gs_densify_prune(int64_t N, int64_t ld, int32_t sh_degree, const float
                                       min_opacity, out, num_out, workspace,
                                       (hipStream_t)stream),
                     "gs_densify_prune");
+}
+
+// ---------------------------------------------------------------------------
+// Token operators
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxStride = (int64_t)1 << 28;
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+gs_status check_stride(int64_t stride) {
+  GS_REQUIRE(stride >= 0 && stride <= kMaxStride, "strides must be in [0, 2^28]");
+  GS_REQUIRE(stride % 8 == 0, "strides must be multiples of 8 elements");
+  return GS_OK;
+}
+
+// A [rows][heads][dim] view; an output's rows and heads must not overlap.
+gs_status check_heads(const gs_heads* t, int64_t rows, int64_t heads, int64_t dim, bool output) {
+  GS_REQUIRE(t != nullptr && t->data != nullptr, "NULL array pointer");
+  GS_REQUIRE(aligned16(t->data), "arrays must be 16-byte aligned");
+  GS_CHECK(check_stride(t->row));
+  GS_CHECK(check_stride(t->head));
+  if (output) {
+    const bool inner_heads = t->head >= dim && t->row >= (heads - 1) * t->head + dim;
+    const bool inner_rows = t->row >= dim && t->head >= (rows - 1) * t->row + dim;
+    GS_REQUIRE(inner_heads || inner_rows || (heads == 1 && t->row >= dim) ||
+                   (rows == 1 && t->head >= dim) || (rows == 1 && heads == 1),
+               "rows or heads of an output overlap");
+  }
+  return GS_OK;
+}
+
+gs_status check_rows(const gs_rows* t, int64_t rows, int64_t channels, bool output) {
+  GS_REQUIRE(t != nullptr && t->data != nullptr, "NULL array pointer");
+  GS_REQUIRE(aligned16(t->data), "arrays must be 16-byte aligned");
+  GS_CHECK(check_stride(t->row));
+  if (output) GS_REQUIRE(rows == 1 || t->row >= channels, "rows of an output overlap");
+  return GS_OK;
+}
+
+gs_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return GS_OK;
+  GS_REQUIRE(workspace != nullptr, "workspace is NULL");
+  GS_REQUIRE(((uintptr_t)workspace & 255u) == 0, "workspace must be 256-byte aligned");
+  GS_REQUIRE(bytes >= need, "workspace smaller than the call's workspace size");
+  return GS_OK;
+}
+
+gs_status check_token_rows(int64_t rows, int64_t heads) {
+  GS_REQUIRE(rows >= 0 && rows < (int64_t)1 << 31, "rows must be in [0, 2^31)");
+  GS_REQUIRE(rows * heads < (int64_t)1 << 31, "rows times heads must be < 2^31");
+  return GS_OK;
+}
+
+gs_status check_documents(const gs_documents* d, bool keys) {
+  GS_REQUIRE(d != nullptr, "documents are NULL");
+  GS_REQUIRE(d->count >= 0 && d->count <= 1 << 24, "document count must be in [0, 2^24]");
+  GS_REQUIRE(d->max_q_len >= 0 && d->max_k_len >= 0, "length bounds must be >= 0");
+  if (d->count == 0) return GS_OK;
+  GS_REQUIRE(d->q_start && d->q_len, "q_start and q_len are NULL");
+  if (keys) GS_REQUIRE(!d->k_start == !d->k_len, "k_start and k_len come together");
+  return GS_OK;
+}
+
+gs_status check_qk(const gs_qk_config* c, int64_t rows) {
+  GS_REQUIRE(c != nullptr, "cfg is NULL");
+  GS_REQUIRE(c->dtype >= GS_F32 && c->dtype <= GS_F16, "dtype must be a gs_dtype");
+  GS_REQUIRE(c->heads_q >= 1 && c->heads_k >= 1 && c->heads_q <= 65536 && c->heads_k <= 65536,
+             "heads must be in [1, 65536]");
+  GS_REQUIRE(c->head_dim >= 8 && c->head_dim <= 512 && c->head_dim % 8 == 0,
+             "head_dim must be a multiple of 8 in [8, 512]");
+  GS_REQUIRE(c->rotary_dim >= 0 && c->rotary_dim <= c->head_dim && c->rotary_dim % 16 == 0,
+             "rotary_dim must be a multiple of 16 in [0, head_dim]");
+  GS_REQUIRE((c->interleaved == 0 || c->interleaved == 1) && (c->norm == 0 || c->norm == 1),
+             "interleaved and norm must be 0 or 1");
+  GS_REQUIRE(std::isfinite(c->eps) && c->eps >= 0.0f, "eps must be >= 0");
+  GS_REQUIRE(std::isfinite(c->amplitude), "amplitude must be finite");
+  return check_token_rows(rows, (int64_t)c->heads_q + c->heads_k);
+}
+
+gs_status check_qk_arrays(const gs_qk_config* c, const int32_t* positions, const float* inv_freq,
+                          const float* wq, const float* wk) {
+  if (c->rotary_dim) GS_REQUIRE(positions && inv_freq, "positions or inv_freq is NULL");
+  if (c->norm) {
+    GS_REQUIRE(wq && wk, "wq or wk is NULL");
+    GS_REQUIRE(aligned16(wq) && aligned16(wk), "wq and wk must be 16-byte aligned");
+  }
+  return GS_OK;
+}
+
+gs_status check_attention(const gs_attention_config* c, const gs_documents* d, int64_t rows_q,
+                          int64_t rows_k) {
+  GS_REQUIRE(c != nullptr, "cfg is NULL");
+  GS_REQUIRE(c->dtype == GS_BF16 || c->dtype == GS_F16, "dtype must be GS_BF16 or GS_F16");
+  GS_REQUIRE(c->heads_k >= 1 && c->heads_q >= c->heads_k && c->heads_q <= 65536,
+             "heads must be in [1, 65536]");
+  GS_REQUIRE(c->heads_q % c->heads_k == 0, "heads_q must be a multiple of heads_k");
+  GS_REQUIRE(c->head_dim >= 8 && c->head_dim <= 128 && c->head_dim % 8 == 0,
+             "head_dim must be a multiple of 8 in [8, 128]");
+  GS_REQUIRE(c->causal == 0 || c->causal == 1, "causal must be 0 or 1");
+  GS_REQUIRE(std::isfinite(c->scale), "scale must be finite");
+  GS_REQUIRE(std::isfinite(c->softcap) && c->softcap >= 0.0f, "softcap must be >= 0");
+  GS_CHECK(check_documents(d, true));
+  GS_CHECK(check_token_rows(rows_q, c->heads_q));
+  return check_token_rows(rows_k, c->heads_q);
+}
+
+gs_status check_scan(const gs_scan_config* c, const gs_documents* d, int64_t rows) {
+  GS_REQUIRE(c != nullptr, "cfg is NULL");
+  GS_REQUIRE(c->dtype >= GS_F32 && c->dtype <= GS_F16, "dtype must be a gs_dtype");
+  GS_REQUIRE(c->coupled == 0 || c->coupled == 1, "coupled must be 0 or 1");
+  GS_REQUIRE(c->channels >= 8 && c->channels <= 1 << 24 && c->channels % 8 == 0,
+             "channels must be a multiple of 8 in [8, 2^24]");
+  GS_CHECK(check_documents(d, false));
+  // a wavefront takes 128 channels or more of a document or a chunk
+  GS_REQUIRE(((int64_t)d->count + rows / 64) * (c->channels / 8) < (int64_t)1 << 31,
+             "too many documents times channels");
+  return check_token_rows(rows, 1);
+}
+
+}  // namespace
+
+gs_status gs_qk_norm_rope_fwd(const gs_qk_config* cfg, int64_t rows, const int32_t* positions,
+                              const float* inv_freq, const float* wq, const float* wk,
+                              const gs_heads* q, const gs_heads* k, const gs_heads* q_out,
+                              const gs_heads* k_out, void* stream) {
+  GS_CHECK(check_qk(cfg, rows));
+  if (rows == 0) return GS_OK;
+  GS_CHECK(check_qk_arrays(cfg, positions, inv_freq, wq, wk));
+  GS_CHECK(check_heads(q, rows, cfg->heads_q, cfg->head_dim, false));
+  GS_CHECK(check_heads(k, rows, cfg->heads_k, cfg->head_dim, false));
+  GS_CHECK(check_heads(q_out, rows, cfg->heads_q, cfg->head_dim, true));
+  GS_CHECK(check_heads(k_out, rows, cfg->heads_k, cfg->head_dim, true));
+  return hip_status(gs_launch_qk_fwd(*cfg, rows, positions, inv_freq, wq, wk, *q, *k, *q_out,
+                                     *k_out, (hipStream_t)stream),
+                    "gs_qk_norm_rope_fwd");
+}
+
+size_t gs_qk_norm_rope_bwd_workspace_size(const gs_qk_config* cfg, int64_t rows) {
+  if (check_qk(cfg, rows) != GS_OK) return 0;
+  return gs_qk_bwd_workspace_bytes(*cfg, rows);
+}
+
+gs_status gs_qk_norm_rope_bwd(const gs_qk_config* cfg, int64_t rows, const int32_t* positions,
+                              const float* inv_freq, const float* wq, const float* wk,
+                              const gs_heads* q, const gs_heads* k, const gs_heads* dL_dq_out,
+                              const gs_heads* dL_dk_out, const gs_heads* dL_dq,
+                              const gs_heads* dL_dk, float* dL_dwq, float* dL_dwk,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  GS_CHECK(check_qk(cfg, rows));
+  if (cfg->norm) GS_REQUIRE(dL_dwq && dL_dwk, "dL_dwq or dL_dwk is NULL");
+  if (rows == 0) {
+    if (!cfg->norm) return GS_OK;
+    // no token: the weight gradients are sums over nothing
+    return hip_status(gs_launch_qk_bwd(*cfg, 0, positions, inv_freq, wq, wk, gs_heads{},
+                                       gs_heads{}, gs_heads{}, gs_heads{}, gs_heads{},
+                                       gs_heads{}, dL_dwq, dL_dwk, nullptr,
+                                       (hipStream_t)stream),
+                      "gs_qk_norm_rope_bwd");
+  }
+  GS_CHECK(check_qk_arrays(cfg, positions, inv_freq, wq, wk));
+  GS_CHECK(check_heads(q, rows, cfg->heads_q, cfg->head_dim, false));
+  GS_CHECK(check_heads(k, rows, cfg->heads_k, cfg->head_dim, false));
+  GS_CHECK(check_heads(dL_dq_out, rows, cfg->heads_q, cfg->head_dim, false));
+  GS_CHECK(check_heads(dL_dk_out, rows, cfg->heads_k, cfg->head_dim, false));
+  GS_CHECK(check_heads(dL_dq, rows, cfg->heads_q, cfg->head_dim, true));
+  GS_CHECK(check_heads(dL_dk, rows, cfg->heads_k, cfg->head_dim, true));
+  GS_CHECK(check_workspace(workspace, workspace_bytes, gs_qk_bwd_workspace_bytes(*cfg, rows)));
+  return hip_status(gs_launch_qk_bwd(*cfg, rows, positions, inv_freq, wq, wk, *q, *k, *dL_dq_out,
+                                     *dL_dk_out, *dL_dq, *dL_dk, dL_dwq, dL_dwk, workspace,
+                                     (hipStream_t)stream),
+                    "gs_qk_norm_rope_bwd");
+}
+
+size_t gs_attention_fwd_workspace_size(const gs_attention_config* cfg, const gs_documents* docs,
+                                       int64_t rows_q, int64_t rows_k) {
+  if (check_attention(cfg, docs, rows_q, rows_k) != GS_OK) return 0;
+  return gs_attention_fwd_bytes(*cfg, *docs, rows_q, rows_k);
+}
+
+gs_status gs_attention_fwd(const gs_attention_config* cfg, const gs_documents* docs,
+                           int64_t rows_q, int64_t rows_k, const gs_heads* q, const gs_heads* k,
+                           const gs_heads* v, const gs_heads* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  GS_CHECK(check_attention(cfg, docs, rows_q, rows_k));
+  if (docs->count == 0 || rows_q == 0) return GS_OK;
+  const gs_heads none = {};
+  GS_CHECK(check_heads(q, rows_q, cfg->heads_q, cfg->head_dim, false));
+  if (rows_k > 0) {
+    GS_CHECK(check_heads(k, rows_k, cfg->heads_k, cfg->head_dim, false));
+    GS_CHECK(check_heads(v, rows_k, cfg->heads_k, cfg->head_dim, false));
+  }
+  GS_CHECK(check_heads(out, rows_q, cfg->heads_q, cfg->head_dim, true));
+  GS_REQUIRE(out->data != q->data && (rows_k == 0 || (out->data != k->data &&
+                                                      out->data != v->data)),
+             "out must not alias the inputs");
+  GS_CHECK(check_workspace(workspace, workspace_bytes,
+                           gs_attention_fwd_bytes(*cfg, *docs, rows_q, rows_k)));
+  return hip_status(gs_launch_attention_fwd(*cfg, *docs, rows_q, rows_k, *q,
+                                            rows_k > 0 ? *k : none, rows_k > 0 ? *v : none, *out,
+                                            lse, workspace, (hipStream_t)stream),
+                    "gs_attention_fwd");
+}
+
+size_t gs_attention_bwd_workspace_size(const gs_attention_config* cfg, const gs_documents* docs,
+                                       int64_t rows_q, int64_t rows_k) {
+  if (check_attention(cfg, docs, rows_q, rows_k) != GS_OK) return 0;
+  return gs_attention_bwd_bytes(*cfg, *docs, rows_q, rows_k);
+}
+
+gs_status gs_attention_bwd(const gs_attention_config* cfg, const gs_documents* docs,
+                           int64_t rows_q, int64_t rows_k, const gs_heads* q, const gs_heads* k,
+                           const gs_heads* v, const gs_heads* out, const float* lse,
+                           const gs_heads* dL_dout, const gs_heads* dL_dq, const gs_heads* dL_dk,
+                           const gs_heads* dL_dv, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  GS_CHECK(check_attention(cfg, docs, rows_q, rows_k));
+  if (docs->count == 0 || (rows_q == 0 && rows_k == 0)) return GS_OK;
+  const gs_heads none = {};
+  if (rows_q > 0) {
+    GS_CHECK(check_heads(q, rows_q, cfg->heads_q, cfg->head_dim, false));
+    GS_CHECK(check_heads(out, rows_q, cfg->heads_q, cfg->head_dim, false));
+    GS_CHECK(check_heads(dL_dout, rows_q, cfg->heads_q, cfg->head_dim, false));
+    GS_CHECK(check_heads(dL_dq, rows_q, cfg->heads_q, cfg->head_dim, true));
+    GS_REQUIRE(lse != nullptr, "lse is NULL");
+  }
+  if (rows_k > 0) {
+    GS_CHECK(check_heads(k, rows_k, cfg->heads_k, cfg->head_dim, false));
+    GS_CHECK(check_heads(v, rows_k, cfg->heads_k, cfg->head_dim, false));
+    GS_CHECK(check_heads(dL_dk, rows_k, cfg->heads_k, cfg->head_dim, true));
+    GS_CHECK(check_heads(dL_dv, rows_k, cfg->heads_k, cfg->head_dim, true));
+    GS_REQUIRE(dL_dk->data != dL_dv->data, "dL_dk and dL_dv must not alias");
+  }
+  const void* in[6] = {rows_q > 0 ? q->data : nullptr, rows_k > 0 ? k->data : nullptr,
+                       rows_k > 0 ? v->data : nullptr, rows_q > 0 ? out->data : nullptr,
+                       rows_q > 0 ? dL_dout->data : nullptr, nullptr};
+  for (int i = 0; i < 5; ++i) {
+    if (in[i] == nullptr) continue;
+    GS_REQUIRE((rows_q == 0 || in[i] != dL_dq->data) &&
+                   (rows_k == 0 || (in[i] != dL_dk->data && in[i] != dL_dv->data)),
+               "gradients must not alias the inputs");
+  }
+  GS_CHECK(check_workspace(workspace, workspace_bytes,
+                           gs_attention_bwd_bytes(*cfg, *docs, rows_q, rows_k)));
+  return hip_status(
+      gs_launch_attention_bwd(*cfg, *docs, rows_q, rows_k, rows_q > 0 ? *q : none,
+                              rows_k > 0 ? *k : none, rows_k > 0 ? *v : none,
+                              rows_q > 0 ? *out : none, lse, rows_q > 0 ? *dL_dout : none,
+                              rows_q > 0 ? *dL_dq : none, rows_k > 0 ? *dL_dk : none,
+                              rows_k > 0 ? *dL_dv : none, workspace, (hipStream_t)stream),
+      "gs_attention_bwd");
+}
+
+size_t gs_gated_scan_saved_size(const gs_scan_config* cfg, const gs_documents* docs,
+                                int64_t rows) {
+  if (check_scan(cfg, docs, rows) != GS_OK) return 0;
+  return gs_gated_saved_bytes(*cfg, *docs, rows);
+}
+
+size_t gs_gated_scan_fwd_workspace_size(const gs_scan_config* cfg, const gs_documents* docs,
+                                        int64_t rows) {
+  if (check_scan(cfg, docs, rows) != GS_OK) return 0;
+  return gs_gated_scan_bytes(*cfg, *docs, rows);
+}
+
+gs_status gs_gated_scan_fwd(const gs_scan_config* cfg, const gs_documents* docs, int64_t rows,
+                            const gs_rows* gate, const gs_rows* x, const float* state_in,
+                            const gs_rows* y, float* state_out, void* saved, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  GS_CHECK(check_scan(cfg, docs, rows));
+  if (docs->count == 0) return GS_OK;
+  const gs_rows none = {};
+  if (rows > 0) {
+    GS_CHECK(check_rows(gate, rows, cfg->channels, false));
+    GS_CHECK(check_rows(x, rows, cfg->channels, false));
+    GS_CHECK(check_rows(y, rows, cfg->channels, true));
+    GS_REQUIRE(y->data != gate->data && y->data != x->data, "y must not alias the inputs");
+  }
+  GS_REQUIRE(aligned16(state_in) && aligned16(state_out) && aligned16(saved),
+             "states must be 16-byte aligned");
+  GS_CHECK(check_workspace(workspace, workspace_bytes,
+                           gs_gated_scan_bytes(*cfg, *docs, rows)));
+  return hip_status(gs_launch_gated_fwd(*cfg, *docs, rows, rows > 0 ? *gate : none,
+                                       rows > 0 ? *x : none, state_in, rows > 0 ? *y : none,
+                                       state_out, (float*)saved, workspace,
+                                       (hipStream_t)stream),
+                    "gs_gated_scan_fwd");
+}
+
+size_t gs_gated_scan_bwd_workspace_size(const gs_scan_config* cfg, const gs_documents* docs,
+                                        int64_t rows) {
+  if (check_scan(cfg, docs, rows) != GS_OK) return 0;
+  return gs_gated_scan_bytes(*cfg, *docs, rows);
+}
+
+gs_status gs_gated_scan_bwd(const gs_scan_config* cfg, const gs_documents* docs, int64_t rows,
+                            const gs_rows* gate, const gs_rows* x, const void* saved,
+                            const gs_rows* dL_dy, const float* dL_dstate_out,
+                            const gs_rows* dL_dgate, const gs_rows* dL_dx, float* dL_dstate_in,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  GS_CHECK(check_scan(cfg, docs, rows));
+  if (docs->count == 0) return GS_OK;
+  const gs_rows none = {};
+  if (rows > 0) {
+    GS_CHECK(check_rows(gate, rows, cfg->channels, false));
+    GS_CHECK(check_rows(x, rows, cfg->channels, false));
+    GS_CHECK(check_rows(dL_dy, rows, cfg->channels, false));
+    GS_CHECK(check_rows(dL_dgate, rows, cfg->channels, true));
+    GS_CHECK(check_rows(dL_dx, rows, cfg->channels, true));
+    GS_REQUIRE(saved != nullptr, "saved is NULL");
+    GS_REQUIRE(dL_dgate->data != dL_dx->data, "dL_dgate and dL_dx must not alias");
+    const void* in[3] = {gate->data, x->data, dL_dy->data};
+    for (const void* p : in)
+      GS_REQUIRE(p != dL_dgate->data && p != dL_dx->data, "gradients must not alias the inputs");
+  }
+  GS_REQUIRE(aligned16(dL_dstate_out) && aligned16(dL_dstate_in) && aligned16(saved),
+             "states must be 16-byte aligned");
+  GS_CHECK(check_workspace(workspace, workspace_bytes,
+                           gs_gated_scan_bytes(*cfg, *docs, rows)));
+  return hip_status(gs_launch_gated_bwd(*cfg, *docs, rows, rows > 0 ? *gate : none,
+                                       rows > 0 ? *x : none, (const float*)saved,
+                                       rows > 0 ? *dL_dy : none, dL_dstate_out,
+                                       rows > 0 ? *dL_dgate : none, rows > 0 ? *dL_dx : none,
+                                       dL_dstate_in, workspace, (hipStream_t)stream),
+                    "gs_gated_scan_bwd");
 }
 
 }  // extern "C"

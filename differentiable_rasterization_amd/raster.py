@@ -34,7 +34,13 @@ EXPORTED = ("gs_default_settings", "gs_status_string", "gs_last_error", "gs_num_
             "gs_rasterize_fwd_batched", "gs_rasterize_bwd_batched", "gs_project_bwd_batched",
             "gs_bin_and_sort_device", "gs_rasterize_fwd_loss", "gs_tile_order",
             "gs_rasterize_fwd_loss_batched", "gs_bin_and_sort_noalloc",
-            "gs_rasterize_workspace_size")
+            "gs_rasterize_workspace_size", "gs_qk_norm_rope_fwd",
+            "gs_qk_norm_rope_bwd_workspace_size", "gs_qk_norm_rope_bwd",
+            "gs_attention_fwd_workspace_size", "gs_attention_fwd",
+            "gs_attention_bwd_workspace_size", "gs_attention_bwd", "gs_gated_scan_saved_size",
+            "gs_gated_scan_fwd_workspace_size", "gs_gated_scan_fwd",
+            "gs_gated_scan_bwd_workspace_size", "gs_gated_scan_bwd")
+GS_F32, GS_BF16, GS_F16 = 0, 1, 2
 
 
 class GsError(RuntimeError):
@@ -61,6 +67,36 @@ _lib = None
 class gs_adam_config(C.Structure):
     _fields_ = [(n, C.c_float) for n in ("lr_means", "lr_scales", "lr_quats", "lr_opacities",
                                          "lr_sh", "beta1", "beta2", "eps")]
+
+
+class gs_heads(C.Structure):
+    """[rows][heads][dim] view (element strides); keeps its tensor alive."""
+    _fields_ = [("data", C.c_void_p), ("row", C.c_int64), ("head", C.c_int64)]
+
+
+class gs_rows(C.Structure):
+    """[rows][channels] view (element stride); keeps its tensor alive."""
+    _fields_ = [("data", C.c_void_p), ("row", C.c_int64)]
+
+
+class gs_documents(C.Structure):
+    _fields_ = [("count", C.c_int32), ("max_q_len", C.c_int32), ("max_k_len", C.c_int32)] + \
+        [(n, C.c_void_p) for n in ("q_start", "q_len", "k_start", "k_len", "prefix")]
+
+
+class gs_qk_config(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("dtype", "heads_q", "heads_k", "head_dim",
+                                         "rotary_dim", "interleaved", "norm")] + \
+        [("eps", C.c_float), ("amplitude", C.c_float)]
+
+
+class gs_attention_config(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("dtype", "heads_q", "heads_k", "head_dim", "causal")] + \
+        [("scale", C.c_float), ("softcap", C.c_float), ("slopes", C.c_void_p)]
+
+
+class gs_scan_config(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("coupled", C.c_int32), ("channels", C.c_int64)]
 
 
 def load():
@@ -165,6 +201,27 @@ def load():
     lib.gs_densify_prune.restype = C.c_int
     lib.gs_densify_prune.argtypes = [i64, i64, i32] + [P] * 6 + [C.c_float, C.c_float, i64] + \
         [P] * 5 + [P, P, C.c_size_t, P]
+    lib.gs_qk_norm_rope_fwd.restype = C.c_int
+    lib.gs_qk_norm_rope_fwd.argtypes = [P, i64] + [P] * 4 + [P] * 4 + [P]
+    lib.gs_qk_norm_rope_bwd_workspace_size.restype = SZ
+    lib.gs_qk_norm_rope_bwd_workspace_size.argtypes = [P, i64]
+    lib.gs_qk_norm_rope_bwd.restype = C.c_int
+    lib.gs_qk_norm_rope_bwd.argtypes = [P, i64] + [P] * 4 + [P] * 6 + [P, P] + [P, SZ, P]
+    for name in ("fwd", "bwd"):
+        fn = getattr(lib, "gs_attention_%s_workspace_size" % name)
+        fn.restype, fn.argtypes = SZ, [P, P, i64, i64]
+        fn = getattr(lib, "gs_gated_scan_%s_workspace_size" % name)
+        fn.restype, fn.argtypes = SZ, [P, P, i64]
+    lib.gs_attention_fwd.restype = C.c_int
+    lib.gs_attention_fwd.argtypes = [P, P, i64, i64] + [P] * 5 + [P, SZ, P]
+    lib.gs_attention_bwd.restype = C.c_int
+    lib.gs_attention_bwd.argtypes = [P, P, i64, i64] + [P] * 9 + [P, SZ, P]
+    lib.gs_gated_scan_saved_size.restype = SZ
+    lib.gs_gated_scan_saved_size.argtypes = [P, P, i64]
+    lib.gs_gated_scan_fwd.restype = C.c_int
+    lib.gs_gated_scan_fwd.argtypes = [P, P, i64] + [P] * 6 + [P, SZ, P]
+    lib.gs_gated_scan_bwd.restype = C.c_int
+    lib.gs_gated_scan_bwd.argtypes = [P, P, i64] + [P] * 8 + [P, SZ, P]
     _lib = lib
     return lib
 
@@ -575,6 +632,164 @@ def gs_densify_prune(N, ld, sh_degree, means, scales, quats, opacities, sh, dL_d
                                 _p(quats_out), _p(opacities_out), _p(sh_out), C.byref(n_out),
                                 _p(workspace), workspace_bytes, _stream(stream)))
     return int(n_out.value)
+
+# ---------------------------------------------------------------------------
+# Token operators
+# ---------------------------------------------------------------------------
+def _dtype(dtype) -> int:
+    import torch
+    kinds = {torch.float32: GS_F32, torch.bfloat16: GS_BF16, torch.float16: GS_F16}
+    if dtype not in kinds:
+        raise ValueError("dtype must be torch.float32, bfloat16 or float16, not %s" % dtype)
+    return kinds[dtype]
+
+
+def heads(t) -> gs_heads:
+    """The view of a [rows, heads, dim] device tensor (last dimension
+    contiguous).  Calls take the tensor or its view; a view made once saves
+    the calls their making it."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError("need a [rows, heads, dim] tensor with contiguous elements")
+    h = gs_heads(t.data_ptr(), t.stride(0), t.stride(1))
+    h.tensor = t
+    return h
+
+
+def rows(t) -> gs_rows:
+    """The view of a [rows, channels] device tensor (last dimension
+    contiguous)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("need a [rows, channels] tensor with contiguous elements")
+    r = gs_rows(t.data_ptr(), t.stride(0))
+    r.tensor = t
+    return r
+
+
+def _heads(t):
+    return None if t is None else C.byref(t if isinstance(t, gs_heads) else heads(t))
+
+
+def _rows(t):
+    return None if t is None else C.byref(t if isinstance(t, gs_rows) else rows(t))
+
+
+def documents(q_start, q_len, k_start=None, k_len=None, prefix=None, max_q_len=0,
+              max_k_len=0) -> gs_documents:
+    """gs_documents of int32 device tensors (kept alive with it)."""
+    import torch
+    arrays = (q_start, q_len, k_start, k_len, prefix)
+    for t in arrays:
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or
+                              t.numel() != q_start.numel()):
+            raise ValueError("documents need contiguous int32 arrays of one length")
+    d = gs_documents(q_start.numel(), int(max_q_len), int(max_k_len),
+                     *[None if t is None else t.data_ptr() for t in arrays])
+    d.tensors = arrays
+    return d
+
+
+def qk_config(dtype, heads_q, heads_k, head_dim, rotary_dim=None, interleaved=False, norm=True,
+              eps=1e-6, amplitude=1.0) -> gs_qk_config:
+    """dtype: a torch dtype; rotary_dim: None for the whole head."""
+    return gs_qk_config(_dtype(dtype), int(heads_q), int(heads_k), int(head_dim),
+                        int(head_dim if rotary_dim is None else rotary_dim), int(interleaved),
+                        int(norm), float(eps), float(amplitude))
+
+
+def attention_config(dtype, heads_q, heads_k, head_dim, scale, causal=False, softcap=0.0,
+                     slopes=None) -> gs_attention_config:
+    """dtype: torch.bfloat16 or float16; slopes: fp32 device tensor [heads_q]."""
+    if slopes is not None and (slopes.numel() != heads_q or not slopes.is_contiguous() or
+                               _dtype(slopes.dtype) != GS_F32):
+        raise ValueError("slopes must be a contiguous float32 tensor [heads_q]")
+    c = gs_attention_config(_dtype(dtype), int(heads_q), int(heads_k), int(head_dim),
+                            int(causal), float(scale), float(softcap),
+                            None if slopes is None else slopes.data_ptr())
+    c.tensor = slopes
+    return c
+
+
+def scan_config(dtype, channels, coupled=True) -> gs_scan_config:
+    return gs_scan_config(_dtype(dtype), int(coupled), int(channels))
+
+
+def gs_qk_norm_rope_fwd(cfg, rows, positions, inv_freq, wq, wk, q, k, q_out, k_out, stream=None):
+    lib = load()
+    _check(lib.gs_qk_norm_rope_fwd(C.byref(cfg), rows, _p(positions), _p(inv_freq), _p(wq),
+                                   _p(wk), _heads(q), _heads(k), _heads(q_out), _heads(k_out),
+                                   _stream(stream)))
+
+
+def gs_qk_norm_rope_bwd_workspace_size(cfg, rows) -> int:
+    return int(load().gs_qk_norm_rope_bwd_workspace_size(C.byref(cfg), rows))
+
+
+def gs_qk_norm_rope_bwd(cfg, rows, positions, inv_freq, wq, wk, q, k, dL_dq_out, dL_dk_out,
+                        dL_dq, dL_dk, dL_dwq, dL_dwk, workspace, workspace_bytes, stream=None):
+    lib = load()
+    _check(lib.gs_qk_norm_rope_bwd(C.byref(cfg), rows, _p(positions), _p(inv_freq), _p(wq),
+                                   _p(wk), _heads(q), _heads(k), _heads(dL_dq_out),
+                                   _heads(dL_dk_out), _heads(dL_dq), _heads(dL_dk), _p(dL_dwq),
+                                   _p(dL_dwk), _p(workspace), int(workspace_bytes),
+                                   _stream(stream)))
+
+
+def gs_attention_fwd_workspace_size(cfg, docs, rows_q, rows_k) -> int:
+    return int(load().gs_attention_fwd_workspace_size(C.byref(cfg), C.byref(docs), rows_q,
+                                                      rows_k))
+
+
+def gs_attention_fwd(cfg, docs, rows_q, rows_k, q, k, v, out, lse, workspace, workspace_bytes,
+                     stream=None):
+    """lse: fp32 [heads_q, rows_q], or None where no gradient follows."""
+    lib = load()
+    _check(lib.gs_attention_fwd(C.byref(cfg), C.byref(docs), rows_q, rows_k, _heads(q), _heads(k),
+                                _heads(v), _heads(out), _p(lse), _p(workspace),
+                                int(workspace_bytes), _stream(stream)))
+
+
+def gs_attention_bwd_workspace_size(cfg, docs, rows_q, rows_k) -> int:
+    return int(load().gs_attention_bwd_workspace_size(C.byref(cfg), C.byref(docs), rows_q,
+                                                      rows_k))
+
+
+def gs_attention_bwd(cfg, docs, rows_q, rows_k, q, k, v, out, lse, dL_dout, dL_dq, dL_dk, dL_dv,
+                     workspace, workspace_bytes, stream=None):
+    lib = load()
+    _check(lib.gs_attention_bwd(C.byref(cfg), C.byref(docs), rows_q, rows_k, _heads(q), _heads(k),
+                                _heads(v), _heads(out), _p(lse), _heads(dL_dout), _heads(dL_dq),
+                                _heads(dL_dk), _heads(dL_dv), _p(workspace),
+                                int(workspace_bytes), _stream(stream)))
+
+
+def gs_gated_scan_saved_size(cfg, docs, rows) -> int:
+    return int(load().gs_gated_scan_saved_size(C.byref(cfg), C.byref(docs), rows))
+
+
+def gs_gated_scan_fwd_workspace_size(cfg, docs, rows) -> int:
+    return int(load().gs_gated_scan_fwd_workspace_size(C.byref(cfg), C.byref(docs), rows))
+
+
+def gs_gated_scan_fwd(cfg, docs, rows, gate, x, state_in, y, state_out, saved, workspace,
+                      workspace_bytes, stream=None):
+    """saved: None, or gs_gated_scan_saved_size() bytes for the gradient."""
+    lib = load()
+    _check(lib.gs_gated_scan_fwd(C.byref(cfg), C.byref(docs), rows, _rows(gate), _rows(x),
+                                 _p(state_in), _rows(y), _p(state_out), _p(saved), _p(workspace),
+                                 int(workspace_bytes), _stream(stream)))
+
+
+def gs_gated_scan_bwd_workspace_size(cfg, docs, rows) -> int:
+    return int(load().gs_gated_scan_bwd_workspace_size(C.byref(cfg), C.byref(docs), rows))
+
+
+def gs_gated_scan_bwd(cfg, docs, rows, gate, x, saved, dL_dy, dL_dstate_out, dL_dgate, dL_dx,
+                      dL_dstate_in, workspace, workspace_bytes, stream=None):
+    lib = load()
+    _check(lib.gs_gated_scan_bwd(C.byref(cfg), C.byref(docs), rows, _rows(gate), _rows(x),
+                                 _p(saved), _rows(dL_dy), _p(dL_dstate_out), _rows(dL_dgate),
+                                 _rows(dL_dx), _p(dL_dstate_in), _p(workspace),
+                                 int(workspace_bytes), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -629,6 +629,180 @@ GS_API gs_status gs_densify_prune(int64_t N, int64_t ld, int32_t sh_degree, cons
                                   float* sh_out, int64_t* num_out, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
+/* Token operators: the mixing layers of a network whose tokens become
+ * Gaussians (its last layer writes the planes of gs_project_fwd, and the
+ * gradients of gs_project_bwd go back into it).  A batch is ragged: rows of
+ * tokens, divided into documents (one scene, or one request).
+ *
+ * Conventions of these calls, beside the shared ones
+ *   - Elements are of a gs_dtype.  All sums, softmax statistics, norms and
+ *     states are fp32; what a call returns in a 16-bit type is rounded to it
+ *     once, to nearest even, unless said otherwise.
+ *   - gs_heads is a [rows][heads][dim] view and gs_rows a [rows][channels]
+ *     view (HOST structs): element strides of a row and a head, the last
+ *     dimension contiguous; so queries, keys and values may be columns of one
+ *     projection.  data is 16-byte aligned, strides are multiples of 8
+ *     elements in [0, 2^28].  Outputs must not overlap: each row of an output
+ *     is its own.
+ *   - rows < 2^31, and rows times heads < 2^31.  Zero rows or documents are
+ *     valid and launch nothing; pointers may then be NULL.
+ *   - Results are reproducible bit for bit: there are no atomics. */
+typedef enum { GS_F32 = 0, GS_BF16 = 1, GS_F16 = 2 } gs_dtype;
+
+typedef struct {
+  void* data;
+  int64_t row, head;
+} gs_heads;
+
+typedef struct {
+  void* data;
+  int64_t row;
+} gs_rows;
+
+/* Documents (HOST struct of DEVICE int32 [count] arrays).  Document d is rows
+ * q_start[d] .. + q_len[d] of the tokens; in attention its keys are rows
+ * k_start[d] .. + k_len[d] of the keys and values (both NULL: the same rows),
+ * which may be slots of a cache with room to spare, and prefix[d] (NULL: 0)
+ * of them are seen by all its tokens.  Token ranges of different documents
+ * are disjoint, and so are key ranges where a gradient is taken; lengths may
+ * be zero, documents may stand in any order, and rows between them are not
+ * written and do not matter.  Ranges are clamped to the call's rows.
+ * max_q_len, max_k_len: HOST upper bounds of the lengths where the caller
+ * knows them, else 0; they choose how the work is split, never what is
+ * computed. */
+typedef struct {
+  int32_t count;
+  int32_t max_q_len, max_k_len;
+  const int32_t *q_start, *q_len, *k_start, *k_len, *prefix;
+} gs_documents;
+
+/* Norm and rotary position of query and key heads, in one pass.  Per token
+ * and head of head_dim elements (a multiple of 8, at most 512):
+ *   n = w x / sqrt(mean x^2 + eps)    (norm = 1; n = x with norm = 0),
+ * then the first rotary_dim elements in pairs (interleaved = 0: i and
+ * i + rotary_dim / 2; 1: 2i and 2i + 1) are turned by
+ * theta_i = position * inv_freq[i] and multiplied by amplitude:
+ *   (a, b) -> amplitude (a cos - b sin, b cos + a sin);
+ * the others are n.  rotary_dim is a multiple of 16, 0 .. head_dim.  Long
+ * contexts are the caller's choice of inv_freq and amplitude (positions
+ * divided by a factor, a larger base, a blend per frequency). */
+typedef struct {
+  int32_t dtype; /* gs_dtype */
+  int32_t heads_q, heads_k, head_dim, rotary_dim;
+  int32_t interleaved, norm;
+  float eps, amplitude;
+} gs_qk_config;
+
+/* positions [rows] int32, inv_freq [rotary_dim / 2], wq and wk [head_dim]
+ * (fp32, 16-byte aligned; NULL with norm = 0; inv_freq and positions NULL
+ * with rotary_dim = 0).  q_out and k_out may be q and k (in place). */
+GS_API gs_status gs_qk_norm_rope_fwd(const gs_qk_config* cfg, int64_t rows,
+                                     const int32_t* positions, const float* inv_freq,
+                                     const float* wq, const float* wk, const gs_heads* q,
+                                     const gs_heads* k, const gs_heads* q_out,
+                                     const gs_heads* k_out, void* stream);
+
+/* Gradients of the call above from its inputs and those of its outputs:
+ * dL_dq, dL_dk, and dL_dwq, dL_dwk [head_dim] fp32, summed over tokens and
+ * heads (overwritten; not touched with norm = 0).  workspace: 256-byte
+ * aligned device memory of gs_qk_norm_rope_bwd_workspace_size() bytes.
+ * dL_dq may be dL_dq_out and dL_dk may be dL_dk_out. */
+GS_API size_t gs_qk_norm_rope_bwd_workspace_size(const gs_qk_config* cfg, int64_t rows);
+GS_API gs_status gs_qk_norm_rope_bwd(const gs_qk_config* cfg, int64_t rows,
+                                     const int32_t* positions, const float* inv_freq,
+                                     const float* wq, const float* wk, const gs_heads* q,
+                                     const gs_heads* k, const gs_heads* dL_dq_out,
+                                     const gs_heads* dL_dk_out, const gs_heads* dL_dq,
+                                     const gs_heads* dL_dk, float* dL_dwq, float* dL_dwk,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention within documents.  Query head h reads key head
+ * h / (heads_q / heads_k).  Token i of a document stands at position
+ * i' = i + k_len - q_len (the last token at the last key).  Score of key j:
+ *   s = scale q.k;  softcap > 0: s = softcap tanh(s / softcap);
+ *   slopes [heads_q] (fp32 DEVICE, NULL: none): s -= slopes[h] |i' - j|.
+ * Key j is seen when causal = 0, or j <= i', or j < prefix.  The output is
+ * the softmax over the seen keys times the values; a token that sees no key
+ * gets 0.  lse [heads_q][rows_q] fp32 (NULL to skip; the gradient needs it):
+ * the logarithm of the sum of exponentials, -inf where no key is seen.
+ * dtype is GS_BF16 or GS_F16; head_dim a multiple of 8, at most 128.
+ * Softmax weights are rounded to dtype for the product with the values.
+ * Non-finite values reach no other document and no row outside their own; a
+ * non-finite key or value may reach every token of its document, also one
+ * that does not see it.  workspace: 256-byte aligned, of
+ * gs_attention_fwd_workspace_size() bytes. */
+typedef struct {
+  int32_t dtype; /* GS_BF16 or GS_F16 */
+  int32_t heads_q, heads_k, head_dim;
+  int32_t causal;
+  float scale, softcap;
+  const float* slopes;
+} gs_attention_config;
+
+GS_API size_t gs_attention_fwd_workspace_size(const gs_attention_config* cfg,
+                                              const gs_documents* docs, int64_t rows_q,
+                                              int64_t rows_k);
+GS_API gs_status gs_attention_fwd(const gs_attention_config* cfg, const gs_documents* docs,
+                                  int64_t rows_q, int64_t rows_k, const gs_heads* q,
+                                  const gs_heads* k, const gs_heads* v, const gs_heads* out,
+                                  float* lse, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Gradients with respect to q, k and v (slopes are constants), from the
+ * forward's inputs, out and lse and the gradient of out; gradients of shared
+ * key heads are summed over their query heads in fp32.  Softmax weights and
+ * score gradients are rounded to dtype for the matrix products.  Gradient
+ * rows of no document are not written. */
+GS_API size_t gs_attention_bwd_workspace_size(const gs_attention_config* cfg,
+                                              const gs_documents* docs, int64_t rows_q,
+                                              int64_t rows_k);
+GS_API gs_status gs_attention_bwd(const gs_attention_config* cfg, const gs_documents* docs,
+                                  int64_t rows_q, int64_t rows_k, const gs_heads* q,
+                                  const gs_heads* k, const gs_heads* v, const gs_heads* out,
+                                  const float* lse, const gs_heads* dL_dout,
+                                  const gs_heads* dL_dq, const gs_heads* dL_dk,
+                                  const gs_heads* dL_dv, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Gated linear recurrence over the tokens of each document (q_start, q_len),
+ * per channel:
+ *   a = sigmoid(gate);  h_t = a_t h_{t-1} + u_t;  y_t = h_t,
+ * with u = (1 - a) x (coupled = 1: compositing's over operator, alpha =
+ * 1 - a) or u = x.  h_0 = state_in [count][channels] (fp32; NULL: zero);
+ * state_out [count][channels] (NULL to skip; may be state_in) receives the
+ * state after the last token (state_in's for an empty document).  saved: NULL,
+ * or gs_gated_scan_saved_size() bytes that the gradient reads.  channels is a
+ * multiple of 8, at most 2^24.  fp32 pointers are 16-byte aligned; workspace
+ * 256-byte aligned, of gs_gated_scan_fwd_workspace_size() bytes (0 where every
+ * document is short). */
+typedef struct {
+  int32_t dtype; /* gs_dtype */
+  int32_t coupled;
+  int64_t channels;
+} gs_scan_config;
+
+GS_API size_t gs_gated_scan_saved_size(const gs_scan_config* cfg, const gs_documents* docs,
+                                       int64_t rows);
+GS_API size_t gs_gated_scan_fwd_workspace_size(const gs_scan_config* cfg,
+                                               const gs_documents* docs, int64_t rows);
+GS_API gs_status gs_gated_scan_fwd(const gs_scan_config* cfg, const gs_documents* docs,
+                                   int64_t rows, const gs_rows* gate, const gs_rows* x,
+                                   const float* state_in, const gs_rows* y, float* state_out,
+                                   void* saved, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* Gradients from those of y and of state_out (dL_dstate_out NULL: zero):
+ * dL_dgate, dL_dx and dL_dstate_in (NULL to skip).  saved is the forward's,
+ * for the same inputs and documents. */
+GS_API size_t gs_gated_scan_bwd_workspace_size(const gs_scan_config* cfg,
+                                               const gs_documents* docs, int64_t rows);
+GS_API gs_status gs_gated_scan_bwd(const gs_scan_config* cfg, const gs_documents* docs,
+                                   int64_t rows, const gs_rows* gate, const gs_rows* x,
+                                   const void* saved, const gs_rows* dL_dy,
+                                   const float* dL_dstate_out, const gs_rows* dL_dgate,
+                                   const gs_rows* dL_dx, float* dL_dstate_in, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
