@@ -1184,6 +1184,8 @@ gs_status check_attention(const gs_attention_config* c, const gs_documents* d, i
   GS_REQUIRE(std::isfinite(c->scale), "scale must be finite");
   GS_REQUIRE(std::isfinite(c->softcap) && c->softcap >= 0.0f, "softcap must be >= 0");
   GS_CHECK(check_documents(d, true));
+  GS_REQUIRE((int64_t)d->count * c->heads_q <= (int64_t)1 << 26,
+             "documents times heads must be <= 2^26");
   GS_CHECK(check_token_rows(rows_q, c->heads_q));
   return check_token_rows(rows_k, c->heads_q);
 }

@@ -43,12 +43,21 @@ struct AttnArgs {
   int64_t out0_row, out0_head, out1_row, out1_head;
   float* lse;    // [heads_q][rows_q]
   float* delta;  // [heads_q][rows_q]
+  int parts;          // dk, dv: sums per query head
+  int pieces, piece;  // one-token form: pieces of a document's keys, keys of one
+  int col_tiles;      // one-token form: column tiles in the grid
+  float* part_ml;     // [pieces][heads_q][rows_q][2]
+  float* part_o;      // [pieces][heads_q][rows_q][dim]
 };
 
-constexpr int kKeys = 64;     // keys of a staged tile
-constexpr int kCols = 128;    // columns of a workgroup: four wavefronts of 32
-constexpr int kKeyCols = 128; // keys of a workgroup of the dk, dv kernel
-constexpr int kRows = 64;     // query rows of its staged tile
+constexpr int kKeys = 64;  // keys of a staged tile
+constexpr int kCols = 128; // columns of a workgroup: four wavefronts of 32
+constexpr int kRows = 32;  // query rows of a staged tile of the dk, dv kernel
+constexpr int kPieceKeys = 128;  // one-token form: keys the four wavefronts take at a time
+
+// How scores are made: kMode bits.
+constexpr int kCap = 1;      // capped by tanh
+constexpr int kGeneral = 2;  // distance bias, or a scale that is not positive
 
 template <typename T>
 struct Mat;
@@ -173,52 +182,197 @@ __device__ inline void load_cols(const uint16_t* p, bool ok, int dim,
   }
 }
 
-// Rows [0, rows) of a key tile into LDS, zeros past `valid`.
+// A tile of ROWS rows on its way into LDS: loaded into registers while the
+// tile before it is computed, zeros past `valid` rows and dim elements.
 template <int DT, int ROWS>
-__device__ inline void stage_keys(uint16_t* tile, const uint16_t* base, int64_t row_stride,
-                                  int valid, int dim) {
-  constexpr int kChunks = DT / 8;
+struct Staged {
+  static constexpr int kChunks = DT / 8;
+  static constexpr int kPer = ROWS * kChunks / 256;
+  u32x4 w[kPer];
+  __device__ inline void load(const uint16_t* base, int64_t row_stride, int valid, int dim) {
 #pragma unroll
-  for (int i = 0; i < ROWS * kChunks / 256; ++i) {
-    const int x = threadIdx.x + 256 * i, r = x / kChunks, c = x % kChunks;
-    u32x4 w = {0, 0, 0, 0};
-    if (r < valid && c * 8 < dim) w = *(const u32x4*)(base + (int64_t)r * row_stride + c * 8);
-    *(u32x4*)(tile + place<DT>(r, c)) = w;
+    for (int i = 0; i < kPer; ++i) {
+      const int x = threadIdx.x + 256 * i, r = x / kChunks, c = x % kChunks;
+      w[i] = (u32x4)(0);
+      if (r < valid && c * 8 < dim) w[i] = *(const u32x4*)(base + (int64_t)r * row_stride + c * 8);
+    }
+  }
+  __device__ inline void store(uint16_t* tile) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int x = threadIdx.x + 256 * i;
+      *(u32x4*)(tile + place<DT>(x / kChunks, x % kChunks)) = w[i];
+    }
+  }
+};
+
+// Products over a staged tile, operands read two steps ahead of their use.
+// The barriers keep the compiler from moving every read to the front, which
+// costs more registers than there are.
+template <typename T, int DT>
+__device__ inline f32x16 times_rows(const uint16_t* tile, int r0,
+                                    const typename Mat<T>::V8 (&f)[DT / 16]) {
+  constexpr int N = DT / 16;
+  typename Mat<T>::V8 x[3];
+  f32x16 s = (f32x16)(0.0f);
+  x[0] = read_rows<T, DT>(tile, r0, 0);
+  x[1] = read_rows<T, DT>(tile, r0, 1);
+#pragma unroll
+  for (int ks = 0; ks < N; ++ks) {
+    if (ks + 2 < N) x[(ks + 2) % 3] = read_rows<T, DT>(tile, r0, ks + 2);
+    s = Mat<T>::mul(x[ks % 3], f[ks], s);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  return s;
+}
+
+// o += (rows r0 .. r0 + 32 of the tile, transposed) times p.
+template <typename T, int DT>
+__device__ inline void add_cols(const uint16_t* tile, int r0, const f32x16& p,
+                                f32x16 (&o)[DT / 32]) {
+  constexpr int M = DT / 32, N = 2 * M;
+  typename Mat<T>::V8 x[3], w[2];
+  w[0] = pack_cols<T>(p, 0);
+  w[1] = pack_cols<T>(p, 1);
+  x[0] = read_cols<T, DT>(tile, r0, 0);
+  x[1] = read_cols<T, DT>(tile, r0 + 1 / M * 16, 1 % M * 32);
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    if (n + 2 < N) x[(n + 2) % 3] = read_cols<T, DT>(tile, r0 + (n + 2) / M * 16, (n + 2) % M * 32);
+    o[n % M] = Mat<T>::mul(x[n % 3], w[n / M], o[n % M]);
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// Score bookkeeping shared by the three kernels: raw products of one register
-// tile to scores in units of log2.  `away(i)` is |i' - j| of register i.
-// With kFactor, t receives 1 - tanh^2.
-template <bool kFactor, typename Away>
-__device__ inline void scores(const AttnArgs& a, f32x16& s, float mul, float cap_in,
-                              float cap_out, Away away, float (*t)[16]) {
-  if (a.softcap > 0.0f) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float th = tanh_of(s[i] * cap_in);
-      if constexpr (kFactor) (*t)[i] = fmaf(-th, th, 1.0f);
-      s[i] = th * cap_out;
-    }
+// Constants of the scores, in units of log2.
+struct Scale {
+  float mul, cap_in, cap_out;
+};
+template <int kMode>
+__device__ inline Scale scale_of(const AttnArgs& a) {
+  Scale c;
+  c.mul = a.scale * kLog2e;
+  c.cap_in = kMode & kCap ? a.scale / a.softcap : 0.0f;
+  c.cap_out = a.softcap * kLog2e;
+  return c;
+}
+
+// A raw product as a score, less `away` = slope |i' - j|; f receives
+// 1 - tanh^2.  Plain scores stay raw (their factor mul is applied with the
+// subtraction that follows).
+template <int kMode, typename Away>
+__device__ inline float score(float s, const Scale& c, Away away, float& f) {
+  f = 1.0f;
+  if constexpr (kMode == 0) return s;
+  float x;
+  if constexpr (kMode & kCap) {
+    const float th = tanh_of(s * c.cap_in);
+    f = fmaf(-th, th, 1.0f);
+    x = th * c.cap_out;
   } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] *= mul;
+    x = s * c.mul;
   }
-  if (a.slopes) {
+  if constexpr (kMode & kGeneral) x -= away();
+  return x;
+}
+
+// Four results of 16 as they are stored: rows 8 i + 4 half + j of the
+// transposed output, i.e. four consecutive elements of the lane's column.
+template <typename T, int DT, typename F>
+__device__ inline void store_col(uint16_t* p, int dim, F value) {
+  const int half = (threadIdx.x & 63) >> 5;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] -= away(i);
+  for (int dt = 0; dt < DT / 32; ++dt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = dt * 32 + 8 * i + 4 * half;
+      if (e < dim) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = value(dt, 4 * i + j);
+        store_elems((T*)(p + e), x);
+      }
+    }
   }
+}
+
+// A query column of this lane.
+struct Col {
+  int token, head, pos, lim;
+  bool ok;
+};
+__device__ inline Col column(const AttnArgs& a, const Doc& d, int hk, uint32_t c, uint32_t cols) {
+  Col o;
+  o.ok = c < cols;
+  o.token = (int)(c / a.group);
+  o.head = hk * a.group + (int)(c % a.group);
+  o.pos = o.token + d.kl - d.ql;
+  o.lim = key_limit(a, d, o.token);
+  return o;
 }
 
 // ---------------------------------------------------------------------------
 // Forward
 // ---------------------------------------------------------------------------
-template <typename T, int DT>
+// The running softmax of N 32-key tiles of a column, from key k0: masks,
+// moves the reference m where a score passes it by more than 8 (weights then
+// stay below 2^8, far inside every type, and the accumulators are rarely
+// rescaled), and leaves the weights in s.
+template <int DT, int N>
+__device__ inline void softmax_step(f32x16 (&s)[N], float mul, bool masked, int k0, int lim,
+                                    float& m, float& l, f32x16 (&o)[DT / 32]) {
+  if (masked) {
+#pragma unroll
+    for (int rt = 0; rt < N; ++rt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        s[rt][i] = k0 + rt * 32 + result_row(i) < lim ? s[rt][i] : -INFINITY;
+  }
+  float top = -INFINITY;
+#pragma unroll
+  for (int rt = 0; rt < N; ++rt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[rt][i]);
+  top = both_max(top) * mul;
+  if (__any(top > m + 8.0f)) {
+    const float now = fmaxf(m, top);
+    const float alpha = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+    l *= alpha;
+#pragma unroll
+    for (int i = 0; i < DT / 32; ++i) o[i] *= alpha;
+    m = now;
+  }
+  const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+  for (int rt = 0; rt < N; ++rt)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[rt][i] = __builtin_amdgcn_exp2f(fmaf(s[rt][i], mul, -ref));
+      l += s[rt][i];
+    }
+}
+
+// Scores of one 32-key tile in place.
+template <int kMode>
+__device__ inline void make_scores(f32x16& s, const Scale& c, float slope, int off) {
+  if constexpr (kMode != 0) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float f;
+      s[i] = score<kMode>(s[i], c,
+                          [&] { return slope * fabsf((float)(off - result_row(i))); }, f);
+    }
+  }
+}
+
+// A workgroup takes 128 columns, a wavefront 32; key tiles of 64 pass through
+// LDS, the next one on its way in registers.
+template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
-  __shared__ __align__(16) uint16_t s_k[kKeys * DT];
-  __shared__ __align__(16) uint16_t s_v[kKeys * DT];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  __shared__ __align__(16) uint16_t s_k[2][kKeys * DT];
+  __shared__ __align__(16) uint16_t s_v[2][kKeys * DT];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int hk = blockIdx.x % a.heads_k;
   uint32_t local, units;
   const int doc = find_document(a.docs.q_start, a.docs.q_len, a.docs.rows_q, a.docs.count,
@@ -228,104 +382,256 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
   // long causal rows first
   const uint32_t col0 = (units - 1 - local) * kCols;
   const uint32_t cols = (uint32_t)d.ql * a.group;
-  const uint32_t c = col0 + wave * 32 + (lane & 31);
-  const bool ok = c < cols;
-  const int token = (int)(c / a.group), head = hk * a.group + (int)(c % a.group);
-  const int lim = key_limit(a, d, token);
-  const int pos = token + d.kl - d.ql;
+  const Col col = column(a, d, hk, col0 + wave * 32 + (lane & 31), cols);
+  const int64_t row = d.qs + col.token;
   V8 qf[DT / 16];
-  load_cols<T, DT>(a.q + (int64_t)(d.qs + token) * a.q_row + (int64_t)head * a.q_head, ok, a.dim,
-                   qf);
-  const float mul = a.scale * kLog2e;
-  const float cap_in = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
-  const float cap_out = a.softcap * kLog2e;
-  const float slope = a.slopes && ok ? a.slopes[head] * kLog2e : 0.0f;
-
+  load_cols<T, DT>(a.q + row * a.q_row + (int64_t)col.head * a.q_head, col.ok, a.dim, qf);
+  const Scale sc = scale_of<kMode>(a);
+  const float mul = kMode == 0 ? sc.mul : 1.0f;
+  const float slope = (kMode & kGeneral) && a.slopes && col.ok ? a.slopes[col.head] * kLog2e
+                                                               : 0.0f;
   f32x16 o[DT / 32];
 #pragma unroll
   for (int i = 0; i < DT / 32; ++i) o[i] = (f32x16)(0.0f);
   float m = -INFINITY, l = 0.0f;
   const int last_token = (int)((min(col0 + kCols, cols) - 1) / a.group);
   const int end = key_limit(a, d, last_token);
-  const int wave_lo = __builtin_amdgcn_readlane(lim, 0);
-  const int wave_hi = min(__builtin_amdgcn_readlane(lim, 31), end);
+  const int wave_lo = __builtin_amdgcn_readlane(col.lim, 0);
+  const int wave_hi = min(__builtin_amdgcn_readlane(col.lim, 31), end);
   const uint16_t* kb = a.k + (int64_t)d.ks * a.k_row + (int64_t)hk * a.k_head;
   const uint16_t* vb = a.v + (int64_t)d.ks * a.v_row + (int64_t)hk * a.v_head;
-  for (int k0 = 0; k0 < end; k0 += kKeys) {
+  Staged<DT, kKeys> sk, sv;
+  if (end > 0) {
+    sk.load(kb, a.k_row, d.kl, a.dim);
+    sv.load(vb, a.v_row, d.kl, a.dim);
+    sk.store(s_k[0]);
+    sv.store(s_v[0]);
+  }
+  int buf = 0;
+  for (int k0 = 0; k0 < end; k0 += kKeys, buf ^= 1) {
     __syncthreads();
-    stage_keys<DT, kKeys>(s_k, kb + (int64_t)k0 * a.k_row, a.k_row, d.kl - k0, a.dim);
-    stage_keys<DT, kKeys>(s_v, vb + (int64_t)k0 * a.v_row, a.v_row, d.kl - k0, a.dim);
-    __syncthreads();
-    if (k0 >= wave_hi) continue;
-    f32x16 s[2];
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt) {
-      s[rt] = (f32x16)(0.0f);
-#pragma unroll
-      for (int ks = 0; ks < DT / 16; ++ks)
-        s[rt] = Mat<T>::mul(read_rows<T, DT>(s_k, rt * 32, ks), qf[ks], s[rt]);
+    const bool more = k0 + kKeys < end;
+    if (more) {
+      sk.load(kb + (int64_t)(k0 + kKeys) * a.k_row, a.k_row, d.kl - k0 - kKeys, a.dim);
+      sv.load(vb + (int64_t)(k0 + kKeys) * a.v_row, a.v_row, d.kl - k0 - kKeys, a.dim);
     }
+    if (k0 < wave_hi) {
+      f32x16 s[2];
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) {
+        s[rt] = times_rows<T, DT>(s_k[buf], rt * 32, qf);
+        make_scores<kMode>(s[rt], sc, slope, col.pos - k0 - rt * 32);
+      }
+      softmax_step<DT, 2>(s, mul, k0 + kKeys > wave_lo, k0, col.lim, m, l, o);
+#pragma unroll
+      for (int rt = 0; rt < 2; ++rt) add_cols<T, DT>(s_v[buf], rt * 32, s[rt], o);
+    }
+    if (more) {
+      sk.store(s_k[buf ^ 1]);
+      sv.store(s_v[buf ^ 1]);
+    }
+  }
+  const float sum = both_sum(l);
+  if (!col.ok) return;
+  const bool none = col.lim <= 0;
+  const float inv = none || sum == 0.0f ? 0.0f : 1.0f / sum;
+  store_col<T, DT>(a.out0 + row * a.out0_row + (int64_t)col.head * a.out0_head, a.dim,
+                   [&](int dt, int i) { return none ? 0.0f : o[dt][i] * inv; });
+  if (a.lse && lane < 32)
+    a.lse[(int64_t)col.head * a.docs.rows_q + row] =
+        none ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+// Few columns a document (one new token, all its heads): the keys are what
+// there is to split.  A workgroup takes one piece of a document's keys for 32
+// columns of a key head, its four wavefronts 32 keys each in turn.  Keys come
+// straight from memory as the left operand, values pass through the
+// wavefront's own LDS for the transposing read, and both are on their way for
+// the next tile while this one is computed.  The wavefronts' results are
+// joined in LDS; where a document has several pieces,
+// attention_join_kernel joins those.
+template <typename T, int DT, int kMode>
+__global__ __launch_bounds__(256, 2) void attention_step_kernel(AttnArgs a) {
+  typedef typename Mat<T>::V8 V8;
+  constexpr int kChunks = DT / 8;
+  constexpr int kPer = 32 * kChunks / 64;
+  constexpr int kStride = DT + 4;
+  // the values' tiles, and after the loop the wavefronts' results
+  __shared__ __align__(16) float s_raw[4 * 32 * kStride];
+  __shared__ float s_m[4][32], s_l[4][32];
+  uint16_t* const s_v = (uint16_t*)s_raw + (threadIdx.x >> 6) * 32 * DT;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  int u = blockIdx.x;
+  const int hk = u % a.heads_k;
+  u /= a.heads_k;
+  const int tile0 = u % a.col_tiles;
+  u /= a.col_tiles;
+  const int piece = u % a.pieces, doc = u / a.pieces;
+  const Doc d = load_doc(a.docs, doc);
+  const int pieces = max(1, min(a.pieces, (d.kl + a.piece - 1) / a.piece));
+  if (piece >= pieces) return;
+  const int key_lo = piece * a.piece;
+  const int key_hi = piece == pieces - 1 ? d.kl : key_lo + a.piece;
+  const uint32_t cols = (uint32_t)d.ql * a.group;
+  const uint16_t* kb = a.k + (int64_t)d.ks * a.k_row + (int64_t)hk * a.k_head;
+  const uint16_t* vb = a.v + (int64_t)d.ks * a.v_row + (int64_t)hk * a.v_head;
+  const Scale sc = scale_of<kMode>(a);
+  const float mul = kMode == 0 ? sc.mul : 1.0f;
+  for (uint32_t col0 = tile0 * 32; col0 < cols; col0 += a.col_tiles * 32) {
+    const Col col = column(a, d, hk, col0 + (lane & 31), cols);
+    V8 qf[DT / 16];
+    load_cols<T, DT>(a.q + (int64_t)(d.qs + col.token) * a.q_row + (int64_t)col.head * a.q_head,
+                     col.ok, a.dim, qf);
+    const float slope = (kMode & kGeneral) && a.slopes && col.ok ? a.slopes[col.head] * kLog2e
+                                                                 : 0.0f;
+    const int last_token = (int)((min(col0 + 32, cols) - 1) / a.group);
+    const int end = min(key_hi, key_limit(a, d, last_token));
+    const int wave_lo = __builtin_amdgcn_readlane(col.lim, 0);
+    f32x16 o[DT / 32];
+#pragma unroll
+    for (int i = 0; i < DT / 32; ++i) o[i] = (f32x16)(0.0f);
+    float m = -INFINITY, l = 0.0f;
+    V8 kf[DT / 16];
+    u32x4 vw[kPer];
+    auto fetch = [&](int k0) {
+      const int key = k0 + (lane & 31);
+      load_cols<T, DT>(kb + (int64_t)key * a.k_row, key < d.kl, a.dim, kf);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int x = lane + 64 * i, r = x / kChunks, c = x % kChunks;
+        vw[i] = (u32x4)(0);
+        if (k0 + r < d.kl && c * 8 < a.dim)
+          vw[i] = *(const u32x4*)(vb + (int64_t)(k0 + r) * a.v_row + c * 8);
+      }
+    };
+    int k0 = key_lo + wave * 32;
+    if (k0 < end) fetch(k0);
+    for (; k0 < end; k0 += kPieceKeys) {
+      f32x16 s[1] = {(f32x16)(0.0f)};
+#pragma unroll
+      for (int ks = 0; ks < DT / 16; ++ks) s[0] = Mat<T>::mul(kf[ks], qf[ks], s[0]);
+      // the wavefront's own tile: its earlier reads are done, in order
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int x = lane + 64 * i;
+        *(u32x4*)(s_v + place<DT>(x / kChunks, x % kChunks)) = vw[i];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      const int next = k0 + kPieceKeys;
+      if (next < end) fetch(next);
+      make_scores<kMode>(s[0], sc, slope, col.pos - k0);
+      // past the piece's end are other pieces' keys
+      softmax_step<DT, 1>(s, mul, k0 + 32 > min(wave_lo, key_hi), k0, min(col.lim, key_hi), m, l,
+                          o);
+      add_cols<T, DT>(s_v, 0, s[0], o);
+    }
+    l = both_sum(l);
+    __syncthreads();
+    if (half == 0) {
+      s_m[wave][lane] = m;
+      s_l[wave][lane] = l;
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT / 32; ++dt) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 x = {o[dt][4 * i], o[dt][4 * i + 1], o[dt][4 * i + 2], o[dt][4 * i + 3]};
+        *(f32x4*)(s_raw + (wave * 32 + (lane & 31)) * kStride + dt * 32 + 8 * i + 4 * half) = x;
+      }
+    }
+    __syncthreads();
+    // eight lanes a column join the four wavefronts, in order
+    const int cc = threadIdx.x >> 3, e0 = (threadIdx.x & 7) * (DT / 8);
+    const uint32_t c = col0 + cc;
+    if (c < cols) {
+      const Col w = column(a, d, hk, c, cols);
+      float top = s_m[0][cc];
+#pragma unroll
+      for (int i = 1; i < 4; ++i) top = fmaxf(top, s_m[i][cc]);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      float f[4], sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[i] = __builtin_amdgcn_exp2f(s_m[i][cc] - ref);
+        sum = fmaf(f[i], s_l[i][cc], sum);
+      }
+      const int64_t row = d.qs + w.token;
+      const int64_t at = ((int64_t)piece * a.heads_q + w.head) * a.docs.rows_q + row;
+      const bool last = pieces == 1, none = w.lim <= 0;
+      const float inv = none || sum == 0.0f ? 0.0f : 1.0f / sum;
+      for (int e = e0; e < e0 + DT / 8 && e < a.dim; e += 8) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[j] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[j] = fmaf(f[i], s_raw[(i * 32 + cc) * kStride + e + j], x[j]);
+          if (last) x[j] = none ? 0.0f : x[j] * inv;
+        }
+        if (last)
+          store_elems((T*)(a.out0 + row * a.out0_row + (int64_t)w.head * a.out0_head + e), x);
+        else
+          store_elems(a.part_o + at * a.dim + e, x);
+      }
+      if ((threadIdx.x & 7) == 0) {
+        if (!last) {
+          a.part_ml[at * 2] = top;
+          a.part_ml[at * 2 + 1] = sum;
+        } else if (a.lse) {
+          a.lse[(int64_t)w.head * a.docs.rows_q + row] =
+              none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// The pieces of each column, joined in order; 16 lanes a column, 8 elements a
+// lane.
+template <typename T>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+  const int doc = blockIdx.x / a.heads_q, head = blockIdx.x % a.heads_q;
+  const Doc d = load_doc(a.docs, doc);
+  const int pieces = max(1, min(a.pieces, (d.kl + a.piece - 1) / a.piece));
+  if (pieces == 1) return;
+  const int e = (threadIdx.x & 15) * 8;
+  const int64_t step = (int64_t)a.heads_q * a.docs.rows_q;
+  for (int t = threadIdx.x >> 4; t < d.ql; t += 16) {
+    const int64_t at = (int64_t)head * a.docs.rows_q + d.qs + t;
     float top = -INFINITY;
+    for (int i = threadIdx.x & 15; i < pieces; i += 16)
+      top = fmaxf(top, a.part_ml[(at + i * step) * 2]);
 #pragma unroll
-    for (int rt = 0; rt < 2; ++rt) {
-      const int kr = k0 + rt * 32;
-      scores<false>(a, s[rt], mul, cap_in, cap_out,
-                    [&](int i) { return slope * fabsf((float)(pos - kr - result_row(i))); },
-                    nullptr);
-      if (k0 + kKeys > wave_lo) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[rt][i] = kr + result_row(i) < lim ? s[rt][i] : -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[rt][i]);
-    }
-    top = fmaxf(m, both_max(top));
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 16));
     const float ref = top == -INFINITY ? 0.0f : top;
-    if (__any(top > m)) {
-      const float alpha = __builtin_amdgcn_exp2f(m - ref);
-      l *= alpha;
+    float sum = 0.0f, x[8];
 #pragma unroll
-      for (int i = 0; i < DT / 32; ++i) o[i] *= alpha;
-      m = top;
-    }
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[rt][i] = __builtin_amdgcn_exp2f(s[rt][i] - ref);
-        l += s[rt][i];
-      }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const V8 p = pack_cols<T>(s[rt], ks);
-#pragma unroll
-        for (int dt = 0; dt < DT / 32; ++dt)
-          o[dt] = Mat<T>::mul(read_cols<T, DT>(s_v, rt * 32 + ks * 16, dt * 32), p, o[dt]);
-      }
-    }
-  }
-  l = both_sum(l);
-  if (!ok) return;
-  const bool none = lim <= 0;
-  const float inv = none || l == 0.0f ? 0.0f : 1.0f / l;
-  uint16_t* po = a.out0 + (int64_t)(d.qs + token) * a.out0_row + (int64_t)head * a.out0_head;
-#pragma unroll
-  for (int dt = 0; dt < DT / 32; ++dt) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = dt * 32 + 8 * i + 4 * half;
+    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
+    for (int i = 0; i < pieces; ++i) {
+      const f32x2 ml = *(const f32x2*)(a.part_ml + (at + i * step) * 2);
+      const float f = __builtin_amdgcn_exp2f(ml.x - ref);
+      sum = fmaf(f, ml.y, sum);
       if (e < a.dim) {
-        float x[4];
+        float y[8];
+        load_elems(a.part_o + (at + i * step) * a.dim + e, y);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = none ? 0.0f : o[dt][4 * i + j] * inv;
-        store_elems((T*)(po + e), x);
+        for (int j = 0; j < 8; ++j) x[j] = fmaf(f, y[j], x[j]);
       }
     }
+    const bool none = key_limit(a, d, t) <= 0;
+    const float inv = none || sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (e < a.dim) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = none ? 0.0f : x[j] * inv;
+      store_elems((T*)(a.out0 + (int64_t)(d.qs + t) * a.out0_row + (int64_t)head * a.out0_head + e),
+                  x);
+    }
+    if (a.lse && e == 0)
+      a.lse[at] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
   }
-  if (a.lse && half == 0)
-    a.lse[(int64_t)head * a.docs.rows_q + d.qs + token] =
-        none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------
@@ -351,13 +657,35 @@ __global__ __launch_bounds__(256) void attention_delta_kernel(AttnArgs a) {
   if (lane == 0) a.delta[(int64_t)head * a.docs.rows_q + row] = sum;
 }
 
+// p and ds of one 32 x 32 tile, in place of the products s and dp: register i
+// has the logarithm lse(i), delta(i) and the bias away(i).
+template <int kMode, typename Lse, typename Delta, typename Away>
+__device__ inline void weigh(f32x16& s, f32x16& dp, const Scale& c, Lse lse, Delta delta,
+                             Away away) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float f;
+    const float x = score<kMode>(s[i], c, [&] { return away(i); }, f);
+    const float p = __builtin_amdgcn_exp2f(kMode == 0 ? fmaf(x, c.mul, -lse(i)) : x - lse(i));
+    float g = p * (dp[i] - delta(i));
+    if constexpr (kMode & kCap) g *= f;
+    s[i] = p;
+    dp[i] = g;
+  }
+}
+
 // dq: the forward's loop, with p from the stored logarithm of the sum.
-template <typename T, int DT>
+// delta = do.o carries the rounding of o, which in rows of few keys (where o
+// is as large as a value) would be half of the gradient's error.  Rows whose
+// keys all stand in the first tile therefore take delta = sum_j p_j dp_j,
+// which is the same number without that rounding, and leave it for the dk, dv
+// kernel.
+template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
-  __shared__ __align__(16) uint16_t s_k[kKeys * DT];
-  __shared__ __align__(16) uint16_t s_v[kKeys * DT];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
+  __shared__ __align__(16) uint16_t s_k[2][kKeys * DT];
+  __shared__ __align__(16) uint16_t s_v[2][kKeys * DT];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int hk = blockIdx.x % a.heads_k;
   uint32_t local, units;
   const int doc = find_document(a.docs.q_start, a.docs.q_len, a.docs.rows_q, a.docs.count,
@@ -366,224 +694,277 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   const Doc d = load_doc(a.docs, doc);
   const uint32_t col0 = (units - 1 - local) * kCols;
   const uint32_t cols = (uint32_t)d.ql * a.group;
-  const uint32_t c = col0 + wave * 32 + (lane & 31);
-  const bool ok = c < cols;
-  const int token = (int)(c / a.group), head = hk * a.group + (int)(c % a.group);
-  const int lim = key_limit(a, d, token);
-  const int pos = token + d.kl - d.ql;
+  const Col col = column(a, d, hk, col0 + wave * 32 + (lane & 31), cols);
+  const int64_t row = d.qs + col.token;
+  const bool any = col.ok && col.lim > 0;
   V8 qf[DT / 16], df[DT / 16];
-  load_cols<T, DT>(a.q + (int64_t)(d.qs + token) * a.q_row + (int64_t)head * a.q_head, ok, a.dim,
-                   qf);
-  load_cols<T, DT>(a.d + (int64_t)(d.qs + token) * a.d_row + (int64_t)head * a.d_head, ok, a.dim,
-                   df);
-  float lse = INFINITY, delta = 0.0f;
-  if (ok && lim > 0) {
-    const int64_t at = (int64_t)head * a.docs.rows_q + d.qs + token;
-    lse = a.lse[at] * kLog2e;
-    delta = a.delta[at];
-  }
-  const float mul = a.scale * kLog2e;
-  const float cap_in = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
-  const float cap_out = a.softcap * kLog2e;
-  const float slope = a.slopes && ok ? a.slopes[head] * kLog2e : 0.0f;
+  load_cols<T, DT>(a.q + row * a.q_row + (int64_t)col.head * a.q_head, col.ok, a.dim, qf);
+  load_cols<T, DT>(a.d + row * a.d_row + (int64_t)col.head * a.d_head, col.ok, a.dim, df);
+  const int64_t at = (int64_t)col.head * a.docs.rows_q + row;
+  const float lse = any ? a.lse[at] * kLog2e : INFINITY;
+  float delta = any ? a.delta[at] : 0.0f;
+  const float slope = (kMode & kGeneral) && a.slopes && col.ok ? a.slopes[col.head] * kLog2e
+                                                               : 0.0f;
+  const Scale sc = scale_of<kMode>(a);
   f32x16 g[DT / 32];
 #pragma unroll
   for (int i = 0; i < DT / 32; ++i) g[i] = (f32x16)(0.0f);
   const int last_token = (int)((min(col0 + kCols, cols) - 1) / a.group);
   const int end = key_limit(a, d, last_token);
-  const int wave_lo = __builtin_amdgcn_readlane(lim, 0);
-  const int wave_hi = min(__builtin_amdgcn_readlane(lim, 31), end);
+  const int wave_lo = __builtin_amdgcn_readlane(col.lim, 0);
+  const int wave_hi = min(__builtin_amdgcn_readlane(col.lim, 31), end);
   const uint16_t* kb = a.k + (int64_t)d.ks * a.k_row + (int64_t)hk * a.k_head;
   const uint16_t* vb = a.v + (int64_t)d.ks * a.v_row + (int64_t)hk * a.v_head;
-  for (int k0 = 0; k0 < end; k0 += kKeys) {
-    __syncthreads();
-    stage_keys<DT, kKeys>(s_k, kb + (int64_t)k0 * a.k_row, a.k_row, d.kl - k0, a.dim);
-    stage_keys<DT, kKeys>(s_v, vb + (int64_t)k0 * a.v_row, a.v_row, d.kl - k0, a.dim);
-    __syncthreads();
-    if (k0 >= wave_hi) continue;
+  Staged<DT, kKeys> sk, sv;
+  if (end > 0) {
+    sk.load(kb, a.k_row, d.kl, a.dim);
+    sv.load(vb, a.v_row, d.kl, a.dim);
+    sk.store(s_k[0]);
+    sv.store(s_v[0]);
+  }
+  // p (in s) and ds (in dp) of the 32 keys from k0 + r0
+  auto tile = [&](int buf, int k0, int r0, f32x16& s, f32x16& dp) {
+    s = times_rows<T, DT>(s_k[buf], r0, qf);
+    dp = times_rows<T, DT>(s_v[buf], r0, df);
+    const int off = col.pos - k0 - r0;
+    weigh<kMode>(s, dp, sc, [&](int) { return lse; }, [&](int) { return delta; },
+                 [&](int i) { return slope * fabsf((float)(off - result_row(i))); });
+    if (k0 + kKeys > wave_lo) {
 #pragma unroll
-    for (int rt = 0; rt < 2; ++rt) {
-      f32x16 s = (f32x16)(0.0f), dp = (f32x16)(0.0f);
-#pragma unroll
-      for (int ks = 0; ks < DT / 16; ++ks) {
-        s = Mat<T>::mul(read_rows<T, DT>(s_k, rt * 32, ks), qf[ks], s);
-        dp = Mat<T>::mul(read_rows<T, DT>(s_v, rt * 32, ks), df[ks], dp);
-      }
-      const int kr = k0 + rt * 32;
-      float t[16];
-      scores<true>(a, s, mul, cap_in, cap_out,
-                   [&](int i) { return slope * fabsf((float)(pos - kr - result_row(i))); }, &t);
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        s[i] = __builtin_amdgcn_exp2f(s[i] - lse) * (dp[i] - delta);
-      if (a.softcap > 0.0f) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] *= t[i];
-      }
-      if (k0 + kKeys > wave_lo) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = kr + result_row(i) < lim ? s[i] : 0.0f;
-      }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const V8 p = pack_cols<T>(s, ks);
-#pragma unroll
-        for (int dt = 0; dt < DT / 32; ++dt)
-          g[dt] = Mat<T>::mul(read_cols<T, DT>(s_k, rt * 32 + ks * 16, dt * 32), p, g[dt]);
+      for (int i = 0; i < 16; ++i) {
+        const bool seen = k0 + r0 + result_row(i) < col.lim;
+        s[i] = seen ? s[i] : 0.0f;
+        dp[i] = seen ? dp[i] : 0.0f;
       }
     }
-  }
-  if (!ok) return;
-  const bool none = lim <= 0;
-  uint16_t* po = a.out0 + (int64_t)(d.qs + token) * a.out0_row + (int64_t)head * a.out0_head;
+  };
+  int buf = 0;
+  for (int k0 = 0; k0 < end; k0 += kKeys, buf ^= 1) {
+    __syncthreads();
+    const bool more = k0 + kKeys < end;
+    if (more) {
+      sk.load(kb + (int64_t)(k0 + kKeys) * a.k_row, a.k_row, d.kl - k0 - kKeys, a.dim);
+      sv.load(vb + (int64_t)(k0 + kKeys) * a.v_row, a.v_row, d.kl - k0 - kKeys, a.dim);
+    }
+    if (k0 == 0 && wave_lo <= kKeys && wave_hi > 0) {
+      // sum_j p_j dp_j of the rows that end in this tile
+      float sum = 0.0f;
+#pragma unroll 1
+      for (int r0 = 0; r0 < kKeys; r0 += 32) {
+        f32x16 s = times_rows<T, DT>(s_k[0], r0, qf), dp = times_rows<T, DT>(s_v[0], r0, df);
 #pragma unroll
-  for (int dt = 0; dt < DT / 32; ++dt) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = dt * 32 + 8 * i + 4 * half;
-      if (e < a.dim) {
-        float x[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = none ? 0.0f : g[dt][4 * i + j] * a.scale;
-        store_elems((T*)(po + e), x);
+        for (int i = 0; i < 16; ++i) {
+          float f;
+          const int off = col.pos - r0 - result_row(i);
+          const float x = score<kMode>(s[i], sc, [&] { return slope * fabsf((float)off); }, f);
+          const float p = __builtin_amdgcn_exp2f(kMode == 0 ? fmaf(x, sc.mul, -lse) : x - lse);
+          if (r0 + result_row(i) < col.lim) sum = fmaf(p, dp[i], sum);
+        }
+      }
+      sum = both_sum(sum);
+      if (any && col.lim <= kKeys) {
+        delta = sum;
+        if (lane < 32) a.delta[at] = sum;
       }
     }
+    if (k0 < wave_hi) {
+#pragma unroll
+      for (int r0 = 0; r0 < kKeys; r0 += 32) {
+        f32x16 s, dp;
+        tile(buf, k0, r0, s, dp);
+        add_cols<T, DT>(s_k[buf], r0, dp, g);
+      }
+    }
+    if (more) {
+      sk.store(s_k[buf ^ 1]);
+      sv.store(s_v[buf ^ 1]);
+    }
   }
+  if (!col.ok) return;
+  const bool none = col.lim <= 0;
+  store_col<T, DT>(a.out0 + row * a.out0_row + (int64_t)col.head * a.out0_head, a.dim,
+                   [&](int dt, int i) { return none ? 0.0f : g[dt][i] * a.scale; });
 }
 
-// dk and dv: a workgroup owns 128 keys of one key head and walks the tokens
-// (with all their heads of the group) that may see them.
-template <typename T, int DT>
+// dk and dv: a wavefront owns 32 keys of one key head, a workgroup 128, and
+// walks the tokens that may see them, 32 at a time, for one query head after
+// the other.  With a.parts a workgroup takes one query head of the group and
+// leaves fp32 sums, which attention_heads_kernel adds over the group in order:
+// with few keys there are otherwise too few workgroups to fill the chip.
+// Heads of 128 elements keep the workgroup's values in LDS: beside both
+// accumulators and the keys there is no room for them in registers.
+template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
-  __shared__ __align__(16) uint16_t s_q[kRows * DT];
-  __shared__ __align__(16) uint16_t s_d[kRows * DT];
-  __shared__ __align__(16) float s_lse[kRows], s_delta[kRows], s_slope[kRows];
-  __shared__ __align__(16) int s_lim[kRows], s_pos[kRows];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-  const int hk = blockIdx.x % a.heads_k;
+  constexpr bool kValuesInLds = DT == 128;
+  __shared__ __align__(16) uint16_t s_q[2][kRows * DT];
+  __shared__ __align__(16) uint16_t s_d[2][kRows * DT];
+  __shared__ __align__(16) uint16_t s_v[kValuesInLds ? kCols * DT : 8];
+  __shared__ __align__(16) float s_lse[2][kRows], s_delta[2][kRows];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int heads = a.parts ? a.heads_q : a.heads_k;
+  const int hb = blockIdx.x % heads;
+  const int hk = a.parts ? hb / a.group : hb;
+  const int head0 = a.parts ? hb : hb * a.group, nheads = a.parts ? 1 : a.group;
   uint32_t local, units;
   const int doc = find_document(a.docs.k_start, a.docs.k_len, a.docs.rows_k, a.docs.count, 1,
-                                kKeyCols, blockIdx.x / a.heads_k, &local, &units);
+                                kCols, blockIdx.x / heads, &local, &units);
   if (doc < 0) return;
   const Doc d = load_doc(a.docs, doc);
-  const int key0 = (int)local * kKeyCols;
+  const int key0 = (int)local * kCols;
   const int wkey = key0 + wave * 32;
   const int key = wkey + (lane & 31);
   const bool ok = key < d.kl;
-  V8 kf[DT / 16], vf[DT / 16];
-  load_cols<T, DT>(a.k + (int64_t)(d.ks + key) * a.k_row + (int64_t)hk * a.k_head, ok, a.dim, kf);
-  load_cols<T, DT>(a.v + (int64_t)(d.ks + key) * a.v_row + (int64_t)hk * a.v_head, ok, a.dim, vf);
-  const float mul = a.scale * kLog2e;
-  const float cap_in = a.softcap > 0.0f ? a.scale / a.softcap : 0.0f;
-  const float cap_out = a.softcap * kLog2e;
+  const int64_t row = d.ks + key;
+  V8 kf[DT / 16], vf[kValuesInLds ? 1 : DT / 16];
   f32x16 gk[DT / 32], gv[DT / 32];
+  load_cols<T, DT>(a.k + row * a.k_row + (int64_t)hk * a.k_head, ok, a.dim, kf);
+  if constexpr (kValuesInLds) {
+    Staged<DT, kCols> sv;
+    sv.load(a.v + (int64_t)(d.ks + key0) * a.v_row + (int64_t)hk * a.v_head, a.v_row, d.kl - key0,
+            a.dim);
+    sv.store(s_v);
+  } else {
+    load_cols<T, DT>(a.v + row * a.v_row + (int64_t)hk * a.v_head, ok, a.dim, vf);
+  }
 #pragma unroll
   for (int i = 0; i < DT / 32; ++i) gk[i] = gv[i] = (f32x16)(0.0f);
-  const uint32_t cols = (uint32_t)d.ql * a.group;
-  // the first token that sees key0
-  uint32_t c0 = 0;
-  if (a.causal && key0 >= d.prefix)
-    c0 = (uint32_t)max(key0 - (d.kl - d.ql), 0) * a.group / kRows * kRows;
-  for (; c0 < cols; c0 += kRows) {
-    __syncthreads();
-    constexpr int kChunks = DT / 8;
-#pragma unroll
-    for (int i = 0; i < kRows * kChunks / 256; ++i) {
-      const int x = threadIdx.x + 256 * i, r = x / kChunks, ch = x % kChunks;
-      const uint32_t c = c0 + r;
-      const int token = (int)(c / a.group), head = hk * a.group + (int)(c % a.group);
-      u32x4 wq = {0, 0, 0, 0}, wd = {0, 0, 0, 0};
-      if (c < cols && ch * 8 < a.dim) {
-        wq = *(const u32x4*)(a.q + (int64_t)(d.qs + token) * a.q_row + (int64_t)head * a.q_head +
-                             ch * 8);
-        wd = *(const u32x4*)(a.d + (int64_t)(d.qs + token) * a.d_row + (int64_t)head * a.d_head +
-                             ch * 8);
-      }
-      *(u32x4*)(s_q + place<DT>(r, ch)) = wq;
-      *(u32x4*)(s_d + place<DT>(r, ch)) = wd;
-    }
+  const Scale sc = scale_of<kMode>(a);
+  // the first token that sees key0, and the tiles of a head
+  const int shift = d.kl - d.ql;
+  int first = 0;
+  if (a.causal && key0 >= d.prefix) first = min(max(key0 - shift, 0), d.ql) / kRows * kRows;
+  const int tiles = (d.ql - first + kRows - 1) / kRows;
+  Staged<DT, kRows> sq, sd;
+  float r_lse = 0.0f, r_delta = 0.0f;
+  // tokens t0 .. t0 + 31 of head head0 + h
+  auto fetch = [&](int h, int t0) {
+    const int64_t r = d.qs + t0;
+    sq.load(a.q + r * a.q_row + (int64_t)(head0 + h) * a.q_head, a.q_row, d.ql - t0, a.dim);
+    sd.load(a.d + r * a.d_row + (int64_t)(head0 + h) * a.d_head, a.d_row, d.ql - t0, a.dim);
     if (threadIdx.x < kRows) {
-      const uint32_t c = c0 + threadIdx.x;
-      const int token = (int)(c / a.group), head = hk * a.group + (int)(c % a.group);
-      const int lim = key_limit(a, d, token);
-      float lse = INFINITY, delta = 0.0f, slope = 0.0f;
-      if (c < cols) {
-        const int64_t at = (int64_t)head * a.docs.rows_q + d.qs + token;
-        if (lim > 0) {
-          lse = a.lse[at] * kLog2e;
-          delta = a.delta[at];
-        }
-        if (a.slopes) slope = a.slopes[head] * kLog2e;
+      const int t = t0 + (int)threadIdx.x;
+      r_lse = INFINITY;
+      r_delta = 0.0f;
+      if (t < d.ql && key_limit(a, d, t) > 0) {
+        const int64_t at = (int64_t)(head0 + h) * a.docs.rows_q + d.qs + t;
+        r_lse = a.lse[at] * kLog2e;
+        r_delta = a.delta[at];
       }
-      s_lse[threadIdx.x] = lse;
-      s_delta[threadIdx.x] = delta;
-      s_slope[threadIdx.x] = slope;
-      s_lim[threadIdx.x] = lim;
-      s_pos[threadIdx.x] = token + d.kl - d.ql;
     }
-    __syncthreads();
-    if (s_lim[kRows - 1] <= wkey) continue;
-    const bool full = s_lim[0] >= wkey + 32;
+  };
+  auto put = [&](int buf) {
+    sq.store(s_q[buf]);
+    sd.store(s_d[buf]);
+    if (threadIdx.x < kRows) {
+      s_lse[buf][threadIdx.x] = r_lse;
+      s_delta[buf][threadIdx.x] = r_delta;
+    }
+  };
+  if (tiles > 0) {
+    fetch(0, first);
+    put(0);
+  }
+  int buf = 0;
+  for (int h = 0; h < nheads; ++h) {
+    const float slope = (kMode & kGeneral) && a.slopes ? a.slopes[head0 + h] * kLog2e : 0.0f;
+    for (int t0 = first; t0 < d.ql; t0 += kRows, buf ^= 1) {
+      __syncthreads();
+      const bool wrap = t0 + kRows >= d.ql, more = !wrap || h + 1 < nheads;
+      if (more) fetch(wrap ? h + 1 : h, wrap ? first : t0 + kRows);
+      // limits of the tile's rows grow with the token
+      if (wkey < key_limit(a, d, t0 + kRows - 1)) {
+        f32x16 s = times_rows<T, DT>(s_q[buf], 0, kf), dp;
+        if constexpr (kValuesInLds) {
+          dp = (f32x16)(0.0f);
 #pragma unroll
-    for (int rt = 0; rt < kRows / 32; ++rt) {
-      f32x16 s = (f32x16)(0.0f), dp = (f32x16)(0.0f);
-#pragma unroll
-      for (int ks = 0; ks < DT / 16; ++ks) {
-        s = Mat<T>::mul(read_rows<T, DT>(s_q, rt * 32, ks), kf[ks], s);
-        dp = Mat<T>::mul(read_rows<T, DT>(s_d, rt * 32, ks), vf[ks], dp);
-      }
-      float t[16];
-      scores<true>(a, s, mul, cap_in, cap_out,
-                   [&](int i) {
-                     const int r = rt * 32 + result_row(i);
-                     return s_slope[r] * fabsf((float)(s_pos[r] - key));
-                   },
-                   &t);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = rt * 32 + result_row(i);
-        float p = __builtin_amdgcn_exp2f(s[i] - s_lse[r]);
-        float x = p * (dp[i] - s_delta[r]);
-        if (a.softcap > 0.0f) x *= t[i];
-        if (!full) {
-          const bool seen = key < s_lim[r];
-          p = seen ? p : 0.0f;
-          x = seen ? x : 0.0f;
+          for (int ks = 0; ks < DT / 16; ++ks) {
+            dp = Mat<T>::mul(read_rows<T, DT>(s_d[buf], 0, ks),
+                             read_rows<T, DT>(s_v, wave * 32, ks), dp);
+            if (ks & 1) __builtin_amdgcn_sched_barrier(0);
+          }
+        } else {
+          dp = times_rows<T, DT>(s_d[buf], 0, vf);
         }
-        s[i] = p;
-        dp[i] = x;
-      }
+        const int off = t0 + shift - key;
+        weigh<kMode>(s, dp, sc, [&](int i) { return s_lse[buf][result_row(i)]; },
+                     [&](int i) { return s_delta[buf][result_row(i)]; },
+                     [&](int i) { return slope * fabsf((float)(off + result_row(i))); });
+        if (key_limit(a, d, t0) < wkey + 32) {
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const V8 p = pack_cols<T>(s, ks), x = pack_cols<T>(dp, ks);
-#pragma unroll
-        for (int dt = 0; dt < DT / 32; ++dt) {
-          gv[dt] = Mat<T>::mul(read_cols<T, DT>(s_d, rt * 32 + ks * 16, dt * 32), p, gv[dt]);
-          gk[dt] = Mat<T>::mul(read_cols<T, DT>(s_q, rt * 32 + ks * 16, dt * 32), x, gk[dt]);
+          for (int i = 0; i < 16; ++i) {
+            const bool seen = key < key_limit(a, d, t0 + result_row(i));
+            s[i] = seen ? s[i] : 0.0f;
+            dp[i] = seen ? dp[i] : 0.0f;
+          }
         }
+        add_cols<T, DT>(s_d[buf], 0, s, gv);
+        add_cols<T, DT>(s_q[buf], 0, dp, gk);
       }
+      if (more) put(buf ^ 1);
     }
   }
   if (!ok) return;
-  uint16_t* pk = a.out0 + (int64_t)(d.ks + key) * a.out0_row + (int64_t)hk * a.out0_head;
-  uint16_t* pv = a.out1 + (int64_t)(d.ks + key) * a.out1_row + (int64_t)hk * a.out1_head;
+  if (a.parts) {
+    // [key row][query head][dk, dv][dim]
+    float* p = a.part_o + (row * a.heads_q + hb) * 2 * a.dim;
 #pragma unroll
-  for (int dt = 0; dt < DT / 32; ++dt) {
+    for (int dt = 0; dt < DT / 32; ++dt) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = dt * 32 + 8 * i + 4 * half;
-      if (e < a.dim) {
-        float x[4], y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[j] = gk[dt][4 * i + j] * a.scale;
-          y[j] = gv[dt][4 * i + j];
+      for (int i = 0; i < 4; ++i) {
+        const int e = dt * 32 + 8 * i + 4 * (lane >> 5);
+        if (e < a.dim) {
+          const f32x4 x = {gk[dt][4 * i], gk[dt][4 * i + 1], gk[dt][4 * i + 2],
+                           gk[dt][4 * i + 3]};
+          const f32x4 y = {gv[dt][4 * i], gv[dt][4 * i + 1], gv[dt][4 * i + 2],
+                           gv[dt][4 * i + 3]};
+          *(f32x4*)(p + e) = x;
+          *(f32x4*)(p + a.dim + e) = y;
         }
-        store_elems((T*)(pk + e), x);
-        store_elems((T*)(pv + e), y);
       }
     }
+  } else {
+    store_col<T, DT>(a.out0 + row * a.out0_row + (int64_t)hk * a.out0_head, a.dim,
+                     [&](int dt, int i) { return gk[dt][i] * a.scale; });
+    store_col<T, DT>(a.out1 + row * a.out1_row + (int64_t)hk * a.out1_head, a.dim,
+                     [&](int dt, int i) { return gv[dt][i]; });
+  }
+}
+
+// Sums of a key head's dk and dv over its query heads, in order: 64 keys a
+// workgroup, 16 lanes a key, 8 elements a lane.
+template <typename T>
+__global__ __launch_bounds__(256) void attention_heads_kernel(AttnArgs a) {
+  const int hk = blockIdx.x % a.heads_k;
+  uint32_t local, units;
+  const int doc = find_document(a.docs.k_start, a.docs.k_len, a.docs.rows_k, a.docs.count, 1, 64,
+                                blockIdx.x / a.heads_k, &local, &units);
+  if (doc < 0) return;
+  const Doc d = load_doc(a.docs, doc);
+  const int e = (threadIdx.x & 15) * 8;
+  if (e >= a.dim) return;
+  for (int i = 0; i < 4; ++i) {
+    const int key = (int)local * 64 + i * 16 + (threadIdx.x >> 4);
+    if (key >= d.kl) return;
+    const int64_t row = d.ks + key;
+    float x[8], y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
+    const float* p = a.part_o + (row * a.heads_q + (int64_t)hk * a.group) * 2 * a.dim + e;
+    for (int h = 0; h < a.group; ++h, p += 2 * a.dim) {
+      float u[8], w[8];
+      load_elems(p, u);
+      load_elems(p + a.dim, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] += u[j];
+        y[j] += w[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= a.scale;
+    store_elems((T*)(a.out0 + row * a.out0_row + (int64_t)hk * a.out0_head + e), x);
+    store_elems((T*)(a.out1 + row * a.out1_row + (int64_t)hk * a.out1_head + e), y);
   }
 }
 
@@ -623,45 +1004,121 @@ int64_t unit_bound(int64_t columns, int64_t step, int32_t count) {
   return columns / step + count;
 }
 
-template <typename T, int DT>
-hipError_t run_fwd(const AttnArgs& a, hipStream_t s) {
-  const int64_t units = unit_bound((int64_t)a.docs.rows_q * a.group, kCols, a.docs.count);
-  attention_fwd_kernel<T, DT><<<dim3((uint32_t)(units * a.heads_k)), dim3(256), 0, s>>>(a);
-  return hipGetLastError();
+// The one-token form: how many pieces a document's keys are cut into.
+struct Split {
+  bool step;
+  int pieces, piece, col_tiles;
+};
+Split split_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q,
+               int64_t rows_k) {
+  Split o = {};
+  const int64_t longest_q = d.max_q_len > 0 && d.max_q_len < rows_q ? d.max_q_len : rows_q;
+  const int64_t longest_k = d.max_k_len > 0 && d.max_k_len < rows_k ? d.max_k_len : rows_k;
+  const int64_t cols = longest_q * (cfg.heads_q / cfg.heads_k);
+  o.step = cols <= 32;
+  o.col_tiles = 1;
+  const int64_t base = (int64_t)d.count * cfg.heads_k;
+  const int64_t want = (2048 + base - 1) / base;
+  int64_t piece = (longest_k + want - 1) / want;
+  piece = (piece + kPieceKeys - 1) / kPieceKeys * kPieceKeys;
+  if (piece < 2 * kPieceKeys) piece = 2 * kPieceKeys;
+  o.piece = (int)piece;
+  o.pieces = (int)((longest_k + piece - 1) / piece);
+  if (o.pieces < 1) o.pieces = 1;
+  return o;
 }
 
-template <typename T, int DT>
-hipError_t run_bwd(AttnArgs a, const gs_heads& dq, const gs_heads& dk, const gs_heads& dv,
-                   hipStream_t s) {
-  if (a.docs.rows_q > 0) {
-    const int64_t items = (int64_t)a.docs.rows_q * a.heads_q;
-    attention_delta_kernel<T><<<dim3((uint32_t)((items + 15) / 16)), dim3(256), 0, s>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    a.out0 = (uint16_t*)dq.data; a.out0_row = dq.row; a.out0_head = dq.head;
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// The kernels of one element type, head size and way to make scores.
+template <typename T, int DT, int kMode>
+struct Run {
+  static hipError_t fwd(const AttnArgs& a, bool step, hipStream_t s) {
+    if (step) {
+      const int64_t blocks = (int64_t)a.docs.count * a.pieces * a.col_tiles * a.heads_k;
+      attention_step_kernel<T, DT, kMode><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess || a.pieces == 1) return e;
+      attention_join_kernel<T><<<dim3((uint32_t)((int64_t)a.docs.count * a.heads_q)), dim3(256),
+                                 0, s>>>(a);
+      return hipGetLastError();
+    }
     const int64_t units = unit_bound((int64_t)a.docs.rows_q * a.group, kCols, a.docs.count);
-    attention_dq_kernel<T, DT><<<dim3((uint32_t)(units * a.heads_k)), dim3(256), 0, s>>>(a);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    attention_fwd_kernel<T, DT, kMode>
+        <<<dim3((uint32_t)(units * a.heads_k)), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
   }
-  a.out0 = (uint16_t*)dk.data; a.out0_row = dk.row; a.out0_head = dk.head;
-  a.out1 = (uint16_t*)dv.data; a.out1_row = dv.row; a.out1_head = dv.head;
-  const int64_t units = unit_bound(a.docs.rows_k, kKeyCols, a.docs.count);
-  attention_dkv_kernel<T, DT><<<dim3((uint32_t)(units * a.heads_k)), dim3(256), 0, s>>>(a);
-  return hipGetLastError();
+
+  static hipError_t bwd(AttnArgs a, const gs_heads& dq, const gs_heads& dk, const gs_heads& dv,
+                        hipStream_t s) {
+    const dim3 block(256);
+    if (a.docs.rows_q > 0) {
+      const int64_t items = (int64_t)a.docs.rows_q * a.heads_q;
+      attention_delta_kernel<T><<<dim3((uint32_t)((items + 15) / 16)), block, 0, s>>>(a);
+      hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      a.out0 = (uint16_t*)dq.data; a.out0_row = dq.row; a.out0_head = dq.head;
+      const int64_t units = unit_bound((int64_t)a.docs.rows_q * a.group, kCols, a.docs.count);
+      attention_dq_kernel<T, DT, kMode><<<dim3((uint32_t)(units * a.heads_k)), block, 0, s>>>(a);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    a.out0 = (uint16_t*)dk.data; a.out0_row = dk.row; a.out0_head = dk.head;
+    a.out1 = (uint16_t*)dv.data; a.out1_row = dv.row; a.out1_head = dv.head;
+    const int64_t blocks = unit_bound(a.docs.rows_k, kCols, a.docs.count) *
+                           (a.parts ? a.heads_q : a.heads_k);
+    attention_dkv_kernel<T, DT, kMode><<<dim3((uint32_t)blocks), block, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.parts) return e;
+    const int64_t sums = unit_bound(a.docs.rows_k, 64, a.docs.count) * a.heads_k;
+    attention_heads_kernel<T><<<dim3((uint32_t)sums), block, 0, s>>>(a);
+    return hipGetLastError();
+  }
+};
+
+template <typename T, int DT, typename F>
+hipError_t with_mode(const AttnArgs& a, F f) {
+  const bool cap = a.softcap > 0.0f, general = a.slopes != nullptr || !(a.scale > 0.0f);
+  if (cap) return general ? f(Run<T, DT, kCap | kGeneral>()) : f(Run<T, DT, kCap>());
+  return general ? f(Run<T, DT, kGeneral>()) : f(Run<T, DT, 0>());
+}
+
+// Heads of up to 64 elements, or of up to 128 (shorter ones are filled with
+// zeros in LDS).
+template <typename F>
+hipError_t dispatch(const gs_attention_config& cfg, const AttnArgs& a, F f) {
+  if (cfg.dtype == GS_BF16)
+    return cfg.head_dim > 64 ? with_mode<Bf16, 128>(a, f) : with_mode<Bf16, 64>(a, f);
+  return cfg.head_dim > 64 ? with_mode<F16, 128>(a, f) : with_mode<F16, 64>(a, f);
+}
+
+// Whether dk and dv are summed per query head first: too few workgroups
+// otherwise, with as many as two to a compute unit.
+bool head_parts(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_k) {
+  return cfg.heads_q > cfg.heads_k &&
+         unit_bound(rows_k, kCols, d.count) * cfg.heads_k < 2048;
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t gs_attention_fwd_bytes(const gs_attention_config&, const gs_documents&, int64_t, int64_t) {
-  return 0;
+size_t gs_attention_fwd_bytes(const gs_attention_config& cfg, const gs_documents& d,
+                              int64_t rows_q, int64_t rows_k) {
+  if (d.count == 0 || rows_q == 0) return 0;
+  const Split p = split_of(cfg, d, rows_q, rows_k);
+  if (!p.step || p.pieces == 1) return 0;
+  const size_t columns = (size_t)p.pieces * cfg.heads_q * rows_q;
+  return align256(columns * 2 * sizeof(float)) + columns * cfg.head_dim * sizeof(float);
 }
 
-size_t gs_attention_bwd_bytes(const gs_attention_config& cfg, const gs_documents&, int64_t rows_q,
-                              int64_t) {
-  return (size_t)rows_q * cfg.heads_q * sizeof(float);
+size_t gs_attention_bwd_bytes(const gs_attention_config& cfg, const gs_documents& d,
+                              int64_t rows_q, int64_t rows_k) {
+  if (d.count == 0) return 0;
+  size_t n = align256((size_t)rows_q * cfg.heads_q * sizeof(float));
+  if (head_parts(cfg, d, rows_k))
+    n += (size_t)rows_k * cfg.heads_q * 2 * cfg.head_dim * sizeof(float);
+  return n;
 }
 
 hipError_t gs_launch_attention_fwd(const gs_attention_config& cfg, const gs_documents& d,
@@ -671,9 +1128,14 @@ hipError_t gs_launch_attention_fwd(const gs_attention_config& cfg, const gs_docu
   AttnArgs a = make_args(cfg, d, rows_q, rows_k, q, k, v);
   a.out0 = (uint16_t*)out.data; a.out0_row = out.row; a.out0_head = out.head;
   a.lse = lse;
-  if (cfg.dtype == GS_BF16)
-    return cfg.head_dim > 64 ? run_fwd<Bf16, 128>(a, s) : run_fwd<Bf16, 64>(a, s);
-  return cfg.head_dim > 64 ? run_fwd<F16, 128>(a, s) : run_fwd<F16, 64>(a, s);
+  const Split p = split_of(cfg, d, rows_q, rows_k);
+  a.pieces = p.pieces;
+  a.piece = p.piece;
+  a.col_tiles = p.col_tiles;
+  a.part_ml = (float*)workspace;
+  a.part_o = (float*)((char*)workspace +
+                      align256((size_t)p.pieces * cfg.heads_q * rows_q * 2 * sizeof(float)));
+  return dispatch(cfg, a, [&](auto run) { return run.fwd(a, p.step, s); });
 }
 
 hipError_t gs_launch_attention_bwd(const gs_attention_config& cfg, const gs_documents& d,
@@ -687,11 +1149,9 @@ hipError_t gs_launch_attention_bwd(const gs_attention_config& cfg, const gs_docu
   a.d = (const uint16_t*)dout.data; a.d_row = dout.row; a.d_head = dout.head;
   a.lse = const_cast<float*>(lse);
   a.delta = (float*)workspace;
-  if (cfg.dtype == GS_BF16)
-    return cfg.head_dim > 64 ? run_bwd<Bf16, 128>(a, dq, dk, dv, s)
-                             : run_bwd<Bf16, 64>(a, dq, dk, dv, s);
-  return cfg.head_dim > 64 ? run_bwd<F16, 128>(a, dq, dk, dv, s)
-                           : run_bwd<F16, 64>(a, dq, dk, dv, s);
+  a.part_o = (float*)((char*)workspace + align256((size_t)rows_q * cfg.heads_q * sizeof(float)));
+  a.parts = head_parts(cfg, d, rows_k);
+  return dispatch(cfg, a, [&](auto run) { return run.bwd(a, dq, dk, dv, s); });
 }
 
 }  // extern "C"
