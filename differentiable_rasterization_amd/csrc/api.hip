@@ -1097,6 +1097,14 @@ gs_status check_stride(int64_t stride) {
   return GS_OK;
 }
 
+// The attention kernels reach the rows of a tile with 32-bit byte offsets.
+constexpr int64_t kMaxAttentionRow = (int64_t)1 << 23;
+
+gs_status check_tile_row(const gs_heads* t) {
+  GS_REQUIRE(t->row < kMaxAttentionRow, "row strides of attention must be below 2^23");
+  return GS_OK;
+}
+
 // A [rows][heads][dim] view; an output's rows and heads must not overlap.
 gs_status check_heads(const gs_heads* t, int64_t rows, int64_t heads, int64_t dim, bool output) {
   GS_REQUIRE(t != nullptr && t->data != nullptr, "NULL array pointer");
@@ -1274,6 +1282,8 @@ gs_status gs_attention_fwd(const gs_attention_config* cfg, const gs_documents* d
   if (rows_k > 0) {
     GS_CHECK(check_heads(k, rows_k, cfg->heads_k, cfg->head_dim, false));
     GS_CHECK(check_heads(v, rows_k, cfg->heads_k, cfg->head_dim, false));
+    GS_CHECK(check_tile_row(k));
+    GS_CHECK(check_tile_row(v));
   }
   GS_CHECK(check_heads(out, rows_q, cfg->heads_q, cfg->head_dim, true));
   GS_REQUIRE(out->data != q->data && (rows_k == 0 || (out->data != k->data &&
@@ -1308,12 +1318,16 @@ gs_status gs_attention_bwd(const gs_attention_config* cfg, const gs_documents* d
     GS_CHECK(check_heads(dL_dout, rows_q, cfg->heads_q, cfg->head_dim, false));
     GS_CHECK(check_heads(dL_dq, rows_q, cfg->heads_q, cfg->head_dim, true));
     GS_REQUIRE(lse != nullptr, "lse is NULL");
+    GS_CHECK(check_tile_row(q));
+    GS_CHECK(check_tile_row(dL_dout));
   }
   if (rows_k > 0) {
     GS_CHECK(check_heads(k, rows_k, cfg->heads_k, cfg->head_dim, false));
     GS_CHECK(check_heads(v, rows_k, cfg->heads_k, cfg->head_dim, false));
     GS_CHECK(check_heads(dL_dk, rows_k, cfg->heads_k, cfg->head_dim, true));
     GS_CHECK(check_heads(dL_dv, rows_k, cfg->heads_k, cfg->head_dim, true));
+    GS_CHECK(check_tile_row(k));
+    GS_CHECK(check_tile_row(v));
     GS_REQUIRE(dL_dk->data != dL_dv->data, "dL_dk and dL_dv must not alias");
   }
   const void* in[6] = {rows_q > 0 ? q->data : nullptr, rows_k > 0 ? k->data : nullptr,

@@ -183,18 +183,28 @@ __device__ inline void load_cols(const uint16_t* p, bool ok, int dim,
 }
 
 // A tile of ROWS rows on its way into LDS: loaded into registers while the
-// tile before it is computed, zeros past `valid` rows and dim elements.
+// tile before it is computed.  The loads go through a buffer descriptor that
+// ends with the document's last row, so that rows past `valid` (and elements
+// past dim, whose offset is past every end) come back as zeros without a
+// branch; rows of a tile are within 2^31 bytes of each other (row strides are
+// below 2^23 elements).
 template <int DT, int ROWS>
 struct Staged {
   static constexpr int kChunks = DT / 8;
   static constexpr int kPer = ROWS * kChunks / 256;
   u32x4 w[kPer];
   __device__ inline void load(const uint16_t* base, int64_t row_stride, int valid, int dim) {
+    const int stride = (int)row_stride * 2;
+    const int64_t bytes = valid > 0 ? (int64_t)(valid - 1) * stride + dim * 2 : 0;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(base), 0, (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff),
+        0x00027000);
+    const int r = threadIdx.x / kChunks, c = threadIdx.x % kChunks;
+    int at = c * 8 < dim ? r * stride + c * 16 : (int)0x80000000;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int x = threadIdx.x + 256 * i, r = x / kChunks, c = x % kChunks;
-      w[i] = (u32x4)(0);
-      if (r < valid && c * 8 < dim) w[i] = *(const u32x4*)(base + (int64_t)r * row_stride + c * 8);
+      w[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0);
+      at = c * 8 < dim ? at + 256 / kChunks * stride : at;
     }
   }
   __device__ inline void store(uint16_t* tile) const {
@@ -314,6 +324,15 @@ __device__ inline Col column(const AttnArgs& a, const Doc& d, int hk, uint32_t c
 // ---------------------------------------------------------------------------
 // Forward
 // ---------------------------------------------------------------------------
+// The same value, unknown to the compiler.  Taken inside a uniform branch it
+// keeps what depends on it there: masks are needed in few tiles, and the
+// compiler would rather select in all of them (104 of the forward's 233 vector
+// instructions a tile).
+__device__ inline int only_here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // The running softmax of N 32-key tiles of a column, from key k0: masks,
 // moves the reference m where a score passes it by more than 8 (weights then
 // stay below 2^8, far inside every type, and the accumulators are rarely
@@ -322,11 +341,12 @@ template <int DT, int N>
 __device__ inline void softmax_step(f32x16 (&s)[N], float mul, bool masked, int k0, int lim,
                                     float& m, float& l, f32x16 (&o)[DT / 32]) {
   if (masked) {
+    const int room = only_here(lim - k0);
 #pragma unroll
     for (int rt = 0; rt < N; ++rt)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        s[rt][i] = k0 + rt * 32 + result_row(i) < lim ? s[rt][i] : -INFINITY;
+        s[rt][i] = rt * 32 + result_row(i) < room ? s[rt][i] : -INFINITY;
   }
   float top = -INFINITY;
 #pragma unroll
@@ -589,28 +609,30 @@ __global__ __launch_bounds__(256, 2) void attention_step_kernel(AttnArgs a) {
   }
 }
 
-// The pieces of each column, joined in order; 16 lanes a column, 8 elements a
-// lane.
+// The pieces of each column, joined in order: a workgroup a document and
+// head; 16 groups of 16 lanes (8 elements a lane) take every 16th piece, and
+// their sums are added in order.
 template <typename T>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+  __shared__ float s_x[16][16][9], s_sum[16];
   const int doc = blockIdx.x / a.heads_q, head = blockIdx.x % a.heads_q;
   const Doc d = load_doc(a.docs, doc);
   const int pieces = max(1, min(a.pieces, (d.kl + a.piece - 1) / a.piece));
   if (pieces == 1) return;
-  const int e = (threadIdx.x & 15) * 8;
+  const int sub = threadIdx.x & 15, group = threadIdx.x >> 4, e = sub * 8;
   const int64_t step = (int64_t)a.heads_q * a.docs.rows_q;
-  for (int t = threadIdx.x >> 4; t < d.ql; t += 16) {
+  for (int t = 0; t < d.ql; ++t) {
     const int64_t at = (int64_t)head * a.docs.rows_q + d.qs + t;
     float top = -INFINITY;
-    for (int i = threadIdx.x & 15; i < pieces; i += 16)
+    for (int i = threadIdx.x & 63; i < pieces; i += 64)
       top = fmaxf(top, a.part_ml[(at + i * step) * 2]);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 16));
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
     const float ref = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, x[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = 0.0f;
-    for (int i = 0; i < pieces; ++i) {
+    for (int i = group; i < pieces; i += 16) {
       const f32x2 ml = *(const f32x2*)(a.part_ml + (at + i * step) * 2);
       const float f = __builtin_amdgcn_exp2f(ml.x - ref);
       sum = fmaf(f, ml.y, sum);
@@ -621,16 +643,29 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
         for (int j = 0; j < 8; ++j) x[j] = fmaf(f, y[j], x[j]);
       }
     }
-    const bool none = key_limit(a, d, t) <= 0;
-    const float inv = none || sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (e < a.dim) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = none ? 0.0f : x[j] * inv;
-      store_elems((T*)(a.out0 + (int64_t)(d.qs + t) * a.out0_row + (int64_t)head * a.out0_head + e),
-                  x);
+    for (int j = 0; j < 8; ++j) s_x[group][sub][j] = x[j];
+    if (sub == 0) s_sum[group] = sum;
+    __syncthreads();
+    if (threadIdx.x < 16) {
+      for (int g = 1; g < 16; ++g) {
+        sum = g == 1 ? s_sum[0] + s_sum[1] : sum + s_sum[g];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] += s_x[g][sub][j];
+      }
+      const bool none = key_limit(a, d, t) <= 0;
+      const float inv = none || sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (e < a.dim) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = none ? 0.0f : x[j] * inv;
+        store_elems((T*)(a.out0 + (int64_t)(d.qs + t) * a.out0_row + (int64_t)head * a.out0_head +
+                         e),
+                    x);
+      }
+      if (a.lse && e == 0)
+        a.lse[at] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
     }
-    if (a.lse && e == 0)
-      a.lse[at] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    __syncthreads();
   }
 }
 
@@ -675,11 +710,12 @@ __device__ inline void weigh(f32x16& s, f32x16& dp, const Scale& c, Lse lse, Del
 }
 
 // dq: the forward's loop, with p from the stored logarithm of the sum.
-// delta = do.o carries the rounding of o, which in rows of few keys (where o
-// is as large as a value) would be half of the gradient's error.  Rows whose
-// keys all stand in the first tile therefore take delta = sum_j p_j dp_j,
-// which is the same number without that rounding, and leave it for the dk, dv
-// kernel.
+// delta = do.o carries the roundings of o and of the weights that made it.
+// Where a row leans on few keys, so that o is as large as a value, they would
+// be a third of the gradient's error.  Rows whose keys all stand in the first
+// tile, and all rows under a distance bias, therefore take delta =
+// sum_j p_j dp_j, the same number without those roundings, in a pass of its
+// own over their keys, and leave it for the dk, dv kernel.
 template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
@@ -716,70 +752,70 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   const uint16_t* kb = a.k + (int64_t)d.ks * a.k_row + (int64_t)hk * a.k_head;
   const uint16_t* vb = a.v + (int64_t)d.ks * a.v_row + (int64_t)hk * a.v_head;
   Staged<DT, kKeys> sk, sv;
-  if (end > 0) {
+  int buf = 0;
+  // the staged key tiles [0, last) in turn, each with its products' first key
+  auto walk = [&](int last, auto use) {
+    if (last <= 0) return;
+    __syncthreads();
     sk.load(kb, a.k_row, d.kl, a.dim);
     sv.load(vb, a.v_row, d.kl, a.dim);
-    sk.store(s_k[0]);
-    sv.store(s_v[0]);
-  }
-  // p (in s) and ds (in dp) of the 32 keys from k0 + r0
-  auto tile = [&](int buf, int k0, int r0, f32x16& s, f32x16& dp) {
-    s = times_rows<T, DT>(s_k[buf], r0, qf);
-    dp = times_rows<T, DT>(s_v[buf], r0, df);
-    const int off = col.pos - k0 - r0;
-    weigh<kMode>(s, dp, sc, [&](int) { return lse; }, [&](int) { return delta; },
-                 [&](int i) { return slope * fabsf((float)(off - result_row(i))); });
-    if (k0 + kKeys > wave_lo) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const bool seen = k0 + r0 + result_row(i) < col.lim;
-        s[i] = seen ? s[i] : 0.0f;
-        dp[i] = seen ? dp[i] : 0.0f;
+    sk.store(s_k[buf]);
+    sv.store(s_v[buf]);
+    for (int k0 = 0; k0 < last; k0 += kKeys, buf ^= 1) {
+      __syncthreads();
+      const bool more = k0 + kKeys < last;
+      if (more) {
+        sk.load(kb + (int64_t)(k0 + kKeys) * a.k_row, a.k_row, d.kl - k0 - kKeys, a.dim);
+        sv.load(vb + (int64_t)(k0 + kKeys) * a.v_row, a.v_row, d.kl - k0 - kKeys, a.dim);
+      }
+      if (k0 < wave_hi) use(k0);
+      if (more) {
+        sk.store(s_k[buf ^ 1]);
+        sv.store(s_v[buf ^ 1]);
       }
     }
   };
-  int buf = 0;
-  for (int k0 = 0; k0 < end; k0 += kKeys, buf ^= 1) {
-    __syncthreads();
-    const bool more = k0 + kKeys < end;
-    if (more) {
-      sk.load(kb + (int64_t)(k0 + kKeys) * a.k_row, a.k_row, d.kl - k0 - kKeys, a.dim);
-      sv.load(vb + (int64_t)(k0 + kKeys) * a.v_row, a.v_row, d.kl - k0 - kKeys, a.dim);
-    }
-    if (k0 == 0 && wave_lo <= kKeys && wave_hi > 0) {
-      // sum_j p_j dp_j of the rows that end in this tile
-      float sum = 0.0f;
+  const bool biased = (kMode & kGeneral) && a.slopes;
+  const int block_lo = key_limit(a, d, (int)(col0 / a.group));
+  if (biased || block_lo <= kKeys) {
+    float sum = 0.0f;
+    walk(biased ? end : min(end, kKeys), [&](int k0) {
 #pragma unroll 1
       for (int r0 = 0; r0 < kKeys; r0 += 32) {
-        f32x16 s = times_rows<T, DT>(s_k[0], r0, qf), dp = times_rows<T, DT>(s_v[0], r0, df);
+        const f32x16 s = times_rows<T, DT>(s_k[buf], r0, qf);
+        const f32x16 dp = times_rows<T, DT>(s_v[buf], r0, df);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float f;
-          const int off = col.pos - r0 - result_row(i);
-          const float x = score<kMode>(s[i], sc, [&] { return slope * fabsf((float)off); }, f);
+          const int at_key = k0 + r0 + result_row(i);
+          const float x = score<kMode>(
+              s[i], sc, [&] { return slope * fabsf((float)(col.pos - at_key)); }, f);
           const float p = __builtin_amdgcn_exp2f(kMode == 0 ? fmaf(x, sc.mul, -lse) : x - lse);
-          if (r0 + result_row(i) < col.lim) sum = fmaf(p, dp[i], sum);
+          sum = at_key < col.lim ? fmaf(p, dp[i], sum) : sum;
         }
       }
-      sum = both_sum(sum);
-      if (any && col.lim <= kKeys) {
-        delta = sum;
-        if (lane < 32) a.delta[at] = sum;
-      }
-    }
-    if (k0 < wave_hi) {
-#pragma unroll
-      for (int r0 = 0; r0 < kKeys; r0 += 32) {
-        f32x16 s, dp;
-        tile(buf, k0, r0, s, dp);
-        add_cols<T, DT>(s_k[buf], r0, dp, g);
-      }
-    }
-    if (more) {
-      sk.store(s_k[buf ^ 1]);
-      sv.store(s_v[buf ^ 1]);
+    });
+    sum = both_sum(sum);
+    if (any && (biased || col.lim <= kKeys)) {
+      delta = sum;
+      if (lane < 32) a.delta[at] = sum;
     }
   }
+  walk(end, [&](int k0) {
+#pragma unroll
+    for (int r0 = 0; r0 < kKeys; r0 += 32) {
+      f32x16 s = times_rows<T, DT>(s_k[buf], r0, qf), dp = times_rows<T, DT>(s_v[buf], r0, df);
+      const int off = col.pos - k0 - r0;
+      weigh<kMode>(s, dp, sc, [&](int) { return lse; }, [&](int) { return delta; },
+                   [&](int i) { return slope * fabsf((float)(off - result_row(i))); });
+      if (k0 + kKeys > wave_lo) {
+        const int room = only_here(col.lim - k0 - r0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dp[i] = result_row(i) < room ? dp[i] : 0.0f;
+      }
+      add_cols<T, DT>(s_k[buf], r0, dp, g);
+    }
+  });
   if (!col.ok) return;
   const bool none = col.lim <= 0;
   store_col<T, DT>(a.out0 + row * a.out0_row + (int64_t)col.head * a.out0_head, a.dim,
@@ -891,9 +927,10 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
                      [&](int i) { return s_delta[buf][result_row(i)]; },
                      [&](int i) { return slope * fabsf((float)(off + result_row(i))); });
         if (key_limit(a, d, t0) < wkey + 32) {
+          const int here = only_here(key);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const bool seen = key < key_limit(a, d, t0 + result_row(i));
+            const bool seen = here < key_limit(a, d, t0 + result_row(i));
             s[i] = seen ? s[i] : 0.0f;
             dp[i] = seen ? dp[i] : 0.0f;
           }

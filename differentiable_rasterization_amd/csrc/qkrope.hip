@@ -254,20 +254,22 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
   }
 }
 
-// Column sums of partials [blocks][2 dim]: 64 columns a workgroup, 16 rows at
-// a time, then the 16 sums in order.
+// Column sums of partials [blocks][2 dim]: 16 columns a workgroup, 64 rows at
+// a time, then the 64 sums in order.
 __global__ __launch_bounds__(1024) void qk_weight_kernel(int blocks, int dim,
                                                          const float* __restrict__ partials,
                                                          float* dwq, float* dwk) {
-  __shared__ float s_sum[16][64];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), part = threadIdx.x >> 6;
+  __shared__ float s_sum[64][17];
+  const int c = threadIdx.x & 15, part = threadIdx.x >> 4;
+  const int col = blockIdx.x * 16 + c;  // 2 dim is a multiple of 16
   float sum = 0.0f;
-  if (col < 2 * dim)
-    for (int b = part; b < blocks; b += 16) sum += partials[(int64_t)b * 2 * dim + col];
-  s_sum[part][threadIdx.x & 63] = sum;
+#pragma unroll 4
+  for (int b = part; b < blocks; b += 64) sum += partials[(int64_t)b * 2 * dim + col];
+  s_sum[part][c] = sum;
   __syncthreads();
-  if (part == 0 && col < 2 * dim) {
-    for (int i = 1; i < 16; ++i) sum += s_sum[i][threadIdx.x];
+  if (part == 0) {
+#pragma unroll 8
+    for (int i = 1; i < 64; ++i) sum += s_sum[i][c];
     if (col < dim) dwq[col] = sum;
     else dwk[col - dim] = sum;
   }
@@ -363,7 +365,7 @@ hipError_t gs_launch_qk_bwd(const gs_qk_config& cfg, int64_t rows, const int32_t
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !cfg.norm) return e;
   }
-  qk_weight_kernel<<<dim3((2 * cfg.head_dim + 63) / 64), dim3(1024), 0, s>>>(
+  qk_weight_kernel<<<dim3(2 * cfg.head_dim / 16), dim3(1024), 0, s>>>(
       blocks, cfg.head_dim, (const float*)workspace, dwq, dwk);
   return hipGetLastError();
 }

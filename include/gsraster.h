@@ -725,7 +725,8 @@ GS_API gs_status gs_qk_norm_rope_bwd(const gs_qk_config* cfg, int64_t rows,
  * the softmax over the seen keys times the values; a token that sees no key
  * gets 0.  lse [heads_q][rows_q] fp32 (NULL to skip; the gradient needs it):
  * the logarithm of the sum of exponentials, -inf where no key is seen.
- * dtype is GS_BF16 or GS_F16; head_dim a multiple of 8, at most 128.
+ * dtype is GS_BF16 or GS_F16; head_dim a multiple of 8, at most 128; row
+ * strides are below 2^23.
  * Softmax weights are rounded to dtype for the product with the values.
  * Non-finite values reach no other document and no row outside their own; a
  * non-finite key or value may reach every token of its document, also one
