@@ -85,26 +85,41 @@ __device__ inline int place(int r, int c) {
   else return r * DT + ((c ^ ((((r >> 1) & 1) << 2) | ((r >> 2) & 3))) << 3);
 }
 
-// Left or right operand: rows r0 + lane % 32, contraction 16 ks + 8 half ...
+// Byte offsets of this lane's operand reads in a staged tile.  Within a row the
+// place of a chunk is its number XOR a few bits of the row, so every other
+// read of a tile is these offsets XOR a constant (contraction step, column
+// tile) plus a constant (row tile): few registers hold addresses.
+template <int DT>
+struct Lane {
+  int rows;         // row lane % 32, chunk half
+  int cols0, cols8; // transposing read: rows 4 half + (lane % 16) / 4 and 8 on
+  __device__ inline Lane() {
+    const int lane = threadIdx.x & 63;
+    rows = 2 * place<DT>(lane & 31, lane >> 5);
+    const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
+    const int d = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    cols0 = 2 * (place<DT>(r, d >> 3) + (d & 7));
+    cols8 = 2 * (place<DT>(r + 8, d >> 3) + (d & 7));
+  }
+};
+
+// Left or right operand: rows lane % 32 of the 32-row tile at byte `base` plus
+// the lane's offset, contraction 16 ks + 8 half ...
 template <typename T, int DT>
-__device__ inline typename Mat<T>::V8 read_rows(const uint16_t* tile, int r0, int ks) {
-  const int lane = threadIdx.x & 63;
-  const u32x4 w = *(const u32x4*)(tile + place<DT>(r0 + (lane & 31), 2 * ks + (lane >> 5)));
+__device__ inline typename Mat<T>::V8 read_rows(const char* mem, int at, int r0, int ks) {
+  const u32x4 w = *(const u32x4*)(mem + (at ^ (32 * ks)) + 2 * r0 * DT);
   return __builtin_bit_cast(typename Mat<T>::V8, w);
 }
 
-// Left operand of the transposed tile: rows are elements d0 + lane % 32,
+// Left operand of the transposed tile: rows are elements 32 dt + lane % 32,
 // contraction slots the tile's rows r0 + 8 (j / 4) + 4 half + j % 4.
 template <typename T, int DT>
-__device__ inline typename Mat<T>::V8 read_cols(const uint16_t* tile, int r0, int d0) {
+__device__ inline typename Mat<T>::V8 read_cols(const char* mem, int at0, int at8, int r0, int dt) {
   typedef __attribute__((address_space(3))) s16x4 L;
-  const int lane = threadIdx.x & 63;
-  const int r = r0 + 4 * (lane >> 5) + ((lane & 15) >> 2);
-  const int d = d0 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-  const uint16_t* p0 = tile + place<DT>(r, d >> 3) + (d & 7);
-  const uint16_t* p1 = tile + place<DT>(r + 8, d >> 3) + (d & 7);
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)p0);
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)p1);
+  const s16x4 a =
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(mem + (at0 ^ (64 * dt)) + 2 * r0 * DT));
+  const s16x4 b =
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(mem + (at8 ^ (64 * dt)) + 2 * r0 * DT));
   const s16x8 w = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   return __builtin_bit_cast(typename Mat<T>::V8, w);
 }
@@ -207,30 +222,50 @@ struct Staged {
       at = c * 8 < dim ? at + 256 / kChunks * stride : at;
     }
   }
-  __device__ inline void store(uint16_t* tile) const {
+  __device__ inline void store(char* mem, int tile) const {
+    const int at = tile + 2 * place<DT>(threadIdx.x / kChunks, threadIdx.x % kChunks);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int x = threadIdx.x + 256 * i;
-      *(u32x4*)(tile + place<DT>(x / kChunks, x % kChunks)) = w[i];
-    }
+    for (int i = 0; i < kPer; ++i) *(u32x4*)(mem + at + i * 4096) = w[i];
   }
 };
 
-// Products over a staged tile, operands read two steps ahead of their use.
-// The barriers keep the compiler from moving every read to the front, which
-// costs more registers than there are.
+// Products over a staged tile (bytes at `tile` of mem), operands read two steps
+// ahead of their use.  The barriers keep the compiler from moving every read
+// to the front, which costs more registers than there are.
 template <typename T, int DT>
-__device__ inline f32x16 times_rows(const uint16_t* tile, int r0,
+__device__ inline f32x16 times_rows(const char* mem, int tile, int r0, const Lane<DT>& at,
                                     const typename Mat<T>::V8 (&f)[DT / 16]) {
   constexpr int N = DT / 16;
   typename Mat<T>::V8 x[3];
   f32x16 s = (f32x16)(0.0f);
-  x[0] = read_rows<T, DT>(tile, r0, 0);
-  x[1] = read_rows<T, DT>(tile, r0, 1);
+  const int a = at.rows + tile;
+  x[0] = read_rows<T, DT>(mem, a, r0, 0);
+  x[1] = read_rows<T, DT>(mem, a, r0, 1);
 #pragma unroll
   for (int ks = 0; ks < N; ++ks) {
-    if (ks + 2 < N) x[(ks + 2) % 3] = read_rows<T, DT>(tile, r0, ks + 2);
+    if (ks + 2 < N) x[(ks + 2) % 3] = read_rows<T, DT>(mem, a, r0, ks + 2);
     s = Mat<T>::mul(x[ks % 3], f[ks], s);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  return s;
+}
+
+// The same with the right operand in LDS too (32 rows at byte `right`).
+template <typename T, int DT>
+__device__ inline f32x16 times_staged(const char* mem, int tile, int right, const Lane<DT>& at) {
+  constexpr int N = DT / 16;
+  typename Mat<T>::V8 x[2], y[2];
+  f32x16 s = (f32x16)(0.0f);
+  const int a = at.rows + tile, b = at.rows + right;
+  x[0] = read_rows<T, DT>(mem, a, 0, 0);
+  y[0] = read_rows<T, DT>(mem, b, 0, 0);
+#pragma unroll
+  for (int ks = 0; ks < N; ++ks) {
+    if (ks + 1 < N) {
+      x[(ks + 1) % 2] = read_rows<T, DT>(mem, a, 0, ks + 1);
+      y[(ks + 1) % 2] = read_rows<T, DT>(mem, b, 0, ks + 1);
+    }
+    s = Mat<T>::mul(x[ks % 2], y[ks % 2], s);
     __builtin_amdgcn_sched_barrier(0);
   }
   return s;
@@ -238,17 +273,18 @@ __device__ inline f32x16 times_rows(const uint16_t* tile, int r0,
 
 // o += (rows r0 .. r0 + 32 of the tile, transposed) times p.
 template <typename T, int DT>
-__device__ inline void add_cols(const uint16_t* tile, int r0, const f32x16& p,
-                                f32x16 (&o)[DT / 32]) {
+__device__ inline void add_cols(const char* mem, int tile, int r0, const Lane<DT>& at,
+                                const f32x16& p, f32x16 (&o)[DT / 32]) {
   constexpr int M = DT / 32, N = 2 * M;
   typename Mat<T>::V8 x[3], w[2];
+  const int a = at.cols0 + tile, b = at.cols8 + tile;
   w[0] = pack_cols<T>(p, 0);
   w[1] = pack_cols<T>(p, 1);
-  x[0] = read_cols<T, DT>(tile, r0, 0);
-  x[1] = read_cols<T, DT>(tile, r0 + 1 / M * 16, 1 % M * 32);
+  x[0] = read_cols<T, DT>(mem, a, b, r0, 0);
+  x[1] = read_cols<T, DT>(mem, a, b, r0 + 1 / M * 16, 1 % M);
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    if (n + 2 < N) x[(n + 2) % 3] = read_cols<T, DT>(tile, r0 + (n + 2) / M * 16, (n + 2) % M * 32);
+    if (n + 2 < N) x[(n + 2) % 3] = read_cols<T, DT>(mem, a, b, r0 + (n + 2) / M * 16, (n + 2) % M);
     o[n % M] = Mat<T>::mul(x[n % 3], w[n / M], o[n % M]);
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -390,8 +426,10 @@ __device__ inline void make_scores(f32x16& s, const Scale& c, float slope, int o
 template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
-  __shared__ __align__(16) uint16_t s_k[2][kKeys * DT];
-  __shared__ __align__(16) uint16_t s_v[2][kKeys * DT];
+  // two buffers of a key and a value tile each
+  constexpr int kTile = kKeys * DT * 2;
+  __shared__ __align__(256) char mem[4 * kTile];
+  const Lane<DT> at;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int hk = blockIdx.x % a.heads_k;
   uint32_t local, units;
@@ -424,11 +462,11 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
   if (end > 0) {
     sk.load(kb, a.k_row, d.kl, a.dim);
     sv.load(vb, a.v_row, d.kl, a.dim);
-    sk.store(s_k[0]);
-    sv.store(s_v[0]);
+    sk.store(mem, 0);
+    sv.store(mem, kTile);
   }
   int buf = 0;
-  for (int k0 = 0; k0 < end; k0 += kKeys, buf ^= 1) {
+  for (int k0 = 0; k0 < end; k0 += kKeys, buf ^= 2 * kTile) {
     __syncthreads();
     const bool more = k0 + kKeys < end;
     if (more) {
@@ -439,16 +477,17 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
       f32x16 s[2];
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt) {
-        s[rt] = times_rows<T, DT>(s_k[buf], rt * 32, qf);
+        s[rt] = times_rows<T, DT>(mem, buf, rt * 32, at, qf);
         make_scores<kMode>(s[rt], sc, slope, col.pos - k0 - rt * 32);
       }
       softmax_step<DT, 2>(s, mul, k0 + kKeys > wave_lo, k0, col.lim, m, l, o);
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt) add_cols<T, DT>(s_v[buf], rt * 32, s[rt], o);
+      for (int rt = 0; rt < 2; ++rt)
+        add_cols<T, DT>(mem, buf + kTile, rt * 32, at, s[rt], o);
     }
     if (more) {
-      sk.store(s_k[buf ^ 1]);
-      sv.store(s_v[buf ^ 1]);
+      sk.store(mem, buf ^ (2 * kTile));
+      sv.store(mem, (buf ^ (2 * kTile)) + kTile);
     }
   }
   const float sum = both_sum(l);
@@ -477,9 +516,11 @@ __global__ __launch_bounds__(256, 2) void attention_step_kernel(AttnArgs a) {
   constexpr int kPer = 32 * kChunks / 64;
   constexpr int kStride = DT + 4;
   // the values' tiles, and after the loop the wavefronts' results
-  __shared__ __align__(16) float s_raw[4 * 32 * kStride];
+  __shared__ __align__(256) float s_raw[4 * 32 * kStride];
   __shared__ float s_m[4][32], s_l[4][32];
-  uint16_t* const s_v = (uint16_t*)s_raw + (threadIdx.x >> 6) * 32 * DT;
+  char* const mem = (char*)s_raw;
+  const int tile = (threadIdx.x >> 6) * 32 * DT * 2;
+  const Lane<DT> at_lane;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
   int u = blockIdx.x;
   const int hk = u % a.heads_k;
@@ -534,7 +575,7 @@ __global__ __launch_bounds__(256, 2) void attention_step_kernel(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int x = lane + 64 * i;
-        *(u32x4*)(s_v + place<DT>(x / kChunks, x % kChunks)) = vw[i];
+        *(u32x4*)(mem + tile + 2 * place<DT>(x / kChunks, x % kChunks)) = vw[i];
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
@@ -545,7 +586,7 @@ __global__ __launch_bounds__(256, 2) void attention_step_kernel(AttnArgs a) {
       // past the piece's end are other pieces' keys
       softmax_step<DT, 1>(s, mul, k0 + 32 > min(wave_lo, key_hi), k0, min(col.lim, key_hi), m, l,
                           o);
-      add_cols<T, DT>(s_v, 0, s[0], o);
+      add_cols<T, DT>(mem, tile, 0, at_lane, s[0], o);
     }
     l = both_sum(l);
     __syncthreads();
@@ -719,8 +760,10 @@ __device__ inline void weigh(f32x16& s, f32x16& dp, const Scale& c, Lse lse, Del
 template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
-  __shared__ __align__(16) uint16_t s_k[2][kKeys * DT];
-  __shared__ __align__(16) uint16_t s_v[2][kKeys * DT];
+  // two buffers of a key and a value tile each
+  constexpr int kTile = kKeys * DT * 2;
+  __shared__ __align__(256) char mem[4 * kTile];
+  const Lane<DT> at;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int hk = blockIdx.x % a.heads_k;
   uint32_t local, units;
@@ -736,9 +779,9 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   V8 qf[DT / 16], df[DT / 16];
   load_cols<T, DT>(a.q + row * a.q_row + (int64_t)col.head * a.q_head, col.ok, a.dim, qf);
   load_cols<T, DT>(a.d + row * a.d_row + (int64_t)col.head * a.d_head, col.ok, a.dim, df);
-  const int64_t at = (int64_t)col.head * a.docs.rows_q + row;
-  const float lse = any ? a.lse[at] * kLog2e : INFINITY;
-  float delta = any ? a.delta[at] : 0.0f;
+  const int64_t place_of = (int64_t)col.head * a.docs.rows_q + row;
+  const float lse = any ? a.lse[place_of] * kLog2e : INFINITY;
+  float delta = any ? a.delta[place_of] : 0.0f;
   const float slope = (kMode & kGeneral) && a.slopes && col.ok ? a.slopes[col.head] * kLog2e
                                                                : 0.0f;
   const Scale sc = scale_of<kMode>(a);
@@ -759,9 +802,9 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
     __syncthreads();
     sk.load(kb, a.k_row, d.kl, a.dim);
     sv.load(vb, a.v_row, d.kl, a.dim);
-    sk.store(s_k[buf]);
-    sv.store(s_v[buf]);
-    for (int k0 = 0; k0 < last; k0 += kKeys, buf ^= 1) {
+    sk.store(mem, buf);
+    sv.store(mem, buf + kTile);
+    for (int k0 = 0; k0 < last; k0 += kKeys, buf ^= 2 * kTile) {
       __syncthreads();
       const bool more = k0 + kKeys < last;
       if (more) {
@@ -770,8 +813,8 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
       }
       if (k0 < wave_hi) use(k0);
       if (more) {
-        sk.store(s_k[buf ^ 1]);
-        sv.store(s_v[buf ^ 1]);
+        sk.store(mem, buf ^ (2 * kTile));
+        sv.store(mem, (buf ^ (2 * kTile)) + kTile);
       }
     }
   };
@@ -782,8 +825,8 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
     walk(biased ? end : min(end, kKeys), [&](int k0) {
 #pragma unroll 1
       for (int r0 = 0; r0 < kKeys; r0 += 32) {
-        const f32x16 s = times_rows<T, DT>(s_k[buf], r0, qf);
-        const f32x16 dp = times_rows<T, DT>(s_v[buf], r0, df);
+        const f32x16 s = times_rows<T, DT>(mem, buf, r0, at, qf);
+        const f32x16 dp = times_rows<T, DT>(mem, buf + kTile, r0, at, df);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float f;
@@ -798,13 +841,14 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
     sum = both_sum(sum);
     if (any && (biased || col.lim <= kKeys)) {
       delta = sum;
-      if (lane < 32) a.delta[at] = sum;
+      if (lane < 32) a.delta[place_of] = sum;
     }
   }
   walk(end, [&](int k0) {
 #pragma unroll
     for (int r0 = 0; r0 < kKeys; r0 += 32) {
-      f32x16 s = times_rows<T, DT>(s_k[buf], r0, qf), dp = times_rows<T, DT>(s_v[buf], r0, df);
+      f32x16 s = times_rows<T, DT>(mem, buf, r0, at, qf);
+      f32x16 dp = times_rows<T, DT>(mem, buf + kTile, r0, at, df);
       const int off = col.pos - k0 - r0;
       weigh<kMode>(s, dp, sc, [&](int) { return lse; }, [&](int) { return delta; },
                    [&](int i) { return slope * fabsf((float)(off - result_row(i))); });
@@ -813,7 +857,7 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) dp[i] = result_row(i) < room ? dp[i] : 0.0f;
       }
-      add_cols<T, DT>(s_k[buf], r0, dp, g);
+      add_cols<T, DT>(mem, buf, r0, at, dp, g);
     }
   });
   if (!col.ok) return;
@@ -833,10 +877,11 @@ template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
   constexpr bool kValuesInLds = DT == 128;
-  __shared__ __align__(16) uint16_t s_q[2][kRows * DT];
-  __shared__ __align__(16) uint16_t s_d[2][kRows * DT];
-  __shared__ __align__(16) uint16_t s_v[kValuesInLds ? kCols * DT : 8];
+  // two buffers of a tile of q and of do, then the values
+  constexpr int kTile = kRows * DT * 2;
+  __shared__ __align__(256) char mem[4 * kTile + (kValuesInLds ? kCols * DT * 2 : 0)];
   __shared__ __align__(16) float s_lse[2][kRows], s_delta[2][kRows];
+  const Lane<DT> at;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int heads = a.parts ? a.heads_q : a.heads_k;
   const int hb = blockIdx.x % heads;
@@ -859,7 +904,7 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
     Staged<DT, kCols> sv;
     sv.load(a.v + (int64_t)(d.ks + key0) * a.v_row + (int64_t)hk * a.v_head, a.v_row, d.kl - key0,
             a.dim);
-    sv.store(s_v);
+    sv.store(mem, 4 * kTile);
   } else {
     load_cols<T, DT>(a.v + row * a.v_row + (int64_t)hk * a.v_head, ok, a.dim, vf);
   }
@@ -890,8 +935,8 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
     }
   };
   auto put = [&](int buf) {
-    sq.store(s_q[buf]);
-    sd.store(s_d[buf]);
+    sq.store(mem, buf * 2 * kTile);
+    sd.store(mem, buf * 2 * kTile + kTile);
     if (threadIdx.x < kRows) {
       s_lse[buf][threadIdx.x] = r_lse;
       s_delta[buf][threadIdx.x] = r_delta;
@@ -910,18 +955,12 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
       if (more) fetch(wrap ? h + 1 : h, wrap ? first : t0 + kRows);
       // limits of the tile's rows grow with the token
       if (wkey < key_limit(a, d, t0 + kRows - 1)) {
-        f32x16 s = times_rows<T, DT>(s_q[buf], 0, kf), dp;
-        if constexpr (kValuesInLds) {
-          dp = (f32x16)(0.0f);
-#pragma unroll
-          for (int ks = 0; ks < DT / 16; ++ks) {
-            dp = Mat<T>::mul(read_rows<T, DT>(s_d[buf], 0, ks),
-                             read_rows<T, DT>(s_v, wave * 32, ks), dp);
-            if (ks & 1) __builtin_amdgcn_sched_barrier(0);
-          }
-        } else {
-          dp = times_rows<T, DT>(s_d[buf], 0, vf);
-        }
+        const int tile = buf * 2 * kTile;
+        f32x16 s = times_rows<T, DT>(mem, tile, 0, at, kf), dp;
+        if constexpr (kValuesInLds)
+          dp = times_staged<T, DT>(mem, tile + kTile, 4 * kTile + wave * 32 * DT * 2, at);
+        else
+          dp = times_rows<T, DT>(mem, tile + kTile, 0, at, vf);
         const int off = t0 + shift - key;
         weigh<kMode>(s, dp, sc, [&](int i) { return s_lse[buf][result_row(i)]; },
                      [&](int i) { return s_delta[buf][result_row(i)]; },
@@ -935,8 +974,8 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
             dp[i] = seen ? dp[i] : 0.0f;
           }
         }
-        add_cols<T, DT>(s_d[buf], 0, s, gv);
-        add_cols<T, DT>(s_q[buf], 0, dp, gk);
+        add_cols<T, DT>(mem, tile + kTile, 0, at, s, gv);
+        add_cols<T, DT>(mem, tile, 0, at, dp, gk);
       }
       if (more) put(buf ^ 1);
     }
