@@ -24,6 +24,7 @@
 // c of a document is token c / group, head c % group, so one staged key tile
 // serves all of them, and one-token requests fill the columns with heads.
 #include "tokens.h"
+#include <stdlib.h>
 
 namespace gs {
 
@@ -45,7 +46,7 @@ struct AttnArgs {
   float* delta;  // [heads_q][rows_q]
   int parts;          // dk, dv: sums per query head
   int pieces, piece;  // one-token form: pieces of a document's keys, keys of one
-  int col_tiles;      // one-token form: column tiles in the grid
+  int col_units;      // few-column form: column tiles are units of the grid
   float* part_ml;     // [pieces][heads_q][rows_q][2]
   float* part_o;      // [pieces][heads_q][rows_q][dim]
 };
@@ -164,19 +165,6 @@ __device__ inline float tanh_of(float x) {
   return 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// A document as the kernels use it.
-struct Doc {
-  int qs, ql, ks, kl, prefix;
-};
-__device__ inline Doc load_doc(const Docs& d, int i) {
-  Doc o;
-  o.qs = clamp_start(d.q_start[i], d.rows_q);
-  o.ql = clamp_len(d.q_start[i], d.q_len[i], d.rows_q);
-  o.ks = clamp_start(d.k_start[i], d.rows_k);
-  o.kl = clamp_len(d.k_start[i], d.k_len[i], d.rows_k);
-  o.prefix = d.prefix ? min(max(d.prefix[i], 0), o.kl) : 0;
-  return o;
-}
 // Token i sees the keys below this.
 __device__ inline int key_limit(const AttnArgs& a, const Doc& d, int token) {
   return a.causal ? min(d.kl, max(token + d.kl - d.ql + 1, d.prefix)) : d.kl;
@@ -229,66 +217,171 @@ struct Staged {
   }
 };
 
-// Products over a staged tile (bytes at `tile` of mem), operands read two steps
-// ahead of their use.  The barriers keep the compiler from moving every read
-// to the front, which costs more registers than there are.
+// Thirty-two rows as operand fragments straight from memory (row lane % 32,
+// elements 16 ks + 8 half ...), zeros past `valid` rows and dim elements; and
+// their place in a staged tile.
 template <typename T, int DT>
-__device__ inline f32x16 times_rows(const char* mem, int tile, int r0, const Lane<DT>& at,
-                                    const typename Mat<T>::V8 (&f)[DT / 16]) {
-  constexpr int N = DT / 16;
-  typename Mat<T>::V8 x[3];
-  f32x16 s = (f32x16)(0.0f);
-  const int a = at.rows + tile;
-  x[0] = read_rows<T, DT>(mem, a, r0, 0);
-  x[1] = read_rows<T, DT>(mem, a, r0, 1);
+struct Fragments {
+  typename Mat<T>::V8 f[DT / 16];
+  __device__ inline void load(const uint16_t* base, int64_t row_stride, int valid, int dim) {
+    const int stride = (int)row_stride * 2;
+    const int64_t bytes = valid > 0 ? (int64_t)(valid - 1) * stride + dim * 2 : 0;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(base), 0, (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff),
+        0x00027000);
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int at = (lane & 31) * stride + half * 16;
 #pragma unroll
-  for (int ks = 0; ks < N; ++ks) {
-    if (ks + 2 < N) x[(ks + 2) % 3] = read_rows<T, DT>(mem, a, r0, ks + 2);
-    s = Mat<T>::mul(x[ks % 3], f[ks], s);
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  return s;
-}
-
-// The same with the right operand in LDS too (32 rows at byte `right`).
-template <typename T, int DT>
-__device__ inline f32x16 times_staged(const char* mem, int tile, int right, const Lane<DT>& at) {
-  constexpr int N = DT / 16;
-  typename Mat<T>::V8 x[2], y[2];
-  f32x16 s = (f32x16)(0.0f);
-  const int a = at.rows + tile, b = at.rows + right;
-  x[0] = read_rows<T, DT>(mem, a, 0, 0);
-  y[0] = read_rows<T, DT>(mem, b, 0, 0);
-#pragma unroll
-  for (int ks = 0; ks < N; ++ks) {
-    if (ks + 1 < N) {
-      x[(ks + 1) % 2] = read_rows<T, DT>(mem, a, 0, ks + 1);
-      y[(ks + 1) % 2] = read_rows<T, DT>(mem, b, 0, ks + 1);
+    for (int ks = 0; ks < DT / 16; ++ks) {
+      const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(
+          rsrc, 16 * ks + 8 * half < dim ? at + 32 * ks : (int)0x80000000, 0, 0);
+      f[ks] = __builtin_bit_cast(typename Mat<T>::V8, w);
     }
-    s = Mat<T>::mul(x[ks % 2], y[ks % 2], s);
-    __builtin_amdgcn_sched_barrier(0);
   }
-  return s;
+  __device__ inline void store(char* mem, int tile, const Lane<DT>& at) const {
+#pragma unroll
+    for (int ks = 0; ks < DT / 16; ++ks)
+      *(u32x4*)(mem + ((at.rows + tile) ^ (32 * ks))) = __builtin_bit_cast(u32x4, f[ks]);
+  }
+  __device__ inline f32x16 times(const typename Mat<T>::V8 (&b)[DT / 16]) const {
+    f32x16 s = (f32x16)(0.0f);
+#pragma unroll
+    for (int ks = 0; ks < DT / 16; ++ks) s = Mat<T>::mul(f[ks], b[ks], s);
+    return s;
+  }
+};
+
+// What a wavefront wrote to its own LDS is there for its next reads.
+__device__ inline void own_lds_written() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// o += (rows r0 .. r0 + 32 of the tile, transposed) times p.
-template <typename T, int DT>
-__device__ inline void add_cols(const char* mem, int tile, int r0, const Lane<DT>& at,
-                                const f32x16& p, f32x16 (&o)[DT / 32]) {
-  constexpr int M = DT / 32, N = 2 * M;
-  typename Mat<T>::V8 x[3], w[2];
-  const int a = at.cols0 + tile, b = at.cols8 + tile;
-  w[0] = pack_cols<T>(p, 0);
-  w[1] = pack_cols<T>(p, 1);
-  x[0] = read_cols<T, DT>(mem, a, b, r0, 0);
-  x[1] = read_cols<T, DT>(mem, a, b, r0 + 1 / M * 16, 1 % M);
+// Dot product of two fragment columns, both halves together.
+template <typename T, int N>
+__device__ inline float dot_cols(const typename Mat<T>::V8 (&x)[N],
+                                 const typename Mat<T>::V8 (&y)[N]) {
+  float sum = 0.0f;
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    if (n + 2 < N) x[(n + 2) % 3] = read_cols<T, DT>(mem, a, b, r0 + (n + 2) / M * 16, (n + 2) % M);
-    o[n % M] = Mat<T>::mul(x[n % 3], w[n / M], o[n % M]);
-    __builtin_amdgcn_sched_barrier(0);
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf((float)x[i][j], (float)y[i][j], sum);
+  return both_sum(sum);
+}
+
+// Four wavefronts' accumulators of 32 columns into LDS, for their sum.
+template <int DT>
+__device__ inline void leave_cols(float* s_raw, const f32x16 (&o)[DT / 32]) {
+  constexpr int kStride = DT + 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int dt = 0; dt < DT / 32; ++dt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 x = {o[dt][4 * i], o[dt][4 * i + 1], o[dt][4 * i + 2], o[dt][4 * i + 3]};
+      *(f32x4*)(s_raw + (wave * 32 + (lane & 31)) * kStride + dt * 32 + 8 * i + 4 * (lane >> 5)) =
+          x;
+    }
   }
 }
+
+// N steps of a product whose operand `read(n)` comes from LDS: each read is
+// issued A steps before its use (an LDS read takes about as long as four of the
+// instructions it feeds), and the barriers keep the compiler from moving every
+// read to the front, which costs more registers than there are.  prime() may
+// stand well before run(), to have the first reads under way.
+template <typename V, int N, int A>
+struct Pipeline {
+  V x[A + 1];
+  template <typename Read>
+  __device__ inline void prime(Read read) {
+#pragma unroll
+    for (int n = 0; n < A && n < N; ++n) x[n] = read(n);
+  }
+  template <typename Read, typename Use>
+  __device__ inline void run(Read read, Use use) {
+    // while the matrix unit is fed, this wavefront goes before others that are
+    // at their scores
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (n + A < N) x[(n + A) % (A + 1)] = read(n + A);
+      use(n, x[n % (A + 1)]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_setprio(0);
+  }
+};
+
+// s0 = tile at byte t0 times f0, s1 = tile at byte t1 times f1 (32 rows each,
+// taken in turn so that no instruction waits for the one before it).
+template <typename T, int DT, int A = 3>
+__device__ inline void two_products(const char* mem, int t0, int t1, const Lane<DT>& at,
+                                    const typename Mat<T>::V8 (&f0)[DT / 16],
+                                    const typename Mat<T>::V8 (&f1)[DT / 16], f32x16& s0,
+                                    f32x16& s1) {
+  typedef typename Mat<T>::V8 V8;
+  const int a0 = at.rows + t0, a1 = at.rows + t1;
+  Pipeline<V8, DT / 8, A> p;
+  auto read = [&](int n) { return read_rows<T, DT>(mem, n & 1 ? a1 : a0, 0, n >> 1); };
+  s0 = s1 = (f32x16)(0.0f);
+  p.prime(read);
+  p.run(read, [&](int n, const V8& x) {
+    if (n & 1) s1 = Mat<T>::mul(x, f1[n >> 1], s1);
+    else s0 = Mat<T>::mul(x, f0[n >> 1], s0);
+  });
+}
+
+// The same with the second product's right operand in LDS too (byte right).
+template <typename T, int DT, int A>
+__device__ inline void two_products_staged(const char* mem, int t0, int t1, int right,
+                                           const Lane<DT>& at,
+                                           const typename Mat<T>::V8 (&f0)[DT / 16], f32x16& s0,
+                                           f32x16& s1) {
+  typedef typename Mat<T>::V8 V8;
+  struct Pair {
+    V8 x, y;
+  };
+  const int a0 = at.rows + t0, a1 = at.rows + t1, r = at.rows + right;
+  Pipeline<Pair, DT / 8, A> p;
+  auto read = [&](int n) {
+    Pair o;
+    o.x = read_rows<T, DT>(mem, n & 1 ? a1 : a0, 0, n >> 1);
+    if (n & 1) o.y = read_rows<T, DT>(mem, r, 0, n >> 1);
+    return o;
+  };
+  s0 = s1 = (f32x16)(0.0f);
+  p.prime(read);
+  p.run(read, [&](int n, const Pair& v) {
+    if (n & 1) s1 = Mat<T>::mul(v.x, v.y, s1);
+    else s0 = Mat<T>::mul(v.x, f0[n >> 1], s0);
+  });
+}
+
+// o += (32 R rows from byte `tile`, transposed) times the R tiles of p.
+template <typename T, int DT, int R, int A = 3>
+struct AddCols {
+  typedef typename Mat<T>::V8 V8;
+  static constexpr int M = DT / 32;
+  Pipeline<V8, 2 * M * R, A> p;
+  const char* mem;
+  int a, b;
+  __device__ inline V8 read(int n) const {
+    return read_cols<T, DT>(mem, a, b, n / M * 16, n % M);
+  }
+  __device__ inline AddCols(const char* mem, int tile, const Lane<DT>& at)
+      : mem(mem), a(at.cols0 + tile), b(at.cols8 + tile) {
+    p.prime([&](int n) { return read(n); });
+  }
+  __device__ inline void run(const f32x16 (&s)[R], f32x16 (&o)[DT / 32]) {
+    V8 w[2 * R];
+#pragma unroll
+    for (int i = 0; i < 2 * R; ++i) w[i] = pack_cols<T>(s[i / 2], i % 2);
+    p.run([&](int n) { return read(n); },
+          [&](int n, const V8& x) { o[n % M] = Mat<T>::mul(x, w[n / M], o[n % M]); });
+  }
+};
 
 // Constants of the scores, in units of log2.
 struct Scale {
@@ -433,10 +526,9 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int hk = blockIdx.x % a.heads_k;
   uint32_t local, units;
-  const int doc = find_document(a.docs.q_start, a.docs.q_len, a.docs.rows_q, a.docs.count,
-                                a.group, kCols, blockIdx.x / a.heads_k, &local, &units);
-  if (doc < 0) return;
-  const Doc d = load_doc(a.docs, doc);
+  Doc d;
+  if (find_document<false>(a.docs, a.group, kCols, blockIdx.x / a.heads_k, &local, &units, &d) < 0)
+    return;
   // long causal rows first
   const uint32_t col0 = (units - 1 - local) * kCols;
   const uint32_t cols = (uint32_t)d.ql * a.group;
@@ -475,15 +567,13 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
     }
     if (k0 < wave_hi) {
       f32x16 s[2];
-#pragma unroll
-      for (int rt = 0; rt < 2; ++rt) {
-        s[rt] = times_rows<T, DT>(mem, buf, rt * 32, at, qf);
-        make_scores<kMode>(s[rt], sc, slope, col.pos - k0 - rt * 32);
-      }
-      softmax_step<DT, 2>(s, mul, k0 + kKeys > wave_lo, k0, col.lim, m, l, o);
+      two_products<T, DT>(mem, buf, buf + kTile / 2, at, qf, qf, s[0], s[1]);
+      AddCols<T, DT, 2> add(mem, buf + kTile, at);
 #pragma unroll
       for (int rt = 0; rt < 2; ++rt)
-        add_cols<T, DT>(mem, buf + kTile, rt * 32, at, s[rt], o);
+        make_scores<kMode>(s[rt], sc, slope, col.pos - k0 - rt * 32);
+      softmax_step<DT, 2>(s, mul, k0 + kKeys > wave_lo, k0, col.lim, m, l, o);
+      add.run(s, o);
     }
     if (more) {
       sk.store(mem, buf ^ (2 * kTile));
@@ -501,16 +591,44 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
         none ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-// Few columns a document (one new token, all its heads): the keys are what
-// there is to split.  A workgroup takes one piece of a document's keys for 32
-// columns of a key head, its four wavefronts 32 keys each in turn.  Keys come
-// straight from memory as the left operand, values pass through the
-// wavefront's own LDS for the transposing read, and both are on their way for
-// the next tile while this one is computed.  The wavefronts' results are
-// joined in LDS; where a document has several pieces,
-// attention_join_kernel joins those.
+// Few columns in all: the keys are what there is to split.  A workgroup takes
+// 32 columns of a key head and one piece of their document's keys, its four
+// wavefronts 32 keys each in turn.  Keys come straight from memory as the left
+// operand, values pass through the wavefront's own LDS for the transposing
+// read, and both are on their way for the next tile while this one is
+// computed.  The wavefronts' results are joined in LDS; where a document has
+// several pieces, attention_join_kernel joins those.  One-token requests (all
+// of a key head's query heads are columns) have one column tile a document;
+// otherwise (col_units) the document of a column tile is looked up.
+struct StepItem {
+  int hk, piece;
+  uint32_t col0;
+  bool none;
+  Doc d;
+};
+__device__ inline StepItem step_item(const AttnArgs& a, int u) {
+  StepItem o;
+  o.hk = u % a.heads_k;
+  u /= a.heads_k;
+  o.piece = u % a.pieces;
+  u /= a.pieces;
+  o.col0 = 0;
+  o.none = false;
+  if (a.col_units) {
+    uint32_t local = 0, units = 1;
+    o.none = find_document<false>(a.docs, a.group, 32, u, &local, &units, &o.d) < 0;
+    o.col0 = (units - 1 - local) * 32;  // long causal rows first
+  } else {
+    o.d = load_doc(a.docs, u);
+  }
+  return o;
+}
+__device__ inline int pieces_of(const AttnArgs& a, const Doc& d) {
+  return max(1, min(a.pieces, (d.kl + a.piece - 1) / a.piece));
+}
+
 template <typename T, int DT, int kMode>
-__global__ __launch_bounds__(256, 2) void attention_step_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, DT == 128 ? 2 : 3) void attention_step_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
   constexpr int kChunks = DT / 8;
   constexpr int kPer = 32 * kChunks / 64;
@@ -522,14 +640,10 @@ __global__ __launch_bounds__(256, 2) void attention_step_kernel(AttnArgs a) {
   const int tile = (threadIdx.x >> 6) * 32 * DT * 2;
   const Lane<DT> at_lane;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-  int u = blockIdx.x;
-  const int hk = u % a.heads_k;
-  u /= a.heads_k;
-  const int tile0 = u % a.col_tiles;
-  u /= a.col_tiles;
-  const int piece = u % a.pieces, doc = u / a.pieces;
-  const Doc d = load_doc(a.docs, doc);
-  const int pieces = max(1, min(a.pieces, (d.kl + a.piece - 1) / a.piece));
+  const StepItem it = step_item(a, blockIdx.x);
+  if (it.none) return;
+  const Doc& d = it.d;
+  const int hk = it.hk, piece = it.piece, pieces = pieces_of(a, d);
   if (piece >= pieces) return;
   const int key_lo = piece * a.piece;
   const int key_hi = piece == pieces - 1 ? d.kl : key_lo + a.piece;
@@ -538,7 +652,7 @@ __global__ __launch_bounds__(256, 2) void attention_step_kernel(AttnArgs a) {
   const uint16_t* vb = a.v + (int64_t)d.ks * a.v_row + (int64_t)hk * a.v_head;
   const Scale sc = scale_of<kMode>(a);
   const float mul = kMode == 0 ? sc.mul : 1.0f;
-  for (uint32_t col0 = tile0 * 32; col0 < cols; col0 += a.col_tiles * 32) {
+  for (uint32_t col0 = it.col0; col0 < cols; col0 += 32) {
     const Col col = column(a, d, hk, col0 + (lane & 31), cols);
     V8 qf[DT / 16];
     load_cols<T, DT>(a.q + (int64_t)(d.qs + col.token) * a.q_row + (int64_t)col.head * a.q_head,
@@ -552,41 +666,41 @@ __global__ __launch_bounds__(256, 2) void attention_step_kernel(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < DT / 32; ++i) o[i] = (f32x16)(0.0f);
     float m = -INFINITY, l = 0.0f;
-    V8 kf[DT / 16];
+    Fragments<T, DT> kf;
     u32x4 vw[kPer];
     auto fetch = [&](int k0) {
-      const int key = k0 + (lane & 31);
-      load_cols<T, DT>(kb + (int64_t)key * a.k_row, key < d.kl, a.dim, kf);
+      kf.load(kb + (int64_t)k0 * a.k_row, a.k_row, d.kl - k0, a.dim);
+      const int stride = (int)a.v_row * 2;
+      const int64_t bytes = (int64_t)(d.kl - k0 - 1) * stride + a.dim * 2;
+      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint16_t*>(vb + (int64_t)k0 * a.v_row), 0,
+          (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff), 0x00027000);
+      const int r = lane / kChunks, c = lane % kChunks;
+      int at = c * 8 < a.dim ? r * stride + c * 16 : (int)0x80000000;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int x = lane + 64 * i, r = x / kChunks, c = x % kChunks;
-        vw[i] = (u32x4)(0);
-        if (k0 + r < d.kl && c * 8 < a.dim)
-          vw[i] = *(const u32x4*)(vb + (int64_t)(k0 + r) * a.v_row + c * 8);
+        vw[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0);
+        at = c * 8 < a.dim ? at + 64 / kChunks * stride : at;
       }
     };
     int k0 = key_lo + wave * 32;
     if (k0 < end) fetch(k0);
     for (; k0 < end; k0 += kPieceKeys) {
-      f32x16 s[1] = {(f32x16)(0.0f)};
-#pragma unroll
-      for (int ks = 0; ks < DT / 16; ++ks) s[0] = Mat<T>::mul(kf[ks], qf[ks], s[0]);
+      f32x16 s[1] = {kf.times(qf)};
       // the wavefront's own tile: its earlier reads are done, in order
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int x = lane + 64 * i;
         *(u32x4*)(mem + tile + 2 * place<DT>(x / kChunks, x % kChunks)) = vw[i];
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      own_lds_written();
       const int next = k0 + kPieceKeys;
       if (next < end) fetch(next);
       make_scores<kMode>(s[0], sc, slope, col.pos - k0);
       // past the piece's end are other pieces' keys
       softmax_step<DT, 1>(s, mul, k0 + 32 > min(wave_lo, key_hi), k0, min(col.lim, key_hi), m, l,
                           o);
-      add_cols<T, DT>(mem, tile, 0, at_lane, s[0], o);
+      AddCols<T, DT, 1>(mem, tile, at_lane).run(s, o);
     }
     l = both_sum(l);
     __syncthreads();
@@ -594,14 +708,7 @@ __global__ __launch_bounds__(256, 2) void attention_step_kernel(AttnArgs a) {
       s_m[wave][lane] = m;
       s_l[wave][lane] = l;
     }
-#pragma unroll
-    for (int dt = 0; dt < DT / 32; ++dt) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 x = {o[dt][4 * i], o[dt][4 * i + 1], o[dt][4 * i + 2], o[dt][4 * i + 3]};
-        *(f32x4*)(s_raw + (wave * 32 + (lane & 31)) * kStride + dt * 32 + 8 * i + 4 * half) = x;
-      }
-    }
+    leave_cols<DT>(s_raw, o);
     __syncthreads();
     // eight lanes a column join the four wavefronts, in order
     const int cc = threadIdx.x >> 3, e0 = (threadIdx.x & 7) * (DT / 8);
@@ -646,24 +753,31 @@ __global__ __launch_bounds__(256, 2) void attention_step_kernel(AttnArgs a) {
         }
       }
     }
+    if (a.col_units) break;  // the document's other tiles have workgroups
     __syncthreads();
   }
 }
 
-// The pieces of each column, joined in order: a workgroup a document and
-// head; 16 groups of 16 lanes (8 elements a lane) take every 16th piece, and
-// their sums are added in order.
+// The pieces of a column, joined in order: a workgroup a column; 16 groups of
+// 16 lanes (8 elements a lane) take every 16th piece, and their sums are added
+// in order.
 template <typename T>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int tile_cols) {
   __shared__ float s_x[16][16][9], s_sum[16];
-  const int doc = blockIdx.x / a.heads_q, head = blockIdx.x % a.heads_q;
-  const Doc d = load_doc(a.docs, doc);
-  const int pieces = max(1, min(a.pieces, (d.kl + a.piece - 1) / a.piece));
+  int u = blockIdx.x / tile_cols;
+  const int hk = u % a.heads_k;
+  u /= a.heads_k;
+  const StepItem it = step_item(a, u * a.pieces * a.heads_k);
+  if (it.none) return;
+  const Doc& d = it.d;
+  const int pieces = pieces_of(a, d);
   if (pieces == 1) return;
+  const uint32_t cols = (uint32_t)d.ql * a.group;
   const int sub = threadIdx.x & 15, group = threadIdx.x >> 4, e = sub * 8;
   const int64_t step = (int64_t)a.heads_q * a.docs.rows_q;
-  for (int t = 0; t < d.ql; ++t) {
-    const int64_t at = (int64_t)head * a.docs.rows_q + d.qs + t;
+  for (uint32_t c = it.col0 + blockIdx.x % tile_cols; c < cols; c += tile_cols) {
+    const Col w = column(a, d, hk, c, cols);
+    const int64_t row = d.qs + w.token, at = (int64_t)w.head * a.docs.rows_q + row;
     float top = -INFINITY;
     for (int i = threadIdx.x & 63; i < pieces; i += 64)
       top = fmaxf(top, a.part_ml[(at + i * step) * 2]);
@@ -694,18 +808,17 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] += s_x[g][sub][j];
       }
-      const bool none = key_limit(a, d, t) <= 0;
+      const bool none = w.lim <= 0;
       const float inv = none || sum == 0.0f ? 0.0f : 1.0f / sum;
       if (e < a.dim) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = none ? 0.0f : x[j] * inv;
-        store_elems((T*)(a.out0 + (int64_t)(d.qs + t) * a.out0_row + (int64_t)head * a.out0_head +
-                         e),
-                    x);
+        store_elems((T*)(a.out0 + row * a.out0_row + (int64_t)w.head * a.out0_head + e), x);
       }
       if (a.lse && e == 0)
         a.lse[at] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
     }
+    if (a.col_units) break;
     __syncthreads();
   }
 }
@@ -713,26 +826,6 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 // ---------------------------------------------------------------------------
 // Backward
 // ---------------------------------------------------------------------------
-// delta = do.o of every row and head: 16 lanes each.
-template <typename T>
-__global__ __launch_bounds__(256) void attention_delta_kernel(AttnArgs a) {
-  const int64_t item = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
-  const int lane = threadIdx.x & 15;
-  if (item >= (int64_t)a.docs.rows_q * a.heads_q) return;
-  const int row = (int)(item / a.heads_q), head = (int)(item % a.heads_q);
-  float sum = 0.0f;
-  if (lane * 8 < a.dim) {
-    float x[8], y[8];
-    load_elems((const T*)a.o + row * a.o_row + head * a.o_head + lane * 8, x);
-    load_elems((const T*)a.d + row * a.d_row + head * a.d_head + lane * 8, y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
-  }
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 16);
-  if (lane == 0) a.delta[(int64_t)head * a.docs.rows_q + row] = sum;
-}
-
 // p and ds of one 32 x 32 tile, in place of the products s and dp: register i
 // has the logarithm lse(i), delta(i) and the bias away(i).
 template <int kMode, typename Lse, typename Delta, typename Away>
@@ -750,13 +843,13 @@ __device__ inline void weigh(f32x16& s, f32x16& dp, const Scale& c, Lse lse, Del
   }
 }
 
-// dq: the forward's loop, with p from the stored logarithm of the sum.
-// delta = do.o carries the roundings of o and of the weights that made it.
+// dq: the forward's loop, with p from the stored logarithm of the sum, and
+// delta for the dk, dv kernel, which runs after it.  delta = do.o carries the roundings of o and of the weights that made it.
 // Where a row leans on few keys, so that o is as large as a value, they would
 // be a third of the gradient's error.  Rows whose keys all stand in the first
 // tile, and all rows under a distance bias, therefore take delta =
 // sum_j p_j dp_j, the same number without those roundings, in a pass of its
-// own over their keys, and leave it for the dk, dv kernel.
+// own over their keys.
 template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
@@ -767,10 +860,9 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int hk = blockIdx.x % a.heads_k;
   uint32_t local, units;
-  const int doc = find_document(a.docs.q_start, a.docs.q_len, a.docs.rows_q, a.docs.count,
-                                a.group, kCols, blockIdx.x / a.heads_k, &local, &units);
-  if (doc < 0) return;
-  const Doc d = load_doc(a.docs, doc);
+  Doc d;
+  if (find_document<false>(a.docs, a.group, kCols, blockIdx.x / a.heads_k, &local, &units, &d) < 0)
+    return;
   const uint32_t col0 = (units - 1 - local) * kCols;
   const uint32_t cols = (uint32_t)d.ql * a.group;
   const Col col = column(a, d, hk, col0 + wave * 32 + (lane & 31), cols);
@@ -781,7 +873,12 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   load_cols<T, DT>(a.d + row * a.d_row + (int64_t)col.head * a.d_head, col.ok, a.dim, df);
   const int64_t place_of = (int64_t)col.head * a.docs.rows_q + row;
   const float lse = any ? a.lse[place_of] * kLog2e : INFINITY;
-  float delta = any ? a.delta[place_of] : 0.0f;
+  float delta;
+  {
+    V8 of[DT / 16];
+    load_cols<T, DT>(a.o + row * a.o_row + (int64_t)col.head * a.o_head, any, a.dim, of);
+    delta = dot_cols<T, DT / 16>(of, df);
+  }
   const float slope = (kMode & kGeneral) && a.slopes && col.ok ? a.slopes[col.head] * kLog2e
                                                                : 0.0f;
   const Scale sc = scale_of<kMode>(a);
@@ -825,8 +922,9 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
     walk(biased ? end : min(end, kKeys), [&](int k0) {
 #pragma unroll 1
       for (int r0 = 0; r0 < kKeys; r0 += 32) {
-        const f32x16 s = times_rows<T, DT>(mem, buf, r0, at, qf);
-        const f32x16 dp = times_rows<T, DT>(mem, buf + kTile, r0, at, df);
+        f32x16 s, dp;
+        const int rows = buf + r0 * DT * 2;
+        two_products<T, DT>(mem, rows, rows + kTile, at, qf, df, s, dp);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float f;
@@ -839,25 +937,25 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
       }
     });
     sum = both_sum(sum);
-    if (any && (biased || col.lim <= kKeys)) {
-      delta = sum;
-      if (lane < 32) a.delta[place_of] = sum;
-    }
+    if (biased || col.lim <= kKeys) delta = any ? sum : 0.0f;
   }
+  if (col.ok && lane < 32) a.delta[place_of] = delta;
   walk(end, [&](int k0) {
 #pragma unroll
     for (int r0 = 0; r0 < kKeys; r0 += 32) {
-      f32x16 s = times_rows<T, DT>(mem, buf, r0, at, qf);
-      f32x16 dp = times_rows<T, DT>(mem, buf + kTile, r0, at, df);
+      f32x16 s, dp[1];
+      const int rows = buf + r0 * DT * 2;
+      two_products<T, DT>(mem, rows, rows + kTile, at, qf, df, s, dp[0]);
+      AddCols<T, DT, 1> add(mem, rows, at);
       const int off = col.pos - k0 - r0;
-      weigh<kMode>(s, dp, sc, [&](int) { return lse; }, [&](int) { return delta; },
+      weigh<kMode>(s, dp[0], sc, [&](int) { return lse; }, [&](int) { return delta; },
                    [&](int i) { return slope * fabsf((float)(off - result_row(i))); });
       if (k0 + kKeys > wave_lo) {
         const int room = only_here(col.lim - k0 - r0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dp[i] = result_row(i) < room ? dp[i] : 0.0f;
+        for (int i = 0; i < 16; ++i) dp[0][i] = result_row(i) < room ? dp[0][i] : 0.0f;
       }
-      add_cols<T, DT>(mem, buf, r0, at, dp, g);
+      add.run(dp, g);
     }
   });
   if (!col.ok) return;
@@ -888,10 +986,8 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
   const int hk = a.parts ? hb / a.group : hb;
   const int head0 = a.parts ? hb : hb * a.group, nheads = a.parts ? 1 : a.group;
   uint32_t local, units;
-  const int doc = find_document(a.docs.k_start, a.docs.k_len, a.docs.rows_k, a.docs.count, 1,
-                                kCols, blockIdx.x / heads, &local, &units);
-  if (doc < 0) return;
-  const Doc d = load_doc(a.docs, doc);
+  Doc d;
+  if (find_document<true>(a.docs, 1, kCols, blockIdx.x / heads, &local, &units, &d) < 0) return;
   const int key0 = (int)local * kCols;
   const int wkey = key0 + wave * 32;
   const int key = wkey + (lane & 31);
@@ -956,13 +1052,14 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
       // limits of the tile's rows grow with the token
       if (wkey < key_limit(a, d, t0 + kRows - 1)) {
         const int tile = buf * 2 * kTile;
-        f32x16 s = times_rows<T, DT>(mem, tile, 0, at, kf), dp;
+        f32x16 s[1], dp[1];
         if constexpr (kValuesInLds)
-          dp = times_staged<T, DT>(mem, tile + kTile, 4 * kTile + wave * 32 * DT * 2, at);
+          two_products_staged<T, DT, 2>(mem, tile, tile + kTile, 4 * kTile + wave * 32 * DT * 2, at,
+                                     kf, s[0], dp[0]);
         else
-          dp = times_rows<T, DT>(mem, tile + kTile, 0, at, vf);
+          two_products<T, DT>(mem, tile, tile + kTile, at, kf, vf, s[0], dp[0]);
         const int off = t0 + shift - key;
-        weigh<kMode>(s, dp, sc, [&](int i) { return s_lse[buf][result_row(i)]; },
+        weigh<kMode>(s[0], dp[0], sc, [&](int i) { return s_lse[buf][result_row(i)]; },
                      [&](int i) { return s_delta[buf][result_row(i)]; },
                      [&](int i) { return slope * fabsf((float)(off + result_row(i))); });
         if (key_limit(a, d, t0) < wkey + 32) {
@@ -970,12 +1067,12 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const bool seen = here < key_limit(a, d, t0 + result_row(i));
-            s[i] = seen ? s[i] : 0.0f;
-            dp[i] = seen ? dp[i] : 0.0f;
+            s[0][i] = seen ? s[0][i] : 0.0f;
+            dp[0][i] = seen ? dp[0][i] : 0.0f;
           }
         }
-        add_cols<T, DT>(mem, tile + kTile, 0, at, s, gv);
-        add_cols<T, DT>(mem, tile, 0, at, dp, gk);
+        AddCols<T, DT, 1, 2>(mem, tile + kTile, at).run(s, gv);
+        AddCols<T, DT, 1, 2>(mem, tile, at).run(dp, gk);
       }
       if (more) put(buf ^ 1);
     }
@@ -1007,16 +1104,233 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
   }
 }
 
+// dq where there are few columns: as the forward's few-column form, a
+// workgroup takes 32 columns, its wavefronts 32 keys each in turn, and their
+// sums are added in order.
+template <typename T, int DT, int kMode>
+__global__ __launch_bounds__(256, DT == 128 ? 2 : 3) void attention_dq_few_kernel(AttnArgs a) {
+  typedef typename Mat<T>::V8 V8;
+  constexpr int kStride = DT + 4;
+  __shared__ __align__(256) float s_raw[4 * 32 * kStride];
+  __shared__ float s_delta[4][32];
+  char* const mem = (char*)s_raw;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tile = wave * 32 * DT * 2;
+  const Lane<DT> at;
+  const int hk = blockIdx.x % a.heads_k;
+  uint32_t local, units;
+  Doc d;
+  if (find_document<false>(a.docs, a.group, 32, blockIdx.x / a.heads_k, &local, &units, &d) < 0)
+    return;
+  const uint32_t col0 = (units - 1 - local) * 32, cols = (uint32_t)d.ql * a.group;
+  const Col col = column(a, d, hk, col0 + (lane & 31), cols);
+  const int64_t row = d.qs + col.token;
+  const bool any = col.ok && col.lim > 0;
+  V8 qf[DT / 16], df[DT / 16];
+  load_cols<T, DT>(a.q + row * a.q_row + (int64_t)col.head * a.q_head, col.ok, a.dim, qf);
+  load_cols<T, DT>(a.d + row * a.d_row + (int64_t)col.head * a.d_head, col.ok, a.dim, df);
+  const int64_t place_of = (int64_t)col.head * a.docs.rows_q + row;
+  const float lse = any ? a.lse[place_of] * kLog2e : INFINITY;
+  float delta;
+  {
+    V8 of[DT / 16];
+    load_cols<T, DT>(a.o + row * a.o_row + (int64_t)col.head * a.o_head, any, a.dim, of);
+    delta = dot_cols<T, DT / 16>(of, df);
+  }
+  const float slope = (kMode & kGeneral) && a.slopes && col.ok ? a.slopes[col.head] * kLog2e
+                                                               : 0.0f;
+  const Scale sc = scale_of<kMode>(a);
+  const int last_token = (int)((min(col0 + 32, cols) - 1) / a.group);
+  const int end = key_limit(a, d, last_token);
+  const int wave_lo = __builtin_amdgcn_readlane(col.lim, 0);
+  const uint16_t* kb = a.k + (int64_t)d.ks * a.k_row + (int64_t)hk * a.k_head;
+  const uint16_t* vb = a.v + (int64_t)d.ks * a.v_row + (int64_t)hk * a.v_head;
+  Fragments<T, DT> kf, vf;
+  auto fetch = [&](int k0) {
+    kf.load(kb + (int64_t)k0 * a.k_row, a.k_row, d.kl - k0, a.dim);
+    vf.load(vb + (int64_t)k0 * a.v_row, a.v_row, d.kl - k0, a.dim);
+  };
+  const bool biased = (kMode & kGeneral) && a.slopes;
+  if (biased || wave_lo <= kKeys) {
+    float sum = 0.0f;
+    const int last = biased ? end : min(end, kKeys);
+    int k0 = wave * 32;
+    if (k0 < last) fetch(k0);
+    for (; k0 < last; k0 += kPieceKeys) {
+      const f32x16 s = kf.times(qf), dp = vf.times(df);
+      if (k0 + kPieceKeys < last) fetch(k0 + kPieceKeys);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float f;
+        const int key = k0 + result_row(i);
+        const float x = score<kMode>(
+            s[i], sc, [&] { return slope * fabsf((float)(col.pos - key)); }, f);
+        const float p = __builtin_amdgcn_exp2f(kMode == 0 ? fmaf(x, sc.mul, -lse) : x - lse);
+        sum = key < col.lim ? fmaf(p, dp[i], sum) : sum;
+      }
+    }
+    sum = both_sum(sum);
+    if (lane < 32) s_delta[wave][lane] = sum;
+    __syncthreads();
+    sum = ((s_delta[0][lane & 31] + s_delta[1][lane & 31]) + s_delta[2][lane & 31]) +
+          s_delta[3][lane & 31];
+    if (biased || col.lim <= kKeys) delta = any ? sum : 0.0f;
+  }
+  if (col.ok && wave == 0 && lane < 32) a.delta[place_of] = delta;
+  f32x16 g[DT / 32];
+#pragma unroll
+  for (int i = 0; i < DT / 32; ++i) g[i] = (f32x16)(0.0f);
+  int k0 = wave * 32;
+  if (k0 < end) fetch(k0);
+  for (; k0 < end; k0 += kPieceKeys) {
+    f32x16 s = kf.times(qf), dp[1] = {vf.times(df)};
+    kf.store(mem, tile, at);
+    own_lds_written();
+    if (k0 + kPieceKeys < end) fetch(k0 + kPieceKeys);
+    const int off = col.pos - k0;
+    weigh<kMode>(s, dp[0], sc, [&](int) { return lse; }, [&](int) { return delta; },
+                 [&](int i) { return slope * fabsf((float)(off - result_row(i))); });
+    if (k0 + 32 > wave_lo) {
+      const int room = only_here(col.lim - k0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dp[0][i] = result_row(i) < room ? dp[0][i] : 0.0f;
+    }
+    AddCols<T, DT, 1>(mem, tile, at).run(dp, g);
+  }
+  __syncthreads();
+  leave_cols<DT>(s_raw, g);
+  __syncthreads();
+  const int cc = threadIdx.x >> 3, e0 = (threadIdx.x & 7) * (DT / 8);
+  if (col0 + cc >= cols) return;
+  const Col w = column(a, d, hk, col0 + cc, cols);
+  uint16_t* out = a.out0 + (int64_t)(d.qs + w.token) * a.out0_row + (int64_t)w.head * a.out0_head;
+  for (int e = e0; e < e0 + DT / 8 && e < a.dim; e += 8) {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float* p = s_raw + cc * kStride + e + j;
+      x[j] = ((p[0] + p[32 * kStride]) + p[64 * kStride]) + p[96 * kStride];
+      x[j] = w.lim <= 0 ? 0.0f : x[j] * a.scale;
+    }
+    store_elems((T*)(out + e), x);
+  }
+}
+
+// dk and dv where there are few keys: a workgroup takes 32 keys of a key head,
+// its wavefronts 32 tokens of a query head each in turn, and their sums are
+// added in order (a.parts: as above).
+template <typename T, int DT, int kMode>
+__global__ __launch_bounds__(256, DT == 128 ? 1 : 2) void attention_dkv_few_kernel(AttnArgs a) {
+  typedef typename Mat<T>::V8 V8;
+  constexpr int kStride = DT + 4;
+  constexpr int kTile = 32 * DT * 2;
+  constexpr int kBytes = 8 * kTile > 4 * 32 * kStride * 4 ? 8 * kTile : 4 * 32 * kStride * 4;
+  __shared__ __align__(256) float s_raw[kBytes / 4];
+  __shared__ __align__(16) float s_row[4][2][32];
+  char* const mem = (char*)s_raw;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tile = wave * 2 * kTile;
+  const Lane<DT> at;
+  const int heads = a.parts ? a.heads_q : a.heads_k;
+  const int hb = blockIdx.x % heads;
+  const int hk = a.parts ? hb / a.group : hb;
+  const int head0 = a.parts ? hb : hb * a.group, nheads = a.parts ? 1 : a.group;
+  uint32_t local, units;
+  Doc d;
+  if (find_document<true>(a.docs, 1, 32, blockIdx.x / heads, &local, &units, &d) < 0) return;
+  const int key0 = (int)local * 32, key = key0 + (lane & 31);
+  const int64_t row = d.ks + key0;
+  Fragments<T, DT> kf, vf, qf, df;
+  kf.load(a.k + row * a.k_row + (int64_t)hk * a.k_head, a.k_row, d.kl - key0, a.dim);
+  vf.load(a.v + row * a.v_row + (int64_t)hk * a.v_head, a.v_row, d.kl - key0, a.dim);
+  f32x16 gk[DT / 32], gv[DT / 32];
+#pragma unroll
+  for (int i = 0; i < DT / 32; ++i) gk[i] = gv[i] = (f32x16)(0.0f);
+  const Scale sc = scale_of<kMode>(a);
+  const int shift = d.kl - d.ql;
+  int first = 0;
+  if (a.causal && key0 >= d.prefix) first = min(max(key0 - shift, 0), d.ql) / 32 * 32;
+  const int tiles = (d.ql - first + 31) / 32, total = tiles * nheads;
+  float r_lse = 0.0f, r_delta = 0.0f;
+  // tile n: tokens first + 32 (n % tiles) of query head head0 + n / tiles
+  auto fetch = [&](int n) {
+    const int h = n / tiles, t0 = first + (n - h * tiles) * 32, head = head0 + h;
+    const int64_t r = d.qs + t0;
+    qf.load(a.q + r * a.q_row + (int64_t)head * a.q_head, a.q_row, d.ql - t0, a.dim);
+    df.load(a.d + r * a.d_row + (int64_t)head * a.d_head, a.d_row, d.ql - t0, a.dim);
+    const int t = t0 + (lane & 31);
+    r_lse = INFINITY;
+    r_delta = 0.0f;
+    if (t < d.ql && key_limit(a, d, t) > 0) {
+      const int64_t p = (int64_t)head * a.docs.rows_q + d.qs + t;
+      r_lse = a.lse[p] * kLog2e;
+      r_delta = a.delta[p];
+    }
+  };
+  int n = wave;
+  if (n < total) fetch(n);
+  for (; n < total; n += 4) {
+    const int h = n / tiles, t0 = first + (n - h * tiles) * 32;
+    f32x16 s[1] = {qf.times(kf.f)}, dp[1] = {df.times(vf.f)};
+    qf.store(mem, tile, at);
+    df.store(mem, tile + kTile, at);
+    if (lane < 32) {
+      s_row[wave][0][lane] = r_lse;
+      s_row[wave][1][lane] = r_delta;
+    }
+    own_lds_written();
+    if (n + 4 < total) fetch(n + 4);
+    const float slope =
+        (kMode & kGeneral) && a.slopes ? a.slopes[head0 + h] * kLog2e : 0.0f;
+    const int off = t0 + shift - key;
+    weigh<kMode>(s[0], dp[0], sc, [&](int i) { return s_row[wave][0][result_row(i)]; },
+                 [&](int i) { return s_row[wave][1][result_row(i)]; },
+                 [&](int i) { return slope * fabsf((float)(off + result_row(i))); });
+    if (key_limit(a, d, t0) < key0 + 32) {
+      const int here = only_here(key);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool seen = here < key_limit(a, d, t0 + result_row(i));
+        s[0][i] = seen ? s[0][i] : 0.0f;
+        dp[0][i] = seen ? dp[0][i] : 0.0f;
+      }
+    }
+    AddCols<T, DT, 1>(mem, tile + kTile, at).run(s, gv);
+    AddCols<T, DT, 1>(mem, tile, at).run(dp, gk);
+  }
+  const int cc = threadIdx.x >> 3, e0 = (threadIdx.x & 7) * (DT / 8);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    __syncthreads();
+    leave_cols<DT>(s_raw, w ? gv : gk);
+    __syncthreads();
+    if (key0 + cc >= d.kl) continue;
+    uint16_t* out = w ? a.out1 + (row + cc) * a.out1_row + (int64_t)hk * a.out1_head
+                      : a.out0 + (row + cc) * a.out0_row + (int64_t)hk * a.out0_head;
+    for (int e = e0; e < e0 + DT / 8 && e < a.dim; e += 8) {
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float* p = s_raw + cc * kStride + e + j;
+        x[j] = ((p[0] + p[32 * kStride]) + p[64 * kStride]) + p[96 * kStride];
+        if (!w && !a.parts) x[j] *= a.scale;
+      }
+      if (a.parts)
+        store_elems(a.part_o + (((row + cc) * a.heads_q + hb) * 2 + w) * a.dim + e, x);
+      else
+        store_elems((T*)(out + e), x);
+    }
+  }
+}
+
 // Sums of a key head's dk and dv over its query heads, in order: 64 keys a
 // workgroup, 16 lanes a key, 8 elements a lane.
 template <typename T>
 __global__ __launch_bounds__(256) void attention_heads_kernel(AttnArgs a) {
   const int hk = blockIdx.x % a.heads_k;
   uint32_t local, units;
-  const int doc = find_document(a.docs.k_start, a.docs.k_len, a.docs.rows_k, a.docs.count, 1, 64,
-                                blockIdx.x / a.heads_k, &local, &units);
-  if (doc < 0) return;
-  const Doc d = load_doc(a.docs, doc);
+  Doc d;
+  if (find_document<true>(a.docs, 1, 64, blockIdx.x / a.heads_k, &local, &units, &d) < 0) return;
   const int e = (threadIdx.x & 15) * 8;
   if (e >= a.dim) return;
   for (int i = 0; i < 4; ++i) {
@@ -1080,24 +1394,39 @@ int64_t unit_bound(int64_t columns, int64_t step, int32_t count) {
   return columns / step + count;
 }
 
-// The one-token form: how many pieces a document's keys are cut into.
+// The few-column form, and how many pieces it cuts a document's keys into.
 struct Split {
-  bool step;
-  int pieces, piece, col_tiles;
+  bool few, col_units;
+  int pieces, piece;
+  int64_t units;  // column tiles of a key head
+  int cols;       // columns of a tile that a document may have
 };
+// Workgroups of the 128-column form below which the few-column form is taken.
+int64_t few_blocks() {
+  const char* e = getenv("GS_FEW");
+  return e ? atoi(e) : 1024;
+}
 Split split_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q,
                int64_t rows_k) {
   Split o = {};
+  const int64_t group = cfg.heads_q / cfg.heads_k;
   const int64_t longest_q = d.max_q_len > 0 && d.max_q_len < rows_q ? d.max_q_len : rows_q;
   const int64_t longest_k = d.max_k_len > 0 && d.max_k_len < rows_k ? d.max_k_len : rows_k;
-  const int64_t cols = longest_q * (cfg.heads_q / cfg.heads_k);
-  o.step = cols <= 32;
-  o.col_tiles = 1;
-  const int64_t base = (int64_t)d.count * cfg.heads_k;
-  const int64_t want = (2048 + base - 1) / base;
+  // one tile a document, or a look-up
+  o.col_units = longest_q * group > 32;
+  o.units = o.col_units ? unit_bound(rows_q * group, 32, d.count) : d.count;
+  o.cols = o.col_units ? 32 : (int)(longest_q * group);
+  o.few = !o.col_units || unit_bound(rows_q * group, kCols, d.count) * cfg.heads_k < few_blocks();
+  const int64_t base = o.units * cfg.heads_k;
+  // two rounds of the three workgroups a compute unit holds: fewer leave it
+  // waiting for the longest, more pay a workgroup's start and end too often
+  // (64 caches of 100,003 keys in all: 59, 54, 44, 67 us at 512, 768, 1536,
+  // 2048 wanted)
+  const int64_t want = ((o.col_units ? 512 : 1536) + base - 1) / base;
   int64_t piece = (longest_k + want - 1) / want;
   piece = (piece + kPieceKeys - 1) / kPieceKeys * kPieceKeys;
-  if (piece < 2 * kPieceKeys) piece = 2 * kPieceKeys;
+  const int64_t least = o.col_units ? 8 * kPieceKeys : 2 * kPieceKeys;
+  if (piece < least) piece = least;
   o.piece = (int)piece;
   o.pieces = (int)((longest_k + piece - 1) / piece);
   if (o.pieces < 1) o.pieces = 1;
@@ -1106,17 +1435,31 @@ Split split_of(const gs_attention_config& cfg, const gs_documents& d, int64_t ro
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
+// The few-key form of dk and dv: few workgroups of the 128-key form even with
+// one to a query head.
+bool few_keys(int64_t rows_k, int32_t count, int32_t heads_q) {
+  return unit_bound(rows_k, kCols, count) * heads_q < few_blocks();
+}
+
+// Whether dk and dv are summed per query head first: too few workgroups
+// otherwise, with as many as two to a compute unit.
+bool head_parts(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_k) {
+  if (cfg.heads_q == cfg.heads_k) return false;
+  const int step = few_keys(rows_k, d.count, cfg.heads_q) ? 32 : kCols;
+  return unit_bound(rows_k, step, d.count) * cfg.heads_k < 2048;
+}
+
 // The kernels of one element type, head size and way to make scores.
 template <typename T, int DT, int kMode>
 struct Run {
-  static hipError_t fwd(const AttnArgs& a, bool step, hipStream_t s) {
-    if (step) {
-      const int64_t blocks = (int64_t)a.docs.count * a.pieces * a.col_tiles * a.heads_k;
-      attention_step_kernel<T, DT, kMode><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(a);
+  static hipError_t fwd(const AttnArgs& a, const Split& p, hipStream_t s) {
+    if (p.few) {
+      const int64_t tiles = p.units * a.heads_k;
+      attention_step_kernel<T, DT, kMode>
+          <<<dim3((uint32_t)(tiles * a.pieces)), dim3(256), 0, s>>>(a);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess || a.pieces == 1) return e;
-      attention_join_kernel<T><<<dim3((uint32_t)((int64_t)a.docs.count * a.heads_q)), dim3(256),
-                                 0, s>>>(a);
+      attention_join_kernel<T><<<dim3((uint32_t)(tiles * p.cols)), dim3(256), 0, s>>>(a, p.cols);
       return hipGetLastError();
     }
     const int64_t units = unit_bound((int64_t)a.docs.rows_q * a.group, kCols, a.docs.count);
@@ -1129,21 +1472,29 @@ struct Run {
                         hipStream_t s) {
     const dim3 block(256);
     if (a.docs.rows_q > 0) {
-      const int64_t items = (int64_t)a.docs.rows_q * a.heads_q;
-      attention_delta_kernel<T><<<dim3((uint32_t)((items + 15) / 16)), block, 0, s>>>(a);
-      hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
       a.out0 = (uint16_t*)dq.data; a.out0_row = dq.row; a.out0_head = dq.head;
-      const int64_t units = unit_bound((int64_t)a.docs.rows_q * a.group, kCols, a.docs.count);
-      attention_dq_kernel<T, DT, kMode><<<dim3((uint32_t)(units * a.heads_k)), block, 0, s>>>(a);
-      e = hipGetLastError();
+      const int64_t columns = (int64_t)a.docs.rows_q * a.group;
+      const int64_t blocks = unit_bound(columns, kCols, a.docs.count) * a.heads_k;
+      if (blocks < few_blocks()) {
+        const int64_t few = unit_bound(columns, 32, a.docs.count) * a.heads_k;
+        attention_dq_few_kernel<T, DT, kMode><<<dim3((uint32_t)few), block, 0, s>>>(a);
+      } else {
+        attention_dq_kernel<T, DT, kMode><<<dim3((uint32_t)blocks), block, 0, s>>>(a);
+      }
+      const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
     a.out0 = (uint16_t*)dk.data; a.out0_row = dk.row; a.out0_head = dk.head;
     a.out1 = (uint16_t*)dv.data; a.out1_row = dv.row; a.out1_head = dv.head;
-    const int64_t blocks = unit_bound(a.docs.rows_k, kCols, a.docs.count) *
-                           (a.parts ? a.heads_q : a.heads_k);
-    attention_dkv_kernel<T, DT, kMode><<<dim3((uint32_t)blocks), block, 0, s>>>(a);
+    if (few_keys(a.docs.rows_k, a.docs.count, a.heads_q)) {
+      const int64_t few = unit_bound(a.docs.rows_k, 32, a.docs.count) *
+                          (a.parts ? a.heads_q : a.heads_k);
+      attention_dkv_few_kernel<T, DT, kMode><<<dim3((uint32_t)few), block, 0, s>>>(a);
+    } else {
+      const int64_t blocks = unit_bound(a.docs.rows_k, kCols, a.docs.count) *
+                             (a.parts ? a.heads_q : a.heads_k);
+      attention_dkv_kernel<T, DT, kMode><<<dim3((uint32_t)blocks), block, 0, s>>>(a);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.parts) return e;
     const int64_t sums = unit_bound(a.docs.rows_k, 64, a.docs.count) * a.heads_k;
@@ -1168,13 +1519,6 @@ hipError_t dispatch(const gs_attention_config& cfg, const AttnArgs& a, F f) {
   return cfg.head_dim > 64 ? with_mode<F16, 128>(a, f) : with_mode<F16, 64>(a, f);
 }
 
-// Whether dk and dv are summed per query head first: too few workgroups
-// otherwise, with as many as two to a compute unit.
-bool head_parts(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_k) {
-  return cfg.heads_q > cfg.heads_k &&
-         unit_bound(rows_k, kCols, d.count) * cfg.heads_k < 2048;
-}
-
 }  // namespace
 
 extern "C" {
@@ -1183,7 +1527,7 @@ size_t gs_attention_fwd_bytes(const gs_attention_config& cfg, const gs_documents
                               int64_t rows_q, int64_t rows_k) {
   if (d.count == 0 || rows_q == 0) return 0;
   const Split p = split_of(cfg, d, rows_q, rows_k);
-  if (!p.step || p.pieces == 1) return 0;
+  if (!p.few || p.pieces == 1) return 0;
   const size_t columns = (size_t)p.pieces * cfg.heads_q * rows_q;
   return align256(columns * 2 * sizeof(float)) + columns * cfg.head_dim * sizeof(float);
 }
@@ -1207,11 +1551,11 @@ hipError_t gs_launch_attention_fwd(const gs_attention_config& cfg, const gs_docu
   const Split p = split_of(cfg, d, rows_q, rows_k);
   a.pieces = p.pieces;
   a.piece = p.piece;
-  a.col_tiles = p.col_tiles;
+  a.col_units = p.col_units;
   a.part_ml = (float*)workspace;
   a.part_o = (float*)((char*)workspace +
                       align256((size_t)p.pieces * cfg.heads_q * rows_q * 2 * sizeof(float)));
-  return dispatch(cfg, a, [&](auto run) { return run.fwd(a, p.step, s); });
+  return dispatch(cfg, a, [&](auto run) { return run.fwd(a, p, s); });
 }
 
 hipError_t gs_launch_attention_bwd(const gs_attention_config& cfg, const gs_documents& d,

@@ -90,14 +90,12 @@ __device__ inline Item chunk_item(const GatedArgs& a) {
   uint32_t local, n;
   it.doc = -1;
   if (unit >= a.chunks) return it;
-  it.doc = find_document(a.docs.q_start, a.docs.q_len, a.docs.rows_q, a.docs.count, 1, kChunk,
-                         unit, &local, &n);
+  Doc d;
+  it.doc = find_document<false>(a.docs, 1, kChunk, unit, &local, &n, &d, false);
   if (it.doc < 0) return it;
-  const int start = a.docs.q_start[it.doc];
-  const int len = clamp_len(start, a.docs.q_len[it.doc], a.docs.rows_q);
   it.chunk = unit;
-  it.row0 = (int64_t)clamp_start(start, a.docs.rows_q) + (int64_t)local * kChunk;
-  it.steps = min(kChunk, len - (int)local * kChunk);
+  it.row0 = (int64_t)d.qs + (int64_t)local * kChunk;
+  it.steps = min(kChunk, d.ql - (int)local * kChunk);
   it.ch = (group * 64 + (threadIdx.x & 63)) * V;
   it.on = it.ch < a.channels;
   return it;

@@ -41,33 +41,68 @@ __device__ inline int clamp_len(int start, int len, int rows) {
   return min(max(len, 0), rows - clamp_start(start, rows));
 }
 
+// Inclusive sum over the wavefront's 64 lanes, by lane-to-lane moves.
+__device__ inline uint32_t wave_scan(uint32_t v) {
+#define GS_SCAN(ctrl, rows) \
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xF, true)
+  GS_SCAN(0x111, 0xF);  // row_shr:1
+  GS_SCAN(0x112, 0xF);  // row_shr:2
+  GS_SCAN(0x114, 0xF);  // row_shr:4
+  GS_SCAN(0x118, 0xF);  // row_shr:8
+  GS_SCAN(0x142, 0xA);  // row_bcast:15 into rows 1 and 3
+  GS_SCAN(0x143, 0xC);  // row_bcast:31 into rows 2 and 3
+#undef GS_SCAN
+  return v;
+}
+
+// A document as the kernels use it.
+struct Doc {
+  int qs, ql, ks, kl, prefix;
+};
+__device__ inline Doc load_doc(const Docs& d, int i, bool keys = true) {
+  Doc o;
+  const int qs = d.q_start[i], ql = d.q_len[i];
+  const int ks = keys ? d.k_start[i] : qs, kl = keys ? d.k_len[i] : ql;
+  const int prefix = keys && d.prefix ? d.prefix[i] : 0;
+  o.qs = clamp_start(qs, d.rows_q);
+  o.ql = clamp_len(qs, ql, d.rows_q);
+  o.ks = clamp_start(ks, d.rows_k);
+  o.kl = clamp_len(ks, kl, d.rows_k);
+  o.prefix = min(max(prefix, 0), o.kl);
+  return o;
+}
+
 // The document of work unit `unit`, where document d has
-// ceil(len[d] * mult / step) units, and the unit's index within it.  Every
-// wavefront of the workgroup does the same scan, 64 documents at a time.
-// Returns -1 past the last unit.
-__device__ inline int find_document(const int* start, const int* len, int rows, int count,
-                                    uint32_t mult, uint32_t step, uint32_t unit,
-                                    uint32_t* local, uint32_t* units_of) {
+// ceil(n * mult / step) units, n its number of keys (kByKeys) or tokens, and
+// the unit's index within it.  Every wavefront of the workgroup does the same
+// scan, 64 documents at a time; all of a document's numbers are loaded
+// together, since nothing else can start before they are there.  Returns -1
+// past the last unit.
+template <bool kByKeys>
+__device__ inline int find_document(const Docs& docs, uint32_t mult, uint32_t step, uint32_t unit,
+                                    uint32_t* local, uint32_t* units_of, Doc* doc,
+                                    bool keys = true) {
   const int lane = threadIdx.x & 63;
-  for (int base = 0; base < count; base += 64) {
-    const int d = base + lane;
-    uint32_t n = 0;
-    if (d < count) n = ((uint32_t)clamp_len(start[d], len[d], rows) * mult + step - 1) / step;
-    uint32_t cum = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t up = __shfl_up(cum, o, 64);
-      if (lane >= o) cum += up;
-    }
+  for (int base = 0; base < docs.count; base += 64) {
+    const int i = base + lane;
+    Doc d = {0, 0, 0, 0, 0};
+    if (i < docs.count) d = load_doc(docs, i, keys);
+    const uint32_t n = ((uint32_t)(kByKeys ? d.kl : d.ql) * mult + step - 1) / step;
+    const uint32_t cum = wave_scan(n);
     const uint64_t hit = __ballot(cum > unit);
     if (hit) {
       const int f = __ffsll((unsigned long long)hit) - 1;
-      const uint32_t nf = __shfl(n, f, 64), cf = __shfl(cum, f, 64);
-      *local = __builtin_amdgcn_readfirstlane(unit - (cf - nf));
-      *units_of = __builtin_amdgcn_readfirstlane(nf);
-      return __builtin_amdgcn_readfirstlane(base + f);
+      const uint32_t nf = (uint32_t)__builtin_amdgcn_readlane((int)n, f);
+      *local = unit - ((uint32_t)__builtin_amdgcn_readlane((int)cum, f) - nf);
+      *units_of = nf;
+      doc->qs = __builtin_amdgcn_readlane(d.qs, f);
+      doc->ql = __builtin_amdgcn_readlane(d.ql, f);
+      doc->ks = __builtin_amdgcn_readlane(d.ks, f);
+      doc->kl = __builtin_amdgcn_readlane(d.kl, f);
+      doc->prefix = __builtin_amdgcn_readlane(d.prefix, f);
+      return base + f;
     }
-    unit -= __shfl(cum, 63, 64);
+    unit -= (uint32_t)__builtin_amdgcn_readlane((int)cum, 63);
   }
   return -1;
 }

@@ -241,10 +241,26 @@ def _p(t):
     return C.c_void_p(t.data_ptr())
 
 
+_raw_stream = None
+
+
 def _stream(stream):
-    import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return C.c_void_p(s.cuda_stream)
+    """hipStream_t of a torch stream, or of the current one (by its raw handle
+    where torch offers it: making a Stream object costs 2.5 us a call, as much
+    as a kernel launch)."""
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        if raw is not None and device is not None:
+            torch.cuda.current_stream()  # initialises the device
+            _raw_stream = lambda: raw(device())
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+    return _raw_stream()
 
 
 def make_camera(cam) -> gs_camera:
@@ -666,11 +682,20 @@ def rows(t) -> gs_rows:
 
 
 def _heads(t):
-    return None if t is None else C.byref(t if isinstance(t, gs_heads) else heads(t))
+    if t is None:
+        return None
+    return C.byref(t if type(t) is gs_heads else heads(t))
 
 
 def _rows(t):
-    return None if t is None else C.byref(t if isinstance(t, gs_rows) else rows(t))
+    if t is None:
+        return None
+    return C.byref(t if type(t) is gs_rows else rows(t))
+
+
+def _at(t):
+    """Device address of a tensor, None for None."""
+    return None if t is None else t.data_ptr()
 
 
 def documents(q_start, q_len, k_start=None, k_len=None, prefix=None, max_q_len=0,
@@ -715,8 +740,8 @@ def scan_config(dtype, channels, coupled=True) -> gs_scan_config:
 
 def gs_qk_norm_rope_fwd(cfg, rows, positions, inv_freq, wq, wk, q, k, q_out, k_out, stream=None):
     lib = load()
-    _check(lib.gs_qk_norm_rope_fwd(C.byref(cfg), rows, _p(positions), _p(inv_freq), _p(wq),
-                                   _p(wk), _heads(q), _heads(k), _heads(q_out), _heads(k_out),
+    _check(lib.gs_qk_norm_rope_fwd(C.byref(cfg), rows, _at(positions), _at(inv_freq), _at(wq),
+                                   _at(wk), _heads(q), _heads(k), _heads(q_out), _heads(k_out),
                                    _stream(stream)))
 
 
@@ -727,10 +752,10 @@ def gs_qk_norm_rope_bwd_workspace_size(cfg, rows) -> int:
 def gs_qk_norm_rope_bwd(cfg, rows, positions, inv_freq, wq, wk, q, k, dL_dq_out, dL_dk_out,
                         dL_dq, dL_dk, dL_dwq, dL_dwk, workspace, workspace_bytes, stream=None):
     lib = load()
-    _check(lib.gs_qk_norm_rope_bwd(C.byref(cfg), rows, _p(positions), _p(inv_freq), _p(wq),
-                                   _p(wk), _heads(q), _heads(k), _heads(dL_dq_out),
-                                   _heads(dL_dk_out), _heads(dL_dq), _heads(dL_dk), _p(dL_dwq),
-                                   _p(dL_dwk), _p(workspace), int(workspace_bytes),
+    _check(lib.gs_qk_norm_rope_bwd(C.byref(cfg), rows, _at(positions), _at(inv_freq), _at(wq),
+                                   _at(wk), _heads(q), _heads(k), _heads(dL_dq_out),
+                                   _heads(dL_dk_out), _heads(dL_dq), _heads(dL_dk), _at(dL_dwq),
+                                   _at(dL_dwk), _at(workspace), int(workspace_bytes),
                                    _stream(stream)))
 
 
@@ -744,7 +769,7 @@ def gs_attention_fwd(cfg, docs, rows_q, rows_k, q, k, v, out, lse, workspace, wo
     """lse: fp32 [heads_q, rows_q], or None where no gradient follows."""
     lib = load()
     _check(lib.gs_attention_fwd(C.byref(cfg), C.byref(docs), rows_q, rows_k, _heads(q), _heads(k),
-                                _heads(v), _heads(out), _p(lse), _p(workspace),
+                                _heads(v), _heads(out), _at(lse), _at(workspace),
                                 int(workspace_bytes), _stream(stream)))
 
 
@@ -757,8 +782,8 @@ def gs_attention_bwd(cfg, docs, rows_q, rows_k, q, k, v, out, lse, dL_dout, dL_d
                      workspace, workspace_bytes, stream=None):
     lib = load()
     _check(lib.gs_attention_bwd(C.byref(cfg), C.byref(docs), rows_q, rows_k, _heads(q), _heads(k),
-                                _heads(v), _heads(out), _p(lse), _heads(dL_dout), _heads(dL_dq),
-                                _heads(dL_dk), _heads(dL_dv), _p(workspace),
+                                _heads(v), _heads(out), _at(lse), _heads(dL_dout), _heads(dL_dq),
+                                _heads(dL_dk), _heads(dL_dv), _at(workspace),
                                 int(workspace_bytes), _stream(stream)))
 
 
@@ -775,7 +800,7 @@ def gs_gated_scan_fwd(cfg, docs, rows, gate, x, state_in, y, state_out, saved, w
     """saved: None, or gs_gated_scan_saved_size() bytes for the gradient."""
     lib = load()
     _check(lib.gs_gated_scan_fwd(C.byref(cfg), C.byref(docs), rows, _rows(gate), _rows(x),
-                                 _p(state_in), _rows(y), _p(state_out), _p(saved), _p(workspace),
+                                 _at(state_in), _rows(y), _at(state_out), _at(saved), _at(workspace),
                                  int(workspace_bytes), _stream(stream)))
 
 
@@ -787,8 +812,8 @@ def gs_gated_scan_bwd(cfg, docs, rows, gate, x, saved, dL_dy, dL_dstate_out, dL_
                       dL_dstate_in, workspace, workspace_bytes, stream=None):
     lib = load()
     _check(lib.gs_gated_scan_bwd(C.byref(cfg), C.byref(docs), rows, _rows(gate), _rows(x),
-                                 _p(saved), _rows(dL_dy), _p(dL_dstate_out), _rows(dL_dgate),
-                                 _rows(dL_dx), _p(dL_dstate_in), _p(workspace),
+                                 _at(saved), _rows(dL_dy), _at(dL_dstate_out), _rows(dL_dgate),
+                                 _rows(dL_dx), _at(dL_dstate_in), _at(workspace),
                                  int(workspace_bytes), _stream(stream)))
 
 
