@@ -24,7 +24,6 @@
 // c of a document is token c / group, head c % group, so one staged key tile
 // serves all of them, and one-token requests fill the columns with heads.
 #include "tokens.h"
-#include <stdlib.h>
 
 namespace gs {
 
@@ -185,37 +184,44 @@ __device__ inline void load_cols(const uint16_t* p, bool ok, int dim,
   }
 }
 
-// A tile of ROWS rows on its way into LDS: loaded into registers while the
-// tile before it is computed.  The loads go through a buffer descriptor that
-// ends with the document's last row, so that rows past `valid` (and elements
-// past dim, whose offset is past every end) come back as zeros without a
-// branch; rows of a tile are within 2^31 bytes of each other (row strides are
-// below 2^23 elements).
+// A tile of ROWS rows, copied from memory into LDS by all 256 lanes without
+// passing through registers (buffer loads with an LDS destination: lane l of a
+// wavefront fills the 16 bytes l of its kilobyte, so it is the source address
+// that follows the tile's chunk order).  The buffer descriptor ends with the
+// document's last row: rows past `valid` (and elements past dim, whose offset
+// is past every end) arrive as zeros, without a branch; rows of a tile are
+// within 2^31 bytes of each other (row strides are below 2^23 elements).
+// The copies are counted by vmcnt but unknown to the compiler, whose own waits
+// can only be longer for it: arrived() must come before the barrier after
+// which the tile is read.
 template <int DT, int ROWS>
-struct Staged {
-  static constexpr int kChunks = DT / 8;
-  static constexpr int kPer = ROWS * kChunks / 256;
-  u32x4 w[kPer];
-  __device__ inline void load(const uint16_t* base, int64_t row_stride, int valid, int dim) {
-    const int stride = (int)row_stride * 2;
-    const int64_t bytes = valid > 0 ? (int64_t)(valid - 1) * stride + dim * 2 : 0;
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(base), 0, (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff),
-        0x00027000);
-    const int r = threadIdx.x / kChunks, c = threadIdx.x % kChunks;
-    int at = c * 8 < dim ? r * stride + c * 16 : (int)0x80000000;
+__device__ inline void copy_tile(const char* mem, int tile, const uint16_t* base,
+                                 int64_t row_stride, int valid, int dim) {
+  constexpr int kChunks = DT / 8, kStep = 256 / kChunks;  // rows a pass
+  static_assert(ROWS % kStep == 0 && kStep % 16 == 0, "a pass keeps the chunk order");
+  const int stride = (int)row_stride * 2;
+  const int64_t bytes = valid > 0 ? (int64_t)(valid - 1) * stride + dim * 2 : 0;
+  const uint64_t address = (uint64_t)base;
+  const i32x4 rsrc = {(int)address, (int)((address >> 32) & 0xffff),
+                      (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff), 0x00027000};
+  const int r = threadIdx.x / kChunks;
+  // place() moves chunk c of row r by an exclusive or, its own inverse
+  const int c = (place<DT>(r, threadIdx.x % kChunks) - r * DT) / 8;
+  int at = c * 8 < dim ? r * stride + c * 16 : (int)0x80000000;
+  const uint32_t lds =
+      __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
+                                         __attribute__((address_space(3))) const char*)mem +
+                                     tile + (threadIdx.x >> 6) * 1024);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      w[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0);
-      at = c * 8 < dim ? at + 256 / kChunks * stride : at;
-    }
+  for (int i = 0; i < ROWS / kStep; ++i) {
+    asm volatile(
+        "s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(at),
+        "s"(rsrc), "s"(lds + i * 4096)
+        : "memory");
+    at = c * 8 < dim ? at + kStep * stride : at;
   }
-  __device__ inline void store(char* mem, int tile) const {
-    const int at = tile + 2 * place<DT>(threadIdx.x / kChunks, threadIdx.x % kChunks);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) *(u32x4*)(mem + at + i * 4096) = w[i];
-  }
-};
+}
+__device__ inline void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Thirty-two rows as operand fragments straight from memory (row lane % 32,
 // elements 16 ks + 8 half ...), zeros past `valid` rows and dim elements; and
@@ -378,6 +384,9 @@ struct AddCols {
     V8 w[2 * R];
 #pragma unroll
     for (int i = 0; i < 2 * R; ++i) w[i] = pack_cols<T>(s[i / 2], i % 2);
+    run(w, o);
+  }
+  __device__ inline void run(const V8 (&w)[2 * R], f32x16 (&o)[DT / 32]) {
     p.run([&](int n) { return read(n); },
           [&](int n, const V8& x) { o[n % M] = Mat<T>::mul(x, w[n / M], o[n % M]); });
   }
@@ -462,27 +471,30 @@ __device__ inline int only_here(int x) {
   return x;
 }
 
-// The running softmax of N 32-key tiles of a column, from key k0: masks,
-// moves the reference m where a score passes it by more than 8 (weights then
-// stay below 2^8, far inside every type, and the accumulators are rarely
-// rescaled), and leaves the weights in s.
-template <int DT, int N>
-__device__ inline void softmax_step(f32x16 (&s)[N], float mul, bool masked, int k0, int lim,
-                                    float& m, float& l, f32x16 (&o)[DT / 32]) {
-  if (masked) {
-    const int room = only_here(lim - k0);
+// The running softmax of a column over N 32-key tiles of scores.
+template <int N>
+__device__ inline void mask_scores(f32x16 (&s)[N], int room) {
+  const int here = only_here(room);
 #pragma unroll
-    for (int rt = 0; rt < N; ++rt)
+  for (int rt = 0; rt < N; ++rt)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        s[rt][i] = rt * 32 + result_row(i) < room ? s[rt][i] : -INFINITY;
-  }
+    for (int i = 0; i < 16; ++i)
+      s[rt][i] = rt * 32 + result_row(i) < here ? s[rt][i] : -INFINITY;
+}
+template <int N>
+__device__ inline float highest(const f32x16 (&s)[N]) {
   float top = -INFINITY;
 #pragma unroll
   for (int rt = 0; rt < N; ++rt)
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[rt][i]);
-  top = both_max(top) * mul;
+  return both_max(top);
+}
+// Moves the reference m where a score passes it by more than 8: weights then
+// stay below 2^8, far inside every type, and the accumulators are rarely
+// rescaled.
+template <int DT, int N>
+__device__ inline void move_reference(float top, float& m, float& l, f32x16 (&o)[DT / 32]) {
   if (__any(top > m + 8.0f)) {
     const float now = fmaxf(m, top);
     const float alpha = now == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - now);
@@ -491,14 +503,22 @@ __device__ inline void softmax_step(f32x16 (&s)[N], float mul, bool masked, int 
     for (int i = 0; i < DT / 32; ++i) o[i] *= alpha;
     m = now;
   }
+}
+__device__ inline void weights_of(f32x16& s, float mul, float ref, float& l) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], mul, -ref));
+    l += s[i];
+  }
+}
+template <int DT, int N>
+__device__ inline void softmax_step(f32x16 (&s)[N], float mul, bool masked, int k0, int lim,
+                                    float& m, float& l, f32x16 (&o)[DT / 32]) {
+  if (masked) mask_scores(s, lim - k0);
+  move_reference<DT, N>(highest(s) * mul, m, l, o);
   const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-  for (int rt = 0; rt < N; ++rt)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      s[rt][i] = __builtin_amdgcn_exp2f(fmaf(s[rt][i], mul, -ref));
-      l += s[rt][i];
-    }
+  for (int rt = 0; rt < N; ++rt) weights_of(s[rt], mul, ref, l);
 }
 
 // Scores of one 32-key tile in place.
@@ -514,8 +534,13 @@ __device__ inline void make_scores(f32x16& s, const Scale& c, float slope, int o
   }
 }
 
-// A workgroup takes 128 columns, a wavefront 32; key tiles of 64 pass through
-// LDS, the next one on its way in registers.
+// A workgroup takes 128 columns, a wavefront 32; key and value tiles of 64
+// pass through LDS, copied there one tile ahead of their use.  Two workgroups
+// share a compute unit, one's matrix instructions beside the other's
+// exponentials.  (The next tile's products and this one's exponentials
+// interleaved in one instruction stream were no faster with 128-element heads
+// and a sixth slower with 64; nor were workgroups of eight wavefronts, which
+// copy each tile half as often.)
 template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
@@ -532,6 +557,15 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
   // long causal rows first
   const uint32_t col0 = (units - 1 - local) * kCols;
   const uint32_t cols = (uint32_t)d.ql * a.group;
+  const int last_token = (int)((min(col0 + kCols, cols) - 1) / a.group);
+  const int end = key_limit(a, d, last_token);
+  const uint16_t* kb = a.k + (int64_t)d.ks * a.k_row + (int64_t)hk * a.k_head;
+  const uint16_t* vb = a.v + (int64_t)d.ks * a.v_row + (int64_t)hk * a.v_head;
+  auto copy = [&](int k0, int to) {
+    copy_tile<DT, kKeys>(mem, to, kb + (int64_t)k0 * a.k_row, a.k_row, d.kl - k0, a.dim);
+    copy_tile<DT, kKeys>(mem, to + kTile, vb + (int64_t)k0 * a.v_row, a.v_row, d.kl - k0, a.dim);
+  };
+  if (end > 0) copy(0, 0);
   const Col col = column(a, d, hk, col0 + wave * 32 + (lane & 31), cols);
   const int64_t row = d.qs + col.token;
   V8 qf[DT / 16];
@@ -544,41 +578,22 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
 #pragma unroll
   for (int i = 0; i < DT / 32; ++i) o[i] = (f32x16)(0.0f);
   float m = -INFINITY, l = 0.0f;
-  const int last_token = (int)((min(col0 + kCols, cols) - 1) / a.group);
-  const int end = key_limit(a, d, last_token);
   const int wave_lo = __builtin_amdgcn_readlane(col.lim, 0);
   const int wave_hi = min(__builtin_amdgcn_readlane(col.lim, 31), end);
-  const uint16_t* kb = a.k + (int64_t)d.ks * a.k_row + (int64_t)hk * a.k_head;
-  const uint16_t* vb = a.v + (int64_t)d.ks * a.v_row + (int64_t)hk * a.v_head;
-  Staged<DT, kKeys> sk, sv;
-  if (end > 0) {
-    sk.load(kb, a.k_row, d.kl, a.dim);
-    sv.load(vb, a.v_row, d.kl, a.dim);
-    sk.store(mem, 0);
-    sv.store(mem, kTile);
-  }
   int buf = 0;
   for (int k0 = 0; k0 < end; k0 += kKeys, buf ^= 2 * kTile) {
+    arrived();
     __syncthreads();
-    const bool more = k0 + kKeys < end;
-    if (more) {
-      sk.load(kb + (int64_t)(k0 + kKeys) * a.k_row, a.k_row, d.kl - k0 - kKeys, a.dim);
-      sv.load(vb + (int64_t)(k0 + kKeys) * a.v_row, a.v_row, d.kl - k0 - kKeys, a.dim);
-    }
-    if (k0 < wave_hi) {
-      f32x16 s[2];
-      two_products<T, DT>(mem, buf, buf + kTile / 2, at, qf, qf, s[0], s[1]);
-      AddCols<T, DT, 2> add(mem, buf + kTile, at);
+    if (k0 + kKeys < end) copy(k0 + kKeys, buf ^ (2 * kTile));
+    if (k0 >= wave_hi) continue;
+    f32x16 s[2];
+    two_products<T, DT>(mem, buf, buf + kTile / 2, at, qf, qf, s[0], s[1]);
+    AddCols<T, DT, 2> add(mem, buf + kTile, at);
 #pragma unroll
-      for (int rt = 0; rt < 2; ++rt)
-        make_scores<kMode>(s[rt], sc, slope, col.pos - k0 - rt * 32);
-      softmax_step<DT, 2>(s, mul, k0 + kKeys > wave_lo, k0, col.lim, m, l, o);
-      add.run(s, o);
-    }
-    if (more) {
-      sk.store(mem, buf ^ (2 * kTile));
-      sv.store(mem, (buf ^ (2 * kTile)) + kTile);
-    }
+    for (int rt = 0; rt < 2; ++rt)
+      make_scores<kMode>(s[rt], sc, slope, col.pos - k0 - rt * 32);
+    softmax_step<DT, 2>(s, mul, k0 + kKeys > wave_lo, k0, col.lim, m, l, o);
+    add.run(s, o);
   }
   const float sum = both_sum(l);
   if (!col.ok) return;
@@ -891,28 +906,21 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   const int wave_hi = min(__builtin_amdgcn_readlane(col.lim, 31), end);
   const uint16_t* kb = a.k + (int64_t)d.ks * a.k_row + (int64_t)hk * a.k_head;
   const uint16_t* vb = a.v + (int64_t)d.ks * a.v_row + (int64_t)hk * a.v_head;
-  Staged<DT, kKeys> sk, sv;
   int buf = 0;
-  // the staged key tiles [0, last) in turn, each with its products' first key
+  auto copy = [&](int k0, int to) {
+    copy_tile<DT, kKeys>(mem, to, kb + (int64_t)k0 * a.k_row, a.k_row, d.kl - k0, a.dim);
+    copy_tile<DT, kKeys>(mem, to + kTile, vb + (int64_t)k0 * a.v_row, a.v_row, d.kl - k0, a.dim);
+  };
+  // the key tiles [0, last) in turn, each copied while the one before is used
   auto walk = [&](int last, auto use) {
     if (last <= 0) return;
     __syncthreads();
-    sk.load(kb, a.k_row, d.kl, a.dim);
-    sv.load(vb, a.v_row, d.kl, a.dim);
-    sk.store(mem, buf);
-    sv.store(mem, buf + kTile);
+    copy(0, buf);
     for (int k0 = 0; k0 < last; k0 += kKeys, buf ^= 2 * kTile) {
+      arrived();
       __syncthreads();
-      const bool more = k0 + kKeys < last;
-      if (more) {
-        sk.load(kb + (int64_t)(k0 + kKeys) * a.k_row, a.k_row, d.kl - k0 - kKeys, a.dim);
-        sv.load(vb + (int64_t)(k0 + kKeys) * a.v_row, a.v_row, d.kl - k0 - kKeys, a.dim);
-      }
+      if (k0 + kKeys < last) copy(k0 + kKeys, buf ^ (2 * kTile));
       if (k0 < wave_hi) use(k0);
-      if (more) {
-        sk.store(mem, buf ^ (2 * kTile));
-        sv.store(mem, (buf ^ (2 * kTile)) + kTile);
-      }
     }
   };
   const bool biased = (kMode & kGeneral) && a.slopes;
@@ -997,10 +1005,9 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
   f32x16 gk[DT / 32], gv[DT / 32];
   load_cols<T, DT>(a.k + row * a.k_row + (int64_t)hk * a.k_head, ok, a.dim, kf);
   if constexpr (kValuesInLds) {
-    Staged<DT, kCols> sv;
-    sv.load(a.v + (int64_t)(d.ks + key0) * a.v_row + (int64_t)hk * a.v_head, a.v_row, d.kl - key0,
-            a.dim);
-    sv.store(mem, 4 * kTile);
+    copy_tile<DT, kCols>(mem, 4 * kTile,
+                         a.v + (int64_t)(d.ks + key0) * a.v_row + (int64_t)hk * a.v_head, a.v_row,
+                         d.kl - key0, a.dim);
   } else {
     load_cols<T, DT>(a.v + row * a.v_row + (int64_t)hk * a.v_head, ok, a.dim, vf);
   }
@@ -1012,13 +1019,16 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
   int first = 0;
   if (a.causal && key0 >= d.prefix) first = min(max(key0 - shift, 0), d.ql) / kRows * kRows;
   const int tiles = (d.ql - first + kRows - 1) / kRows;
-  Staged<DT, kRows> sq, sd;
   float r_lse = 0.0f, r_delta = 0.0f;
-  // tokens t0 .. t0 + 31 of head head0 + h
-  auto fetch = [&](int h, int t0) {
+  // tokens t0 .. t0 + 31 of head head0 + h on their way into a buffer
+  auto fetch = [&](int h, int t0, int buf) {
     const int64_t r = d.qs + t0;
-    sq.load(a.q + r * a.q_row + (int64_t)(head0 + h) * a.q_head, a.q_row, d.ql - t0, a.dim);
-    sd.load(a.d + r * a.d_row + (int64_t)(head0 + h) * a.d_head, a.d_row, d.ql - t0, a.dim);
+    copy_tile<DT, kRows>(mem, buf * 2 * kTile,
+                         a.q + r * a.q_row + (int64_t)(head0 + h) * a.q_head, a.q_row, d.ql - t0,
+                         a.dim);
+    copy_tile<DT, kRows>(mem, buf * 2 * kTile + kTile,
+                         a.d + r * a.d_row + (int64_t)(head0 + h) * a.d_head, a.d_row, d.ql - t0,
+                         a.dim);
     if (threadIdx.x < kRows) {
       const int t = t0 + (int)threadIdx.x;
       r_lse = INFINITY;
@@ -1031,24 +1041,23 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
     }
   };
   auto put = [&](int buf) {
-    sq.store(mem, buf * 2 * kTile);
-    sd.store(mem, buf * 2 * kTile + kTile);
     if (threadIdx.x < kRows) {
       s_lse[buf][threadIdx.x] = r_lse;
       s_delta[buf][threadIdx.x] = r_delta;
     }
   };
   if (tiles > 0) {
-    fetch(0, first);
+    fetch(0, first, 0);
     put(0);
   }
   int buf = 0;
   for (int h = 0; h < nheads; ++h) {
     const float slope = (kMode & kGeneral) && a.slopes ? a.slopes[head0 + h] * kLog2e : 0.0f;
     for (int t0 = first; t0 < d.ql; t0 += kRows, buf ^= 1) {
+      arrived();
       __syncthreads();
       const bool wrap = t0 + kRows >= d.ql, more = !wrap || h + 1 < nheads;
-      if (more) fetch(wrap ? h + 1 : h, wrap ? first : t0 + kRows);
+      if (more) fetch(wrap ? h + 1 : h, wrap ? first : t0 + kRows, buf ^ 1);
       // limits of the tile's rows grow with the token
       if (wkey < key_limit(a, d, t0 + kRows - 1)) {
         const int tile = buf * 2 * kTile;
@@ -1323,39 +1332,36 @@ __global__ __launch_bounds__(256, DT == 128 ? 1 : 2) void attention_dkv_few_kern
   }
 }
 
-// Sums of a key head's dk and dv over its query heads, in order: 64 keys a
+// Sums of a key head's dk and dv over its query heads, in order: 16 keys a
 // workgroup, 16 lanes a key, 8 elements a lane.
 template <typename T>
 __global__ __launch_bounds__(256) void attention_heads_kernel(AttnArgs a) {
   const int hk = blockIdx.x % a.heads_k;
   uint32_t local, units;
   Doc d;
-  if (find_document<true>(a.docs, 1, 64, blockIdx.x / a.heads_k, &local, &units, &d) < 0) return;
-  const int e = (threadIdx.x & 15) * 8;
-  if (e >= a.dim) return;
-  for (int i = 0; i < 4; ++i) {
-    const int key = (int)local * 64 + i * 16 + (threadIdx.x >> 4);
-    if (key >= d.kl) return;
-    const int64_t row = d.ks + key;
-    float x[8], y[8];
+  if (find_document<true>(a.docs, 1, 16, blockIdx.x / a.heads_k, &local, &units, &d) < 0) return;
+  const int e = (threadIdx.x & 15) * 8, key = (int)local * 16 + (threadIdx.x >> 4);
+  if (e >= a.dim || key >= d.kl) return;
+  const int64_t row = d.ks + key;
+  float x[8], y[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
-    const float* p = a.part_o + (row * a.heads_q + (int64_t)hk * a.group) * 2 * a.dim + e;
-    for (int h = 0; h < a.group; ++h, p += 2 * a.dim) {
-      float u[8], w[8];
-      load_elems(p, u);
-      load_elems(p + a.dim, w);
+  for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.0f;
+  const float* p = a.part_o + (row * a.heads_q + (int64_t)hk * a.group) * 2 * a.dim + e;
+#pragma unroll 4
+  for (int h = 0; h < a.group; ++h) {
+    float u[8], w[8];
+    load_elems(p + (int64_t)h * 2 * a.dim, u);
+    load_elems(p + ((int64_t)h * 2 + 1) * a.dim, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] += u[j];
-        y[j] += w[j];
-      }
+    for (int j = 0; j < 8; ++j) {
+      x[j] += u[j];
+      y[j] += w[j];
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] *= a.scale;
-    store_elems((T*)(a.out0 + row * a.out0_row + (int64_t)hk * a.out0_head + e), x);
-    store_elems((T*)(a.out1 + row * a.out1_row + (int64_t)hk * a.out1_head + e), y);
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] *= a.scale;
+  store_elems((T*)(a.out0 + row * a.out0_row + (int64_t)hk * a.out0_head + e), x);
+  store_elems((T*)(a.out1 + row * a.out1_row + (int64_t)hk * a.out1_head + e), y);
 }
 
 }  // namespace gs
@@ -1394,6 +1400,17 @@ int64_t unit_bound(int64_t columns, int64_t step, int32_t count) {
   return columns / step + count;
 }
 
+// Whether `blocks` workgroups of the 128-column form are too few: with less
+// than one a compute unit, its time is its longest document's, which the
+// few-column form divides by four at half the throughput.  Under a distance
+// bias dq walks the keys twice and the turning point is later.  Measured, us,
+// 128-column form : few-column form (forward; dq), heads of 64:
+//   74 workgroups  7.4 : 6.5;  8.8 : 8.3      262  16.6 : 19.7;  17.7 : 26.0
+//   262 with a bias and uneven documents      32.4 : 26.2;  78 : 51
+bool few_columns(const gs_attention_config& cfg, int64_t blocks) {
+  return blocks < (cfg.slopes ? 512 : 256);
+}
+
 // The few-column form, and how many pieces it cuts a document's keys into.
 struct Split {
   bool few, col_units;
@@ -1401,11 +1418,6 @@ struct Split {
   int64_t units;  // column tiles of a key head
   int cols;       // columns of a tile that a document may have
 };
-// Workgroups of the 128-column form below which the few-column form is taken.
-int64_t few_blocks() {
-  const char* e = getenv("GS_FEW");
-  return e ? atoi(e) : 1024;
-}
 Split split_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q,
                int64_t rows_k) {
   Split o = {};
@@ -1416,7 +1428,8 @@ Split split_of(const gs_attention_config& cfg, const gs_documents& d, int64_t ro
   o.col_units = longest_q * group > 32;
   o.units = o.col_units ? unit_bound(rows_q * group, 32, d.count) : d.count;
   o.cols = o.col_units ? 32 : (int)(longest_q * group);
-  o.few = !o.col_units || unit_bound(rows_q * group, kCols, d.count) * cfg.heads_k < few_blocks();
+  o.few = !o.col_units ||
+          few_columns(cfg, unit_bound(rows_q * group, kCols, d.count) * cfg.heads_k);
   const int64_t base = o.units * cfg.heads_k;
   // two rounds of the three workgroups a compute unit holds: fewer leave it
   // waiting for the longest, more pay a workgroup's start and end too often
@@ -1436,9 +1449,10 @@ Split split_of(const gs_attention_config& cfg, const gs_documents& d, int64_t ro
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The few-key form of dk and dv: few workgroups of the 128-key form even with
-// one to a query head.
+// one to a query head (64 workgroups of 128-element heads: 93 : 52 us; 304 under
+// a bias, uneven documents, heads of 64: 63 : 42; 296 without: 32.6 : 31.1).
 bool few_keys(int64_t rows_k, int32_t count, int32_t heads_q) {
-  return unit_bound(rows_k, kCols, count) * heads_q < few_blocks();
+  return unit_bound(rows_k, kCols, count) * heads_q < 384;
 }
 
 // Whether dk and dv are summed per query head first: too few workgroups
@@ -1462,20 +1476,20 @@ struct Run {
       attention_join_kernel<T><<<dim3((uint32_t)(tiles * p.cols)), dim3(256), 0, s>>>(a, p.cols);
       return hipGetLastError();
     }
-    const int64_t units = unit_bound((int64_t)a.docs.rows_q * a.group, kCols, a.docs.count);
-    attention_fwd_kernel<T, DT, kMode>
-        <<<dim3((uint32_t)(units * a.heads_k)), dim3(256), 0, s>>>(a);
+    const int64_t columns = (int64_t)a.docs.rows_q * a.group;
+    const int64_t blocks = unit_bound(columns, kCols, a.docs.count) * a.heads_k;
+    attention_fwd_kernel<T, DT, kMode><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(a);
     return hipGetLastError();
   }
 
-  static hipError_t bwd(AttnArgs a, const gs_heads& dq, const gs_heads& dk, const gs_heads& dv,
+  static hipError_t bwd(AttnArgs a, const gs_attention_config& cfg, const gs_heads& dq, const gs_heads& dk, const gs_heads& dv,
                         hipStream_t s) {
     const dim3 block(256);
     if (a.docs.rows_q > 0) {
       a.out0 = (uint16_t*)dq.data; a.out0_row = dq.row; a.out0_head = dq.head;
       const int64_t columns = (int64_t)a.docs.rows_q * a.group;
       const int64_t blocks = unit_bound(columns, kCols, a.docs.count) * a.heads_k;
-      if (blocks < few_blocks()) {
+      if (few_columns(cfg, blocks)) {
         const int64_t few = unit_bound(columns, 32, a.docs.count) * a.heads_k;
         attention_dq_few_kernel<T, DT, kMode><<<dim3((uint32_t)few), block, 0, s>>>(a);
       } else {
@@ -1497,7 +1511,7 @@ struct Run {
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.parts) return e;
-    const int64_t sums = unit_bound(a.docs.rows_k, 64, a.docs.count) * a.heads_k;
+    const int64_t sums = unit_bound(a.docs.rows_k, 16, a.docs.count) * a.heads_k;
     attention_heads_kernel<T><<<dim3((uint32_t)sums), block, 0, s>>>(a);
     return hipGetLastError();
   }
@@ -1571,7 +1585,7 @@ hipError_t gs_launch_attention_bwd(const gs_attention_config& cfg, const gs_docu
   a.delta = (float*)workspace;
   a.part_o = (float*)((char*)workspace + align256((size_t)rows_q * cfg.heads_q * sizeof(float)));
   a.parts = head_parts(cfg, d, rows_k);
-  return dispatch(cfg, a, [&](auto run) { return run.bwd(a, dq, dk, dv, s); });
+  return dispatch(cfg, a, [&](auto run) { return run.bwd(a, cfg, dq, dk, dv, s); });
 }
 
 }  // extern "C"
