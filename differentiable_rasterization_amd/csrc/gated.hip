@@ -164,21 +164,22 @@ __global__ __launch_bounds__(256) void gated_maps_bwd_kernel(GatedArgs a) {
 }
 
 // 2. The state every chunk of a document starts from (backward: the message
-// it receives, chunks from the last).  16 channels a workgroup, 16 lanes a
+// it receives, chunks from the last).  16 channels a workgroup, S lanes a
 // channel: each composes its share of the chunks, the shares are applied in
 // order, and each lane walks its share again.
-template <bool kBack>
-__global__ __launch_bounds__(256) void gated_carry_kernel(GatedArgs a) {
-  __shared__ float s_a[16][17], s_h[16][17];
+template <bool kBack, int S>
+__global__ __launch_bounds__(16 * S) void gated_carry_kernel(GatedArgs a) {
+  __shared__ float s_a[S][17], s_h[S][17];
   const int per = (a.channels + 15) / 16;
   const int doc = blockIdx.x / per;
-  const int ch = (blockIdx.x % per) * 16 + (threadIdx.x & 15), seg = threadIdx.x >> 4;
+  const int c = threadIdx.x & 15, seg = threadIdx.x >> 4;
+  const int ch = (blockIdx.x % per) * 16 + c;
   const uint32_t base = units_before(a.docs.q_start, a.docs.q_len, a.docs.rows_q, doc, kChunk);
   const int len = clamp_len(a.docs.q_start[doc], a.docs.q_len[doc], a.docs.rows_q);
   const int n = (len + kChunk - 1) / kChunk;
   if (base + n > a.chunks) return;  // documents that share rows: no room for their maps
   const bool on = ch < a.channels;
-  const int lo = (int)((int64_t)n * seg / 16), hi = (int)((int64_t)n * (seg + 1) / 16);
+  const int lo = (int)((int64_t)n * seg / S), hi = (int)((int64_t)n * (seg + 1) / S);
   float h = on && a.state_in ? a.state_in[(int64_t)doc * a.channels + ch] : 0.0f;
   float A = 1.0f, H = 0.0f;
   if (on) {
@@ -190,12 +191,12 @@ __global__ __launch_bounds__(256) void gated_carry_kernel(GatedArgs a) {
       A *= m;
     }
   }
-  s_a[seg][threadIdx.x & 15] = A;
-  s_h[seg][threadIdx.x & 15] = H;
+  s_a[seg][c] = A;
+  s_h[seg][c] = H;
   __syncthreads();
   if (!on) return;
-  for (int i = 0; i < seg; ++i)
-    h = fmaf(s_a[i][threadIdx.x & 15], h, s_h[i][threadIdx.x & 15]);
+#pragma unroll 8
+  for (int i = 0; i < seg; ++i) h = fmaf(s_a[i][c], h, s_h[i][c]);
 #pragma unroll 4
   for (int i = lo; i < hi; ++i) {
     const int64_t o = (int64_t)(base + (kBack ? n - 1 - i : i)) * a.channels + ch;
@@ -203,7 +204,7 @@ __global__ __launch_bounds__(256) void gated_carry_kernel(GatedArgs a) {
     a.carry[o] = h;
     h = fmaf(m, h, H);
   }
-  if (seg == 15 && a.state_out) a.state_out[(int64_t)doc * a.channels + ch] = h;
+  if (seg == S - 1 && a.state_out) a.state_out[(int64_t)doc * a.channels + ch] = h;
 }
 
 // The whole document of this wavefront, for the one-launch form.
@@ -377,8 +378,16 @@ dim3 grid_of(const GatedArgs& a, bool direct) {
   return dim3((uint32_t)((waves + 3) / 4));
 }
 
-dim3 carry_grid(const GatedArgs& a) {
-  return dim3((uint32_t)((int64_t)((a.channels + 15) / 16) * a.docs.count));
+// Long documents (a thousand chunks: 27 us with 16 lanes a channel) are shared
+// among 64 lanes.
+template <bool kBack>
+hipError_t run_carry(const GatedArgs& a, hipStream_t s) {
+  const dim3 grid((uint32_t)((int64_t)((a.channels + 15) / 16) * a.docs.count));
+  if (a.chunks / a.docs.count > 128)
+    gated_carry_kernel<kBack, 64><<<grid, dim3(1024), 0, s>>>(a);
+  else
+    gated_carry_kernel<kBack, 16><<<grid, dim3(256), 0, s>>>(a);
+  return hipGetLastError();
 }
 
 template <typename T, int V>
@@ -391,8 +400,7 @@ hipError_t run_fwd(const GatedArgs& a, bool direct, hipStream_t s) {
   gated_maps_kernel<T, V><<<grid_of(a, false), block, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  gated_carry_kernel<false><<<carry_grid(a), block, 0, s>>>(a);
-  e = hipGetLastError();
+  e = run_carry<false>(a, s);
   if (e != hipSuccess) return e;
   gated_run_kernel<T, V, false><<<grid_of(a, false), block, 0, s>>>(a);
   return hipGetLastError();
@@ -408,8 +416,7 @@ hipError_t run_bwd(const GatedArgs& a, bool direct, hipStream_t s) {
   gated_maps_bwd_kernel<T, V><<<grid_of(a, false), block, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  gated_carry_kernel<true><<<carry_grid(a), block, 0, s>>>(a);
-  e = hipGetLastError();
+  e = run_carry<true>(a, s);
   if (e != hipSuccess) return e;
   gated_run_bwd_kernel<T, V, false><<<grid_of(a, false), block, 0, s>>>(a);
   return hipGetLastError();
