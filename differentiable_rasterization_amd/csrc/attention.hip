@@ -207,7 +207,7 @@ __device__ inline void copy_tile(const char* mem, int tile, const uint16_t* base
   const int r = threadIdx.x / kChunks;
   // place() moves chunk c of row r by an exclusive or, its own inverse
   const int c = (place<DT>(r, threadIdx.x % kChunks) - r * DT) / 8;
-  int at = c * 8 < dim ? r * stride + c * 16 : (int)0x80000000;
+  uint32_t at = c * 8 < dim ? (uint32_t)(r * stride + c * 16) : 0x80000000u;
   const uint32_t lds =
       __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(
                                          __attribute__((address_space(3))) const char*)mem +
@@ -217,8 +217,8 @@ __device__ inline void copy_tile(const char* mem, int tile, const uint16_t* base
     asm volatile(
         "s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(at),
         "s"(rsrc), "s"(lds + i * 4096)
-        : "memory");
-    at = c * 8 < dim ? at + kStep * stride : at;
+        : "memory", "m0");
+    at = c * 8 < dim ? at + (uint32_t)(kStep * stride) : at;
   }
 }
 __device__ inline void arrived() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
@@ -691,11 +691,11 @@ __global__ __launch_bounds__(256, DT == 128 ? 2 : 3) void attention_step_kernel(
           const_cast<uint16_t*>(vb + (int64_t)k0 * a.v_row), 0,
           (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff), 0x00027000);
       const int r = lane / kChunks, c = lane % kChunks;
-      int at = c * 8 < a.dim ? r * stride + c * 16 : (int)0x80000000;
+      uint32_t at = c * 8 < a.dim ? (uint32_t)(r * stride + c * 16) : 0x80000000u;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        vw[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0);
-        at = c * 8 < a.dim ? at + 64 / kChunks * stride : at;
+        vw[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)at, 0, 0);
+        at = c * 8 < a.dim ? at + (uint32_t)(64 / kChunks * stride) : at;
       }
     };
     int k0 = key_lo + wave * 32;
@@ -1086,6 +1086,7 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
       if (more) put(buf ^ 1);
     }
   }
+  arrived();  // the values, where no token sees these keys
   if (!ok) return;
   if (a.parts) {
     // [key row][query head][dk, dv][dim]

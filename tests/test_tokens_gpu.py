@@ -252,6 +252,10 @@ def _run_attention(case, dtype, layout, seed=0, gap=3, bounds=True, stream=None)
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("case", ATTENTION, ids=range(len(ATTENTION)))
 def test_attention(case, dtype, layout):
+    _check_attention(case, dtype, layout)
+
+
+def _check_attention(case, dtype, layout):
     r = _run_attention(case, dtype, layout, bounds=layout != "heads")
     lq, lk, hq, hk, dim, opt = case
     klen = lq if lk is None else lk
@@ -275,6 +279,98 @@ def test_attention(case, dtype, layout):
     for n, at in (("o", inside), ("dq", inside), ("dk", kin), ("dv", kin)):
         assert (r[n][~at] == 7.0).all(), n
     assert (r["lse"][:, ~inside] == 7.0).all()
+
+
+# many heads: enough workgroups for the forms with 128 columns or keys each
+MANY = [
+    ([130, 65, 257, 1], None, 128, 64, 64, dict(causal=True)),
+    ([130, 65, 257, 1], None, 64, 64, 128, dict(causal=True)),
+    ([200, 64, 100], None, 128, 32, 128, dict(causal=True, softcap=8.0, prefix=[30, 64, 0])),
+    ([200, 64, 100], None, 128, 128, 40, dict(causal=True, slopes=True)),
+    ([150, 200], [400, 70], 128, 64, 96, dict(causal=True, slopes=True, softcap=15.0)),
+    ([150, 200, 9], [400, 70, 0], 128, 64, 128, dict(causal=False)),
+    ([3] * 150 + [0, 1, 65], None, 4, 2, 32, dict(causal=True)),
+]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("case", MANY, ids=range(len(MANY)))
+def test_attention_many_heads_or_documents(case, dtype):
+    _check_attention(case, dtype, "fused")
+
+
+def _captured(run, outputs):
+    """Replays of a captured call against its eager results, with the
+    program's own work in between."""
+    run()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outputs]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        for t in outputs:
+            t.fill_(3.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, w in zip(outputs, want):
+            assert torch.equal(t, w)
+
+
+def test_token_calls_can_be_captured():
+    gen = _gen(21)
+    n, hq, hk, dim, dtype = 300, 8, 2, 64, torch.bfloat16
+    q, k, v, do = (_normal(gen, dtype, n, h, dim) for h in (hq, hk, hk, hq))
+    o, dq, dk, dv = (torch.empty_like(t) for t in (q, q, k, v))
+    lse = torch.empty((hq, n), device="cuda")
+    cfg = raster.attention_config(dtype, hq, hk, dim, 0.125, True)
+    docs = raster.documents(_ints([0, 100]), _ints([100, 200]))
+    nb = max(raster.gs_attention_fwd_workspace_size(cfg, docs, n, n),
+             raster.gs_attention_bwd_workspace_size(cfg, docs, n, n))
+    ws = _space(nb)
+
+    def attention():
+        raster.gs_attention_fwd(cfg, docs, n, n, q, k, v, o, lse, ws, nb)
+        raster.gs_attention_bwd(cfg, docs, n, n, q, k, v, o, lse, do, dq, dk, dv, ws, nb)
+    _captured(attention, (o, lse, dq, dk, dv))
+
+    # one token over long caches: split over the keys and joined
+    one = raster.documents(_ints([0, 1]), _ints([1, 1]), _ints([0, 4096]), _ints([4000, 1500]),
+                           max_q_len=1, max_k_len=4000)
+    ck, cv = (_normal(gen, dtype, 8192, hk, dim) for _ in range(2))
+    oo = torch.empty_like(q[:2])
+    ns = raster.gs_attention_fwd_workspace_size(cfg, one, 2, 8192)
+    assert ns > 0
+    wss = _space(ns)
+    _captured(lambda: raster.gs_attention_fwd(cfg, one, 2, 8192, q[:2], ck, cv, oo, None, wss, ns),
+              (oo,))
+
+    ch = 64
+    gate, x, dy = (_normal(gen, dtype, n, ch) for _ in range(3))
+    y, df, dx = (torch.empty_like(x) for _ in range(3))
+    end, ds = torch.zeros((2, ch), device="cuda"), torch.zeros((2, ch), device="cuda")
+    scan = raster.scan_config(dtype, ch)
+    saved = _space(raster.gs_gated_scan_saved_size(scan, docs, n))
+    nc = raster.gs_gated_scan_fwd_workspace_size(scan, docs, n)
+    wsc = _space(nc)
+
+    def gated():
+        raster.gs_gated_scan_fwd(scan, docs, n, gate, x, None, y, end, saved, wsc, nc)
+        raster.gs_gated_scan_bwd(scan, docs, n, gate, x, saved, dy, None, df, dx, ds, wsc, nc)
+    _captured(gated, (y, end, df, dx, ds))
+
+    qk = raster.qk_config(dtype, hq, hk, dim)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    freq, w = torch.rand(32, generator=gen, device="cuda"), torch.ones(dim, device="cuda")
+    dwq, dwk = torch.empty_like(w), torch.empty_like(w)
+    nq = raster.gs_qk_norm_rope_bwd_workspace_size(qk, n)
+    wsq = _space(nq)
+
+    def turned():
+        raster.gs_qk_norm_rope_fwd(qk, n, pos, freq, w, w, q, k, dq, dk)
+        raster.gs_qk_norm_rope_bwd(qk, n, pos, freq, w, w, q, k, do, v, o, dv, dwq, dwk, wsq, nq)
+    _captured(turned, (dq, dk, o, dv, dwq, dwk))
 
 
 @pytest.mark.parametrize("case", [ATTENTION[3], ATTENTION[9], ATTENTION[11], ATTENTION[16]])
