@@ -44,7 +44,9 @@ struct AttnArgs {
   float* lse;    // [heads_q][rows_q]
   float* delta;  // [heads_q][rows_q]
   int parts;          // dk, dv: sums per query head
-  int pieces, piece;  // one-token form: pieces of a document's keys, keys of one
+  int pieces, piece;  // few-column form: pieces of a document's keys, keys of one
+  int tiles;          // few-column form: column tiles of a key head in the grid
+  int pieces_last;    // few-column form: the order of the grid
   int col_units;      // few-column form: column tiles are units of the grid
   float* part_ml;     // [pieces][heads_q][rows_q][2]
   float* part_o;      // [pieces][heads_q][rows_q][dim]
@@ -625,8 +627,17 @@ __device__ inline StepItem step_item(const AttnArgs& a, int u) {
   StepItem o;
   o.hk = u % a.heads_k;
   u /= a.heads_k;
-  o.piece = u % a.pieces;
-  u /= a.pieces;
+  // With many documents, all first pieces before all second ones: documents
+  // have different numbers of them, and workgroups are dealt to the compute
+  // units in turn, so that with four pieces a document every fourth unit would
+  // get all the fourth ones.  With few, a document's pieces in a row.
+  if (a.pieces_last) {
+    o.piece = u / a.tiles;
+    u %= a.tiles;
+  } else {
+    o.piece = u % a.pieces;
+    u /= a.pieces;
+  }
   o.col0 = 0;
   o.none = false;
   if (a.col_units) {
@@ -782,7 +793,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int til
   int u = blockIdx.x / tile_cols;
   const int hk = u % a.heads_k;
   u /= a.heads_k;
-  const StepItem it = step_item(a, u * a.pieces * a.heads_k);
+  const StepItem it = step_item(a, (a.pieces_last ? u : u * a.pieces) * a.heads_k);
   if (it.none) return;
   const Doc& d = it.d;
   const int pieces = pieces_of(a, d);
@@ -1414,7 +1425,7 @@ bool few_columns(const gs_attention_config& cfg, int64_t blocks) {
 
 // The few-column form, and how many pieces it cuts a document's keys into.
 struct Split {
-  bool few, col_units;
+  bool few, col_units, pieces_last;
   int pieces, piece;
   int64_t units;  // column tiles of a key head
   int cols;       // columns of a tile that a document may have
@@ -1432,11 +1443,14 @@ Split split_of(const gs_attention_config& cfg, const gs_documents& d, int64_t ro
   o.few = !o.col_units ||
           few_columns(cfg, unit_bound(rows_q * group, kCols, d.count) * cfg.heads_k);
   const int64_t base = o.units * cfg.heads_k;
-  // two rounds of the three workgroups a compute unit holds: fewer leave it
-  // waiting for the longest, more pay a workgroup's start and end too often
-  // (64 caches of 100,003 keys in all: 59, 54, 44, 67 us at 512, 768, 1536,
-  // 2048 wanted)
-  const int64_t want = ((o.col_units ? 512 : 1536) + base - 1) / base;
+  // Workgroups wanted: with few documents a round of what the chip holds (four
+  // caches of 120,001 keys in all, us: 77, 63, 78, 70, 72 at 512, 768, 1024,
+  // 1536, 2048); with many of uneven length more, so that the long ones end
+  // sooner (64 caches of 100,003: 87, 85, 75, 78, 72 at 512, 768, 1536, 2048,
+  // 3072).  Column tiles that are looked up are many already.
+  o.pieces_last = base >= 256;
+  const int64_t target = o.col_units ? 512 : o.pieces_last ? 3072 : 768;
+  const int64_t want = (target + base - 1) / base;
   int64_t piece = (longest_k + want - 1) / want;
   piece = (piece + kPieceKeys - 1) / kPieceKeys * kPieceKeys;
   const int64_t least = o.col_units ? 8 * kPieceKeys : 2 * kPieceKeys;
@@ -1567,6 +1581,8 @@ hipError_t gs_launch_attention_fwd(const gs_attention_config& cfg, const gs_docu
   a.pieces = p.pieces;
   a.piece = p.piece;
   a.col_units = p.col_units;
+  a.tiles = (int)p.units;
+  a.pieces_last = p.pieces_last;
   a.part_ml = (float*)workspace;
   a.part_o = (float*)((char*)workspace +
                       align256((size_t)p.pieces * cfg.heads_q * rows_q * 2 * sizeof(float)));
