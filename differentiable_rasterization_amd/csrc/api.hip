@@ -1138,7 +1138,8 @@ gs_status check_workspace(const void* workspace, size_t bytes, size_t need) {
 }
 
 gs_status check_token_rows(int64_t rows, int64_t heads) {
-  GS_REQUIRE(rows >= 0 && rows < (int64_t)1 << 31, "rows must be in [0, 2^31)");
+  // kernels step past the last row by up to a few tiles, in 32 bits
+  GS_REQUIRE(rows >= 0 && rows < ((int64_t)1 << 31) - 4096, "rows must be in [0, 2^31 - 4096)");
   GS_REQUIRE(rows * heads < (int64_t)1 << 31, "rows times heads must be < 2^31");
   return GS_OK;
 }

@@ -650,7 +650,7 @@ __device__ inline StepItem step_item(const AttnArgs& a, int u) {
   return o;
 }
 __device__ inline int pieces_of(const AttnArgs& a, const Doc& d) {
-  return max(1, min(a.pieces, (d.kl + a.piece - 1) / a.piece));
+  return max(1, min(a.pieces, (int)(((uint32_t)d.kl + a.piece - 1) / (uint32_t)a.piece)));
 }
 
 template <typename T, int DT, int kMode>
@@ -1455,6 +1455,7 @@ Split split_of(const gs_attention_config& cfg, const gs_documents& d, int64_t ro
   piece = (piece + kPieceKeys - 1) / kPieceKeys * kPieceKeys;
   const int64_t least = o.col_units ? 8 * kPieceKeys : 2 * kPieceKeys;
   if (piece < least) piece = least;
+  if (piece > (1 << 30)) piece = 1 << 30;
   o.piece = (int)piece;
   o.pieces = (int)((longest_k + piece - 1) / piece);
   if (o.pieces < 1) o.pieces = 1;

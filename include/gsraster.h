@@ -644,7 +644,8 @@ GS_API gs_status gs_densify_prune(int64_t N, int64_t ld, int32_t sh_degree, cons
  *     projection.  data is 16-byte aligned, strides are multiples of 8
  *     elements in [0, 2^28].  Outputs must not overlap: each row of an output
  *     is its own.
- *   - rows < 2^31, and rows times heads < 2^31.  Zero rows or documents are
+ *   - rows < 2^31 - 4096, rows times heads < 2^31, and in attention documents
+ *     times heads <= 2^26.  Zero rows or documents are
  *     valid and launch nothing; pointers may then be NULL.
  *   - Results are reproducible bit for bit: there are no atomics. */
 typedef enum { GS_F32 = 0, GS_BF16 = 1, GS_F16 = 2 } gs_dtype;
