@@ -10,15 +10,20 @@
 // A step costs a dozen operations on six to twelve bytes, so the operator is
 // bound by memory traffic; what stands in the way is that the steps depend on
 // each other.  The recurrence is a composition of maps h -> A h + H, which is
-// associative, so each document is cut into chunks of 64 steps:
-//   1. every chunk composes its own map (A, H), all chunks at once;
-//   2. per document and channel, the chunks' maps are applied in order to the
-//      document's state: the state each chunk starts from;
-//   3. every chunk runs its steps from that state and writes its outputs.
-// Documents of at most a chunk need only the third, in one launch.  The order
-// of every sum is fixed, so results are the same bits every time.
-// Lanes run over channels, a wavefront over the steps of one chunk; states are
-// fp32 throughout, and only the outputs are rounded, once.
+// associative, so each document is cut into chunks whose maps are formed at
+// the same time.
+//   Documents of at most 64 steps: a wavefront walks a document.
+//   Otherwise, one pass over the data: a workgroup keeps its chunk's inputs in
+//   registers, composes its map, publishes it, composes the maps of the chunks
+//   before it in its document as they appear, and runs its steps from the
+//   state that gives.  Every workgroup reads all earlier maps (a thousandth of
+//   the chunk each), so nobody waits for more than a map, and the maps are
+//   composed in one order whatever the timing.
+//   Documents of more chunks than that is worth: three passes (chunk maps;
+//   per channel, the state every chunk starts from; the steps).
+// The order of every sum is fixed, so results are the same bits every time.
+// Lanes run over channels, wavefronts over steps; states are fp32 throughout,
+// and only the outputs are rounded, once.
 //
 // The backward needs h_{t-1} in fp32: reading it from the rounded outputs
 // would put their rounding into the gate's gradient.  The forward therefore
@@ -341,6 +346,404 @@ __global__ __launch_bounds__(256) void gated_run_bwd_kernel(GatedArgs a) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// One pass
+// ---------------------------------------------------------------------------
+constexpr int kPassWaves = 8;
+// A published map is one 64-bit word a channel, (A, H), so that it needs no
+// flag beside it; all bits set is "not yet" (a NaN is stored as another NaN).
+constexpr uint64_t kNoMap = ~(uint64_t)0;
+
+__device__ inline uint64_t map_word(float a, float h) {
+  if (a != a) a = __builtin_nanf("");
+  if (h != h) h = __builtin_nanf("");
+  return (uint64_t)__builtin_bit_cast(uint32_t, a) << 32 | __builtin_bit_cast(uint32_t, h);
+}
+
+// Clears the maps and the ticket, and takes a copy of the states, since the
+// last chunk of a document may replace them (state_out may be state_in) before
+// the first has read them; hands an empty document's state through.
+__global__ __launch_bounds__(256) void gated_clear_kernel(GatedArgs a, uint64_t* maps,
+                                                          int64_t words, uint32_t* ticket,
+                                                          float* states_in) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t k = i; k < words; k += step) maps[k] = kNoMap;
+  if (i == 0) *ticket = 0;
+  const int64_t states = (int64_t)a.docs.count * a.channels;
+  for (int64_t k = i; k < states; k += step) {
+    const float h = a.state_in ? a.state_in[k] : 0.0f;
+    states_in[k] = h;
+    const int doc = (int)(k / a.channels);
+    if (a.state_out && clamp_len(a.docs.q_start[doc], a.docs.q_len[doc], a.docs.rows_q) == 0)
+      a.state_out[k] = h;
+  }
+}
+
+// A 32-bit word of a row: two 16-bit channels or one fp32.
+template <typename T>
+struct Pack {
+  static constexpr int V = 4 / sizeof(T);
+};
+template <typename T>
+__device__ inline void open_word(uint32_t w, float (&v)[Pack<T>::V]) {
+  if constexpr (__is_same(T, float)) v[0] = __builtin_bit_cast(float, w);
+  else unpack2<T>(w, v[0], v[1]);
+}
+template <typename T>
+__device__ inline uint32_t close_word(const float (&v)[Pack<T>::V]) {
+  if constexpr (__is_same(T, float)) return __builtin_bit_cast(uint32_t, v[0]);
+  else return pack2<T>(v[0], v[1]);
+}
+
+// The workgroup's chunk, by ticket: tickets are taken in the order workgroups
+// start, so every chunk that this one waits for has a workgroup that runs and
+// itself waits only for earlier ones.
+struct PassItem {
+  int doc;
+  uint32_t unit, local, units;
+  uint32_t chunk64;  // index of the document's first chunk of kChunk steps
+  Doc d;
+  int ch;
+  bool on;
+};
+template <int V, bool kBack>
+__device__ inline PassItem pass_item(const GatedArgs& a, uint32_t chunks, int chunk,
+                                     uint32_t* ticket) {
+  __shared__ uint32_t s_ticket;
+  if (threadIdx.x == 0) s_ticket = atomicAdd(ticket, 1u);
+  __syncthreads();
+  const uint32_t t = __builtin_amdgcn_readfirstlane(s_ticket);
+  PassItem it;
+  it.doc = -1;
+  const uint32_t u = t / (uint32_t)a.groups;
+  if (u >= chunks) return it;
+  it.unit = kBack ? chunks - 1 - u : u;
+  it.ch = ((int)(t % (uint32_t)a.groups) * 64 + (threadIdx.x & 63)) * V;
+  it.on = it.ch < a.channels;
+  it.doc = find_document<false>(a.docs, 1, (uint32_t)chunk, it.unit, &it.local, &it.units, &it.d,
+                                false);
+  // documents that share rows have more chunks than there is room for
+  if (it.doc >= 0 && it.unit - it.local + it.units > chunks) it.doc = -1;
+  it.chunk64 = it.doc < 0 || !a.saved ? 0
+                                      : units_before(a.docs.q_start, a.docs.q_len, a.docs.rows_q,
+                                                     it.doc, kChunk);
+  if (a.saved && it.chunk64 + (it.d.ql + kChunk - 1) / kChunk > a.chunks) it.doc = -1;
+  return it;
+}
+
+// Composes maps [from, from + step, ...) (n of them) of the lane's channels,
+// in that order, after the map (A, H) so far.  Waits are for workgroups that
+// are already running (microseconds); the bound, some seconds in all, only ends
+// a wait that cannot end, with results that are not numbers.
+template <int V>
+__device__ inline void compose_maps(const uint64_t* maps, int64_t from, int64_t step, int n,
+                                    float (&A)[V], float (&H)[V]) {
+  constexpr int kBatch = 8;
+  int spins = 1 << 20;
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    uint64_t w[kBatch][V];
+    while (true) {
+      bool all = true;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          w[i][v] = __hip_atomic_load(maps + from + (int64_t)min(i0 + i, n - 1) * step + v,
+                                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          all = all && w[i][v] != kNoMap;
+        }
+      }
+      if (__ballot(!all) == 0 || --spins <= 0) break;
+      __builtin_amdgcn_s_sleep(2);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (i0 + i < n) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float m = __builtin_bit_cast(float, (uint32_t)(w[i][v] >> 32));
+          H[v] = fmaf(m, H[v], __builtin_bit_cast(float, (uint32_t)w[i][v]));
+          A[v] *= m;
+        }
+      }
+    }
+  }
+}
+
+// Forward: STEPS steps of a wavefront's channels in registers, two words each.
+template <typename T, int STEPS>
+__global__ __launch_bounds__(64 * kPassWaves, 2) void gated_pass_kernel(GatedArgs a,
+                                                                        uint64_t* maps,
+                                                                        uint32_t chunks,
+                                                                        uint32_t* ticket) {
+  constexpr int V = Pack<T>::V, kLong = STEPS * kPassWaves;
+  constexpr bool kExact = __is_same(T, float);
+  __shared__ float s_a[kPassWaves][64 * V], s_h[kPassWaves][64 * V];
+  __shared__ float p_a[kPassWaves][64 * V], p_h[kPassWaves][64 * V];
+  const PassItem it = pass_item<V, false>(a, chunks, kLong, ticket);
+  if (it.doc < 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t0 = (int)it.local * kLong + wave * STEPS;
+  const int n = min(STEPS, it.d.ql - t0);
+  const int64_t row = (int64_t)it.d.qs + t0;
+  uint32_t f[STEPS], x[STEPS];
+  float A[V], H[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = 1.0f;
+    H[v] = 0.0f;
+  }
+  if (n > 0 && it.on) {
+    const T* pf = row_ptr<T>(a.gate, row, a.gate_row, it.ch);
+    const T* px = row_ptr<T>(a.x, row, a.x_row, it.ch);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      f[i] = *(const uint32_t*)(pf + min(i, n - 1) * a.gate_row);
+      x[i] = *(const uint32_t*)(px + min(i, n - 1) * a.x_row);
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      if (i < n) {
+        float fv[V], xv[V];
+        open_word<T>(f[i], fv);
+        open_word<T>(x[i], xv);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float g, z;
+          gate_of<kExact>(fv[v], g, z);
+          A[v] *= g;
+          H[v] = fmaf(g, H[v], a.coupled ? z * xv[v] : xv[v]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    s_a[wave][lane * V + v] = A[v];
+    s_h[wave][lane * V + v] = H[v];
+  }
+  __syncthreads();
+  const int64_t first = ((int64_t)it.unit - it.local) * a.channels + it.ch;
+  if (wave == 0 && it.on && it.local + 1 < it.units) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float ma = 1.0f, mh = 0.0f;
+      for (int w = 0; w < kPassWaves; ++w) {
+        mh = fmaf(s_a[w][lane * V + v], mh, s_h[w][lane * V + v]);
+        ma *= s_a[w][lane * V + v];
+      }
+      __hip_atomic_store(maps + first + (int64_t)it.local * a.channels + v, map_word(ma, mh),
+                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  // the chunks before this one, shared out among the wavefronts in order
+  const int lo = (int)it.local * wave / kPassWaves, hi = (int)it.local * (wave + 1) / kPassWaves;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = 1.0f;
+    H[v] = 0.0f;
+  }
+  if (it.on && hi > lo)
+    compose_maps<V>(maps, first + (int64_t)lo * a.channels, a.channels, hi - lo, A, H);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    p_a[wave][lane * V + v] = A[v];
+    p_h[wave][lane * V + v] = H[v];
+  }
+  __syncthreads();
+  if (n <= 0 || !it.on) return;
+  float h[V];
+  const int64_t so = (int64_t)it.doc * a.channels + it.ch;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    h[v] = a.state_in ? a.state_in[so + v] : 0.0f;
+    for (int w = 0; w < kPassWaves; ++w)
+      h[v] = fmaf(p_a[w][lane * V + v], h[v], p_h[w][lane * V + v]);
+    for (int w = 0; w < wave; ++w)
+      h[v] = fmaf(s_a[w][lane * V + v], h[v], s_h[w][lane * V + v]);
+  }
+  T* py = (T*)a.y + row * a.y_row + it.ch;
+  float* save = nullptr;
+  if (a.saved) {
+    const int64_t chunk = (int64_t)it.chunk64 + t0 / kChunk;
+    save = a.saved + (chunk * (kChunk / kSub) + t0 % kChunk / kSub) * a.channels + it.ch;
+  }
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i) {
+    if (i < n) {
+      if (i % kSub == 0 && save) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) save[(int64_t)(i / kSub) * a.channels + v] = h[v];
+      }
+      float fv[V], xv[V];
+      open_word<T>(f[i], fv);
+      open_word<T>(x[i], xv);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float g, z;
+        gate_of<kExact>(fv[v], g, z);
+        h[v] = fmaf(g, h[v], a.coupled ? z * xv[v] : xv[v]);
+      }
+      *(uint32_t*)(py + i * a.y_row) = close_word<T>(h);
+    }
+  }
+  if (a.state_out && t0 + n == it.d.ql) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.state_out[so + v] = h[v];
+  }
+}
+
+// Backward: the same from the other end, three words a step.
+template <typename T, int STEPS>
+__global__ __launch_bounds__(64 * kPassWaves, 2) void gated_pass_bwd_kernel(GatedArgs a,
+                                                                            uint64_t* maps,
+                                                                            uint32_t chunks,
+                                                                            uint32_t* ticket) {
+  constexpr int V = Pack<T>::V, kLong = STEPS * kPassWaves;
+  constexpr bool kExact = __is_same(T, float);
+  __shared__ float s_a[kPassWaves][64 * V], s_h[kPassWaves][64 * V];
+  __shared__ float p_a[kPassWaves][64 * V], p_h[kPassWaves][64 * V];
+  const PassItem it = pass_item<V, true>(a, chunks, kLong, ticket);
+  if (it.doc < 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t0 = (int)it.local * kLong + wave * STEPS;
+  const int n = min(STEPS, it.d.ql - t0);
+  const int64_t row = (int64_t)it.d.qs + t0;
+  uint32_t f[STEPS], x[STEPS], d[STEPS];
+  float A[V], E[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = 1.0f;
+    E[v] = 0.0f;
+  }
+  if (n > 0 && it.on) {
+    const T* pf = row_ptr<T>(a.gate, row, a.gate_row, it.ch);
+    const T* px = row_ptr<T>(a.x, row, a.x_row, it.ch);
+    const T* pd = row_ptr<T>(a.dy, row, a.dy_row, it.ch);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      f[i] = *(const uint32_t*)(pf + min(i, n - 1) * a.gate_row);
+      d[i] = *(const uint32_t*)(pd + min(i, n - 1) * a.dy_row);
+      x[i] = *(const uint32_t*)(px + min(i, n - 1) * a.x_row);
+    }
+#pragma unroll
+    for (int i = STEPS - 1; i >= 0; --i) {
+      if (i < n) {
+        float fv[V], dv[V];
+        open_word<T>(f[i], fv);
+        open_word<T>(d[i], dv);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float g, z;
+          gate_of<kExact>(fv[v], g, z);
+          A[v] *= g;
+          E[v] = g * (dv[v] + E[v]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    s_a[wave][lane * V + v] = A[v];
+    s_h[wave][lane * V + v] = E[v];
+  }
+  __syncthreads();
+  const int64_t first = ((int64_t)it.unit - it.local) * a.channels + it.ch;
+  if (wave == 0 && it.on && it.local > 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float ma = 1.0f, mh = 0.0f;
+      for (int w = kPassWaves - 1; w >= 0; --w) {
+        mh = fmaf(s_a[w][lane * V + v], mh, s_h[w][lane * V + v]);
+        ma *= s_a[w][lane * V + v];
+      }
+      __hip_atomic_store(maps + first + (int64_t)it.local * a.channels + v, map_word(ma, mh),
+                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  // the chunks after this one, from the last, shared out among the wavefronts
+  const int after = (int)(it.units - 1 - it.local);
+  const int lo = after * wave / kPassWaves, hi = after * (wave + 1) / kPassWaves;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = 1.0f;
+    E[v] = 0.0f;
+  }
+  if (it.on && hi > lo)
+    compose_maps<V>(maps, first + (int64_t)((int)it.units - 1 - lo) * a.channels, -a.channels,
+                    hi - lo, A, E);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    p_a[wave][lane * V + v] = A[v];
+    p_h[wave][lane * V + v] = E[v];
+  }
+  __syncthreads();
+  if (n <= 0 || !it.on) return;
+  float e[V];
+  const int64_t so = (int64_t)it.doc * a.channels + it.ch;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    e[v] = a.state_in ? a.state_in[so + v] : 0.0f;
+    for (int w = 0; w < kPassWaves; ++w)
+      e[v] = fmaf(p_a[w][lane * V + v], e[v], p_h[w][lane * V + v]);
+    for (int w = kPassWaves - 1; w > wave; --w)
+      e[v] = fmaf(s_a[w][lane * V + v], e[v], s_h[w][lane * V + v]);
+  }
+  T* of = (T*)a.dgate + row * a.dgate_row + it.ch;
+  T* ox = (T*)a.dx + row * a.dx_row + it.ch;
+  const int64_t chunk = (int64_t)it.chunk64 + t0 / kChunk;
+  const float* save =
+      a.saved + (chunk * (kChunk / kSub) + t0 % kChunk / kSub) * a.channels + it.ch;
+#pragma unroll
+  for (int sub = STEPS / kSub - 1; sub >= 0; --sub) {
+    if (sub * kSub < n) {
+      float before[kSub][V], h[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = save[(int64_t)sub * a.channels + v];
+#pragma unroll
+      for (int j = 0; j < kSub; ++j) {
+        const int i = sub * kSub + j;
+        float fv[V], xv[V];
+        open_word<T>(f[i], fv);
+        open_word<T>(x[i], xv);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float g, z;
+          gate_of<kExact>(fv[v], g, z);
+          before[j][v] = h[v];
+          h[v] = fmaf(g, h[v], a.coupled ? z * xv[v] : xv[v]);
+        }
+      }
+#pragma unroll
+      for (int j = kSub - 1; j >= 0; --j) {
+        const int i = sub * kSub + j;
+        if (i < n) {
+          float fv[V], xv[V], dv[V], df[V], dx[V];
+          open_word<T>(f[i], fv);
+          open_word<T>(x[i], xv);
+          open_word<T>(d[i], dv);
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            float g, z;
+            gate_of<kExact>(fv[v], g, z);
+            const float up = dv[v] + e[v];
+            dx[v] = a.coupled ? up * z : up;
+            df[v] = up * (a.coupled ? before[j][v] - xv[v] : before[j][v]) * (g * z);
+            e[v] = g * up;
+          }
+          *(uint32_t*)(of + i * a.dgate_row) = close_word<T>(df);
+          *(uint32_t*)(ox + i * a.dx_row) = close_word<T>(dx);
+        }
+      }
+    }
+  }
+  if (a.state_out && t0 == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.state_out[so + v] = e[v];
+  }
+}
+
 }  // namespace gs
 
 using namespace gs;
@@ -351,10 +754,28 @@ uint32_t chunk_bound(int64_t rows, int32_t count) {
   return (uint32_t)(rows / kChunk + count);
 }
 
-// The one-launch form: no document is longer than a chunk.
-bool direct_form(const gs_documents& d, int64_t rows) {
+// Which form a call takes.  kPass: a document's maps are few enough that every
+// workgroup reads them all (at 256 chunks that is as much as its inputs' third).
+enum Form { kDirectForm, kPassForm, kThreeForm };
+constexpr int kPassFwd = 64, kPassBwd = 32;  // steps of a wavefront
+Form form_of(const gs_documents& d, int64_t rows, int steps) {
   const int64_t longest = d.max_q_len > 0 && d.max_q_len < rows ? d.max_q_len : rows;
-  return longest <= kChunk;
+  if (longest <= kChunk) return kDirectForm;
+  return longest <= (int64_t)256 * steps * kPassWaves ? kPassForm : kThreeForm;
+}
+uint32_t pass_chunks(int64_t rows, int32_t count, int steps) {
+  return (uint32_t)(rows / (steps * kPassWaves) + count);
+}
+// Workspace of a form: the ticket, the maps and the states; or the chunks' maps
+// and states.
+size_t form_bytes(const gs_scan_config& cfg, const gs_documents& d, int64_t rows, int steps) {
+  switch (form_of(d, rows, steps)) {
+    case kDirectForm: return 0;
+    case kPassForm:
+      return 256 + (size_t)pass_chunks(rows, d.count, steps) * cfg.channels * sizeof(uint64_t) +
+             (size_t)d.count * cfg.channels * sizeof(float);
+    default: return (size_t)chunk_bound(rows, d.count) * cfg.channels * 2 * sizeof(float);
+  }
 }
 
 GatedArgs make_args(const gs_scan_config& cfg, const gs_documents& d, int64_t rows, int V,
@@ -390,10 +811,42 @@ hipError_t run_carry(const GatedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The one-pass form: clear, then a workgroup a chunk and channel group.
+struct Pass {
+  uint32_t* ticket;
+  uint64_t* maps;
+  uint32_t chunks;
+  dim3 grid;
+};
+hipError_t clear_pass(GatedArgs& a, int64_t rows, int steps, int V, void* workspace, Pass& p,
+                      hipStream_t s) {
+  p.ticket = (uint32_t*)workspace;
+  p.maps = (uint64_t*)((char*)workspace + 256);
+  p.chunks = pass_chunks(rows, a.docs.count, steps);
+  a.groups = (a.channels + 64 * V - 1) / (64 * V);
+  p.grid = dim3(p.chunks * (uint32_t)a.groups);
+  const int64_t words = (int64_t)p.chunks * a.channels;
+  const int64_t work = words > (int64_t)a.docs.count * a.channels
+                           ? words : (int64_t)a.docs.count * a.channels;
+  const int64_t blocks = (work + 1023) / 1024;
+  gated_clear_kernel<<<dim3((uint32_t)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s>>>(
+      a, p.maps, words, p.ticket, (float*)(p.maps + words));
+  a.state_in = (float*)(p.maps + words);
+  return hipGetLastError();
+}
+
 template <typename T, int V>
-hipError_t run_fwd(const GatedArgs& a, bool direct, hipStream_t s) {
+hipError_t run_fwd(GatedArgs a, Form form, int64_t rows, void* workspace, hipStream_t s) {
   const dim3 block(256);
-  if (direct) {
+  if (form == kPassForm) {
+    Pass p;
+    const hipError_t e = clear_pass(a, rows, kPassFwd, Pack<T>::V, workspace, p, s);
+    if (e != hipSuccess) return e;
+    gated_pass_kernel<T, kPassFwd><<<p.grid, dim3(64 * kPassWaves), 0, s>>>(a, p.maps, p.chunks,
+                                                                            p.ticket);
+    return hipGetLastError();
+  }
+  if (form == kDirectForm) {
     gated_run_kernel<T, V, true><<<grid_of(a, true), block, 0, s>>>(a);
     return hipGetLastError();
   }
@@ -407,9 +860,17 @@ hipError_t run_fwd(const GatedArgs& a, bool direct, hipStream_t s) {
 }
 
 template <typename T, int V>
-hipError_t run_bwd(const GatedArgs& a, bool direct, hipStream_t s) {
+hipError_t run_bwd(GatedArgs a, Form form, int64_t rows, void* workspace, hipStream_t s) {
   const dim3 block(256);
-  if (direct) {
+  if (form == kPassForm) {
+    Pass p;
+    const hipError_t e = clear_pass(a, rows, kPassBwd, Pack<T>::V, workspace, p, s);
+    if (e != hipSuccess) return e;
+    gated_pass_bwd_kernel<T, kPassBwd>
+        <<<p.grid, dim3(64 * kPassWaves), 0, s>>>(a, p.maps, p.chunks, p.ticket);
+    return hipGetLastError();
+  }
+  if (form == kDirectForm) {
     gated_run_bwd_kernel<T, V, true><<<grid_of(a, true), block, 0, s>>>(a);
     return hipGetLastError();
   }
@@ -426,9 +887,10 @@ hipError_t run_bwd(const GatedArgs& a, bool direct, hipStream_t s) {
 
 extern "C" {
 
+// One size for both directions, so that a training program can keep one.
 size_t gs_gated_scan_bytes(const gs_scan_config& cfg, const gs_documents& d, int64_t rows) {
-  if (direct_form(d, rows)) return 0;
-  return (size_t)chunk_bound(rows, d.count) * cfg.channels * 2 * sizeof(float);
+  const size_t fwd = form_bytes(cfg, d, rows, kPassFwd), bwd = form_bytes(cfg, d, rows, kPassBwd);
+  return fwd > bwd ? fwd : bwd;
 }
 
 size_t gs_gated_saved_bytes(const gs_scan_config& cfg, const gs_documents& d, int64_t rows) {
@@ -447,10 +909,10 @@ hipError_t gs_launch_gated_fwd(const gs_scan_config& cfg, const gs_documents& d,
   a.state_in = state_in;
   a.state_out = state_out;
   a.saved = saved;
-  const bool direct = direct_form(d, rows);
-  if (cfg.dtype == GS_F32) return run_fwd<float, V>(a, direct, s);
-  if (cfg.dtype == GS_BF16) return run_fwd<Bf16, V>(a, direct, s);
-  return run_fwd<F16, V>(a, direct, s);
+  const Form form = form_of(d, rows, kPassFwd);
+  if (cfg.dtype == GS_F32) return run_fwd<float, V>(a, form, rows, workspace, s);
+  if (cfg.dtype == GS_BF16) return run_fwd<Bf16, V>(a, form, rows, workspace, s);
+  return run_fwd<F16, V>(a, form, rows, workspace, s);
 }
 
 hipError_t gs_launch_gated_bwd(const gs_scan_config& cfg, const gs_documents& d, int64_t rows,
@@ -468,10 +930,10 @@ hipError_t gs_launch_gated_bwd(const gs_scan_config& cfg, const gs_documents& d,
   a.state_in = dstate_out;
   a.state_out = dstate_in;
   a.saved = const_cast<float*>(saved);
-  const bool direct = direct_form(d, rows);
-  if (cfg.dtype == GS_F32) return run_bwd<float, V>(a, direct, s);
-  if (cfg.dtype == GS_BF16) return run_bwd<Bf16, V>(a, direct, s);
-  return run_bwd<F16, V>(a, direct, s);
+  const Form form = form_of(d, rows, kPassBwd);
+  if (cfg.dtype == GS_F32) return run_bwd<float, V>(a, form, rows, workspace, s);
+  if (cfg.dtype == GS_BF16) return run_bwd<Bf16, V>(a, form, rows, workspace, s);
+  return run_bwd<F16, V>(a, form, rows, workspace, s);
 }
 
 }  // extern "C"
