@@ -1206,9 +1206,10 @@ gs_status check_scan(const gs_scan_config* c, const gs_documents* d, int64_t row
   GS_REQUIRE(c->channels >= 8 && c->channels <= 1 << 24 && c->channels % 8 == 0,
              "channels must be a multiple of 8 in [8, 2^24]");
   GS_CHECK(check_documents(d, false));
-  // a wavefront takes 128 channels or more of a document or a chunk
-  GS_REQUIRE(((int64_t)d->count + rows / 64) * (c->channels / 8) < (int64_t)1 << 31,
-             "too many documents times channels");
+  // a launch has fewer than 2^32 work items: 512 for a chunk of 256 steps and
+  // 64 channels at the least
+  GS_REQUIRE(((int64_t)d->count + rows / 256) * ((c->channels + 63) / 64) < (int64_t)1 << 23,
+             "too many documents or rows times channels");
   return check_token_rows(rows, 1);
 }
 

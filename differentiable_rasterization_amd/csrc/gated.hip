@@ -16,8 +16,8 @@
 //   Otherwise, one pass over the data: a workgroup keeps its chunk's inputs in
 //   registers, composes its map, publishes it, composes the maps of the chunks
 //   before it in its document as they appear, and runs its steps from the
-//   state that gives.  Every workgroup reads all earlier maps (a thousandth of
-//   the chunk each), so nobody waits for more than a map, and the maps are
+//   state that gives.  Every workgroup reads all earlier maps (eight bytes
+//   a channel each), so nobody waits for more than a map, and the maps are
 //   composed in one order whatever the timing.
 //   Documents of more chunks than that is worth: three passes (chunk maps;
 //   per channel, the state every chunk starts from; the steps).
@@ -61,10 +61,15 @@ struct GatedArgs {
 // the exponent's rounding along.
 template <bool kExact>
 __device__ inline void gate_of(float f, float& a, float& z) {
-  const float v = fabsf(f) > 128.0f ? 128.0f : fabsf(f);  // keeps NaN
-  const float t = -v * kLog2e;
-  float m = __builtin_amdgcn_exp2f(t);
-  if constexpr (kExact) m = fmaf(m, fmaf(-v, kLog2e, -t) * kLn2, m);
+  float m;
+  if constexpr (kExact) {
+    const float v = fabsf(f) > 128.0f ? 128.0f : fabsf(f);  // keeps NaN
+    const float t = -v * kLog2e;
+    m = __builtin_amdgcn_exp2f(t);
+    m = fmaf(m, fmaf(-v, kLog2e, -t) * kLn2, m);
+  } else {
+    m = __builtin_amdgcn_exp2f(fabsf(f) * -kLog2e);
+  }
   const float r = __builtin_amdgcn_rcpf(1.0f + m);
   const float small = m * r, big = 1.0f - small;
   a = f >= 0.0f ? big : small;
@@ -473,7 +478,7 @@ __device__ inline void compose_maps(const uint64_t* maps, int64_t from, int64_t 
 
 // Forward: STEPS steps of a wavefront's channels in registers, two words each.
 template <typename T, int STEPS>
-__global__ __launch_bounds__(64 * kPassWaves, 2) void gated_pass_kernel(GatedArgs a,
+__global__ __launch_bounds__(64 * kPassWaves, 4) void gated_pass_kernel(GatedArgs a,
                                                                         uint64_t* maps,
                                                                         uint32_t chunks,
                                                                         uint32_t* ticket) {
@@ -754,14 +759,18 @@ uint32_t chunk_bound(int64_t rows, int32_t count) {
   return (uint32_t)(rows / kChunk + count);
 }
 
-// Which form a call takes.  kPass: a document's maps are few enough that every
-// workgroup reads them all (at 256 chunks that is as much as its inputs' third).
+// Which form a call takes.  kPass: up to 1024 chunks, since every workgroup
+// reads the maps before it.  One pass against three, forward and backward of a
+// document: 131,072 x 1,024 bf16 291 and 492 us against 307 and 782, fp32 402
+// and 657 against 557 and 768; 262,144 x 512 bf16 367 and 560 against 319 and
+// 786, fp32 437 and 730 against 588 and 785.  Past that the maps, which grow
+// with the square, cost more than a pass over the inputs.
 enum Form { kDirectForm, kPassForm, kThreeForm };
-constexpr int kPassFwd = 64, kPassBwd = 32;  // steps of a wavefront
+constexpr int kPassFwd = 32, kPassBwd = 32;  // steps of a wavefront
 Form form_of(const gs_documents& d, int64_t rows, int steps) {
   const int64_t longest = d.max_q_len > 0 && d.max_q_len < rows ? d.max_q_len : rows;
   if (longest <= kChunk) return kDirectForm;
-  return longest <= (int64_t)256 * steps * kPassWaves ? kPassForm : kThreeForm;
+  return longest <= (int64_t)1024 * steps * kPassWaves ? kPassForm : kThreeForm;
 }
 uint32_t pass_chunks(int64_t rows, int32_t count, int steps) {
   return (uint32_t)(rows / (steps * kPassWaves) + count);

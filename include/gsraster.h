@@ -774,9 +774,10 @@ GS_API gs_status gs_attention_bwd(const gs_attention_config* cfg, const gs_docum
  * state_out [count][channels] (NULL to skip; may be state_in) receives the
  * state after the last token (state_in's for an empty document).  saved: NULL,
  * or gs_gated_scan_saved_size() bytes that the gradient reads.  channels is a
- * multiple of 8, at most 2^24.  fp32 pointers are 16-byte aligned; workspace
- * 256-byte aligned, of gs_gated_scan_fwd_workspace_size() bytes (0 where every
- * document is short). */
+ * multiple of 8, at most 2^24, and (count + rows / 256) * ceil(channels / 64)
+ * is below 2^23.  fp32 pointers are 16-byte aligned; workspace 256-byte
+ * aligned, of gs_gated_scan_fwd_workspace_size() bytes (0 where max_q_len or
+ * rows says that every document has at most 64 tokens). */
 typedef struct {
   int32_t dtype; /* gs_dtype */
   int32_t coupled;
@@ -794,8 +795,8 @@ GS_API gs_status gs_gated_scan_fwd(const gs_scan_config* cfg, const gs_documents
                                    void* stream);
 
 /* Gradients from those of y and of state_out (dL_dstate_out NULL: zero):
- * dL_dgate, dL_dx and dL_dstate_in (NULL to skip).  saved is the forward's,
- * for the same inputs and documents. */
+ * dL_dgate, dL_dx and dL_dstate_in (NULL to skip; may be dL_dstate_out).
+ * saved is the forward's, for the same inputs and documents. */
 GS_API size_t gs_gated_scan_bwd_workspace_size(const gs_scan_config* cfg,
                                                const gs_documents* docs, int64_t rows);
 GS_API gs_status gs_gated_scan_bwd(const gs_scan_config* cfg, const gs_documents* docs,

@@ -604,6 +604,104 @@ def test_gated_scan_carried_on_in_pieces():
     tu.close(state[0], end[0], 2 * ref["estate"], "state")
 
 
+def _recurrence(a, u, start):
+    """h_t = a_t h_{t-1} + u_t down the rows, in 64 bits, by doubling."""
+    a, h = a.double().clone(), u.double().clone()
+    h[0] += a[0] * start.double()
+    s = 1
+    while s < len(h):
+        h[s:] = h[s:] + a[s:] * h[:-s]
+        a[s:] = a[s:] * a[:-s]
+        s *= 2
+    return h
+
+
+def _after(h, start):
+    return torch.cat([start.double()[None], h[:-1]])
+
+
+def _scan_long(gate, x, h0, coupled, dy, dh):
+    """tu.scan_document's values and bounds for documents of any length."""
+    f, x, dy = gate.double(), x.double(), dy.double()
+    a, z = torch.sigmoid(f), torch.sigmoid(-f)
+    none = torch.zeros_like(a[0])
+    u = z * x if coupled else x
+    y = _recurrence(a, u, h0)
+    before = _after(y, h0)
+    ey = _recurrence(a, tu.GATE * (a * before.abs() + u.abs()), none)
+    ebefore = _after(ey, none)
+    later = torch.cat([a[1:], torch.ones_like(a[:1])]).flip(0)
+    g = _recurrence(later, dy.flip(0), dh).flip(0)
+    e = g - dy
+    gnext = torch.cat([g[1:].abs(), none[None]])
+    eg = _recurrence(later, (later.flip(0) * tu.GATE * gnext + tu.GATE
+                             * (dy.abs() + e.abs())).flip(0), none).flip(0)
+    d = before - x if coupled else before
+    ad = before.abs() + (x.abs() if coupled else 0.0)
+    w = z if coupled else 1.0
+    return dict(y=y, ey=ey, state=y[-1], estate=ey[-1], dx=g * w, edx=(eg + tu.GATE * g.abs()) * w,
+                df=g * d * a * z, dstate=a[0] * g[0], edstate=a[0] * (eg[0] + tu.GATE * g[0].abs()),
+                edf=(eg * d.abs() + g.abs() * (ebefore + 2.0 * tu.GATE * ad)) * a * z)
+
+
+def test_gated_scan_long_reference():
+    gen = _gen(21)
+    gate, x, dy = (_normal(gen, torch.float32, 77, 3) for _ in range(3))
+    h0, dh = (torch.randn(3, generator=gen, device="cuda") for _ in range(2))
+    for coupled in (True, False):
+        a = tu.scan_document(gate, x, h0, coupled, dy, dh)
+        b = _scan_long(gate, x, h0, coupled, dy, dh)
+        for key, want in a.items():
+            assert torch.allclose(b[key], want, rtol=1e-11, atol=1e-13), key
+
+
+# a few chunks and a thousand of them; more tokens than a pass is made for
+@pytest.mark.parametrize("dtype", [torch.float32] + TYPES)
+@pytest.mark.parametrize("lens,channels,coupled", [
+    ([700, 100000, 3], 136, True), ([262144], 8, False), ([262145, 300, 0, 64], 16, True)])
+def test_gated_scan_long_documents(lens, channels, coupled, dtype):
+    r = _run_scan(lens, channels, coupled, dtype)
+    u = tu.U[dtype]
+    for d, (a, n) in enumerate(zip(r["starts"], lens)):
+        if n == 0:
+            assert torch.equal(r["state"][d], r["h0"][d]) and torch.equal(r["dstate"][d], r["dh"][d])
+            continue
+        at = slice(a, a + n)
+        ref = _scan_long(r["gate"][at], r["x"][at], r["h0"][d], coupled, r["dy"][at], r["dh"][d])
+        for key in ("y", "dx", "df"):
+            want = ref[key]
+            tu.close(r[key][at], want, u * want.abs() + ref["e" + key] + tu.TINY[dtype], key)
+        tu.close(r["state"][d], ref["state"], ref["estate"] + 1e-30, "state")
+        tu.close(r["dstate"][d], ref["dstate"], ref["edstate"] + 1e-30, "dstate")
+    for key in ("y", "df", "dx"):
+        assert (r[key][~r["used"]] == 7.0).all()
+
+
+@pytest.mark.parametrize("n", [1, 64, 65, 1000, 262200])
+def test_gated_scan_state_in_place(n):
+    """The state written over the one taken in gives the bits of two buffers."""
+    gen = _gen(22)
+    ch = 136 if n < 2000 else 8
+    gate, x, dy = (_normal(gen, torch.bfloat16, n, ch) for _ in range(3))
+    cfg = raster.scan_config(torch.bfloat16, ch, True)
+    docs = raster.documents(_ints([0]), _ints([n]), max_q_len=n)
+    saved = _space(raster.gs_gated_scan_saved_size(cfg, docs, n))
+    nf = raster.gs_gated_scan_fwd_workspace_size(cfg, docs, n)
+    nb = raster.gs_gated_scan_bwd_workspace_size(cfg, docs, n)
+    ws = _space(max(nf, nb))
+    h0, dh = (torch.randn((1, ch), generator=gen, device="cuda") for _ in range(2))
+    runs = []
+    for same in (False, True):
+        h, e = h0.clone(), dh.clone()
+        ho, eo = (h, e) if same else (torch.empty_like(h), torch.empty_like(e))
+        y, df, dx = (torch.empty_like(x) for _ in range(3))
+        raster.gs_gated_scan_fwd(cfg, docs, n, gate, x, h, y, ho, saved, ws, nf)
+        raster.gs_gated_scan_bwd(cfg, docs, n, gate, x, saved, dy, e, df, dx, eo, ws, nb)
+        runs.append((y, ho, df, dx, eo))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+
+
 def test_gated_scan_wrong_bound_is_only_slower():
     """max_q_len chooses the launch form; a document longer than it says is
     still computed."""
