@@ -477,6 +477,9 @@ __device__ inline void compose_maps(const uint64_t* maps, int64_t from, int64_t 
 }
 
 // Forward: STEPS steps of a wavefront's channels in registers, two words each.
+// With 32 steps two workgroups fit a compute unit, one loading beside the other's
+// steps: 65,536 x 2,048 bf16, 805 MB in 226 us (3.6 TB/s), the call 234; with 64
+// steps and one workgroup 262.
 template <typename T, int STEPS>
 __global__ __launch_bounds__(64 * kPassWaves, 4) void gated_pass_kernel(GatedArgs a,
                                                                         uint64_t* maps,
@@ -599,7 +602,9 @@ __global__ __launch_bounds__(64 * kPassWaves, 4) void gated_pass_kernel(GatedArg
   }
 }
 
-// Backward: the same from the other end, three words a step.
+// Backward: the same from the other end, three words a step.  20,011 x 1,024
+// fp32 of 12 documents: 100 us after a forward of 61 (410 and 246 MB and the saved
+// states: 4.3 TB/s with what the forward left in cache).
 template <typename T, int STEPS>
 __global__ __launch_bounds__(64 * kPassWaves, 2) void gated_pass_bwd_kernel(GatedArgs a,
                                                                             uint64_t* maps,
