@@ -392,6 +392,17 @@ struct AddCols {
     p.run([&](int n) { return read(n); },
           [&](int n, const V8& x) { o[n % M] = Mat<T>::mul(x, w[n / M], o[n % M]); });
   }
+  // two sums at once
+  __device__ inline void run(const f32x16& s0, f32x16 (&o0)[DT / 32], const f32x16& s1,
+                             f32x16 (&o1)[DT / 32]) {
+    static_assert(R == 1, "one tile of rows");
+    const V8 w0[2] = {pack_cols<T>(s0, 0), pack_cols<T>(s0, 1)};
+    const V8 w1[2] = {pack_cols<T>(s1, 0), pack_cols<T>(s1, 1)};
+    p.run([&](int n) { return read(n); }, [&](int n, const V8& x) {
+      o0[n % M] = Mat<T>::mul(x, w0[n / M], o0[n % M]);
+      o1[n % M] = Mat<T>::mul(x, w1[n / M], o1[n % M]);
+    });
+  }
 };
 
 // Constants of the scores, in units of log2.
@@ -876,16 +887,56 @@ __device__ inline void weigh(f32x16& s, f32x16& dp, const Scale& c, Lse lse, Del
   }
 }
 
+// The same where delta is still to be corrected (below): ds with the delta at
+// hand, the derivative of a score's weight p f in place of p, and their sum's
+// share sum_j p (dp - delta) over the keys below `room`.
+template <int kMode, typename Away>
+__device__ inline void weigh_once(f32x16& s, f32x16& dp, const Scale& c, float lse, float delta,
+                                  Away away, bool part, int room, float& sum) {
+  const int here = part ? room : 32;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float f;
+    const float x = score<kMode>(s[i], c, [&] { return away(i); }, f);
+    float p = __builtin_amdgcn_exp2f(x - lse);
+    float g = p * (dp[i] - delta);
+    if constexpr (kMode & kCap) {
+      sum += result_row(i) < here ? g : 0.0f;
+      p *= f;
+      g *= f;
+    }
+    s[i] = p;
+    dp[i] = g;
+  }
+  if (part) {
+    const int last = only_here(room);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[i] = result_row(i) < last ? s[i] : 0.0f;
+      dp[i] = result_row(i) < last ? dp[i] : 0.0f;
+    }
+  }
+  if constexpr (!(kMode & kCap)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += dp[i];
+  }
+}
+
 // dq: the forward's loop, with p from the stored logarithm of the sum, and
 // delta for the dk, dv kernel, which runs after it.  delta = do.o carries the
 // roundings of o and of the weights that made it.  Where a row leans on few
 // keys, so that o is as large as a value, they would be a third of the
 // gradient's error.  Rows whose keys all stand in the first tile, and all rows
 // under a distance bias, therefore take delta = sum_j p_j dp_j, the same number
-// without those roundings, in a pass of its own over their keys.
+// without those roundings, in a pass of its own over their keys.  Under a bias
+// heads of 64 elements have the registers to do without that pass: with
+// e = sum_j p_j (dp_j - delta), delta is corrected by e, and dq by
+// -e sum_j p_j k_j, which is summed beside it.
 // Causal documents of 3,360 and 13,024 tokens, 16 bf16 heads of 128 over 4,
 // capped scores: 1.23 ms for three products a pair, 0.90 PFLOP/s; the cap is as
 // much vector work again as the exponential.
+template <int DT, int kMode>
+constexpr bool kCorrect = DT == 64 && (kMode & kGeneral) != 0;
 template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
@@ -944,9 +995,10 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
       if (k0 < wave_hi) use(k0);
     }
   };
+  constexpr bool kOnce = kCorrect<DT, kMode>;
   const bool biased = (kMode & kGeneral) && a.slopes;
   const int block_lo = key_limit(a, d, (int)(col0 / a.group));
-  if (biased || block_lo <= kKeys) {
+  if (!kOnce && (biased || block_lo <= kKeys)) {
     float sum = 0.0f;
     walk(biased ? end : min(end, kKeys), [&](int k0) {
 #pragma unroll 1
@@ -968,7 +1020,11 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
     sum = both_sum(sum);
     if (biased || col.lim <= kKeys) delta = any ? sum : 0.0f;
   }
-  if (col.ok && lane < 32) a.delta[place_of] = delta;
+  if (!kOnce && col.ok && lane < 32) a.delta[place_of] = delta;
+  f32x16 pk[DT / 32];
+#pragma unroll
+  for (int i = 0; i < DT / 32; ++i) pk[i] = (f32x16)(0.0f);
+  float sum = 0.0f;
   walk(end, [&](int k0) {
 #pragma unroll
     for (int r0 = 0; r0 < kKeys; r0 += 32) {
@@ -977,8 +1033,14 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
       two_products<T, DT>(mem, rows, rows + kTile, at, qf, df, s, dp[0]);
       AddCols<T, DT, 1> add(mem, rows, at);
       const int off = col.pos - k0 - r0;
-      weigh<kMode>(s, dp[0], sc, [&](int) { return lse; }, [&](int) { return delta; },
-                   [&](int i) { return slope * fabsf((float)(off - result_row(i))); });
+      const auto away = [&](int i) { return slope * fabsf((float)(off - result_row(i))); };
+      if constexpr (kOnce) {
+        weigh_once<kMode>(s, dp[0], sc, lse, delta, away, k0 + kKeys > wave_lo,
+                          col.lim - k0 - r0, sum);
+        add.run(dp[0], g, s, pk);
+        continue;
+      }
+      weigh<kMode>(s, dp[0], sc, [&](int) { return lse; }, [&](int) { return delta; }, away);
       if (k0 + kKeys > wave_lo) {
         const int room = only_here(col.lim - k0 - r0);
 #pragma unroll
@@ -987,6 +1049,14 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
       add.run(dp, g);
     }
   });
+  if constexpr (kOnce) {
+    sum = both_sum(sum);
+    if (col.ok && lane < 32) a.delta[place_of] = any ? delta + sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < DT / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) g[i][j] = fmaf(-sum, pk[i][j], g[i][j]);
+  }
   if (!col.ok) return;
   const bool none = col.lim <= 0;
   store_col<T, DT>(a.out0 + row * a.out0_row + (int64_t)col.head * a.out0_head, a.dim,
@@ -1142,11 +1212,13 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
 // dq where there are few columns: as the forward's few-column form, a
 // workgroup takes 32 columns, its wavefronts 32 keys each in turn, and their
 // sums are added in order.  Six documents of 4,099 tokens in all, 8 fp16 heads of
-// 64 over 2, a prefix and a bias: 51 us, bound by the longest document's walk,
-// taken twice for delta (128-column form: 78).
+// 64 over 2, a prefix and a bias: 32 us, bound by the longest document's walk
+// (51 with a walk of its own for delta; 128-column form: 39).
 template <typename T, int DT, int kMode>
-__global__ __launch_bounds__(256, DT == 128 ? 2 : 3) void attention_dq_few_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, (DT == 128 || kCorrect<DT, kMode>) ? 2 : 3) void
+attention_dq_few_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
+  constexpr bool kOnce = kCorrect<DT, kMode>;
   constexpr int kStride = DT + 4;
   __shared__ __align__(256) float s_raw[4 * 32 * kStride];
   __shared__ float s_delta[4][32];
@@ -1188,7 +1260,7 @@ __global__ __launch_bounds__(256, DT == 128 ? 2 : 3) void attention_dq_few_kerne
     vf.load(vb + (int64_t)k0 * a.v_row, a.v_row, d.kl - k0, a.dim);
   };
   const bool biased = (kMode & kGeneral) && a.slopes;
-  if (biased || wave_lo <= kKeys) {
+  if (!kOnce && (biased || wave_lo <= kKeys)) {
     float sum = 0.0f;
     const int last = biased ? end : min(end, kKeys);
     int k0 = wave * 32;
@@ -1213,10 +1285,11 @@ __global__ __launch_bounds__(256, DT == 128 ? 2 : 3) void attention_dq_few_kerne
           s_delta[3][lane & 31];
     if (biased || col.lim <= kKeys) delta = any ? sum : 0.0f;
   }
-  if (col.ok && wave == 0 && lane < 32) a.delta[place_of] = delta;
-  f32x16 g[DT / 32];
+  if (!kOnce && col.ok && wave == 0 && lane < 32) a.delta[place_of] = delta;
+  f32x16 g[DT / 32], pk[DT / 32];
 #pragma unroll
-  for (int i = 0; i < DT / 32; ++i) g[i] = (f32x16)(0.0f);
+  for (int i = 0; i < DT / 32; ++i) g[i] = pk[i] = (f32x16)(0.0f);
+  float sum = 0.0f;
   int k0 = wave * 32;
   if (k0 < end) fetch(k0);
   for (; k0 < end; k0 += kPieceKeys) {
@@ -1225,14 +1298,31 @@ __global__ __launch_bounds__(256, DT == 128 ? 2 : 3) void attention_dq_few_kerne
     own_lds_written();
     if (k0 + kPieceKeys < end) fetch(k0 + kPieceKeys);
     const int off = col.pos - k0;
-    weigh<kMode>(s, dp[0], sc, [&](int) { return lse; }, [&](int) { return delta; },
-                 [&](int i) { return slope * fabsf((float)(off - result_row(i))); });
+    const auto away = [&](int i) { return slope * fabsf((float)(off - result_row(i))); };
+    if constexpr (kOnce) {
+      weigh_once<kMode>(s, dp[0], sc, lse, delta, away, k0 + 32 > wave_lo, col.lim - k0, sum);
+      AddCols<T, DT, 1>(mem, tile, at).run(dp[0], g, s, pk);
+      continue;
+    }
+    weigh<kMode>(s, dp[0], sc, [&](int) { return lse; }, [&](int) { return delta; }, away);
     if (k0 + 32 > wave_lo) {
       const int room = only_here(col.lim - k0);
 #pragma unroll
       for (int i = 0; i < 16; ++i) dp[0][i] = result_row(i) < room ? dp[0][i] : 0.0f;
     }
     AddCols<T, DT, 1>(mem, tile, at).run(dp, g);
+  }
+  if constexpr (kOnce) {
+    sum = both_sum(sum);
+    if (lane < 32) s_delta[wave][lane] = sum;
+    __syncthreads();
+    sum = ((s_delta[0][lane & 31] + s_delta[1][lane & 31]) + s_delta[2][lane & 31]) +
+          s_delta[3][lane & 31];
+    if (col.ok && wave == 0 && lane < 32) a.delta[place_of] = any ? delta + sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < DT / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) g[i][j] = fmaf(-sum, pk[i][j], g[i][j]);
   }
   __syncthreads();
   leave_cols<DT>(s_raw, g);
@@ -1431,10 +1521,11 @@ int64_t unit_bound(int64_t columns, int64_t step, int32_t count) {
 // Whether `blocks` workgroups of the 128-column form are too few: with less
 // than one a compute unit, its time is its longest document's, which the
 // few-column form divides by four at half the throughput.  Under a distance
-// bias dq walks the keys twice and the turning point is later.  Measured, us,
+// bias a key takes longer (and dq of 128-element heads walks the keys twice),
+// and the turning point is later.  Measured, us,
 // 128-column form : few-column form (forward; dq), heads of 64:
 //   74 workgroups  7.4 : 6.5;  8.8 : 8.3      262  16.6 : 19.7;  17.7 : 26.0
-//   262 with a bias and uneven documents      32.4 : 26.2;  78 : 51
+//   268 with a bias and uneven documents      36.7 : 25.2;  39 : 32
 bool few_columns(const gs_attention_config& cfg, int64_t blocks) {
   return blocks < (cfg.slopes ? 512 : 256);
 }
