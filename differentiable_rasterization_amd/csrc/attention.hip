@@ -929,14 +929,12 @@ __device__ inline void weigh_once(f32x16& s, f32x16& dp, const Scale& c, float l
 // gradient's error.  Rows whose keys all stand in the first tile, and all rows
 // under a distance bias, therefore take delta = sum_j p_j dp_j, the same number
 // without those roundings, in a pass of its own over their keys.  Under a bias
-// heads of 64 elements have the registers to do without that pass: with
-// e = sum_j p_j (dp_j - delta), delta is corrected by e, and dq by
-// -e sum_j p_j k_j, which is summed beside it.
+// the pass can be spared where registers allow (here heads of 64 elements, all
+// heads in the few-column form): with e = sum_j p_j (dp_j - delta), delta is
+// corrected by e, and dq by -e sum_j p_j k_j, which is summed beside it.
 // Causal documents of 3,360 and 13,024 tokens, 16 bf16 heads of 128 over 4,
 // capped scores: 1.23 ms for three products a pair, 0.90 PFLOP/s; the cap is as
 // much vector work again as the exponential.
-template <int DT, int kMode>
-constexpr bool kCorrect = DT == 64 && (kMode & kGeneral) != 0;
 template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
@@ -995,7 +993,7 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
       if (k0 < wave_hi) use(k0);
     }
   };
-  constexpr bool kOnce = kCorrect<DT, kMode>;
+  constexpr bool kOnce = DT == 64 && (kMode & kGeneral) != 0;
   const bool biased = (kMode & kGeneral) && a.slopes;
   const int block_lo = key_limit(a, d, (int)(col0 / a.group));
   if (!kOnce && (biased || block_lo <= kKeys)) {
@@ -1213,12 +1211,14 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
 // workgroup takes 32 columns, its wavefronts 32 keys each in turn, and their
 // sums are added in order.  Six documents of 4,099 tokens in all, 8 fp16 heads of
 // 64 over 2, a prefix and a bias: 32 us, bound by the longest document's walk
-// (51 with a walk of its own for delta; 128-column form: 39).
+// (51 with a walk of its own for delta; 128-column form: 39).  Heads of 128
+// under a bias: 80 (130).  They take one workgroup a compute unit, all registers:
+// with two, 50 of them spill (three documents of 1,500 tokens 18 : 23 us).
 template <typename T, int DT, int kMode>
-__global__ __launch_bounds__(256, (DT == 128 || kCorrect<DT, kMode>) ? 2 : 3) void
+__global__ __launch_bounds__(256, DT == 128 ? 1 : (kMode & kGeneral) ? 2 : 3) void
 attention_dq_few_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
-  constexpr bool kOnce = kCorrect<DT, kMode>;
+  constexpr bool kOnce = (kMode & kGeneral) != 0;
   constexpr int kStride = DT + 4;
   __shared__ __align__(256) float s_raw[4 * 32 * kStride];
   __shared__ float s_delta[4][32];
@@ -1521,8 +1521,8 @@ int64_t unit_bound(int64_t columns, int64_t step, int32_t count) {
 // Whether `blocks` workgroups of the 128-column form are too few: with less
 // than one a compute unit, its time is its longest document's, which the
 // few-column form divides by four at half the throughput.  Under a distance
-// bias a key takes longer (and dq of 128-element heads walks the keys twice),
-// and the turning point is later.  Measured, us,
+// bias a key takes longer (and dq's 128-column form walks the keys of
+// 128-element heads twice), and the turning point is later.  Measured, us,
 // 128-column form : few-column form (forward; dq), heads of 64:
 //   74 workgroups  7.4 : 6.5;  8.8 : 8.3      262  16.6 : 19.7;  17.7 : 26.0
 //   268 with a bias and uneven documents      36.7 : 25.2;  39 : 32
@@ -1562,6 +1562,9 @@ Split split_of(const gs_attention_config& cfg, const gs_documents& d, int64_t ro
   piece = (piece + kPieceKeys - 1) / kPieceKeys * kPieceKeys;
   const int64_t least = o.col_units ? 8 * kPieceKeys : 2 * kPieceKeys;
   if (piece < least) piece = least;
+  // the join of thousands of columns costs 12 us or so (one piece : several, us:
+  // documents of 1,500 tokens 14 : 28, of 2,500 37 : 37, of 4,000 51 : 40)
+  if (o.col_units && longest_k <= 20 * kPieceKeys) piece = 20 * kPieceKeys;
   if (piece > (1 << 30)) piece = 1 << 30;
   o.piece = (int)piece;
   o.pieces = (int)((longest_k + piece - 1) / piece);
@@ -1572,17 +1575,20 @@ Split split_of(const gs_attention_config& cfg, const gs_documents& d, int64_t ro
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // The few-key form of dk and dv: few workgroups of the 128-key form even with
-// one to a query head (64 workgroups of 128-element heads: 93 : 52 us; 304 under
-// a bias, uneven documents, heads of 64: 63 : 42; 296 without: 32.6 : 31.1).
-bool few_keys(int64_t rows_k, int32_t count, int32_t heads_q) {
-  return unit_bound(rows_k, kCols, count) * heads_q < 384;
+// one to a query head.  Heads of 128 elements fill a SIMD's registers with one
+// wavefront there, and turn earlier.  128-key form : few-key form, us: heads of
+// 64, 304 workgroups 33 : 31 (under a bias, uneven documents, 63 : 42); heads
+// of 128, 64 workgroups 93 : 52; training passes with 114 137 : 96, with 228
+// 167 : 153, with 304 160 : 170.
+bool few_keys(const gs_attention_config& cfg, int64_t rows_k, int32_t count) {
+  return unit_bound(rows_k, kCols, count) * cfg.heads_q < (cfg.head_dim > 64 ? 256 : 384);
 }
 
 // Whether dk and dv are summed per query head first: too few workgroups
 // otherwise, with as many as two to a compute unit.
 bool head_parts(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_k) {
   if (cfg.heads_q == cfg.heads_k) return false;
-  const int step = few_keys(rows_k, d.count, cfg.heads_q) ? 32 : kCols;
+  const int step = few_keys(cfg, rows_k, d.count) ? 32 : kCols;
   return unit_bound(rows_k, step, d.count) * cfg.heads_k < 2048;
 }
 
@@ -1623,7 +1629,7 @@ struct Run {
     }
     a.out0 = (uint16_t*)dk.data; a.out0_row = dk.row; a.out0_head = dk.head;
     a.out1 = (uint16_t*)dv.data; a.out1_row = dv.row; a.out1_head = dv.head;
-    if (few_keys(a.docs.rows_k, a.docs.count, a.heads_q)) {
+    if (few_keys(cfg, a.docs.rows_k, a.docs.count)) {
       const int64_t few = unit_bound(a.docs.rows_k, 32, a.docs.count) *
                           (a.parts ? a.heads_q : a.heads_k);
       attention_dkv_few_kernel<T, DT, kMode><<<dim3((uint32_t)few), block, 0, s>>>(a);
