@@ -779,7 +779,8 @@ __global__ __launch_bounds__(256, DT == 128 ? 2 : 3) void attention_step_kernel(
         for (int j = 0; j < 8; ++j) {
           x[j] = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[j] = fmaf(f[i], s_raw[(i * 32 + cc) * kStride + e + j], x[j]);
+          for (int i = 0; i < 4; ++i)
+            x[j] = fmaf(f[i], s_raw[(i * 32 + cc) * kStride + e + j], x[j]);
           if (last) x[j] = none ? 0.0f : x[j] * inv;
         }
         if (last)
@@ -1611,8 +1612,8 @@ struct Run {
     return hipGetLastError();
   }
 
-  static hipError_t bwd(AttnArgs a, const gs_attention_config& cfg, const gs_heads& dq, const gs_heads& dk, const gs_heads& dv,
-                        hipStream_t s) {
+  static hipError_t bwd(AttnArgs a, const gs_attention_config& cfg, const gs_heads& dq,
+                        const gs_heads& dk, const gs_heads& dv, hipStream_t s) {
     const dim3 block(256);
     if (a.docs.rows_q > 0) {
       a.out0 = (uint16_t*)dq.data; a.out0_row = dq.row; a.out0_head = dq.head;
