@@ -69,31 +69,34 @@ __device__ inline void sincos_turns(double t, float& s, float& c) {
 }
 
 // The lane's 8 factors: element e of chunk `chunk` turns by (c[e], s[e]), its
-// partner's share signed already: y[e] = x[e] c[e] + partner[e] s[e].
+// partner's share signed already: y[e] = x[e] c[e] + partner[e] s[e].  With
+// nothing to turn there may be no positions and no frequencies.
 __device__ inline void lane_angles(const QkArgs& a, int row, int chunk, float (&c)[8],
                                    float (&s)[8]) {
   const int e0 = chunk * 8;
   const int half = a.rotary / 2;
-  const double pos = (double)a.positions[row] * 0.15915494309189535;  // 1 / (2 pi)
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     c[e] = 1.0f;
     s[e] = 0.0f;
-    if (e0 < a.rotary) {
-      int i;
-      bool second;
-      if (a.interleaved) {
-        i = (e0 + e) >> 1;
-        second = e & 1;
-      } else {
-        second = e0 >= half;
-        i = e0 + e - (second ? half : 0);
-      }
-      float sn, cs;
-      sincos_turns(pos * (double)a.inv_freq[i], sn, cs);
-      c[e] = cs * a.amplitude;
-      s[e] = (second ? sn : -sn) * a.amplitude;
+  }
+  if (e0 >= a.rotary) return;
+  const double pos = (double)a.positions[row] * 0.15915494309189535;  // 1 / (2 pi)
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    int i;
+    bool second;
+    if (a.interleaved) {
+      i = (e0 + e) >> 1;
+      second = e & 1;
+    } else {
+      second = e0 >= half;
+      i = e0 + e - (second ? half : 0);
     }
+    float sn, cs;
+    sincos_turns(pos * (double)a.inv_freq[i], sn, cs);
+    c[e] = cs * a.amplitude;
+    s[e] = (second ? sn : -sn) * a.amplitude;
   }
 }
 

@@ -1,0 +1,62 @@
+"""Edges of the token operators' arguments: what a call may leave out, and
+values at the ends of their ranges.  Tolerances are token_util's bounds."""
+import pytest
+import torch
+
+import token_util as tu
+from differentiable_rasterization_amd import raster
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _normal(gen, dtype, *shape):
+    return torch.randn(shape, generator=gen, device="cuda").to(dtype)
+
+
+def _space(nbytes):
+    return torch.full((max(int(nbytes), 256),), 0xAB, dtype=torch.uint8, device="cuda")
+
+
+def _check_qk(rows, hq, hk, dim, rotary, norm, eps, dtype, positions, freq):
+    """Both directions of the norm and rotary position, against 64 bits."""
+    gen = _gen(rows + dim + hq)
+    q, k, dyq, dyk = (_normal(gen, dtype, rows, h, dim) for h in (hq, hk, hq, hk))
+    wq, wk = (1 + 0.2 * torch.randn(dim, generator=gen, device="cuda") if norm else None
+              for _ in "qk")
+    cfg = raster.qk_config(dtype, hq, hk, dim, rotary, False, norm, eps, 1.0)
+    oq, ok, dq, dk = (torch.full_like(t, 7.0) for t in (q, k, q, k))
+    dwq, dwk = (torch.full((dim,), 7.0, device="cuda") for _ in "qk")
+    raster.gs_qk_norm_rope_fwd(cfg, rows, positions, freq, wq, wk, q, k, oq, ok)
+    n = raster.gs_qk_norm_rope_bwd_workspace_size(cfg, rows)
+    raster.gs_qk_norm_rope_bwd(cfg, rows, positions, freq, wq, wk, q, k, dyq, dyk, dq, dk, dwq,
+                               dwk, _space(n), n)
+    at = positions if positions is not None else torch.zeros(rows, dtype=torch.int32,
+                                                             device="cuda")
+    turn = tu.turn_matrix(at, freq, dim, rotary, False, 1.0)
+    u = tu.U[dtype]
+    # the bounds of test_tokens_gpu.test_qk_norm_rope: 4e-6 for fp32 of a sum of
+    # dim squares, a root, three products and the angle
+    for x, w, y, dy, dx, dw in ((q, wq, oq, dyq, dq, dwq), (k, wk, ok, dyk, dk, dwk)):
+        want, size = tu.qk_forward(x, w, turn, eps)
+        tu.close(y, want, u * want.abs() + 4e-6 * size + tu.TINY[dtype], "y")
+        gx, agx, gw, agw = tu.qk_backward(x, w, turn, eps, dy)
+        tu.close(dx, gx, u * gx.abs() + 8e-6 * agx + tu.TINY[dtype], "dx")
+        if norm:
+            tu.close(dw, gw, 3e-5 * agw, "dw")
+        else:
+            assert (dw == 7.0).all()
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,hq,hk,dim", [(1, 1, 1, 8), (5, 4, 2, 64), (300, 5, 3, 96),
+                                            (1200, 6, 2, 128)])
+def test_qk_nothing_turned_needs_no_positions(rows, hq, hk, dim, dtype, norm):
+    _check_qk(rows, hq, hk, dim, 0, norm, 1e-6, dtype, None, None)
