@@ -234,7 +234,8 @@ __global__ __launch_bounds__(256) void qk_bwd_kernel(QkArgs a) {
         const float m = group_sum(gx, a.lanes) * inv_dim * r * r;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float dw = d[e] * x[e] * r;
+          // r of lanes without a head has no value where eps is 0
+          const float dw = act ? d[e] * x[e] * r : 0.0f;
           if (isq) aq[e] += dw;
           else ak[e] += dw;
           d[e] = r * (g[e] - x[e] * m);

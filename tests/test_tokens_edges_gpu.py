@@ -60,3 +60,15 @@ def _check_qk(rows, hq, hk, dim, rotary, norm, eps, dtype, positions, freq):
                                             (1200, 6, 2, 128)])
 def test_qk_nothing_turned_needs_no_positions(rows, hq, hk, dim, dtype, norm):
     _check_qk(rows, hq, hk, dim, 0, norm, 1e-6, dtype, None, None)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,hq,hk,dim", [(1, 1, 1, 64), (7, 5, 2, 128), (300, 5, 2, 128),
+                                            (33, 3, 1, 24), (64, 9, 3, 96)])
+def test_qk_norm_without_epsilon(rows, hq, hk, dim, dtype):
+    """Head counts that do not fill a wavefront: what its idle lanes do must
+    not reach the weight gradients (1 / sqrt(0 + eps) has no value there)."""
+    gen = _gen(rows)
+    positions = torch.randint(0, 5000, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+    freq = torch.rand(8, generator=gen, device="cuda")
+    _check_qk(rows, hq, hk, dim, 16, True, 0.0, dtype, positions, freq)
