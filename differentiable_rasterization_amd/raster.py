@@ -222,6 +222,7 @@ def load():
     lib.gs_gated_scan_fwd.argtypes = [P, P, i64] + [P] * 6 + [P, SZ, P]
     lib.gs_gated_scan_bwd.restype = C.c_int
     lib.gs_gated_scan_bwd.argtypes = [P, P, i64] + [P] * 8 + [P, SZ, P]
+    _name_types()
     _lib = lib
     return lib
 
@@ -652,12 +653,34 @@ def gs_densify_prune(N, ld, sh_degree, means, scales, quats, opacities, sh, dL_d
 # ---------------------------------------------------------------------------
 # Token operators
 # ---------------------------------------------------------------------------
+_kinds = {}            # torch dtype: gs_dtype
+_F32 = _I32 = None     # torch.float32, torch.int32 (torch is imported on first use)
+
+
+def _name_types():
+    global _F32, _I32
+    if not _kinds:
+        import torch
+        _F32, _I32 = torch.float32, torch.int32
+        _kinds.update({torch.float32: GS_F32, torch.bfloat16: GS_BF16, torch.float16: GS_F16})
+
+
 def _dtype(dtype) -> int:
-    import torch
-    kinds = {torch.float32: GS_F32, torch.bfloat16: GS_BF16, torch.float16: GS_F16}
-    if dtype not in kinds:
+    _name_types()
+    if dtype not in _kinds:
         raise ValueError("dtype must be torch.float32, bfloat16 or float16, not %s" % dtype)
-    return kinds[dtype]
+    return _kinds[dtype]
+
+
+def _on_device(t) -> bool:
+    """Whether kernels may read a tensor that is not device memory itself."""
+    return t.is_cuda or t.is_pinned()
+
+
+def _extent(t):
+    """What calls hold against their configuration: type, then sizes."""
+    _name_types()
+    return (_kinds.get(t.dtype) if _on_device(t) else None,) + tuple(t.shape)
 
 
 def heads(t) -> gs_heads:
@@ -667,7 +690,7 @@ def heads(t) -> gs_heads:
     if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
         raise ValueError("need a [rows, heads, dim] tensor with contiguous elements")
     h = gs_heads(t.data_ptr(), t.stride(0), t.stride(1))
-    h.tensor = t
+    h.tensor, h.extent, h.address = t, _extent(t), C.addressof(h)
     return h
 
 
@@ -677,25 +700,61 @@ def rows(t) -> gs_rows:
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("need a [rows, channels] tensor with contiguous elements")
     r = gs_rows(t.data_ptr(), t.stride(0))
-    r.tensor = t
+    r.tensor, r.extent, r.address = t, _extent(t), C.addressof(r)
     return r
 
 
-def _heads(t):
+def _view(make, t, want):
+    """The view of a tensor, or a view that a call was given, if it has the
+    type and at least the sizes ``want``: another one would be read past its
+    end."""
     if t is None:
         return None
-    return C.byref(t if type(t) is gs_heads else heads(t))
+    v = t if type(t) in (gs_heads, gs_rows) else make(t)
+    e = getattr(v, "extent", None)
+    if e is None:  # filled in by the caller
+        v.address = C.addressof(v)
+    elif e[0] != want[0] or len(e) != len(want) or any(x < y for x, y in zip(e[1:], want[1:])):
+        raise ValueError("need a device tensor %s of the configuration's dtype, not %s of %s" %
+                         (list(want[1:]), list(e[1:]), v.tensor.dtype))
+    return v
 
 
-def _rows(t):
+def _heads(t, want):
+    """want: (gs_dtype, rows, heads, dim)."""
+    return t if type(t) is gs_heads and getattr(t, "extent", None) == want else \
+        _view(heads, t, want)
+
+
+def _rows(t, want):
+    """want: (gs_dtype, rows, channels)."""
+    return t if type(t) is gs_rows and getattr(t, "extent", None) == want else \
+        _view(rows, t, want)
+
+
+def _where(view):
+    return None if view is None else view.address
+
+
+def _at(t, dtype, n):
+    """Device address of n contiguous elements of a dtype; None for None."""
     if t is None:
         return None
-    return C.byref(t if type(t) is gs_rows else rows(t))
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or \
+            not (t.is_cuda or _on_device(t)):
+        raise ValueError("need a contiguous %s device tensor of %d elements, not %s of %s" %
+                         (dtype, n, list(t.shape), t.dtype))
+    return t.data_ptr()
 
 
-def _at(t):
-    """Device address of a tensor, None for None."""
-    return None if t is None else t.data_ptr()
+def _bytes(t, n):
+    """Device address of n bytes of a tensor of any type; None for None."""
+    if t is None:
+        return None
+    if t.nbytes < n or not t.is_contiguous() or not (t.is_cuda or _on_device(t)):
+        raise ValueError("need a contiguous device tensor of %d bytes, not %s of %s" %
+                         (n, list(t.shape), t.dtype))
+    return t.data_ptr()
 
 
 def documents(q_start, q_len, k_start=None, k_len=None, prefix=None, max_q_len=0,
@@ -707,6 +766,8 @@ def documents(q_start, q_len, k_start=None, k_len=None, prefix=None, max_q_len=0
         if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or
                               t.numel() != q_start.numel()):
             raise ValueError("documents need contiguous int32 arrays of one length")
+        if t is not None and t.numel() and not _on_device(t):
+            raise ValueError("documents need device arrays")
     d = gs_documents(q_start.numel(), int(max_q_len), int(max_k_len),
                      *[None if t is None else t.data_ptr() for t in arrays])
     d.tensors = arrays
@@ -727,6 +788,8 @@ def attention_config(dtype, heads_q, heads_k, head_dim, scale, causal=False, sof
     if slopes is not None and (slopes.numel() != heads_q or not slopes.is_contiguous() or
                                _dtype(slopes.dtype) != GS_F32):
         raise ValueError("slopes must be a contiguous float32 tensor [heads_q]")
+    if slopes is not None and not _on_device(slopes):
+        raise ValueError("slopes must be a device tensor")
     c = gs_attention_config(_dtype(dtype), int(heads_q), int(heads_k), int(head_dim),
                             int(causal), float(scale), float(softcap),
                             None if slopes is None else slopes.data_ptr())
@@ -738,11 +801,24 @@ def scan_config(dtype, channels, coupled=True) -> gs_scan_config:
     return gs_scan_config(_dtype(dtype), int(coupled), int(channels))
 
 
+def _qk_arrays(cfg, n, dim, positions, inv_freq, wq, wk):
+    """Addresses of a call's arrays; what the configuration leaves out is not
+    looked at."""
+    turned, norm = cfg.rotary_dim, cfg.norm
+    return (_at(positions, _I32, n) if turned else None,
+            _at(inv_freq, _F32, turned // 2) if turned else None,
+            _at(wq, _F32, dim) if norm else None, _at(wk, _F32, dim) if norm else None)
+
+
 def gs_qk_norm_rope_fwd(cfg, rows, positions, inv_freq, wq, wk, q, k, q_out, k_out, stream=None):
-    lib = load()
-    _check(lib.gs_qk_norm_rope_fwd(C.byref(cfg), rows, _at(positions), _at(inv_freq), _at(wq),
-                                   _at(wk), _heads(q), _heads(k), _heads(q_out), _heads(k_out),
-                                   _stream(stream)))
+    kind, dim = cfg.dtype, cfg.head_dim
+    for_q, for_k = (kind, rows, cfg.heads_q, dim), (kind, rows, cfg.heads_k, dim)
+    # views made here live until the call is made
+    q, k, q_out, k_out = (_heads(q, for_q), _heads(k, for_k), _heads(q_out, for_q),
+                          _heads(k_out, for_k))
+    _check(load().gs_qk_norm_rope_fwd(
+        C.byref(cfg), rows, *_qk_arrays(cfg, rows, dim, positions, inv_freq, wq, wk), _where(q),
+        _where(k), _where(q_out), _where(k_out), _stream(stream)))
 
 
 def gs_qk_norm_rope_bwd_workspace_size(cfg, rows) -> int:
@@ -751,12 +827,15 @@ def gs_qk_norm_rope_bwd_workspace_size(cfg, rows) -> int:
 
 def gs_qk_norm_rope_bwd(cfg, rows, positions, inv_freq, wq, wk, q, k, dL_dq_out, dL_dk_out,
                         dL_dq, dL_dk, dL_dwq, dL_dwk, workspace, workspace_bytes, stream=None):
-    lib = load()
-    _check(lib.gs_qk_norm_rope_bwd(C.byref(cfg), rows, _at(positions), _at(inv_freq), _at(wq),
-                                   _at(wk), _heads(q), _heads(k), _heads(dL_dq_out),
-                                   _heads(dL_dk_out), _heads(dL_dq), _heads(dL_dk), _at(dL_dwq),
-                                   _at(dL_dwk), _at(workspace), int(workspace_bytes),
-                                   _stream(stream)))
+    kind, dim, norm = cfg.dtype, cfg.head_dim, cfg.norm
+    for_q, for_k = (kind, rows, cfg.heads_q, dim), (kind, rows, cfg.heads_k, dim)
+    v = (_heads(q, for_q), _heads(k, for_k), _heads(dL_dq_out, for_q), _heads(dL_dk_out, for_k),
+         _heads(dL_dq, for_q), _heads(dL_dk, for_k))
+    _check(load().gs_qk_norm_rope_bwd(
+        C.byref(cfg), rows, *_qk_arrays(cfg, rows, dim, positions, inv_freq, wq, wk),
+        *map(_where, v), _at(dL_dwq, _F32, dim) if norm else None,
+        _at(dL_dwk, _F32, dim) if norm else None, _bytes(workspace, workspace_bytes),
+        int(workspace_bytes), _stream(stream)))
 
 
 def gs_attention_fwd_workspace_size(cfg, docs, rows_q, rows_k) -> int:
@@ -767,10 +846,13 @@ def gs_attention_fwd_workspace_size(cfg, docs, rows_q, rows_k) -> int:
 def gs_attention_fwd(cfg, docs, rows_q, rows_k, q, k, v, out, lse, workspace, workspace_bytes,
                      stream=None):
     """lse: fp32 [heads_q, rows_q], or None where no gradient follows."""
-    lib = load()
-    _check(lib.gs_attention_fwd(C.byref(cfg), C.byref(docs), rows_q, rows_k, _heads(q), _heads(k),
-                                _heads(v), _heads(out), _at(lse), _at(workspace),
-                                int(workspace_bytes), _stream(stream)))
+    kind, hq, dim = cfg.dtype, cfg.heads_q, cfg.head_dim
+    for_q, for_k = (kind, rows_q, hq, dim), (kind, rows_k, cfg.heads_k, dim)
+    q, k, v, out = _heads(q, for_q), _heads(k, for_k), _heads(v, for_k), _heads(out, for_q)
+    _check(load().gs_attention_fwd(
+        C.byref(cfg), C.byref(docs), rows_q, rows_k, _where(q), _where(k), _where(v), _where(out),
+        _at(lse, _F32, hq * rows_q), _bytes(workspace, workspace_bytes), int(workspace_bytes),
+        _stream(stream)))
 
 
 def gs_attention_bwd_workspace_size(cfg, docs, rows_q, rows_k) -> int:
@@ -780,11 +862,15 @@ def gs_attention_bwd_workspace_size(cfg, docs, rows_q, rows_k) -> int:
 
 def gs_attention_bwd(cfg, docs, rows_q, rows_k, q, k, v, out, lse, dL_dout, dL_dq, dL_dk, dL_dv,
                      workspace, workspace_bytes, stream=None):
-    lib = load()
-    _check(lib.gs_attention_bwd(C.byref(cfg), C.byref(docs), rows_q, rows_k, _heads(q), _heads(k),
-                                _heads(v), _heads(out), _at(lse), _heads(dL_dout), _heads(dL_dq),
-                                _heads(dL_dk), _heads(dL_dv), _at(workspace),
-                                int(workspace_bytes), _stream(stream)))
+    kind, hq, dim = cfg.dtype, cfg.heads_q, cfg.head_dim
+    for_q, for_k = (kind, rows_q, hq, dim), (kind, rows_k, cfg.heads_k, dim)
+    inputs = _heads(q, for_q), _heads(k, for_k), _heads(v, for_k), _heads(out, for_q)
+    grads = (_heads(dL_dout, for_q), _heads(dL_dq, for_q), _heads(dL_dk, for_k),
+             _heads(dL_dv, for_k))
+    _check(load().gs_attention_bwd(
+        C.byref(cfg), C.byref(docs), rows_q, rows_k, *map(_where, inputs),
+        _at(lse, _F32, hq * rows_q), *map(_where, grads), _bytes(workspace, workspace_bytes),
+        int(workspace_bytes), _stream(stream)))
 
 
 def gs_gated_scan_saved_size(cfg, docs, rows) -> int:
@@ -795,13 +881,19 @@ def gs_gated_scan_fwd_workspace_size(cfg, docs, rows) -> int:
     return int(load().gs_gated_scan_fwd_workspace_size(C.byref(cfg), C.byref(docs), rows))
 
 
+def _saved(cfg, docs, n, saved):
+    return None if saved is None else _bytes(saved, gs_gated_scan_saved_size(cfg, docs, n))
+
+
 def gs_gated_scan_fwd(cfg, docs, rows, gate, x, state_in, y, state_out, saved, workspace,
                       workspace_bytes, stream=None):
     """saved: None, or gs_gated_scan_saved_size() bytes for the gradient."""
-    lib = load()
-    _check(lib.gs_gated_scan_fwd(C.byref(cfg), C.byref(docs), rows, _rows(gate), _rows(x),
-                                 _at(state_in), _rows(y), _at(state_out), _at(saved), _at(workspace),
-                                 int(workspace_bytes), _stream(stream)))
+    want, states = (cfg.dtype, rows, cfg.channels), docs.count * cfg.channels
+    gate, x, y = _rows(gate, want), _rows(x, want), _rows(y, want)
+    _check(load().gs_gated_scan_fwd(
+        C.byref(cfg), C.byref(docs), rows, _where(gate), _where(x), _at(state_in, _F32, states),
+        _where(y), _at(state_out, _F32, states), _saved(cfg, docs, rows, saved),
+        _bytes(workspace, workspace_bytes), int(workspace_bytes), _stream(stream)))
 
 
 def gs_gated_scan_bwd_workspace_size(cfg, docs, rows) -> int:
@@ -810,11 +902,14 @@ def gs_gated_scan_bwd_workspace_size(cfg, docs, rows) -> int:
 
 def gs_gated_scan_bwd(cfg, docs, rows, gate, x, saved, dL_dy, dL_dstate_out, dL_dgate, dL_dx,
                       dL_dstate_in, workspace, workspace_bytes, stream=None):
-    lib = load()
-    _check(lib.gs_gated_scan_bwd(C.byref(cfg), C.byref(docs), rows, _rows(gate), _rows(x),
-                                 _at(saved), _rows(dL_dy), _at(dL_dstate_out), _rows(dL_dgate),
-                                 _rows(dL_dx), _at(dL_dstate_in), _at(workspace),
-                                 int(workspace_bytes), _stream(stream)))
+    want, states = (cfg.dtype, rows, cfg.channels), docs.count * cfg.channels
+    gate, x, dL_dy = _rows(gate, want), _rows(x, want), _rows(dL_dy, want)
+    dL_dgate, dL_dx = _rows(dL_dgate, want), _rows(dL_dx, want)
+    _check(load().gs_gated_scan_bwd(
+        C.byref(cfg), C.byref(docs), rows, _where(gate), _where(x),
+        _saved(cfg, docs, rows, saved), _where(dL_dy), _at(dL_dstate_out, _F32, states),
+        _where(dL_dgate), _where(dL_dx), _at(dL_dstate_in, _F32, states),
+        _bytes(workspace, workspace_bytes), int(workspace_bytes), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------
