@@ -43,6 +43,7 @@ struct QkArgs {
   int lanes;        // lanes of a head: power of two >= dim / 8
   int items;        // wavefront items a token: 1 (all passes), or one a pass
   int passes_q, passes_k;
+  uint32_t block0;  // forward: first workgroup of the launch
 };
 
 // sin and cos of t turns, t in 64 bits: reduced to the nearest quarter turn
@@ -125,7 +126,7 @@ __device__ inline float group_sum(float v, int lanes) {
 template <typename T>
 __global__ __launch_bounds__(256) void qk_fwd_kernel(QkArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t item = ((int64_t)a.block0 + blockIdx.x) * 4 + (threadIdx.x >> 6);
   const int row = (int)(item / a.items);
   if (row >= a.rows) return;
   const int chunk = lane & (a.lanes - 1), sub = lane / a.lanes, per = 64 / a.lanes;
@@ -349,11 +350,13 @@ hipError_t gs_launch_qk_fwd(const gs_qk_config& cfg, int64_t rows, const int32_t
   // chip, a wavefront a pass
   a.items = rows * passes <= 4096 ? passes : 1;
   const int64_t blocks = (rows * a.items + 3) / 4;
-  const dim3 grid((uint32_t)blocks), block(256);
-  if (cfg.dtype == GS_F32) qk_fwd_kernel<float><<<grid, block, 0, s>>>(a);
-  else if (cfg.dtype == GS_BF16) qk_fwd_kernel<Bf16><<<grid, block, 0, s>>>(a);
-  else qk_fwd_kernel<F16><<<grid, block, 0, s>>>(a);
-  return hipGetLastError();
+  const dim3 block(256);
+  return launch_all(blocks, 256, [&](uint32_t first, dim3 grid) {
+    a.block0 = first;
+    if (cfg.dtype == GS_F32) qk_fwd_kernel<float><<<grid, block, 0, s>>>(a);
+    else if (cfg.dtype == GS_BF16) qk_fwd_kernel<Bf16><<<grid, block, 0, s>>>(a);
+    else qk_fwd_kernel<F16><<<grid, block, 0, s>>>(a);
+  });
 }
 
 hipError_t gs_launch_qk_bwd(const gs_qk_config& cfg, int64_t rows, const int32_t* positions,

@@ -22,6 +22,21 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLn2 = 0.6931471805599453f;
 
+// `blocks` workgroups of `lanes` lanes, in as many launches as they need: the
+// work items of one are counted in 32 bits and would wrap without an error.
+// launch(first, n) starts n of them; the kernel adds `first` to its index.
+template <typename F>
+hipError_t launch_all(int64_t blocks, int lanes, F launch) {
+  const int64_t most = ((int64_t)1 << 32) / lanes - 1;
+  for (int64_t first = 0; first < blocks; first += most) {
+    const int64_t n = blocks - first < most ? blocks - first : most;
+    launch((uint32_t)first, dim3((uint32_t)n));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 // Documents as the kernels take them.  Starts and lengths come from device
 // memory that the host cannot check, so every use clamps them to the rows
 // the caller's buffers have.

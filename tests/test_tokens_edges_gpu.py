@@ -72,3 +72,16 @@ def test_qk_norm_without_epsilon(rows, hq, hk, dim, dtype):
     positions = torch.randint(0, 5000, (rows,), generator=gen, device="cuda", dtype=torch.int32)
     freq = torch.rand(8, generator=gen, device="cuda")
     _check_qk(rows, hq, hk, dim, 16, True, 0.0, dtype, positions, freq)
+
+
+def test_qk_more_rows_than_a_launch_has_workgroups():
+    """2^26 and a few tokens, a wavefront each, are more than 2^32 work items.
+    Nothing is normed or turned, so the outputs are the inputs."""
+    rows = (1 << 26) + 9
+    cfg = raster.qk_config(torch.bfloat16, 1, 1, 8, 0, norm=False)
+    row = torch.arange(rows, dtype=torch.int32, device="cuda")
+    q = (row % 251).to(torch.bfloat16)[:, None, None].expand(rows, 1, 8).contiguous()
+    k = (row % 241).to(torch.bfloat16)[:, None, None].expand(rows, 1, 8).contiguous()
+    oq, ok = torch.zeros_like(q), torch.zeros_like(k)
+    raster.gs_qk_norm_rope_fwd(cfg, rows, None, None, None, None, q, k, oq, ok)
+    assert torch.equal(oq, q) and torch.equal(ok, k)
