@@ -50,7 +50,10 @@ struct AttnArgs {
   int col_units;      // few-column form: column tiles are units of the grid
   float* part_ml;     // [pieces][heads_q][rows_q][2]
   float* part_o;      // [pieces][heads_q][rows_q][dim]
+  uint32_t block0;    // first workgroup of the launch
 };
+
+__device__ inline uint32_t block_of(const AttnArgs& a) { return a.block0 + blockIdx.x; }
 
 constexpr int kKeys = 64;  // keys of a staged tile
 constexpr int kCols = 128; // columns of a workgroup: four wavefronts of 32
@@ -566,10 +569,10 @@ __global__ __launch_bounds__(256, 2) void attention_fwd_kernel(AttnArgs a) {
   __shared__ __align__(256) char mem[4 * kTile];
   const Lane<DT> at;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int hk = blockIdx.x % a.heads_k;
+  const int hk = block_of(a) % a.heads_k;
   uint32_t local, units;
   Doc d;
-  if (find_document<false>(a.docs, a.group, kCols, blockIdx.x / a.heads_k, &local, &units, &d) < 0)
+  if (find_document<false>(a.docs, a.group, kCols, block_of(a) / a.heads_k, &local, &units, &d) < 0)
     return;
   // long causal rows first
   const uint32_t col0 = (units - 1 - local) * kCols;
@@ -684,7 +687,7 @@ __global__ __launch_bounds__(256, DT == 128 ? 2 : 3) void attention_step_kernel(
   const int tile = (threadIdx.x >> 6) * 32 * DT * 2;
   const Lane<DT> at_lane;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, half = lane >> 5;
-  const StepItem it = step_item(a, blockIdx.x);
+  const StepItem it = step_item(a, block_of(a));
   if (it.none) return;
   const Doc& d = it.d;
   const int hk = it.hk, piece = it.piece, pieces = pieces_of(a, d);
@@ -809,7 +812,7 @@ __global__ __launch_bounds__(256, DT == 128 ? 2 : 3) void attention_step_kernel(
 template <typename T>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int tile_cols) {
   __shared__ float s_x[16][16][9], s_sum[16];
-  int u = blockIdx.x / tile_cols;
+  int u = block_of(a) / tile_cols;
   const int hk = u % a.heads_k;
   u /= a.heads_k;
   const StepItem it = step_item(a, (a.pieces_last ? u : u * a.pieces) * a.heads_k);
@@ -820,7 +823,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int til
   const uint32_t cols = (uint32_t)d.ql * a.group;
   const int sub = threadIdx.x & 15, group = threadIdx.x >> 4, e = sub * 8;
   const int64_t step = (int64_t)a.heads_q * a.docs.rows_q;
-  for (uint32_t c = it.col0 + blockIdx.x % tile_cols; c < cols; c += tile_cols) {
+  for (uint32_t c = it.col0 + block_of(a) % tile_cols; c < cols; c += tile_cols) {
     const Col w = column(a, d, hk, c, cols);
     const int64_t row = d.qs + w.token, at = (int64_t)w.head * a.docs.rows_q + row;
     float top = -INFINITY;
@@ -944,10 +947,10 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   __shared__ __align__(256) char mem[4 * kTile];
   const Lane<DT> at;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int hk = blockIdx.x % a.heads_k;
+  const int hk = block_of(a) % a.heads_k;
   uint32_t local, units;
   Doc d;
-  if (find_document<false>(a.docs, a.group, kCols, blockIdx.x / a.heads_k, &local, &units, &d) < 0)
+  if (find_document<false>(a.docs, a.group, kCols, block_of(a) / a.heads_k, &local, &units, &d) < 0)
     return;
   const uint32_t col0 = (units - 1 - local) * kCols;
   const uint32_t cols = (uint32_t)d.ql * a.group;
@@ -1084,12 +1087,12 @@ __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
   const Lane<DT> at;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int heads = a.parts ? a.heads_q : a.heads_k;
-  const int hb = blockIdx.x % heads;
+  const int hb = block_of(a) % heads;
   const int hk = a.parts ? hb / a.group : hb;
   const int head0 = a.parts ? hb : hb * a.group, nheads = a.parts ? 1 : a.group;
   uint32_t local, units;
   Doc d;
-  if (find_document<true>(a.docs, 1, kCols, blockIdx.x / heads, &local, &units, &d) < 0) return;
+  if (find_document<true>(a.docs, 1, kCols, block_of(a) / heads, &local, &units, &d) < 0) return;
   const int key0 = (int)local * kCols;
   const int wkey = key0 + wave * 32;
   const int key = wkey + (lane & 31);
@@ -1227,10 +1230,10 @@ attention_dq_few_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int tile = wave * 32 * DT * 2;
   const Lane<DT> at;
-  const int hk = blockIdx.x % a.heads_k;
+  const int hk = block_of(a) % a.heads_k;
   uint32_t local, units;
   Doc d;
-  if (find_document<false>(a.docs, a.group, 32, blockIdx.x / a.heads_k, &local, &units, &d) < 0)
+  if (find_document<false>(a.docs, a.group, 32, block_of(a) / a.heads_k, &local, &units, &d) < 0)
     return;
   const uint32_t col0 = (units - 1 - local) * 32, cols = (uint32_t)d.ql * a.group;
   const Col col = column(a, d, hk, col0 + (lane & 31), cols);
@@ -1360,12 +1363,12 @@ __global__ __launch_bounds__(256, DT == 128 ? 1 : 2) void attention_dkv_few_kern
   const int tile = wave * 2 * kTile;
   const Lane<DT> at;
   const int heads = a.parts ? a.heads_q : a.heads_k;
-  const int hb = blockIdx.x % heads;
+  const int hb = block_of(a) % heads;
   const int hk = a.parts ? hb / a.group : hb;
   const int head0 = a.parts ? hb : hb * a.group, nheads = a.parts ? 1 : a.group;
   uint32_t local, units;
   Doc d;
-  if (find_document<true>(a.docs, 1, 32, blockIdx.x / heads, &local, &units, &d) < 0) return;
+  if (find_document<true>(a.docs, 1, 32, block_of(a) / heads, &local, &units, &d) < 0) return;
   const int key0 = (int)local * 32, key = key0 + (lane & 31);
   const int64_t row = d.ks + key0;
   Fragments<T, DT> kf, vf, qf, df;
@@ -1455,10 +1458,10 @@ __global__ __launch_bounds__(256, DT == 128 ? 1 : 2) void attention_dkv_few_kern
 // workgroup, 16 lanes a key, 8 elements a lane.
 template <typename T>
 __global__ __launch_bounds__(256) void attention_heads_kernel(AttnArgs a) {
-  const int hk = blockIdx.x % a.heads_k;
+  const int hk = block_of(a) % a.heads_k;
   uint32_t local, units;
   Doc d;
-  if (find_document<true>(a.docs, 1, 16, blockIdx.x / a.heads_k, &local, &units, &d) < 0) return;
+  if (find_document<true>(a.docs, 1, 16, block_of(a) / a.heads_k, &local, &units, &d) < 0) return;
   const int e = (threadIdx.x & 15) * 8, key = (int)local * 16 + (threadIdx.x >> 4);
   if (e >= a.dim || key >= d.kl) return;
   const int64_t row = d.ks + key;
@@ -1596,54 +1599,54 @@ bool head_parts(const gs_attention_config& cfg, const gs_documents& d, int64_t r
 // The kernels of one element type, head size and way to make scores.
 template <typename T, int DT, int kMode>
 struct Run {
+  // kernel<<<blocks, 256>>>(a, more ...)
+  template <typename K, typename... More>
+  static hipError_t launch(K kernel, int64_t blocks, AttnArgs a, hipStream_t s, More... more) {
+    return launch_all(blocks, 256, [&](uint32_t first, dim3 grid) {
+      a.block0 = first;
+      kernel<<<grid, dim3(256), 0, s>>>(a, more...);
+    });
+  }
+
   static hipError_t fwd(const AttnArgs& a, const Split& p, hipStream_t s) {
     if (p.few) {
       const int64_t tiles = p.units * a.heads_k;
-      attention_step_kernel<T, DT, kMode>
-          <<<dim3((uint32_t)(tiles * a.pieces)), dim3(256), 0, s>>>(a);
-      const hipError_t e = hipGetLastError();
+      const hipError_t e =
+          launch(attention_step_kernel<T, DT, kMode>, tiles * a.pieces, a, s);
       if (e != hipSuccess || a.pieces == 1) return e;
-      attention_join_kernel<T><<<dim3((uint32_t)(tiles * p.cols)), dim3(256), 0, s>>>(a, p.cols);
-      return hipGetLastError();
+      return launch(attention_join_kernel<T>, tiles * p.cols, a, s, p.cols);
     }
     const int64_t columns = (int64_t)a.docs.rows_q * a.group;
-    const int64_t blocks = unit_bound(columns, kCols, a.docs.count) * a.heads_k;
-    attention_fwd_kernel<T, DT, kMode><<<dim3((uint32_t)blocks), dim3(256), 0, s>>>(a);
-    return hipGetLastError();
+    return launch(attention_fwd_kernel<T, DT, kMode>,
+                  unit_bound(columns, kCols, a.docs.count) * a.heads_k, a, s);
   }
 
   static hipError_t bwd(AttnArgs a, const gs_attention_config& cfg, const gs_heads& dq,
                         const gs_heads& dk, const gs_heads& dv, hipStream_t s) {
-    const dim3 block(256);
+    hipError_t e;
     if (a.docs.rows_q > 0) {
       a.out0 = (uint16_t*)dq.data; a.out0_row = dq.row; a.out0_head = dq.head;
       const int64_t columns = (int64_t)a.docs.rows_q * a.group;
       const int64_t blocks = unit_bound(columns, kCols, a.docs.count) * a.heads_k;
-      if (few_columns(cfg, blocks)) {
-        const int64_t few = unit_bound(columns, 32, a.docs.count) * a.heads_k;
-        attention_dq_few_kernel<T, DT, kMode><<<dim3((uint32_t)few), block, 0, s>>>(a);
-      } else {
-        attention_dq_kernel<T, DT, kMode><<<dim3((uint32_t)blocks), block, 0, s>>>(a);
-      }
-      const hipError_t e = hipGetLastError();
+      if (few_columns(cfg, blocks))
+        e = launch(attention_dq_few_kernel<T, DT, kMode>,
+                   unit_bound(columns, 32, a.docs.count) * a.heads_k, a, s);
+      else
+        e = launch(attention_dq_kernel<T, DT, kMode>, blocks, a, s);
       if (e != hipSuccess) return e;
     }
     a.out0 = (uint16_t*)dk.data; a.out0_row = dk.row; a.out0_head = dk.head;
     a.out1 = (uint16_t*)dv.data; a.out1_row = dv.row; a.out1_head = dv.head;
-    if (few_keys(cfg, a.docs.rows_k, a.docs.count)) {
-      const int64_t few = unit_bound(a.docs.rows_k, 32, a.docs.count) *
-                          (a.parts ? a.heads_q : a.heads_k);
-      attention_dkv_few_kernel<T, DT, kMode><<<dim3((uint32_t)few), block, 0, s>>>(a);
-    } else {
-      const int64_t blocks = unit_bound(a.docs.rows_k, kCols, a.docs.count) *
-                             (a.parts ? a.heads_q : a.heads_k);
-      attention_dkv_kernel<T, DT, kMode><<<dim3((uint32_t)blocks), block, 0, s>>>(a);
-    }
-    const hipError_t e = hipGetLastError();
+    const int heads = a.parts ? a.heads_q : a.heads_k;
+    if (few_keys(cfg, a.docs.rows_k, a.docs.count))
+      e = launch(attention_dkv_few_kernel<T, DT, kMode>,
+                 unit_bound(a.docs.rows_k, 32, a.docs.count) * heads, a, s);
+    else
+      e = launch(attention_dkv_kernel<T, DT, kMode>,
+                 unit_bound(a.docs.rows_k, kCols, a.docs.count) * heads, a, s);
     if (e != hipSuccess || !a.parts) return e;
-    const int64_t sums = unit_bound(a.docs.rows_k, 16, a.docs.count) * a.heads_k;
-    attention_heads_kernel<T><<<dim3((uint32_t)sums), block, 0, s>>>(a);
-    return hipGetLastError();
+    return launch(attention_heads_kernel<T>,
+                  unit_bound(a.docs.rows_k, 16, a.docs.count) * a.heads_k, a, s);
   }
 };
 

@@ -85,3 +85,19 @@ def test_qk_more_rows_than_a_launch_has_workgroups():
     oq, ok = torch.zeros_like(q), torch.zeros_like(k)
     raster.gs_qk_norm_rope_fwd(cfg, rows, None, None, None, None, q, k, oq, ok)
     assert torch.equal(oq, q) and torch.equal(ok, k)
+
+
+def test_attention_more_documents_than_a_launch_has_workgroups():
+    """2^21 one-token documents of eight key heads: 2^24 workgroups and 2^32
+    work items.  Each sees one key, so its output is that key's value."""
+    docs, heads = (1 << 21) + 3, 8
+    q = torch.ones((docs, heads, 8), dtype=torch.bfloat16, device="cuda")
+    v = (torch.arange(docs * heads, dtype=torch.int32, device="cuda") % 253).to(torch.bfloat16)
+    v = v.view(docs, heads, 1).expand(docs, heads, 8).contiguous()
+    start = torch.arange(docs, dtype=torch.int32, device="cuda")
+    cfg = raster.attention_config(torch.bfloat16, heads, heads, 8, 1.0, True)
+    d = raster.documents(start, torch.ones_like(start), max_q_len=1)
+    o = torch.zeros_like(q)
+    n = raster.gs_attention_fwd_workspace_size(cfg, d, docs, docs)
+    raster.gs_attention_fwd(cfg, d, docs, docs, q, q, v, o, None, _space(n), n)
+    assert torch.equal(o, v)
