@@ -54,6 +54,7 @@ struct GatedArgs {
   float* maps;   // [chunk][channels] A
   float* carry;  // [chunk][channels] H, then the state the chunk starts from
   uint32_t chunks;  // bound on the number of chunks
+  uint32_t block0;  // chunks' states: first workgroup of the launch
 };
 
 // a = sigmoid(f) and z = 1 - a, both accurate relative to themselves (a gate
@@ -181,9 +182,10 @@ template <bool kBack, int S>
 __global__ __launch_bounds__(16 * S) void gated_carry_kernel(GatedArgs a) {
   __shared__ float s_a[S][17], s_h[S][17];
   const int per = (a.channels + 15) / 16;
-  const int doc = blockIdx.x / per;
+  const uint32_t block = a.block0 + blockIdx.x;
+  const int doc = block / per;
   const int c = threadIdx.x & 15, seg = threadIdx.x >> 4;
-  const int ch = (blockIdx.x % per) * 16 + c;
+  const int ch = (block % per) * 16 + c;
   const uint32_t base = units_before(a.docs.q_start, a.docs.q_len, a.docs.rows_q, doc, kChunk);
   const int len = clamp_len(a.docs.q_start[doc], a.docs.q_len[doc], a.docs.rows_q);
   const int n = (len + kChunk - 1) / kChunk;
@@ -816,13 +818,14 @@ dim3 grid_of(const GatedArgs& a, bool direct) {
 // Long documents (a thousand chunks: 27 us with 16 lanes a channel) are shared
 // among 64 lanes.
 template <bool kBack>
-hipError_t run_carry(const GatedArgs& a, hipStream_t s) {
-  const dim3 grid((uint32_t)((int64_t)((a.channels + 15) / 16) * a.docs.count));
-  if (a.chunks / a.docs.count > 128)
-    gated_carry_kernel<kBack, 64><<<grid, dim3(1024), 0, s>>>(a);
-  else
-    gated_carry_kernel<kBack, 16><<<grid, dim3(256), 0, s>>>(a);
-  return hipGetLastError();
+hipError_t run_carry(GatedArgs a, hipStream_t s) {
+  const int64_t blocks = (int64_t)((a.channels + 15) / 16) * a.docs.count;
+  const int lanes = a.chunks / a.docs.count > 128 ? 1024 : 256;
+  return launch_all(blocks, lanes, [&](uint32_t first, dim3 grid) {
+    a.block0 = first;
+    if (lanes == 1024) gated_carry_kernel<kBack, 64><<<grid, dim3(lanes), 0, s>>>(a);
+    else gated_carry_kernel<kBack, 16><<<grid, dim3(lanes), 0, s>>>(a);
+  });
 }
 
 // The one-pass form: clear, then a workgroup a chunk and channel group.

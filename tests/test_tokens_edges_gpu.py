@@ -101,3 +101,25 @@ def test_attention_more_documents_than_a_launch_has_workgroups():
     n = raster.gs_attention_fwd_workspace_size(cfg, d, docs, docs)
     raster.gs_attention_fwd(cfg, d, docs, docs, q, q, v, o, None, _space(n), n)
     assert torch.equal(o, v)
+
+
+def test_gated_scan_more_states_than_a_launch_has_workgroups():
+    """One document past what a single pass is made for and 32,768 empty ones,
+    of 8,192 channels: 2^24 workgroups of 256 compose the chunks' states.
+    Open gates and no input keep every state."""
+    docs, ch, n = (1 << 15) + 1, 8192, 262145 + 64
+    lens = torch.zeros(docs, dtype=torch.int32, device="cuda")
+    lens[docs - 2] = n
+    start = torch.zeros_like(lens)
+    gate = torch.full((1, ch), float("inf"), dtype=torch.bfloat16, device="cuda").expand(n, ch)
+    x = torch.zeros((1, ch), dtype=torch.bfloat16, device="cuda").expand(n, ch)
+    h = (torch.arange(docs * ch, dtype=torch.int32, device="cuda") % 257).float().view(docs, ch)
+    y = torch.zeros((n, ch), dtype=torch.bfloat16, device="cuda")
+    end = torch.full_like(h, -1.0)
+    cfg = raster.scan_config(torch.bfloat16, ch, False)
+    d = raster.documents(start, lens)
+    nb = raster.gs_gated_scan_fwd_workspace_size(cfg, d, n)
+    raster.gs_gated_scan_fwd(cfg, d, n, gate, x, h, y, end, None, _space(nb), nb)
+    assert torch.equal(end, h)
+    for at in (0, 63, 64, n - 1):
+        assert torch.equal(y[at], h[docs - 2].to(torch.bfloat16))
