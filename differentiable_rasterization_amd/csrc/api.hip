@@ -89,6 +89,7 @@ size_t gs_attention_fwd_bytes(const gs_attention_config& cfg, const gs_documents
                               int64_t rows_q, int64_t rows_k);
 size_t gs_attention_bwd_bytes(const gs_attention_config& cfg, const gs_documents& d,
                               int64_t rows_q, int64_t rows_k);
+bool gs_attention_searches(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q);
 hipError_t gs_launch_attention_fwd(const gs_attention_config& cfg, const gs_documents& d,
                                    int64_t rows_q, int64_t rows_k, const gs_heads& q,
                                    const gs_heads& k, const gs_heads& v, const gs_heads& out,
@@ -101,6 +102,7 @@ hipError_t gs_launch_attention_bwd(const gs_attention_config& cfg, const gs_docu
                                    hipStream_t s);
 size_t gs_gated_scan_bytes(const gs_scan_config& cfg, const gs_documents& d, int64_t rows);
 size_t gs_gated_saved_bytes(const gs_scan_config& cfg, const gs_documents& d, int64_t rows);
+bool gs_gated_searches(const gs_documents& d, int64_t rows);
 hipError_t gs_launch_gated_fwd(const gs_scan_config& cfg, const gs_documents& d, int64_t rows,
                               const gs_rows& gate, const gs_rows& x, const float* state_in,
                               const gs_rows& y, float* state_out, float* saved, void* workspace,
@@ -1154,6 +1156,17 @@ gs_status check_documents(const gs_documents* d, bool keys) {
   return GS_OK;
 }
 
+// Every workgroup of a call that searches reads the documents before its own:
+// the square of their number.  Past this one launch would hold the device for
+// many seconds, and further on for hours.
+constexpr int32_t kMaxSearched = 1 << 20;
+
+gs_status check_searched(const gs_documents* d, bool searches) {
+  GS_REQUIRE(!searches || d->count <= kMaxSearched,
+             "more than 2^20 documents in a call that searches them");
+  return GS_OK;
+}
+
 gs_status check_qk(const gs_qk_config* c, int64_t rows) {
   GS_REQUIRE(c != nullptr, "cfg is NULL");
   GS_REQUIRE(c->dtype >= GS_F32 && c->dtype <= GS_F16, "dtype must be a gs_dtype");
@@ -1269,7 +1282,9 @@ gs_status gs_qk_norm_rope_bwd(const gs_qk_config* cfg, int64_t rows, const int32
 
 size_t gs_attention_fwd_workspace_size(const gs_attention_config* cfg, const gs_documents* docs,
                                        int64_t rows_q, int64_t rows_k) {
-  if (check_attention(cfg, docs, rows_q, rows_k) != GS_OK) return 0;
+  if (check_attention(cfg, docs, rows_q, rows_k) != GS_OK ||
+      check_searched(docs, gs_attention_searches(*cfg, *docs, rows_q)) != GS_OK)
+    return 0;
   return gs_attention_fwd_bytes(*cfg, *docs, rows_q, rows_k);
 }
 
@@ -1278,6 +1293,7 @@ gs_status gs_attention_fwd(const gs_attention_config* cfg, const gs_documents* d
                            const gs_heads* v, const gs_heads* out, float* lse, void* workspace,
                            size_t workspace_bytes, void* stream) {
   GS_CHECK(check_attention(cfg, docs, rows_q, rows_k));
+  GS_CHECK(check_searched(docs, gs_attention_searches(*cfg, *docs, rows_q)));
   if (docs->count == 0 || rows_q == 0) return GS_OK;
   const gs_heads none = {};
   GS_CHECK(check_heads(q, rows_q, cfg->heads_q, cfg->head_dim, false));
@@ -1301,7 +1317,8 @@ gs_status gs_attention_fwd(const gs_attention_config* cfg, const gs_documents* d
 
 size_t gs_attention_bwd_workspace_size(const gs_attention_config* cfg, const gs_documents* docs,
                                        int64_t rows_q, int64_t rows_k) {
-  if (check_attention(cfg, docs, rows_q, rows_k) != GS_OK) return 0;
+  if (check_attention(cfg, docs, rows_q, rows_k) != GS_OK || check_searched(docs, true) != GS_OK)
+    return 0;
   return gs_attention_bwd_bytes(*cfg, *docs, rows_q, rows_k);
 }
 
@@ -1312,6 +1329,7 @@ gs_status gs_attention_bwd(const gs_attention_config* cfg, const gs_documents* d
                            const gs_heads* dL_dv, void* workspace, size_t workspace_bytes,
                            void* stream) {
   GS_CHECK(check_attention(cfg, docs, rows_q, rows_k));
+  GS_CHECK(check_searched(docs, true));
   if (docs->count == 0 || (rows_q == 0 && rows_k == 0)) return GS_OK;
   const gs_heads none = {};
   if (rows_q > 0) {
@@ -1354,13 +1372,16 @@ gs_status gs_attention_bwd(const gs_attention_config* cfg, const gs_documents* d
 
 size_t gs_gated_scan_saved_size(const gs_scan_config* cfg, const gs_documents* docs,
                                 int64_t rows) {
-  if (check_scan(cfg, docs, rows) != GS_OK) return 0;
+  // where states are saved depends on the documents before
+  if (check_scan(cfg, docs, rows) != GS_OK || check_searched(docs, true) != GS_OK) return 0;
   return gs_gated_saved_bytes(*cfg, *docs, rows);
 }
 
 size_t gs_gated_scan_fwd_workspace_size(const gs_scan_config* cfg, const gs_documents* docs,
                                         int64_t rows) {
-  if (check_scan(cfg, docs, rows) != GS_OK) return 0;
+  if (check_scan(cfg, docs, rows) != GS_OK ||
+      check_searched(docs, gs_gated_searches(*docs, rows)) != GS_OK)
+    return 0;
   return gs_gated_scan_bytes(*cfg, *docs, rows);
 }
 
@@ -1369,6 +1390,7 @@ gs_status gs_gated_scan_fwd(const gs_scan_config* cfg, const gs_documents* docs,
                             const gs_rows* y, float* state_out, void* saved, void* workspace,
                             size_t workspace_bytes, void* stream) {
   GS_CHECK(check_scan(cfg, docs, rows));
+  GS_CHECK(check_searched(docs, saved != nullptr || gs_gated_searches(*docs, rows)));
   if (docs->count == 0) return GS_OK;
   const gs_rows none = {};
   if (rows > 0) {
@@ -1390,7 +1412,7 @@ gs_status gs_gated_scan_fwd(const gs_scan_config* cfg, const gs_documents* docs,
 
 size_t gs_gated_scan_bwd_workspace_size(const gs_scan_config* cfg, const gs_documents* docs,
                                         int64_t rows) {
-  if (check_scan(cfg, docs, rows) != GS_OK) return 0;
+  if (check_scan(cfg, docs, rows) != GS_OK || check_searched(docs, true) != GS_OK) return 0;
   return gs_gated_scan_bytes(*cfg, *docs, rows);
 }
 
@@ -1400,6 +1422,7 @@ gs_status gs_gated_scan_bwd(const gs_scan_config* cfg, const gs_documents* docs,
                             const gs_rows* dL_dgate, const gs_rows* dL_dx, float* dL_dstate_in,
                             void* workspace, size_t workspace_bytes, void* stream) {
   GS_CHECK(check_scan(cfg, docs, rows));
+  GS_CHECK(check_searched(docs, true));
   if (docs->count == 0) return GS_OK;
   const gs_rows none = {};
   if (rows > 0) {

@@ -1670,6 +1670,12 @@ hipError_t dispatch(const gs_attention_config& cfg, const AttnArgs& a, F f) {
 
 extern "C" {
 
+// Whether the forward's workgroups search the documents for their tokens.
+bool gs_attention_searches(const gs_attention_config& cfg, const gs_documents& d,
+                           int64_t rows_q) {
+  return split_of(cfg, d, rows_q, 0).col_units;
+}
+
 size_t gs_attention_fwd_bytes(const gs_attention_config& cfg, const gs_documents& d,
                               int64_t rows_q, int64_t rows_k) {
   if (d.count == 0 || rows_q == 0) return 0;

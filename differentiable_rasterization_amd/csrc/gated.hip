@@ -910,6 +910,12 @@ size_t gs_gated_scan_bytes(const gs_scan_config& cfg, const gs_documents& d, int
   return fwd > bwd ? fwd : bwd;
 }
 
+// Whether the workgroups search the documents for their steps (with saved
+// states they all do).
+bool gs_gated_searches(const gs_documents& d, int64_t rows) {
+  return form_of(d, rows, kPassFwd) != kDirectForm;
+}
+
 size_t gs_gated_saved_bytes(const gs_scan_config& cfg, const gs_documents& d, int64_t rows) {
   return (size_t)chunk_bound(rows, d.count) * (kChunk / kSub) * cfg.channels * sizeof(float);
 }

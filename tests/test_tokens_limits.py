@@ -1,0 +1,48 @@
+"""Limits of the token operators' calls, on the host (nothing is launched)."""
+import ctypes as C
+import os
+
+import pytest
+
+from differentiable_rasterization_amd import raster
+from test_tokens_abi import BAD, P, _at_cfg, _docs, _h
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(raster.LIB_PATH):
+        from differentiable_rasterization_amd import build
+        build.build()
+    return raster.load()
+
+
+def test_searched_documents_are_bounded(lib):
+    """Calls that search the documents take 2^20 of them; those that do not
+    go on to their next check (here: an array is missing)."""
+    many, rows = 1 << 21, 1 << 22
+    c, h, s = _at_cfg(), C.byref(_h()), raster.gs_scan_config(1, 1, 64)
+
+    def error(status):
+        assert status == BAD
+        return lib.gs_last_error().decode()
+    for count, max_q_len, refused in ((many, 0, True), (many, 17, True), (many, 16, False),
+                                      (1 << 20, 0, False)):
+        d = C.byref(_docs(count=count, max_q_len=max_q_len))
+        text = error(lib.gs_attention_fwd(C.byref(c), d, rows, rows, h, h, h, None, None, P,
+                                          1 << 50, None))
+        assert ("2^20" in text) == refused, text
+    for count, max_q_len, saved, refused in ((many, 0, None, True), (many, 65, None, True),
+                                             (many, 64, None, False), (many, 64, P, True),
+                                             (1 << 20, 0, P, False)):
+        d = C.byref(_docs(count=count, max_q_len=max_q_len))
+        text = error(lib.gs_gated_scan_fwd(C.byref(s), d, rows, None, None, None, None, None,
+                                           saved, P, 1 << 50, None))
+        assert ("2^20" in text) == refused, text
+    for count, size in ((many, False), (1 << 20, True)):
+        d = C.byref(_docs(count=count, max_q_len=1))
+        assert bool(lib.gs_attention_bwd_workspace_size(C.byref(c), d, rows, rows)) == size
+        assert bool(lib.gs_gated_scan_saved_size(C.byref(s), d, rows)) == size
+        assert ("2^20" in error(lib.gs_attention_bwd(C.byref(c), d, rows, rows, h, h, h, h, P, h, h,
+                                                     h, None, P, 1 << 50, None))) != size
+        assert ("2^20" in error(lib.gs_gated_scan_bwd(C.byref(s), d, rows, None, None, P, None, None,
+                                                      None, None, None, P, 1 << 50, None))) != size
