@@ -1204,7 +1204,8 @@ gs_status check_attention(const gs_attention_config* c, const gs_documents* d, i
              "head_dim must be a multiple of 8 in [8, 128]");
   GS_REQUIRE(c->causal == 0 || c->causal == 1, "causal must be 0 or 1");
   GS_REQUIRE(std::isfinite(c->scale), "scale must be finite");
-  GS_REQUIRE(std::isfinite(c->softcap) && c->softcap >= 0.0f, "softcap must be >= 0");
+  GS_REQUIRE(c->softcap == 0.0f || (c->softcap >= 0x1p-100f && c->softcap <= 0x1p100f),
+             "softcap must be 0 or in [2^-100, 2^100]");
   GS_CHECK(check_documents(d, true));
   GS_REQUIRE((int64_t)d->count * c->heads_q <= (int64_t)1 << 26,
              "documents times heads must be <= 2^26");

@@ -727,7 +727,7 @@ GS_API gs_status gs_qk_norm_rope_bwd(const gs_qk_config* cfg, int64_t rows,
 /* Attention within documents.  Query head h reads key head
  * h / (heads_q / heads_k).  Token i of a document stands at position
  * i' = i + k_len - q_len (the last token at the last key).  Score of key j:
- *   s = scale q.k;  softcap > 0: s = softcap tanh(s / softcap);
+ *   s = scale q.k;  softcap > 0 (2^-100 .. 2^100): s = softcap tanh(s / softcap);
  *   slopes [heads_q] (fp32 DEVICE, NULL: none): s -= slopes[h] |i' - j|.
  * Key j is seen when causal = 0, or j <= i', or j < prefix.  The output is
  * the softmax over the seen keys times the values; a token that sees no key

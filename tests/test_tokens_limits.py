@@ -46,3 +46,14 @@ def test_searched_documents_are_bounded(lib):
                                                      h, None, P, 1 << 50, None))) != size
         assert ("2^20" in error(lib.gs_gated_scan_bwd(C.byref(s), d, rows, None, None, P, None, None,
                                                       None, None, None, P, 1 << 50, None))) != size
+
+
+@pytest.mark.parametrize("softcap", [1e-40, 2.0 ** -101, 2.0 ** 101, 3e38])
+def test_caps_beyond_fp32_products_are_refused(lib, softcap):
+    c, d, h = _at_cfg(softcap=softcap), _docs(), C.byref(_h())
+    assert lib.gs_attention_fwd(C.byref(c), C.byref(d), 8, 8, h, h, h, C.byref(_h(2 * P)), P, P,
+                                1 << 40, None) == BAD
+    assert lib.gs_attention_bwd_workspace_size(C.byref(c), C.byref(d), 8, 8) == 0
+    for fine in (2.0 ** -100, 2.0 ** 100):
+        c = _at_cfg(softcap=fine)
+        assert lib.gs_attention_bwd_workspace_size(C.byref(c), C.byref(d), 8, 8) > 0
