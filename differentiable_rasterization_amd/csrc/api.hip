@@ -1193,6 +1193,17 @@ gs_status check_qk_arrays(const gs_qk_config* c, const int32_t* positions, const
   return GS_OK;
 }
 
+// An output may stand over the input it comes from, element on element, and
+// over nothing else: other tokens would be read after they are written.
+gs_status check_in_place(const gs_heads* out, const gs_heads* in, const gs_heads* other,
+                         int64_t rows, int64_t heads) {
+  if (out->data == in->data)
+    GS_REQUIRE((rows == 1 || out->row == in->row) && (heads == 1 || out->head == in->head),
+               "an output in place of an input must have its strides");
+  GS_REQUIRE(out->data != other->data, "outputs must not alias each other's inputs");
+  return GS_OK;
+}
+
 gs_status check_attention(const gs_attention_config* c, const gs_documents* d, int64_t rows_q,
                           int64_t rows_k) {
   GS_REQUIRE(c != nullptr, "cfg is NULL");
@@ -1240,6 +1251,9 @@ gs_status gs_qk_norm_rope_fwd(const gs_qk_config* cfg, int64_t rows, const int32
   GS_CHECK(check_heads(k, rows, cfg->heads_k, cfg->head_dim, false));
   GS_CHECK(check_heads(q_out, rows, cfg->heads_q, cfg->head_dim, true));
   GS_CHECK(check_heads(k_out, rows, cfg->heads_k, cfg->head_dim, true));
+  GS_CHECK(check_in_place(q_out, q, k, rows, cfg->heads_q));
+  GS_CHECK(check_in_place(k_out, k, q, rows, cfg->heads_k));
+  GS_REQUIRE(q_out->data != k_out->data, "q_out and k_out must not alias");
   return hip_status(gs_launch_qk_fwd(*cfg, rows, positions, inv_freq, wq, wk, *q, *k, *q_out,
                                      *k_out, (hipStream_t)stream),
                     "gs_qk_norm_rope_fwd");
@@ -1274,6 +1288,13 @@ gs_status gs_qk_norm_rope_bwd(const gs_qk_config* cfg, int64_t rows, const int32
   GS_CHECK(check_heads(dL_dk_out, rows, cfg->heads_k, cfg->head_dim, false));
   GS_CHECK(check_heads(dL_dq, rows, cfg->heads_q, cfg->head_dim, true));
   GS_CHECK(check_heads(dL_dk, rows, cfg->heads_k, cfg->head_dim, true));
+  GS_CHECK(check_in_place(dL_dq, dL_dq_out, dL_dk_out, rows, cfg->heads_q));
+  GS_CHECK(check_in_place(dL_dk, dL_dk_out, dL_dq_out, rows, cfg->heads_k));
+  if (cfg->norm) {  // without, q and k are not read
+    GS_CHECK(check_in_place(dL_dq, q, k, rows, cfg->heads_q));
+    GS_CHECK(check_in_place(dL_dk, k, q, rows, cfg->heads_k));
+  }
+  GS_REQUIRE(dL_dq->data != dL_dk->data, "dL_dq and dL_dk must not alias");
   GS_CHECK(check_workspace(workspace, workspace_bytes, gs_qk_bwd_workspace_bytes(*cfg, rows)));
   return hip_status(gs_launch_qk_bwd(*cfg, rows, positions, inv_freq, wq, wk, *q, *k, *dL_dq_out,
                                      *dL_dk_out, *dL_dq, *dL_dk, dL_dwq, dL_dwk, workspace,

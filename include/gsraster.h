@@ -703,7 +703,8 @@ typedef struct {
 
 /* positions [rows] int32, inv_freq [rotary_dim / 2], wq and wk [head_dim]
  * (fp32, 16-byte aligned; NULL with norm = 0; inv_freq and positions NULL
- * with rotary_dim = 0).  q_out and k_out may be q and k (in place). */
+ * with rotary_dim = 0).  q_out and k_out may be q and k (in place, with their
+ * strides). */
 GS_API gs_status gs_qk_norm_rope_fwd(const gs_qk_config* cfg, int64_t rows,
                                      const int32_t* positions, const float* inv_freq,
                                      const float* wq, const float* wk, const gs_heads* q,
@@ -714,7 +715,7 @@ GS_API gs_status gs_qk_norm_rope_fwd(const gs_qk_config* cfg, int64_t rows,
  * dL_dq, dL_dk, and dL_dwq, dL_dwk [head_dim] fp32, summed over tokens and
  * heads (overwritten; not touched with norm = 0).  workspace: 256-byte
  * aligned device memory of gs_qk_norm_rope_bwd_workspace_size() bytes.
- * dL_dq may be dL_dq_out and dL_dk may be dL_dk_out. */
+ * dL_dq may be dL_dq_out or q, and dL_dk dL_dk_out or k, with their strides. */
 GS_API size_t gs_qk_norm_rope_bwd_workspace_size(const gs_qk_config* cfg, int64_t rows);
 GS_API gs_status gs_qk_norm_rope_bwd(const gs_qk_config* cfg, int64_t rows,
                                      const int32_t* positions, const float* inv_freq,

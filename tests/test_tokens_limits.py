@@ -57,3 +57,35 @@ def test_caps_beyond_fp32_products_are_refused(lib, softcap):
     for fine in (2.0 ** -100, 2.0 ** 100):
         c = _at_cfg(softcap=fine)
         assert lib.gs_attention_bwd_workspace_size(C.byref(c), C.byref(d), 8, 8) > 0
+
+
+def _qk_call(lib, q, k, oq, ok, back=None):
+    """Status of a call of 8 tokens, 4 and 2 heads of 64; a workspace that is
+    too small, or a weight that is missing, ends the ones that pass."""
+    b = C.byref
+    c = raster.gs_qk_config(1, 4, 2, 64, 0, 0, 0 if back is None else 1, 1e-6, 1.0)
+    if back is None:
+        return lib.gs_qk_norm_rope_fwd(b(c), 8, None, None, None, None, b(q), b(k), b(oq), b(ok),
+                                       None), ""
+    status = lib.gs_qk_norm_rope_bwd(b(c), 8, None, None, P, P, b(q), b(k), b(back[0]),
+                                     b(back[1]), b(oq), b(ok), P, P, P, 1, None)
+    return status, lib.gs_last_error().decode()
+
+
+def test_outputs_over_other_elements_are_refused(lib):
+    """An output at an input's address with other strides writes tokens that
+    are still to be read."""
+    q, k, o, p = _h(P), _h(2 * P), _h(3 * P), _h(4 * P)
+    other = lambda n: _h(n * P, row=256)
+    assert _qk_call(lib, q, k, other(1), p)[0] == BAD
+    assert _qk_call(lib, q, k, o, other(2))[0] == BAD
+    assert _qk_call(lib, q, k, k, p)[0] == BAD and _qk_call(lib, q, k, o, q)[0] == BAD
+    assert _qk_call(lib, q, k, o, _h(3 * P, row=512))[0] == BAD
+    dq, dk = _h(5 * P), _h(6 * P)
+    fine = "workspace smaller"
+    for a, b in ((o, p), (dq, dk), (q, k), (_h(7 * P, row=512), _h(8 * P, row=128))):
+        assert fine in _qk_call(lib, q, k, a, b, (dq, dk))[1]
+    for a, b in ((other(5), p), (o, other(6)), (other(1), p), (o, other(2)), (dk, p), (o, dq),
+                 (k, p), (o, q), (o, o)):
+        status, text = _qk_call(lib, q, k, a, b, (dq, dk))
+        assert status == BAD and fine not in text, text
