@@ -954,8 +954,9 @@ __device__ inline void weigh_once(f32x16& s, f32x16& dp, const Scale& c, float l
 // heads in the few-column form): with e = sum_j p_j (dp_j - delta), delta is
 // corrected by e, and dq by -e sum_j p_j k_j, which is summed beside it.
 // Causal documents of 3,360 and 13,024 tokens, 16 bf16 heads of 128 over 4,
-// capped scores: 1.23 ms for three products a pair, 0.90 PFLOP/s; the cap is as
-// much vector work again as the exponential.
+// capped scores: 1.23 ms for three products a pair, 0.90 PFLOP/s.  By counters
+// the vector unit issues in 72% of the cycles and the matrix unit works in 41%:
+// bound by vector issue; the cap is as much vector work again as the exponential.
 template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
@@ -1092,7 +1093,8 @@ __global__ __launch_bounds__(256, 2) void attention_dq_kernel(AttnArgs a) {
 // The same documents: 1.73 ms for four products a pair, 0.86 PFLOP/s, and 0.06
 // for the sums over heads; two accumulators leave registers for two wavefronts a
 // SIMD and for 32 columns, so every left operand is read from LDS for one
-// product only.
+// product only (cycles with vector issue 53%, the matrix unit at work 37%, LDS
+// 28%: two wavefronts do not cover each other's waits).
 template <typename T, int DT, int kMode>
 __global__ __launch_bounds__(256, 2) void attention_dkv_kernel(AttnArgs a) {
   typedef typename Mat<T>::V8 V8;
@@ -1575,7 +1577,10 @@ Split split_of(const gs_attention_config& cfg, const gs_documents& d, int64_t ro
   // caches of 120,001 keys in all, us: 77, 63, 78, 70, 72 at 512, 768, 1024,
   // 1536, 2048); with many of uneven length more, so that the long ones end
   // sooner (64 caches of 100,003: 87, 85, 75, 78, 72 at 512, 768, 1536, 2048,
-  // 3072).  Column tiles that are looked up are many already.
+  // 3072).  Column tiles that are looked up are many already.  Even caches do
+  // not care (8 to 64 caches of eight heads of 64, 100,000 keys: 42 to 44 at any
+  // of these); of the uneven ones, those with just under 256 tiles lose by the
+  // step (31 caches: 69 at 768, 47 at 3072; 32 caches: 66, 45).
   o.pieces_last = base >= 256;
   const int64_t target = o.col_units ? 512 : o.pieces_last ? 3072 : 768;
   const int64_t want = (target + base - 1) / base;
@@ -1605,8 +1610,13 @@ bool few_keys(const gs_attention_config& cfg, int64_t rows_k, int32_t count) {
   return unit_bound(rows_k, kCols, count) * cfg.heads_q < (cfg.head_dim > 64 ? 256 : 384);
 }
 
-// Whether dk and dv are summed per query head first: too few workgroups
-// otherwise, with as many as two to a compute unit.
+// Whether dk and dv are summed per query head first: there are otherwise few
+// workgroups, whose walks over all heads of a group end late.  Backward of
+// documents of 2,048 tokens, us, per key head : per query head and summed, by
+// the workgroups of the former:
+//   16 heads of 128 over 4:  136  450 : 227;  544  729 : 653;  1,632  2056 : 1826;
+//                            2,176  2567 : 2412;  3,264  3796 : 3716
+//   16 heads of 64 over 8:   2,176  734 : 750;  4,352  1371 : 1434
 bool head_parts(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_k) {
   if (cfg.heads_q == cfg.heads_k) return false;
   const int step = few_keys(cfg, rows_k, d.count) ? 32 : kCols;

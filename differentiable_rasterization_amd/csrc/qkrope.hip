@@ -5,8 +5,9 @@
 //   (n_i, n_j) turned by theta = position * inv_freq_i and times amplitude,
 //   pairs (i, i + R/2) or (2i, 2i + 1) for i < R/2; dims >= R keep n.
 //
-// Both directions move every element once and compute little, so they are
-// bound by memory traffic.  A wavefront takes one token; 8 elements a lane
+// Both directions move every element once and compute little: memory traffic
+// is what should bound them, and does in fp32; in 16-bit types the instructions
+// take as long (below).  A wavefront takes one token; 8 elements a lane
 // (16 bytes of a 16-bit type), a power-of-two group of lanes a head, so the
 // sum of squares is a butterfly inside the group and the other half of a
 // rotated pair is either in the same lane or one shuffle away.  The angles
@@ -15,9 +16,12 @@
 // product at position 65536 would already be off by 4e-3 rad.
 //
 // Measured: 16,384 tokens of 20 bf16 heads of 128 elements forward, 168 MB in
-// 36 us with the inputs in cache (4.7 TB/s), 43 from memory (3.9); 6,007 tokens
-// of 24 fp32 heads of 96 forward 21 us and backward 32 + 4.7 for the weights
-// (221 MB, 70 us in all from memory); eight tokens 5 us, a launch's latency.
+// 35 us with the inputs in cache (4.8 TB/s), 39 from memory (4.3); its 21 million
+// vector instructions, one a cycle and compute unit, are 35 us at 2.4 GHz too:
+// bound by issue.  6,007 tokens of 24 fp32 heads of 96 forward 21 us and backward
+// 31 + 4.7 for the weights (8.4 and 12.6 million instructions, 14 and 21 us;
+// 277 MB in all, 67 us from memory).  Eight tokens: a kernel of 4.2 us in a call
+// of 5.7 from Python.
 #include "tokens.h"
 
 namespace gs {

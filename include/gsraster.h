@@ -645,9 +645,13 @@ GS_API gs_status gs_densify_prune(int64_t N, int64_t ld, int32_t sh_degree, cons
  *     elements in [0, 2^28].  Outputs must not overlap: each row of an output
  *     is its own.
  *   - rows < 2^31 - 4096, rows times heads < 2^31, and in attention documents
- *     times heads <= 2^26.  Zero rows or documents are
- *     valid and launch nothing; pointers may then be NULL.
- *   - Results are reproducible bit for bit: there are no atomics. */
+ *     times heads <= 2^26.  Zero rows or documents are valid; pointers to
+ *     what then has no elements may be NULL.  What remains is still written:
+ *     states, weight gradients (zero), outputs of tokens without keys (zero),
+ *     gradients of keys without tokens (zero).
+ *   - Results are reproducible bit for bit: no floating-point atomics (the
+ *     scan's workgroups take tickets and publish what they found through
+ *     integer ones, and compose it in one order). */
 typedef enum { GS_F32 = 0, GS_BF16 = 1, GS_F16 = 2 } gs_dtype;
 
 typedef struct {
@@ -761,8 +765,12 @@ GS_API gs_status gs_attention_fwd(const gs_attention_config* cfg, const gs_docum
 /* Gradients with respect to q, k and v (slopes are constants), from the
  * forward's inputs, out and lse and the gradient of out; gradients of shared
  * key heads are summed over their query heads in fp32.  Softmax weights and
- * score gradients are rounded to dtype for the matrix products.  Gradient
- * rows of no document are not written. */
+ * score gradients p (dp - delta) are rounded to dtype for the matrix products;
+ * with GS_F16 they must stay inside its range, as the gradients returned must.
+ * Gradient rows of no document are not written.  Where key heads are shared
+ * and a call has fewer than 2,048 tiles of 128 keys and a key head, the
+ * workspace holds dk and dv of every query head: rows_k heads_q 2 head_dim
+ * floats, up to 8.6 GB for 32 query heads of 128 over one. */
 GS_API size_t gs_attention_bwd_workspace_size(const gs_attention_config* cfg,
                                               const gs_documents* docs, int64_t rows_q,
                                               int64_t rows_k);
