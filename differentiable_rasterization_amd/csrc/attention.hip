@@ -135,7 +135,13 @@ __device__ inline typename Mat<T>::V8 read_cols(const char* mem, int at0, int at
 }
 
 // Eight results of a 32-row tile (registers 8 ks ...) as the right operand's
-// 16 contraction slots.
+// 16 contraction slots.  Here softmax weights and score gradients are rounded
+// to the type, since the matrix instruction takes no wider operand: the sums
+// over them stay fp32, and what it adds is of the size of the inputs' and the
+// outputs' own roundings (against 64 bits, outputs and gradients are off by 1.15
+// to 1.45 times what a form in 32 bits, rounded at the end, is).  A second
+// product for what the rounding leaves out would make the forward's matrix work
+// half as much again.
 template <typename T>
 __device__ inline typename Mat<T>::V8 pack_cols(const f32x16& s, int ks) {
   u32x4 w;

@@ -59,7 +59,8 @@ struct GatedArgs {
 
 // a = sigmoid(f) and z = 1 - a, both accurate relative to themselves (a gate
 // that is nearly open has a tiny z, a shut one a tiny a).  fp32 inputs carry
-// the exponent's rounding along.
+// the exponent's rounding along; of 16-bit ones it is 2^-24 |f| beside the 2^-9 or
+// 2^-12 |f| that f itself was rounded by, and is left.
 template <bool kExact>
 __device__ inline void gate_of(float f, float& a, float& z) {
   float m;

@@ -53,7 +53,8 @@ struct QkArgs {
 // sin and cos of t turns, t in 64 bits: reduced to the nearest quarter turn
 // there, so that what is left of the angle, |x| <= pi / 4, keeps its relative
 // accuracy in fp32, and so do both results near their zeros.  The series are
-// Taylor's, to below 3e-8.
+// Taylor's, to below 3e-8 (the cosine's next term would take its error from 1.85e-8
+// to 1.77e-8, root mean square: the rest is fp32's rounding).
 __device__ inline void sincos_turns(double t, float& s, float& c) {
   const double q = __builtin_rint(4.0 * t);
   const float x = (float)((t - 0.25 * q) * 6.283185307179586);
