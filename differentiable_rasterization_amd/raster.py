@@ -673,7 +673,7 @@ def _dtype(dtype) -> int:
 
 
 def _on_device(t) -> bool:
-    """Whether kernels may read a tensor that is not device memory itself."""
+    """Whether kernels may read the tensor: device memory, or page-locked."""
     return t.is_cuda or t.is_pinned()
 
 
@@ -687,7 +687,7 @@ def heads(t) -> gs_heads:
     """The view of a [rows, heads, dim] device tensor (last dimension
     contiguous).  Calls take the tensor or its view; a view made once saves
     the calls their making it."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+    if type(t) is gs_rows or t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
         raise ValueError("need a [rows, heads, dim] tensor with contiguous elements")
     h = gs_heads(t.data_ptr(), t.stride(0), t.stride(1))
     h.tensor, h.extent, h.address = t, _extent(t), C.addressof(h)
@@ -697,24 +697,24 @@ def heads(t) -> gs_heads:
 def rows(t) -> gs_rows:
     """The view of a [rows, channels] device tensor (last dimension
     contiguous)."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if type(t) is gs_heads or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("need a [rows, channels] tensor with contiguous elements")
     r = gs_rows(t.data_ptr(), t.stride(0))
     r.tensor, r.extent, r.address = t, _extent(t), C.addressof(r)
     return r
 
 
-def _view(make, t, want):
+def _view(kind, make, t, want):
     """The view of a tensor, or a view that a call was given, if it has the
     type and at least the sizes ``want``: another one would be read past its
     end."""
     if t is None:
         return None
-    v = t if type(t) in (gs_heads, gs_rows) else make(t)
+    v = t if type(t) is kind else make(t)
     e = getattr(v, "extent", None)
     if e is None:  # filled in by the caller
         v.address = C.addressof(v)
-    elif e[0] != want[0] or len(e) != len(want) or any(x < y for x, y in zip(e[1:], want[1:])):
+    elif e[0] != want[0] or any(x < y for x, y in zip(e[1:], want[1:])):
         raise ValueError("need a device tensor %s of the configuration's dtype, not %s of %s" %
                          (list(want[1:]), list(e[1:]), v.tensor.dtype))
     return v
@@ -723,13 +723,13 @@ def _view(make, t, want):
 def _heads(t, want):
     """want: (gs_dtype, rows, heads, dim)."""
     return t if type(t) is gs_heads and getattr(t, "extent", None) == want else \
-        _view(heads, t, want)
+        _view(gs_heads, heads, t, want)
 
 
 def _rows(t, want):
     """want: (gs_dtype, rows, channels)."""
     return t if type(t) is gs_rows and getattr(t, "extent", None) == want else \
-        _view(rows, t, want)
+        _view(gs_rows, rows, t, want)
 
 
 def _where(view):

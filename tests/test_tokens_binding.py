@@ -145,3 +145,14 @@ def test_what_the_configuration_leaves_out_is_not_looked_at(lib):
         fn(*first, *dict(arrays, **none, **more).values(), *last, stream=NO_STREAM)
         fn(*first, *dict(arrays, positions=_t(1), wq=_t(1)).values(), *last, stream=NO_STREAM)
     assert lib.calls == 4
+
+
+def test_a_view_of_the_other_kind_is_refused(lib):
+    x = _t(N, C)
+    with pytest.raises(ValueError):
+        _call(0, q=raster.rows(x))
+    with pytest.raises(ValueError):
+        _call(4, x=raster.heads(_t(N, 1, C)))
+    # views filled in by the caller are taken as they are
+    _call(0, q=raster.gs_heads(4096, HQ * D, D))
+    assert lib.calls == 1
