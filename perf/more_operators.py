@@ -1,0 +1,545 @@
+"""Operators of serving in 8 and 4 bits as they are measured: products with
+8-bit weights, a key and value cache that is quantised as it is written, and
+attention over such a cache, also where many requests share a long prefix.
+
+A trained network that predicts Gaussians answers requests a few tokens at a
+time; its weights and its caches are then most of what is read.  ``run``
+computes the operators in their plain form, or calls the framework where
+``own`` is true; ``exact`` computes them in 64 bits.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+LEAST = 2.0 ** -116      # spans below this count as none
+
+
+# ---------------------------------------------------------------------------
+# Cases
+# ---------------------------------------------------------------------------
+def _linear(name, rows, inputs, outputs, dtype, bias):
+    """y = x w^T with w in 8 bits and x brought to 8 bits row by row."""
+    return {"name": name, "op": "linear", "rows": rows, "inputs": inputs, "outputs": outputs,
+            "dtype": dtype, "bias": bias}
+
+
+def _cache(name, docs, fresh, kept, heads, dim, dtype, bits):
+    """fresh: tokens of all requests that are written; kept: those that stood
+    in the cache before.  Afterwards all are read back."""
+    return {"name": name, "op": "cache", "docs": docs, "fresh": fresh, "kept": kept,
+            "heads": heads, "dim": dim, "dtype": dtype, "bits": bits}
+
+
+def _attention(name, docs, fresh, keys, heads_q, heads_k, dim, dtype, bits, groups=0, shared=0,
+               softcap=0.0, slopes=False):
+    """fresh: query tokens of all requests, the last of each one's own keys;
+    keys: own keys of all requests; groups: how many shared prefixes there
+    are, of shared keys together, each of which serves a run of requests."""
+    return {"name": name, "op": "attention", "docs": docs, "fresh": fresh, "keys": keys,
+            "heads_q": heads_q, "heads_k": heads_k, "dim": dim, "dtype": dtype, "bits": bits,
+            "groups": groups, "shared": shared, "softcap": softcap, "slopes": slopes}
+
+
+def listed():
+    return [
+        # one request, one token: a product that is the reading of its weights
+        _linear("linear_one", 1, 2048, 8192, "bf16", False),
+        # many requests, one token each
+        _linear("linear_step", 33, 4096, 4096, "fp16", True),
+        # a small packed batch of scenes
+        _linear("linear_docs", 3001, 2048, 2048, "bf16", True),
+        # long prompts: the largest product
+        _linear("linear_prompt", 16384, 4096, 8192, "bf16", False),
+        # a step of a few requests, whose caches are then handed on whole
+        _cache("cache_step", 8, 8, 2001, 4, 128, "bf16", 8),
+        # packed prompts written into a cache of 4 bits
+        _cache("cache_prompt", 12, 20011, 0, 8, 64, "fp16", 4),
+        # few requests with long caches, one token each
+        _attention("cached_step_long", 4, 4, 120001, 16, 4, 128, "bf16", 8, softcap=30.0),
+        # many requests with caches of many lengths, 4 bits
+        _attention("cached_step_many", 64, 64, 100003, 8, 8, 64, "fp16", 4, slopes=True),
+        # requests that check a few drafted tokens each
+        _attention("cached_draft", 24, 101, 30011, 12, 4, 96, "fp16", 8),
+        # many requests behind one long prompt
+        _attention("cached_shared", 64, 64, 20011, 16, 4, 128, "bf16", 8, groups=1, shared=16384),
+        # three prompts of different lengths, each with its own requests
+        _attention("cached_shared_docs", 48, 131, 9001, 8, 2, 64, "bf16", 4, groups=3,
+                   shared=12007),
+        # a long prompt taken in pieces: the largest pass over a cache
+        _attention("cached_piece", 1, 1024, 32768, 16, 4, 128, "bf16", 8),
+    ]
+
+
+def _spread(rng, lo, hi):
+    """A whole number of [lo, hi], spread over its logarithm."""
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 1)))))))
+
+
+def draw(rng):
+    op = rng.choice(("linear", "cache", "attention", "attention"))
+    dtype = rng.choice(("bf16", "fp16"))
+    if op == "linear":
+        return _nameless(_linear("", _spread(rng, 1, 16384), 16 * _spread(rng, 8, 256),
+                                 8 * _spread(rng, 16, 1024), rng.choice((dtype, "fp32")),
+                                 rng.random() < 0.5))
+    bits, dim, docs = rng.choice((8, 4)), rng.choice((64, 96, 128)), _spread(rng, 1, 64)
+    if op == "cache":
+        fresh = docs if rng.random() < 0.5 else max(docs, _spread(rng, 64, 20000))
+        return _nameless(_cache("", docs, fresh, rng.choice((0, _spread(rng, 64, 20000))),
+                                rng.choice((1, 2, 4, 8)), dim, rng.choice((dtype, "fp32")), bits))
+    heads_k = rng.choice((1, 2, 4))
+    fresh = docs if rng.random() < 0.5 else max(docs, _spread(rng, 8, 512))
+    groups = rng.choice((0, 1, 2, 3))
+    return _nameless(_attention("", docs, fresh, fresh + _spread(rng, 64, 60000),
+                                heads_k * rng.choice((1, 2, 3, 4)), heads_k, dim, dtype, bits,
+                                groups, _spread(rng, 256, 16384) if groups else 0,
+                                rng.choice((0.0, 30.0)), not groups and rng.random() < 0.5))
+
+
+def _nameless(case):
+    del case["name"]
+    return case
+
+
+def _lengths(n, total, least=1):
+    """n lengths: uneven, at least ``least`` each, ``total`` in all."""
+    rng = random.Random(n * 1000003 + total)
+    w = [0.2 + rng.random() ** 2 for _ in range(n)]
+    free, whole = total - n * least, sum(w)
+    out = [least + int(free * x / whole) for x in w]
+    out[0] += total - sum(out)
+    return out
+
+
+def _layout(case):
+    """Lengths of a case: of each request its query tokens and its own keys, of
+    each shared prefix its keys and the requests it serves (first, number)."""
+    docs = case["docs"]
+    fresh = _lengths(docs, case["fresh"])
+    if case["op"] == "cache":
+        kept = _lengths(docs, case["kept"], 0)
+        return fresh, [a + b for a, b in zip(fresh, kept)], [], []
+    more = _lengths(docs, case["keys"] - case["fresh"], 0)
+    own_keys = [a + b for a, b in zip(fresh, more)]
+    groups = min(case["groups"], docs)
+    prefixes = _lengths(groups, case["shared"]) if groups else []
+    served = [(docs * g // groups, docs * (g + 1) // groups - docs * g // groups)
+              for g in range(groups)]
+    return fresh, own_keys, prefixes, served
+
+
+def _pairs(case):
+    """Query token and key pairs that are seen: its own (causal) and shared ones."""
+    fresh, keys, prefixes, served = _layout(case)
+    n = sum(q * k - q * (q - 1) // 2 for q, k in zip(fresh, keys))
+    return n + sum(p * sum(fresh[a:a + m]) for p, (a, m) in zip(prefixes, served))
+
+
+def work(case):
+    size = 4 if case["dtype"] == "fp32" else 2
+    if case["op"] == "linear":
+        m, k, n = case["rows"], case["inputs"], case["outputs"]
+        return {"bytes": m * (k + n) * size + k * n + 4 * n * (2 if case["bias"] else 1),
+                "flops": 2 * m * k * n}
+    if case["op"] == "cache":
+        # tokens in, their codes and two numbers each out; all codes in, all tokens out
+        head = case["dim"] * case["bits"] // 8 + 8
+        wide = case["dim"] * size
+        fresh, whole = case["fresh"], case["fresh"] + case["kept"]
+        return {"bytes": 2 * case["heads"] * (fresh * (wide + head) + whole * (wide + head)),
+                "flops": 2 * case["heads"] * case["dim"] * (4 * fresh + 2 * whole)}
+    head = case["dim"] * case["bits"] // 8 + 8
+    return {"bytes": 2 * case["heads_k"] * head * (case["keys"] + case["shared"]) +
+            2 * case["fresh"] * case["heads_q"] * case["dim"] * size,
+            "flops": 4 * _pairs(case) * case["heads_q"] * case["dim"]}
+
+
+# ---------------------------------------------------------------------------
+# What a program has in hand
+# ---------------------------------------------------------------------------
+def prepare(case, seed):
+    state = {"case": dict(case)}
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    {"linear": _prepare_linear, "cache": _prepare_cache,
+     "attention": _prepare_attention}[case["op"]](state, case, gen)
+    if own:
+        {"linear": _plan_linear, "cache": _plan_cache,
+         "attention": _plan_attention}[case["op"]](state, case)
+    return state
+
+
+def _normal(gen, dtype, *shape):
+    return torch.randn(shape, generator=gen, device="cuda", dtype=torch.float32).to(TYPES[dtype])
+
+
+def _ints(values):
+    return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+
+def _starts(lengths, at=0):
+    out = []
+    for n in lengths:
+        out.append(at)
+        at += n
+    return out
+
+
+def _prepare_linear(state, case, gen):
+    m, k, n = case["rows"], case["inputs"], case["outputs"]
+    state["x"] = _normal(gen, case["dtype"], m, k)
+    # trained weights in 8 bits, a scale for each output channel
+    state["w"] = torch.randint(-127, 128, (n, k), generator=gen, device="cuda", dtype=torch.int8)
+    state["ws"] = (0.5 + torch.rand(n, generator=gen, device="cuda")) / (73.0 * math.sqrt(k))
+    state["bias"] = torch.randn(n, generator=gen, device="cuda") if case["bias"] else None
+
+
+def _rows_of_cache(state, fresh, keys, prefixes):
+    """Places in the cache: shared prefixes, then a slot for each request."""
+    at = sum(prefixes)
+    room = (max(keys) + 255) // 256 * 256
+    state["fresh"], state["keys"], state["prefixes"] = fresh, keys, prefixes
+    state["p_starts"] = _starts(prefixes)
+    state["k_starts"] = [at + i * room for i in range(len(keys))]
+    state["q_starts"] = _starts(fresh)
+    state["rows"] = (sum(fresh), at + room * len(keys))
+    state["at"] = [_ints(v) for v in (state["q_starts"], fresh, state["k_starts"], keys)]
+
+
+def _filled(gen, rows, heads, dim, bits):
+    """A cache that holds normal values, some channels of larger mean."""
+    codes = torch.empty((rows, heads, dim * bits // 8), dtype=torch.uint8, device="cuda")
+    low = torch.empty((heads, rows), device="cuda")
+    step = torch.empty((heads, rows), device="cuda")
+    mean = 0.5 * torch.randn((heads, dim), generator=gen, device="cuda")
+    for a in range(0, rows, 16384):
+        b = min(rows, a + 16384)
+        x = torch.randn((b - a, heads, dim), generator=gen, device="cuda") + mean
+        u, lo, st = _quantised(x, bits)
+        codes[a:b], low[:, a:b], step[:, a:b] = _packed(u, bits), lo.T, st.T
+    return codes, low, step
+
+
+def _prepare_cache(state, case, gen):
+    fresh, keys, _, _ = _layout(case)
+    _rows_of_cache(state, fresh, keys, [])
+    rows_q, rows_k = state["rows"]
+    # keys and values are columns of one projection that holds the queries too
+    fused = _normal(gen, case["dtype"], rows_q, 3 * case["heads"], case["dim"])
+    state["k"], state["v"] = fused[:, case["heads"]:2 * case["heads"]], fused[:, 2 * case["heads"]:]
+    state["kc"] = _filled(gen, rows_k, case["heads"], case["dim"], case["bits"])
+    state["vc"] = _filled(gen, rows_k, case["heads"], case["dim"], case["bits"])
+
+
+def _prepare_attention(state, case, gen):
+    fresh, keys, prefixes, served = _layout(case)
+    _rows_of_cache(state, fresh, keys, prefixes)
+    hq, hk, dim = case["heads_q"], case["heads_k"], case["dim"]
+    state["served"] = [(state["q_starts"][a], sum(fresh[a:a + n])) for a, n in served]
+    group = [-1] * len(fresh)
+    for g, (a, n) in enumerate(served):
+        group[a:a + n] = [g] * n
+    # of each request the keys before its own: where they stand, how many
+    state["before"] = [_ints([state["p_starts"][g] if g >= 0 else 0 for g in group]),
+                       _ints([prefixes[g] if g >= 0 else 0 for g in group])]
+    state["longest"] = max(k + (prefixes[g] if g >= 0 else 0) for k, g in zip(keys, group))
+    state["q"] = _normal(gen, case["dtype"], state["rows"][0], hq, dim)
+    state["kc"] = _filled(gen, state["rows"][1], hk, dim, case["bits"])
+    state["vc"] = _filled(gen, state["rows"][1], hk, dim, case["bits"])
+    state["scale"] = 1.0 / math.sqrt(dim)
+    state["slopes"] = None
+    if case["slopes"]:
+        state["slopes"] = 2.0 ** (-8.0 * (torch.arange(hq, device="cuda", dtype=torch.float32) + 1)
+                                  / hq)
+
+
+# ---------------------------------------------------------------------------
+# The framework's plans: outputs, workspaces and descriptions kept by a program
+# ---------------------------------------------------------------------------
+def _space(size):
+    """A 256-byte aligned workspace of size bytes."""
+    return torch.empty((max(size, 256),), dtype=torch.uint8, device="cuda")
+
+
+def _plan_linear(state, case):
+    from differentiable_rasterization_amd import raster
+    s = state
+    s["cfg"] = raster.linear_config(s["x"].dtype, case["inputs"], case["outputs"])
+    s["y"] = torch.empty((case["rows"], case["outputs"]), dtype=s["x"].dtype, device="cuda")
+    s["xy"] = [raster.rows(s["x"]), raster.rows(s["y"])]
+    s["size"] = raster.gs_linear_i8_workspace_size(s["cfg"], case["rows"])
+    s["space"] = _space(s["size"])
+
+
+def _plan_cache(state, case):
+    from differentiable_rasterization_amd import raster
+    s = state
+    s["cfg"] = raster.cache_config(s["k"].dtype, case["heads"], case["dim"])
+    s["docs"] = raster.documents(*s["at"], max_q_len=max(s["fresh"]), max_k_len=max(s["keys"]))
+    # to read a request whole, its tokens are all its keys
+    whole = [_ints(_starts(s["keys"])), s["at"][3], s["at"][2], s["at"][3]]
+    s["whole"] = raster.documents(*whole, max_q_len=max(s["keys"]), max_k_len=max(s["keys"]))
+    s["kv"] = [raster.heads(s["k"]), raster.heads(s["v"])]
+    s["codes"] = [raster.codes(*s[n], case["bits"]) for n in ("kc", "vc")]
+    shape = (sum(s["keys"]), case["heads"], case["dim"])
+    s["out"] = [torch.empty(shape, dtype=s["k"].dtype, device="cuda") for _ in range(2)]
+    s["out_heads"] = [raster.heads(t) for t in s["out"]]
+
+
+def _plan_attention(state, case):
+    from differentiable_rasterization_amd import raster
+    s = state
+    s["cfg"] = raster.attention_config(s["q"].dtype, case["heads_q"], case["heads_k"],
+                                       case["dim"], s["scale"], causal=True,
+                                       softcap=case["softcap"], slopes=s["slopes"])
+    s["docs"] = raster.documents(*s["at"], max_q_len=max(s["fresh"]), max_k_len=max(s["keys"]))
+    s["shared"] = None
+    if s["prefixes"]:
+        starts, lens = zip(*s["served"])
+        s["shared"] = raster.documents(_ints(starts), _ints(lens), _ints(s["p_starts"]),
+                                       _ints(s["prefixes"]), max_q_len=max(lens),
+                                       max_k_len=max(s["prefixes"]))
+    s["codes"] = [raster.codes(*s[n], case["bits"]) for n in ("kc", "vc")]
+    s["out"] = torch.empty(s["q"].shape, dtype=s["q"].dtype, device="cuda")
+    s["lse"] = torch.empty((case["heads_q"], s["rows"][0]), device="cuda")
+    s["qo"] = [raster.heads(s["q"]), raster.heads(s["out"])]
+    s["size"] = raster.gs_cached_attention_fwd_workspace_size(s["cfg"], case["bits"], s["docs"],
+                                                              s["shared"], *s["rows"])
+    s["space"] = _space(s["size"])
+
+
+# ---------------------------------------------------------------------------
+# One pass
+# ---------------------------------------------------------------------------
+def run(state):
+    op = state["case"]["op"]
+    if own:
+        return {"linear": _own_linear, "cache": _own_cache,
+                "attention": _own_attention}[op](state)
+    return {"linear": _plain_linear, "cache": _plain_cache,
+            "attention": _plain_attention}[op](state)
+
+
+def _own_linear(s):
+    from differentiable_rasterization_amd import raster
+    raster.gs_linear_i8(s["cfg"], s["case"]["rows"], s["xy"][0], s["w"], s["ws"], s["bias"],
+                        s["xy"][1], s["space"], s["size"])
+    return s["y"]
+
+
+def _own_cache(s):
+    from differentiable_rasterization_amd import raster
+    rows_q, rows_k = s["rows"]
+    raster.gs_cache_write(s["cfg"], s["docs"], rows_q, rows_k, *s["kv"], *s["codes"])
+    raster.gs_cache_read(s["cfg"], s["whole"], s["out"][0].shape[0], rows_k, *s["codes"],
+                         *s["out_heads"])
+    return s["out"]
+
+
+def _own_attention(s):
+    from differentiable_rasterization_amd import raster
+    raster.gs_cached_attention_fwd(s["cfg"], s["docs"], s["shared"], *s["rows"], s["qo"][0],
+                                   *s["codes"], s["qo"][1], s["lse"], s["space"], s["size"])
+    return [s["out"], s["lse"]]
+
+
+# ---------------------------------------------------------------------------
+# The plain forms, in 32 bits
+# ---------------------------------------------------------------------------
+def _plain_linear(s):
+    # codes are formed in 64 bits: in 32 a value next to the border of two codes
+    # would go to the wrong one
+    x = s["x"].double()
+    top = x.abs().amax(1, keepdim=True)
+    none = top < LEAST
+    u = torch.round(x * torch.where(none, 0.0, 127.0 / top)).float()
+    scale = torch.where(none, 0.0, top / 127.0).float()
+    y = torch.matmul(u, s["w"].float().T) * (scale * s["ws"])
+    if s["bias"] is not None:
+        y = y + s["bias"]
+    return y.to(s["x"].dtype)
+
+
+def _quantised(x, bits):
+    """(codes, low, step) of x [..., dim]: x is near low + step code.  Codes are
+    formed in 64 bits, as above."""
+    x = x.double()
+    lo, hi = x.amin(-1), x.amax(-1)
+    span, most = hi - lo, 2.0 ** bits - 1.0
+    none = span < LEAST
+    u = torch.round((x - lo[..., None]) * torch.where(none, 0.0, most / span)[..., None])
+    return u, lo.float(), torch.where(none, 0.0, span / most).float()
+
+
+def _packed(u, bits):
+    """Bytes of the codes; in 4 bits, each 32-bit word holds elements 2i in
+    bits 4i and elements 2i + 1 in bits 16 + 4i."""
+    if bits == 8:
+        return u.to(torch.uint8)
+    e = u.to(torch.uint8).unflatten(-1, (-1, 4, 2)).transpose(-1, -2)
+    return (e[..., 0::2] | (e[..., 1::2] << 4)).flatten(-3).contiguous()
+
+
+def _unpacked(codes, bits):
+    if bits == 8:
+        return codes.float()
+    word = codes.contiguous().view(torch.int32)[..., None]
+    shift = torch.tensor([0, 16, 4, 20, 8, 24, 12, 28], device=codes.device, dtype=torch.int32)
+    return ((word >> shift) & 15).flatten(-2).float()
+
+
+def _values(cache, rows, bits):
+    """What the cache holds at rows: [*rows.shape, heads, dim]."""
+    codes, low, step = cache
+    return low.T[rows][..., None] + step.T[rows][..., None] * _unpacked(codes[rows], bits)
+
+
+def _token_rows(starts, lens, total):
+    """Where each of the tokens of all requests stands, requests one by one."""
+    lens = lens.long()
+    first = torch.cumsum(lens, 0) - lens
+    at = torch.repeat_interleave(starts.long() - first, lens, output_size=total)
+    return at + torch.arange(total, device="cuda")
+
+
+def _plain_cache(s):
+    c, at = s["case"], s["at"]
+    rows = _token_rows(at[2] + at[3] - at[1], at[1], s["rows"][0])
+    whole = _token_rows(at[2], at[3], c["fresh"] + c["kept"])
+    ku, klo, kst = _quantised(s["k"], c["bits"])
+    vu, vlo, vst = _quantised(s["v"], c["bits"])
+    s["kc"][0][rows], s["kc"][1][:, rows], s["kc"][2][:, rows] = _packed(ku, c["bits"]), klo.T, kst.T
+    s["vc"][0][rows], s["vc"][1][:, rows], s["vc"][2][:, rows] = _packed(vu, c["bits"]), vlo.T, vst.T
+    return [_values(s["kc"], whole, c["bits"]).to(s["k"].dtype),
+            _values(s["vc"], whole, c["bits"]).to(s["v"].dtype)]
+
+
+def _plain_attention(s):
+    c = s["case"]
+    docs, hk, group, dim = c["docs"], c["heads_k"], c["heads_q"] // c["heads_k"], c["dim"]
+    q_start, fresh, k_start, keys = (t.long()[:, None] for t in s["at"])
+    p_start, before = (t.long()[:, None] for t in s["before"])
+    most = max(s["fresh"])
+    i = torch.arange(most, device="cuda")[None, :]
+    j = torch.arange(s["longest"], device="cuda")[None, :]
+    # a request's keys: the shared ones, then its own
+    rows = torch.where(j < before, p_start + j, k_start + j - before)
+    rows = torch.where(j < before + keys, rows, 0)
+    place = before + keys - fresh + i
+    seen = (j[:, None] <= place[..., None]) & (j < before + keys)[:, None]
+    token = torch.where(i < fresh, q_start + i, 0)
+    q = s["q"].float()[token].view(docs, most, hk, group * dim).transpose(1, 2)
+    q = q.reshape(docs, hk, most * group, dim)
+    k = _values(s["kc"], rows, c["bits"]).permute(0, 2, 3, 1).contiguous()
+    score = (torch.matmul(q, k) * s["scale"]).view(docs, hk, most, group, -1)
+    del k
+    if c["softcap"]:
+        score = torch.tanh(score / c["softcap"]) * c["softcap"]
+    if s["slopes"] is not None:
+        away = (place[..., None] - j[:, None]).abs().float()[:, None, :, None]
+        score = score - s["slopes"].view(1, hk, 1, group, 1) * away
+    score = torch.where(seen[:, None, :, None], score, float("-inf"))
+    # rows behind a request's last token are dropped below
+    top = score.amax(-1, keepdim=True)
+    p = torch.exp(score - top)
+    total = p.sum(-1, keepdim=True)
+    v = _values(s["vc"], rows, c["bits"]).transpose(1, 2).contiguous()
+    o = torch.matmul((p / total).view(docs, hk, most * group, -1), v)
+    o = o.view(docs, hk, most, group, dim).permute(0, 2, 1, 3, 4)
+    lse = (top + torch.log(total))[..., 0].permute(0, 2, 1, 3)
+    here = i < fresh
+    out = torch.empty(s["q"].shape, dtype=s["q"].dtype, device="cuda")
+    out[token[here]] = o[here].reshape(-1, c["heads_q"], dim).to(out.dtype)
+    sums = torch.empty((s["rows"][0], c["heads_q"]), device="cuda")
+    sums[token[here]] = lse[here].reshape(-1, c["heads_q"])
+    return [out, sums.T.contiguous()]
+
+
+# ---------------------------------------------------------------------------
+# From the definitions, in 64 bits
+# ---------------------------------------------------------------------------
+def exact(case, seed):
+    state = prepare(case, seed)
+    return {"linear": _exact_linear, "cache": _exact_cache,
+            "attention": _exact_attention}[case["op"]](state)
+
+
+def _exact_linear(s):
+    x = s["x"].double()
+    top = x.abs().max(1).values[:, None]
+    codes = torch.round(x * (127.0 / top.clamp(min=1e-300)))
+    y = torch.einsum("mk,nk->mn", codes, s["w"].double()) * (top / 127.0) * s["ws"].double()
+    return y if s["bias"] is None else y + s["bias"].double()
+
+
+def _exact_codes(codes, bits, dim):
+    """Codes [rows, dim] of one head, byte by byte."""
+    if bits == 8:
+        return codes.double()
+    out = torch.empty((codes.shape[0], dim), dtype=torch.float64, device="cuda")
+    for b in range(4):
+        byte = codes[:, b::4].int()
+        for half in range(2):
+            nibble = 2 * b + half
+            element = 2 * nibble if nibble < 4 else 2 * (nibble - 4) + 1
+            out[:, element::8] = ((byte >> (4 * half)) & 15).double()
+    return out
+
+
+def _exact_held(cache, rows, head, bits, dim):
+    codes, low, step = cache
+    return (_exact_codes(codes[rows, head], bits, dim) * step[head, rows].double()[:, None] +
+            low[head, rows].double()[:, None])
+
+
+def _exact_cache(s):
+    c = s["case"]
+    outs = []
+    for x, cache in ((s["k"], s["kc"]), (s["v"], s["vc"])):
+        out = torch.empty((sum(s["keys"]), c["heads"], c["dim"]), dtype=torch.float64,
+                          device="cuda")
+        x = x.double()
+        low, high = x.min(-1, keepdim=True).values, x.max(-1, keepdim=True).values
+        levels = 2 ** c["bits"] - 1
+        codes = torch.round((x - low) * (levels / (high - low).clamp(min=1e-300)))
+        written = low + (high - low) / levels * codes
+        at = 0
+        for q0, nq, k0, nk in zip(s["q_starts"], s["fresh"], s["k_starts"], s["keys"]):
+            old = torch.arange(k0, k0 + nk - nq, device="cuda")
+            for h in range(c["heads"]):
+                out[at:at + nk - nq, h] = _exact_held(cache, old, h, c["bits"], c["dim"])
+            out[at + nk - nq:at + nk] = written[q0:q0 + nq]
+            at += nk
+        outs.append(out)
+    return outs
+
+
+def _exact_attention(s):
+    c = s["case"]
+    group = c["heads_q"] // c["heads_k"]
+    o = torch.zeros(s["q"].shape, dtype=torch.float64, device="cuda")
+    lse = torch.zeros((c["heads_q"], s["rows"][0]), dtype=torch.float64, device="cuda")
+    before = [t.tolist() for t in s["before"]]
+    for d in range(c["docs"]):
+        q0, nq, k0, nk = s["q_starts"][d], s["fresh"][d], s["k_starts"][d], s["keys"][d]
+        rows = torch.cat((torch.arange(before[0][d], before[0][d] + before[1][d], device="cuda"),
+                          torch.arange(k0, k0 + nk, device="cuda")))
+        away = (torch.arange(nq, device="cuda") + len(rows) - nq)[:, None] - \
+            torch.arange(len(rows), device="cuda")[None, :]
+        for h in range(c["heads_k"]):
+            k, v = (_exact_held(t, rows, h, c["bits"], c["dim"]) for t in (s["kc"], s["vc"]))
+            for g in range(h * group, (h + 1) * group):
+                x = (s["q"][q0:q0 + nq, g].double() @ k.T) * s["scale"]
+                if c["softcap"]:
+                    x = c["softcap"] * torch.tanh(x / c["softcap"])
+                if s["slopes"] is not None:
+                    x = x - float(s["slopes"][g]) * away.abs().double()
+                x = x.masked_fill(away < 0, float("-inf"))
+                y = torch.logsumexp(x, -1)
+                lse[g, q0:q0 + nq] = y
+                o[q0:q0 + nq, g] = torch.exp(x - y[:, None]) @ v
+    return [o, lse]
