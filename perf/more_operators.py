@@ -351,12 +351,12 @@ def _own_attention(s):
 # The plain forms, in 32 bits
 # ---------------------------------------------------------------------------
 def _plain_linear(s):
-    # codes are formed in 64 bits: in 32 a value next to the border of two codes
-    # would go to the wrong one
+    # codes are formed in 64 bits, the division last: in 32 a value next to the
+    # border of two codes would go to the wrong one
     x = s["x"].double()
     top = x.abs().amax(1, keepdim=True)
     none = top < LEAST
-    u = torch.round(x * torch.where(none, 0.0, 127.0 / top)).float()
+    u = torch.where(none, 0.0, torch.round(x * 127.0 / top)).float()
     scale = torch.where(none, 0.0, top / 127.0).float()
     y = torch.matmul(u, s["w"].float().T) * (scale * s["ws"])
     if s["bias"] is not None:
@@ -371,7 +371,8 @@ def _quantised(x, bits):
     lo, hi = x.amin(-1), x.amax(-1)
     span, most = hi - lo, 2.0 ** bits - 1.0
     none = span < LEAST
-    u = torch.round((x - lo[..., None]) * torch.where(none, 0.0, most / span)[..., None])
+    u = torch.round((x - lo[..., None]) * most / span[..., None])
+    u = torch.where(none[..., None], 0.0, u)
     return u, lo.float(), torch.where(none, 0.0, span / most).float()
 
 
@@ -471,7 +472,7 @@ def exact(case, seed):
 def _exact_linear(s):
     x = s["x"].double()
     top = x.abs().max(1).values[:, None]
-    codes = torch.round(x * (127.0 / top.clamp(min=1e-300)))
+    codes = torch.round(127.0 * x / top.clamp(min=1e-300))
     y = torch.einsum("mk,nk->mn", codes, s["w"].double()) * (top / 127.0) * s["ws"].double()
     return y if s["bias"] is None else y + s["bias"].double()
 
@@ -505,7 +506,7 @@ def _exact_cache(s):
         x = x.double()
         low, high = x.min(-1, keepdim=True).values, x.max(-1, keepdim=True).values
         levels = 2 ** c["bits"] - 1
-        codes = torch.round((x - low) * (levels / (high - low).clamp(min=1e-300)))
+        codes = torch.round(levels * (x - low) / (high - low).clamp(min=1e-300))
         written = low + (high - low) / levels * codes
         at = 0
         for q0, nq, k0, nk in zip(s["q_starts"], s["fresh"], s["k_starts"], s["keys"]):
