@@ -23,7 +23,8 @@ LIB = os.path.join(HERE, "libgsraster.so")
 # sha256 of the sources and flags a library was built from, written beside it
 HASH_FILE = LIB + ".srchash"
 SOURCES = ["project.hip", "binsort.hip", "raster.hip", "densify.hip", "train.hip",
-           "qkrope.hip", "attention.hip", "gated.hip", "api.hip"]
+           "qkrope.hip", "attention.hip", "gated.hip", "linear8.hip",
+           "api.hip"]
 ARCH = "gfx950"
 
 

@@ -112,6 +112,13 @@ hipError_t gs_launch_gated_bwd(const gs_scan_config& cfg, const gs_documents& d,
                               const gs_rows& dy, const float* dstate_out, const gs_rows& dgate,
                               const gs_rows& dx, float* dstate_in, void* workspace,
                               hipStream_t s);
+hipError_t gs_launch_quantize_rows(int32_t dtype, int64_t rows, int64_t channels,
+                                   const gs_rows& x, int8_t* codes, float* scales,
+                                   hipStream_t s);
+size_t gs_linear_i8_bytes(const gs_linear_config& cfg, int64_t rows);
+hipError_t gs_launch_linear_i8(const gs_linear_config& cfg, int64_t rows, const gs_rows& x,
+                               const int8_t* w, const float* w_scale, const float* bias,
+                               const gs_rows& y, void* workspace, hipStream_t s);
 }
 
 namespace {
@@ -1092,6 +1099,7 @@ namespace {
 constexpr int64_t kMaxStride = (int64_t)1 << 28;
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 gs_status check_stride(int64_t stride) {
   GS_REQUIRE(stride >= 0 && stride <= kMaxStride, "strides must be in [0, 2^28]");
@@ -1469,6 +1477,67 @@ gs_status gs_gated_scan_bwd(const gs_scan_config* cfg, const gs_documents* docs,
                                        rows > 0 ? *dL_dgate : none, rows > 0 ? *dL_dx : none,
                                        dL_dstate_in, workspace, (hipStream_t)stream),
                     "gs_gated_scan_bwd");
+}
+
+// ---------------------------------------------------------------------------
+// Serving in 8 and 4 bits
+// ---------------------------------------------------------------------------
+namespace {
+
+gs_status check_codes_of_rows(int32_t dtype, int64_t rows, int64_t channels) {
+  GS_REQUIRE(dtype >= GS_F32 && dtype <= GS_F16, "dtype must be a gs_dtype");
+  // sums of 131,056 products of 128 by 128 stay inside 32 bits
+  GS_REQUIRE(channels >= 16 && channels <= 131056 && channels % 16 == 0,
+             "channels must be a multiple of 16 in [16, 131056]");
+  return check_token_rows(rows, 1);
+}
+
+gs_status check_linear(const gs_linear_config* c, int64_t rows) {
+  GS_REQUIRE(c != nullptr, "cfg is NULL");
+  GS_CHECK(check_codes_of_rows(c->dtype, rows, c->inputs));
+  GS_REQUIRE(c->outputs >= 8 && c->outputs <= 1 << 24 && c->outputs % 8 == 0,
+             "outputs must be a multiple of 8 in [8, 2^24]");
+  GS_REQUIRE(rows <= ((int64_t)1 << 37) / c->outputs, "rows times outputs must be <= 2^37");
+  return GS_OK;
+}
+
+}  // namespace
+
+gs_status gs_quantize_rows(int32_t dtype, int64_t rows, int64_t channels, const gs_rows* x,
+                           int8_t* codes, float* scales, void* stream) {
+  GS_CHECK(check_codes_of_rows(dtype, rows, channels));
+  if (rows == 0) return GS_OK;
+  GS_CHECK(check_rows(x, rows, channels, false));
+  GS_REQUIRE(codes && scales, "codes or scales is NULL");
+  GS_REQUIRE(aligned16(codes) && aligned4(scales), "codes must be 16-byte aligned, scales 4");
+  GS_REQUIRE((const void*)codes != x->data && (const void*)scales != x->data,
+             "outputs must not alias the input");
+  return hip_status(gs_launch_quantize_rows(dtype, rows, channels, *x, codes, scales,
+                                            (hipStream_t)stream),
+                    "gs_quantize_rows");
+}
+
+size_t gs_linear_i8_workspace_size(const gs_linear_config* cfg, int64_t rows) {
+  if (check_linear(cfg, rows) != GS_OK) return 0;
+  return gs_linear_i8_bytes(*cfg, rows);
+}
+
+gs_status gs_linear_i8(const gs_linear_config* cfg, int64_t rows, const gs_rows* x,
+                       const int8_t* weight, const float* weight_scale, const float* bias,
+                       const gs_rows* y, void* workspace, size_t workspace_bytes, void* stream) {
+  GS_CHECK(check_linear(cfg, rows));
+  if (rows == 0) return GS_OK;
+  GS_CHECK(check_rows(x, rows, cfg->inputs, false));
+  GS_CHECK(check_rows(y, rows, cfg->outputs, true));
+  GS_REQUIRE(weight && weight_scale, "weight or weight_scale is NULL");
+  GS_REQUIRE(aligned16(weight) && aligned4(weight_scale) && aligned4(bias),
+             "weight must be 16-byte aligned, scales and bias 4");
+  const void* in[4] = {x->data, weight, weight_scale, bias};
+  for (const void* p : in) GS_REQUIRE(y->data != p, "y must not alias the inputs");
+  GS_CHECK(check_workspace(workspace, workspace_bytes, gs_linear_i8_bytes(*cfg, rows)));
+  return hip_status(gs_launch_linear_i8(*cfg, rows, *x, weight, weight_scale, bias, *y, workspace,
+                                        (hipStream_t)stream),
+                    "gs_linear_i8");
 }
 
 }  // extern "C"

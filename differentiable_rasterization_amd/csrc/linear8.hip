@@ -1,0 +1,396 @@
+// linear8.hip — rows brought to 8 bits, and products of them with 8-bit
+// weights.
+//
+//   scale_i = max_k |x_ik| / 127,  u_ik = rint(127 x_ik / max),
+//   y_ij = (sum_k u_ik w_jk) (scale_i wscale_j) + bias_j.
+//
+// The sums are whole numbers in 32 bits, so no order of them changes a result.
+// Codes are formed in 64 bits: the fp32 product would put a value next to the
+// border of two codes into either.
+#include "tokens.h"
+
+namespace gs {
+
+struct LinearArgs {
+  int64_t rows;
+  int inputs, outputs;
+  const int8_t* u;       // [rows][inputs]
+  const float* u_scale;  // [rows]
+  const int8_t* w;       // [outputs][inputs]
+  const float* w_scale;  // [outputs]
+  const float* bias;     // [outputs] or NULL
+  void* y;
+  int64_t y_row;
+  uint32_t tiles_n;  // tiles over the outputs
+  uint32_t tiles;
+};
+
+// Eight elements of any type.
+template <typename T>
+__device__ inline void load8(const T* p, float (&v)[8]) {
+  load_elems(p, v);
+}
+
+// kLanes lanes a row; each keeps up to kKeep pieces of eight elements in
+// registers between the maximum and the codes and reads the others again.
+template <typename T, int kLanes>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int channels, const T* x,
+                                                            int64_t x_row, int8_t* codes,
+                                                            float* scales, uint32_t block0) {
+  constexpr int kKeep = 4;
+  __shared__ float s_top[4];
+  const int64_t row = (int64_t)(block0 + blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
+  const int at = (threadIdx.x % kLanes) * 8;
+  const bool here = row < rows;
+  const T* in = x + (here ? row : 0) * x_row;
+  float kept[kKeep][8];
+  float top = 0.0f;
+  bool bad = false;
+  auto look = [&](const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      top = fmaxf(top, fabsf(v[i]));
+      bad = bad || !(fabsf(v[i]) < __builtin_huge_valf());
+    }
+  };
+#pragma unroll
+  for (int p = 0; p < kKeep; ++p) {
+    const int e = at + p * kLanes * 8;
+    if (here && e < channels) {
+      load8(in + e, kept[p]);
+      look(kept[p]);
+    }
+  }
+  for (int e = at + kKeep * kLanes * 8; here && e < channels; e += kLanes * 8) {
+    float v[8];
+    load8(in + e, v);
+    look(v);
+  }
+  if (bad) top = __builtin_huge_valf();
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  if constexpr (kLanes == 256) {
+    if ((threadIdx.x & 63) == 0) s_top[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+  }
+  if (!here) return;
+  // a row with an infinity or a NaN has no codes: its scale is NaN, and so is
+  // all that comes of it
+  const bool none = !(top >= kLeastSpan), wrong = !(top < __builtin_huge_valf());
+  const double inv = none || wrong ? 0.0 : 127.0 / (double)top;
+  if (threadIdx.x % kLanes == 0)
+    scales[row] = wrong ? __builtin_nanf("") : none ? 0.0f : (float)((double)top / 127.0);
+  int8_t* out = codes + row * channels;
+  auto put = [&](int e, const float (&v)[8]) {
+    uint32_t w[2] = {0, 0};
+    if (!wrong) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)(code_of(v[i], inv) & 255) << (8 * (i & 3));
+    }
+    *(u32x2*)(out + e) = u32x2{w[0], w[1]};
+  };
+#pragma unroll
+  for (int p = 0; p < kKeep; ++p) {
+    const int e = at + p * kLanes * 8;
+    if (e < channels) put(e, kept[p]);
+  }
+  for (int e = at + kKeep * kLanes * 8; e < channels; e += kLanes * 8) {
+    float v[8];
+    load8(in + e, v);
+    put(e, v);
+  }
+}
+
+template <typename T>
+__device__ inline void store4(T* p, const float (&v)[4]) {
+  store_elems(p, v);
+}
+
+// Few rows: the product is the reading of the weights.  A workgroup has 16
+// outputs, its wavefronts a share of the inputs each; weights and codes go from
+// memory straight into the operands of the 16x16x64 instruction (rows lane %
+// 16, 16 inputs a lane), and the wavefronts' sums meet in LDS.
+constexpr int kFewWaves = 8;
+template <typename T, int kTiles>
+__global__ void __launch_bounds__(kFewWaves * 64) linear_few_kernel(LinearArgs a) {
+  __shared__ i32x4 s_sum[kFewWaves][kTiles][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n0 = blockIdx.x * 16;
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * kTiles);
+  const int steps = (a.inputs + 63) / 64;
+  const int share = (steps + kFewWaves - 1) / kFewWaves;
+  const int first = wave * share, last = min(steps, first + share);
+  const int part = 16 * (lane >> 4);
+  // rows past the end repeat the last one; what comes of them is not stored
+  const int8_t* w = a.w + (int64_t)min(n0 + (lane & 15), a.outputs - 1) * a.inputs + part;
+  const int8_t* u[kTiles];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) {
+    const int64_t m = m0 + 16 * t + (lane & 15);
+    u[t] = a.u + (m < a.rows ? m : a.rows - 1) * a.inputs + part;
+  }
+  i32x4 sum[kTiles];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) sum[t] = i32x4{0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = first; s < last; ++s) {
+    const bool in = 64 * s + part < a.inputs;  // inputs are a multiple of 16
+    i32x4 x = {0, 0, 0, 0};
+    if (in) x = *(const i32x4*)(w + 64 * s);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      i32x4 y = {0, 0, 0, 0};
+      if (in) y = *(const i32x4*)(u[t] + 64 * s);
+      sum[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x, y, sum[t], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t) s_sum[wave][t][lane] = sum[t];
+  __syncthreads();
+  for (int t = wave; t < kTiles; t += kFewWaves) {
+    i32x4 all = s_sum[0][t][lane];
+#pragma unroll
+    for (int i = 1; i < kFewWaves; ++i) all += s_sum[i][t][lane];
+    const int64_t m = m0 + 16 * t + (lane & 15);
+    const int n = n0 + 4 * (lane >> 4);
+    if (m >= a.rows || n >= a.outputs) continue;
+    const float scale = a.u_scale[m];
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = (float)all[i] * (scale * a.w_scale[n + i]);
+      if (a.bias) v[i] += a.bias[n + i];
+    }
+    store4((T*)a.y + m * a.y_row + n, v);
+  }
+}
+
+// Place in a staged tile of 128-byte rows: 16-byte chunk c of row r stands at
+// chunk c ^ turn(r).  Outputs are read in the order 0..3, 16..19, 4..7, 20..23
+// ..., rows in their own: eight rows read together have eight different turns,
+// so that they fall on all the banks.
+template <bool kOutputs>
+__device__ inline int turn(int r) {
+  return kOutputs ? (r & 3) | ((r >> 2) & 4) : r & 7;
+}
+
+// Copies kRows rows of 128 bytes from column k on into LDS, without passing
+// through registers.  at: each lane's source offsets, of row and chunk.
+template <int kRows, int kWaves, bool kOutputs>
+struct Stage {
+  static constexpr int kCopies = kRows / 8 / kWaves;
+  uint32_t at[kCopies];
+  int chunk[kCopies];
+  __device__ inline void start(int inputs) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      const int r = (i * kWaves + wave) * 8 + (lane >> 3);
+      chunk[i] = ((lane & 7) ^ turn<kOutputs>(r)) * 16;
+      at[i] = (uint32_t)(r * inputs + chunk[i]);
+    }
+  }
+  __device__ inline void copy(const i32x4& rsrc, uint32_t lds, int k, int inputs) {
+    const int wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      // chunks past the row's end arrive as zeros
+      const uint32_t from = k + chunk[i] < inputs ? at[i] + (uint32_t)k : 0x80000000u;
+      const uint32_t to = __builtin_amdgcn_readfirstlane(lds + (i * kWaves + wave) * 1024);
+      asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(
+                       from),
+                   "s"(rsrc), "s"(to)
+                   : "memory", "m0");
+    }
+  }
+};
+
+__device__ inline i32x4 rows_from(const int8_t* base, int64_t bytes) {
+  const uint64_t address = (uint64_t)base;
+  return i32x4{(int)__builtin_amdgcn_readfirstlane((uint32_t)address),
+               (int)__builtin_amdgcn_readfirstlane((uint32_t)(address >> 32) & 0xffff),
+               (int)__builtin_amdgcn_readfirstlane((uint32_t)bytes), 0x00027000};
+}
+
+// Many rows: tiles of kM rows by kN outputs, kWm by kWn wavefronts of 32x32x32
+// products, 128 inputs a step, two tiles in LDS: while one is multiplied the
+// next is copied in.
+template <typename T, int kM, int kN, int kWm, int kWn>
+__global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a) {
+  constexpr int kWaves = kWm * kWn;
+  constexpr int kTm = kM / kWm / 32, kTn = kN / kWn / 32;
+  constexpr int kBytes = (kM + kN) * 128;
+  __shared__ __align__(1024) char s_mem[2 * kBytes];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // Workgroups go to the eight XCDs in turn; each XCD takes a run of tiles, in
+  // blocks of eight tiles of rows, so that its L2 holds what they share.
+  const uint32_t each = (a.tiles + 7) / 8;
+  const uint32_t tile = (blockIdx.x & 7) * each + (blockIdx.x >> 3);
+  if ((blockIdx.x >> 3) >= each || tile >= a.tiles) return;
+  const uint32_t tiles_m = a.tiles / a.tiles_n, block = tile / (8 * a.tiles_n);
+  const uint32_t tall = min(8u, tiles_m - block * 8);
+  const uint32_t in_block = tile - block * 8 * a.tiles_n;
+  const int64_t m0 = (int64_t)(block * 8 + in_block % tall) * kM;
+  const int n0 = (int)(in_block / tall) * kN;
+  const int64_t rows = min(a.rows - m0, (int64_t)kM);
+  const int outputs = min(a.outputs - n0, kN);
+  const i32x4 from_u = rows_from(a.u + m0 * a.inputs, rows * a.inputs);
+  const i32x4 from_w = rows_from(a.w + (int64_t)n0 * a.inputs, (int64_t)outputs * a.inputs);
+  const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)s_mem;
+  Stage<kM, kWaves, false> stage_u;
+  Stage<kN, kWaves, true> stage_w;
+  stage_u.start(a.inputs);
+  stage_w.start(a.inputs);
+  auto copy = [&](int k, int buffer) {
+    stage_u.copy(from_u, lds + buffer * kBytes, k, a.inputs);
+    stage_w.copy(from_w, lds + buffer * kBytes + kM * 128, k, a.inputs);
+  };
+  // operand rows of this lane: its output row m of a 32-row product is such that
+  // the sixteen results it gets are sixteen outputs side by side
+  const int r32 = lane & 31, half = lane >> 5;
+  const int wr = 16 * ((r32 >> 2) & 1) + 4 * (r32 >> 3) + (r32 & 3);
+  const int wave_m = (wave % kWm) * (kM / kWm), wave_n = (wave / kWm) * (kN / kWn);
+  const int at_u = (wave_m + r32) * 128 + ((half ^ turn<false>(r32)) << 4);
+  const int at_w = kM * 128 + (wave_n + wr) * 128 + ((half ^ turn<true>(wr)) << 4);
+  i32x16 sum[kTn][kTm];
+#pragma unroll
+  for (int i = 0; i < kTn; ++i)
+#pragma unroll
+    for (int j = 0; j < kTm; ++j) sum[i][j] = (i32x16)(0);
+  const int steps = (a.inputs + 127) / 128;
+  copy(0, 0);
+  for (int s = 0; s < steps; ++s) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (s + 1 < steps) copy((s + 1) * 128, (s + 1) & 1);
+    const char* mem = s_mem + (s & 1) * kBytes;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      i32x4 w[kTn], u[kTm];
+#pragma unroll
+      for (int i = 0; i < kTn; ++i)
+        w[i] = *(const i32x4*)(mem + (at_w ^ (ks * 32)) + i * 32 * 128);
+#pragma unroll
+      for (int j = 0; j < kTm; ++j)
+        u[j] = *(const i32x4*)(mem + (at_u ^ (ks * 32)) + j * 32 * 128);
+#pragma unroll
+      for (int i = 0; i < kTn; ++i)
+#pragma unroll
+        for (int j = 0; j < kTm; ++j)
+          sum[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[i], u[j], sum[i][j], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kTm; ++j) {
+    const int64_t m = m0 + wave_m + 32 * j + r32;
+    const float scale = m < a.rows ? a.u_scale[m] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) {
+      const int n = n0 + wave_n + 32 * i + 16 * half;
+      if (m >= a.rows) continue;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {  // outputs are a multiple of 8
+        if (n + 8 * g >= a.outputs) continue;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[e] = (float)sum[i][j][8 * g + e] * (scale * a.w_scale[n + 8 * g + e]);
+          if (a.bias) v[e] += a.bias[n + 8 * g + e];
+        }
+        store_elems((T*)a.y + m * a.y_row + n + 8 * g, v);
+      }
+    }
+  }
+}
+
+namespace {
+
+template <typename T>
+hipError_t quantize(int64_t rows, int64_t channels, const gs_rows& x, int8_t* codes,
+                    float* scales, hipStream_t s) {
+  // a row by a wavefront keeps its elements in registers up to 2,048 channels
+  if (channels <= 2048)
+    return launch_all((rows + 3) / 4, 256, [&](uint32_t first, dim3 n) {
+      quantize_rows_kernel<T, 64><<<n, 256, 0, s>>>(rows, (int)channels, (const T*)x.data, x.row,
+                                                    codes, scales, first);
+    });
+  return launch_all(rows, 256, [&](uint32_t first, dim3 n) {
+    quantize_rows_kernel<T, 256><<<n, 256, 0, s>>>(rows, (int)channels, (const T*)x.data, x.row,
+                                                   codes, scales, first);
+  });
+}
+
+template <typename T, int kTiles>
+hipError_t few(const LinearArgs& a, hipStream_t s) {
+  linear_few_kernel<T, kTiles><<<dim3((a.outputs + 15) / 16,
+                                      (uint32_t)((a.rows + 16 * kTiles - 1) / (16 * kTiles))),
+                                 kFewWaves * 64, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, int kM, int kN, int kWm, int kWn>
+hipError_t many(LinearArgs a, hipStream_t s) {
+  a.tiles_n = (uint32_t)((a.outputs + kN - 1) / kN);
+  a.tiles = (uint32_t)((a.rows + kM - 1) / kM) * a.tiles_n;
+  linear_many_kernel<T, kM, kN, kWm, kWn>
+      <<<dim3((a.tiles + 7) / 8 * 8), kWm * kWn * 64, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t linear(const LinearArgs& a, hipStream_t s) {
+  if (a.rows <= 16) return few<T, 1>(a, s);
+  if (a.rows <= 32) return few<T, 2>(a, s);
+  if (a.rows <= 64) return few<T, 4>(a, s);
+  const int64_t large = ((a.rows + 255) / 256) * ((a.outputs + 255) / 256);
+  if (large >= 256) return many<T, 256, 256, 2, 4>(a, s);
+  return many<T, 128, 128, 2, 2>(a, s);
+}
+
+size_t codes_bytes(int64_t rows, int64_t channels) {
+  return ((size_t)rows * channels + 255) / 256 * 256;
+}
+
+}  // namespace
+}  // namespace gs
+
+extern "C" {
+
+size_t gs_linear_i8_bytes(const gs_linear_config& cfg, int64_t rows) {
+  return gs::codes_bytes(rows, cfg.inputs) + (size_t)rows * 4;
+}
+
+hipError_t gs_launch_quantize_rows(int32_t dtype, int64_t rows, int64_t channels,
+                                   const gs_rows& x, int8_t* codes, float* scales,
+                                   hipStream_t s) {
+  if (dtype == GS_F32) return gs::quantize<float>(rows, channels, x, codes, scales, s);
+  if (dtype == GS_BF16) return gs::quantize<gs::Bf16>(rows, channels, x, codes, scales, s);
+  return gs::quantize<gs::F16>(rows, channels, x, codes, scales, s);
+}
+
+hipError_t gs_launch_linear_i8(const gs_linear_config& cfg, int64_t rows, const gs_rows& x,
+                               const int8_t* w, const float* w_scale, const float* bias,
+                               const gs_rows& y, void* workspace, hipStream_t s) {
+  int8_t* u = (int8_t*)workspace;
+  float* u_scale = (float*)(u + gs::codes_bytes(rows, cfg.inputs));
+  const hipError_t e =
+      gs_launch_quantize_rows(cfg.dtype, rows, cfg.inputs, x, u, u_scale, s);
+  if (e != hipSuccess) return e;
+  gs::LinearArgs a = {};
+  a.rows = rows;
+  a.inputs = (int)cfg.inputs;
+  a.outputs = (int)cfg.outputs;
+  a.u = u;
+  a.u_scale = u_scale;
+  a.w = w;
+  a.w_scale = w_scale;
+  a.bias = bias;
+  a.y = y.data;
+  a.y_row = y.row;
+  if (cfg.dtype == GS_F32) return gs::linear<float>(a, s);
+  if (cfg.dtype == GS_BF16) return gs::linear<gs::Bf16>(a, s);
+  return gs::linear<gs::F16>(a, s);
+}
+
+}  // extern "C"

@@ -13,6 +13,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -205,6 +206,20 @@ template <typename T>
 __device__ inline uint32_t pack2(float a, float b) {
   if constexpr (__is_same(T, Bf16)) return pack_bf16(a, b);
   else return pack_f16(a, b);
+}
+
+// Spans and magnitudes below this count as none: their scale would leave the
+// normal numbers of fp32.
+constexpr float kLeastSpan = 0x1p-116f;
+
+// The whole number next to x times inv (at most 255), to even at a tie, where
+// inv is a quotient levels / span.  The product is off by 2^-45 at most, while
+// levels x / span of 24-bit x and span of like exponents is a tie or 2^-33 away
+// from one: rounded to multiples of 2^-36 first (adding and taking away 1.5
+// 2^16), ties are ties.  Adding 1.5 2^52 leaves the whole number in the low word.
+__device__ inline int code_of(double x, double inv) {
+  const double v = (x * inv + 0x1.8p16) - 0x1.8p16;
+  return (int)(uint32_t)__builtin_bit_cast(uint64_t, v + 0x1.8p52);
 }
 
 template <int W>

@@ -39,7 +39,8 @@ EXPORTED = ("gs_default_settings", "gs_status_string", "gs_last_error", "gs_num_
             "gs_attention_fwd_workspace_size", "gs_attention_fwd",
             "gs_attention_bwd_workspace_size", "gs_attention_bwd", "gs_gated_scan_saved_size",
             "gs_gated_scan_fwd_workspace_size", "gs_gated_scan_fwd",
-            "gs_gated_scan_bwd_workspace_size", "gs_gated_scan_bwd")
+            "gs_gated_scan_bwd_workspace_size", "gs_gated_scan_bwd", "gs_quantize_rows",
+            "gs_linear_i8_workspace_size", "gs_linear_i8")
 GS_F32, GS_BF16, GS_F16 = 0, 1, 2
 
 
@@ -97,6 +98,10 @@ class gs_attention_config(C.Structure):
 
 class gs_scan_config(C.Structure):
     _fields_ = [("dtype", C.c_int32), ("coupled", C.c_int32), ("channels", C.c_int64)]
+
+
+class gs_linear_config(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("inputs", C.c_int64), ("outputs", C.c_int64)]
 
 
 def load():
@@ -222,6 +227,12 @@ def load():
     lib.gs_gated_scan_fwd.argtypes = [P, P, i64] + [P] * 6 + [P, SZ, P]
     lib.gs_gated_scan_bwd.restype = C.c_int
     lib.gs_gated_scan_bwd.argtypes = [P, P, i64] + [P] * 8 + [P, SZ, P]
+    lib.gs_quantize_rows.restype = C.c_int
+    lib.gs_quantize_rows.argtypes = [i32, i64, i64, P, P, P, P]
+    lib.gs_linear_i8_workspace_size.restype = SZ
+    lib.gs_linear_i8_workspace_size.argtypes = [P, i64]
+    lib.gs_linear_i8.restype = C.c_int
+    lib.gs_linear_i8.argtypes = [P, i64] + [P] * 5 + [P, SZ, P]
     _name_types()
     _lib = lib
     return lib
@@ -654,14 +665,14 @@ def gs_densify_prune(N, ld, sh_degree, means, scales, quats, opacities, sh, dL_d
 # Token operators
 # ---------------------------------------------------------------------------
 _kinds = {}            # torch dtype: gs_dtype
-_F32 = _I32 = None     # torch.float32, torch.int32 (torch is imported on first use)
+_F32 = _I32 = _I8 = None  # torch.float32, int32, int8 (torch is imported on first use)
 
 
 def _name_types():
-    global _F32, _I32
+    global _F32, _I32, _I8
     if not _kinds:
         import torch
-        _F32, _I32 = torch.float32, torch.int32
+        _F32, _I32, _I8 = torch.float32, torch.int32, torch.int8
         _kinds.update({torch.float32: GS_F32, torch.bfloat16: GS_BF16, torch.float16: GS_F16})
 
 
@@ -910,6 +921,37 @@ def gs_gated_scan_bwd(cfg, docs, rows, gate, x, saved, dL_dy, dL_dstate_out, dL_
         _saved(cfg, docs, rows, saved), _where(dL_dy), _at(dL_dstate_out, _F32, states),
         _where(dL_dgate), _where(dL_dx), _at(dL_dstate_in, _F32, states),
         _bytes(workspace, workspace_bytes), int(workspace_bytes), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Serving in 8 and 4 bits
+# ---------------------------------------------------------------------------
+def linear_config(dtype, inputs, outputs) -> gs_linear_config:
+    """dtype: a torch dtype, of x and y."""
+    return gs_linear_config(_dtype(dtype), int(inputs), int(outputs))
+
+
+def gs_quantize_rows(dtype, rows, channels, x, codes, scales, stream=None):
+    """dtype: a torch dtype; codes: int8 [rows, channels], scales: fp32 [rows]."""
+    kind = _dtype(dtype)
+    x = _rows(x, (kind, rows, channels))
+    _check(load().gs_quantize_rows(kind, rows, channels, _where(x), _at(codes, _I8, rows * channels),
+                                   _at(scales, _F32, rows), _stream(stream)))
+
+
+def gs_linear_i8_workspace_size(cfg, rows) -> int:
+    return int(load().gs_linear_i8_workspace_size(C.byref(cfg), rows))
+
+
+def gs_linear_i8(cfg, rows, x, weight, weight_scale, bias, y, workspace, workspace_bytes,
+                 stream=None):
+    """weight: int8 [outputs, inputs], weight_scale: fp32 [outputs], bias: the same or None."""
+    kind, k, n = cfg.dtype, cfg.inputs, cfg.outputs
+    x, y = _rows(x, (kind, rows, k)), _rows(y, (kind, rows, n))
+    _check(load().gs_linear_i8(
+        C.byref(cfg), rows, _where(x), _at(weight, _I8, n * k), _at(weight_scale, _F32, n),
+        _at(bias, _F32, n), _where(y), _bytes(workspace, workspace_bytes), int(workspace_bytes),
+        _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -822,6 +822,40 @@ GS_API gs_status gs_gated_scan_bwd(const gs_scan_config* cfg, const gs_documents
                                    const gs_rows* dL_dx, float* dL_dstate_in, void* workspace,
                                    size_t workspace_bytes, void* stream);
 
+/* Serving in 8 and 4 bits: a network that answers a few tokens at a time reads
+ * little but its weights and its caches.  These calls keep both small; they
+ * have no gradients.  The conventions are those of the token operators. */
+
+/* Rows brought to 8 bits: scale = max |x| / 127 of the row, code =
+ * 127 x / max |x| to the nearest whole number, to even at a tie.  codes is
+ * [rows][channels] int8, 16-byte aligned, scales [rows] fp32; channels is a
+ * multiple of 16, at most 131,056.  A row whose largest magnitude is below
+ * 2^-116 gets scale 0 and codes 0, one that holds an infinity or a NaN scale
+ * NaN and codes 0.  Weights [outputs][inputs] of gs_linear_i8 are brought to 8
+ * bits by this call once, and then kept. */
+GS_API gs_status gs_quantize_rows(int32_t dtype, int64_t rows, int64_t channels,
+                                  const gs_rows* x, int8_t* codes, float* scales, void* stream);
+
+/* Products with 8-bit weights: x [rows][inputs] is brought to 8 bits row by row
+ * as above, with scale_i and codes u, and
+ *   y_ij = (sum_k u_ik weight_jk) (scale_i weight_scale_j) + bias_j,
+ * the sum in 32-bit integers (exact), the rest in fp32, y rounded once.  weight
+ * is [outputs][inputs] int8, 16-byte aligned; weight_scale and bias (NULL: none)
+ * are [outputs] fp32.  inputs is a multiple of 16, at most 131,056, outputs a
+ * multiple of 8, at most 2^24, rows times outputs at most 2^37.  A row of x that
+ * holds an infinity or a NaN gives NaN, and reaches no other row.  workspace:
+ * 256-byte aligned, of gs_linear_i8_workspace_size() bytes. */
+typedef struct {
+  int32_t dtype; /* gs_dtype of x and y */
+  int64_t inputs, outputs;
+} gs_linear_config;
+
+GS_API size_t gs_linear_i8_workspace_size(const gs_linear_config* cfg, int64_t rows);
+GS_API gs_status gs_linear_i8(const gs_linear_config* cfg, int64_t rows, const gs_rows* x,
+                              const int8_t* weight, const float* weight_scale, const float* bias,
+                              const gs_rows* y, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 #ifdef __cplusplus
 }
 #endif
