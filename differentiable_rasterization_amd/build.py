@@ -24,7 +24,7 @@ LIB = os.path.join(HERE, "libgsraster.so")
 HASH_FILE = LIB + ".srchash"
 SOURCES = ["project.hip", "binsort.hip", "raster.hip", "densify.hip", "train.hip",
            "qkrope.hip", "attention.hip", "gated.hip", "linear8.hip",
-           "api.hip"]
+           "cache.hip", "cached.hip", "api.hip"]
 ARCH = "gfx950"
 
 

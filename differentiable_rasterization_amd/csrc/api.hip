@@ -119,6 +119,19 @@ size_t gs_linear_i8_bytes(const gs_linear_config& cfg, int64_t rows);
 hipError_t gs_launch_linear_i8(const gs_linear_config& cfg, int64_t rows, const gs_rows& x,
                                const int8_t* w, const float* w_scale, const float* bias,
                                const gs_rows& y, void* workspace, hipStream_t s);
+hipError_t gs_launch_cache_write(const gs_cache_config& cfg, const gs_documents& d, int64_t rows_q,
+                                 int64_t rows_k, const gs_heads& k, const gs_heads& v,
+                                 const gs_codes& kc, const gs_codes& vc, hipStream_t s);
+hipError_t gs_launch_cache_read(const gs_cache_config& cfg, const gs_documents& d, int64_t rows_q,
+                                int64_t rows_k, const gs_codes& kc, const gs_codes& vc,
+                                const gs_heads& k, const gs_heads& v, hipStream_t s);
+size_t gs_cached_attention_bytes(const gs_attention_config& cfg, const gs_documents& d,
+                                 const gs_documents* shared, int64_t rows_q, int64_t rows_k);
+hipError_t gs_launch_cached_attention(const gs_attention_config& cfg, const gs_documents& d,
+                                      const gs_documents* shared, int64_t rows_q, int64_t rows_k,
+                                      const gs_heads& q, const gs_codes& k, const gs_codes& v,
+                                      const gs_heads& out, float* lse, void* workspace,
+                                      hipStream_t s);
 }
 
 namespace {
@@ -1501,6 +1514,84 @@ gs_status check_linear(const gs_linear_config* c, int64_t rows) {
   return GS_OK;
 }
 
+gs_status check_codes_dim(int64_t dim) {
+  GS_REQUIRE(dim >= 16 && dim <= 128 && dim % 16 == 0,
+             "head_dim must be a multiple of 16 in [16, 128]");
+  return GS_OK;
+}
+
+gs_status check_bits(int32_t bits) {
+  GS_REQUIRE(bits == 8 || bits == 4, "bits must be 8 or 4");
+  return GS_OK;
+}
+
+gs_status check_codes(const gs_codes* t, int64_t rows, int64_t heads, int64_t dim) {
+  GS_REQUIRE(t != nullptr, "a cache is NULL");
+  GS_CHECK(check_bits(t->bits));
+  if (rows == 0) return GS_OK;
+  GS_REQUIRE(t->codes && t->low && t->step, "NULL array pointer in a cache");
+  GS_REQUIRE(aligned16(t->codes), "codes must be 16-byte aligned");
+  GS_REQUIRE(aligned4(t->low) && aligned4(t->step), "low and step must be 4-byte aligned");
+  GS_REQUIRE(t->low != t->step && t->codes != t->low && t->codes != t->step,
+             "the arrays of a cache must not alias");
+  GS_REQUIRE(t->row >= 0 && t->head >= 0 && t->row % 4 == 0 && t->head % 4 == 0,
+             "strides of codes must be multiples of 4 bytes");
+  // rows of a tile are reached with 32-bit byte offsets
+  GS_REQUIRE(t->row < (int64_t)1 << 25 && t->head <= (int64_t)1 << 40,
+             "row strides of codes must be below 2^25, head strides up to 2^40");
+  const int64_t bytes = dim * t->bits / 8;
+  GS_REQUIRE(t->row >= bytes, "rows of codes overlap");
+  GS_REQUIRE(heads == 1 || (t->head >= bytes && t->row >= (heads - 1) * t->head + bytes) ||
+                 t->head >= (rows - 1) * t->row + bytes,
+             "rows or heads of codes overlap");
+  GS_REQUIRE(t->ld >= rows && t->ld <= (int64_t)1 << 40, "ld must be at least the rows");
+  return GS_OK;
+}
+
+// Two caches that are used together.
+gs_status check_caches(const gs_codes* k, const gs_codes* v, int64_t rows, int64_t heads,
+                       int64_t dim) {
+  GS_CHECK(check_codes(k, rows, heads, dim));
+  GS_CHECK(check_codes(v, rows, heads, dim));
+  GS_REQUIRE(k->bits == v->bits, "bits of both caches must be alike");
+  return GS_OK;
+}
+
+gs_status check_cache(const gs_cache_config* c, const gs_documents* d, int64_t rows_q,
+                      int64_t rows_k) {
+  GS_REQUIRE(c != nullptr, "cfg is NULL");
+  GS_REQUIRE(c->dtype >= GS_F32 && c->dtype <= GS_F16, "dtype must be a gs_dtype");
+  GS_REQUIRE(c->heads >= 1 && c->heads <= 65536, "heads must be in [1, 65536]");
+  GS_CHECK(check_codes_dim(c->head_dim));
+  GS_CHECK(check_documents(d, true));
+  GS_CHECK(check_searched(d, true));
+  GS_CHECK(check_token_rows(rows_q, c->heads));
+  return check_token_rows(rows_k, c->heads);
+}
+
+// Whether an array of a cache is one of the tokens'.
+gs_status check_apart(const gs_codes* c, const gs_heads* t) {
+  GS_REQUIRE(t->data != c->codes && t->data != c->low && t->data != c->step,
+             "a cache must not alias the tokens");
+  return GS_OK;
+}
+
+gs_status check_cached(const gs_attention_config* c, int32_t bits, const gs_documents* d,
+                       const gs_documents* shared, int64_t rows_q, int64_t rows_k) {
+  GS_CHECK(check_attention(c, d, rows_q, rows_k));
+  GS_CHECK(check_codes_dim(c->head_dim));
+  GS_CHECK(check_bits(bits));
+  GS_CHECK(check_searched(d, true));
+  if (shared == nullptr) return GS_OK;
+  GS_CHECK(check_documents(shared, true));
+  GS_CHECK(check_searched(shared, true));
+  GS_REQUIRE((int64_t)shared->count * c->heads_q <= (int64_t)1 << 26,
+             "shared documents times heads must be <= 2^26");
+  GS_REQUIRE(shared->count == 0 || shared->k_start, "shared documents need key ranges");
+  GS_REQUIRE(shared->count == 0 || !c->slopes, "slopes need shared = NULL");
+  return GS_OK;
+}
+
 }  // namespace
 
 gs_status gs_quantize_rows(int32_t dtype, int64_t rows, int64_t channels, const gs_rows* x,
@@ -1538,6 +1629,72 @@ gs_status gs_linear_i8(const gs_linear_config* cfg, int64_t rows, const gs_rows*
   return hip_status(gs_launch_linear_i8(*cfg, rows, *x, weight, weight_scale, bias, *y, workspace,
                                         (hipStream_t)stream),
                     "gs_linear_i8");
+}
+
+gs_status gs_cache_write(const gs_cache_config* cfg, const gs_documents* docs, int64_t rows_q,
+                         int64_t rows_k, const gs_heads* k, const gs_heads* v,
+                         const gs_codes* k_cache, const gs_codes* v_cache, void* stream) {
+  GS_CHECK(check_cache(cfg, docs, rows_q, rows_k));
+  GS_CHECK(check_caches(k_cache, v_cache, rows_k, cfg->heads, cfg->head_dim));
+  if (docs->count == 0 || rows_q == 0 || rows_k == 0) return GS_OK;
+  GS_CHECK(check_heads(k, rows_q, cfg->heads, cfg->head_dim, false));
+  GS_CHECK(check_heads(v, rows_q, cfg->heads, cfg->head_dim, false));
+  for (const gs_codes* c : {k_cache, v_cache})
+    for (const gs_heads* t : {k, v}) GS_CHECK(check_apart(c, t));
+  for (const void* a : {(const void*)k_cache->codes, (const void*)k_cache->low,
+                        (const void*)k_cache->step})
+    GS_REQUIRE(a != v_cache->codes && a != v_cache->low && a != v_cache->step,
+               "the caches must not alias each other");
+  return hip_status(gs_launch_cache_write(*cfg, *docs, rows_q, rows_k, *k, *v, *k_cache, *v_cache,
+                                          (hipStream_t)stream),
+                    "gs_cache_write");
+}
+
+gs_status gs_cache_read(const gs_cache_config* cfg, const gs_documents* docs, int64_t rows_q,
+                        int64_t rows_k, const gs_codes* k_cache, const gs_codes* v_cache,
+                        const gs_heads* k, const gs_heads* v, void* stream) {
+  GS_CHECK(check_cache(cfg, docs, rows_q, rows_k));
+  GS_CHECK(check_caches(k_cache, v_cache, rows_k, cfg->heads, cfg->head_dim));
+  if (docs->count == 0 || rows_q == 0) return GS_OK;
+  GS_CHECK(check_heads(k, rows_q, cfg->heads, cfg->head_dim, true));
+  GS_CHECK(check_heads(v, rows_q, cfg->heads, cfg->head_dim, true));
+  GS_REQUIRE(k->data != v->data, "k and v must not alias");
+  for (const gs_codes* c : {k_cache, v_cache})
+    for (const gs_heads* t : {k, v}) GS_CHECK(check_apart(c, t));
+  return hip_status(gs_launch_cache_read(*cfg, *docs, rows_q, rows_k, *k_cache, *v_cache, *k, *v,
+                                         (hipStream_t)stream),
+                    "gs_cache_read");
+}
+
+size_t gs_cached_attention_fwd_workspace_size(const gs_attention_config* cfg, int32_t bits,
+                                              const gs_documents* docs,
+                                              const gs_documents* shared, int64_t rows_q,
+                                              int64_t rows_k) {
+  if (check_cached(cfg, bits, docs, shared, rows_q, rows_k) != GS_OK) return 0;
+  return gs_cached_attention_bytes(*cfg, *docs, shared, rows_q, rows_k);
+}
+
+gs_status gs_cached_attention_fwd(const gs_attention_config* cfg, const gs_documents* docs,
+                                  const gs_documents* shared, int64_t rows_q, int64_t rows_k,
+                                  const gs_heads* q, const gs_codes* k_cache,
+                                  const gs_codes* v_cache, const gs_heads* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  GS_REQUIRE(k_cache != nullptr, "a cache is NULL");
+  GS_CHECK(check_cached(cfg, k_cache->bits, docs, shared, rows_q, rows_k));
+  GS_CHECK(check_caches(k_cache, v_cache, rows_k, cfg->heads_k, cfg->head_dim));
+  if (docs->count == 0 || rows_q == 0) return GS_OK;
+  GS_CHECK(check_heads(q, rows_q, cfg->heads_q, cfg->head_dim, false));
+  GS_CHECK(check_heads(out, rows_q, cfg->heads_q, cfg->head_dim, true));
+  GS_REQUIRE(out->data != q->data, "out must not alias the inputs");
+  if (rows_k > 0)
+    for (const gs_codes* c : {k_cache, v_cache}) GS_CHECK(check_apart(c, out));
+  GS_REQUIRE(aligned4(lse), "lse must be 4-byte aligned");
+  GS_CHECK(check_workspace(workspace, workspace_bytes,
+                           gs_cached_attention_bytes(*cfg, *docs, shared, rows_q, rows_k)));
+  return hip_status(gs_launch_cached_attention(*cfg, *docs, shared, rows_q, rows_k, *q, *k_cache,
+                                               *v_cache, *out, lse, workspace,
+                                               (hipStream_t)stream),
+                    "gs_cached_attention_fwd");
 }
 
 }  // extern "C"

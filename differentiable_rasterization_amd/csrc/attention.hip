@@ -64,10 +64,6 @@ constexpr int kPieceKeys = 128;  // one-token form: keys the four wavefronts tak
 constexpr int kCap = 1;      // capped by tanh
 constexpr int kGeneral = 2;  // distance bias, or a scale that is not positive
 constexpr int kWide = 4;     // a cap far above most scores (with the other two)
-// Caps up to here leave a score the accuracy that fp32 has at the cap's size
-// (training, documents of 3,360 and 13,024 tokens, 16 bf16 heads of 128 over 4:
-// 4.11 ms with a cap of 64, 5.07 with one of 65).
-constexpr float kWideCap = 64.0f;
 
 template <typename T>
 struct Mat;
@@ -172,24 +168,6 @@ __device__ inline float both_sum(float x) {
   float lo, hi;
   both_halves(x, lo, hi);
   return lo + hi;
-}
-
-// tanh to fp32 accuracy of the result (absolute), any finite or infinite x.
-__device__ inline float tanh_of(float x) {
-  const float e = __builtin_amdgcn_exp2f(x * (2.0f * kLog2e));
-  return 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + e);
-}
-
-// The same with an error relative to the result, for caps that leave most
-// scores nearly as they are: a score would otherwise have an error relative to
-// its cap.  Below 1/4 the Taylor series, to 1e-8 of the result.
-__device__ inline float tanh_wide(float x) {
-  const float y = x * x;
-  float p = fmaf(y, 2.1869489e-2f, -5.3968254e-2f);
-  p = fmaf(y, p, 1.3333333e-1f);
-  p = fmaf(y, p, -3.3333333e-1f);
-  const float small = fmaf(x * y, p, x), big = tanh_of(x);
-  return fabsf(x) < 0.25f ? small : big;
 }
 
 // Token i sees the keys below this.

@@ -1,0 +1,194 @@
+// cache.hip — keys and values brought to 8 or 4 bits as they are written into a
+// cache, and read back.
+//
+// Each head of a token is x = low + step code, low its smallest element, step
+// the (2^bits - 1)-th part of its span; codes are to nearest, formed in 64 bits.
+// In 4 bits a 32-bit word holds eight elements, 2i in bits 4i and 2i + 1 in bits
+// 16 + 4i: a shift and a mask then give two elements in the halves of a word.
+//
+// Memory bound: eight elements a lane (16 bytes of a 16-bit type, 8 or 4 of
+// codes), 8 or 16 lanes a head, keys and values in one launch.
+#include "cached.h"
+
+namespace gs {
+
+struct CacheArgs {
+  Docs docs;
+  int heads, dim;
+  const void* x[2];  // keys, values
+  int64_t x_row[2], x_head[2];
+  uint8_t* codes[2];
+  float* low[2];
+  float* step[2];
+  int64_t row[2], head[2], ld[2];  // strides of codes in bytes; of low and step
+  uint32_t block0;
+};
+
+constexpr int kUnit = 16;  // tokens of a workgroup
+
+// The codes of eight elements, as they are stored.
+template <int kBits>
+__device__ inline void store_codes(uint8_t* p, const int (&u)[8]) {
+  if constexpr (kBits == 8) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w[i] = (uint32_t)(u[4 * i] | u[4 * i + 1] << 8 | u[4 * i + 2] << 16 | u[4 * i + 3] << 24);
+    *(uint32_t*)p = w[0];
+    *(uint32_t*)(p + 4) = w[1];
+  } else {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= (uint32_t)(u[2 * i] << 4 * i | u[2 * i + 1] << (16 + 4 * i));
+    *(uint32_t*)p = w;
+  }
+}
+template <int kBits>
+__device__ inline void load_codes(const uint8_t* p, int (&u)[8]) {
+  if constexpr (kBits == 8) {
+    const uint32_t w[2] = {*(const uint32_t*)p, *(const uint32_t*)(p + 4)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = (int)(w[i >> 2] >> 8 * (i & 3) & 255);
+  } else {
+    const uint32_t w = *(const uint32_t*)p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = (int)(w >> (4 * (i >> 1) + 16 * (i & 1)) & 15);
+  }
+}
+
+// The heads of a workgroup's tokens, kLanes lanes each: f(token row, row of the
+// cache or -1, head, keys or values, first element).
+template <int kLanes, typename F>
+__device__ inline void each_head(const CacheArgs& a, F f) {
+  uint32_t local, units;
+  Doc d;
+  if (find_document<false>(a.docs, 1, kUnit, a.block0 + blockIdx.x, &local, &units, &d) < 0)
+    return;
+  const int first = (int)local * kUnit, count = min(kUnit, d.ql - first);
+  const int items = count * 2 * a.heads;
+  for (int i = threadIdx.x / kLanes; i < items; i += 256 / kLanes) {
+    const int token = first + i / (2 * a.heads), which = i % (2 * a.heads);
+    // the document's last tokens are its last keys
+    const int key = token + d.kl - d.ql;
+    f(d.qs + token, key < 0 ? -1 : d.ks + key, which % a.heads, which / a.heads,
+      (int)(threadIdx.x % kLanes) * 8);
+  }
+}
+
+template <typename T, int kBits, int kLanes>
+__global__ void __launch_bounds__(256) cache_write_kernel(CacheArgs a) {
+  constexpr float kLevels = kBits == 8 ? 255.0f : 15.0f;
+  each_head<kLanes>(a, [&](int64_t token, int64_t row, int head, int kv, int e) {
+    // a lane past the head's end repeats its first elements
+    const bool mine = e < a.dim;
+    float x[8];
+    load_elems((const T*)a.x[kv] + token * a.x_row[kv] + head * a.x_head[kv] + (mine ? e : 0), x);
+    float lo = x[0], hi = x[0];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo = fminf(lo, x[i]);
+      hi = fmaxf(hi, x[i]);
+      bad = bad || x[i] != x[i];
+    }
+    if (bad) hi = __builtin_huge_valf();
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
+      lo = fminf(lo, __shfl_xor(lo, o, 64));
+      hi = fmaxf(hi, __shfl_xor(hi, o, 64));
+    }
+    if (row < 0) return;  // a token without a key
+    // a head with an infinity or a NaN, or too wide for fp32, has no codes
+    const bool wrong = !(hi - lo < 0x1p127f);
+    const double span = (double)hi - (double)lo;
+    const bool none = span < (double)kLeastSpan;
+    const double inv = none || wrong ? 0.0 : (double)kLevels / span;
+    int u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = wrong ? 0 : code_of((double)x[i] - (double)lo, inv);
+    if (mine)
+      store_codes<kBits>(a.codes[kv] + row * a.row[kv] + head * a.head[kv] + e * kBits / 8, u);
+    if (e == 0) {
+      const float nan = __builtin_nanf("");
+      a.low[kv][head * a.ld[kv] + row] = wrong ? nan : lo;
+      a.step[kv][head * a.ld[kv] + row] =
+          wrong ? nan : none ? 0.0f : (float)(span / (double)kLevels);
+    }
+  });
+}
+
+template <typename T, int kBits, int kLanes>
+__global__ void __launch_bounds__(256) cache_read_kernel(CacheArgs a) {
+  each_head<kLanes>(a, [&](int64_t token, int64_t row, int head, int kv, int e) {
+    if (e >= a.dim) return;
+    float x[8];
+    if (row < 0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    } else {
+      const float lo = a.low[kv][head * a.ld[kv] + row], step = a.step[kv][head * a.ld[kv] + row];
+      int u[8];
+      load_codes<kBits>(a.codes[kv] + row * a.row[kv] + head * a.head[kv] + e * kBits / 8, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = lo + step * (float)u[i];
+    }
+    store_elems((T*)a.x[kv] + token * a.x_row[kv] + head * a.x_head[kv] + e, x);
+  });
+}
+
+namespace {
+
+template <bool kWrite, typename T, int kBits>
+hipError_t run(CacheArgs a, hipStream_t s) {
+  const int64_t blocks = (int64_t)a.docs.rows_q / kUnit + a.docs.count;
+  return launch_all(blocks, 256, [&](uint32_t first, dim3 n) {
+    a.block0 = first;
+    if constexpr (kWrite) {
+      if (a.dim <= 64) cache_write_kernel<T, kBits, 8><<<n, 256, 0, s>>>(a);
+      else cache_write_kernel<T, kBits, 16><<<n, 256, 0, s>>>(a);
+    } else {
+      if (a.dim <= 64) cache_read_kernel<T, kBits, 8><<<n, 256, 0, s>>>(a);
+      else cache_read_kernel<T, kBits, 16><<<n, 256, 0, s>>>(a);
+    }
+  });
+}
+
+template <bool kWrite>
+hipError_t run(const gs_cache_config& cfg, const gs_documents& d, int64_t rows_q, int64_t rows_k,
+               const gs_heads& k, const gs_heads& v, const gs_codes& kc, const gs_codes& vc,
+               hipStream_t s) {
+  CacheArgs a = {};
+  a.docs = make_docs(d, rows_q, rows_k);
+  a.heads = cfg.heads;
+  a.dim = cfg.head_dim;
+  const gs_heads* x[2] = {&k, &v};
+  const gs_codes* c[2] = {&kc, &vc};
+  for (int i = 0; i < 2; ++i) {
+    a.x[i] = x[i]->data; a.x_row[i] = x[i]->row; a.x_head[i] = x[i]->head;
+    a.codes[i] = (uint8_t*)c[i]->codes; a.row[i] = c[i]->row; a.head[i] = c[i]->head;
+    a.low[i] = c[i]->low; a.step[i] = c[i]->step; a.ld[i] = c[i]->ld;
+  }
+  const bool wide = kc.bits == 8;
+  if (cfg.dtype == GS_F32) return wide ? run<kWrite, float, 8>(a, s) : run<kWrite, float, 4>(a, s);
+  if (cfg.dtype == GS_BF16) return wide ? run<kWrite, Bf16, 8>(a, s) : run<kWrite, Bf16, 4>(a, s);
+  return wide ? run<kWrite, F16, 8>(a, s) : run<kWrite, F16, 4>(a, s);
+}
+
+}  // namespace
+}  // namespace gs
+
+extern "C" {
+
+hipError_t gs_launch_cache_write(const gs_cache_config& cfg, const gs_documents& d, int64_t rows_q,
+                                 int64_t rows_k, const gs_heads& k, const gs_heads& v,
+                                 const gs_codes& kc, const gs_codes& vc, hipStream_t s) {
+  return gs::run<true>(cfg, d, rows_q, rows_k, k, v, kc, vc, s);
+}
+
+hipError_t gs_launch_cache_read(const gs_cache_config& cfg, const gs_documents& d, int64_t rows_q,
+                                int64_t rows_k, const gs_codes& kc, const gs_codes& vc,
+                                const gs_heads& k, const gs_heads& v, hipStream_t s) {
+  return gs::run<false>(cfg, d, rows_q, rows_k, k, v, kc, vc, s);
+}
+
+}  // extern "C"

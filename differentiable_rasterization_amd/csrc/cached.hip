@@ -1,0 +1,730 @@
+// cached.hip — attention of a few new tokens over a cache of 8- or 4-bit codes,
+// with keys that many requests share read once for all of them.
+//
+//   key j = low_j + step_j u_j:  q.k_j = step_j (q.u_j) + low_j sum(q),
+//   sum_j p_j v_j = sum_j (p_j step_j) (u_j - mid) + sum_j p_j (low_j + mid step_j).
+// Codes are whole numbers that the 16-bit types hold exactly, so both products
+// run on the matrix unit from codes brought to 16 bits in registers; only the
+// weights p_j step_j are rounded, to fp16 (11 bits) for either type: taken
+// relative to a power of two near the largest step, so that they stay in its
+// range.  Codes are centred there, since the rounding of a weight acts on the
+// whole of what it multiplies.
+//
+// Query heads that share a key head stand beside each other: column c of a
+// document is token c / group, head c % group.  A wavefront takes 32 keys at a
+// time by 16 or 64 columns, on the 16x16x32 instruction:
+//   S^T = K Q^T: lane l has column l % 16 and keys 4 (l / 16) + 0..3 of both
+//     16-key halves; its 8 weights are the right operand of
+//   O^T = V^T P^T, if the contraction runs over the keys in that order; the left
+//     operand takes single elements of those keys' rows, which each lane loads
+//     itself (16 lanes a row) and pairs by byte permutes.
+// So nothing passes through LDS but the four wavefronts' results at the end.
+//
+// Keys are cut into pieces where there are few columns; a second kernel joins a
+// token's pieces and those of the keys it shares.
+#include "cached.h"
+
+namespace gs {
+
+typedef _Float16 f16x2v __attribute__((ext_vector_type(2)));
+
+struct CachedArgs {
+  Docs docs;    // of this pass
+  Docs shared;  // join: count 0 without shared keys
+  int heads_q, heads_k, group, dim, causal;
+  float scale, softcap;
+  const float* slopes;
+  const uint16_t* q;
+  int64_t q_row, q_head;
+  const uint8_t *kc, *vc;  // codes; strides in bytes
+  int64_t kc_row, kc_head, vc_row, vc_head;
+  const float *klow, *kstep, *vlow, *vstep;  // [heads_k][ld]
+  int64_t k_ld, v_ld;
+  uint16_t* out;
+  int64_t out_row, out_head;
+  float* lse;
+  float* part_ml;  // [pieces][heads_q][rows_q][2]
+  float* part_o;   // [pieces][heads_q][rows_q][dim]
+  int pieces, pieces_shared;
+  int first_piece;  // of this pass, in the arrays above
+  int whole;        // one piece and nothing shared: the result is written at once
+  int looked_up;    // column tiles are units of the grid, else documents
+  uint32_t units, block0;
+};
+
+constexpr int kStepKeys = 128;  // keys the four wavefronts take at a time
+
+// Keys of a piece of a document of kl keys.
+__device__ inline int piece_keys(int kl, int pieces) {
+  const int n = (int)(((int64_t)kl + pieces - 1) / pieces);
+  return max((n + kStepKeys - 1) / kStepKeys * kStepKeys, 2 * kStepKeys);
+}
+
+// Token i sees the keys below this.
+__device__ inline int key_limit(const CachedArgs& a, const Doc& d, int token) {
+  return a.causal ? min(d.kl, max(token + d.kl - d.ql + 1, d.prefix)) : d.kl;
+}
+
+// x of lane l % 16 in all four rows of 16 lanes: largest, sum.
+template <typename F>
+__device__ inline float across(float x, F f) {
+  uint32_t w = __builtin_bit_cast(uint32_t, x);
+  const auto a = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  const uint32_t a0 = a[0], a1 = a[1];
+  const float y = f(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
+  w = __builtin_bit_cast(uint32_t, y);
+  const auto b = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  const uint32_t b0 = b[0], b1 = b[1];
+  return f(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
+}
+__device__ inline float across_max(float x) {
+  return across(x, [](float p, float q) { return fmaxf(p, q); });
+}
+__device__ inline float across_sum(float x) {
+  return across(x, [](float p, float q) { return p + q; });
+}
+
+template <typename T>
+struct Mat16;
+template <>
+struct Mat16<Bf16> {
+  typedef bf16x8 V8;
+  static __device__ inline f32x4 mul(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mat16<F16> {
+  typedef f16x8 V8;
+  static __device__ inline f32x4 mul(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+
+// (lo, hi) fp16 numbers of a word, times mul, plus add: exact here.
+__device__ inline uint32_t fma_f16(uint32_t w, _Float16 mul, _Float16 add) {
+  const f16x2v m = {mul, mul}, c = {add, add};
+  return __builtin_bit_cast(uint32_t,
+                            __builtin_elementwise_fma(__builtin_bit_cast(f16x2v, w), m, c));
+}
+
+// Eight codes as key operand, x = (code - kOff) / kMul exactly.
+template <typename T, int kBits>
+struct KeyCodes {
+  // 8 bits in bf16: the code itself; in fp16: (u - 128) / 512.
+  // 4 bits: 1 + u / 16, made by placing the four bits in a mantissa.
+  static constexpr float kMul = kBits == 4 ? 16.0f : __is_same(T, Bf16) ? 1.0f : 512.0f;
+  static constexpr float kOff = kBits == 4 ? -16.0f : __is_same(T, Bf16) ? 0.0f : 128.0f;
+  static __device__ inline typename Mat16<T>::V8 operand(const uint32_t* w) {
+    uint32_t o[4];
+    if constexpr (kBits == 4) {
+      constexpr bool kB = __is_same(T, Bf16);
+      constexpr uint32_t one = kB ? 0x3f803f80u : 0x3c003c00u;
+      constexpr uint32_t mask = kB ? 0x00780078u : 0x03c003c0u;
+      constexpr int place = kB ? 3 : 6;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int right = 4 * i - place;
+        o[i] = ((right >= 0 ? w[0] >> (right & 31) : w[0] << (-right & 31)) & mask) | one;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = w[i >> 1], at = 16 * (i & 1);
+        if constexpr (__is_same(T, Bf16)) {
+          o[i] = pack_bf16((float)(x >> at & 255), (float)(x >> (at + 8) & 255));
+        } else {
+          // two bytes as the subnormal numbers u 2^-24
+          const uint32_t pair = __builtin_amdgcn_perm(0, x, i & 1 ? 0x0c030c02u : 0x0c010c00u);
+          o[i] = fma_f16(pair, (_Float16)32768.0f, (_Float16)-0.25f);
+        }
+      }
+    }
+    return __builtin_bit_cast(typename Mat16<T>::V8, u32x4{o[0], o[1], o[2], o[3]});
+  }
+};
+
+// What a lane loads of the eight rows of values it has, and element e of all of
+// them as operand: (code - kMid) / 512.
+template <int kBits, int DT>
+struct ValueCodes {
+  static constexpr int kElems = DT / 16;  // of a row, a lane
+  static constexpr int kWords = kBits == 8 ? kElems / 4 : 1;
+  static constexpr float kMid = kBits == 8 ? 128.0f : 8.0f;
+  // First byte of lane n's part of a row (4 bits, 64 elements: half a word, of
+  // the even or the odd elements), and its first element.
+  static __device__ inline int byte_of(int n) { return n * kElems * kBits / 8; }
+  static __device__ inline int first_of(int n) {
+    return kBits == 4 && DT == 64 ? 8 * (n >> 1) : n * kElems;
+  }
+  // Element e of lane n's part.
+  static __device__ inline int element(int n, int e) {
+    if (kBits == 8) return n * kElems + e;
+    if (DT == 64) return 8 * (n >> 1) + 2 * e + (n & 1);
+    return 8 * n + (e < 4 ? 2 * e : 2 * (e - 4) + 1);
+  }
+  static __device__ inline f16x8 operand(const uint32_t (&v)[8][kWords], int e) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (kBits == 8) {
+        const uint32_t c = e & 3;
+        const uint32_t pair = __builtin_amdgcn_perm(v[2 * i + 1][e >> 2], v[2 * i][e >> 2],
+                                                    0x0c000c00u | c | (4 + c) << 16);
+        o[i] = fma_f16(pair, (_Float16)32768.0f, (_Float16)-0.25f);
+      } else {
+        const uint32_t p = __builtin_amdgcn_perm(v[2 * i + 1][0], v[2 * i][0],
+                                                 e < 4 ? 0x05040100u : 0x07060302u) >>
+                           (e & 2 ? 8 : 0);
+        o[i] = e & 1 ? fma_f16(p & 0x00f000f0u, (_Float16)2048.0f, (_Float16)-0.015625f)
+                     : fma_f16(p & 0x000f000fu, (_Float16)32768.0f, (_Float16)-0.015625f);
+      }
+    }
+    return __builtin_bit_cast(f16x8, u32x4{o[0], o[1], o[2], o[3]});
+  }
+};
+
+typedef f32x4 f32x4_unaligned __attribute__((aligned(4)));
+
+// The codes of 32 keys, and their numbers, as a lane has them.
+template <int kBits, int DT>
+struct KeyTile {
+  static constexpr int kPieces = DT / 64;           // of 16 elements, of a key, a lane
+  static constexpr int kPieceWords = kBits / 2;     // of such a piece
+  typedef ValueCodes<kBits, DT> V;
+  uint32_t k[2][kPieces * kPieceWords];
+  uint32_t v[8][V::kWords];
+  f32x4 kstep[2], klow[2], vstep[2], vlow[2];
+
+  // keys row .. of the cache, `valid` of them: codes of keys past that are zero.
+  // Their numbers are whatever stands there.
+  __device__ inline void load(const CachedArgs& a, int hk, int64_t row, int valid) {
+    const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
+    const int bytes = a.dim * kBits / 8;
+    const auto from_k = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(a.kc + row * a.kc_row + hk * a.kc_head), 0,
+        (int)((valid - 1) * a.kc_row) + bytes, 0x00027000);
+    const auto from_v = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(a.vc + row * a.vc_row + hk * a.vc_head), 0,
+        (int)((valid - 1) * a.vc_row) + bytes, 0x00027000);
+    const int kRow = (int)a.kc_row, vRow = (int)a.vc_row;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int e = kg * (DT / 4) + 16 * i;
+        const int at = e < a.dim ? (16 * t + n) * kRow + e * kBits / 8 : (int)0x80000000;
+        uint32_t* to = k[t] + i * kPieceWords;
+        if constexpr (kBits == 8) {
+          const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(from_k, at, 0, 0);
+          to[0] = w.x; to[1] = w.y; to[2] = w.z; to[3] = w.w;
+        } else {
+          const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(from_k, at, 0, 0);
+          to[0] = w.x; to[1] = w.y;
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int key = 16 * (j >> 2) + 4 * kg + (j & 3);
+      const int at = V::first_of(n) < a.dim ? key * vRow + V::byte_of(n) : (int)0x80000000;
+      if constexpr (V::kWords == 2) {
+        const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(from_v, at, 0, 0);
+        v[j][0] = w.x; v[j][1] = w.y;
+      } else if constexpr (kBits == 4 && DT == 64) {
+        v[j][0] = __builtin_amdgcn_raw_buffer_load_b16(from_v, at, 0, 0);
+      } else {
+        v[j][0] = __builtin_amdgcn_raw_buffer_load_b32(from_v, at, 0, 0);
+      }
+    }
+    // Numbers of four keys side by side in one load, unless that would reach
+    // past the end of the arrays: past the last head's last row.
+    const int64_t at_k = hk * a.k_ld + row, at_v = hk * a.v_ld + row;
+    const int64_t end_k = (a.heads_k - 1) * a.k_ld + a.docs.rows_k;
+    const int64_t end_v = (a.heads_k - 1) * a.v_ld + a.docs.rows_k;
+    if (at_k + 32 <= end_k && at_v + 32 <= end_v) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int key = 16 * t + 4 * kg;
+        kstep[t] = *(const f32x4_unaligned*)(a.kstep + at_k + key);
+        klow[t] = *(const f32x4_unaligned*)(a.klow + at_k + key);
+        vstep[t] = *(const f32x4_unaligned*)(a.vstep + at_v + key);
+        vlow[t] = *(const f32x4_unaligned*)(a.vlow + at_v + key);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int key = min(16 * (j >> 2) + 4 * kg + (j & 3), valid - 1);
+        kstep[j >> 2][j & 3] = a.kstep[at_k + key];
+        klow[j >> 2][j & 3] = a.klow[at_k + key];
+        vstep[j >> 2][j & 3] = a.vstep[at_v + key];
+        vlow[j >> 2][j & 3] = a.vlow[at_v + key];
+      }
+    }
+  }
+};
+
+// Weights are 2^(score - reference): up to 2^kRoom when the reference is taken,
+// and the reference moves only when a score has passed it by kGrowth more, so
+// they stay below 2^14.
+constexpr float kRoom = 8.0f, kGrowth = 6.0f;
+
+template <typename T, int kBits, int DT, int CT>
+__global__ void __launch_bounds__(256, CT == 1 ? 2 : 1) cached_attention_kernel(CachedArgs a) {
+  typedef KeyCodes<T, kBits> K;
+  typedef KeyTile<kBits, DT> Tile;
+  typedef typename Tile::V V;
+  typedef typename Mat16<T>::V8 V8;
+  constexpr int kSteps = DT / 32;    // of the scores' contraction
+  constexpr int kElems = V::kElems;  // products of 16 elements of the values
+  constexpr int kStride = DT + 4;
+  __shared__ __align__(16) float s_o[4][16][kStride];
+  __shared__ float s_m[4][16], s_l[4][16], s_c[4][16];
+  const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
+  const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // All heads of the same keys go to one XCD, one after the other: rows of
+  // neighbouring heads share lines.
+  const uint32_t block = a.block0 + blockIdx.x;
+  const uint32_t turn = block >> 3;
+  const int hk = (int)(turn % (uint32_t)a.heads_k);
+  const uint32_t place = turn / (uint32_t)a.heads_k * 8 + (block & 7);
+  const uint32_t unit = place % a.units;
+  const int piece = (int)(place / a.units);
+  if (piece >= a.pieces) return;
+  Doc d;
+  int col_first = 0, col_end = 0x7fffffff;
+  if (a.looked_up) {
+    uint32_t local, units;
+    if (find_document<false>(a.docs, (uint32_t)a.group, 16 * CT, unit, &local, &units, &d) < 0)
+      return;
+    col_first = (int)local * 16 * CT;
+    col_end = col_first + 16 * CT;
+  } else {
+    d = load_doc(a.docs, (int)unit);
+  }
+  const int cols = d.ql * a.group;
+  const int keys = piece_keys(d.kl, a.pieces);
+  if (piece > 0 && (int64_t)piece * keys >= d.kl) return;
+  const int key0 = piece * keys;
+
+  const float to_log2 = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
+  const float cap = a.softcap * kLog2e;
+  for (int col0 = col_first; col0 < min(col_end, cols); col0 += 16 * CT) {
+    // Columns past the last one repeat it, and are not stored.
+    V8 q[CT][kSteps];
+    float qsum[CT], slope[CT];
+    int limit[CT], pos[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const int c = min(col0 + 16 * ct + n, cols - 1);
+      const int token = c / a.group, head = hk * a.group + c % a.group;
+      const uint16_t* p = a.q + (int64_t)(d.qs + token) * a.q_row + head * a.q_head;
+      float sum = 0.0f;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int e = kg * (DT / 4) + 8 * s;
+        u32x4 w = {0, 0, 0, 0};
+        if (e < a.dim) w = *(const u32x4*)(p + e);
+        q[ct][s] = __builtin_bit_cast(V8, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x, y;
+          unpack2<T>(w[i], x, y);
+          sum += x + y;
+        }
+      }
+      qsum[ct] = across_sum(sum);
+      limit[ct] = key_limit(a, d, token);
+      pos[ct] = token + d.kl - d.ql;
+      slope[ct] = a.slopes ? a.slopes[head] * kLog2e : 0.0f;
+    }
+    const int last_col = min(col0 + 16 * CT, cols) - 1;
+    const int all_see = key_limit(a, d, col0 / a.group);
+    const int key_end =
+        min((int)min((int64_t)d.kl, (int64_t)key0 + keys), key_limit(a, d, last_col / a.group));
+
+    f32x4 o[CT][kElems];
+    float m[CT], ref[CT], l[CT], mean[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      m[ct] = -INFINITY;
+      ref[ct] = l[ct] = mean[ct] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < kElems; ++e) o[ct][e] = (f32x4)(0.0f);
+    }
+    // steps are taken relative to unit_step, a power of two
+    float unit_step = 0x1p-126f;
+    Tile tile, next;
+    int key = key0 + 32 * wave;
+    if (key < key_end) next.load(a, hk, (int64_t)d.ks + key, min(32, d.kl - key));
+    for (; key < key_end; key += kStepKeys) {
+      tile = next;
+      if (key + kStepKeys < key_end)
+        next.load(a, hk, (int64_t)d.ks + key + kStepKeys, min(32, d.kl - key - kStepKeys));
+      f32x4 s[2][CT];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) s[0][ct] = s[1][ct] = (f32x4)(0.0f);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const V8 x = K::operand(tile.k[t] + i * kBits / 4);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) s[t][ct] = Mat16<T>::mul(x, q[ct][i], s[t][ct]);
+        }
+      const bool masked = key + 32 > all_see || key + 32 > key_end;
+      float kmul[8], kadd[8], vmul[8], vadd[8];
+      float steps = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int t = j >> 2, r = j & 3;
+        const float ks = tile.kstep[t][r], kl = tile.klow[t][r];
+        kmul[j] = ks * (K::kMul * to_log2);
+        kadd[j] = fmaf(ks, K::kOff, kl) * to_log2;
+        vmul[j] = tile.vstep[t][r];
+        vadd[j] = fmaf(vmul[j], V::kMid, tile.vlow[t][r]);
+        // what no column sees has no part in the range of the weights
+        if (masked && key + 16 * t + 4 * kg + r >= key_end) vmul[j] = 0.0f;
+        steps = vmul[j] < __builtin_huge_valf() ? fmaxf(steps, vmul[j]) : steps;
+      }
+      if (__ballot(steps >= 2.0f * unit_step)) {
+        float top = steps;
+#pragma unroll
+        for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
+        const float now =
+            __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, top) & 0x7f800000u);
+        const float f = unit_step / now;
+        unit_step = now;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+          for (int e = 0; e < kElems; ++e) o[ct][e] *= f;
+      }
+      const float per_unit = 1.0f / unit_step;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vmul[j] *= per_unit;
+
+      f16x8 w[CT];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) {
+        float x[8], top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int t = j >> 2, r = j & 3;
+          x[j] = fmaf(s[t][ct][r], kmul[j], kadd[j] * qsum[ct]);
+        }
+        if (a.softcap > kWideCap) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = cap * tanh_wide(x[j]);
+        } else if (a.softcap > 0.0f) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = cap * tanh_of(x[j]);
+        }
+        const int first = key + 4 * kg;  // keys first + 0..3 and 16 + 0..3
+        if (a.slopes) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            x[j] = fmaf(-slope[ct],
+                        fabsf((float)(pos[ct] - first - (16 * (j >> 2) + (j & 3)))), x[j]);
+        }
+        if (masked) {
+          const int end = min(limit[ct], key_end) - first;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = 16 * (j >> 2) + (j & 3) < end ? x[j] : -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, x[j]);
+        if (__ballot(top > m[ct] + kGrowth)) {
+          const float now = fmaxf(m[ct], across_max(top));
+          const float f = m[ct] == now ? 1.0f : __builtin_amdgcn_exp2f(m[ct] - now);
+          m[ct] = now;
+          ref[ct] = now == -INFINITY ? 0.0f : now - kRoom;
+          l[ct] *= f;
+          mean[ct] *= f;
+#pragma unroll
+          for (int e = 0; e < kElems; ++e) o[ct][e] *= f;
+        }
+        float p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          p[j] = __builtin_amdgcn_exp2f(x[j] - ref[ct]);
+          l[ct] += p[j];
+          // what a column does not see may hold a NaN
+          const bool seen = !masked || x[j] != -INFINITY;
+          mean[ct] = seen ? fmaf(p[j], vadd[j], mean[ct]) : mean[ct];
+          p[j] = seen ? p[j] * vmul[j] : 0.0f;
+        }
+        w[ct] = __builtin_bit_cast(f16x8, u32x4{pack_f16(p[0], p[1]), pack_f16(p[2], p[3]),
+                                                pack_f16(p[4], p[5]), pack_f16(p[6], p[7])});
+      }
+#pragma unroll
+      for (int e = 0; e < kElems; ++e) {
+        const f16x8 x = V::operand(tile.v, e);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+          o[ct][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w[ct], o[ct][e], 0, 0, 0);
+      }
+    }
+
+    // The four wavefronts' sums, 16 columns at a time: 16 lanes a column.
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const float lsum = across_sum(l[ct]), msum = across_sum(mean[ct]);
+      __syncthreads();
+      if (kg == 0) {
+        s_m[wave][n] = ref[ct];
+        s_l[wave][n] = lsum;
+        s_c[wave][n] = msum;
+      }
+#pragma unroll
+      for (int e = 0; e < kElems; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s_o[wave][n][V::element(4 * kg + r, e)] =
+            o[ct][e][r] * 512.0f * unit_step;
+      __syncthreads();
+      const int col = threadIdx.x >> 4, first = (threadIdx.x & 15) * kElems;
+      const int c = col0 + 16 * ct + col;
+      if (c < cols && first < a.dim) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = s_l[i][col] == 0.0f ? top : fmaxf(top, s_m[i][col]);
+        float sum = 0.0f, add = 0.0f, y[kElems];
+#pragma unroll
+        for (int e = 0; e < kElems; ++e) y[e] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (s_l[i][col] == 0.0f) continue;
+          const float f = __builtin_amdgcn_exp2f(s_m[i][col] - top);
+          sum = fmaf(f, s_l[i][col], sum);
+          add = fmaf(f, s_c[i][col], add);
+#pragma unroll
+          for (int e = 0; e < kElems; ++e) y[e] = fmaf(f, s_o[i][col][first + e], y[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < kElems; ++e) y[e] += add;
+        const int64_t token = d.qs + c / a.group;
+        const int head = hk * a.group + c % a.group;
+        if (a.whole) {
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+          for (int e = 0; e < kElems; ++e) y[e] *= inv;
+          store_elems((T*)(a.out + token * a.out_row + head * a.out_head + first), y);
+          if (a.lse && first == 0)
+            a.lse[(int64_t)head * a.docs.rows_q + token] =
+                sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+        } else {
+          const int64_t slot =
+              ((int64_t)(a.first_piece + piece) * a.heads_q + head) * a.docs.rows_q + token;
+          store_elems(a.part_o + slot * a.dim + first, y);
+          if (first == 0) {
+            a.part_ml[2 * slot] = top;
+            a.part_ml[2 * slot + 1] = sum;
+          }
+        }
+      }
+    }
+  }
+}
+
+// A token's pieces, and those of the keys it shares: a wavefront a head, two
+// elements a lane.
+template <typename T>
+__global__ void __launch_bounds__(256) cached_join_kernel(CachedArgs a) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t heads = (uint32_t)(a.heads_q + 3) / 4;
+  const uint32_t block = a.block0 + blockIdx.x;
+  const int head = (int)(block % heads) * 4 + (threadIdx.x >> 6);
+  uint32_t local, units;
+  Doc d;
+  if (find_document<false>(a.docs, 1, 1, block / heads, &local, &units, &d) < 0) return;
+  if (head >= a.heads_q) return;
+  const int64_t token = d.qs + (int)local;
+  const int own = max(1, (int)(((int64_t)d.kl + piece_keys(d.kl, a.pieces) - 1) /
+                               piece_keys(d.kl, a.pieces)));
+  int more = 0;
+  for (int base = 0; base < a.shared.count; base += 64) {
+    Doc g = {0, 0, 0, 0, 0};
+    if (base + lane < a.shared.count) g = load_doc(a.shared, base + lane);
+    const uint64_t hit = __ballot(token >= g.qs && token < (int64_t)g.qs + g.ql);
+    if (!hit) continue;
+    const int kl = __builtin_amdgcn_readlane(g.kl, __ffsll((unsigned long long)hit) - 1);
+    const int n = piece_keys(kl, a.pieces_shared);
+    more = (int)(((int64_t)kl + n - 1) / n);
+    break;
+  }
+  const int e = 2 * lane;
+  float top = -INFINITY, sum = 0.0f, x = 0.0f, y = 0.0f;
+  // pieces in order, 64 at a time
+  for (int base = 0; base < own + more; base += 64) {
+    const int i = base + lane;
+    float m = -INFINITY, l = 0.0f;
+    const auto slot = [&](int p) {
+      return ((int64_t)(p < own ? p : a.pieces + p - own) * a.heads_q + head) * a.docs.rows_q +
+             token;
+    };
+    if (i < own + more) {
+      m = a.part_ml[2 * slot(i)];
+      l = a.part_ml[2 * slot(i) + 1];
+    }
+    float now = l == 0.0f ? -INFINITY : m;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) now = fmaxf(now, __shfl_xor(now, o, 64));
+    now = fmaxf(now, top);
+    if (now == -INFINITY && !__ballot(l != 0.0f)) continue;
+    const float old = top == now ? 1.0f : __builtin_amdgcn_exp2f(top - now);
+    top = now;
+    const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+    sum *= old;
+    x *= old;
+    y *= old;
+    const int count = min(64, own + more - base);
+#pragma unroll 4
+    for (int p = 0; p < count; ++p) {
+      const float fp = __shfl(f, p, 64), lp = __shfl(l, p, 64);
+      f32x2 v = {0.0f, 0.0f};
+      if (e < a.dim) v = *(const f32x2*)(a.part_o + slot(base + p) * a.dim + e);
+      sum = fmaf(fp, lp, sum);
+      // a piece whose sum is zero holds zeros
+      x = fmaf(fp, v.x, x);
+      y = fmaf(fp, v.y, y);
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (e < a.dim)
+    *(uint32_t*)(a.out + token * a.out_row + head * a.out_head + e) = pack2<T>(x * inv, y * inv);
+  if (a.lse && lane == 0)
+    a.lse[(int64_t)head * a.docs.rows_q + token] =
+        sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+namespace {
+
+// How a pass is cut: columns of a tile, tiles, pieces of a document's keys.
+struct Cut {
+  int tiles;  // of 16 columns, a workgroup: 1 or 4
+  bool looked_up;
+  int64_t units;
+  int pieces;
+};
+Cut cut_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q,
+           int64_t rows_k) {
+  Cut o = {};
+  const int64_t group = cfg.heads_q / cfg.heads_k;
+  const int64_t longest_q = d.max_q_len > 0 && d.max_q_len < rows_q ? d.max_q_len : rows_q;
+  const int64_t longest_k = d.max_k_len > 0 && d.max_k_len < rows_k ? d.max_k_len : rows_k;
+  o.tiles = longest_q * group <= 16 ? 1 : 4;
+  o.looked_up = longest_q * group > 16 * o.tiles;
+  o.units = o.looked_up ? rows_q * group / (16 * o.tiles) + d.count : d.count;
+  const int64_t base = o.units * cfg.heads_k;
+  const int64_t target = 2048;
+  int64_t pieces = (target + base - 1) / (base > 0 ? base : 1);
+  const int64_t most = (longest_k + 2 * kStepKeys - 1) / (2 * kStepKeys);
+  if (pieces > most) pieces = most;
+  o.pieces = (int)(pieces < 1 ? 1 : pieces);
+  return o;
+}
+
+struct Plan {
+  Cut own, shared;
+  bool whole;
+  int64_t slots;
+};
+Plan plan_of(const gs_attention_config& cfg, const gs_documents& d, const gs_documents* shared,
+             int64_t rows_q, int64_t rows_k) {
+  Plan p = {};
+  p.own = cut_of(cfg, d, rows_q, rows_k);
+  if (shared && shared->count > 0) p.shared = cut_of(cfg, *shared, rows_q, rows_k);
+  p.whole = p.own.pieces == 1 && p.shared.pieces == 0;
+  p.slots = p.whole ? 0 : (int64_t)(p.own.pieces + p.shared.pieces) * cfg.heads_q * rows_q;
+  return p;
+}
+
+size_t ml_bytes(const Plan& p) { return ((size_t)p.slots * 8 + 255) / 256 * 256; }
+
+template <typename T, int kBits, int DT>
+hipError_t pass(CachedArgs a, const Cut& c, hipStream_t s) {
+  a.pieces = c.pieces;
+  a.looked_up = c.looked_up;
+  a.units = (uint32_t)c.units;
+  const int64_t blocks = (c.units * c.pieces + 7) / 8 * 8 * a.heads_k;
+  return launch_all(blocks, 256, [&](uint32_t first, dim3 n) {
+    a.block0 = first;
+    if (c.tiles == 1) cached_attention_kernel<T, kBits, DT, 1><<<n, 256, 0, s>>>(a);
+    else cached_attention_kernel<T, kBits, DT, 4><<<n, 256, 0, s>>>(a);
+  });
+}
+
+template <typename T, int kBits, int DT>
+hipError_t run(const CachedArgs& a, const Plan& p, const Docs& shared, hipStream_t s) {
+  if (p.shared.pieces > 0) {
+    CachedArgs b = a;
+    b.docs = shared;
+    b.causal = 0;
+    b.first_piece = p.own.pieces;
+    const hipError_t e = pass<T, kBits, DT>(b, p.shared, s);
+    if (e != hipSuccess) return e;
+  }
+  const hipError_t e = pass<T, kBits, DT>(a, p.own, s);
+  if (e != hipSuccess || p.whole) return e;
+  CachedArgs j = a;
+  j.shared = shared;
+  j.pieces = p.own.pieces;
+  j.pieces_shared = p.shared.pieces;
+  return launch_all((int64_t)a.docs.rows_q * ((a.heads_q + 3) / 4), 256,
+                    [&](uint32_t first, dim3 n) {
+                      j.block0 = first;
+                      cached_join_kernel<T><<<n, 256, 0, s>>>(j);
+                    });
+}
+
+template <typename T>
+hipError_t run(const CachedArgs& a, const Plan& p, const Docs& shared, int bits, hipStream_t s) {
+  if (bits == 8)
+    return a.dim <= 64 ? run<T, 8, 64>(a, p, shared, s) : run<T, 8, 128>(a, p, shared, s);
+  return a.dim <= 64 ? run<T, 4, 64>(a, p, shared, s) : run<T, 4, 128>(a, p, shared, s);
+}
+
+}  // namespace
+}  // namespace gs
+
+extern "C" {
+
+size_t gs_cached_attention_bytes(const gs_attention_config& cfg, const gs_documents& d,
+                                 const gs_documents* shared, int64_t rows_q, int64_t rows_k) {
+  const gs::Plan p = gs::plan_of(cfg, d, shared, rows_q, rows_k);
+  return p.whole ? 0 : gs::ml_bytes(p) + (size_t)p.slots * cfg.head_dim * 4;
+}
+
+hipError_t gs_launch_cached_attention(const gs_attention_config& cfg, const gs_documents& d,
+                                      const gs_documents* shared, int64_t rows_q, int64_t rows_k,
+                                      const gs_heads& q, const gs_codes& k, const gs_codes& v,
+                                      const gs_heads& out, float* lse, void* workspace,
+                                      hipStream_t s) {
+  const gs::Plan p = gs::plan_of(cfg, d, shared, rows_q, rows_k);
+  gs::CachedArgs a = {};
+  a.docs = gs::make_docs(d, rows_q, rows_k);
+  gs::Docs more = {};
+  if (shared) more = gs::make_docs(*shared, rows_q, rows_k);
+  more.prefix = nullptr;  // all tokens see all shared keys
+  a.heads_q = cfg.heads_q;
+  a.heads_k = cfg.heads_k;
+  a.group = cfg.heads_q / cfg.heads_k;
+  a.dim = cfg.head_dim;
+  a.causal = cfg.causal;
+  a.scale = cfg.scale;
+  a.softcap = cfg.softcap;
+  a.slopes = cfg.slopes;
+  a.q = (const uint16_t*)q.data; a.q_row = q.row; a.q_head = q.head;
+  a.kc = (const uint8_t*)k.codes; a.kc_row = k.row; a.kc_head = k.head;
+  a.vc = (const uint8_t*)v.codes; a.vc_row = v.row; a.vc_head = v.head;
+  a.klow = k.low; a.kstep = k.step; a.k_ld = k.ld;
+  a.vlow = v.low; a.vstep = v.step; a.v_ld = v.ld;
+  a.out = (uint16_t*)out.data; a.out_row = out.row; a.out_head = out.head;
+  a.lse = lse;
+  a.whole = p.whole;
+  a.part_ml = (float*)workspace;
+  a.part_o = (float*)((char*)workspace + gs::ml_bytes(p));
+  if (cfg.dtype == GS_BF16) return gs::run<gs::Bf16>(a, p, more, k.bits, s);
+  return gs::run<gs::F16>(a, p, more, k.bits, s);
+}
+
+}  // extern "C"

@@ -40,7 +40,8 @@ EXPORTED = ("gs_default_settings", "gs_status_string", "gs_last_error", "gs_num_
             "gs_attention_bwd_workspace_size", "gs_attention_bwd", "gs_gated_scan_saved_size",
             "gs_gated_scan_fwd_workspace_size", "gs_gated_scan_fwd",
             "gs_gated_scan_bwd_workspace_size", "gs_gated_scan_bwd", "gs_quantize_rows",
-            "gs_linear_i8_workspace_size", "gs_linear_i8")
+            "gs_linear_i8_workspace_size", "gs_linear_i8", "gs_cache_write", "gs_cache_read",
+            "gs_cached_attention_fwd_workspace_size", "gs_cached_attention_fwd")
 GS_F32, GS_BF16, GS_F16 = 0, 1, 2
 
 
@@ -98,6 +99,16 @@ class gs_attention_config(C.Structure):
 
 class gs_scan_config(C.Structure):
     _fields_ = [("dtype", C.c_int32), ("coupled", C.c_int32), ("channels", C.c_int64)]
+
+
+class gs_codes(C.Structure):
+    """A cache of keys or values in 8 or 4 bits; keeps its tensors alive."""
+    _fields_ = [("codes", C.c_void_p), ("low", C.c_void_p), ("step", C.c_void_p),
+                ("row", C.c_int64), ("head", C.c_int64), ("ld", C.c_int64), ("bits", C.c_int32)]
+
+
+class gs_cache_config(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("heads", C.c_int32), ("head_dim", C.c_int32)]
 
 
 class gs_linear_config(C.Structure):
@@ -233,6 +244,13 @@ def load():
     lib.gs_linear_i8_workspace_size.argtypes = [P, i64]
     lib.gs_linear_i8.restype = C.c_int
     lib.gs_linear_i8.argtypes = [P, i64] + [P] * 5 + [P, SZ, P]
+    for name in ("write", "read"):
+        fn = getattr(lib, "gs_cache_" + name)
+        fn.restype, fn.argtypes = C.c_int, [P, P, i64, i64] + [P] * 5
+    lib.gs_cached_attention_fwd_workspace_size.restype = SZ
+    lib.gs_cached_attention_fwd_workspace_size.argtypes = [P, i32, P, P, i64, i64]
+    lib.gs_cached_attention_fwd.restype = C.c_int
+    lib.gs_cached_attention_fwd.argtypes = [P, P, P, i64, i64] + [P] * 5 + [P, SZ, P]
     _name_types()
     _lib = lib
     return lib
@@ -952,6 +970,90 @@ def gs_linear_i8(cfg, rows, x, weight, weight_scale, bias, y, workspace, workspa
         C.byref(cfg), rows, _where(x), _at(weight, _I8, n * k), _at(weight_scale, _F32, n),
         _at(bias, _F32, n), _where(y), _bytes(workspace, workspace_bytes), int(workspace_bytes),
         _stream(stream)))
+
+
+def codes(codes, low, step, bits) -> gs_codes:
+    """The cache of a uint8 tensor [rows, heads, head_dim * bits / 8] (last
+    dimension contiguous) and fp32 tensors low and step [heads, rows] (rows
+    contiguous, one distance of heads)."""
+    import torch
+    if bits not in (8, 4):
+        raise ValueError("bits must be 8 or 4, not %s" % bits)
+    if codes.dtype != torch.uint8 or codes.dim() != 3 or \
+            (codes.shape[2] > 1 and codes.stride(2) != 1):
+        raise ValueError("need a uint8 tensor [rows, heads, bytes] with contiguous bytes")
+    n, h, _ = codes.shape
+    for t in (low, step):
+        if t.dtype != torch.float32 or tuple(t.shape) != (h, n) or (n > 1 and t.stride(1) != 1):
+            raise ValueError("low and step must be float32 tensors [%d, %d] with contiguous rows, "
+                             "not %s of %s" % (h, n, list(t.shape), t.dtype))
+    if h > 1 and low.stride(0) != step.stride(0):
+        raise ValueError("low and step must have one distance of heads")
+    for t in (codes, low, step):
+        if t.numel() and not _on_device(t):
+            raise ValueError("a cache needs device tensors")
+    # a stride without a second element says nothing
+    c = gs_codes(codes.data_ptr(), low.data_ptr(), step.data_ptr(),
+                 codes.stride(0) if n > 1 else max(codes.shape[1] * codes.shape[2], 1),
+                 codes.stride(1) if h > 1 else codes.shape[2],
+                 low.stride(0) if h > 1 else max(n, 1), bits)
+    c.tensors = (codes, low, step)
+    c.extent, c.address = (n, h, codes.shape[2] * 8 // bits), C.addressof(c)
+    return c
+
+
+def _codes(c, rows, heads, dim):
+    """The address of a cache that has at least these sizes."""
+    if type(c) is not gs_codes:
+        raise ValueError("need a cache made by codes()")
+    e = getattr(c, "extent", None)
+    if e is not None and (e[0] < rows or e[1] < heads or e[2] < dim):
+        raise ValueError("need a cache of %d rows, %d heads of %d, not of %d, %d of %d" %
+                         (rows, heads, dim, *e))
+    return C.addressof(c) if e is None else c.address
+
+
+def cache_config(dtype, heads, head_dim) -> gs_cache_config:
+    """dtype: a torch dtype, of the tokens."""
+    return gs_cache_config(_dtype(dtype), int(heads), int(head_dim))
+
+
+def gs_cache_write(cfg, docs, rows_q, rows_k, k, v, k_cache, v_cache, stream=None):
+    want, held = (cfg.dtype, rows_q, cfg.heads, cfg.head_dim), (rows_k, cfg.heads, cfg.head_dim)
+    k, v = _heads(k, want), _heads(v, want)
+    _check(load().gs_cache_write(C.byref(cfg), C.byref(docs), rows_q, rows_k, _where(k), _where(v),
+                                 _codes(k_cache, *held), _codes(v_cache, *held),
+                                 _stream(stream)))
+
+
+def gs_cache_read(cfg, docs, rows_q, rows_k, k_cache, v_cache, k, v, stream=None):
+    want, held = (cfg.dtype, rows_q, cfg.heads, cfg.head_dim), (rows_k, cfg.heads, cfg.head_dim)
+    k, v = _heads(k, want), _heads(v, want)
+    _check(load().gs_cache_read(C.byref(cfg), C.byref(docs), rows_q, rows_k,
+                                _codes(k_cache, *held), _codes(v_cache, *held), _where(k),
+                                _where(v), _stream(stream)))
+
+
+def _shared(docs):
+    return None if docs is None else C.byref(docs)
+
+
+def gs_cached_attention_fwd_workspace_size(cfg, bits, docs, shared, rows_q, rows_k) -> int:
+    return int(load().gs_cached_attention_fwd_workspace_size(
+        C.byref(cfg), bits, C.byref(docs), _shared(shared), rows_q, rows_k))
+
+
+def gs_cached_attention_fwd(cfg, docs, shared, rows_q, rows_k, q, k_cache, v_cache, out, lse,
+                            workspace, workspace_bytes, stream=None):
+    """shared: documents whose keys their tokens have in front of their own, or
+    None; lse: fp32 [heads_q, rows_q], or None."""
+    hq, dim = cfg.heads_q, cfg.head_dim
+    want, held = (cfg.dtype, rows_q, hq, dim), (rows_k, cfg.heads_k, dim)
+    q, out = _heads(q, want), _heads(out, want)
+    _check(load().gs_cached_attention_fwd(
+        C.byref(cfg), C.byref(docs), _shared(shared), rows_q, rows_k, _where(q),
+        _codes(k_cache, *held), _codes(v_cache, *held), _where(out), _at(lse, _F32, hq * rows_q),
+        _bytes(workspace, workspace_bytes), int(workspace_bytes), _stream(stream)))
 
 
 # ---------------------------------------------------------------------------

@@ -856,6 +856,72 @@ GS_API gs_status gs_linear_i8(const gs_linear_config* cfg, int64_t rows, const g
                               const gs_rows* y, void* workspace, size_t workspace_bytes,
                               void* stream);
 
+/* A cache of keys or values in 8 or 4 bits (HOST struct of DEVICE arrays).  Each
+ * head of a row is low + step code with codes of 0 .. 2^bits - 1: codes
+ * [rows][heads][head_dim * bits / 8] bytes (16-byte aligned; row and head are
+ * strides in bytes, multiples of 4, row below 2^25, heads and rows must not
+ * overlap), low and step [heads][ld] fp32 with ld >= rows.  In 8 bits byte i is
+ * element i; in 4 bits each 32-bit word holds eight elements, 2i in bits 4i ..
+ * 4i + 3 and 2i + 1 in bits 16 + 4i .. 19 + 4i. */
+typedef struct {
+  void* codes;
+  float *low, *step;
+  int64_t row, head, ld;
+  int32_t bits; /* 8 or 4 */
+} gs_codes;
+
+/* Tokens brought to codes as they are written into a cache, and read back.  The
+ * tokens of a document are the last q_len of its k_len keys: token i goes to row
+ * k_start + k_len - q_len + i of both caches (documents as for gs_attention_fwd,
+ * which then describe the step; one whose q_len is k_len is read or written
+ * whole).  Key ranges of documents that are written are disjoint.  Per head,
+ *   low = min x, step = (max x - min x) / (2^bits - 1),
+ *   code = (2^bits - 1) (x - low) / (max x - min x) to the nearest whole number
+ * (even at a tie), and read x = low + step code in fp32, rounded once.  A span
+ * below 2^-116 counts as none (step 0, codes 0); a head that holds an infinity or
+ * a NaN, or spans 2^127 or more, gets low and step NaN and codes 0.  A token
+ * without a key (q_len > k_len) is not written, and read as 0.  Other rows of the
+ * caches, and of the outputs, are left as they are.  head_dim is a multiple of
+ * 16, at most 128.  At most 2^20 documents. */
+typedef struct {
+  int32_t dtype; /* gs_dtype of the tokens */
+  int32_t heads, head_dim;
+} gs_cache_config;
+
+GS_API gs_status gs_cache_write(const gs_cache_config* cfg, const gs_documents* docs,
+                                int64_t rows_q, int64_t rows_k, const gs_heads* k,
+                                const gs_heads* v, const gs_codes* k_cache,
+                                const gs_codes* v_cache, void* stream);
+GS_API gs_status gs_cache_read(const gs_cache_config* cfg, const gs_documents* docs,
+                               int64_t rows_q, int64_t rows_k, const gs_codes* k_cache,
+                               const gs_codes* v_cache, const gs_heads* k, const gs_heads* v,
+                               void* stream);
+
+/* gs_attention_fwd over caches of codes: the same configuration, documents,
+ * scores and outputs, with keys and values low + step code.  Made for few new
+ * tokens a document.  shared (NULL: none) are keys that the tokens of many
+ * documents have in front of their own and that are read once for all of them:
+ * documents again, whose tokens (q_start, q_len) are all the tokens that share
+ * the keys (k_start, k_len) of the caches; each of these sees all of them, and of
+ * its own document what it sees without.  Their token ranges are disjoint, their
+ * prefix is not read, and slopes need shared = NULL (a distance to a shared key
+ * is not defined).  Tokens outside docs are not written.
+ * bits, head_dim and heads of both caches are alike; head_dim is a multiple of
+ * 16, at most 128; at most 2^20 documents and 2^20 shared ones.  Softmax weights
+ * times step are rounded to fp16, relative to a power of two near the largest
+ * step seen.  Values are below 2^100.  A key or value that is not seen has no
+ * effect, also one that is NaN.  Results are the same bits every time. */
+GS_API size_t gs_cached_attention_fwd_workspace_size(const gs_attention_config* cfg, int32_t bits,
+                                                     const gs_documents* docs,
+                                                     const gs_documents* shared, int64_t rows_q,
+                                                     int64_t rows_k);
+GS_API gs_status gs_cached_attention_fwd(const gs_attention_config* cfg, const gs_documents* docs,
+                                         const gs_documents* shared, int64_t rows_q,
+                                         int64_t rows_k, const gs_heads* q,
+                                         const gs_codes* k_cache, const gs_codes* v_cache,
+                                         const gs_heads* out, float* lse, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
