@@ -52,6 +52,7 @@ struct CachedArgs {
   uint32_t units, block0;
 };
 
+constexpr int kManyTiles = 2;   // column tiles of a workgroup, where there are many columns
 constexpr int kStepKeys = 128;  // keys the four wavefronts take at a time
 
 // Keys of a piece of a document of kl keys.
@@ -184,101 +185,83 @@ struct ValueCodes {
   }
 };
 
-typedef f32x4 f32x4_unaligned __attribute__((aligned(4)));
+// Numbers of a wavefront's 32 keys in LDS: what scores are multiplied by and what is
+// added, the same of weights.
+constexpr int kNumbers = 4 * 32;
 
-// The codes of 32 keys, and their numbers, as a lane has them.
+// The codes of 32 keys as a lane has them.  Rows of the cache are reached through
+// a buffer descriptor that ends with the last of `valid` rows: codes of keys past
+// that, and of elements past dim, whose offset is past every end, are zero.
 template <int kBits, int DT>
-struct KeyTile {
-  static constexpr int kPieces = DT / 64;           // of 16 elements, of a key, a lane
-  static constexpr int kPieceWords = kBits / 2;     // of such a piece
-  typedef ValueCodes<kBits, DT> V;
-  uint32_t k[2][kPieces * kPieceWords];
-  uint32_t v[8][V::kWords];
-  f32x4 kstep[2], klow[2], vstep[2], vlow[2];
-
-  // keys row .. of the cache, `valid` of them: codes of keys past that are zero.
-  // Their numbers are whatever stands there.
-  __device__ inline void load(const CachedArgs& a, int hk, int64_t row, int valid) {
-    const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
-    const int bytes = a.dim * kBits / 8;
-    const auto from_k = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(a.kc + row * a.kc_row + hk * a.kc_head), 0,
-        (int)((valid - 1) * a.kc_row) + bytes, 0x00027000);
-    const auto from_v = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(a.vc + row * a.vc_row + hk * a.vc_head), 0,
-        (int)((valid - 1) * a.vc_row) + bytes, 0x00027000);
-    const int kRow = (int)a.kc_row, vRow = (int)a.vc_row;
+struct KeyRows {
+  static constexpr int kPieces = DT / 64;        // of 16 elements, of a key, a lane
+  static constexpr int kPieceWords = kBits / 2;  // of such a piece
+  uint32_t w[2][kPieces * kPieceWords];
+  __device__ inline void load(const uint8_t* base, int row, int valid, int dim) {
+    const int n = threadIdx.x & 15, kg = (threadIdx.x & 63) >> 4;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(base), 0, valid > 0 ? (valid - 1) * row + dim * kBits / 8 : 0,
+        0x00027000);
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int e = kg * (DT / 4) + 16 * i;
-        const int at = e < a.dim ? (16 * t + n) * kRow + e * kBits / 8 : (int)0x80000000;
-        uint32_t* to = k[t] + i * kPieceWords;
+        const int at = e < dim ? (16 * t + n) * row + e * kBits / 8 : (int)0x80000000;
+        uint32_t* to = w[t] + i * kPieceWords;
         if constexpr (kBits == 8) {
-          const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(from_k, at, 0, 0);
-          to[0] = w.x; to[1] = w.y; to[2] = w.z; to[3] = w.w;
+          const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0);
+          to[0] = x.x; to[1] = x.y; to[2] = x.z; to[3] = x.w;
         } else {
-          const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(from_k, at, 0, 0);
-          to[0] = w.x; to[1] = w.y;
+          const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rsrc, at, 0, 0);
+          to[0] = x.x; to[1] = x.y;
         }
       }
+  }
+};
+template <int kBits, int DT>
+struct ValueRows {
+  typedef ValueCodes<kBits, DT> V;
+  uint32_t w[8][V::kWords];
+  __device__ inline void load(const uint8_t* base, int row, int valid, int dim) {
+    const int n = threadIdx.x & 15, kg = (threadIdx.x & 63) >> 4;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(base), 0, valid > 0 ? (valid - 1) * row + dim * kBits / 8 : 0,
+        0x00027000);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int key = 16 * (j >> 2) + 4 * kg + (j & 3);
-      const int at = V::first_of(n) < a.dim ? key * vRow + V::byte_of(n) : (int)0x80000000;
+      const int at = V::first_of(n) < dim ? key * row + V::byte_of(n) : (int)0x80000000;
       if constexpr (V::kWords == 2) {
-        const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(from_v, at, 0, 0);
-        v[j][0] = w.x; v[j][1] = w.y;
+        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rsrc, at, 0, 0);
+        w[j][0] = x.x; w[j][1] = x.y;
       } else if constexpr (kBits == 4 && DT == 64) {
-        v[j][0] = __builtin_amdgcn_raw_buffer_load_b16(from_v, at, 0, 0);
+        w[j][0] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0);
       } else {
-        v[j][0] = __builtin_amdgcn_raw_buffer_load_b32(from_v, at, 0, 0);
-      }
-    }
-    // Numbers of four keys side by side in one load, unless that would reach
-    // past the end of the arrays: past the last head's last row.
-    const int64_t at_k = hk * a.k_ld + row, at_v = hk * a.v_ld + row;
-    const int64_t end_k = (a.heads_k - 1) * a.k_ld + a.docs.rows_k;
-    const int64_t end_v = (a.heads_k - 1) * a.v_ld + a.docs.rows_k;
-    if (at_k + 32 <= end_k && at_v + 32 <= end_v) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int key = 16 * t + 4 * kg;
-        kstep[t] = *(const f32x4_unaligned*)(a.kstep + at_k + key);
-        klow[t] = *(const f32x4_unaligned*)(a.klow + at_k + key);
-        vstep[t] = *(const f32x4_unaligned*)(a.vstep + at_v + key);
-        vlow[t] = *(const f32x4_unaligned*)(a.vlow + at_v + key);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int key = min(16 * (j >> 2) + 4 * kg + (j & 3), valid - 1);
-        kstep[j >> 2][j & 3] = a.kstep[at_k + key];
-        klow[j >> 2][j & 3] = a.klow[at_k + key];
-        vstep[j >> 2][j & 3] = a.vstep[at_v + key];
-        vlow[j >> 2][j & 3] = a.vlow[at_v + key];
+        w[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
       }
     }
   }
 };
 
 // Weights are 2^(score - reference): up to 2^kRoom when the reference is taken,
-// and the reference moves only when a score has passed it by kGrowth more, so
-// they stay below 2^14.
+// and it moves only when a score has passed that by kGrowth, so they stay below
+// 2^14.
 constexpr float kRoom = 8.0f, kGrowth = 6.0f;
 
-template <typename T, int kBits, int DT, int CT>
-__global__ void __launch_bounds__(256, CT == 1 ? 2 : 1) cached_attention_kernel(CachedArgs a) {
+// kGeneral: capped scores or a distance bias.
+template <typename T, int kBits, int DT, int CT, bool kGeneral>
+__global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 2 : 1)
+    cached_attention_kernel(CachedArgs a) {
   typedef KeyCodes<T, kBits> K;
-  typedef KeyTile<kBits, DT> Tile;
-  typedef typename Tile::V V;
+  typedef ValueCodes<kBits, DT> V;
   typedef typename Mat16<T>::V8 V8;
   constexpr int kSteps = DT / 32;    // of the scores' contraction
   constexpr int kElems = V::kElems;  // products of 16 elements of the values
   constexpr int kStride = DT + 4;
   __shared__ __align__(16) float s_o[4][16][kStride];
   __shared__ float s_m[4][16], s_l[4][16], s_c[4][16];
+  __shared__ __align__(16) float s_num[4][kNumbers];
   const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
   const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // All heads of the same keys go to one XCD, one after the other: rows of
@@ -305,6 +288,16 @@ __global__ void __launch_bounds__(256, CT == 1 ? 2 : 1) cached_attention_kernel(
   const int keys = piece_keys(d.kl, a.pieces);
   if (piece > 0 && (int64_t)piece * keys >= d.kl) return;
   const int key0 = piece * keys;
+  const uint8_t* const kc = a.kc + (int64_t)d.ks * a.kc_row + hk * a.kc_head;
+  const uint8_t* const vc = a.vc + (int64_t)d.ks * a.vc_row + hk * a.vc_head;
+  // Numbers of a key: lanes 0..31 have the 32 keys' own, lanes 32..63 their
+  // values'.  Each is brought to what a score or a weight needs of it by its one
+  // lane, and goes through LDS to those that use it.
+  const bool of_values = lane >= 32;
+  const int64_t num_at = of_values ? hk * a.v_ld + d.ks : hk * a.k_ld + d.ks;
+  const float* const lows = (of_values ? a.vlow : a.klow) + num_at;
+  const float* const steps = (of_values ? a.vstep : a.kstep) + num_at;
+  float* const nums = s_num[wave];
 
   const float to_log2 = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
   const float cap = a.softcap * kLog2e;
@@ -335,7 +328,7 @@ __global__ void __launch_bounds__(256, CT == 1 ? 2 : 1) cached_attention_kernel(
       qsum[ct] = across_sum(sum);
       limit[ct] = key_limit(a, d, token);
       pos[ct] = token + d.kl - d.ql;
-      slope[ct] = a.slopes ? a.slopes[head] * kLog2e : 0.0f;
+      slope[ct] = kGeneral && a.slopes ? a.slopes[head] * kLog2e : 0.0f;
     }
     const int last_col = min(col0 + 16 * CT, cols) - 1;
     const int all_see = key_limit(a, d, col0 / a.group);
@@ -343,51 +336,44 @@ __global__ void __launch_bounds__(256, CT == 1 ? 2 : 1) cached_attention_kernel(
         min((int)min((int64_t)d.kl, (int64_t)key0 + keys), key_limit(a, d, last_col / a.group));
 
     f32x4 o[CT][kElems];
-    float m[CT], ref[CT], l[CT], mean[CT];
+    // weights are relative to ref; a score above most moves it
+    float ref[CT], most[CT], l[CT], mean[CT];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      m[ct] = -INFINITY;
+      most[ct] = -INFINITY;
       ref[ct] = l[ct] = mean[ct] = 0.0f;
 #pragma unroll
       for (int e = 0; e < kElems; ++e) o[ct][e] = (f32x4)(0.0f);
     }
     // steps are taken relative to unit_step, a power of two
     float unit_step = 0x1p-126f;
-    Tile tile, next;
+    KeyRows<kBits, DT> kr;
+    ValueRows<kBits, DT> vr;
+    float low = 0.0f, step = 0.0f;
+    auto load_keys = [&](int key) {
+      kr.load(kc + (int64_t)key * a.kc_row, (int)a.kc_row, key < key_end ? min(32, d.kl - key) : 0,
+              a.dim);
+    };
+    auto load_values = [&](int key) {
+      vr.load(vc + (int64_t)key * a.vc_row, (int)a.vc_row, key < key_end ? min(32, d.kl - key) : 0,
+              a.dim);
+    };
+    auto load_numbers = [&](int key) {
+      if (key >= key_end) return;
+      const int at = key + min(lane & 31, d.kl - key - 1);
+      low = lows[at];
+      step = steps[at];
+    };
     int key = key0 + 32 * wave;
-    if (key < key_end) next.load(a, hk, (int64_t)d.ks + key, min(32, d.kl - key));
+    load_numbers(key);
+    load_keys(key);
+    load_values(key);
     for (; key < key_end; key += kStepKeys) {
-      tile = next;
-      if (key + kStepKeys < key_end)
-        next.load(a, hk, (int64_t)d.ks + key + kStepKeys, min(32, d.kl - key - kStepKeys));
-      f32x4 s[2][CT];
-#pragma unroll
-      for (int ct = 0; ct < CT; ++ct) s[0][ct] = s[1][ct] = (f32x4)(0.0f);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          const V8 x = K::operand(tile.k[t] + i * kBits / 4);
-#pragma unroll
-          for (int ct = 0; ct < CT; ++ct) s[t][ct] = Mat16<T>::mul(x, q[ct][i], s[t][ct]);
-        }
       const bool masked = key + 32 > all_see || key + 32 > key_end;
-      float kmul[8], kadd[8], vmul[8], vadd[8];
-      float steps = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int t = j >> 2, r = j & 3;
-        const float ks = tile.kstep[t][r], kl = tile.klow[t][r];
-        kmul[j] = ks * (K::kMul * to_log2);
-        kadd[j] = fmaf(ks, K::kOff, kl) * to_log2;
-        vmul[j] = tile.vstep[t][r];
-        vadd[j] = fmaf(vmul[j], V::kMid, tile.vlow[t][r]);
-        // what no column sees has no part in the range of the weights
-        if (masked && key + 16 * t + 4 * kg + r >= key_end) vmul[j] = 0.0f;
-        steps = vmul[j] < __builtin_huge_valf() ? fmaxf(steps, vmul[j]) : steps;
-      }
-      if (__ballot(steps >= 2.0f * unit_step)) {
-        float top = steps;
+      // what no column sees has no part in the range of the weights
+      const float st = of_values && key + (lane & 31) >= key_end ? 0.0f : step;
+      if (__ballot(of_values && st >= 2.0f * unit_step && st < __builtin_huge_valf())) {
+        float top = of_values && st < __builtin_huge_valf() ? st : 0.0f;
 #pragma unroll
         for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
         const float now =
@@ -399,70 +385,113 @@ __global__ void __launch_bounds__(256, CT == 1 ? 2 : 1) cached_attention_kernel(
 #pragma unroll
           for (int e = 0; e < kElems; ++e) o[ct][e] *= f;
       }
-      const float per_unit = 1.0f / unit_step;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) vmul[j] *= per_unit;
+      nums[2 * (lane & 32) + (lane & 31)] = st * (of_values ? 1.0f / unit_step : K::kMul * to_log2);
+      nums[2 * (lane & 32) + 32 + (lane & 31)] =
+          fmaf(step, of_values ? V::kMid : K::kOff, low) * (of_values ? 1.0f : to_log2);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      load_numbers(key + kStepKeys);
 
+      f32x4 s[2][CT];
+#pragma unroll
+      for (int ct = 0; ct < CT; ++ct) s[0][ct] = s[1][ct] = (f32x4)(0.0f);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const V8 x = K::operand(kr.w[t] + i * kBits / 4);
+#pragma unroll
+          for (int ct = 0; ct < CT; ++ct) s[t][ct] = Mat16<T>::mul(x, q[ct][i], s[t][ct]);
+        }
+      // the keys' registers are free: the next ones come while this tile is
+      // finished
+      load_keys(key + kStepKeys);
+      __builtin_amdgcn_sched_barrier(0);
+
+      const int first = key + 4 * kg;  // this lane's keys: first + 0..3 and 16 + 0..3
       f16x8 w[CT];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) {
-        float x[8], top = -INFINITY;
+        float y[8], top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int t = j >> 2, r = j & 3;
-          x[j] = fmaf(s[t][ct][r], kmul[j], kadd[j] * qsum[ct]);
+        for (int t = 0; t < 2; ++t) {
+          const f32x4 kmul = *(const f32x4*)(nums + 16 * t + 4 * kg);
+          const f32x4 kadd = *(const f32x4*)(nums + 32 + 16 * t + 4 * kg);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float& z = y[4 * t + r];
+            if constexpr (!kGeneral) {
+              z = fmaf(s[t][ct][r], kmul[r], fmaf(kadd[r], qsum[ct], -ref[ct]));
+            } else {
+              z = fmaf(s[t][ct][r], kmul[r], kadd[r] * qsum[ct]);
+            }
+          }
         }
-        if (a.softcap > kWideCap) {
+        if constexpr (kGeneral) {
+          if (a.softcap > kWideCap) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = cap * tanh_wide(x[j]);
-        } else if (a.softcap > 0.0f) {
+            for (int j = 0; j < 8; ++j) y[j] = cap * tanh_wide(y[j]);
+          } else if (a.softcap > 0.0f) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = cap * tanh_of(x[j]);
-        }
-        const int first = key + 4 * kg;  // keys first + 0..3 and 16 + 0..3
-        if (a.slopes) {
+            for (int j = 0; j < 8; ++j) y[j] = cap * tanh_of(y[j]);
+          }
+          // slope 0: no bias
+          const float at = (float)(pos[ct] - first);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            x[j] = fmaf(-slope[ct],
-                        fabsf((float)(pos[ct] - first - (16 * (j >> 2) + (j & 3)))), x[j]);
+            y[j] = fmaf(-slope[ct], fabsf(at - (float)(16 * (j >> 2) + (j & 3))), y[j]) - ref[ct];
         }
         if (masked) {
           const int end = min(limit[ct], key_end) - first;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = 16 * (j >> 2) + (j & 3) < end ? x[j] : -INFINITY;
+          for (int j = 0; j < 8; ++j) y[j] = 16 * (j >> 2) + (j & 3) < end ? y[j] : -INFINITY;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, x[j]);
-        if (__ballot(top > m[ct] + kGrowth)) {
-          const float now = fmaxf(m[ct], across_max(top));
-          const float f = m[ct] == now ? 1.0f : __builtin_amdgcn_exp2f(m[ct] - now);
-          m[ct] = now;
-          ref[ct] = now == -INFINITY ? 0.0f : now - kRoom;
-          l[ct] *= f;
-          mean[ct] *= f;
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, y[j]);
+        if (__ballot(top > most[ct])) {
+          top = across_max(top);
+          const float over = top > (most[ct] == -INFINITY ? -INFINITY : kRoom) ? top - kRoom : 0.0f;
+          const float f = __builtin_amdgcn_exp2f(-over);
+          ref[ct] += over;
+          if (top > -INFINITY) most[ct] = kRoom + kGrowth;
+          // nothing has been summed where the first reference is taken
+          l[ct] = l[ct] == 0.0f ? 0.0f : l[ct] * f;
+          mean[ct] = mean[ct] == 0.0f ? 0.0f : mean[ct] * f;
 #pragma unroll
-          for (int e = 0; e < kElems; ++e) o[ct][e] *= f;
-        }
-        float p[8];
+          for (int e = 0; e < kElems; ++e)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          p[j] = __builtin_amdgcn_exp2f(x[j] - ref[ct]);
-          l[ct] += p[j];
-          // what a column does not see may hold a NaN
-          const bool seen = !masked || x[j] != -INFINITY;
-          mean[ct] = seen ? fmaf(p[j], vadd[j], mean[ct]) : mean[ct];
-          p[j] = seen ? p[j] * vmul[j] : 0.0f;
+            for (int r = 0; r < 4; ++r) o[ct][e][r] = o[ct][e][r] == 0.0f ? 0.0f : o[ct][e][r] * f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] -= over;
         }
-        w[ct] = __builtin_bit_cast(f16x8, u32x4{pack_f16(p[0], p[1]), pack_f16(p[2], p[3]),
-                                                pack_f16(p[4], p[5]), pack_f16(p[6], p[7])});
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const f32x4 vmul = *(const f32x4*)(nums + 64 + 16 * t + 4 * kg);
+          const f32x4 vadd = *(const f32x4*)(nums + 96 + 16 * t + 4 * kg);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float& z = y[4 * t + r];
+            const float p = __builtin_amdgcn_exp2f(z);
+            l[ct] += p;
+            // what a column does not see may hold a NaN
+            const bool seen = !masked || z != -INFINITY;
+            mean[ct] = seen ? fmaf(p, vadd[r], mean[ct]) : mean[ct];
+            z = seen ? p * vmul[r] : 0.0f;
+          }
+        }
+        w[ct] = __builtin_bit_cast(f16x8, u32x4{pack_f16(y[0], y[1]), pack_f16(y[2], y[3]),
+                                                pack_f16(y[4], y[5]), pack_f16(y[6], y[7])});
       }
 #pragma unroll
       for (int e = 0; e < kElems; ++e) {
-        const f16x8 x = V::operand(tile.v, e);
+        const f16x8 x = V::operand(vr.w, e);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
           o[ct][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w[ct], o[ct][e], 0, 0, 0);
       }
+      load_values(key + kStepKeys);
+      __builtin_amdgcn_sched_barrier(0);
     }
 
     // The four wavefronts' sums, 16 columns at a time: 16 lanes a column.
@@ -600,7 +629,7 @@ namespace {
 
 // How a pass is cut: columns of a tile, tiles, pieces of a document's keys.
 struct Cut {
-  int tiles;  // of 16 columns, a workgroup: 1 or 4
+  int tiles;  // of 16 columns, a workgroup: 1 or kManyTiles
   bool looked_up;
   int64_t units;
   int pieces;
@@ -611,7 +640,7 @@ Cut cut_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q
   const int64_t group = cfg.heads_q / cfg.heads_k;
   const int64_t longest_q = d.max_q_len > 0 && d.max_q_len < rows_q ? d.max_q_len : rows_q;
   const int64_t longest_k = d.max_k_len > 0 && d.max_k_len < rows_k ? d.max_k_len : rows_k;
-  o.tiles = longest_q * group <= 16 ? 1 : 4;
+  o.tiles = longest_q * group <= 16 ? 1 : kManyTiles;
   o.looked_up = longest_q * group > 16 * o.tiles;
   o.units = o.looked_up ? rows_q * group / (16 * o.tiles) + d.count : d.count;
   const int64_t base = o.units * cfg.heads_k;
@@ -640,7 +669,7 @@ Plan plan_of(const gs_attention_config& cfg, const gs_documents& d, const gs_doc
 
 size_t ml_bytes(const Plan& p) { return ((size_t)p.slots * 8 + 255) / 256 * 256; }
 
-template <typename T, int kBits, int DT>
+template <typename T, int kBits, int DT, bool kGeneral>
 hipError_t pass(CachedArgs a, const Cut& c, hipStream_t s) {
   a.pieces = c.pieces;
   a.looked_up = c.looked_up;
@@ -648,22 +677,22 @@ hipError_t pass(CachedArgs a, const Cut& c, hipStream_t s) {
   const int64_t blocks = (c.units * c.pieces + 7) / 8 * 8 * a.heads_k;
   return launch_all(blocks, 256, [&](uint32_t first, dim3 n) {
     a.block0 = first;
-    if (c.tiles == 1) cached_attention_kernel<T, kBits, DT, 1><<<n, 256, 0, s>>>(a);
-    else cached_attention_kernel<T, kBits, DT, 4><<<n, 256, 0, s>>>(a);
+    if (c.tiles == 1) cached_attention_kernel<T, kBits, DT, 1, kGeneral><<<n, 256, 0, s>>>(a);
+    else cached_attention_kernel<T, kBits, DT, kManyTiles, kGeneral><<<n, 256, 0, s>>>(a);
   });
 }
 
-template <typename T, int kBits, int DT>
+template <typename T, int kBits, int DT, bool kGeneral>
 hipError_t run(const CachedArgs& a, const Plan& p, const Docs& shared, hipStream_t s) {
   if (p.shared.pieces > 0) {
     CachedArgs b = a;
     b.docs = shared;
     b.causal = 0;
     b.first_piece = p.own.pieces;
-    const hipError_t e = pass<T, kBits, DT>(b, p.shared, s);
+    const hipError_t e = pass<T, kBits, DT, kGeneral>(b, p.shared, s);
     if (e != hipSuccess) return e;
   }
-  const hipError_t e = pass<T, kBits, DT>(a, p.own, s);
+  const hipError_t e = pass<T, kBits, DT, kGeneral>(a, p.own, s);
   if (e != hipSuccess || p.whole) return e;
   CachedArgs j = a;
   j.shared = shared;
@@ -674,6 +703,12 @@ hipError_t run(const CachedArgs& a, const Plan& p, const Docs& shared, hipStream
                       j.block0 = first;
                       cached_join_kernel<T><<<n, 256, 0, s>>>(j);
                     });
+}
+
+template <typename T, int kBits, int DT>
+hipError_t run(const CachedArgs& a, const Plan& p, const Docs& shared, hipStream_t s) {
+  return a.softcap > 0.0f || a.slopes ? run<T, kBits, DT, true>(a, p, shared, s)
+                                      : run<T, kBits, DT, false>(a, p, shared, s);
 }
 
 template <typename T>
