@@ -45,7 +45,8 @@ struct CachedArgs {
   float* lse;
   float* part_ml;  // [pieces][heads_q][rows_q][2]
   float* part_o;   // [pieces][heads_q][rows_q][dim]
-  int pieces, pieces_shared;
+  int pieces, pieces_shared;  // at most, of a document
+  int piece, piece_shared;    // keys of one
   int first_piece;  // of this pass, in the arrays above
   int whole;        // one piece and nothing shared: the result is written at once
   int looked_up;    // column tiles are units of the grid, else documents
@@ -55,10 +56,12 @@ struct CachedArgs {
 constexpr int kManyTiles = 2;   // column tiles of a workgroup, where there are many columns
 constexpr int kStepKeys = 128;  // keys the four wavefronts take at a time
 
-// Keys of a piece of a document of kl keys.
-__device__ inline int piece_keys(int kl, int pieces) {
+// Keys of a piece of a document of kl keys.  Pieces have one size in all
+// documents, so that long ones do not end late; one that is longer than the
+// caller said gets larger pieces.
+__device__ inline int piece_keys(int kl, int pieces, int piece) {
   const int n = (int)(((int64_t)kl + pieces - 1) / pieces);
-  return max((n + kStepKeys - 1) / kStepKeys * kStepKeys, 2 * kStepKeys);
+  return max((n + kStepKeys - 1) / kStepKeys * kStepKeys, piece);
 }
 
 // Token i sees the keys below this.
@@ -197,23 +200,31 @@ struct KeyRows {
   static constexpr int kPieces = DT / 64;        // of 16 elements, of a key, a lane
   static constexpr int kPieceWords = kBits / 2;  // of such a piece
   uint32_t w[2][kPieces * kPieceWords];
-  __device__ inline void load(const uint8_t* base, int row, int valid, int dim) {
+  uint32_t at[kPieces];  // of this lane's first key
+  __device__ inline void start(int row, int dim) {
     const int n = threadIdx.x & 15, kg = (threadIdx.x & 63) >> 4;
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(base), 0, valid > 0 ? (valid - 1) * row + dim * kBits / 8 : 0,
-        0x00027000);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int e = kg * (DT / 4) + 16 * i;
+      at[i] = e < dim ? (uint32_t)(n * row + e * kBits / 8) : 0x80000000u;
+      // not to be taken for one of two constants, with a branch for each
+      asm("" : "+v"(at[i]));
+    }
+  }
+  __device__ inline void load(const uint8_t* base, int row, int bytes) {
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, bytes,
+                                                        0x00027000);
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const int e = kg * (DT / 4) + 16 * i;
-        const int at = e < dim ? (16 * t + n) * row + e * kBits / 8 : (int)0x80000000;
+        const int from = (int)(at[i] + (uint32_t)(16 * t * row));
         uint32_t* to = w[t] + i * kPieceWords;
         if constexpr (kBits == 8) {
-          const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, 0, 0);
+          const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rsrc, from, 0, 0);
           to[0] = x.x; to[1] = x.y; to[2] = x.z; to[3] = x.w;
         } else {
-          const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rsrc, at, 0, 0);
+          const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rsrc, from, 0, 0);
           to[0] = x.x; to[1] = x.y;
         }
       }
@@ -223,22 +234,25 @@ template <int kBits, int DT>
 struct ValueRows {
   typedef ValueCodes<kBits, DT> V;
   uint32_t w[8][V::kWords];
-  __device__ inline void load(const uint8_t* base, int row, int valid, int dim) {
+  uint32_t at;  // of this lane's first key
+  __device__ inline void start(int row, int dim) {
     const int n = threadIdx.x & 15, kg = (threadIdx.x & 63) >> 4;
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(base), 0, valid > 0 ? (valid - 1) * row + dim * kBits / 8 : 0,
-        0x00027000);
+    at = V::first_of(n) < dim ? (uint32_t)(4 * kg * row + V::byte_of(n)) : 0x80000000u;
+    asm("" : "+v"(at));
+  }
+  __device__ inline void load(const uint8_t* base, int row, int bytes) {
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, bytes,
+                                                        0x00027000);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int key = 16 * (j >> 2) + 4 * kg + (j & 3);
-      const int at = V::first_of(n) < dim ? key * row + V::byte_of(n) : (int)0x80000000;
+      const int from = (int)(at + (uint32_t)((16 * (j >> 2) + (j & 3)) * row));
       if constexpr (V::kWords == 2) {
-        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rsrc, at, 0, 0);
+        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rsrc, from, 0, 0);
         w[j][0] = x.x; w[j][1] = x.y;
       } else if constexpr (kBits == 4 && DT == 64) {
-        w[j][0] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0);
+        w[j][0] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, from, 0, 0);
       } else {
-        w[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
+        w[j][0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, from, 0, 0);
       }
     }
   }
@@ -249,8 +263,9 @@ struct ValueRows {
 // 2^14.
 constexpr float kRoom = 8.0f, kGrowth = 6.0f;
 
-// kGeneral: capped scores or a distance bias.
-template <typename T, int kBits, int DT, int CT, bool kGeneral>
+// kMode: plain scores, capped ones, or a distance bias (with or without a cap).
+constexpr int kPlain = 0, kCapped = 1, kBiased = 2;
+template <typename T, int kBits, int DT, int CT, int kMode>
 __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 2 : 1)
     cached_attention_kernel(CachedArgs a) {
   typedef KeyCodes<T, kBits> K;
@@ -285,7 +300,7 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 
     d = load_doc(a.docs, (int)unit);
   }
   const int cols = d.ql * a.group;
-  const int keys = piece_keys(d.kl, a.pieces);
+  const int keys = piece_keys(d.kl, a.pieces, a.piece);
   if (piece > 0 && (int64_t)piece * keys >= d.kl) return;
   const int key0 = piece * keys;
   const uint8_t* const kc = a.kc + (int64_t)d.ks * a.kc_row + hk * a.kc_head;
@@ -302,6 +317,35 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 
   const float to_log2 = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
   const float cap = a.softcap * kLog2e;
   for (int col0 = col_first; col0 < min(col_end, cols); col0 += 16 * CT) {
+    const int last_col = min(col0 + 16 * CT, cols) - 1;
+    const int all_see = key_limit(a, d, col0 / a.group);
+    const int key_end =
+        min((int)min((int64_t)d.kl, (int64_t)key0 + keys), key_limit(a, d, last_col / a.group));
+    // the first tile is on its way before the queries are looked at
+    KeyRows<kBits, DT> kr;
+    ValueRows<kBits, DT> vr;
+    float low = 0.0f, step = 0.0f;
+    int key = key0 + 32 * wave;
+    const uint8_t* kp = kc + (int64_t)key * a.kc_row;
+    const uint8_t* vp = vc + (int64_t)key * a.vc_row;
+    const int k_row = (int)a.kc_row, v_row = (int)a.vc_row, head_bytes = a.dim * kBits / 8;
+    kr.start(k_row, a.dim);
+    vr.start(v_row, a.dim);
+    // bytes from a tile's first key to its last one's end; none past the end
+    auto bytes_of = [&](int at, int row) {
+      const int valid = min(32, d.kl - at);
+      return at < key_end ? (valid - 1) * row + head_bytes : 0;
+    };
+    auto load_numbers = [&](int key) {
+      if (key >= key_end) return;
+      const int at = key + min(lane & 31, d.kl - key - 1);
+      low = lows[at];
+      step = steps[at];
+    };
+    load_numbers(key);
+    kr.load(kp, k_row, bytes_of(key, k_row));
+    vr.load(vp, v_row, bytes_of(key, v_row));
+
     // Columns past the last one repeat it, and are not stored.
     V8 q[CT][kSteps];
     float qsum[CT], slope[CT];
@@ -328,13 +372,8 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 
       qsum[ct] = across_sum(sum);
       limit[ct] = key_limit(a, d, token);
       pos[ct] = token + d.kl - d.ql;
-      slope[ct] = kGeneral && a.slopes ? a.slopes[head] * kLog2e : 0.0f;
+      slope[ct] = kMode == kBiased ? a.slopes[head] * kLog2e : 0.0f;
     }
-    const int last_col = min(col0 + 16 * CT, cols) - 1;
-    const int all_see = key_limit(a, d, col0 / a.group);
-    const int key_end =
-        min((int)min((int64_t)d.kl, (int64_t)key0 + keys), key_limit(a, d, last_col / a.group));
-
     f32x4 o[CT][kElems];
     // weights are relative to ref; a score above most moves it
     float ref[CT], most[CT], l[CT], mean[CT];
@@ -346,28 +385,7 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 
       for (int e = 0; e < kElems; ++e) o[ct][e] = (f32x4)(0.0f);
     }
     // steps are taken relative to unit_step, a power of two
-    float unit_step = 0x1p-126f;
-    KeyRows<kBits, DT> kr;
-    ValueRows<kBits, DT> vr;
-    float low = 0.0f, step = 0.0f;
-    auto load_keys = [&](int key) {
-      kr.load(kc + (int64_t)key * a.kc_row, (int)a.kc_row, key < key_end ? min(32, d.kl - key) : 0,
-              a.dim);
-    };
-    auto load_values = [&](int key) {
-      vr.load(vc + (int64_t)key * a.vc_row, (int)a.vc_row, key < key_end ? min(32, d.kl - key) : 0,
-              a.dim);
-    };
-    auto load_numbers = [&](int key) {
-      if (key >= key_end) return;
-      const int at = key + min(lane & 31, d.kl - key - 1);
-      low = lows[at];
-      step = steps[at];
-    };
-    int key = key0 + 32 * wave;
-    load_numbers(key);
-    load_keys(key);
-    load_values(key);
+    float unit_step = 0x1p-126f, per_unit = 0x1p126f;
     for (; key < key_end; key += kStepKeys) {
       const bool masked = key + 32 > all_see || key + 32 > key_end;
       // what no column sees has no part in the range of the weights
@@ -380,12 +398,13 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 
             __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, top) & 0x7f800000u);
         const float f = unit_step / now;
         unit_step = now;
+        per_unit = 1.0f / now;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
           for (int e = 0; e < kElems; ++e) o[ct][e] *= f;
       }
-      nums[2 * (lane & 32) + (lane & 31)] = st * (of_values ? 1.0f / unit_step : K::kMul * to_log2);
+      nums[2 * (lane & 32) + (lane & 31)] = st * (of_values ? per_unit : K::kMul * to_log2);
       nums[2 * (lane & 32) + 32 + (lane & 31)] =
           fmaf(step, of_values ? V::kMid : K::kOff, low) * (of_values ? 1.0f : to_log2);
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -406,7 +425,8 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 
         }
       // the keys' registers are free: the next ones come while this tile is
       // finished
-      load_keys(key + kStepKeys);
+      kp += (int64_t)kStepKeys * k_row;
+      kr.load(kp, k_row, bytes_of(key + kStepKeys, k_row));
       __builtin_amdgcn_sched_barrier(0);
 
       const int first = key + 4 * kg;  // this lane's keys: first + 0..3 and 16 + 0..3
@@ -421,26 +441,30 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             float& z = y[4 * t + r];
-            if constexpr (!kGeneral) {
+            if constexpr (kMode == kPlain) {
               z = fmaf(s[t][ct][r], kmul[r], fmaf(kadd[r], qsum[ct], -ref[ct]));
             } else {
               z = fmaf(s[t][ct][r], kmul[r], kadd[r] * qsum[ct]);
             }
           }
         }
-        if constexpr (kGeneral) {
+        if constexpr (kMode != kPlain) {
           if (a.softcap > kWideCap) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = cap * tanh_wide(y[j]);
-          } else if (a.softcap > 0.0f) {
+            for (int j = 0; j < 8; ++j) y[j] = fmaf(cap, tanh_wide(y[j]), -ref[ct]);
+          } else if (kMode == kCapped || a.softcap > 0.0f) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = cap * tanh_of(y[j]);
+            for (int j = 0; j < 8; ++j) y[j] = fmaf(cap, tanh_of(y[j]), -ref[ct]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] -= ref[ct];
           }
-          // slope 0: no bias
+        }
+        if constexpr (kMode == kBiased) {
           const float at = (float)(pos[ct] - first);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            y[j] = fmaf(-slope[ct], fabsf(at - (float)(16 * (j >> 2) + (j & 3))), y[j]) - ref[ct];
+            y[j] = fmaf(-slope[ct], fabsf(at - (float)(16 * (j >> 2) + (j & 3))), y[j]);
         }
         if (masked) {
           const int end = min(limit[ct], key_end) - first;
@@ -474,10 +498,15 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 
             float& z = y[4 * t + r];
             const float p = __builtin_amdgcn_exp2f(z);
             l[ct] += p;
-            // what a column does not see may hold a NaN
-            const bool seen = !masked || z != -INFINITY;
-            mean[ct] = seen ? fmaf(p, vadd[r], mean[ct]) : mean[ct];
-            z = seen ? p * vmul[r] : 0.0f;
+            if (!masked) {
+              mean[ct] = fmaf(p, vadd[r], mean[ct]);
+              z = p * vmul[r];
+            } else {
+              // what a column does not see may hold a NaN
+              const bool seen = z != -INFINITY;
+              mean[ct] = seen ? fmaf(p, vadd[r], mean[ct]) : mean[ct];
+              z = seen ? p * vmul[r] : 0.0f;
+            }
           }
         }
         w[ct] = __builtin_bit_cast(f16x8, u32x4{pack_f16(y[0], y[1]), pack_f16(y[2], y[3]),
@@ -490,7 +519,8 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 
         for (int ct = 0; ct < CT; ++ct)
           o[ct][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w[ct], o[ct][e], 0, 0, 0);
       }
-      load_values(key + kStepKeys);
+      vp += (int64_t)kStepKeys * v_row;
+      vr.load(vp, v_row, bytes_of(key + kStepKeys, v_row));
       __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -554,21 +584,26 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 
   }
 }
 
-// A token's pieces, and those of the keys it shares: a wavefront a head, two
-// elements a lane.
-template <typename T>
-__global__ void __launch_bounds__(256) cached_join_kernel(CachedArgs a) {
-  const int lane = threadIdx.x & 63;
-  const uint32_t heads = (uint32_t)(a.heads_q + 3) / 4;
+// A token's pieces of one head, and those of the keys it shares: kLanes lanes
+// have the head's elements, four each, and the groups of so many lanes take
+// pieces in turn; what they found meets in LDS.  kThreads is 64 where there are
+// few pieces, else 256.
+constexpr int kMostPieces = 256;  // of a pass
+template <typename T, int kLanes, int kThreads>
+__global__ void __launch_bounds__(kThreads) cached_join_kernel(CachedArgs a) {
+  constexpr int kGroups = kThreads / kLanes, kWaves = kThreads / 64;
+  __shared__ float s_f[2 * kMostPieces], s_top[kWaves], s_sum[kWaves];
+  __shared__ __align__(16) f32x4 s_o[kGroups][kLanes];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t block = a.block0 + blockIdx.x;
-  const int head = (int)(block % heads) * 4 + (threadIdx.x >> 6);
+  const int head = (int)(block % (uint32_t)a.heads_q);
   uint32_t local, units;
   Doc d;
-  if (find_document<false>(a.docs, 1, 1, block / heads, &local, &units, &d) < 0) return;
-  if (head >= a.heads_q) return;
+  if (find_document<false>(a.docs, 1, 1, block / (uint32_t)a.heads_q, &local, &units, &d) < 0)
+    return;
   const int64_t token = d.qs + (int)local;
-  const int own = max(1, (int)(((int64_t)d.kl + piece_keys(d.kl, a.pieces) - 1) /
-                               piece_keys(d.kl, a.pieces)));
+  const int size = piece_keys(d.kl, a.pieces, a.piece);
+  const int own = max(1, (int)(((int64_t)d.kl + size - 1) / size));
   int more = 0;
   for (int base = 0; base < a.shared.count; base += 64) {
     Doc g = {0, 0, 0, 0, 0};
@@ -576,51 +611,67 @@ __global__ void __launch_bounds__(256) cached_join_kernel(CachedArgs a) {
     const uint64_t hit = __ballot(token >= g.qs && token < (int64_t)g.qs + g.ql);
     if (!hit) continue;
     const int kl = __builtin_amdgcn_readlane(g.kl, __ffsll((unsigned long long)hit) - 1);
-    const int n = piece_keys(kl, a.pieces_shared);
+    const int n = piece_keys(kl, a.pieces_shared, a.piece_shared);
     more = (int)(((int64_t)kl + n - 1) / n);
     break;
   }
-  const int e = 2 * lane;
-  float top = -INFINITY, sum = 0.0f, x = 0.0f, y = 0.0f;
-  // pieces in order, 64 at a time
-  for (int base = 0; base < own + more; base += 64) {
-    const int i = base + lane;
-    float m = -INFINITY, l = 0.0f;
-    const auto slot = [&](int p) {
-      return ((int64_t)(p < own ? p : a.pieces + p - own) * a.heads_q + head) * a.docs.rows_q +
-             token;
-    };
-    if (i < own + more) {
-      m = a.part_ml[2 * slot(i)];
-      l = a.part_ml[2 * slot(i) + 1];
-    }
-    float now = l == 0.0f ? -INFINITY : m;
+  const int count = own + more;
+  const auto slot = [&](int p) {
+    return ((int64_t)(p < own ? p : a.pieces + p - own) * a.heads_q + head) * a.docs.rows_q + token;
+  };
+  // what each piece counts for: its sum times 2^(its reference - the largest)
+  float top = -INFINITY;
+  for (int p = threadIdx.x; p < count; p += kThreads) {
+    const f32x2 ml = *(const f32x2*)(a.part_ml + 2 * slot(p));
+    s_f[p] = ml.x;
+    top = ml.y == 0.0f ? top : fmaxf(top, ml.x);
+  }
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) now = fmaxf(now, __shfl_xor(now, o, 64));
-    now = fmaxf(now, top);
-    if (now == -INFINITY && !__ballot(l != 0.0f)) continue;
-    const float old = top == now ? 1.0f : __builtin_amdgcn_exp2f(top - now);
-    top = now;
-    const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-    sum *= old;
-    x *= old;
-    y *= old;
-    const int count = min(64, own + more - base);
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  if (kWaves > 1) {
+    if (lane == 0) s_top[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) top = fmaxf(top, s_top[i]);
+  }
+  float sum = 0.0f;
+  for (int p = threadIdx.x; p < count; p += kThreads) {
+    const float l = a.part_ml[2 * slot(p) + 1];
+    // a piece whose sum is zero holds zeros
+    const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(s_f[p] - top);
+    s_f[p] = f;
+    sum = fmaf(f, l, sum);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if (kWaves > 1 && lane == 0) s_sum[wave] = sum;
+  __syncthreads();
+  if (kWaves > 1) {
+    sum = s_sum[0];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) sum += s_sum[i];
+  }
+  const int group = threadIdx.x / kLanes, e = (threadIdx.x % kLanes) * 4;
+  f32x4 x = (f32x4)(0.0f);
+  if (e < a.dim) {
 #pragma unroll 4
-    for (int p = 0; p < count; ++p) {
-      const float fp = __shfl(f, p, 64), lp = __shfl(l, p, 64);
-      f32x2 v = {0.0f, 0.0f};
-      if (e < a.dim) v = *(const f32x2*)(a.part_o + slot(base + p) * a.dim + e);
-      sum = fmaf(fp, lp, sum);
-      // a piece whose sum is zero holds zeros
-      x = fmaf(fp, v.x, x);
-      y = fmaf(fp, v.y, y);
+    for (int p = group; p < count; p += kGroups) {
+      const f32x4 v = *(const f32x4*)(a.part_o + slot(p) * a.dim + e);
+      const float f = s_f[p];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = fmaf(f, v[i], x[i]);
     }
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  if (e < a.dim)
-    *(uint32_t*)(a.out + token * a.out_row + head * a.out_head + e) = pack2<T>(x * inv, y * inv);
-  if (a.lse && lane == 0)
+  s_o[group][threadIdx.x % kLanes] = x;
+  __syncthreads();
+  if (group == 0 && e < a.dim) {
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) x += s_o[i][threadIdx.x];
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
+    store_elems((T*)(a.out + token * a.out_row + head * a.out_head + e), y);
+  }
+  if (a.lse && threadIdx.x == 0)
     a.lse[(int64_t)head * a.docs.rows_q + token] =
         sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
@@ -632,7 +683,7 @@ struct Cut {
   int tiles;  // of 16 columns, a workgroup: 1 or kManyTiles
   bool looked_up;
   int64_t units;
-  int pieces;
+  int pieces, piece;
 };
 Cut cut_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q,
            int64_t rows_k) {
@@ -644,11 +695,30 @@ Cut cut_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q
   o.looked_up = longest_q * group > 16 * o.tiles;
   o.units = o.looked_up ? rows_q * group / (16 * o.tiles) + d.count : d.count;
   const int64_t base = o.units * cfg.heads_k;
-  const int64_t target = 2048;
+  // Workgroups wanted: two a compute unit where there are many columns or few
+  // documents (us at 512, 768, 1024, 2048: four caches of 120,001 keys in all 45, 47,
+  // 50, 57; 64 requests behind 16,384 shared keys 50, 58, 61, -), more where many
+  // documents of uneven length hide each other's ends (64 caches of 100,003 keys, 8
+  // heads of 64 in 4 bits: 40, 35, 34, 32).
+  const int64_t target = o.tiles == 1 && base >= 256 ? 1536 : 512;
   int64_t pieces = (target + base - 1) / (base > 0 ? base : 1);
-  const int64_t most = (longest_k + 2 * kStepKeys - 1) / (2 * kStepKeys);
+  if (pieces > kMostPieces) pieces = kMostPieces;
+  // Where the caller says how long documents are, all pieces have that share of the
+  // longest.  Up to 2,048 keys, since documents of uneven length need pieces that
+  // end together (64 caches of 524,288 keys in all: 228 us uncut, 136, 121, 124, 137
+  // with 4,096, 2,048, 1,024, 512).
+  int64_t piece = 2 * kStepKeys;
+  if (d.max_k_len > 0) {
+    piece = (longest_k + pieces - 1) / pieces;
+    if (o.tiles == 1 && piece > 2048) piece = 2048;
+    piece = (piece + kStepKeys - 1) / kStepKeys * kStepKeys;
+    if (piece < 2 * kStepKeys) piece = 2 * kStepKeys;
+    pieces = kMostPieces;
+  }
+  const int64_t most = (longest_k + piece - 1) / piece;
   if (pieces > most) pieces = most;
   o.pieces = (int)(pieces < 1 ? 1 : pieces);
+  o.piece = (int)piece;
   return o;
 }
 
@@ -669,46 +739,53 @@ Plan plan_of(const gs_attention_config& cfg, const gs_documents& d, const gs_doc
 
 size_t ml_bytes(const Plan& p) { return ((size_t)p.slots * 8 + 255) / 256 * 256; }
 
-template <typename T, int kBits, int DT, bool kGeneral>
+template <typename T, int kBits, int DT, int kMode>
 hipError_t pass(CachedArgs a, const Cut& c, hipStream_t s) {
   a.pieces = c.pieces;
+  a.piece = c.piece;
   a.looked_up = c.looked_up;
   a.units = (uint32_t)c.units;
   const int64_t blocks = (c.units * c.pieces + 7) / 8 * 8 * a.heads_k;
   return launch_all(blocks, 256, [&](uint32_t first, dim3 n) {
     a.block0 = first;
-    if (c.tiles == 1) cached_attention_kernel<T, kBits, DT, 1, kGeneral><<<n, 256, 0, s>>>(a);
-    else cached_attention_kernel<T, kBits, DT, kManyTiles, kGeneral><<<n, 256, 0, s>>>(a);
+    if (c.tiles == 1) cached_attention_kernel<T, kBits, DT, 1, kMode><<<n, 256, 0, s>>>(a);
+    else cached_attention_kernel<T, kBits, DT, kManyTiles, kMode><<<n, 256, 0, s>>>(a);
   });
 }
 
-template <typename T, int kBits, int DT, bool kGeneral>
+template <typename T, int kBits, int DT, int kMode>
 hipError_t run(const CachedArgs& a, const Plan& p, const Docs& shared, hipStream_t s) {
   if (p.shared.pieces > 0) {
     CachedArgs b = a;
     b.docs = shared;
     b.causal = 0;
     b.first_piece = p.own.pieces;
-    const hipError_t e = pass<T, kBits, DT, kGeneral>(b, p.shared, s);
+    const hipError_t e = pass<T, kBits, DT, kMode>(b, p.shared, s);
     if (e != hipSuccess) return e;
   }
-  const hipError_t e = pass<T, kBits, DT, kGeneral>(a, p.own, s);
+  const hipError_t e = pass<T, kBits, DT, kMode>(a, p.own, s);
   if (e != hipSuccess || p.whole) return e;
   CachedArgs j = a;
   j.shared = shared;
   j.pieces = p.own.pieces;
+  j.piece = p.own.piece;
+  j.piece_shared = p.shared.piece;
   j.pieces_shared = p.shared.pieces;
-  return launch_all((int64_t)a.docs.rows_q * ((a.heads_q + 3) / 4), 256,
-                    [&](uint32_t first, dim3 n) {
-                      j.block0 = first;
-                      cached_join_kernel<T><<<n, 256, 0, s>>>(j);
-                    });
+  // with up to 16 pieces a wavefront has them in a few loads
+  const int threads = p.own.pieces + p.shared.pieces <= 16 ? 64 : 256;
+  return launch_all((int64_t)a.docs.rows_q * a.heads_q, threads, [&](uint32_t first, dim3 n) {
+    j.block0 = first;
+    constexpr int kLanes = DT / 4;
+    if (threads == 64) cached_join_kernel<T, kLanes, 64><<<n, 64, 0, s>>>(j);
+    else cached_join_kernel<T, kLanes, 256><<<n, 256, 0, s>>>(j);
+  });
 }
 
 template <typename T, int kBits, int DT>
 hipError_t run(const CachedArgs& a, const Plan& p, const Docs& shared, hipStream_t s) {
-  return a.softcap > 0.0f || a.slopes ? run<T, kBits, DT, true>(a, p, shared, s)
-                                      : run<T, kBits, DT, false>(a, p, shared, s);
+  if (a.slopes) return run<T, kBits, DT, kBiased>(a, p, shared, s);
+  if (a.softcap > 0.0f) return run<T, kBits, DT, kCapped>(a, p, shared, s);
+  return run<T, kBits, DT, kPlain>(a, p, shared, s);
 }
 
 template <typename T>

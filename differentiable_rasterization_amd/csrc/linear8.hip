@@ -168,11 +168,12 @@ __global__ void __launch_bounds__(kFewWaves * 64) linear_few_kernel(LinearArgs a
 
 // Place in a staged tile of 128-byte rows: 16-byte chunk c of row r stands at
 // chunk c ^ turn(r).  Outputs are read in the order 0..3, 16..19, 4..7, 20..23
-// ..., rows in their own: eight rows read together have eight different turns,
-// so that they fall on all the banks.
+// ..., rows in their own: of sixteen rows read together the eight even ones have
+// eight different turns, and so have the odd ones, whose chunks stand in the other
+// half of the 64 banks.
 template <bool kOutputs>
 __device__ inline int turn(int r) {
-  return kOutputs ? (r & 3) | ((r >> 2) & 4) : r & 7;
+  return kOutputs ? ((r >> 1) & 3) | ((r >> 2) & 4) : (r >> 1) & 7;
 }
 
 // Copies kRows rows of 128 bytes from column k on into LDS, without passing
