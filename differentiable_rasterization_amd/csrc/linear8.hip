@@ -14,6 +14,8 @@ namespace gs {
 struct LinearArgs {
   int64_t rows;
   int inputs, outputs;
+  const void* x;         // kOwn: rows as they came
+  int64_t x_row;
   const int8_t* u;       // [rows][inputs]
   const float* u_scale;  // [rows]
   const int8_t* w;       // [outputs][inputs]
@@ -25,10 +27,27 @@ struct LinearArgs {
   uint32_t tiles;
 };
 
-// Eight elements of any type.
-template <typename T>
-__device__ inline void load8(const T* p, float (&v)[8]) {
-  load_elems(p, v);
+// What a row's largest magnitude makes of it.  A row with an infinity or a NaN
+// has no codes: its scale is NaN, and so is all that comes of it.
+struct RowScale {
+  float scale;
+  double inv;
+  __device__ inline explicit RowScale(float top) {
+    const bool none = top < kLeastSpan, wrong = !(top < __builtin_huge_valf());
+    inv = none || wrong ? 0.0 : 127.0 / (double)top;
+    scale = wrong ? __builtin_nanf("") : none ? 0.0f : (float)((double)top / 127.0);
+  }
+};
+
+// Eight codes.
+__device__ inline u32x2 codes_of(const float (&v)[8], const RowScale& r) {
+  uint32_t w[2] = {0, 0};
+  if (r.scale == r.scale) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i >> 2] |= (uint32_t)(code_of(v[i], r.inv) & 255) << (8 * (i & 3));
+  }
+  return u32x2{w[0], w[1]};
 }
 
 // kLanes lanes a row; each keeps up to kKeep pieces of eight elements in
@@ -57,13 +76,13 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int ch
   for (int p = 0; p < kKeep; ++p) {
     const int e = at + p * kLanes * 8;
     if (here && e < channels) {
-      load8(in + e, kept[p]);
+      load_elems(in + e, kept[p]);
       look(kept[p]);
     }
   }
   for (int e = at + kKeep * kLanes * 8; here && e < channels; e += kLanes * 8) {
     float v[8];
-    load8(in + e, v);
+    load_elems(in + e, v);
     look(v);
   }
   if (bad) top = __builtin_huge_valf();
@@ -75,46 +94,40 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int ch
     top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
   }
   if (!here) return;
-  // a row with an infinity or a NaN has no codes: its scale is NaN, and so is
-  // all that comes of it
-  const bool none = !(top >= kLeastSpan), wrong = !(top < __builtin_huge_valf());
-  const double inv = none || wrong ? 0.0 : 127.0 / (double)top;
-  if (threadIdx.x % kLanes == 0)
-    scales[row] = wrong ? __builtin_nanf("") : none ? 0.0f : (float)((double)top / 127.0);
+  const RowScale r(top);
+  if (threadIdx.x % kLanes == 0) scales[row] = r.scale;
   int8_t* out = codes + row * channels;
-  auto put = [&](int e, const float (&v)[8]) {
-    uint32_t w[2] = {0, 0};
-    if (!wrong) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)(code_of(v[i], inv) & 255) << (8 * (i & 3));
-    }
-    *(u32x2*)(out + e) = u32x2{w[0], w[1]};
-  };
 #pragma unroll
   for (int p = 0; p < kKeep; ++p) {
     const int e = at + p * kLanes * 8;
-    if (e < channels) put(e, kept[p]);
+    if (e < channels) *(u32x2*)(out + e) = codes_of(kept[p], r);
   }
   for (int e = at + kKeep * kLanes * 8; e < channels; e += kLanes * 8) {
     float v[8];
-    load8(in + e, v);
-    put(e, v);
+    load_elems(in + e, v);
+    *(u32x2*)(out + e) = codes_of(v, r);
   }
-}
-
-template <typename T>
-__device__ inline void store4(T* p, const float (&v)[4]) {
-  store_elems(p, v);
 }
 
 // Few rows: the product is the reading of the weights.  A workgroup has 16
 // outputs, its wavefronts a share of the inputs each; weights and codes go from
 // memory straight into the operands of the 16x16x64 instruction (rows lane %
-// 16, 16 inputs a lane), and the wavefronts' sums meet in LDS.
-constexpr int kFewWaves = 8;
-template <typename T, int kTiles>
-__global__ void __launch_bounds__(kFewWaves * 64) linear_few_kernel(LinearArgs a) {
+// 16, 16 inputs a lane), and the wavefronts' sums meet in LDS.  Weights of
+// kAhead steps are on their way before anything else is looked at.
+//
+// kOwn: rows are brought to codes here, by every workgroup for itself while its
+// weights are on their way, which saves a launch: up to eight rows of at most
+// kOwnElems elements (rows rounded up to a power of two).
+constexpr int kFewWaves = 8, kAhead = 8;
+constexpr int kOwnElems = 32768;
+template <typename T, int kTiles, bool kOwn>
+__global__ void __launch_bounds__(kFewWaves * 64, 4) linear_few_kernel(LinearArgs a) {
+  constexpr int kKeep = kOwnElems / (8 * kFewWaves * 64);  // pieces of eight elements, a lane
   __shared__ i32x4 s_sum[kFewWaves][kTiles][64];
+  __shared__ uint32_t s_top[8];
+  // a row of codes is 16 bytes longer than its inputs, so that the 16 rows read
+  // together fall on different banks
+  __shared__ __align__(16) int8_t s_codes[kOwn ? kOwnElems + 8 * 16 : 16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n0 = blockIdx.x * 16;
   const int64_t m0 = (int64_t)blockIdx.y * (16 * kTiles);
@@ -124,25 +137,73 @@ __global__ void __launch_bounds__(kFewWaves * 64) linear_few_kernel(LinearArgs a
   const int part = 16 * (lane >> 4);
   // rows past the end repeat the last one; what comes of them is not stored
   const int8_t* w = a.w + (int64_t)min(n0 + (lane & 15), a.outputs - 1) * a.inputs + part;
+  i32x4 ahead[kAhead];
+  auto load_weights = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      ahead[i] = i32x4{0, 0, 0, 0};
+      if (s0 + i < last && 64 * (s0 + i) + part < a.inputs)  // inputs are a multiple of 16
+        ahead[i] = *(const i32x4*)(w + 64 * (s0 + i));
+    }
+  };
+  load_weights(first);
+  if constexpr (kOwn) {
+    // up to eight rows: eight, four, two or one wavefronts a row
+    const int rows = (int)a.rows, each = rows == 1 ? 8 : rows == 2 ? 4 : rows <= 4 ? 2 : 1;
+    const int row = wave / each, at = ((wave % each) * 64 + lane) * 8;
+    const bool mine = row < rows;
+    const T* x = (const T*)a.x + (mine ? row : 0) * a.x_row;
+    if (threadIdx.x < 8) s_top[threadIdx.x] = 0;
+    float kept[kKeep][8];
+#pragma unroll
+    for (int p = 0; p < kKeep; ++p) {
+      const int e = at + p * each * 512;
+      if (mine && e < a.inputs) load_elems(x + e, kept[p]);
+    }
+    __syncthreads();
+    // the largest magnitude as a whole number: an infinity or a NaN is above all
+    uint32_t top = 0;
+#pragma unroll
+    for (int p = 0; p < kKeep; ++p) {
+      if (!mine || at + p * each * 512 >= a.inputs) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        top = max(top, __builtin_bit_cast(uint32_t, kept[p][i]) & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
+    if (mine && lane == 0) atomicMax(&s_top[row], top);
+    __syncthreads();
+    if (mine) {
+      const RowScale r(__builtin_bit_cast(float, s_top[row]));
+#pragma unroll
+      for (int p = 0; p < kKeep; ++p) {
+        const int e = at + p * each * 512;
+        if (e < a.inputs) *(u32x2*)(s_codes + row * (a.inputs + 16) + e) = codes_of(kept[p], r);
+      }
+    }
+    __syncthreads();
+  }
   const int8_t* u[kTiles];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) {
-    const int64_t m = m0 + 16 * t + (lane & 15);
-    u[t] = a.u + (m < a.rows ? m : a.rows - 1) * a.inputs + part;
+    const int64_t m = m0 + 16 * t + (lane & 15), row = m < a.rows ? m : a.rows - 1;
+    u[t] = kOwn ? s_codes + row * (a.inputs + 16) + part : a.u + row * a.inputs + part;
   }
   i32x4 sum[kTiles];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) sum[t] = i32x4{0, 0, 0, 0};
-#pragma unroll 4
-  for (int s = first; s < last; ++s) {
-    const bool in = 64 * s + part < a.inputs;  // inputs are a multiple of 16
-    i32x4 x = {0, 0, 0, 0};
-    if (in) x = *(const i32x4*)(w + 64 * s);
+  for (int s0 = first; s0 < last; s0 += kAhead) {
+    if (s0 > first) load_weights(s0);
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
-      i32x4 y = {0, 0, 0, 0};
-      if (in) y = *(const i32x4*)(u[t] + 64 * s);
-      sum[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x, y, sum[t], 0, 0, 0);
+    for (int i = 0; i < kAhead; ++i) {
+      const bool in = s0 + i < last && 64 * (s0 + i) + part < a.inputs;
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        i32x4 y = {0, 0, 0, 0};
+        if (in) y = *(const i32x4*)(u[t] + 64 * (s0 + i));
+        sum[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(ahead[i], y, sum[t], 0, 0, 0);
+      }
     }
   }
 #pragma unroll
@@ -155,14 +216,15 @@ __global__ void __launch_bounds__(kFewWaves * 64) linear_few_kernel(LinearArgs a
     const int64_t m = m0 + 16 * t + (lane & 15);
     const int n = n0 + 4 * (lane >> 4);
     if (m >= a.rows || n >= a.outputs) continue;
-    const float scale = a.u_scale[m];
+    const float scale =
+        kOwn ? RowScale(__builtin_bit_cast(float, s_top[m & 7])).scale : a.u_scale[m];
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[i] = (float)all[i] * (scale * a.w_scale[n + i]);
       if (a.bias) v[i] += a.bias[n + i];
     }
-    store4((T*)a.y + m * a.y_row + n, v);
+    store_elems((T*)a.y + m * a.y_row + n, v);
   }
 }
 
@@ -322,11 +384,11 @@ hipError_t quantize(int64_t rows, int64_t channels, const gs_rows& x, int8_t* co
   });
 }
 
-template <typename T, int kTiles>
+template <typename T, int kTiles, bool kOwn>
 hipError_t few(const LinearArgs& a, hipStream_t s) {
-  linear_few_kernel<T, kTiles><<<dim3((a.outputs + 15) / 16,
-                                      (uint32_t)((a.rows + 16 * kTiles - 1) / (16 * kTiles))),
-                                 kFewWaves * 64, 0, s>>>(a);
+  linear_few_kernel<T, kTiles, kOwn>
+      <<<dim3((a.outputs + 15) / 16, (uint32_t)((a.rows + 16 * kTiles - 1) / (16 * kTiles))),
+         kFewWaves * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -339,14 +401,30 @@ hipError_t many(LinearArgs a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Whether workgroups bring the rows to codes themselves: where that is little work
+// for all of them together (us with a launch for the codes : without; inputs by
+// outputs): one row of 4,096 by 4,096 10.6 : 7.6, of 16,384 by 4,096 25.0 : 17.0;
+// four of 4,096 by 4,096 10.0 : 8.7; eight of 1,024 by 1,024 10.4 : 7.5, of 4,096 by
+// 4,096 10.7 : 11.0, of 2,048 by 8,192 10.9 : 12.4.
+bool own_codes(int64_t rows, int64_t inputs, int64_t outputs) {
+  const int64_t shares = rows <= 2 ? rows : rows <= 4 ? 4 : 8;
+  return rows <= 8 && shares * inputs <= kOwnElems &&
+         shares * inputs * outputs <= (int64_t)96 << 20;
+}
+
 template <typename T>
 hipError_t linear(const LinearArgs& a, hipStream_t s) {
-  if (a.rows <= 16) return few<T, 1>(a, s);
-  if (a.rows <= 32) return few<T, 2>(a, s);
-  if (a.rows <= 64) return few<T, 4>(a, s);
-  const int64_t large = ((a.rows + 255) / 256) * ((a.outputs + 255) / 256);
-  if (large >= 256) return many<T, 256, 256, 2, 4>(a, s);
-  return many<T, 128, 128, 2, 2>(a, s);
+  if (own_codes(a.rows, a.inputs, a.outputs)) return few<T, 1, true>(a, s);
+  if (a.rows <= 16) return few<T, 1, false>(a, s);
+  if (a.rows <= 32) return few<T, 2, false>(a, s);
+  if (a.rows <= 48) return few<T, 3, false>(a, s);
+  if (a.rows <= 64) return few<T, 4, false>(a, s);
+  const auto tiles = [&](int64_t side) {
+    return ((a.rows + side - 1) / side) * ((a.outputs + side - 1) / side);
+  };
+  if (tiles(256) >= 192) return many<T, 256, 256, 2, 4>(a, s);
+  if (tiles(128) >= 256) return many<T, 128, 128, 2, 2>(a, s);
+  return many<T, 64, 64, 2, 2>(a, s);
 }
 
 size_t codes_bytes(int64_t rows, int64_t channels) {
@@ -359,7 +437,8 @@ size_t codes_bytes(int64_t rows, int64_t channels) {
 extern "C" {
 
 size_t gs_linear_i8_bytes(const gs_linear_config& cfg, int64_t rows) {
-  return gs::codes_bytes(rows, cfg.inputs) + (size_t)rows * 4;
+  return gs::own_codes(rows, cfg.inputs, cfg.outputs) ? 0
+                                         : gs::codes_bytes(rows, cfg.inputs) + (size_t)rows * 4;
 }
 
 hipError_t gs_launch_quantize_rows(int32_t dtype, int64_t rows, int64_t channels,
@@ -375,13 +454,16 @@ hipError_t gs_launch_linear_i8(const gs_linear_config& cfg, int64_t rows, const 
                                const gs_rows& y, void* workspace, hipStream_t s) {
   int8_t* u = (int8_t*)workspace;
   float* u_scale = (float*)(u + gs::codes_bytes(rows, cfg.inputs));
-  const hipError_t e =
-      gs_launch_quantize_rows(cfg.dtype, rows, cfg.inputs, x, u, u_scale, s);
-  if (e != hipSuccess) return e;
+  if (!gs::own_codes(rows, cfg.inputs, cfg.outputs)) {
+    const hipError_t e = gs_launch_quantize_rows(cfg.dtype, rows, cfg.inputs, x, u, u_scale, s);
+    if (e != hipSuccess) return e;
+  }
   gs::LinearArgs a = {};
   a.rows = rows;
   a.inputs = (int)cfg.inputs;
   a.outputs = (int)cfg.outputs;
+  a.x = x.data;
+  a.x_row = x.row;
   a.u = u;
   a.u_scale = u_scale;
   a.w = w;
