@@ -56,83 +56,122 @@ __device__ inline void load_codes(const uint8_t* p, int (&u)[8]) {
   }
 }
 
-// The heads of a workgroup's tokens, kLanes lanes each: f(token row, row of the
-// cache or -1, head, keys or values, first element).
+// A head of a token, of its keys or its values, and where it stands in the cache
+// (row -1: nowhere).
+struct Item {
+  int64_t token, row;
+  int head, kv;
+  bool here;
+};
+
+// The heads of a workgroup's tokens, kLanes lanes each, kItems of them at a time
+// a lane: take(items, first element).
+constexpr int kItems = 4;
 template <int kLanes, typename F>
-__device__ inline void each_head(const CacheArgs& a, F f) {
+__device__ inline void each_heads(const CacheArgs& a, F take) {
   uint32_t local, units;
   Doc d;
   if (find_document<false>(a.docs, 1, kUnit, a.block0 + blockIdx.x, &local, &units, &d) < 0)
     return;
   const int first = (int)local * kUnit, count = min(kUnit, d.ql - first);
-  const int items = count * 2 * a.heads;
-  for (int i = threadIdx.x / kLanes; i < items; i += 256 / kLanes) {
-    const int token = first + i / (2 * a.heads), which = i % (2 * a.heads);
-    // the document's last tokens are its last keys
-    const int key = token + d.kl - d.ql;
-    f(d.qs + token, key < 0 ? -1 : d.ks + key, which % a.heads, which / a.heads,
-      (int)(threadIdx.x % kLanes) * 8);
+  const uint32_t both = 2u * (uint32_t)a.heads, items = (uint32_t)count * both;
+  constexpr uint32_t kGroups = 256 / kLanes;
+  for (uint32_t base = threadIdx.x / kLanes; base < items; base += kItems * kGroups) {
+    Item item[kItems];
+#pragma unroll
+    for (int p = 0; p < kItems; ++p) {
+      const uint32_t i = base + p * kGroups;
+      const int token = first + (int)(i / both), which = (int)(i % both);
+      // the document's last tokens are its last keys
+      const int key = token + d.kl - d.ql;
+      item[p].here = i < items;
+      item[p].token = d.qs + token;
+      item[p].row = key < 0 ? -1 : d.ks + key;
+      item[p].kv = which >= a.heads;
+      item[p].head = which - (item[p].kv ? a.heads : 0);
+    }
+    take(item, (int)(threadIdx.x % kLanes) * 8);
   }
 }
 
 template <typename T, int kBits, int kLanes>
 __global__ void __launch_bounds__(256) cache_write_kernel(CacheArgs a) {
   constexpr float kLevels = kBits == 8 ? 255.0f : 15.0f;
-  each_head<kLanes>(a, [&](int64_t token, int64_t row, int head, int kv, int e) {
+  each_heads<kLanes>(a, [&](const Item (&item)[kItems], int e) {
     // a lane past the head's end repeats its first elements
     const bool mine = e < a.dim;
-    float x[8];
-    load_elems((const T*)a.x[kv] + token * a.x_row[kv] + head * a.x_head[kv] + (mine ? e : 0), x);
-    float lo = x[0], hi = x[0];
-    bool bad = false;
+    float x[kItems][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo = fminf(lo, x[i]);
-      hi = fmaxf(hi, x[i]);
-      bad = bad || x[i] != x[i];
-    }
-    if (bad) hi = __builtin_huge_valf();
+    for (int p = 0; p < kItems; ++p)
+      if (item[p].here)
+        load_elems((const T*)a.x[item[p].kv] + item[p].token * a.x_row[item[p].kv] +
+                       item[p].head * a.x_head[item[p].kv] + (mine ? e : 0),
+                   x[p]);
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) {
-      lo = fminf(lo, __shfl_xor(lo, o, 64));
-      hi = fmaxf(hi, __shfl_xor(hi, o, 64));
-    }
-    if (row < 0) return;  // a token without a key
-    // a head with an infinity or a NaN, or too wide for fp32, has no codes
-    const bool wrong = !(hi - lo < 0x1p127f);
-    const double span = (double)hi - (double)lo;
-    const bool none = span < (double)kLeastSpan;
-    const double inv = none || wrong ? 0.0 : (double)kLevels / span;
-    int u[8];
+    for (int p = 0; p < kItems; ++p) {
+      if (!item[p].here) break;
+      const int kv = item[p].kv;
+      float lo = x[p][0], hi = x[p][0];
+      bool bad = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = wrong ? 0 : code_of((double)x[i] - (double)lo, inv);
-    if (mine)
-      store_codes<kBits>(a.codes[kv] + row * a.row[kv] + head * a.head[kv] + e * kBits / 8, u);
-    if (e == 0) {
-      const float nan = __builtin_nanf("");
-      a.low[kv][head * a.ld[kv] + row] = wrong ? nan : lo;
-      a.step[kv][head * a.ld[kv] + row] =
-          wrong ? nan : none ? 0.0f : (float)(span / (double)kLevels);
+      for (int i = 0; i < 8; ++i) {
+        lo = fminf(lo, x[p][i]);
+        hi = fmaxf(hi, x[p][i]);
+        bad = bad || x[p][i] != x[p][i];
+      }
+      if (bad) hi = __builtin_huge_valf();
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) {
+        lo = fminf(lo, __shfl_xor(lo, o, 64));
+        hi = fmaxf(hi, __shfl_xor(hi, o, 64));
+      }
+      if (item[p].row < 0) continue;  // a token without a key
+      // a head with an infinity or a NaN, or too wide for fp32, has no codes
+      const bool wrong = !(hi - lo < 0x1p127f);
+      const double span = (double)hi - (double)lo;
+      const bool none = span < (double)kLeastSpan;
+      const double inv = none || wrong ? 0.0 : (double)kLevels / span;
+      int u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = wrong ? 0 : code_of((double)x[p][i] - (double)lo, inv);
+      if (mine)
+        store_codes<kBits>(
+            a.codes[kv] + item[p].row * a.row[kv] + item[p].head * a.head[kv] + e * kBits / 8, u);
+      if (e == 0) {
+        const float nan = __builtin_nanf("");
+        const int64_t at = item[p].head * a.ld[kv] + item[p].row;
+        a.low[kv][at] = wrong ? nan : lo;
+        a.step[kv][at] = wrong ? nan : none ? 0.0f : (float)(span / (double)kLevels);
+      }
     }
   });
 }
 
 template <typename T, int kBits, int kLanes>
 __global__ void __launch_bounds__(256) cache_read_kernel(CacheArgs a) {
-  each_head<kLanes>(a, [&](int64_t token, int64_t row, int head, int kv, int e) {
+  each_heads<kLanes>(a, [&](const Item (&item)[kItems], int e) {
     if (e >= a.dim) return;
-    float x[8];
-    if (row < 0) {
+    float lo[kItems], step[kItems];
+    int u[kItems][8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-    } else {
-      const float lo = a.low[kv][head * a.ld[kv] + row], step = a.step[kv][head * a.ld[kv] + row];
-      int u[8];
-      load_codes<kBits>(a.codes[kv] + row * a.row[kv] + head * a.head[kv] + e * kBits / 8, u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = lo + step * (float)u[i];
+    for (int p = 0; p < kItems; ++p) {
+      if (!item[p].here || item[p].row < 0) continue;
+      const int kv = item[p].kv;
+      const int64_t at = item[p].head * a.ld[kv] + item[p].row;
+      lo[p] = a.low[kv][at];
+      step[p] = a.step[kv][at];
+      load_codes<kBits>(
+          a.codes[kv] + item[p].row * a.row[kv] + item[p].head * a.head[kv] + e * kBits / 8, u[p]);
     }
-    store_elems((T*)a.x[kv] + token * a.x_row[kv] + head * a.x_head[kv] + e, x);
+#pragma unroll
+    for (int p = 0; p < kItems; ++p) {
+      if (!item[p].here) break;
+      const int kv = item[p].kv;
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = item[p].row < 0 ? 0.0f : lo[p] + step[p] * (float)u[p][i];
+      store_elems((T*)a.x[kv] + item[p].token * a.x_row[kv] + item[p].head * a.x_head[kv] + e, x);
+    }
   });
 }
 

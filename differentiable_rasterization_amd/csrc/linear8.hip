@@ -113,17 +113,21 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int ch
 // outputs, its wavefronts a share of the inputs each; weights and codes go from
 // memory straight into the operands of the 16x16x64 instruction (rows lane %
 // 16, 16 inputs a lane), and the wavefronts' sums meet in LDS.  Weights of
-// kAhead steps are on their way before anything else is looked at.
+// the first kAheadOfAll steps are on their way before anything else is looked at.
+// 16 wavefronts where there is a workgroup a compute unit or less, 8 where there
+// are more (us, 16 : 8; one row of 4,096 by 4,096 7.2 : 8.3, of 2,048 by 8,192
+// 9.2 : 8.6; 33 rows of 4,096 by 4,096 13.8 : 14.5).
 //
 // kOwn: rows are brought to codes here, by every workgroup for itself while its
 // weights are on their way, which saves a launch: up to eight rows of at most
 // kOwnElems elements (rows rounded up to a power of two).
-constexpr int kFewWaves = 8, kAhead = 8;
+constexpr int kAheadOfAll = 64;
 constexpr int kOwnElems = 32768;
-template <typename T, int kTiles, bool kOwn>
-__global__ void __launch_bounds__(kFewWaves * 64, 4) linear_few_kernel(LinearArgs a) {
-  constexpr int kKeep = kOwnElems / (8 * kFewWaves * 64);  // pieces of eight elements, a lane
-  __shared__ i32x4 s_sum[kFewWaves][kTiles][64];
+template <typename T, int kTiles, int kWaves, bool kOwn>
+__global__ void __launch_bounds__(kWaves * 64, 4) linear_few_kernel(LinearArgs a) {
+  constexpr int kAhead = kAheadOfAll / kWaves;
+  constexpr int kKeep = kOwnElems / (8 * kWaves * 64);  // pieces of eight elements, a lane
+  __shared__ i32x4 s_sum[kWaves][kTiles][64];
   __shared__ uint32_t s_top[8];
   // a row of codes is 16 bytes longer than its inputs, so that the 16 rows read
   // together fall on different banks
@@ -132,7 +136,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, 4) linear_few_kernel(LinearArg
   const int n0 = blockIdx.x * 16;
   const int64_t m0 = (int64_t)blockIdx.y * (16 * kTiles);
   const int steps = (a.inputs + 63) / 64;
-  const int share = (steps + kFewWaves - 1) / kFewWaves;
+  const int share = (steps + kWaves - 1) / kWaves;
   const int first = wave * share, last = min(steps, first + share);
   const int part = 16 * (lane >> 4);
   // rows past the end repeat the last one; what comes of them is not stored
@@ -148,8 +152,8 @@ __global__ void __launch_bounds__(kFewWaves * 64, 4) linear_few_kernel(LinearArg
   };
   load_weights(first);
   if constexpr (kOwn) {
-    // up to eight rows: eight, four, two or one wavefronts a row
-    const int rows = (int)a.rows, each = rows == 1 ? 8 : rows == 2 ? 4 : rows <= 4 ? 2 : 1;
+    // up to eight rows: an eighth of the wavefronts a row, or more
+    const int rows = (int)a.rows, each = kWaves / (rows <= 2 ? rows : rows <= 4 ? 4 : 8);
     const int row = wave / each, at = ((wave % each) * 64 + lane) * 8;
     const bool mine = row < rows;
     const T* x = (const T*)a.x + (mine ? row : 0) * a.x_row;
@@ -209,10 +213,10 @@ __global__ void __launch_bounds__(kFewWaves * 64, 4) linear_few_kernel(LinearArg
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) s_sum[wave][t][lane] = sum[t];
   __syncthreads();
-  for (int t = wave; t < kTiles; t += kFewWaves) {
+  for (int t = wave; t < kTiles; t += kWaves) {
     i32x4 all = s_sum[0][t][lane];
 #pragma unroll
-    for (int i = 1; i < kFewWaves; ++i) all += s_sum[i][t][lane];
+    for (int i = 1; i < kWaves; ++i) all += s_sum[i][t][lane];
     const int64_t m = m0 + 16 * t + (lane & 15);
     const int n = n0 + 4 * (lane >> 4);
     if (m >= a.rows || n >= a.outputs) continue;
@@ -386,9 +390,9 @@ hipError_t quantize(int64_t rows, int64_t channels, const gs_rows& x, int8_t* co
 
 template <typename T, int kTiles, bool kOwn>
 hipError_t few(const LinearArgs& a, hipStream_t s) {
-  linear_few_kernel<T, kTiles, kOwn>
-      <<<dim3((a.outputs + 15) / 16, (uint32_t)((a.rows + 16 * kTiles - 1) / (16 * kTiles))),
-         kFewWaves * 64, 0, s>>>(a);
+  const dim3 grid((a.outputs + 15) / 16, (uint32_t)((a.rows + 16 * kTiles - 1) / (16 * kTiles)));
+  if (grid.x <= 256) linear_few_kernel<T, kTiles, 16, kOwn><<<grid, 16 * 64, 0, s>>>(a);
+  else linear_few_kernel<T, kTiles, 8, kOwn><<<grid, 8 * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 
