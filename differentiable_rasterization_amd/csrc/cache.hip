@@ -24,7 +24,7 @@ struct CacheArgs {
   uint32_t block0;
 };
 
-constexpr int kUnit = 16;  // tokens of a workgroup
+constexpr int kUnit = 8;  // tokens of a workgroup
 
 // The codes of eight elements, as they are stored.
 template <int kBits>
@@ -56,6 +56,22 @@ __device__ inline void load_codes(const uint8_t* p, int (&u)[8]) {
   }
 }
 
+// f over groups of kLanes lanes, by lane-to-lane moves: neighbours, pairs, fours,
+// eights.
+template <int kCtrl>
+__device__ inline float from_lane(float x) {
+  const int w = __builtin_bit_cast(int, x);
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(w, w, kCtrl, 0xF, 0xF, true));
+}
+template <int kLanes, typename F>
+__device__ inline float over_lanes(float x, F f) {
+  x = f(x, from_lane<0xB1>(x));   // quad_perm 1, 0, 3, 2
+  x = f(x, from_lane<0x4E>(x));   // quad_perm 2, 3, 0, 1
+  x = f(x, from_lane<0x141>(x));  // row_half_mirror
+  if (kLanes == 16) x = f(x, from_lane<0x140>(x));  // row_mirror
+  return x;
+}
+
 // A head of a token, of its keys or its values, and where it stands in the cache
 // (row -1: nowhere).
 struct Item {
@@ -80,11 +96,12 @@ __device__ inline void each_heads(const CacheArgs& a, F take) {
     Item item[kItems];
 #pragma unroll
     for (int p = 0; p < kItems; ++p) {
-      const uint32_t i = base + p * kGroups;
+      // what is not there repeats the last, up to what is written
+      const uint32_t at = base + p * kGroups, i = min(at, items - 1);
       const int token = first + (int)(i / both), which = (int)(i % both);
       // the document's last tokens are its last keys
       const int key = token + d.kl - d.ql;
-      item[p].here = i < items;
+      item[p].here = at < items;
       item[p].token = d.qs + token;
       item[p].row = key < 0 ? -1 : d.ks + key;
       item[p].kv = which >= a.heads;
@@ -103,13 +120,11 @@ __global__ void __launch_bounds__(256) cache_write_kernel(CacheArgs a) {
     float x[kItems][8];
 #pragma unroll
     for (int p = 0; p < kItems; ++p)
-      if (item[p].here)
-        load_elems((const T*)a.x[item[p].kv] + item[p].token * a.x_row[item[p].kv] +
-                       item[p].head * a.x_head[item[p].kv] + (mine ? e : 0),
-                   x[p]);
+      load_elems((const T*)a.x[item[p].kv] + item[p].token * a.x_row[item[p].kv] +
+                     item[p].head * a.x_head[item[p].kv] + (mine ? e : 0),
+                 x[p]);
 #pragma unroll
     for (int p = 0; p < kItems; ++p) {
-      if (!item[p].here) break;
       const int kv = item[p].kv;
       float lo = x[p][0], hi = x[p][0];
       bool bad = false;
@@ -120,12 +135,8 @@ __global__ void __launch_bounds__(256) cache_write_kernel(CacheArgs a) {
         bad = bad || x[p][i] != x[p][i];
       }
       if (bad) hi = __builtin_huge_valf();
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor(lo, o, 64));
-        hi = fmaxf(hi, __shfl_xor(hi, o, 64));
-      }
-      if (item[p].row < 0) continue;  // a token without a key
+      lo = over_lanes<kLanes>(lo, [](float y, float z) { return fminf(y, z); });
+      hi = over_lanes<kLanes>(hi, [](float y, float z) { return fmaxf(y, z); });
       // a head with an infinity or a NaN, or too wide for fp32, has no codes
       const bool wrong = !(hi - lo < 0x1p127f);
       const double span = (double)hi - (double)lo;
@@ -134,10 +145,12 @@ __global__ void __launch_bounds__(256) cache_write_kernel(CacheArgs a) {
       int u[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[i] = wrong ? 0 : code_of((double)x[p][i] - (double)lo, inv);
-      if (mine)
+      // a token without a key is not written
+      const bool written = item[p].here && item[p].row >= 0;
+      if (mine && written)
         store_codes<kBits>(
             a.codes[kv] + item[p].row * a.row[kv] + item[p].head * a.head[kv] + e * kBits / 8, u);
-      if (e == 0) {
+      if (e == 0 && written) {
         const float nan = __builtin_nanf("");
         const int64_t at = item[p].head * a.ld[kv] + item[p].row;
         a.low[kv][at] = wrong ? nan : lo;
@@ -152,10 +165,11 @@ __global__ void __launch_bounds__(256) cache_read_kernel(CacheArgs a) {
   each_heads<kLanes>(a, [&](const Item (&item)[kItems], int e) {
     if (e >= a.dim) return;
     float lo[kItems], step[kItems];
-    int u[kItems][8];
+    int u[kItems][8] = {};
 #pragma unroll
     for (int p = 0; p < kItems; ++p) {
-      if (!item[p].here || item[p].row < 0) continue;
+      lo[p] = step[p] = 0.0f;
+      if (item[p].row < 0) continue;  // a token without a key is read as 0
       const int kv = item[p].kv;
       const int64_t at = item[p].head * a.ld[kv] + item[p].row;
       lo[p] = a.low[kv][at];
@@ -165,12 +179,11 @@ __global__ void __launch_bounds__(256) cache_read_kernel(CacheArgs a) {
     }
 #pragma unroll
     for (int p = 0; p < kItems; ++p) {
-      if (!item[p].here) break;
       const int kv = item[p].kv;
       float x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = item[p].row < 0 ? 0.0f : lo[p] + step[p] * (float)u[p][i];
-      store_elems((T*)a.x[kv] + item[p].token * a.x_row[kv] + item[p].head * a.x_head[kv] + e, x);
+      for (int i = 0; i < 8; ++i) x[i] = lo[p] + step[p] * (float)u[p][i];
+      if (item[p].here) store_elems((T*)a.x[kv] + item[p].token * a.x_row[kv] + item[p].head * a.x_head[kv] + e, x);
     }
   });
 }
