@@ -53,7 +53,6 @@ struct CachedArgs {
   uint32_t units, block0;
 };
 
-constexpr int kManyTiles = 2;   // column tiles of a workgroup, where there are many columns
 constexpr int kStepKeys = 128;  // keys the four wavefronts take at a time
 
 // Keys of a piece of a document of kl keys.  Pieces have one size in all
@@ -265,153 +264,364 @@ constexpr float kRoom = 8.0f, kGrowth = 6.0f;
 
 // kMode: plain scores, capped ones, or a distance bias (with or without a cap).
 constexpr int kPlain = 0, kCapped = 1, kBiased = 2;
-template <typename T, int kBits, int DT, int CT, int kMode>
-__global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 2 : 1)
-    cached_attention_kernel(CachedArgs a) {
-  typedef KeyCodes<T, kBits> K;
-  typedef ValueCodes<kBits, DT> V;
-  typedef typename Mat16<T>::V8 V8;
-  constexpr int kSteps = DT / 32;    // of the scores' contraction
-  constexpr int kElems = V::kElems;  // products of 16 elements of the values
-  constexpr int kStride = DT + 4;
-  __shared__ __align__(16) float s_o[4][16][kStride];
-  __shared__ float s_m[4][16], s_l[4][16], s_c[4][16];
-  __shared__ __align__(16) float s_num[4][kNumbers];
-  const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
-  const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // All heads of the same keys go to one XCD, one after the other: rows of
-  // neighbouring heads share lines.
+
+// What a workgroup takes: the piece of a document's keys, of one head, and the
+// columns from first to end.  All heads of the same keys go to one XCD, one after
+// the other: rows of neighbouring heads share lines.
+struct Work {
+  Doc d;
+  int hk, piece, key0, keys;
+  int first, end, cols;
+};
+__device__ inline bool find_work(const CachedArgs& a, int width, Work& w) {
   const uint32_t block = a.block0 + blockIdx.x;
   const uint32_t turn = block >> 3;
-  const int hk = (int)(turn % (uint32_t)a.heads_k);
+  w.hk = (int)(turn % (uint32_t)a.heads_k);
   const uint32_t place = turn / (uint32_t)a.heads_k * 8 + (block & 7);
   const uint32_t unit = place % a.units;
-  const int piece = (int)(place / a.units);
-  if (piece >= a.pieces) return;
-  Doc d;
-  int col_first = 0, col_end = 0x7fffffff;
+  w.piece = (int)(place / a.units);
+  if (w.piece >= a.pieces) return false;
+  w.first = 0;
+  w.end = 0x7fffffff;
   if (a.looked_up) {
     uint32_t local, units;
-    if (find_document<false>(a.docs, (uint32_t)a.group, 16 * CT, unit, &local, &units, &d) < 0)
-      return;
-    col_first = (int)local * 16 * CT;
-    col_end = col_first + 16 * CT;
+    if (find_document<false>(a.docs, (uint32_t)a.group, (uint32_t)width, unit, &local, &units,
+                             &w.d) < 0)
+      return false;
+    w.first = (int)local * width;
+    w.end = w.first + width;
   } else {
-    d = load_doc(a.docs, (int)unit);
+    w.d = load_doc(a.docs, (int)unit);
   }
-  const int cols = d.ql * a.group;
-  const int keys = piece_keys(d.kl, a.pieces, a.piece);
-  if (piece > 0 && (int64_t)piece * keys >= d.kl) return;
-  const int key0 = piece * keys;
-  const uint8_t* const kc = a.kc + (int64_t)d.ks * a.kc_row + hk * a.kc_head;
-  const uint8_t* const vc = a.vc + (int64_t)d.ks * a.vc_row + hk * a.vc_head;
-  // Numbers of a key: lanes 0..31 have the 32 keys' own, lanes 32..63 their
-  // values'.  Each is brought to what a score or a weight needs of it by its one
-  // lane, and goes through LDS to those that use it.
-  const bool of_values = lane >= 32;
-  const int64_t num_at = of_values ? hk * a.v_ld + d.ks : hk * a.k_ld + d.ks;
-  const float* const lows = (of_values ? a.vlow : a.klow) + num_at;
-  const float* const steps = (of_values ? a.vstep : a.kstep) + num_at;
-  float* const nums = s_num[wave];
+  w.cols = w.d.ql * a.group;
+  w.end = min(w.end, w.cols);
+  w.keys = piece_keys(w.d.kl, a.pieces, a.piece);
+  if (w.piece > 0 && (int64_t)w.piece * w.keys >= w.d.kl) return false;
+  w.key0 = w.piece * w.keys;
+  return true;
+}
 
-  const float to_log2 = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
-  const float cap = a.softcap * kLog2e;
-  for (int col0 = col_first; col0 < min(col_end, cols); col0 += 16 * CT) {
-    const int last_col = min(col0 + 16 * CT, cols) - 1;
-    const int all_see = key_limit(a, d, col0 / a.group);
-    const int key_end =
-        min((int)min((int64_t)d.kl, (int64_t)key0 + keys), key_limit(a, d, last_col / a.group));
-    // the first tile is on its way before the queries are looked at
-    KeyRows<kBits, DT> kr;
-    ValueRows<kBits, DT> vr;
-    float low = 0.0f, step = 0.0f;
-    int key = key0 + 32 * wave;
-    const uint8_t* kp = kc + (int64_t)key * a.kc_row;
-    const uint8_t* vp = vc + (int64_t)key * a.vc_row;
-    const int k_row = (int)a.kc_row, v_row = (int)a.vc_row, head_bytes = a.dim * kBits / 8;
-    kr.start(k_row, a.dim);
-    vr.start(v_row, a.dim);
-    // bytes from a tile's first key to its last one's end; none past the end
-    auto bytes_of = [&](int at, int row) {
-      const int valid = min(32, d.kl - at);
-      return at < key_end ? (valid - 1) * row + head_bytes : 0;
-    };
-    auto load_numbers = [&](int key) {
-      if (key >= key_end) return;
-      const int at = key + min(lane & 31, d.kl - key - 1);
-      low = lows[at];
-      step = steps[at];
-    };
+// A wavefront's tiles of 32 keys on their way from memory: its lanes' codes, and
+// of one key low and step (lanes 0..31 have the keys' own, lanes 32..63 their
+// values'), which that lane brings to what a score or a weight needs of it, for
+// all that use it, through LDS.
+template <typename T, int kBits, int DT>
+struct Tiles {
+  typedef KeyCodes<T, kBits> K;
+  typedef ValueCodes<kBits, DT> V;
+  KeyRows<kBits, DT> k;
+  ValueRows<kBits, DT> v;
+  float low, step;
+  const uint8_t *kp, *vp;  // of the next tile
+  const float *lows, *steps;
+  int k_row, v_row, head_bytes, kl, key_end;
+
+  __device__ inline void start(const CachedArgs& a, const Work& w, int key, int end) {
+    const bool of_values = (threadIdx.x & 32) != 0;
+    k_row = (int)a.kc_row;
+    v_row = (int)a.vc_row;
+    head_bytes = a.dim * kBits / 8;
+    kl = w.d.kl;
+    key_end = end;
+    kp = a.kc + (int64_t)(w.d.ks + key) * a.kc_row + w.hk * a.kc_head;
+    vp = a.vc + (int64_t)(w.d.ks + key) * a.vc_row + w.hk * a.vc_head;
+    const int64_t at = of_values ? w.hk * a.v_ld + w.d.ks : w.hk * a.k_ld + w.d.ks;
+    lows = (of_values ? a.vlow : a.klow) + at;
+    steps = (of_values ? a.vstep : a.kstep) + at;
+    k.start(k_row, a.dim);
+    v.start(v_row, a.dim);
+    low = step = 0.0f;
     load_numbers(key);
-    kr.load(kp, k_row, bytes_of(key, k_row));
-    vr.load(vp, v_row, bytes_of(key, v_row));
+    k.load(kp, k_row, bytes(key, k_row));
+    v.load(vp, v_row, bytes(key, v_row));
+  }
+  // From a tile's first key to its last one's end; none past the end.
+  __device__ inline int bytes(int key, int row) const {
+    return key < key_end ? (min(32, kl - key) - 1) * row + head_bytes : 0;
+  }
+  __device__ inline void load_numbers(int key) {
+    if (key >= key_end) return;
+    const int at = key + min((int)(threadIdx.x & 31), kl - key - 1);
+    low = lows[at];
+    step = steps[at];
+  }
+  __device__ inline void next_keys(int key) {
+    kp += (int64_t)kStepKeys * k_row;
+    k.load(kp, k_row, bytes(key, k_row));
+  }
+  __device__ inline void next_values(int key) {
+    vp += (int64_t)kStepKeys * v_row;
+    v.load(vp, v_row, bytes(key, v_row));
+  }
+  // The step of this lane's key's values; what no column sees has no part in the
+  // range of the weights.
+  __device__ inline float seen_step(int key) const {
+    const int lane = threadIdx.x & 63;
+    return lane >= 32 && key + (lane & 31) >= key_end ? 0.0f : step;
+  }
+  // st: the step, of values times what weights are relative to.
+  __device__ inline void leave_numbers(float* nums, float st, float to_log2) const {
+    const int lane = threadIdx.x & 63;
+    const bool of_values = lane >= 32;
+    nums[2 * (lane & 32) + (lane & 31)] = of_values ? st : st * (K::kMul * to_log2);
+    nums[2 * (lane & 32) + 32 + (lane & 31)] =
+        fmaf(step, of_values ? V::kMid : K::kOff, low) * (of_values ? 1.0f : to_log2);
+  }
+};
 
-    // Columns past the last one repeat it, and are not stored.
-    V8 q[CT][kSteps];
-    float qsum[CT], slope[CT];
-    int limit[CT], pos[CT];
+// The largest finite step of the values of a tile, if it is past twice the unit
+// that weights are relative to, else 0.
+__device__ inline float larger_step(float st, float unit_step) {
+  const bool counts = (threadIdx.x & 32) != 0 && st < __builtin_huge_valf();
+  if (!__ballot(counts && st >= 2.0f * unit_step)) return 0.0f;
+  float top = counts ? st : 0.0f;
+#pragma unroll
+  for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
+  return top;
+}
+
+// CT times 16 columns of a wavefront: queries, and the running sums of a softmax.
+// Weights are relative to ref, which a score above most moves; steps to unit_step,
+// a power of two.
+template <typename T, int kBits, int DT, int CT, int kMode>
+struct Columns {
+  typedef ValueCodes<kBits, DT> V;
+  typedef typename Mat16<T>::V8 V8;
+  static constexpr int kSteps = DT / 32;    // of the scores' contraction
+  static constexpr int kElems = V::kElems;  // products of 16 elements of the values
+  V8 q[CT][kSteps];
+  float qsum[CT], slope[CT];
+  int limit[CT], pos[CT];
+  f32x4 o[CT][kElems];
+  float ref[CT], most[CT], l[CT], mean[CT];
+  float unit_step, per_unit;
+
+  // Columns past the last one repeat it, and are not stored.
+  __device__ inline void start(const CachedArgs& a, const Work& w, int col0) {
+    const int n = threadIdx.x & 15, kg = (threadIdx.x & 63) >> 4;
+    unit_step = 0x1p-126f;
+    per_unit = 0x1p126f;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      const int c = min(col0 + 16 * ct + n, cols - 1);
-      const int token = c / a.group, head = hk * a.group + c % a.group;
-      const uint16_t* p = a.q + (int64_t)(d.qs + token) * a.q_row + head * a.q_head;
+      const int c = min(col0 + 16 * ct + n, w.cols - 1);
+      const int token = c / a.group, head = w.hk * a.group + c % a.group;
+      const uint16_t* p = a.q + (int64_t)(w.d.qs + token) * a.q_row + head * a.q_head;
       float sum = 0.0f;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const int e = kg * (DT / 4) + 8 * s;
-        u32x4 w = {0, 0, 0, 0};
-        if (e < a.dim) w = *(const u32x4*)(p + e);
-        q[ct][s] = __builtin_bit_cast(V8, w);
+        u32x4 x = {0, 0, 0, 0};
+        if (e < a.dim) x = *(const u32x4*)(p + e);
+        q[ct][s] = __builtin_bit_cast(V8, x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float x, y;
-          unpack2<T>(w[i], x, y);
-          sum += x + y;
+          float y, z;
+          unpack2<T>(x[i], y, z);
+          sum += y + z;
         }
       }
       qsum[ct] = across_sum(sum);
-      limit[ct] = key_limit(a, d, token);
-      pos[ct] = token + d.kl - d.ql;
+      limit[ct] = key_limit(a, w.d, token);
+      pos[ct] = token + w.d.kl - w.d.ql;
       slope[ct] = kMode == kBiased ? a.slopes[head] * kLog2e : 0.0f;
-    }
-    f32x4 o[CT][kElems];
-    // weights are relative to ref; a score above most moves it
-    float ref[CT], most[CT], l[CT], mean[CT];
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
       most[ct] = -INFINITY;
       ref[ct] = l[ct] = mean[ct] = 0.0f;
 #pragma unroll
       for (int e = 0; e < kElems; ++e) o[ct][e] = (f32x4)(0.0f);
     }
-    // steps are taken relative to unit_step, a power of two
-    float unit_step = 0x1p-126f, per_unit = 0x1p126f;
-    for (; key < key_end; key += kStepKeys) {
-      const bool masked = key + 32 > all_see || key + 32 > key_end;
-      // what no column sees has no part in the range of the weights
-      const float st = of_values && key + (lane & 31) >= key_end ? 0.0f : step;
-      if (__ballot(of_values && st >= 2.0f * unit_step && st < __builtin_huge_valf())) {
-        float top = of_values && st < __builtin_huge_valf() ? st : 0.0f;
+  }
+
+  // Weights relative to the power of two below a step from here on.
+  __device__ inline void take_step(float top) {
+    const float now =
+        __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, top) & 0x7f800000u);
+    const float f = unit_step / now;
+    unit_step = now;
+    per_unit = 1.0f / now;
 #pragma unroll
-        for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
-        const float now =
-            __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, top) & 0x7f800000u);
-        const float f = unit_step / now;
-        unit_step = now;
-        per_unit = 1.0f / now;
+    for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
+      for (int e = 0; e < kElems; ++e) o[ct][e] *= f;
+  }
+
+  template <bool kRaw>
+  __device__ inline f32x4 step_of(const float* nums, int t, int kg) const {
+    const f32x4 x = *(const f32x4*)(nums + 64 + 16 * t + 4 * kg);
+    return kRaw ? x * per_unit : x;
+  }
+  __device__ inline f32x4 mean_of(const float* nums, int t, int kg) const {
+    return *(const f32x4*)(nums + 96 + 16 * t + 4 * kg);
+  }
+
+  // Weights of 32 keys from their scores' products s.  first: this lane's keys are
+  // first + 0..3 and first + 16 + 0..3.  kRaw: the numbers hold plain steps.
+  template <bool kRaw>
+  __device__ inline void weigh(const CachedArgs& a, const float* nums, const f32x4 (&s)[2][CT],
+                               bool masked, int first, int key_end, f16x8 (&w)[CT]) {
+    const int kg = (threadIdx.x & 63) >> 4;
+    const float cap = a.softcap * kLog2e;
 #pragma unroll
-          for (int e = 0; e < kElems; ++e) o[ct][e] *= f;
+    for (int ct = 0; ct < CT; ++ct) {
+      float y[8], top = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const f32x4 kmul = *(const f32x4*)(nums + 16 * t + 4 * kg);
+        const f32x4 kadd = *(const f32x4*)(nums + 32 + 16 * t + 4 * kg);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float& z = y[4 * t + r];
+          if constexpr (kMode == kPlain)
+            z = fmaf(s[t][ct][r], kmul[r], fmaf(kadd[r], qsum[ct], -ref[ct]));
+          else
+            z = fmaf(s[t][ct][r], kmul[r], kadd[r] * qsum[ct]);
+        }
       }
-      nums[2 * (lane & 32) + (lane & 31)] = st * (of_values ? per_unit : K::kMul * to_log2);
-      nums[2 * (lane & 32) + 32 + (lane & 31)] =
-          fmaf(step, of_values ? V::kMid : K::kOff, low) * (of_values ? 1.0f : to_log2);
+      if constexpr (kMode != kPlain) {
+        if (a.softcap > kWideCap) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = fmaf(cap, tanh_wide(y[j]), -ref[ct]);
+        } else if (kMode == kCapped || a.softcap > 0.0f) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = fmaf(cap, tanh_of(y[j]), -ref[ct]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] -= ref[ct];
+        }
+      }
+      if constexpr (kMode == kBiased) {
+        const float at = (float)(pos[ct] - first);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          y[j] = fmaf(-slope[ct], fabsf(at - (float)(16 * (j >> 2) + (j & 3))), y[j]);
+      }
+      if (masked) {
+        const int end = min(limit[ct], key_end) - first;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = 16 * (j >> 2) + (j & 3) < end ? y[j] : -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, y[j]);
+      if (__ballot(top > most[ct])) {
+        top = across_max(top);
+        const float over = top > (most[ct] == -INFINITY ? -INFINITY : kRoom) ? top - kRoom : 0.0f;
+        const float f = __builtin_amdgcn_exp2f(-over);
+        ref[ct] += over;
+        if (top > -INFINITY) most[ct] = kRoom + kGrowth;
+        // nothing has been summed where the first reference is taken
+        l[ct] = l[ct] == 0.0f ? 0.0f : l[ct] * f;
+        mean[ct] = mean[ct] == 0.0f ? 0.0f : mean[ct] * f;
+#pragma unroll
+        for (int e = 0; e < kElems; ++e)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[ct][e][r] = o[ct][e][r] == 0.0f ? 0.0f : o[ct][e][r] * f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] -= over;
+      }
+      // two loops, and not a branch in each turn of one
+      if (!masked) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const f32x4 vmul = step_of<kRaw>(nums, t, kg), vadd = mean_of(nums, t, kg);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float& z = y[4 * t + r];
+            const float p = __builtin_amdgcn_exp2f(z);
+            l[ct] += p;
+            mean[ct] = fmaf(p, vadd[r], mean[ct]);
+            z = p * vmul[r];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const f32x4 vmul = step_of<kRaw>(nums, t, kg), vadd = mean_of(nums, t, kg);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float& z = y[4 * t + r];
+            const float p = __builtin_amdgcn_exp2f(z);
+            l[ct] += p;
+            // what a column does not see may hold a NaN
+            const bool seen = z != -INFINITY;
+            mean[ct] = seen ? fmaf(p, vadd[r], mean[ct]) : mean[ct];
+            z = seen ? p * vmul[r] : 0.0f;
+          }
+        }
+      }
+      w[ct] = __builtin_bit_cast(f16x8, u32x4{pack_f16(y[0], y[1]), pack_f16(y[2], y[3]),
+                                              pack_f16(y[4], y[5]), pack_f16(y[6], y[7])});
+    }
+  }
+
+  __device__ inline void add_values(int e, f16x8 x, const f16x8 (&w)[CT]) {
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+      o[ct][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w[ct], o[ct][e], 0, 0, 0);
+  }
+};
+
+// N elements of column c from element `first` on: y with its sum and reference, as
+// the result or as a piece's share.
+template <typename T, int N>
+__device__ inline void leave(const CachedArgs& a, const Work& w, int c, int first, float (&y)[N],
+                             float sum, float top, bool number) {
+  const int64_t token = w.d.qs + c / a.group;
+  const int head = w.hk * a.group + c % a.group;
+  if (a.whole) {
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int e = 0; e < N; ++e) y[e] *= inv;
+    store_elems((T*)(a.out + token * a.out_row + head * a.out_head + first), y);
+    if (a.lse && number)
+      a.lse[(int64_t)head * a.docs.rows_q + token] =
+          sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+  } else {
+    const int64_t slot =
+        ((int64_t)(a.first_piece + w.piece) * a.heads_q + head) * a.docs.rows_q + token;
+    store_elems(a.part_o + slot * a.dim + first, y);
+    if (number) {
+      a.part_ml[2 * slot] = top;
+      a.part_ml[2 * slot + 1] = sum;
+    }
+  }
+}
+
+// Few columns: 16 CT a workgroup, its wavefronts take the piece's keys in turn.
+// With 16 the kernel is the reading of the cache, with 32 its arithmetic weighs as
+// much.  A tile is in flight in the registers that the one before has freed.
+template <typename T, int kBits, int DT, int CT, int kMode>
+__global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : 2)
+    cached_few_kernel(CachedArgs a) {
+  typedef KeyCodes<T, kBits> K;
+  typedef ValueCodes<kBits, DT> V;
+  constexpr int kSteps = DT / 32, kElems = V::kElems, kStride = DT + 4;
+  __shared__ __align__(16) float s_o[4][16][kStride];
+  __shared__ float s_m[4][16], s_l[4][16], s_c[4][16];
+  __shared__ __align__(16) float s_num[4][kNumbers];
+  const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
+  const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Work w;
+  if (!find_work(a, 16 * CT, w)) return;
+  float* const nums = s_num[wave];
+  const float to_log2 = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
+  for (int col0 = w.first; col0 < w.end; col0 += 16 * CT) {
+    const int last_col = min(col0 + 16 * CT, w.cols) - 1;
+    const int all_see = key_limit(a, w.d, col0 / a.group);
+    const int key_end = min((int)min((int64_t)w.d.kl, (int64_t)w.key0 + w.keys),
+                            key_limit(a, w.d, last_col / a.group));
+    int key = w.key0 + 32 * wave;
+    // the first tile is on its way before the queries are looked at
+    Tiles<T, kBits, DT> tile;
+    tile.start(a, w, key, key_end);
+    Columns<T, kBits, DT, CT, kMode> col;
+    col.start(a, w, col0);
+    for (; key < key_end; key += kStepKeys) {
+      const float st = tile.seen_step(key), top = larger_step(st, col.unit_step);
+      if (top > 0.0f) col.take_step(top);
+      tile.leave_numbers(nums, lane >= 32 ? st * col.per_unit : st, to_log2);
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      load_numbers(key + kStepKeys);
-
+      tile.load_numbers(key + kStepKeys);
       f32x4 s[2][CT];
 #pragma unroll
       for (int ct = 0; ct < CT; ++ct) s[0][ct] = s[1][ct] = (f32x4)(0.0f);
@@ -419,166 +629,159 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : CT == 2 ? 
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          const V8 x = K::operand(kr.w[t] + i * kBits / 4);
+          const auto x = K::operand(tile.k.w[t] + i * kBits / 4);
 #pragma unroll
-          for (int ct = 0; ct < CT; ++ct) s[t][ct] = Mat16<T>::mul(x, q[ct][i], s[t][ct]);
+          for (int ct = 0; ct < CT; ++ct) s[t][ct] = Mat16<T>::mul(x, col.q[ct][i], s[t][ct]);
         }
-      // the keys' registers are free: the next ones come while this tile is
-      // finished
-      kp += (int64_t)kStepKeys * k_row;
-      kr.load(kp, k_row, bytes_of(key + kStepKeys, k_row));
+      tile.next_keys(key + kStepKeys);
       __builtin_amdgcn_sched_barrier(0);
-
-      const int first = key + 4 * kg;  // this lane's keys: first + 0..3 and 16 + 0..3
-      f16x8 w[CT];
+      f16x8 p[CT];
+      col.template weigh<false>(a, nums, s, key + 32 > all_see || key + 32 > key_end, key + 4 * kg,
+                                key_end, p);
 #pragma unroll
-      for (int ct = 0; ct < CT; ++ct) {
-        float y[8], top = -INFINITY;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const f32x4 kmul = *(const f32x4*)(nums + 16 * t + 4 * kg);
-          const f32x4 kadd = *(const f32x4*)(nums + 32 + 16 * t + 4 * kg);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float& z = y[4 * t + r];
-            if constexpr (kMode == kPlain) {
-              z = fmaf(s[t][ct][r], kmul[r], fmaf(kadd[r], qsum[ct], -ref[ct]));
-            } else {
-              z = fmaf(s[t][ct][r], kmul[r], kadd[r] * qsum[ct]);
-            }
-          }
-        }
-        if constexpr (kMode != kPlain) {
-          if (a.softcap > kWideCap) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = fmaf(cap, tanh_wide(y[j]), -ref[ct]);
-          } else if (kMode == kCapped || a.softcap > 0.0f) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = fmaf(cap, tanh_of(y[j]), -ref[ct]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] -= ref[ct];
-          }
-        }
-        if constexpr (kMode == kBiased) {
-          const float at = (float)(pos[ct] - first);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            y[j] = fmaf(-slope[ct], fabsf(at - (float)(16 * (j >> 2) + (j & 3))), y[j]);
-        }
-        if (masked) {
-          const int end = min(limit[ct], key_end) - first;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = 16 * (j >> 2) + (j & 3) < end ? y[j] : -INFINITY;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, y[j]);
-        if (__ballot(top > most[ct])) {
-          top = across_max(top);
-          const float over = top > (most[ct] == -INFINITY ? -INFINITY : kRoom) ? top - kRoom : 0.0f;
-          const float f = __builtin_amdgcn_exp2f(-over);
-          ref[ct] += over;
-          if (top > -INFINITY) most[ct] = kRoom + kGrowth;
-          // nothing has been summed where the first reference is taken
-          l[ct] = l[ct] == 0.0f ? 0.0f : l[ct] * f;
-          mean[ct] = mean[ct] == 0.0f ? 0.0f : mean[ct] * f;
-#pragma unroll
-          for (int e = 0; e < kElems; ++e)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[ct][e][r] = o[ct][e][r] == 0.0f ? 0.0f : o[ct][e][r] * f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] -= over;
-        }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const f32x4 vmul = *(const f32x4*)(nums + 64 + 16 * t + 4 * kg);
-          const f32x4 vadd = *(const f32x4*)(nums + 96 + 16 * t + 4 * kg);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float& z = y[4 * t + r];
-            const float p = __builtin_amdgcn_exp2f(z);
-            l[ct] += p;
-            if (!masked) {
-              mean[ct] = fmaf(p, vadd[r], mean[ct]);
-              z = p * vmul[r];
-            } else {
-              // what a column does not see may hold a NaN
-              const bool seen = z != -INFINITY;
-              mean[ct] = seen ? fmaf(p, vadd[r], mean[ct]) : mean[ct];
-              z = seen ? p * vmul[r] : 0.0f;
-            }
-          }
-        }
-        w[ct] = __builtin_bit_cast(f16x8, u32x4{pack_f16(y[0], y[1]), pack_f16(y[2], y[3]),
-                                                pack_f16(y[4], y[5]), pack_f16(y[6], y[7])});
-      }
-#pragma unroll
-      for (int e = 0; e < kElems; ++e) {
-        const f16x8 x = V::operand(vr.w, e);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-          o[ct][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, w[ct], o[ct][e], 0, 0, 0);
-      }
-      vp += (int64_t)kStepKeys * v_row;
-      vr.load(vp, v_row, bytes_of(key + kStepKeys, v_row));
+      for (int e = 0; e < kElems; ++e) col.add_values(e, V::operand(tile.v.w, e), p);
+      tile.next_values(key + kStepKeys);
       __builtin_amdgcn_sched_barrier(0);
     }
 
     // The four wavefronts' sums, 16 columns at a time: 16 lanes a column.
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-      const float lsum = across_sum(l[ct]), msum = across_sum(mean[ct]);
+      const float lsum = across_sum(col.l[ct]), msum = across_sum(col.mean[ct]);
       __syncthreads();
       if (kg == 0) {
-        s_m[wave][n] = ref[ct];
+        s_m[wave][n] = col.ref[ct];
         s_l[wave][n] = lsum;
         s_c[wave][n] = msum;
       }
 #pragma unroll
       for (int e = 0; e < kElems; ++e)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s_o[wave][n][V::element(4 * kg + r, e)] =
-            o[ct][e][r] * 512.0f * unit_step;
+        for (int r = 0; r < 4; ++r)
+          s_o[wave][n][V::element(4 * kg + r, e)] = col.o[ct][e][r] * 512.0f * col.unit_step;
       __syncthreads();
-      const int col = threadIdx.x >> 4, first = (threadIdx.x & 15) * kElems;
-      const int c = col0 + 16 * ct + col;
-      if (c < cols && first < a.dim) {
+      const int c16 = threadIdx.x >> 4, first = (threadIdx.x & 15) * kElems;
+      const int c = col0 + 16 * ct + c16;
+      if (c < w.cols && first < a.dim) {
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = s_l[i][col] == 0.0f ? top : fmaxf(top, s_m[i][col]);
+        for (int i = 0; i < 4; ++i) top = s_l[i][c16] == 0.0f ? top : fmaxf(top, s_m[i][c16]);
         float sum = 0.0f, add = 0.0f, y[kElems];
 #pragma unroll
         for (int e = 0; e < kElems; ++e) y[e] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (s_l[i][col] == 0.0f) continue;
-          const float f = __builtin_amdgcn_exp2f(s_m[i][col] - top);
-          sum = fmaf(f, s_l[i][col], sum);
-          add = fmaf(f, s_c[i][col], add);
+          if (s_l[i][c16] == 0.0f) continue;
+          const float f = __builtin_amdgcn_exp2f(s_m[i][c16] - top);
+          sum = fmaf(f, s_l[i][c16], sum);
+          add = fmaf(f, s_c[i][c16], add);
 #pragma unroll
-          for (int e = 0; e < kElems; ++e) y[e] = fmaf(f, s_o[i][col][first + e], y[e]);
+          for (int e = 0; e < kElems; ++e) y[e] = fmaf(f, s_o[i][c16][first + e], y[e]);
         }
 #pragma unroll
         for (int e = 0; e < kElems; ++e) y[e] += add;
-        const int64_t token = d.qs + c / a.group;
-        const int head = hk * a.group + c % a.group;
-        if (a.whole) {
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        leave<T>(a, w, c, first, y, sum, top, first == 0);
+      }
+    }
+  }
+}
+
+// Many columns: 32 a wavefront, 128 a workgroup.  Each wavefront brings 32 of 128
+// keys to operands, in LDS and in the order in which lanes read them, for all
+// four: a quarter of the conversions that the few-column form would make.
+constexpr int kManyCols = 128;
+template <typename T, int kBits, int DT, int kMode>
+__global__ void __launch_bounds__(256, 2) cached_many_kernel(CachedArgs a) {
+  typedef KeyCodes<T, kBits> K;
+  typedef ValueCodes<kBits, DT> V;
+  typedef typename Mat16<T>::V8 V8;
+  constexpr int CT = 2, kSteps = DT / 32, kElems = V::kElems;
+  __shared__ __align__(16) u32x4 s_k[4][2 * kSteps][64], s_v[4][kElems][64];
+  __shared__ __align__(16) float s_num[4][kNumbers];
+  __shared__ float s_top[4];
+  const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
+  const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Work w;
+  if (!find_work(a, kManyCols, w)) return;
+  const float to_log2 = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
+  for (int col0 = w.first; col0 < w.end; col0 += kManyCols) {
+    const int last_col = min(col0 + kManyCols, w.cols) - 1;
+    const int key_end = min((int)min((int64_t)w.d.kl, (int64_t)w.key0 + w.keys),
+                            key_limit(a, w.d, last_col / a.group));
+    // this wavefront's own columns, and the keys that all and any of them see
+    const int mine = col0 + 16 * CT * wave, mine_last = min(mine + 16 * CT, w.cols) - 1;
+    const bool idle = mine >= w.cols;
+    const int all_see = idle ? 0 : key_limit(a, w.d, mine / a.group);
+    const int any_sees = idle ? 0 : min(key_end, key_limit(a, w.d, mine_last / a.group));
+    Tiles<T, kBits, DT> tile;
+    tile.start(a, w, w.key0 + 32 * wave, key_end);
+    Columns<T, kBits, DT, CT, kMode> col;
+    col.start(a, w, mine);
+    for (int base = w.key0; base < key_end; base += kStepKeys) {
+      const int own = base + 32 * wave;
+      const float st = tile.seen_step(own), larger = larger_step(st, col.unit_step);
+      // all have read the tiles before
+      __syncthreads();
+      if (lane == 0) s_top[wave] = own < key_end ? larger : 0.0f;
+      tile.leave_numbers(s_num[wave], st, to_log2);
+      tile.load_numbers(own + kStepKeys);
 #pragma unroll
-          for (int e = 0; e < kElems; ++e) y[e] *= inv;
-          store_elems((T*)(a.out + token * a.out_row + head * a.out_head + first), y);
-          if (a.lse && first == 0)
-            a.lse[(int64_t)head * a.docs.rows_q + token] =
-                sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
-        } else {
-          const int64_t slot =
-              ((int64_t)(a.first_piece + piece) * a.heads_q + head) * a.docs.rows_q + token;
-          store_elems(a.part_o + slot * a.dim + first, y);
-          if (first == 0) {
-            a.part_ml[2 * slot] = top;
-            a.part_ml[2 * slot + 1] = sum;
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+          s_k[wave][t * kSteps + i][lane] =
+              __builtin_bit_cast(u32x4, K::operand(tile.k.w[t] + i * kBits / 4));
+      tile.next_keys(own + kStepKeys);
+#pragma unroll
+      for (int e = 0; e < kElems; ++e)
+        s_v[wave][e][lane] = __builtin_bit_cast(u32x4, V::operand(tile.v.w, e));
+      tile.next_values(own + kStepKeys);
+      __syncthreads();
+      const float top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+      if (top > 0.0f) col.take_step(top);
+#pragma unroll 1
+      for (int sub = 0; sub < 4; ++sub) {
+        const int key = base + 32 * sub;
+        if (key >= any_sees) break;
+        f32x4 s[2][CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) s[0][ct] = s[1][ct] = (f32x4)(0.0f);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const V8 x = __builtin_bit_cast(V8, s_k[sub][t * kSteps + i][lane]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) s[t][ct] = Mat16<T>::mul(x, col.q[ct][i], s[t][ct]);
           }
-        }
+        f16x8 p[CT];
+        col.template weigh<true>(a, s_num[sub], s, key + 32 > all_see || key + 32 > key_end,
+                                 key + 4 * kg, key_end, p);
+#pragma unroll
+        for (int e = 0; e < kElems; ++e)
+          col.add_values(e, __builtin_bit_cast(f16x8, s_v[sub][e][lane]), p);
+      }
+    }
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      const float sum = across_sum(col.l[ct]), add = across_sum(col.mean[ct]);
+      const int c = mine + 16 * ct + n;
+      if (c >= w.cols || c >= w.end) continue;
+      // a lane has a quarter of the column's elements, side by side
+      float y[DT / 4];
+#pragma unroll
+      for (int e = 0; e < kElems; ++e)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          y[V::element(r, e)] = col.o[ct][e][r] * 512.0f * col.unit_step + add;
+#pragma unroll
+      for (int i = 0; i < DT / 4; i += 8) {
+        const int first = kg * (DT / 4) + i;
+        if (first >= a.dim) continue;
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = sum == 0.0f ? 0.0f : y[i + e];
+        leave<T>(a, w, c, first, z, sum, sum == 0.0f ? -INFINITY : col.ref[ct], first == 0);
       }
     }
   }
@@ -678,9 +881,10 @@ __global__ void __launch_bounds__(kThreads) cached_join_kernel(CachedArgs a) {
 
 namespace {
 
-// How a pass is cut: columns of a tile, tiles, pieces of a document's keys.
+// How a pass is cut: columns of a workgroup, units, pieces of a document's keys.
+constexpr int64_t kMostFew = 64;
 struct Cut {
-  int tiles;  // of 16 columns, a workgroup: 1 or kManyTiles
+  int width;  // columns of a workgroup: 16, 32 or kManyCols
   bool looked_up;
   int64_t units;
   int pieces, piece;
@@ -691,16 +895,16 @@ Cut cut_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q
   const int64_t group = cfg.heads_q / cfg.heads_k;
   const int64_t longest_q = d.max_q_len > 0 && d.max_q_len < rows_q ? d.max_q_len : rows_q;
   const int64_t longest_k = d.max_k_len > 0 && d.max_k_len < rows_k ? d.max_k_len : rows_k;
-  o.tiles = longest_q * group <= 16 ? 1 : kManyTiles;
-  o.looked_up = longest_q * group > 16 * o.tiles;
-  o.units = o.looked_up ? rows_q * group / (16 * o.tiles) + d.count : d.count;
+  o.width = longest_q * group <= 16 ? 16 : longest_q * group <= kMostFew ? 32 : kManyCols;
+  o.looked_up = longest_q * group > o.width;
+  o.units = o.looked_up ? rows_q * group / o.width + d.count : d.count;
   const int64_t base = o.units * cfg.heads_k;
   // Workgroups wanted: two a compute unit where there are many columns or few
   // documents (us at 512, 768, 1024, 2048: four caches of 120,001 keys in all 45, 47,
   // 50, 57; 64 requests behind 16,384 shared keys 50, 58, 61, -), more where many
   // documents of uneven length hide each other's ends (64 caches of 100,003 keys, 8
   // heads of 64 in 4 bits: 40, 35, 34, 32).
-  const int64_t target = o.tiles == 1 && base >= 256 ? 1536 : 512;
+  const int64_t target = o.width == 16 && base >= 256 ? 1536 : 512;
   int64_t pieces = (target + base - 1) / (base > 0 ? base : 1);
   if (pieces > kMostPieces) pieces = kMostPieces;
   // Where the caller says how long documents are, all pieces have that share of the
@@ -710,7 +914,7 @@ Cut cut_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q
   int64_t piece = 2 * kStepKeys;
   if (d.max_k_len > 0) {
     piece = (longest_k + pieces - 1) / pieces;
-    if (o.tiles == 1 && piece > 2048) piece = 2048;
+    if (o.width == 16 && piece > 2048) piece = 2048;
     piece = (piece + kStepKeys - 1) / kStepKeys * kStepKeys;
     if (piece < 2 * kStepKeys) piece = 2 * kStepKeys;
     pieces = kMostPieces;
@@ -748,8 +952,9 @@ hipError_t pass(CachedArgs a, const Cut& c, hipStream_t s) {
   const int64_t blocks = (c.units * c.pieces + 7) / 8 * 8 * a.heads_k;
   return launch_all(blocks, 256, [&](uint32_t first, dim3 n) {
     a.block0 = first;
-    if (c.tiles == 1) cached_attention_kernel<T, kBits, DT, 1, kMode><<<n, 256, 0, s>>>(a);
-    else cached_attention_kernel<T, kBits, DT, kManyTiles, kMode><<<n, 256, 0, s>>>(a);
+    if (c.width == 16) cached_few_kernel<T, kBits, DT, 1, kMode><<<n, 256, 0, s>>>(a);
+    else if (c.width == 32) cached_few_kernel<T, kBits, DT, 2, kMode><<<n, 256, 0, s>>>(a);
+    else cached_many_kernel<T, kBits, DT, kMode><<<n, 256, 0, s>>>(a);
   });
 }
 
