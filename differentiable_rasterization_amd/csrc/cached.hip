@@ -882,9 +882,8 @@ __global__ void __launch_bounds__(kThreads) cached_join_kernel(CachedArgs a) {
 namespace {
 
 // How a pass is cut: columns of a workgroup, units, pieces of a document's keys.
-constexpr int64_t kMostFew = 64;
 struct Cut {
-  int width;  // columns of a workgroup: 16, 32 or kManyCols
+  int width;  // 16, 32 or kManyCols
   bool looked_up;
   int64_t units;
   int pieces, piece;
@@ -895,17 +894,24 @@ Cut cut_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q
   const int64_t group = cfg.heads_q / cfg.heads_k;
   const int64_t longest_q = d.max_q_len > 0 && d.max_q_len < rows_q ? d.max_q_len : rows_q;
   const int64_t longest_k = d.max_k_len > 0 && d.max_k_len < rows_k ? d.max_k_len : rows_k;
-  o.width = longest_q * group <= 16 ? 16 : longest_q * group <= kMostFew ? 32 : kManyCols;
+  // The form for many columns pays from more than 128 on (us, it : 32 columns; 100
+  // tokens of eight requests, 16 heads of 128 over 4, up to 128 columns 58 : 30; 500
+  // of 16 requests, 8 heads of 64 over 4, 39 : 41; 1,024 of one request 399 : 504).
+  o.width = longest_q * group <= 16 ? 16 : longest_q * group <= 128 ? 32 : kManyCols;
   o.looked_up = longest_q * group > o.width;
   o.units = o.looked_up ? rows_q * group / o.width + d.count : d.count;
-  const int64_t base = o.units * cfg.heads_k;
-  // Workgroups wanted: two a compute unit where there are many columns or few
-  // documents (us at 512, 768, 1024, 2048: four caches of 120,001 keys in all 45, 47,
-  // 50, 57; 64 requests behind 16,384 shared keys 50, 58, 61, -), more where many
-  // documents of uneven length hide each other's ends (64 caches of 100,003 keys, 8
-  // heads of 64 in 4 bits: 40, 35, 34, 32).
-  const int64_t target = o.width == 16 && base >= 256 ? 1536 : 512;
-  int64_t pieces = (target + base - 1) / (base > 0 ? base : 1);
+  // units that have work: documents end inside one, half way on average
+  const int64_t busy = o.looked_up ? rows_q * group / o.width + (d.count + 1) / 2 : d.count;
+  const int64_t base = (busy > 0 ? busy : 1) * cfg.heads_k;
+  // Workgroups wanted.  16 columns: two a compute unit where there are few documents
+  // (four caches of 120,001 keys in all: 45, 47, 50, 57 us with 512, 768, 1,024,
+  // 2,048), more where many of uneven length hide each other's ends (64 caches of
+  // 100,003 keys, 8 heads of 64 in 4 bits: 40, 35, 34, 32).  32 columns: in between
+  // (24 requests of a few tokens, 30,011 keys: 26, 24, 23, 27 with 256, 512, 704,
+  // 1,024).  Many: what the chip holds at a time (the 1,024 tokens: 752, 400, 480, 416
+  // with 256, 512, 768, 1,024).
+  const int64_t target = o.width == 16 ? (base >= 256 ? 1536 : 512) : o.width == 32 ? 704 : 512;
+  int64_t pieces = (target + base - 1) / base;
   if (pieces > kMostPieces) pieces = kMostPieces;
   // Where the caller says how long documents are, all pieces have that share of the
   // longest.  Up to 2,048 keys, since documents of uneven length need pieces that
