@@ -348,24 +348,49 @@ __global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a
           sum[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[i], u[j], sum[i][j], 0, 0, 0);
     }
   }
+  // Results go through LDS, 32 rows by 128 bytes of a wavefront at a time, so that
+  // whole lines are written.  A row there is 16 bytes longer: sixteen rows fall on
+  // different banks.
+  __syncthreads();
+  constexpr int kAcross = kTn * 32 * (int)sizeof(T) < 128 ? kTn : 4 / (int)sizeof(T);
+  constexpr int kRowBytes = kAcross * 32 * (int)sizeof(T), kLong = kRowBytes + 16;
+  constexpr int kChunks = kRowBytes / 16, kTall = 64 / kChunks, kEach = 16 / (int)sizeof(T);
+  char* const mem = s_mem + wave * 32 * kLong;
+  static_assert(kWaves * 32 * kLong <= 2 * kBytes, "the tiles' place holds the results");
 #pragma unroll
   for (int j = 0; j < kTm; ++j) {
-    const int64_t m = m0 + wave_m + 32 * j + r32;
-    const float scale = m < a.rows ? a.u_scale[m] : 0.0f;
+    const int64_t first = m0 + wave_m + 32 * j;
+    const float scale = first + r32 < a.rows ? a.u_scale[first + r32] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < kTn; ++i) {
-      const int n = n0 + wave_n + 32 * i + 16 * half;
-      if (m >= a.rows) continue;
+    for (int i0 = 0; i0 < kTn; i0 += kAcross) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {  // outputs are a multiple of 8
-        if (n + 8 * g >= a.outputs) continue;
-        float v[8];
+      for (int i = i0; i < i0 + kAcross; ++i) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[e] = (float)sum[i][j][8 * g + e] * (scale * a.w_scale[n + 8 * g + e]);
-          if (a.bias) v[e] += a.bias[n + 8 * g + e];
+        for (int g = 0; g < 16 / kEach; ++g) {
+          const int n = n0 + wave_n + 32 * i + 16 * half + g * kEach;
+          float v[kEach];
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) v[e] = 0.0f;
+          if (n < a.outputs) {  // outputs are a multiple of 8
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+              v[e] = (float)sum[i][j][g * kEach + e] * (scale * a.w_scale[n + e]);
+              if (a.bias) v[e] += a.bias[n + e];
+            }
+          }
+          store_elems((T*)(mem + r32 * kLong) + (i - i0) * 32 + 16 * half + g * kEach, v);
         }
-        store_elems((T*)a.y + m * a.y_row + n + 8 * g, v);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+      for (int r = 0; r < 32; r += kTall) {
+        const int row = r + lane / kChunks, at = lane % kChunks;
+        const int n = n0 + wave_n + 32 * i0 + at * kEach;
+        const u32x4 x = *(const u32x4*)(mem + row * kLong + at * 16);
+        if (first + row < a.rows && n < a.outputs)
+          *(u32x4*)((T*)a.y + (first + row) * a.y_row + n) = x;
       }
     }
   }
