@@ -356,27 +356,41 @@ __global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a
   constexpr int kRowBytes = kAcross * 32 * (int)sizeof(T), kLong = kRowBytes + 16;
   constexpr int kChunks = kRowBytes / 16, kTall = 64 / kChunks, kEach = 16 / (int)sizeof(T);
   char* const mem = s_mem + wave * 32 * kLong;
+  // scales and biases of all this lane's results, in one round trip
+  float scale[kTm], w_scale[kTn][16], bias[kTn][16];
+#pragma unroll
+  for (int j = 0; j < kTm; ++j) {
+    const int64_t m = m0 + wave_m + 32 * j + r32;
+    scale[j] = a.u_scale[m < a.rows ? m : a.rows - 1];
+  }
+#pragma unroll
+  for (int i = 0; i < kTn; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; e += 8) {
+      // outputs are a multiple of 8
+      const int n = min(n0 + wave_n + 32 * i + 16 * half + e, a.outputs - 8);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        w_scale[i][e + x] = a.w_scale[n + x];
+        bias[i][e + x] = a.bias ? a.bias[n + x] : 0.0f;
+      }
+    }
   static_assert(kWaves * 32 * kLong <= 2 * kBytes, "the tiles' place holds the results");
 #pragma unroll
   for (int j = 0; j < kTm; ++j) {
     const int64_t first = m0 + wave_m + 32 * j;
-    const float scale = first + r32 < a.rows ? a.u_scale[first + r32] : 0.0f;
 #pragma unroll
     for (int i0 = 0; i0 < kTn; i0 += kAcross) {
 #pragma unroll
       for (int i = i0; i < i0 + kAcross; ++i) {
 #pragma unroll
         for (int g = 0; g < 16 / kEach; ++g) {
-          const int n = n0 + wave_n + 32 * i + 16 * half + g * kEach;
           float v[kEach];
 #pragma unroll
-          for (int e = 0; e < kEach; ++e) v[e] = 0.0f;
-          if (n < a.outputs) {  // outputs are a multiple of 8
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-              v[e] = (float)sum[i][j][g * kEach + e] * (scale * a.w_scale[n + e]);
-              if (a.bias) v[e] += a.bias[n + e];
-            }
+          for (int e = 0; e < kEach; ++e) {
+            const int x = g * kEach + e;
+            v[e] = (float)sum[i][j][x] * (scale[j] * w_scale[i][x]);
+            if (a.bias) v[e] += bias[i][x];
           }
           store_elems((T*)(mem + r32 * kLong) + (i - i0) * 32 + 16 * half + g * kEach, v);
         }
