@@ -122,16 +122,18 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int ch
 // weights are on their way, which saves a launch: up to eight rows of at most
 // kOwnElems elements (rows rounded up to a power of two).
 constexpr int kAheadOfAll = 64;
-constexpr int kOwnElems = 32768;
+constexpr int kOutputsOf16 = 16 * 256;
+constexpr int kKeep = 4;  // pieces of eight elements, a lane
+template <int kWaves>
+constexpr int kOwnElems = kWaves * 64 * 8 * kKeep;
 template <typename T, int kTiles, int kWaves, bool kOwn>
 __global__ void __launch_bounds__(kWaves * 64, 4) linear_few_kernel(LinearArgs a) {
   constexpr int kAhead = kAheadOfAll / kWaves;
-  constexpr int kKeep = kOwnElems / (8 * kWaves * 64);  // pieces of eight elements, a lane
   __shared__ i32x4 s_sum[kWaves][kTiles][64];
   __shared__ uint32_t s_top[8];
   // a row of codes is 16 bytes longer than its inputs, so that the 16 rows read
   // together fall on different banks
-  __shared__ __align__(16) int8_t s_codes[kOwn ? kOwnElems + 8 * 16 : 16];
+  __shared__ __align__(16) int8_t s_codes[kOwn ? kOwnElems<kWaves> + 8 * 16 : 16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n0 = blockIdx.x * 16;
   const int64_t m0 = (int64_t)blockIdx.y * (16 * kTiles);
@@ -194,6 +196,20 @@ __global__ void __launch_bounds__(kWaves * 64, 4) linear_few_kernel(LinearArgs a
     const int64_t m = m0 + 16 * t + (lane & 15), row = m < a.rows ? m : a.rows - 1;
     u[t] = kOwn ? s_codes + row * (a.inputs + 16) + part : a.u + row * a.inputs + part;
   }
+  // the results that this lane will store: one row, four outputs
+  static_assert(kTiles <= kWaves, "a tile of rows a wavefront");
+  const int64_t m = m0 + 16 * wave + (lane & 15);
+  const int n = n0 + 4 * (lane >> 4);
+  const bool stored = wave < kTiles && m < a.rows && n < a.outputs;
+  float scale = 0.0f, w_scale[4] = {0.0f, 0.0f, 0.0f, 0.0f}, bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (stored) {
+    if (!kOwn) scale = a.u_scale[m];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w_scale[i] = a.w_scale[n + i];
+      if (a.bias) bias[i] = a.bias[n + i];
+    }
+  }
   i32x4 sum[kTiles];
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) sum[t] = i32x4{0, 0, 0, 0};
@@ -213,23 +229,19 @@ __global__ void __launch_bounds__(kWaves * 64, 4) linear_few_kernel(LinearArgs a
 #pragma unroll
   for (int t = 0; t < kTiles; ++t) s_sum[wave][t][lane] = sum[t];
   __syncthreads();
-  for (int t = wave; t < kTiles; t += kWaves) {
-    i32x4 all = s_sum[0][t][lane];
+  if (wave >= kTiles) return;
+  i32x4 all = s_sum[0][wave][lane];
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) all += s_sum[i][t][lane];
-    const int64_t m = m0 + 16 * t + (lane & 15);
-    const int n = n0 + 4 * (lane >> 4);
-    if (m >= a.rows || n >= a.outputs) continue;
-    const float scale =
-        kOwn ? RowScale(__builtin_bit_cast(float, s_top[m & 7])).scale : a.u_scale[m];
-    float v[4];
+  for (int i = 1; i < kWaves; ++i) all += s_sum[i][wave][lane];
+  if (!stored) return;
+  if (kOwn) scale = RowScale(__builtin_bit_cast(float, s_top[m & 7])).scale;
+  float v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = (float)all[i] * (scale * a.w_scale[n + i]);
-      if (a.bias) v[i] += a.bias[n + i];
-    }
-    store_elems((T*)a.y + m * a.y_row + n, v);
+  for (int i = 0; i < 4; ++i) {
+    v[i] = (float)all[i] * (scale * w_scale[i]);
+    if (a.bias) v[i] += bias[i];
   }
+  store_elems((T*)a.y + m * a.y_row + n, v);
 }
 
 // Place in a staged tile of 128-byte rows: 16-byte chunk c of row r stands at
@@ -430,7 +442,7 @@ hipError_t quantize(int64_t rows, int64_t channels, const gs_rows& x, int8_t* co
 template <typename T, int kTiles, bool kOwn>
 hipError_t few(const LinearArgs& a, hipStream_t s) {
   const dim3 grid((a.outputs + 15) / 16, (uint32_t)((a.rows + 16 * kTiles - 1) / (16 * kTiles)));
-  if (grid.x <= 256) linear_few_kernel<T, kTiles, 16, kOwn><<<grid, 16 * 64, 0, s>>>(a);
+  if (a.outputs <= kOutputsOf16) linear_few_kernel<T, kTiles, 16, kOwn><<<grid, 16 * 64, 0, s>>>(a);
   else linear_few_kernel<T, kTiles, 8, kOwn><<<grid, 8 * 64, 0, s>>>(a);
   return hipGetLastError();
 }
@@ -451,7 +463,7 @@ hipError_t many(LinearArgs a, hipStream_t s) {
 // 4,096 10.7 : 11.0, of 2,048 by 8,192 10.9 : 12.4.
 bool own_codes(int64_t rows, int64_t inputs, int64_t outputs) {
   const int64_t shares = rows <= 2 ? rows : rows <= 4 ? 4 : 8;
-  return rows <= 8 && shares * inputs <= kOwnElems &&
+  return rows <= 8 && shares * inputs <= (outputs <= kOutputsOf16 ? kOwnElems<16> : kOwnElems<8>) &&
          shares * inputs * outputs <= (int64_t)96 << 20;
 }
 
