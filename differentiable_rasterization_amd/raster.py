@@ -944,6 +944,28 @@ def gs_gated_scan_bwd(cfg, docs, rows, gate, x, saved, dL_dy, dL_dstate_out, dL_
 # ---------------------------------------------------------------------------
 # Serving in 8 and 4 bits
 # ---------------------------------------------------------------------------
+_devices = None  # how many there are
+
+
+def _one_device(stream, *arrays):
+    """Refuses tensors, views and caches of another device than the call's: that of
+    the stream, or the current one.  With one device there is nothing to look at."""
+    global _devices
+    if _devices is None:
+        import torch
+        _devices = torch.cuda.device_count()
+    if _devices < 2:
+        return
+    import torch
+    here = torch.cuda.current_device() if stream is None else \
+        getattr(stream, "device_index", None)
+    for a in arrays:
+        for t in getattr(a, "tensors", (getattr(a, "tensor", a),)):
+            there = t.get_device() if hasattr(t, "get_device") else -1
+            if here is not None and there >= 0 and there != here:
+                raise ValueError("a tensor of device %d in a call on device %d" % (there, here))
+
+
 def linear_config(dtype, inputs, outputs) -> gs_linear_config:
     """dtype: a torch dtype, of x and y."""
     return gs_linear_config(_dtype(dtype), int(inputs), int(outputs))
@@ -953,6 +975,7 @@ def gs_quantize_rows(dtype, rows, channels, x, codes, scales, stream=None):
     """dtype: a torch dtype; codes: int8 [rows, channels], scales: fp32 [rows]."""
     kind = _dtype(dtype)
     x = _rows(x, (kind, rows, channels))
+    _one_device(stream, x, codes, scales)
     _check(load().gs_quantize_rows(kind, rows, channels, _where(x), _at(codes, _I8, rows * channels),
                                    _at(scales, _F32, rows), _stream(stream)))
 
@@ -966,6 +989,7 @@ def gs_linear_i8(cfg, rows, x, weight, weight_scale, bias, y, workspace, workspa
     """weight: int8 [outputs, inputs], weight_scale: fp32 [outputs], bias: the same or None."""
     kind, k, n = cfg.dtype, cfg.inputs, cfg.outputs
     x, y = _rows(x, (kind, rows, k)), _rows(y, (kind, rows, n))
+    _one_device(stream, x, y, weight, weight_scale, bias, workspace)
     _check(load().gs_linear_i8(
         C.byref(cfg), rows, _where(x), _at(weight, _I8, n * k), _at(weight_scale, _F32, n),
         _at(bias, _F32, n), _where(y), _bytes(workspace, workspace_bytes), int(workspace_bytes),
@@ -1021,6 +1045,7 @@ def cache_config(dtype, heads, head_dim) -> gs_cache_config:
 def gs_cache_write(cfg, docs, rows_q, rows_k, k, v, k_cache, v_cache, stream=None):
     want, held = (cfg.dtype, rows_q, cfg.heads, cfg.head_dim), (rows_k, cfg.heads, cfg.head_dim)
     k, v = _heads(k, want), _heads(v, want)
+    _one_device(stream, docs, k, v, k_cache, v_cache)
     _check(load().gs_cache_write(C.byref(cfg), C.byref(docs), rows_q, rows_k, _where(k), _where(v),
                                  _codes(k_cache, *held), _codes(v_cache, *held),
                                  _stream(stream)))
@@ -1029,6 +1054,7 @@ def gs_cache_write(cfg, docs, rows_q, rows_k, k, v, k_cache, v_cache, stream=Non
 def gs_cache_read(cfg, docs, rows_q, rows_k, k_cache, v_cache, k, v, stream=None):
     want, held = (cfg.dtype, rows_q, cfg.heads, cfg.head_dim), (rows_k, cfg.heads, cfg.head_dim)
     k, v = _heads(k, want), _heads(v, want)
+    _one_device(stream, docs, k, v, k_cache, v_cache)
     _check(load().gs_cache_read(C.byref(cfg), C.byref(docs), rows_q, rows_k,
                                 _codes(k_cache, *held), _codes(v_cache, *held), _where(k),
                                 _where(v), _stream(stream)))
@@ -1050,6 +1076,7 @@ def gs_cached_attention_fwd(cfg, docs, shared, rows_q, rows_k, q, k_cache, v_cac
     hq, dim = cfg.heads_q, cfg.head_dim
     want, held = (cfg.dtype, rows_q, hq, dim), (rows_k, cfg.heads_k, dim)
     q, out = _heads(q, want), _heads(out, want)
+    _one_device(stream, docs, shared, q, k_cache, v_cache, out, lse, workspace)
     _check(load().gs_cached_attention_fwd(
         C.byref(cfg), C.byref(docs), _shared(shared), rows_q, rows_k, _where(q),
         _codes(k_cache, *held), _codes(v_cache, *held), _where(out), _at(lse, _F32, hq * rows_q),

@@ -7,11 +7,14 @@ document, gated scan along it) and a last product writes the Gaussians' planes.
 Each scene is rendered against its image, and the gradients the rasterizer
 returns for its Gaussians go back through the network.  ``step`` is the same
 layer in serving: one new token for every document, with the keys and values
-cached and the scan's state carried on.
+cached and the scan's state carried on.  ``Served`` is the layer as it is served in
+8 bits: its products' weights and its cache are kept in 8 (the cache also in 4)
+bits, and a prompt that all requests share is in the cache once.
 
     python examples/token_splats.py [steps]
 
-The matrix products are torch's; everything else on the tokens is the library's.
+In training the matrix products are torch's; everything else on the tokens is the
+library's, in serving in 8 bits its products too.
 """
 import os
 import sys
@@ -144,6 +147,82 @@ class TokenLayer:
         raster.gs_gated_scan_fwd(self.scan, docs, n, gx[:, :self.C], gx[:, self.C:],
                                  cache["state"], h, cache["state"], None, None, 0)
         return (y + h).float() @ self.w["head"]
+
+
+class Served:
+    """A trained layer with 8-bit weights, for requests that share a prompt."""
+
+    def __init__(self, layer, requests, room, prompt=0, bits=8):
+        self.layer, self.bits, self.requests, self.room = layer, bits, requests, room
+        self.prompt, self.used, self.rows = prompt, 0, prompt + requests * room
+        self.w = {}
+        for name in ("qkv", "out", "gate"):
+            w = layer.w[name].T.contiguous()                     # [outputs, inputs]
+            codes = torch.empty(w.shape, dtype=torch.int8, device="cuda")
+            scales = torch.empty(len(w), device="cuda")
+            raster.gs_quantize_rows(w.dtype, *w.shape, w, codes, scales)
+            self.w[name] = codes, scales
+        self.cfg = raster.cache_config(HALF, layer.hk, layer.D)
+        size = (self.rows, layer.hk, layer.D * bits // 8)
+        self.cache = [raster.codes(torch.zeros(size, dtype=torch.uint8, device="cuda"),
+                                   *torch.zeros((2, layer.hk, self.rows), device="cuda"), bits)
+                      for _ in "kv"]
+        self.state = torch.zeros((requests, layer.C), device="cuda")
+
+    def _product(self, name, x):
+        codes, scales = self.w[name]
+        cfg = raster.linear_config(HALF, codes.shape[1], codes.shape[0])
+        y = torch.empty((len(x), codes.shape[0]), dtype=HALF, device="cuda")
+        size = raster.gs_linear_i8_workspace_size(cfg, len(x))
+        raster.gs_linear_i8(cfg, len(x), x, codes, scales, None, y, _space(size), size)
+        return y
+
+    def _run(self, x, positions, docs, shared, state):
+        """New tokens of all documents: into the cache, and through the layer."""
+        layer, n = self.layer, len(x)
+        qkv = self._product("qkv", x).view(n, layer.hq + 2 * layer.hk, layer.D)
+        q, k = qkv[:, :layer.hq], qkv[:, layer.hq:layer.hq + layer.hk]
+        q2, k2 = layer._turn(positions, q, k)
+        raster.gs_cache_write(self.cfg, docs, n, self.rows, k2, qkv[:, layer.hq + layer.hk:],
+                              *self.cache)
+        o = torch.empty_like(q2)
+        size = raster.gs_cached_attention_fwd_workspace_size(layer.attention, self.bits, docs,
+                                                             shared, n, self.rows)
+        raster.gs_cached_attention_fwd(layer.attention, docs, shared, n, self.rows, q2,
+                                       *self.cache, o, None, _space(size), size)
+        y = x + self._product("out", o.view(n, -1))
+        gx = self._product("gate", y)
+        h = torch.empty_like(x)
+        size = raster.gs_gated_scan_fwd_workspace_size(layer.scan, docs, n)
+        raster.gs_gated_scan_fwd(layer.scan, docs, n, gx[:, :layer.C], gx[:, layer.C:], state, h,
+                                 state, None, _space(size), size)
+        return (y + h).float() @ layer.w["head"]
+
+    def take_prompt(self, x):
+        """The shared prompt, x [prompt, C]: its keys stand in front of all requests."""
+        n = len(x)
+        assert n == self.prompt and self.used == 0
+        docs = raster.documents(_ints([0]), _ints([n]), _ints([0]), _ints([n]), max_q_len=n,
+                                max_k_len=n)
+        state = torch.zeros((1, self.layer.C), device="cuda")
+        p = self._run(x, torch.arange(n, dtype=torch.int32, device="cuda"), docs, None, state)
+        self.state.copy_(state.expand_as(self.state))
+        return p
+
+    def step(self, x):
+        """One new token of every request, x [requests, C]."""
+        n, at = len(x), self.used
+        assert n == self.requests and at < self.room
+        one = torch.ones(n, dtype=torch.int32, device="cuda")
+        first = torch.arange(n, dtype=torch.int32, device="cuda")
+        docs = raster.documents(first, one, self.prompt + first * self.room, one * (at + 1),
+                                max_q_len=1, max_k_len=at + 1)
+        shared = None
+        if self.prompt:
+            shared = raster.documents(_ints([0]), _ints([n]), _ints([0]), _ints([self.prompt]),
+                                      max_q_len=n, max_k_len=self.prompt)
+        self.used = at + 1
+        return self._run(x, one * (self.prompt + at), docs, shared, self.state)
 
 
 class Adam:

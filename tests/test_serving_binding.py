@@ -121,6 +121,50 @@ def test_arrays_of_a_cache_are_checked(lib, monkeypatch):
         make()
 
 
+class Elsewhere:
+    """A tensor as if it were on a device."""
+
+    def __init__(self, t, device):
+        self.t, self.device_index = t, device
+
+    def get_device(self):
+        return self.device_index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("i,name", ARRAYS)
+def test_tensors_of_another_device_are_refused(lib, monkeypatch, i, name):
+    import types
+    t = _calls()[i][2][name]
+    fn, first, arrays, last = _calls()[i]
+    call = lambda there, here: fn(*first, *dict(arrays, **{name: Elsewhere(t, there)}).values(),
+                                  *last, stream=types.SimpleNamespace(cuda_stream=0,
+                                                                      device_index=here))
+    monkeypatch.setattr(raster, "_devices", 2)
+    with pytest.raises(ValueError):
+        call(1, 0)
+    assert lib.calls == 0
+    call(1, 1)
+    call(-1, 0)                                                  # page-locked
+    monkeypatch.setattr(raster, "_devices", 1)
+    call(1, 0)
+    assert lib.calls == 3
+
+
+def test_a_cache_of_another_device_is_refused(lib, monkeypatch):
+    import types
+    monkeypatch.setattr(raster, "_devices", 2)
+    fn, first, arrays, last = _calls()[2]
+    c = _cache()
+    c.tensors = tuple(Elsewhere(t, 1) for t in c.tensors)
+    stream = types.SimpleNamespace(cuda_stream=0, device_index=0)
+    with pytest.raises(ValueError):
+        fn(*first, *dict(arrays, k_cache=c).values(), *last, stream=stream)
+    assert lib.calls == 0
+
+
 def test_types_are_named():
     with pytest.raises(ValueError):
         raster.linear_config(torch.float64, 16, 8)
