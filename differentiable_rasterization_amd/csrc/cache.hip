@@ -21,6 +21,7 @@ struct CacheArgs {
   float* low[2];
   float* step[2];
   int64_t row[2], head[2], ld[2];  // strides of codes in bytes; of low and step
+  int looked_up;  // units are those of the documents' tokens, else documents
   uint32_t block0;
 };
 
@@ -81,33 +82,38 @@ struct Item {
 };
 
 // The heads of a workgroup's tokens, kLanes lanes each, kItems of them at a time
-// a lane: take(items, first element).
+// a lane: take(items, first element).  Its tokens are one unit of a document, or
+// where documents are no longer than one all of a document's.
 constexpr int kItems = 4;
 template <int kLanes, typename F>
 __device__ inline void each_heads(const CacheArgs& a, F take) {
-  uint32_t local, units;
+  uint32_t local = 0, units;
   Doc d;
-  if (find_document<false>(a.docs, 1, kUnit, a.block0 + blockIdx.x, &local, &units, &d) < 0)
+  if (!a.looked_up) d = load_doc(a.docs, (int)(a.block0 + blockIdx.x));
+  else if (find_document<false>(a.docs, 1, kUnit, a.block0 + blockIdx.x, &local, &units, &d) < 0)
     return;
-  const int first = (int)local * kUnit, count = min(kUnit, d.ql - first);
-  const uint32_t both = 2u * (uint32_t)a.heads, items = (uint32_t)count * both;
+  const uint32_t both = 2u * (uint32_t)a.heads;
   constexpr uint32_t kGroups = 256 / kLanes;
-  for (uint32_t base = threadIdx.x / kLanes; base < items; base += kItems * kGroups) {
-    Item item[kItems];
+  const int end = a.looked_up ? min((int)(local + 1) * kUnit, d.ql) : d.ql;
+  for (int first = (int)local * kUnit; first < end; first += kUnit) {
+    const uint32_t items = (uint32_t)min(kUnit, end - first) * both;
+    for (uint32_t base = threadIdx.x / kLanes; base < items; base += kItems * kGroups) {
+      Item item[kItems];
 #pragma unroll
-    for (int p = 0; p < kItems; ++p) {
-      // what is not there repeats the last, up to what is written
-      const uint32_t at = base + p * kGroups, i = min(at, items - 1);
-      const int token = first + (int)(i / both), which = (int)(i % both);
-      // the document's last tokens are its last keys
-      const int key = token + d.kl - d.ql;
-      item[p].here = at < items;
-      item[p].token = d.qs + token;
-      item[p].row = key < 0 ? -1 : d.ks + key;
-      item[p].kv = which >= a.heads;
-      item[p].head = which - (item[p].kv ? a.heads : 0);
+      for (int p = 0; p < kItems; ++p) {
+        // what is not there repeats the last, up to what is written
+        const uint32_t at = base + p * kGroups, i = min(at, items - 1);
+        const int token = first + (int)(i / both), which = (int)(i % both);
+        // the document's last tokens are its last keys
+        const int key = token + d.kl - d.ql;
+        item[p].here = at < items;
+        item[p].token = d.qs + token;
+        item[p].row = key < 0 ? -1 : d.ks + key;
+        item[p].kv = which >= a.heads;
+        item[p].head = which - (item[p].kv ? a.heads : 0);
+      }
+      take(item, (int)(threadIdx.x % kLanes) * 8);
     }
-    take(item, (int)(threadIdx.x % kLanes) * 8);
   }
 }
 
@@ -183,7 +189,9 @@ __global__ void __launch_bounds__(256) cache_read_kernel(CacheArgs a) {
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = lo[p] + step[p] * (float)u[p][i];
-      if (item[p].here) store_elems((T*)a.x[kv] + item[p].token * a.x_row[kv] + item[p].head * a.x_head[kv] + e, x);
+      if (item[p].here)
+        store_elems((T*)a.x[kv] + item[p].token * a.x_row[kv] + item[p].head * a.x_head[kv] + e,
+                    x);
     }
   });
 }
@@ -192,7 +200,8 @@ namespace {
 
 template <bool kWrite, typename T, int kBits>
 hipError_t run(CacheArgs a, hipStream_t s) {
-  const int64_t blocks = (int64_t)a.docs.rows_q / kUnit + a.docs.count;
+  const int64_t blocks = a.looked_up ? (int64_t)a.docs.rows_q / kUnit + a.docs.count
+                                     : a.docs.count;
   return launch_all(blocks, 256, [&](uint32_t first, dim3 n) {
     a.block0 = first;
     if constexpr (kWrite) {
@@ -211,6 +220,7 @@ hipError_t run(const gs_cache_config& cfg, const gs_documents& d, int64_t rows_q
                hipStream_t s) {
   CacheArgs a = {};
   a.docs = make_docs(d, rows_q, rows_k);
+  a.looked_up = d.max_q_len == 0 || d.max_q_len > kUnit;
   a.heads = cfg.heads;
   a.dim = cfg.head_dim;
   const gs_heads* x[2] = {&k, &v};

@@ -789,7 +789,8 @@ __global__ void __launch_bounds__(256, 2) cached_many_kernel(CachedArgs a) {
 
 // A token's pieces of one head, and those of the keys it shares: kLanes lanes
 // have the head's elements, four each, and the groups of so many lanes take
-// pieces in turn; what they found meets in LDS.  kThreads is 64 where there are
+// pieces in turn; what they found meets in LDS.  A workgroup has one token, or all
+// of a document of few.  kThreads is 64 where there are
 // few pieces, else 256.
 constexpr int kMostPieces = 256;  // of a pass
 template <typename T, int kLanes, int kThreads>
@@ -800,83 +801,89 @@ __global__ void __launch_bounds__(kThreads) cached_join_kernel(CachedArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t block = a.block0 + blockIdx.x;
   const int head = (int)(block % (uint32_t)a.heads_q);
-  uint32_t local, units;
+  uint32_t local = 0, units;
   Doc d;
-  if (find_document<false>(a.docs, 1, 1, block / (uint32_t)a.heads_q, &local, &units, &d) < 0)
+  if (!a.looked_up) d = load_doc(a.docs, (int)(block / (uint32_t)a.heads_q));
+  else if (find_document<false>(a.docs, 1, 1, block / (uint32_t)a.heads_q, &local, &units, &d) < 0)
     return;
-  const int64_t token = d.qs + (int)local;
-  const int size = piece_keys(d.kl, a.pieces, a.piece);
-  const int own = max(1, (int)(((int64_t)d.kl + size - 1) / size));
-  int more = 0;
-  for (int base = 0; base < a.shared.count; base += 64) {
-    Doc g = {0, 0, 0, 0, 0};
-    if (base + lane < a.shared.count) g = load_doc(a.shared, base + lane);
-    const uint64_t hit = __ballot(token >= g.qs && token < (int64_t)g.qs + g.ql);
-    if (!hit) continue;
-    const int kl = __builtin_amdgcn_readlane(g.kl, __ffsll((unsigned long long)hit) - 1);
-    const int n = piece_keys(kl, a.pieces_shared, a.piece_shared);
-    more = (int)(((int64_t)kl + n - 1) / n);
-    break;
-  }
-  const int count = own + more;
-  const auto slot = [&](int p) {
-    return ((int64_t)(p < own ? p : a.pieces + p - own) * a.heads_q + head) * a.docs.rows_q + token;
-  };
-  // what each piece counts for: its sum times 2^(its reference - the largest)
-  float top = -INFINITY;
-  for (int p = threadIdx.x; p < count; p += kThreads) {
-    const f32x2 ml = *(const f32x2*)(a.part_ml + 2 * slot(p));
-    s_f[p] = ml.x;
-    top = ml.y == 0.0f ? top : fmaxf(top, ml.x);
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-  if (kWaves > 1) {
-    if (lane == 0) s_top[wave] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) top = fmaxf(top, s_top[i]);
-  }
-  float sum = 0.0f;
-  for (int p = threadIdx.x; p < count; p += kThreads) {
-    const float l = a.part_ml[2 * slot(p) + 1];
-    // a piece whose sum is zero holds zeros
-    const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(s_f[p] - top);
-    s_f[p] = f;
-    sum = fmaf(f, l, sum);
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if (kWaves > 1 && lane == 0) s_sum[wave] = sum;
-  __syncthreads();
-  if (kWaves > 1) {
-    sum = s_sum[0];
-#pragma unroll
-    for (int i = 1; i < kWaves; ++i) sum += s_sum[i];
-  }
-  const int group = threadIdx.x / kLanes, e = (threadIdx.x % kLanes) * 4;
-  f32x4 x = (f32x4)(0.0f);
-  if (e < a.dim) {
-#pragma unroll 4
-    for (int p = group; p < count; p += kGroups) {
-      const f32x4 v = *(const f32x4*)(a.part_o + slot(p) * a.dim + e);
-      const float f = s_f[p];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = fmaf(f, v[i], x[i]);
+  const int last = a.looked_up ? (int)local + 1 : d.ql;
+  for (int t = (int)local; t < last; ++t) {
+    const int64_t token = d.qs + t;
+    const int size = piece_keys(d.kl, a.pieces, a.piece);
+    const int own = max(1, (int)(((int64_t)d.kl + size - 1) / size));
+    int more = 0;
+    for (int base = 0; base < a.shared.count; base += 64) {
+      Doc g = {0, 0, 0, 0, 0};
+      if (base + lane < a.shared.count) g = load_doc(a.shared, base + lane);
+      const uint64_t hit = __ballot(token >= g.qs && token < (int64_t)g.qs + g.ql);
+      if (!hit) continue;
+      const int kl = __builtin_amdgcn_readlane(g.kl, __ffsll((unsigned long long)hit) - 1);
+      const int n = piece_keys(kl, a.pieces_shared, a.piece_shared);
+      more = (int)(((int64_t)kl + n - 1) / n);
+      break;
     }
-  }
-  s_o[group][threadIdx.x % kLanes] = x;
-  __syncthreads();
-  if (group == 0 && e < a.dim) {
+    const int count = own + more;
+    const auto slot = [&](int p) {
+      const int at = p < own ? p : a.pieces + p - own;
+      return ((int64_t)at * a.heads_q + head) * a.docs.rows_q + token;
+    };
+    // what each piece counts for: its sum times 2^(its reference - the largest)
+    float top = -INFINITY;
+    for (int p = threadIdx.x; p < count; p += kThreads) {
+      const f32x2 ml = *(const f32x2*)(a.part_ml + 2 * slot(p));
+      s_f[p] = ml.x;
+      top = ml.y == 0.0f ? top : fmaxf(top, ml.x);
+    }
 #pragma unroll
-    for (int i = 1; i < kGroups; ++i) x += s_o[i][threadIdx.x];
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
-    store_elems((T*)(a.out + token * a.out_row + head * a.out_head + e), y);
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    if (kWaves > 1) {
+      if (lane == 0) s_top[wave] = top;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kWaves; ++i) top = fmaxf(top, s_top[i]);
+    }
+    float sum = 0.0f;
+    for (int p = threadIdx.x; p < count; p += kThreads) {
+      const float l = a.part_ml[2 * slot(p) + 1];
+      // a piece whose sum is zero holds zeros
+      const float f = l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(s_f[p] - top);
+      s_f[p] = f;
+      sum = fmaf(f, l, sum);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 64);
+    if (kWaves > 1 && lane == 0) s_sum[wave] = sum;
+    __syncthreads();
+    if (kWaves > 1) {
+      sum = s_sum[0];
+#pragma unroll
+      for (int i = 1; i < kWaves; ++i) sum += s_sum[i];
+    }
+    const int group = threadIdx.x / kLanes, e = (threadIdx.x % kLanes) * 4;
+    f32x4 x = (f32x4)(0.0f);
+    if (e < a.dim) {
+#pragma unroll 4
+      for (int p = group; p < count; p += kGroups) {
+        const f32x4 v = *(const f32x4*)(a.part_o + slot(p) * a.dim + e);
+        const float f = s_f[p];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fmaf(f, v[i], x[i]);
+      }
+    }
+    s_o[group][threadIdx.x % kLanes] = x;
+    __syncthreads();
+    if (group == 0 && e < a.dim) {
+#pragma unroll
+      for (int i = 1; i < kGroups; ++i) x += s_o[i][threadIdx.x];
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
+      store_elems((T*)(a.out + token * a.out_row + head * a.out_head + e), y);
+    }
+    if (a.lse && threadIdx.x == 0)
+      a.lse[(int64_t)head * a.docs.rows_q + token] =
+          sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    __syncthreads();  // before LDS is the next token's
   }
-  if (a.lse && threadIdx.x == 0)
-    a.lse[(int64_t)head * a.docs.rows_q + token] =
-        sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
 namespace {
@@ -923,7 +930,10 @@ Cut cut_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q
     if (o.width == 16 && piece > 2048) piece = 2048;
     piece = (piece + kStepKeys - 1) / kStepKeys * kStepKeys;
     if (piece < 2 * kStepKeys) piece = 2 * kStepKeys;
-    pieces = kMostPieces;
+    // workgroups without work cost little, but not nothing: 2^15 at most, where the
+    // target asks for no more
+    const int64_t room = (1 << 15) / base;
+    pieces = pieces > room ? pieces : room < kMostPieces ? room : kMostPieces;
   }
   const int64_t most = (longest_k + piece - 1) / piece;
   if (pieces > most) pieces = most;
@@ -978,13 +988,15 @@ hipError_t run(const CachedArgs& a, const Plan& p, const Docs& shared, hipStream
   if (e != hipSuccess || p.whole) return e;
   CachedArgs j = a;
   j.shared = shared;
+  j.looked_up = p.own.looked_up;
   j.pieces = p.own.pieces;
   j.piece = p.own.piece;
   j.piece_shared = p.shared.piece;
   j.pieces_shared = p.shared.pieces;
   // with up to 16 pieces a wavefront has them in a few loads
   const int threads = p.own.pieces + p.shared.pieces <= 16 ? 64 : 256;
-  return launch_all((int64_t)a.docs.rows_q * a.heads_q, threads, [&](uint32_t first, dim3 n) {
+  const int64_t units = j.looked_up ? a.docs.rows_q : a.docs.count;
+  return launch_all(units * a.heads_q, threads, [&](uint32_t first, dim3 n) {
     j.block0 = first;
     constexpr int kLanes = DT / 4;
     if (threads == 64) cached_join_kernel<T, kLanes, 64><<<n, 64, 0, s>>>(j);

@@ -170,3 +170,24 @@ def test_nothing_to_do():
     y = x.clone()
     raster.gs_cache_read(cfg, nothing, 3, 4, c.view(), Cache(4, 2, 32, 4).view(), x, y)
     assert (x == 7.0).all() and (y == 7.0).all()
+
+
+@pytest.mark.parametrize("hint", [0, 1, 5, 8, 9, 100])
+def test_hints_do_not_matter(hint):
+    """Documents of one token, of some and of many, whatever the caller says of them."""
+    ql, kl = [1, 0, 30, 8, 9], [4, 2, 33, 8, 10]
+    qs, ks = [0, 1, 1, 31, 39], [0, 4, 6, 40, 50]
+    x = _normal(hint, torch.float16, 48, 6, 48)
+    k, v = x[:, :3], x[:, 3:]
+    caches = [Cache(64, 3, 48, 4) for _ in range(2)]
+    tokens = [a + i for a, n in zip(qs, ql) for i in range(n)]
+    rows = [b + m - n + i for b, m, n in zip(ks, kl, ql) for i in range(n)]
+    want = [_written(c, t, tokens, rows) for c, t in zip(caches, (k, v))]
+    docs = raster.documents(*map(_ints, (qs, ql, ks, kl)), max_q_len=hint)
+    cfg = raster.cache_config(torch.float16, 3, 48)
+    raster.gs_cache_write(cfg, docs, 48, 64, k, v, *[c.view() for c in caches])
+    assert all(_same(_copy(c), w) for c, w in zip(caches, want))
+    out = [torch.full((48, 3, 48), 9.0, dtype=torch.float16, device="cuda") for _ in range(2)]
+    raster.gs_cache_read(cfg, docs, 48, 64, *[c.view() for c in caches], *out)
+    for c, t in zip(caches, out):
+        assert torch.equal(t[tokens], _values(c, rows, torch.float16))
