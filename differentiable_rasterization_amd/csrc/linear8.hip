@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int ch
 // weights are on their way, which saves a launch: up to eight rows of at most
 // kOwnElems elements (rows rounded up to a power of two).
 constexpr int kAheadOfAll = 64;
-constexpr int kOutputsOf16 = 16 * 256;
+constexpr int kUnits = 256;  // compute units
+constexpr int kOutputsOf16 = 16 * kUnits;
 constexpr int kKeep = 4;  // pieces of eight elements, a lane
 template <int kWaves>
 constexpr int kOwnElems = kWaves * 64 * 8 * kKeep;
@@ -293,14 +294,15 @@ __device__ inline i32x4 rows_from(const int8_t* base, int64_t bytes) {
 }
 
 // Many rows: tiles of kM rows by kN outputs, kWm by kWn wavefronts of 32x32x32
-// products, 128 inputs a step, two tiles in LDS: while one is multiplied the
-// next is copied in.
-template <typename T, int kM, int kN, int kWm, int kWn>
+// products, 128 inputs a step, kStages of them in LDS: while one is multiplied the
+// next ones are copied in.
+template <typename T, int kM, int kN, int kWm, int kWn, int kStages>
 __global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a) {
   constexpr int kWaves = kWm * kWn;
   constexpr int kTm = kM / kWm / 32, kTn = kN / kWn / 32;
   constexpr int kBytes = (kM + kN) * 128;
-  __shared__ __align__(1024) char s_mem[2 * kBytes];
+  constexpr int kCopies = (kM + kN) / 8 / kWaves;  // of a stage, a wavefront
+  __shared__ __align__(1024) char s_mem[kStages * kBytes];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   // Workgroups go to the eight XCDs in turn; each XCD takes a run of tiles, in
   // blocks of eight tiles of rows, so that its L2 holds what they share.
@@ -337,13 +339,19 @@ __global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a
   for (int i = 0; i < kTn; ++i)
 #pragma unroll
     for (int j = 0; j < kTm; ++j) sum[i][j] = (i32x16)(0);
+  // What is copied past the inputs' end are zeros, that no step reads: so many copies
+  // are under way at every step.
   const int steps = (a.inputs + 127) / 128;
-  copy(0, 0);
-  for (int s = 0; s < steps; ++s) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  constexpr int kEarly = kStages - 1;
+#pragma unroll
+  for (int s = 0; s < kEarly; ++s) copy(s * 128, s);
+  for (int s = 0, at = 0, to = kEarly; s < steps; ++s) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kEarly - 1) * kCopies) : "memory");
     __syncthreads();
-    if (s + 1 < steps) copy((s + 1) * 128, (s + 1) & 1);
-    const char* mem = s_mem + (s & 1) * kBytes;
+    copy((s + kEarly) * 128, to);
+    const char* mem = s_mem + at * kBytes;
+    at = at + 1 == kStages ? 0 : at + 1;
+    to = to + 1 == kStages ? 0 : to + 1;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       i32x4 w[kTn], u[kTm];
@@ -363,6 +371,7 @@ __global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a
   // Results go through LDS, 32 rows by 128 bytes of a wavefront at a time, so that
   // whole lines are written.  A row there is 16 bytes longer: sixteen rows fall on
   // different banks.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   constexpr int kAcross = kTn * 32 * (int)sizeof(T) < 128 ? kTn : 4 / (int)sizeof(T);
   constexpr int kRowBytes = kAcross * 32 * (int)sizeof(T), kLong = kRowBytes + 16;
@@ -387,7 +396,7 @@ __global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a
         bias[i][e + x] = a.bias ? a.bias[n + x] : 0.0f;
       }
     }
-  static_assert(kWaves * 32 * kLong <= 2 * kBytes, "the tiles' place holds the results");
+  static_assert(kWaves * 32 * kLong <= kStages * kBytes, "the tiles' place holds the results");
 #pragma unroll
   for (int j = 0; j < kTm; ++j) {
     const int64_t first = m0 + wave_m + 32 * j;
@@ -447,11 +456,11 @@ hipError_t few(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int kM, int kN, int kWm, int kWn>
+template <typename T, int kM, int kN, int kWm, int kWn, int kStages>
 hipError_t many(LinearArgs a, hipStream_t s) {
   a.tiles_n = (uint32_t)((a.outputs + kN - 1) / kN);
   a.tiles = (uint32_t)((a.rows + kM - 1) / kM) * a.tiles_n;
-  linear_many_kernel<T, kM, kN, kWm, kWn>
+  linear_many_kernel<T, kM, kN, kWm, kWn, kStages>
       <<<dim3((a.tiles + 7) / 8 * 8), kWm * kWn * 64, 0, s>>>(a);
   return hipGetLastError();
 }
@@ -474,12 +483,28 @@ hipError_t linear(const LinearArgs& a, hipStream_t s) {
   if (a.rows <= 32) return few<T, 2, false>(a, s);
   if (a.rows <= 48) return few<T, 3, false>(a, s);
   if (a.rows <= 64) return few<T, 4, false>(a, s);
-  const auto tiles = [&](int64_t side) {
-    return ((a.rows + side - 1) / side) * ((a.outputs + side - 1) / side);
+  const auto tiles = [&](int64_t tall, int64_t wide) {
+    return ((a.rows + tall - 1) / tall) * ((a.outputs + wide - 1) / wide);
   };
-  if (tiles(256) >= 192) return many<T, 256, 256, 2, 4>(a, s);
-  if (tiles(128) >= 256) return many<T, 128, 128, 2, 2>(a, s);
-  return many<T, 64, 64, 2, 2>(a, s);
+  // Small tiles, each with two steps on their way, where there are so few of them that
+  // all run at a time and wait for memory (us, 64 x 64 : 128 x 128, with 2,048
+  // inputs: 300 by 2,048 13.0 : 17.7, 1,024 by 2,048 15.3 : 18.4; 1,500 by 2,048
+  // 19.9 : 19.4; with one step on its way 1,024 by 2,048 16.5).
+  if (tiles(64, 64) <= 2 * kUnits) return many<T, 64, 64, 2, 2, 3>(a, s);
+  // A tile a compute unit: two steps on their way, or two workgroups with one each
+  // (2,048 by 2,048 20.5 : 21.6; with more tiles, 4,096 by 2,048, 33.3 : 30.3).
+  const int64_t n128 = tiles(128, 128);
+  if (n128 <= kUnits) return many<T, 128, 128, 2, 2, 3>(a, s);
+  // Else the form whose last tiles end first: a unit takes about 10, 25 and 32 us
+  // for a tile of 128 x 128, 192 x 256 and 256 x 256 with 2,048 inputs (us of the
+  // three: 1,024 by 8,192 28.4, 30.5, 34.3; 1,500 by 8,192 38.6, 34.3, 36.7; 4,096 by
+  // 4,096 48.4, 55.8, 44.6; 9,000 by 4,096 109, 99, 112).
+  const auto turns = [](int64_t n) { return (n + kUnits - 1) / kUnits; };
+  const int64_t t128 = 10 * turns(n128), t192 = 25 * turns(tiles(192, 256)),
+                t256 = 32 * turns(tiles(256, 256));
+  if (t256 < t128 && t256 <= t192) return many<T, 256, 256, 2, 4, 2>(a, s);
+  if (t192 < t128) return many<T, 192, 256, 2, 4, 2>(a, s);
+  return many<T, 128, 128, 2, 2, 2>(a, s);
 }
 
 size_t codes_bytes(int64_t rows, int64_t channels) {

@@ -1076,7 +1076,7 @@ def gs_cached_attention_fwd(cfg, docs, shared, rows_q, rows_k, q, k_cache, v_cac
     hq, dim = cfg.heads_q, cfg.head_dim
     want, held = (cfg.dtype, rows_q, hq, dim), (rows_k, cfg.heads_k, dim)
     q, out = _heads(q, want), _heads(out, want)
-    _one_device(stream, docs, shared, q, k_cache, v_cache, out, lse, workspace)
+    _one_device(stream, cfg, docs, shared, q, k_cache, v_cache, out, lse, workspace)
     _check(load().gs_cached_attention_fwd(
         C.byref(cfg), C.byref(docs), _shared(shared), rows_q, rows_k, _where(q),
         _codes(k_cache, *held), _codes(v_cache, *held), _where(out), _at(lse, _F32, hq * rows_q),

@@ -106,6 +106,16 @@ def test_large_products(dtype, rows, inputs, outputs):
     _check(x, w, ws, bias, _run(x, w, ws, bias))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("inputs", [16, 144, 272, 656])
+@pytest.mark.parametrize("rows,outputs", [(1601, 2056), (3001, 2056), (5900, 2040), (4090, 4088)])
+def test_products_of_few_steps_in_each_tile(dtype, rows, outputs, inputs):
+    """128 by 128 outputs with two steps ahead and with one, 192 by 256, 256 by 256."""
+    x = _normal(rows + inputs, dtype, rows, inputs)
+    w, ws, bias = _weights(outputs, outputs, inputs, inputs != 272)
+    _check(x, w, ws, bias, _run(x, w, ws, bias))
+
+
 @pytest.mark.parametrize("rows", [5, 40, 300])
 def test_sums_at_their_ends(rows):
     """All codes at the ends of their range and inputs at their most: sums near

@@ -165,6 +165,17 @@ def test_a_cache_of_another_device_is_refused(lib, monkeypatch):
     assert lib.calls == 0
 
 
+def test_slopes_of_another_device_are_refused(lib, monkeypatch):
+    import types
+    monkeypatch.setattr(raster, "_devices", 2)
+    fn, first, arrays, last = _calls()[4]
+    first[0].tensor = Elsewhere(torch.zeros(first[0].heads_q), 1)
+    stream = types.SimpleNamespace(cuda_stream=0, device_index=0)
+    with pytest.raises(ValueError):
+        fn(*first, *arrays.values(), *last, stream=stream)
+    assert lib.calls == 0
+
+
 def test_types_are_named():
     with pytest.raises(ValueError):
         raster.linear_config(torch.float64, 16, 8)
