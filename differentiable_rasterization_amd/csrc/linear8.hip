@@ -109,14 +109,16 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int ch
   }
 }
 
-// Few rows: the product is the reading of the weights.  A workgroup has 16
+// Up to 16 rows: the product is the reading of the weights.  A workgroup has 16
 // outputs, its wavefronts a share of the inputs each; weights and codes go from
 // memory straight into the operands of the 16x16x64 instruction (rows lane %
 // 16, 16 inputs a lane), and the wavefronts' sums meet in LDS.  Weights of
-// the first kAheadOfAll steps are on their way before anything else is looked at.
+// the first kAheadOfAll steps are on their way before anything else is looked at:
+// 16.8 MB of them, one row of 2,048 by 8,192, take 6.1 us with the call (2.8 TB/s; a
+// launch alone is about 3).
 // 16 wavefronts where there is a workgroup a compute unit or less, 8 where there
 // are more (us, 16 : 8; one row of 4,096 by 4,096 7.2 : 8.3, of 2,048 by 8,192
-// 9.2 : 8.6; 33 rows of 4,096 by 4,096 13.8 : 14.5).
+// 9.2 : 8.6).
 //
 // kOwn: rows are brought to codes here, by every workgroup for itself while its
 // weights are on their way, which saves a launch: up to eight rows of at most
@@ -127,17 +129,16 @@ constexpr int kOutputsOf16 = 16 * kUnits;
 constexpr int kKeep = 4;  // pieces of eight elements, a lane
 template <int kWaves>
 constexpr int kOwnElems = kWaves * 64 * 8 * kKeep;
-template <typename T, int kTiles, int kWaves, bool kOwn>
+template <typename T, int kWaves, bool kOwn>
 __global__ void __launch_bounds__(kWaves * 64, 4) linear_few_kernel(LinearArgs a) {
   constexpr int kAhead = kAheadOfAll / kWaves;
-  __shared__ i32x4 s_sum[kWaves][kTiles][64];
+  __shared__ i32x4 s_sum[kWaves][64];
   __shared__ uint32_t s_top[8];
   // a row of codes is 16 bytes longer than its inputs, so that the 16 rows read
   // together fall on different banks
   __shared__ __align__(16) int8_t s_codes[kOwn ? kOwnElems<kWaves> + 8 * 16 : 16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n0 = blockIdx.x * 16;
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * kTiles);
   const int steps = (a.inputs + 63) / 64;
   const int share = (steps + kWaves - 1) / kWaves;
   const int first = wave * share, last = min(steps, first + share);
@@ -191,17 +192,11 @@ __global__ void __launch_bounds__(kWaves * 64, 4) linear_few_kernel(LinearArgs a
     }
     __syncthreads();
   }
-  const int8_t* u[kTiles];
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    const int64_t m = m0 + 16 * t + (lane & 15), row = m < a.rows ? m : a.rows - 1;
-    u[t] = kOwn ? s_codes + row * (a.inputs + 16) + part : a.u + row * a.inputs + part;
-  }
   // the results that this lane will store: one row, four outputs
-  static_assert(kTiles <= kWaves, "a tile of rows a wavefront");
-  const int64_t m = m0 + 16 * wave + (lane & 15);
-  const int n = n0 + 4 * (lane >> 4);
-  const bool stored = wave < kTiles && m < a.rows && n < a.outputs;
+  const int rows = (int)a.rows, m = lane & 15, n = n0 + 4 * (lane >> 4);
+  const int8_t* u = kOwn ? s_codes + min(m, rows - 1) * (a.inputs + 16) + part
+                         : a.u + (int64_t)min(m, rows - 1) * a.inputs + part;
+  const bool stored = wave == 0 && m < rows && n < a.outputs;
   float scale = 0.0f, w_scale[4] = {0.0f, 0.0f, 0.0f, 0.0f}, bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (stored) {
     if (!kOwn) scale = a.u_scale[m];
@@ -211,38 +206,29 @@ __global__ void __launch_bounds__(kWaves * 64, 4) linear_few_kernel(LinearArgs a
       if (a.bias) bias[i] = a.bias[n + i];
     }
   }
-  i32x4 sum[kTiles];
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) sum[t] = i32x4{0, 0, 0, 0};
+  i32x4 sum = {0, 0, 0, 0};
   for (int s0 = first; s0 < last; s0 += kAhead) {
     if (s0 > first) load_weights(s0);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const bool in = s0 + i < last && 64 * (s0 + i) + part < a.inputs;
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        i32x4 y = {0, 0, 0, 0};
-        if (in) y = *(const i32x4*)(u[t] + 64 * (s0 + i));
-        sum[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(ahead[i], y, sum[t], 0, 0, 0);
-      }
+      i32x4 y = {0, 0, 0, 0};
+      if (s0 + i < last && 64 * (s0 + i) + part < a.inputs) y = *(const i32x4*)(u + 64 * (s0 + i));
+      sum = __builtin_amdgcn_mfma_i32_16x16x64_i8(ahead[i], y, sum, 0, 0, 0);
     }
   }
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) s_sum[wave][t][lane] = sum[t];
+  s_sum[wave][lane] = sum;
   __syncthreads();
-  if (wave >= kTiles) return;
-  i32x4 all = s_sum[0][wave][lane];
-#pragma unroll
-  for (int i = 1; i < kWaves; ++i) all += s_sum[i][wave][lane];
   if (!stored) return;
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) sum += s_sum[i][lane];
   if (kOwn) scale = RowScale(__builtin_bit_cast(float, s_top[m & 7])).scale;
   float v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[i] = (float)all[i] * (scale * w_scale[i]);
+    v[i] = (float)sum[i] * (scale * w_scale[i]);
     if (a.bias) v[i] += bias[i];
   }
-  store_elems((T*)a.y + m * a.y_row + n, v);
+  store_elems((T*)a.y + (int64_t)m * a.y_row + n, v);
 }
 
 // Place in a staged tile of 128-byte rows: 16-byte chunk c of row r stands at
@@ -263,7 +249,7 @@ struct Stage {
   uint32_t at[kCopies];
   int chunk[kCopies];
   __device__ inline void start(int inputs) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) % kWaves;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
       const int r = (i * kWaves + wave) * 8 + (lane >> 3);
@@ -272,12 +258,12 @@ struct Stage {
     }
   }
   __device__ inline void copy(const i32x4& rsrc, uint32_t lds, int k, int inputs) {
-    const int wave = threadIdx.x >> 6;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % kWaves);
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
       // chunks past the row's end arrive as zeros
       const uint32_t from = k + chunk[i] < inputs ? at[i] + (uint32_t)k : 0x80000000u;
-      const uint32_t to = __builtin_amdgcn_readfirstlane(lds + (i * kWaves + wave) * 1024);
+      const uint32_t to = lds + (i * kWaves + wave) * 1024;
       asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(
                        from),
                    "s"(rsrc), "s"(to)
@@ -293,17 +279,20 @@ __device__ inline i32x4 rows_from(const int8_t* base, int64_t bytes) {
                (int)__builtin_amdgcn_readfirstlane((uint32_t)bytes), 0x00027000};
 }
 
-// Many rows: tiles of kM rows by kN outputs, kWm by kWn wavefronts of 32x32x32
+// More rows: tiles of kM rows by kN outputs, kWm by kWn wavefronts of 32x32x32
 // products, 128 inputs a step, kStages of them in LDS: while one is multiplied the
-// next ones are copied in.
-template <typename T, int kM, int kN, int kWm, int kWn, int kStages>
-__global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a) {
+// next ones are copied in.  With kSplit above 1 that many such groups of wavefronts
+// take the steps in turn, each with stages of its own, and their sums meet at the end.
+template <typename T, int kM, int kN, int kWm, int kWn, int kStages, int kSplit>
+__global__ void __launch_bounds__(kWm* kWn* kSplit * 64) linear_many_kernel(LinearArgs a) {
   constexpr int kWaves = kWm * kWn;
   constexpr int kTm = kM / kWm / 32, kTn = kN / kWn / 32;
   constexpr int kBytes = (kM + kN) * 128;
   constexpr int kCopies = (kM + kN) / 8 / kWaves;  // of a stage, a wavefront
-  __shared__ __align__(1024) char s_mem[kStages * kBytes];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ __align__(1024) char s_mem[kSplit * kStages * kBytes];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) % kWaves);
+  const int group = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) / kWaves);
   // Workgroups go to the eight XCDs in turn; each XCD takes a run of tiles, in
   // blocks of eight tiles of rows, so that its L2 holds what they share.
   const uint32_t each = (a.tiles + 7) / 8;
@@ -323,9 +312,11 @@ __global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a
   Stage<kN, kWaves, true> stage_w;
   stage_u.start(a.inputs);
   stage_w.start(a.inputs);
-  auto copy = [&](int k, int buffer) {
-    stage_u.copy(from_u, lds + buffer * kBytes, k, a.inputs);
-    stage_w.copy(from_w, lds + buffer * kBytes + kM * 128, k, a.inputs);
+  auto copy = [&](int s, int buffer) {
+    const int k = (s * kSplit + group) * 128;
+    const uint32_t to = lds + (group * kStages + buffer) * kBytes;
+    stage_u.copy(from_u, to, k, a.inputs);
+    stage_w.copy(from_w, to + kM * 128, k, a.inputs);
   };
   // operand rows of this lane: its output row m of a 32-row product is such that
   // the sixteen results it gets are sixteen outputs side by side
@@ -341,17 +332,15 @@ __global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a
     for (int j = 0; j < kTm; ++j) sum[i][j] = (i32x16)(0);
   // What is copied past the inputs' end are zeros, that no step reads: so many copies
   // are under way at every step.
-  const int steps = (a.inputs + 127) / 128;
+  const int steps = (a.inputs + kSplit * 128 - 1) / (kSplit * 128);
   constexpr int kEarly = kStages - 1;
 #pragma unroll
-  for (int s = 0; s < kEarly; ++s) copy(s * 128, s);
+  for (int s = 0; s < kEarly; ++s) copy(s, s);
   for (int s = 0, at = 0, to = kEarly; s < steps; ++s) {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kEarly - 1) * kCopies) : "memory");
     __syncthreads();
-    copy((s + kEarly) * 128, to);
-    const char* mem = s_mem + at * kBytes;
+    const char* mem = s_mem + (group * kStages + at) * kBytes;
     at = at + 1 == kStages ? 0 : at + 1;
-    to = to + 1 == kStages ? 0 : to + 1;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
       i32x4 w[kTn], u[kTm];
@@ -361,12 +350,15 @@ __global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a
 #pragma unroll
       for (int j = 0; j < kTm; ++j)
         u[j] = *(const i32x4*)(mem + (at_u ^ (ks * 32)) + j * 32 * 128);
+      // the first reads are on their way before the copies are
+      if (ks == 0) copy(s + kEarly, to);
 #pragma unroll
       for (int i = 0; i < kTn; ++i)
 #pragma unroll
         for (int j = 0; j < kTm; ++j)
           sum[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[i], u[j], sum[i][j], 0, 0, 0);
     }
+    to = to + 1 == kStages ? 0 : to + 1;
   }
   // Results go through LDS, 32 rows by 128 bytes of a wavefront at a time, so that
   // whole lines are written.  A row there is 16 bytes longer: sixteen rows fall on
@@ -377,6 +369,31 @@ __global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a
   constexpr int kRowBytes = kAcross * 32 * (int)sizeof(T), kLong = kRowBytes + 16;
   constexpr int kChunks = kRowBytes / 16, kTall = 64 / kChunks, kEach = 16 / (int)sizeof(T);
   char* const mem = s_mem + wave * 32 * kLong;
+  constexpr int kParts = kTn * kTm * 4;
+  const auto part_of = [&](int p) {
+    const i32x16& x = sum[p / 4 / kTm][p / 4 % kTm];
+    const int i = p % 4 * 4;
+    return i32x4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+  };
+  if constexpr (kSplit > 1) {
+    // the groups' sums meet behind the place of the results
+    i32x4* const all = (i32x4*)(s_mem + kWaves * 32 * kLong) + wave * kParts * 64 + lane;
+    if (group > 0) {
+#pragma unroll
+      for (int p = 0; p < kParts; ++p)
+        all[((group - 1) * kWaves * kParts + p) * 64] = part_of(p);
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 0; g < kSplit - 1; ++g)
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) {
+        const i32x4 x = all[(g * kWaves * kParts + p) * 64];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[p / 4 / kTm][p / 4 % kTm][p % 4 * 4 + i] += x[i];
+      }
+  }
   // scales and biases of all this lane's results, in one round trip
   float scale[kTm], w_scale[kTn][16], bias[kTn][16];
 #pragma unroll
@@ -396,7 +413,8 @@ __global__ void __launch_bounds__(kWm* kWn * 64) linear_many_kernel(LinearArgs a
         bias[i][e + x] = a.bias ? a.bias[n + x] : 0.0f;
       }
     }
-  static_assert(kWaves * 32 * kLong <= kStages * kBytes, "the tiles' place holds the results");
+  static_assert(kWaves * (32 * kLong + (kSplit - 1) * kParts * 1024) <= kSplit * kStages * kBytes,
+                "the tiles' place holds the results");
 #pragma unroll
   for (int j = 0; j < kTm; ++j) {
     const int64_t first = m0 + wave_m + 32 * j;
@@ -448,20 +466,19 @@ hipError_t quantize(int64_t rows, int64_t channels, const gs_rows& x, int8_t* co
   });
 }
 
-template <typename T, int kTiles, bool kOwn>
+template <typename T, int kWaves, bool kOwn>
 hipError_t few(const LinearArgs& a, hipStream_t s) {
-  const dim3 grid((a.outputs + 15) / 16, (uint32_t)((a.rows + 16 * kTiles - 1) / (16 * kTiles)));
-  if (a.outputs <= kOutputsOf16) linear_few_kernel<T, kTiles, 16, kOwn><<<grid, 16 * 64, 0, s>>>(a);
-  else linear_few_kernel<T, kTiles, 8, kOwn><<<grid, 8 * 64, 0, s>>>(a);
+  linear_few_kernel<T, kWaves, kOwn>
+      <<<dim3((a.outputs + 15) / 16), kWaves * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <typename T, int kM, int kN, int kWm, int kWn, int kStages>
+template <typename T, int kM, int kN, int kWm, int kWn, int kStages, int kSplit = 1>
 hipError_t many(LinearArgs a, hipStream_t s) {
   a.tiles_n = (uint32_t)((a.outputs + kN - 1) / kN);
   a.tiles = (uint32_t)((a.rows + kM - 1) / kM) * a.tiles_n;
-  linear_many_kernel<T, kM, kN, kWm, kWn, kStages>
-      <<<dim3((a.tiles + 7) / 8 * 8), kWm * kWn * 64, 0, s>>>(a);
+  linear_many_kernel<T, kM, kN, kWm, kWn, kStages, kSplit>
+      <<<dim3((a.tiles + 7) / 8 * 8), kWm * kWn * kSplit * 64, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -478,18 +495,23 @@ bool own_codes(int64_t rows, int64_t inputs, int64_t outputs) {
 
 template <typename T>
 hipError_t linear(const LinearArgs& a, hipStream_t s) {
-  if (own_codes(a.rows, a.inputs, a.outputs)) return few<T, 1, true>(a, s);
-  if (a.rows <= 16) return few<T, 1, false>(a, s);
-  if (a.rows <= 32) return few<T, 2, false>(a, s);
-  if (a.rows <= 48) return few<T, 3, false>(a, s);
-  if (a.rows <= 64) return few<T, 4, false>(a, s);
+  const bool of16 = a.outputs <= kOutputsOf16;
+  if (own_codes(a.rows, a.inputs, a.outputs))
+    return of16 ? few<T, 16, true>(a, s) : few<T, 8, true>(a, s);
   const auto tiles = [&](int64_t tall, int64_t wide) {
     return ((a.rows + tall - 1) / tall) * ((a.outputs + wide - 1) / wide);
   };
-  // Small tiles, each with two steps on their way, where there are so few of them that
-  // all run at a time and wait for memory (us, 64 x 64 : 128 x 128, with 2,048
-  // inputs: 300 by 2,048 13.0 : 17.7, 1,024 by 2,048 15.3 : 18.4; 1,500 by 2,048
-  // 19.9 : 19.4; with one step on its way 1,024 by 2,048 16.5).
+  // us, few rows : tiles of 64 x 32 outputs: 16 rows of 8,192 by 2,048 14.0 : 15.4, of
+  // 4,096 by 4,096 11.4 : 11.3; with more outputs or rows every workgroup's reading
+  // of all rows weighs more (16 of 8,192 by 8,192 22.2 : 17.8, 33 of 4,096 by 4,096
+  // with three such groups of rows 13.4 : 11.7).
+  if (a.rows <= 16 && of16) return few<T, 16, false>(a, s);
+  // Small tiles while all run at a time and wait for memory and for each other's
+  // steps: the steps shared by four groups of wavefronts, by two, by none (us of the
+  // three: 64 rows of 4,096 by 4,096 11.8, 12.9, 14.5; 200 of them 17.8, 13.3, 14.8;
+  // 1,024 of 2,048 by 2,048 24.3, 17.3, 14.6).
+  if (tiles(64, 32) <= kUnits) return many<T, 64, 32, 2, 1, 3, 4>(a, s);
+  if (tiles(64, 64) <= kUnits) return many<T, 64, 64, 2, 2, 3, 2>(a, s);
   if (tiles(64, 64) <= 2 * kUnits) return many<T, 64, 64, 2, 2, 3>(a, s);
   // A tile a compute unit: two steps on their way, or two workgroups with one each
   // (2,048 by 2,048 20.5 : 21.6; with more tiles, 4,096 by 2,048, 33.3 : 30.3).

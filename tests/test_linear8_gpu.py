@@ -107,10 +107,13 @@ def test_large_products(dtype, rows, inputs, outputs):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("inputs", [16, 144, 272, 656])
-@pytest.mark.parametrize("rows,outputs", [(1601, 2056), (3001, 2056), (5900, 2040), (4090, 4088)])
+@pytest.mark.parametrize("inputs", [16, 144, 272, 656, 1552])
+@pytest.mark.parametrize("rows,outputs", [(1601, 2056), (3001, 2056), (5900, 2040), (4090, 4088),
+                                          (10, 4104), (40, 1032), (64, 8), (190, 4088),
+                                          (600, 2056)])
 def test_products_of_few_steps_in_each_tile(dtype, rows, outputs, inputs):
-    """128 by 128 outputs with two steps ahead and with one, 192 by 256, 256 by 256."""
+    """128 by 128 outputs with two steps ahead and with one, 192 by 256, 256 by 256, 64 by
+    32 with the steps in four parts, 64 by 64 in two and in one."""
     x = _normal(rows + inputs, dtype, rows, inputs)
     w, ws, bias = _weights(outputs, outputs, inputs, inputs != 272)
     _check(x, w, ws, bias, _run(x, w, ws, bias))
