@@ -50,7 +50,8 @@ struct CachedArgs {
   int first_piece;  // of this pass, in the arrays above
   int whole;        // one piece and nothing shared: the result is written at once
   int looked_up;    // column tiles are units of the grid, else documents
-  uint32_t units, block0;
+  int width;        // columns of a workgroup
+  uint32_t units, blocks, block0;
 };
 
 constexpr int kStepKeys = 128;  // keys the four wavefronts take at a time
@@ -273,8 +274,7 @@ struct Work {
   int hk, piece, key0, keys;
   int first, end, cols;
 };
-__device__ inline bool find_work(const CachedArgs& a, int width, Work& w) {
-  const uint32_t block = a.block0 + blockIdx.x;
+__device__ inline bool find_work(const CachedArgs& a, uint32_t block, int width, Work& w) {
   const uint32_t turn = block >> 3;
   w.hk = (int)(turn % (uint32_t)a.heads_k);
   const uint32_t place = turn / (uint32_t)a.heads_k * 8 + (block & 7);
@@ -588,20 +588,23 @@ __device__ inline void leave(const CachedArgs& a, const Work& w, int c, int firs
 // Few columns: 16 CT a workgroup, its wavefronts take the piece's keys in turn.
 // With 16 the kernel is the reading of the cache, with 32 its arithmetic weighs as
 // much.  A tile is in flight in the registers that the one before has freed.
+template <int DT>
+struct FewMemory {
+  f32x4 num[4][kNumbers / 4];
+  float o[4][16][DT + 4], m[4][16], l[4][16], c[4][16];
+};
 template <typename T, int kBits, int DT, int CT, int kMode>
-__global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : 2)
-    cached_few_kernel(CachedArgs a) {
+__device__ inline void few_columns(const CachedArgs& a, uint32_t block, FewMemory<DT>& mem) {
   typedef KeyCodes<T, kBits> K;
   typedef ValueCodes<kBits, DT> V;
-  constexpr int kSteps = DT / 32, kElems = V::kElems, kStride = DT + 4;
-  __shared__ __align__(16) float s_o[4][16][kStride];
-  __shared__ float s_m[4][16], s_l[4][16], s_c[4][16];
-  __shared__ __align__(16) float s_num[4][kNumbers];
+  constexpr int kSteps = DT / 32, kElems = V::kElems;
+  auto &s_o = mem.o;
+  auto &s_m = mem.m, &s_l = mem.l, &s_c = mem.c;
   const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
   const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Work w;
-  if (!find_work(a, 16 * CT, w)) return;
-  float* const nums = s_num[wave];
+  if (!find_work(a, block, 16 * CT, w)) return;
+  float* const nums = (float*)mem.num[wave];
   const float to_log2 = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
   for (int col0 = w.first; col0 < w.end; col0 += 16 * CT) {
     const int last_col = min(col0 + 16 * CT, w.cols) - 1;
@@ -690,19 +693,24 @@ __global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : 2)
 // keys to operands, in LDS and in the order in which lanes read them, for all
 // four: a quarter of the conversions that the few-column form would make.
 constexpr int kManyCols = 128;
+template <int DT>
+struct ManyMemory {
+  u32x4 k[4][DT / 16][64], v[4][DT / 16][64];
+  f32x4 num[4][kNumbers / 4];
+  float top[4];
+};
 template <typename T, int kBits, int DT, int kMode>
-__global__ void __launch_bounds__(256, 2) cached_many_kernel(CachedArgs a) {
+__device__ inline void many_columns(const CachedArgs& a, uint32_t block, ManyMemory<DT>& mem) {
   typedef KeyCodes<T, kBits> K;
   typedef ValueCodes<kBits, DT> V;
   typedef typename Mat16<T>::V8 V8;
   constexpr int CT = 2, kSteps = DT / 32, kElems = V::kElems;
-  __shared__ __align__(16) u32x4 s_k[4][2 * kSteps][64], s_v[4][kElems][64];
-  __shared__ __align__(16) float s_num[4][kNumbers];
-  __shared__ float s_top[4];
+  auto &s_k = mem.k, &s_v = mem.v;
+  auto& s_top = mem.top;
   const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
   const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Work w;
-  if (!find_work(a, kManyCols, w)) return;
+  if (!find_work(a, block, kManyCols, w)) return;
   const float to_log2 = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
   for (int col0 = w.first; col0 < w.end; col0 += kManyCols) {
     const int last_col = min(col0 + kManyCols, w.cols) - 1;
@@ -723,7 +731,7 @@ __global__ void __launch_bounds__(256, 2) cached_many_kernel(CachedArgs a) {
       // all have read the tiles before
       __syncthreads();
       if (lane == 0) s_top[wave] = own < key_end ? larger : 0.0f;
-      tile.leave_numbers(s_num[wave], st, to_log2);
+      tile.leave_numbers((float*)mem.num[wave], st, to_log2);
       tile.load_numbers(own + kStepKeys);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -755,7 +763,7 @@ __global__ void __launch_bounds__(256, 2) cached_many_kernel(CachedArgs a) {
             for (int ct = 0; ct < CT; ++ct) s[t][ct] = Mat16<T>::mul(x, col.q[ct][i], s[t][ct]);
           }
         f16x8 p[CT];
-        col.template weigh<true>(a, s_num[sub], s, key + 32 > all_see || key + 32 > key_end,
+        col.template weigh<true>(a, (const float*)mem.num[sub], s, key + 32 > all_see || key + 32 > key_end,
                                  key + 4 * kg, key_end, p);
 #pragma unroll
         for (int e = 0; e < kElems; ++e)
@@ -785,6 +793,39 @@ __global__ void __launch_bounds__(256, 2) cached_many_kernel(CachedArgs a) {
       }
     }
   }
+}
+
+template <typename T, int kBits, int DT, int CT, int kMode>
+__global__ void __launch_bounds__(256, CT == 1 ? (DT == 64 ? 4 : 3) : 2)
+    cached_few_kernel(CachedArgs a) {
+  __shared__ FewMemory<DT> s_mem;
+  few_columns<T, kBits, DT, CT, kMode>(a, a.block0 + blockIdx.x, s_mem);
+}
+template <typename T, int kBits, int DT, int kMode>
+__global__ void __launch_bounds__(256, 2) cached_many_kernel(CachedArgs a) {
+  __shared__ ManyMemory<DT> s_mem;
+  many_columns<T, kBits, DT, kMode>(a, a.block0 + blockIdx.x, s_mem);
+}
+
+// Both passes in one launch, the shared keys' workgroups first: those of either hide
+// what the other waits for.
+template <typename T, int kBits, int DT, int kMode>
+__global__ void __launch_bounds__(256, 2) cached_both_kernel(CachedArgs own, CachedArgs shared) {
+  __shared__ __align__(16) union {
+    FewMemory<DT> few;
+    ManyMemory<DT> many;
+  } s_mem;
+  const uint32_t block = own.block0 + blockIdx.x;
+  const bool of_shared = block < shared.blocks;
+  // read where the launch has put them: a choice between two arguments would
+  // copy both into scratch memory
+  typedef const __attribute__((address_space(4))) CachedArgs* Args;
+  const CachedArgs a =
+      *(const CachedArgs*)((Args)__builtin_amdgcn_kernarg_segment_ptr() + (of_shared ? 1 : 0));
+  const uint32_t at = of_shared ? block : block - shared.blocks;
+  if (a.width == 16) few_columns<T, kBits, DT, 1, kMode>(a, at, s_mem.few);
+  else if (a.width == 32) few_columns<T, kBits, DT, 2, kMode>(a, at, s_mem.few);
+  else many_columns<T, kBits, DT, kMode>(a, at, s_mem.many);
 }
 
 // A token's pieces of one head, and those of the keys it shares: kLanes lanes
@@ -959,14 +1000,19 @@ Plan plan_of(const gs_attention_config& cfg, const gs_documents& d, const gs_doc
 
 size_t ml_bytes(const Plan& p) { return ((size_t)p.slots * 8 + 255) / 256 * 256; }
 
-template <typename T, int kBits, int DT, int kMode>
-hipError_t pass(CachedArgs a, const Cut& c, hipStream_t s) {
+// Arguments of a pass; its workgroups.
+int64_t set_pass(CachedArgs& a, const Cut& c) {
   a.pieces = c.pieces;
   a.piece = c.piece;
   a.looked_up = c.looked_up;
+  a.width = c.width;
   a.units = (uint32_t)c.units;
-  const int64_t blocks = (c.units * c.pieces + 7) / 8 * 8 * a.heads_k;
-  return launch_all(blocks, 256, [&](uint32_t first, dim3 n) {
+  return (c.units * c.pieces + 7) / 8 * 8 * a.heads_k;
+}
+
+template <typename T, int kBits, int DT, int kMode>
+hipError_t pass(CachedArgs a, const Cut& c, hipStream_t s) {
+  return launch_all(set_pass(a, c), 256, [&](uint32_t first, dim3 n) {
     a.block0 = first;
     if (c.width == 16) cached_few_kernel<T, kBits, DT, 1, kMode><<<n, 256, 0, s>>>(a);
     else if (c.width == 32) cached_few_kernel<T, kBits, DT, 2, kMode><<<n, 256, 0, s>>>(a);
@@ -976,15 +1022,21 @@ hipError_t pass(CachedArgs a, const Cut& c, hipStream_t s) {
 
 template <typename T, int kBits, int DT, int kMode>
 hipError_t run(const CachedArgs& a, const Plan& p, const Docs& shared, hipStream_t s) {
-  if (p.shared.pieces > 0) {
-    CachedArgs b = a;
+  hipError_t e;
+  if (kMode != kBiased && p.shared.pieces > 0) {
+    CachedArgs own = a, b = a;
     b.docs = shared;
     b.causal = 0;
     b.first_piece = p.own.pieces;
-    const hipError_t e = pass<T, kBits, DT, kMode>(b, p.shared, s);
-    if (e != hipSuccess) return e;
+    const int64_t blocks = set_pass(b, p.shared);
+    b.blocks = (uint32_t)blocks;
+    e = launch_all(blocks + set_pass(own, p.own), 256, [&](uint32_t first, dim3 n) {
+      own.block0 = first;
+      cached_both_kernel<T, kBits, DT, kMode == kBiased ? kPlain : kMode><<<n, 256, 0, s>>>(own, b);
+    });
+  } else {
+    e = pass<T, kBits, DT, kMode>(a, p.own, s);
   }
-  const hipError_t e = pass<T, kBits, DT, kMode>(a, p.own, s);
   if (e != hipSuccess || p.whole) return e;
   CachedArgs j = a;
   j.shared = shared;
