@@ -15,6 +15,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -59,14 +61,25 @@ def source_hash() -> str:
 
 
 def build(verbose: bool = False) -> str:
+    """Each source in a compiler of its own, up to eight at a time, the longest first."""
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + flags() + [os.path.join(CSRC, s) for s in SOURCES] + ["-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("hipcc failed building libgsraster.so")
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("hipcc failed building libgsraster.so")
+
+    with tempfile.TemporaryDirectory() as there:
+        paths = sorted((os.path.join(CSRC, s) for s in SOURCES), key=os.path.getsize, reverse=True)
+        objects = [os.path.join(there, os.path.basename(p) + ".o") for p in paths]
+        compile_flags = [f for f in flags() if f != "-shared"]
+        with ThreadPoolExecutor(min(8, int(os.environ.get("MAX_JOBS") or 8))) as pool:
+            list(pool.map(lambda at: run([hipcc()] + compile_flags + ["-c", at[0], "-o", at[1]]),
+                          zip(paths, objects)))
+        run([hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC"] + objects + ["-o", tmp])
     os.replace(tmp, LIB)
     with open(HASH_FILE, "w") as fh:
         fh.write(source_hash() + "\n")

@@ -6,8 +6,11 @@
 // In 4 bits a 32-bit word holds eight elements, 2i in bits 4i and 2i + 1 in bits
 // 16 + 4i: a shift and a mask then give two elements in the halves of a word.
 //
-// Memory bound: eight elements a lane (16 bytes of a 16-bit type, 8 or 4 of
-// codes), 8 or 16 lanes a head, keys and values in one launch.
+// Eight elements a lane (16 bytes of a 16-bit type, 8 or 4 of codes), 8 or 16 lanes
+// a head, keys and values in one launch.  20,011 tokens of 8 heads of 64, fp16 to 4
+// bits: written in 22 us, where the codes' 64-bit arithmetic (half of about 1,000
+// vector instructions a wavefront) and the reading of 41 MB weigh alike, read back in
+// 15 (54 MB, 3.6 TB/s).  A few tokens: a launch, 4 to 5 us.
 #include "cached.h"
 
 namespace gs {

@@ -12,16 +12,26 @@
 //
 // Query heads that share a key head stand beside each other: column c of a
 // document is token c / group, head c % group.  A wavefront takes 32 keys at a
-// time by 16 or 64 columns, on the 16x16x32 instruction:
+// time by 16 or 32 columns, on the 16x16x32 instruction:
 //   S^T = K Q^T: lane l has column l % 16 and keys 4 (l / 16) + 0..3 of both
 //     16-key halves; its 8 weights are the right operand of
 //   O^T = V^T P^T, if the contraction runs over the keys in that order; the left
 //     operand takes single elements of those keys' rows, which each lane loads
 //     itself (16 lanes a row) and pairs by byte permutes.
-// So nothing passes through LDS but the four wavefronts' results at the end.
+// So scores and weights never leave their registers; what a key's low and step make
+// of a score or a weight passes through LDS, 512 bytes a tile, and where there are
+// many columns so do the operands, for all four wavefronts.
 //
 // Keys are cut into pieces where there are few columns; a second kernel joins a
 // token's pieces and those of the keys it shares.
+//
+// What bounds it.  One token a request: reading the codes (four caches of 120,001
+// keys in all, 4 heads of 128 in 8 bits: 131 MB in 38.5 us, 3.4 TB/s, and 5 for the
+// join; a large sum that only reads has 3.9).  Many columns: vector instructions and
+// matrix products of two wavefronts a SIMD that overlap little (1,024 tokens over
+// 32,768 keys, 16 heads of 128 over 4: 398 us, 0.68 PFLOP/s; vector issue in 41% of
+// the cycles, matrix unit at work in 23).  Small calls: two launches and a chain of
+// dependent loads (document, codes, pieces), about 15 us.
 #include "cached.h"
 
 namespace gs {
@@ -586,8 +596,8 @@ __device__ inline void leave(const CachedArgs& a, const Work& w, int c, int firs
 }
 
 // Few columns: 16 CT a workgroup, its wavefronts take the piece's keys in turn.
-// With 16 the kernel is the reading of the cache, with 32 its arithmetic weighs as
-// much.  A tile is in flight in the registers that the one before has freed.
+// With 16 it is the reading of the cache, with 32 its arithmetic weighs as much.  A
+// tile is in flight in the registers that the one before has freed.
 template <int DT>
 struct FewMemory {
   f32x4 num[4][kNumbers / 4];
@@ -808,7 +818,8 @@ __global__ void __launch_bounds__(256, 2) cached_many_kernel(CachedArgs a) {
 }
 
 // Both passes in one launch, the shared keys' workgroups first: those of either hide
-// what the other waits for.
+// what the other waits for (us with two launches : with one; 64 requests behind 16,384
+// keys 52.9 : 44.1, 48 behind three prompts 30.0 : 22.2).
 template <typename T, int kBits, int DT, int kMode>
 __global__ void __launch_bounds__(256, 2) cached_both_kernel(CachedArgs own, CachedArgs shared) {
   __shared__ __align__(16) union {
@@ -817,8 +828,9 @@ __global__ void __launch_bounds__(256, 2) cached_both_kernel(CachedArgs own, Cac
   } s_mem;
   const uint32_t block = own.block0 + blockIdx.x;
   const bool of_shared = block < shared.blocks;
-  // read where the launch has put them: a choice between two arguments would
-  // copy both into scratch memory
+  // Read where the launch has put them, one after the other: a choice between two
+  // arguments would copy both into scratch memory (104 us for the first of these).  A
+  // copy, since what is behind a pointer would be read again after each fence (91).
   typedef const __attribute__((address_space(4))) CachedArgs* Args;
   const CachedArgs a =
       *(const CachedArgs*)((Args)__builtin_amdgcn_kernarg_segment_ptr() + (of_shared ? 1 : 0));
@@ -831,8 +843,9 @@ __global__ void __launch_bounds__(256, 2) cached_both_kernel(CachedArgs own, Cac
 // A token's pieces of one head, and those of the keys it shares: kLanes lanes
 // have the head's elements, four each, and the groups of so many lanes take
 // pieces in turn; what they found meets in LDS.  A workgroup has one token, or all
-// of a document of few.  kThreads is 64 where there are
-// few pieces, else 256.
+// of a document of few.  kThreads is 64 where there are few pieces, else 256.  A
+// launch and three dependent reads, 5 us; of large results the pieces' reading (4
+// pieces of 1,024 tokens, 16 heads of 128: 34 MB in 12 us).
 constexpr int kMostPieces = 256;  // of a pass
 template <typename T, int kLanes, int kThreads>
 __global__ void __launch_bounds__(kThreads) cached_join_kernel(CachedArgs a) {

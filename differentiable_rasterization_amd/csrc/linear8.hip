@@ -7,6 +7,11 @@
 // The sums are whole numbers in 32 bits, so no order of them changes a result.
 // Codes are formed in 64 bits: the fp32 product would put a value next to the
 // border of two codes into either.
+//
+// What bounds it.  Few rows: reading the weights, and one launch or two.  Many: the
+// matrix unit at the clock that this load leaves it (16,384 rows of 4,096 by 8,192 in
+// 540 to 570 us, 1.9 to 2.0 POP/s, 50 us of it the codes; the products alone, without
+// loads or results, take 445).
 #include "tokens.h"
 
 namespace gs {
@@ -51,7 +56,8 @@ __device__ inline u32x2 codes_of(const float (&v)[8], const RowScale& r) {
 }
 
 // kLanes lanes a row; each keeps up to kKeep pieces of eight elements in
-// registers between the maximum and the codes and reads the others again.
+// registers between the maximum and the codes and reads the others again.  Memory
+// bound: 16,384 rows of 4,096 in bf16 in 50 us (201 MB, 4.0 TB/s); small ones a launch.
 template <typename T, int kLanes>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int channels, const T* x,
                                                             int64_t x_row, int8_t* codes,
