@@ -29,8 +29,8 @@
 // keys in all, 4 heads of 128 in 8 bits: 131 MB in 38.5 us, 3.4 TB/s, and 5 for the
 // join; a large sum that only reads has 3.9).  Many columns: vector instructions and
 // matrix products of two wavefronts a SIMD that overlap little (1,024 tokens over
-// 32,768 keys, 16 heads of 128 over 4: 398 us, 0.68 PFLOP/s; vector issue in 41% of
-// the cycles, matrix unit at work in 23).  Small calls: two launches and a chain of
+// 32,768 keys, 16 heads of 128 over 4: 400 us, 0.68 PFLOP/s; vector issue in 51% of
+// the cycles, matrix unit at work in 27).  Small calls: two launches and a chain of
 // dependent loads (document, codes, pieces), about 15 us.
 #include "cached.h"
 
