@@ -826,6 +826,8 @@ __global__ void __launch_bounds__(256, 2) cached_both_kernel(CachedArgs own, Cac
     FewMemory<DT> few;
     ManyMemory<DT> many;
   } s_mem;
+  static_assert(sizeof(CachedArgs) % alignof(CachedArgs) == 0 && alignof(CachedArgs) == 8,
+                "one argument right after the other");
   const uint32_t block = own.block0 + blockIdx.x;
   const bool of_shared = block < shared.blocks;
   // Read where the launch has put them, one after the other: a choice between two

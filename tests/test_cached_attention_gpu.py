@@ -176,6 +176,22 @@ def test_shared_keys(dtype, bits, heads_q, heads_k, dim):
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("own", [1, 9, 70])
+@pytest.mark.parametrize("sharing", [1, 8, 70])
+@pytest.mark.parametrize("softcap", [0.0, 5.0, 100.0])
+def test_shared_and_own_keys_in_each_form(dtype, bits, dim, own, sharing, softcap):
+    """16, 32 and 128 columns of either, causal, and rows that see no key at all."""
+    many = max(sharing // own, 1)
+    q_lens = [own] * many + [2, 3]
+    k_lens = [own + 37 * i for i in range(many)] + [0, 1]
+    c = Case(dtype, bits, 4, 1, dim, q_lens, k_lens, softcap=softcap,
+             shared=[(0, many, 700), (many, 1, 0)])
+    c.check(*c.run())
+
+
 @pytest.mark.parametrize("hints", [(0, 0), (1, 1), (1, 100000), (5, 40), (1 << 30, 1 << 30)])
 def test_hints_do_not_matter(hints):
     c = Case(torch.bfloat16, 8, 8, 2, 64, [40, 1, 7, 130], [2000, 900, 7, 131],
