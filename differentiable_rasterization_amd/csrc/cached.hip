@@ -379,9 +379,10 @@ struct Tiles {
   }
 };
 
-// The largest finite step of the values of a tile, if it is past twice the unit
-// that weights are relative to, else 0.
+// The largest finite step of the values of a tile, of either sign, if it is past
+// twice the unit that weights are relative to, else 0.
 __device__ inline float larger_step(float st, float unit_step) {
+  st = fabsf(st);
   const bool counts = (threadIdx.x & 32) != 0 && st < __builtin_huge_valf();
   if (!__ballot(counts && st >= 2.0f * unit_step)) return 0.0f;
   float top = counts ? st : 0.0f;

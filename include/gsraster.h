@@ -862,7 +862,7 @@ GS_API gs_status gs_linear_i8(const gs_linear_config* cfg, int64_t rows, const g
  * strides in bytes, multiples of 4, row below 2^25, heads and rows must not
  * overlap), low and step [heads][ld] fp32 with ld >= rows.  In 8 bits byte i is
  * element i; in 4 bits each 32-bit word holds eight elements, 2i in bits 4i ..
- * 4i + 3 and 2i + 1 in bits 16 + 4i .. 19 + 4i. */
+ * 4i + 3 and 2i + 1 in bits 16 + 4i .. 19 + 4i.  A step may be negative. */
 typedef struct {
   void* codes;
   float *low, *step;
