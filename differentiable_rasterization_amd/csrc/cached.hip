@@ -6,7 +6,7 @@
 // Codes are whole numbers that the 16-bit types hold exactly, so both products
 // run on the matrix unit from codes brought to 16 bits in registers; only the
 // weights p_j step_j are rounded, to fp16 (11 bits) for either type: taken
-// relative to a power of two near the largest step, so that they stay in its
+// relative to a power of two near the column's largest, so that they stay in its
 // range.  Codes are centred there, since the rounding of a weight acts on the
 // whole of what it multiplies.
 //
@@ -273,6 +273,17 @@ struct ValueRows {
 // 2^14.
 constexpr float kRoom = 8.0f, kGrowth = 6.0f;
 
+// Weights times steps become fp16 numbers relative to a unit, a power of two: the
+// largest lies in [2^kUnitRoom, 2 2^kUnitRoom) when the unit is taken, and the unit
+// moves when one passes 2^15.  What is below 2^-22 of a token's largest loses bits.
+constexpr int kUnitRoom = 8;
+constexpr float kMostWeight = 0x1p15f;
+
+__device__ inline int exponent_of(float x) {  // with its bias of 127; x >= 0
+  return (int)(__builtin_bit_cast(uint32_t, x) >> 23);
+}
+__device__ inline float power_of(int e) { return __builtin_bit_cast(float, (uint32_t)e << 23); }
+
 // kMode: plain scores, capped ones, or a distance bias (with or without a cap).
 constexpr int kPlain = 0, kCapped = 1, kBiased = 2;
 
@@ -363,37 +374,20 @@ struct Tiles {
     vp += (int64_t)kStepKeys * v_row;
     v.load(vp, v_row, bytes(key, v_row));
   }
-  // The step of this lane's key's values; what no column sees has no part in the
-  // range of the weights.
-  __device__ inline float seen_step(int key) const {
-    const int lane = threadIdx.x & 63;
-    return lane >= 32 && key + (lane & 31) >= key_end ? 0.0f : step;
-  }
-  // st: the step, of values times what weights are relative to.
-  __device__ inline void leave_numbers(float* nums, float st, float to_log2) const {
+  __device__ inline void leave_numbers(float* nums, float to_log2) const {
     const int lane = threadIdx.x & 63;
     const bool of_values = lane >= 32;
-    nums[2 * (lane & 32) + (lane & 31)] = of_values ? st : st * (K::kMul * to_log2);
+    nums[2 * (lane & 32) + (lane & 31)] = of_values ? step : step * (K::kMul * to_log2);
     nums[2 * (lane & 32) + 32 + (lane & 31)] =
         fmaf(step, of_values ? V::kMid : K::kOff, low) * (of_values ? 1.0f : to_log2);
   }
 };
 
-// The largest finite step of the values of a tile, of either sign, if it is past
-// twice the unit that weights are relative to, else 0.
-__device__ inline float larger_step(float st, float unit_step) {
-  st = fabsf(st);
-  const bool counts = (threadIdx.x & 32) != 0 && st < __builtin_huge_valf();
-  if (!__ballot(counts && st >= 2.0f * unit_step)) return 0.0f;
-  float top = counts ? st : 0.0f;
-#pragma unroll
-  for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
-  return top;
-}
-
 // CT times 16 columns of a wavefront: queries, and the running sums of a softmax.
-// Weights are relative to ref, which a score above most moves; steps to unit_step,
-// a power of two.
+// Weights are relative to ref, which a score above most moves; weights times steps
+// are fp16 numbers times 1 / per_unit, a power of two.  Both belong to the column and
+// move by what it sees alone, by powers of two: keys that it does not see, and what
+// stands in the columns beside it, leave its bits as they are.
 template <typename T, int kBits, int DT, int CT, int kMode>
 struct Columns {
   typedef ValueCodes<kBits, DT> V;
@@ -404,14 +398,11 @@ struct Columns {
   float qsum[CT], slope[CT];
   int limit[CT], pos[CT];
   f32x4 o[CT][kElems];
-  float ref[CT], most[CT], l[CT], mean[CT];
-  float unit_step, per_unit;
+  float ref[CT], most[CT], l[CT], mean[CT], per_unit[CT];
 
   // Columns past the last one repeat it, and are not stored.
   __device__ inline void start(const CachedArgs& a, const Work& w, int col0) {
     const int n = threadIdx.x & 15, kg = (threadIdx.x & 63) >> 4;
-    unit_step = 0x1p-126f;
-    per_unit = 0x1p126f;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
       const int c = min(col0 + 16 * ct + n, w.cols - 1);
@@ -437,36 +428,44 @@ struct Columns {
       slope[ct] = kMode == kBiased ? a.slopes[head] * kLog2e : 0.0f;
       most[ct] = -INFINITY;
       ref[ct] = l[ct] = mean[ct] = 0.0f;
+      per_unit[ct] = 0x1p126f;
 #pragma unroll
       for (int e = 0; e < kElems; ++e) o[ct][e] = (f32x4)(0.0f);
     }
   }
 
-  // Weights relative to the power of two below a step from here on.
-  __device__ inline void take_step(float top) {
-    const float now =
-        __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, top) & 0x7f800000u);
-    const float f = unit_step / now;
-    unit_step = now;
-    per_unit = 1.0f / now;
+  __device__ inline void scale_sums(int ct, int by) {
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct)
+    for (int e = 0; e < kElems; ++e)
 #pragma unroll
-      for (int e = 0; e < kElems; ++e) o[ct][e] *= f;
+      for (int r = 0; r < 4; ++r) o[ct][e][r] = __builtin_amdgcn_ldexpf(o[ct][e][r], by);
   }
+  // The weights so far are 2^-n of what they were: so is the unit, down to 2^-126.
+  __device__ inline void shrink(int ct, int n) {
+    const int e = exponent_of(per_unit[ct]), now = min(e + n, 253);
+    per_unit[ct] = power_of(now);
+    if (__ballot(now < e + n)) scale_sums(ct, now - e - n);
+  }
+  // Room for a weight times step of this size, over the column's lanes.
+  __device__ inline void make_room(int ct, float size) {
+    const float top = across_max(size);
+    const int e = exponent_of(per_unit[ct]);
+    const bool grows = top * per_unit[ct] > kMostWeight && top < __builtin_huge_valf();
+    const int now = grows ? 2 * 127 + kUnitRoom - exponent_of(top) : e;
+    per_unit[ct] = power_of(now);
+    scale_sums(ct, now - e);
+  }
+  __device__ inline float unit(int ct) const { return power_of(254 - exponent_of(per_unit[ct])); }
 
-  template <bool kRaw>
   __device__ inline f32x4 step_of(const float* nums, int t, int kg) const {
-    const f32x4 x = *(const f32x4*)(nums + 64 + 16 * t + 4 * kg);
-    return kRaw ? x * per_unit : x;
+    return *(const f32x4*)(nums + 64 + 16 * t + 4 * kg);
   }
   __device__ inline f32x4 mean_of(const float* nums, int t, int kg) const {
     return *(const f32x4*)(nums + 96 + 16 * t + 4 * kg);
   }
 
   // Weights of 32 keys from their scores' products s.  first: this lane's keys are
-  // first + 0..3 and first + 16 + 0..3.  kRaw: the numbers hold plain steps.
-  template <bool kRaw>
+  // first + 0..3 and first + 16 + 0..3.
   __device__ inline void weigh(const CachedArgs& a, const float* nums, const f32x4 (&s)[2][CT],
                                bool masked, int first, int key_end, f16x8 (&w)[CT]) {
     const int kg = (threadIdx.x & 63) >> 4;
@@ -514,17 +513,16 @@ struct Columns {
       for (int j = 0; j < 8; ++j) top = fmaxf(top, y[j]);
       if (__ballot(top > most[ct])) {
         top = across_max(top);
-        const float over = top > (most[ct] == -INFINITY ? -INFINITY : kRoom) ? top - kRoom : 0.0f;
-        const float f = __builtin_amdgcn_exp2f(-over);
+        // a whole number, and none for columns whose own scores ask for none
+        const bool moves = top > most[ct], first_one = most[ct] == -INFINITY;
+        const float over = moves ? __builtin_ceilf(top) - kRoom : 0.0f;
         ref[ct] += over;
-        if (top > -INFINITY) most[ct] = kRoom + kGrowth;
+        if (moves) most[ct] = kRoom + kGrowth;
         // nothing has been summed where the first reference is taken
-        l[ct] = l[ct] == 0.0f ? 0.0f : l[ct] * f;
-        mean[ct] = mean[ct] == 0.0f ? 0.0f : mean[ct] * f;
-#pragma unroll
-        for (int e = 0; e < kElems; ++e)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) o[ct][e][r] = o[ct][e][r] == 0.0f ? 0.0f : o[ct][e][r] * f;
+        const float f = first_one ? 1.0f : __builtin_amdgcn_exp2f(-over);
+        l[ct] *= f;
+        mean[ct] *= f;
+        shrink(ct, first_one ? 0 : (int)fminf(over, 4096.0f));
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] -= over;
       }
@@ -532,7 +530,7 @@ struct Columns {
       if (!masked) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const f32x4 vmul = step_of<kRaw>(nums, t, kg), vadd = mean_of(nums, t, kg);
+          const f32x4 vmul = step_of(nums, t, kg), vadd = mean_of(nums, t, kg);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             float& z = y[4 * t + r];
@@ -545,7 +543,7 @@ struct Columns {
       } else {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const f32x4 vmul = step_of<kRaw>(nums, t, kg), vadd = mean_of(nums, t, kg);
+          const f32x4 vmul = step_of(nums, t, kg), vadd = mean_of(nums, t, kg);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             float& z = y[4 * t + r];
@@ -558,6 +556,12 @@ struct Columns {
           }
         }
       }
+      float size = fabsf(y[0]);
+#pragma unroll
+      for (int j = 1; j < 8; ++j) size = fmaxf(size, fabsf(y[j]));
+      if (__ballot(size * per_unit[ct] > kMostWeight)) make_room(ct, size);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] *= per_unit[ct];
       w[ct] = __builtin_bit_cast(f16x8, u32x4{pack_f16(y[0], y[1]), pack_f16(y[2], y[3]),
                                               pack_f16(y[4], y[5]), pack_f16(y[6], y[7])});
     }
@@ -629,9 +633,7 @@ __device__ inline void few_columns(const CachedArgs& a, uint32_t block, FewMemor
     Columns<T, kBits, DT, CT, kMode> col;
     col.start(a, w, col0);
     for (; key < key_end; key += kStepKeys) {
-      const float st = tile.seen_step(key), top = larger_step(st, col.unit_step);
-      if (top > 0.0f) col.take_step(top);
-      tile.leave_numbers(nums, lane >= 32 ? st * col.per_unit : st, to_log2);
+      tile.leave_numbers(nums, to_log2);
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -650,7 +652,7 @@ __device__ inline void few_columns(const CachedArgs& a, uint32_t block, FewMemor
       tile.next_keys(key + kStepKeys);
       __builtin_amdgcn_sched_barrier(0);
       f16x8 p[CT];
-      col.template weigh<false>(a, nums, s, key + 32 > all_see || key + 32 > key_end, key + 4 * kg,
+      col.weigh(a, nums, s, key + 32 > all_see || key + 32 > key_end, key + 4 * kg,
                                 key_end, p);
 #pragma unroll
       for (int e = 0; e < kElems; ++e) col.add_values(e, V::operand(tile.v.w, e), p);
@@ -672,7 +674,7 @@ __device__ inline void few_columns(const CachedArgs& a, uint32_t block, FewMemor
       for (int e = 0; e < kElems; ++e)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          s_o[wave][n][V::element(4 * kg + r, e)] = col.o[ct][e][r] * 512.0f * col.unit_step;
+          s_o[wave][n][V::element(4 * kg + r, e)] = col.o[ct][e][r] * 512.0f * col.unit(ct);
       __syncthreads();
       const int c16 = threadIdx.x >> 4, first = (threadIdx.x & 15) * kElems;
       const int c = col0 + 16 * ct + c16;
@@ -708,7 +710,6 @@ template <int DT>
 struct ManyMemory {
   u32x4 k[4][DT / 16][64], v[4][DT / 16][64];
   f32x4 num[4][kNumbers / 4];
-  float top[4];
 };
 template <typename T, int kBits, int DT, int kMode>
 __device__ inline void many_columns(const CachedArgs& a, uint32_t block, ManyMemory<DT>& mem) {
@@ -717,7 +718,6 @@ __device__ inline void many_columns(const CachedArgs& a, uint32_t block, ManyMem
   typedef typename Mat16<T>::V8 V8;
   constexpr int CT = 2, kSteps = DT / 32, kElems = V::kElems;
   auto &s_k = mem.k, &s_v = mem.v;
-  auto& s_top = mem.top;
   const int lane = threadIdx.x & 63, n = lane & 15, kg = lane >> 4;
   const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Work w;
@@ -738,11 +738,9 @@ __device__ inline void many_columns(const CachedArgs& a, uint32_t block, ManyMem
     col.start(a, w, mine);
     for (int base = w.key0; base < key_end; base += kStepKeys) {
       const int own = base + 32 * wave;
-      const float st = tile.seen_step(own), larger = larger_step(st, col.unit_step);
       // all have read the tiles before
       __syncthreads();
-      if (lane == 0) s_top[wave] = own < key_end ? larger : 0.0f;
-      tile.leave_numbers((float*)mem.num[wave], st, to_log2);
+      tile.leave_numbers((float*)mem.num[wave], to_log2);
       tile.load_numbers(own + kStepKeys);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -756,8 +754,6 @@ __device__ inline void many_columns(const CachedArgs& a, uint32_t block, ManyMem
         s_v[wave][e][lane] = __builtin_bit_cast(u32x4, V::operand(tile.v.w, e));
       tile.next_values(own + kStepKeys);
       __syncthreads();
-      const float top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
-      if (top > 0.0f) col.take_step(top);
 #pragma unroll 1
       for (int sub = 0; sub < 4; ++sub) {
         const int key = base + 32 * sub;
@@ -774,8 +770,8 @@ __device__ inline void many_columns(const CachedArgs& a, uint32_t block, ManyMem
             for (int ct = 0; ct < CT; ++ct) s[t][ct] = Mat16<T>::mul(x, col.q[ct][i], s[t][ct]);
           }
         f16x8 p[CT];
-        col.template weigh<true>(a, (const float*)mem.num[sub], s, key + 32 > all_see || key + 32 > key_end,
-                                 key + 4 * kg, key_end, p);
+        col.weigh(a, (const float*)mem.num[sub], s, key + 32 > all_see || key + 32 > key_end,
+                  key + 4 * kg, key_end, p);
 #pragma unroll
         for (int e = 0; e < kElems; ++e)
           col.add_values(e, __builtin_bit_cast(f16x8, s_v[sub][e][lane]), p);
@@ -792,7 +788,7 @@ __device__ inline void many_columns(const CachedArgs& a, uint32_t block, ManyMem
       for (int e = 0; e < kElems; ++e)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          y[V::element(r, e)] = col.o[ct][e][r] * 512.0f * col.unit_step + add;
+          y[V::element(r, e)] = col.o[ct][e][r] * 512.0f * col.unit(ct) + add;
 #pragma unroll
       for (int i = 0; i < DT / 4; i += 8) {
         const int first = kg * (DT / 4) + i;
