@@ -268,10 +268,10 @@ struct ValueRows {
   }
 };
 
-// Weights are 2^(score - reference): up to 2^kRoom when the reference is taken,
-// and it moves only when a score has passed that by kGrowth, so they stay below
-// 2^14.
-constexpr float kRoom = 8.0f, kGrowth = 6.0f;
+// Weights are 2^(score - reference): up to 1 when the reference is taken, and it
+// moves only when a score has passed it by kGrowth, so they stay below 2^6.  Sums of
+// weights times values then end where those of the values alone reach 2^122.
+constexpr float kGrowth = 6.0f;
 
 // Weights times steps become fp16 numbers relative to a unit, a power of two: the
 // largest lies in [2^kUnitRoom, 2 2^kUnitRoom) when the unit is taken, and the unit
@@ -515,9 +515,9 @@ struct Columns {
         top = across_max(top);
         // a whole number, and none for columns whose own scores ask for none
         const bool moves = top > most[ct], first_one = most[ct] == -INFINITY;
-        const float over = moves ? __builtin_ceilf(top) - kRoom : 0.0f;
+        const float over = moves ? __builtin_ceilf(top) : 0.0f;
         ref[ct] += over;
-        if (moves) most[ct] = kRoom + kGrowth;
+        if (moves) most[ct] = kGrowth;
         // nothing has been summed where the first reference is taken
         const float f = first_one ? 1.0f : __builtin_amdgcn_exp2f(-over);
         l[ct] *= f;

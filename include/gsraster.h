@@ -910,8 +910,9 @@ GS_API gs_status gs_cache_read(const gs_cache_config* cfg, const gs_documents* d
  * 16, at most 128; at most 2^20 documents and 2^20 shared ones.  Softmax weights
  * times step are rounded to fp16, relative to a power of two near the largest of
  * the token and head: those below 2^-22 of it lose bits, down to an error of 2^-33
- * of it.  Values are below 2^100.  A key or value that is not seen has no effect,
- * whatever it holds.  Results are the same bits every time. */
+ * of it.  Values are below 2^100, and their sum over a token's keys below 2^120.  A
+ * key or value that is not seen has no effect, whatever it holds.  Results are the
+ * same bits every time. */
 GS_API size_t gs_cached_attention_fwd_workspace_size(const gs_attention_config* cfg, int32_t bits,
                                                      const gs_documents* docs,
                                                      const gs_documents* shared, int64_t rows_q,

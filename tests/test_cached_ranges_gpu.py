@@ -137,3 +137,19 @@ def test_large_steps_with_little_weight(monkeypatch, dtype, bits, dim, own, shar
             _plain_key(c, at + 100 + i, 15.0)
     monkeypatch.setattr(base, "cached_head", _by_weight)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_many_large_values(bits):
+    """2^17 values of 2^99, whose keys' scores rise after the first of each piece: the
+    sum of the values is 2^116, that of the weights is held relative to a score."""
+    n = 1 << 17
+    c = Case(torch.bfloat16, bits, 1, 1, 16, [1], [n])
+    rows = torch.arange(c.k_starts[0], c.k_starts[0] + n, device="cuda")
+    c.q.fill_(1.0)
+    _plain_key(c, rows, torch.where((rows - c.k_starts[0]) % 512 < 128, 0.0, 1.02))
+    c.v.low[:, rows], c.v.step[:, rows] = 2.0 ** 99, 0.0
+    out, _ = c.run()
+    token = out[c.q_starts[0]].double()
+    # fp32 sums of n numbers in chains of a lane each, and the type's rounding
+    assert ((token / 2.0 ** 99 - 1.0).abs() <= 2.0 ** -8 + (n / 128 + 16) * 2.0 ** -24).all()
