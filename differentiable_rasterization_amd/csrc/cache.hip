@@ -76,6 +76,48 @@ __device__ inline float over_lanes(float x, F f) {
   return x;
 }
 
+// Whether code_of may take for ties in a 16-bit head what is only near them.  A quotient's
+// distance from a tie is a multiple of 1 / (2 span) times the unit of the last place
+// of the smallest of x, low and high, and none below 2^-36 is mistaken.  least: twice
+// the bits of a magnitude of the lane's elements and low, less one, at the smallest.
+template <typename T>
+__device__ inline bool near_ties(uint32_t least, float span) {
+  if constexpr (__is_same(T, F16)) return span > 0x1p10f;  // all are multiples of 2^-24
+  // a unit is 2^-8 of the number or more; twice that for span's rounding
+  return span > 0x1p26f * __builtin_bit_cast(float, least >> 1);
+}
+__device__ inline uint32_t twice_bits_less_one(float x) {
+  return (__builtin_bit_cast(uint32_t, x) << 1) - 1;  // a zero comes last
+}
+
+// 0 where code_of(d, inv) has taken d times inv for a tie.
+__device__ inline uint32_t off_tie(double d, double inv) {
+  // the multiples of 2^-36 that it rounds to, in the 36 low bits
+  const uint64_t w = __builtin_bit_cast(uint64_t, d * inv + 0x1.8p16);
+  return (uint32_t)w | (((uint32_t)(w >> 32) ^ 8) & 15);
+}
+
+// a + b = s + e exactly (Knuth's two-sum).
+__device__ inline double two_sum(double a, double b, double& e) {
+  const double s = a + b, t = s - a;
+  e = (a - (s - t)) + (b - t);
+  return s;
+}
+
+// The code of x next to the tie of codes k and k + 1: a head's differences may have
+// more bits than 64-bit numbers, so the sign of
+//   2 levels (x - lo) - (2 k + 1) (hi - lo) = 2 levels x - n hi - (2 levels - n) lo,
+// three exact products, is taken of their exact sum (Shewchuk's expansions).
+__device__ inline int code_at_tie(float x, float lo, float hi, int levels, int k) {
+  const double n = 2 * k + 1, most = 2 * levels;
+  double e0, e1, e2;
+  const double s0 = two_sum(most * (double)x, -n * (double)hi, e0);
+  const double s1 = two_sum(-(most - n) * (double)lo, e0, e1);
+  const double s2 = two_sum(s1, s0, e2);
+  const double sign = s2 != 0.0 ? s2 : e2 != 0.0 ? e2 : e1;
+  return sign > 0.0 ? k + 1 : sign < 0.0 ? k : k + (k & 1);
+}
+
 // A head of a token, of its keys or its values, and where it stands in the cache
 // (row -1: nowhere).
 struct Item {
@@ -85,8 +127,8 @@ struct Item {
 };
 
 // The heads of a workgroup's tokens, kLanes lanes each, kItems of them at a time
-// a lane: take(items, first element).  Its tokens are one unit of a document, or
-// where documents are no longer than one all of a document's.
+// a lane: take(items, first element, the same item by item).  Its tokens are one
+// unit of a document, or where documents are no longer than one all of a document's.
 constexpr int kItems = 4;
 template <int kLanes, typename F>
 __device__ inline void each_heads(const CacheArgs& a, F take) {
@@ -101,77 +143,127 @@ __device__ inline void each_heads(const CacheArgs& a, F take) {
   for (int first = (int)local * kUnit; first < end; first += kUnit) {
     const uint32_t items = (uint32_t)min(kUnit, end - first) * both;
     for (uint32_t base = threadIdx.x / kLanes; base < items; base += kItems * kGroups) {
-      Item item[kItems];
-#pragma unroll
-      for (int p = 0; p < kItems; ++p) {
+      const auto item_of = [&](int p) {
         // what is not there repeats the last, up to what is written
         const uint32_t at = base + p * kGroups, i = min(at, items - 1);
         const int token = first + (int)(i / both), which = (int)(i % both);
         // the document's last tokens are its last keys
         const int key = token + d.kl - d.ql;
-        item[p].here = at < items;
-        item[p].token = d.qs + token;
-        item[p].row = key < 0 ? -1 : d.ks + key;
-        item[p].kv = which >= a.heads;
-        item[p].head = which - (item[p].kv ? a.heads : 0);
-      }
-      take(item, (int)(threadIdx.x % kLanes) * 8);
+        Item o;
+        o.here = at < items;
+        o.token = d.qs + token;
+        o.row = key < 0 ? -1 : d.ks + key;
+        o.kv = which >= a.heads;
+        o.head = which - (o.kv ? a.heads : 0);
+        return o;
+      };
+      Item item[kItems];
+#pragma unroll
+      for (int p = 0; p < kItems; ++p) item[p] = item_of(p);
+      take(item, (int)(threadIdx.x % kLanes) * 8, item_of);
     }
   }
 }
 
+// Eight elements of an item; a lane past the head's end repeats its first ones.
+template <typename T>
+__device__ inline void load_item(const CacheArgs& a, const Item& t, int e, float (&x)[8]) {
+  load_elems((const T*)a.x[t.kv] + t.token * a.x_row[t.kv] + t.head * a.x_head[t.kv] +
+                 (e < a.dim ? e : 0),
+             x);
+}
+template <int kBits>
+__device__ inline void store_item(const CacheArgs& a, const Item& t, int e, const int (&u)[8]) {
+  // a token without a key is not written
+  if (e < a.dim && t.here && t.row >= 0)
+    store_codes<kBits>(a.codes[t.kv] + t.row * a.row[t.kv] + t.head * a.head[t.kv] + e * kBits / 8,
+                       u);
+}
+
+// A head's smallest and largest element, from its lanes' eight.  One with an infinity
+// or a NaN, or too wide for fp32, is wrong: it has no codes.
+template <int kLanes, int kLevels>
+struct Range {
+  float lo, hi;
+  double span, inv;
+  bool wrong, none;
+  __device__ inline explicit Range(const float (&x)[8]) {
+    lo = hi = x[0];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo = fminf(lo, x[i]);
+      hi = fmaxf(hi, x[i]);
+      bad = bad || x[i] != x[i];
+    }
+    if (bad) hi = __builtin_huge_valf();
+    lo = over_lanes<kLanes>(lo, [](float y, float z) { return fminf(y, z); });
+    hi = over_lanes<kLanes>(hi, [](float y, float z) { return fmaxf(y, z); });
+    wrong = !(hi - lo < 0x1p127f);
+    span = (double)hi - (double)lo;
+    none = span < (double)kLeastSpan;
+    inv = none || wrong ? 0.0 : (double)kLevels / span;
+  }
+};
+
 template <typename T, int kBits, int kLanes>
 __global__ void __launch_bounds__(256) cache_write_kernel(CacheArgs a) {
-  constexpr float kLevels = kBits == 8 ? 255.0f : 15.0f;
-  each_heads<kLanes>(a, [&](const Item (&item)[kItems], int e) {
-    // a lane past the head's end repeats its first elements
-    const bool mine = e < a.dim;
+  constexpr int kLevels = kBits == 8 ? 255 : 15;
+  each_heads<kLanes>(a, [&](const Item (&item)[kItems], int e, const auto& item_of) {
     float x[kItems][8];
 #pragma unroll
-    for (int p = 0; p < kItems; ++p)
-      load_elems((const T*)a.x[item[p].kv] + item[p].token * a.x_row[item[p].kv] +
-                     item[p].head * a.x_head[item[p].kv] + (mine ? e : 0),
-                 x[p]);
+    for (int p = 0; p < kItems; ++p) load_item<T>(a, item[p], e, x[p]);
+    bool tie = false;
+    uint32_t off = 1;
 #pragma unroll
     for (int p = 0; p < kItems; ++p) {
       const int kv = item[p].kv;
-      float lo = x[p][0], hi = x[p][0];
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[p][i]);
-        hi = fmaxf(hi, x[p][i]);
-        bad = bad || x[p][i] != x[p][i];
-      }
-      if (bad) hi = __builtin_huge_valf();
-      lo = over_lanes<kLanes>(lo, [](float y, float z) { return fminf(y, z); });
-      hi = over_lanes<kLanes>(hi, [](float y, float z) { return fmaxf(y, z); });
-      // a head with an infinity or a NaN, or too wide for fp32, has no codes
-      const bool wrong = !(hi - lo < 0x1p127f);
-      const double span = (double)hi - (double)lo;
-      const bool none = span < (double)kLeastSpan;
-      const double inv = none || wrong ? 0.0 : (double)kLevels / span;
+      const Range<kLanes, kLevels> r(x[p]);
+      uint32_t least = twice_bits_less_one(r.lo);
       int u[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = wrong ? 0 : code_of((double)x[p][i] - (double)lo, inv);
-      // a token without a key is not written
-      const bool written = item[p].here && item[p].row >= 0;
-      if (mine && written)
-        store_codes<kBits>(
-            a.codes[kv] + item[p].row * a.row[kv] + item[p].head * a.head[kv] + e * kBits / 8, u);
-      if (e == 0 && written) {
+      for (int i = 0; i < 8; ++i) {
+        const double d = (double)x[p][i] - (double)r.lo;
+        u[i] = r.wrong ? 0 : code_of(d, r.inv);
+        // elements of fp32 are often small enough for near ties, which are then looked for
+        if constexpr (__is_same(T, float)) off = min(off, off_tie(d, r.inv));
+        else least = min(least, twice_bits_less_one(x[p][i]));
+      }
+      if constexpr (!__is_same(T, float)) tie = tie || near_ties<T>(least, r.hi - r.lo);
+      store_item<kBits>(a, item[p], e, u);
+      if (e == 0 && item[p].here && item[p].row >= 0) {
         const float nan = __builtin_nanf("");
         const int64_t at = item[p].head * a.ld[kv] + item[p].row;
-        a.low[kv][at] = wrong ? nan : lo;
-        a.step[kv][at] = wrong ? nan : none ? 0.0f : (float)(span / (double)kLevels);
+        a.low[kv][at] = r.wrong ? nan : r.lo;
+        a.step[kv][at] = r.wrong ? nan : r.none ? 0.0f : (float)(r.span / (double)kLevels);
       }
+    }
+    // Ties that may be none are rare: the wavefront's codes again, item by item, with
+    // each of them decided (held beside the others it would cost a third of the
+    // wavefronts, 40 us for 35).
+    if (!__ballot(tie || off == 0)) return;
+#pragma unroll 1
+    for (int p = 0; p < kItems; ++p) {
+      const Item t = item_of(p);
+      float y[8];
+      load_item<T>(a, t, e, y);
+      const Range<kLanes, kLevels> r(y);
+      int u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double d = (double)y[i] - (double)r.lo;
+        u[i] = r.wrong ? 0 : code_of(d, r.inv);
+        if (!r.wrong && off_tie(d, r.inv) == 0)
+          u[i] = code_at_tie(y[i], r.lo, r.hi, kLevels, (int)(d * r.inv));
+      }
+      store_item<kBits>(a, t, e, u);
     }
   });
 }
 
 template <typename T, int kBits, int kLanes>
 __global__ void __launch_bounds__(256) cache_read_kernel(CacheArgs a) {
-  each_heads<kLanes>(a, [&](const Item (&item)[kItems], int e) {
+  each_heads<kLanes>(a, [&](const Item (&item)[kItems], int e, const auto&) {
     if (e >= a.dim) return;
     float lo[kItems], step[kItems];
     int u[kItems][8] = {};

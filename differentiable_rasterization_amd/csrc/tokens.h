@@ -239,7 +239,8 @@ constexpr float kLeastSpan = 0x1p-116f;
 // inv is a quotient levels / span.  The product is off by 2^-45 at most, while
 // levels x / span of 24-bit x and span of like exponents is a tie or 2^-33 away
 // from one: rounded to multiples of 2^-36 first (adding and taking away 1.5
-// 2^16), ties are ties.  Adding 1.5 2^52 leaves the whole number in the low word.
+// 2^16), ties are ties.  (Of an x with more bits, what is within 2^-37 of a tie
+// counts as one.)  Adding 1.5 2^52 leaves the whole number in the low word.
 __device__ inline int code_of(double x, double inv) {
   const double v = (x * inv + 0x1.8p16) - 0x1.8p16;
   return (int)(uint32_t)__builtin_bit_cast(uint64_t, v + 0x1.8p52);
