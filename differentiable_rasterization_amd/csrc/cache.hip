@@ -5,6 +5,8 @@
 // the (2^bits - 1)-th part of its span; codes are to nearest, formed in 64 bits.
 // In 4 bits a 32-bit word holds eight elements, 2i in bits 4i and 2i + 1 in bits
 // 16 + 4i: a shift and a mask then give two elements in the halves of a word.
+// A quotient next to a tie of codes, which 64 bits may not tell from one, is decided
+// by an exact sum.
 //
 // Eight elements a lane (16 bytes of a 16-bit type, 8 or 4 of codes), 8 or 16 lanes
 // a head, keys and values in one launch.  20,011 tokens of 8 heads of 64, fp16 to 4
@@ -78,8 +80,9 @@ __device__ inline float over_lanes(float x, F f) {
 
 // Whether code_of may take for ties in a 16-bit head what is only near them.  A quotient's
 // distance from a tie is a multiple of 1 / (2 span) times the unit of the last place
-// of the smallest of x, low and high, and none below 2^-36 is mistaken.  least: twice
-// the bits of a magnitude of the lane's elements and low, less one, at the smallest.
+// of the smallest of x, low and high, and none of 2^-36 or more is mistaken.  least:
+// twice the bits of a magnitude less one, of a lane's smallest element: the whole
+// wavefront acts on it, also for the lanes that do not have low or high.
 template <typename T>
 __device__ inline bool near_ties(uint32_t least, float span) {
   if constexpr (__is_same(T, F16)) return span > 0x1p10f;  // all are multiples of 2^-24
@@ -199,8 +202,8 @@ struct Range {
     if (bad) hi = __builtin_huge_valf();
     lo = over_lanes<kLanes>(lo, [](float y, float z) { return fminf(y, z); });
     hi = over_lanes<kLanes>(hi, [](float y, float z) { return fmaxf(y, z); });
-    wrong = !(hi - lo < 0x1p127f);
     span = (double)hi - (double)lo;
+    wrong = !(span < 0x1p127);
     none = span < (double)kLeastSpan;
     inv = none || wrong ? 0.0 : (double)kLevels / span;
   }
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(256) cache_write_kernel(CacheArgs a) {
     for (int p = 0; p < kItems; ++p) {
       const int kv = item[p].kv;
       const Range<kLanes, kLevels> r(x[p]);
-      uint32_t least = twice_bits_less_one(r.lo);
+      uint32_t least = 0xffffffffu;
       int u[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {

@@ -74,3 +74,23 @@ def test_random_heads_of_wide_range(dtype, bits):
     want = torch.tensor([_exact(h, bits) for h in x.double().tolist()])
     cache = _write(x.cuda()[:, None], bits)[0]
     assert torch.equal(cache.codes[:, 0].cpu(), pack(want, bits).view(len(x), -1))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_the_widest_heads(bits):
+    """Spans next to 2^127: below it codes, also where fp32 rounds the span to it."""
+    top = 2.0 ** 126
+    below = top - 2.0 ** 102                                   # the next fp32 number
+    x = torch.randn((3, 1, 16), generator=torch.Generator().manual_seed(bits)) * 2.0 ** 120
+    x[0, 0, 3], x[0, 0, 7] = top, -below
+    x[1, 0, 3], x[1, 0, 7] = top, -top
+    x[2, 0, 3], x[2, 0, 7] = below, -below
+    cache = _write(x.cuda(), bits)[0]
+    want = torch.tensor([_exact(x[i, 0].double().tolist(), bits) if i != 1 else [0] * 16
+                         for i in range(3)])
+    assert torch.equal(cache.codes[:, 0].cpu(), pack(want, bits).view(3, -1))
+    assert torch.isnan(cache.low[0, 1]) and torch.isnan(cache.step[0, 1])
+    for i in (0, 2):
+        span = x[i].double().max() - x[i].double().min()
+        assert float(cache.low[0, i]) == -below
+        assert float(cache.step[0, i]) == float((span / (2 ** bits - 1)).float())
