@@ -60,8 +60,17 @@ def source_hash() -> str:
     return h.hexdigest()
 
 
+def jobs() -> int:
+    """Compilers at a time: eight, or MAX_JOBS where it is a smaller positive number."""
+    try:
+        most = int(os.environ.get("MAX_JOBS", ""))
+    except ValueError:
+        most = 0
+    return min(8, most) if most > 0 else 8
+
+
 def build(verbose: bool = False) -> str:
-    """Each source in a compiler of its own, up to eight at a time, the longest first."""
+    """Each source in a compiler of its own, jobs() at a time, the longest first."""
     tmp = LIB + ".tmp%d" % os.getpid()
 
     def run(cmd):
@@ -76,7 +85,7 @@ def build(verbose: bool = False) -> str:
         paths = sorted((os.path.join(CSRC, s) for s in SOURCES), key=os.path.getsize, reverse=True)
         objects = [os.path.join(there, os.path.basename(p) + ".o") for p in paths]
         compile_flags = [f for f in flags() if f != "-shared"]
-        with ThreadPoolExecutor(min(8, int(os.environ.get("MAX_JOBS") or 8))) as pool:
+        with ThreadPoolExecutor(jobs()) as pool:
             list(pool.map(lambda at: run([hipcc()] + compile_flags + ["-c", at[0], "-o", at[1]]),
                           zip(paths, objects)))
         run([hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC"] + objects + ["-o", tmp])
