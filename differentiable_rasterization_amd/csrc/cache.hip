@@ -10,9 +10,10 @@
 //
 // Eight elements a lane (16 bytes of a 16-bit type, 8 or 4 of codes), 8 or 16 lanes
 // a head, keys and values in one launch.  20,011 tokens of 8 heads of 64, fp16 to 4
-// bits: written in 22 us, where the codes' 64-bit arithmetic (half of about 1,000
-// vector instructions a wavefront) and the reading of 41 MB weigh alike, read back in
-// 15 (54 MB, 3.6 TB/s).  A few tokens: a launch, 4 to 5 us.
+// bits: 54 MB written in 22 us, with vector instructions issued in 60% of the cycles
+// (1,030 a wavefront, 300 of them 64-bit ones of the codes; places, strides and
+// packing are most), and read back in 15 (3.6 TB/s; 690, of which 110 make the
+// numbers).  A few tokens: a launch, 4 to 5 us.
 #include "cached.h"
 
 namespace gs {

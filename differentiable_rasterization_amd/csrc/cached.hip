@@ -26,12 +26,13 @@
 // token's pieces and those of the keys it shares.
 //
 // What bounds it.  One token a request: reading the codes (four caches of 120,001
-// keys in all, 4 heads of 128 in 8 bits: 131 MB in 38.5 us, 3.4 TB/s, and 5 for the
+// keys in all, 4 heads of 128 in 8 bits: 131 MB in 37.6 us, 3.5 TB/s, and 5 for the
 // join; a large sum that only reads has 3.9).  Many columns: vector instructions and
 // matrix products of two wavefronts a SIMD that overlap little (1,024 tokens over
-// 32,768 keys, 16 heads of 128 over 4: 400 us, 0.68 PFLOP/s; vector issue in 51% of
-// the cycles, matrix unit at work in 27).  Small calls: two launches and a chain of
-// dependent loads (document, codes, pieces), about 15 us.
+// 32,768 keys, 16 heads of 128 over 4: 416 us, 0.65 PFLOP/s, up to 20% more in the
+// first 50 calls after a pause; vector issue in 52% of the cycles, matrix unit at work
+// in 26).  Small calls: two launches and a chain of dependent loads (document, codes,
+// pieces), about 15 us.
 #include "cached.h"
 
 namespace gs {
@@ -815,8 +816,8 @@ __global__ void __launch_bounds__(256, 2) cached_many_kernel(CachedArgs a) {
 }
 
 // Both passes in one launch, the shared keys' workgroups first: those of either hide
-// what the other waits for (us with two launches : with one; 64 requests behind 16,384
-// keys 52.9 : 44.1, 48 behind three prompts 30.0 : 22.2).
+// what the other waits for (us with two launches : with one, caches from memory; 64
+// requests behind 16,384 keys 54.5 : 48.0, 48 behind three prompts 31.0 : 22.6).
 template <typename T, int kBits, int DT, int kMode>
 __global__ void __launch_bounds__(256, 2) cached_both_kernel(CachedArgs own, CachedArgs shared) {
   __shared__ __align__(16) union {
@@ -954,29 +955,30 @@ Cut cut_of(const gs_attention_config& cfg, const gs_documents& d, int64_t rows_q
   const int64_t group = cfg.heads_q / cfg.heads_k;
   const int64_t longest_q = d.max_q_len > 0 && d.max_q_len < rows_q ? d.max_q_len : rows_q;
   const int64_t longest_k = d.max_k_len > 0 && d.max_k_len < rows_k ? d.max_k_len : rows_k;
-  // The form for many columns pays from more than 128 on (us, it : 32 columns; 100
-  // tokens of eight requests, 16 heads of 128 over 4, up to 128 columns 58 : 30; 500
-  // of 16 requests, 8 heads of 64 over 4, 39 : 41; 1,024 of one request 399 : 504).
+  // The form for many columns pays where documents have several times 128 (us, it : 32
+  // columns; 1,024 tokens of one request, 16 heads of 128 over 4, 417 : 465), not up to
+  // 128 (100 tokens of eight requests 91 : 31), and not yet just past that (500 of 16
+  // requests, 8 heads of 64 over 4, 47 : 36).
   o.width = longest_q * group <= 16 ? 16 : longest_q * group <= 128 ? 32 : kManyCols;
   o.looked_up = longest_q * group > o.width;
   o.units = o.looked_up ? rows_q * group / o.width + d.count : d.count;
   // units that have work: documents end inside one, half way on average
   const int64_t busy = o.looked_up ? rows_q * group / o.width + (d.count + 1) / 2 : d.count;
   const int64_t base = (busy > 0 ? busy : 1) * cfg.heads_k;
-  // Workgroups wanted.  16 columns: two a compute unit where there are few documents
-  // (four caches of 120,001 keys in all: 45, 47, 50, 57 us with 512, 768, 1,024,
-  // 2,048), more where many of uneven length hide each other's ends (64 caches of
-  // 100,003 keys, 8 heads of 64 in 4 bits: 40, 35, 34, 32).  32 columns: in between
-  // (24 requests of a few tokens, 30,011 keys: 26, 24, 23, 27 with 256, 512, 704,
-  // 1,024).  Many: what the chip holds at a time (the 1,024 tokens: 752, 400, 480, 416
-  // with 256, 512, 768, 1,024).
+  // Workgroups wanted (all figures with caches from memory).  16 columns: two a compute
+  // unit where there are few documents (four caches of 120,001 keys in all: 43, 46, 48,
+  // 49 us with 512, 768, 1,024, 1,536), more where many of uneven length hide each
+  // other's ends (64 caches of 100,003 keys, 8 heads of 64 in 4 bits: 40, 40, 40, 37, and
+  // 35 with 2,048).  32 columns: in between (24 requests of a few tokens, 30,011 keys:
+  // 26, 24, 23, 27 with 256, 512, 704, 1,024).  Many: what the chip holds at a time (the
+  // 1,024 tokens: 788, 417, 497, 429 with 256, 512, 768, 1,024).
   const int64_t target = o.width == 16 ? (base >= 256 ? 1536 : 512) : o.width == 32 ? 704 : 512;
   int64_t pieces = (target + base - 1) / base;
   if (pieces > kMostPieces) pieces = kMostPieces;
   // Where the caller says how long documents are, all pieces have that share of the
   // longest.  Up to 2,048 keys, since documents of uneven length need pieces that
-  // end together (64 caches of 524,288 keys in all: 228 us uncut, 136, 121, 124, 137
-  // with 4,096, 2,048, 1,024, 512).
+  // end together (64 caches of 524,288 keys in all: 137 us without that limit, 123,
+  // 114, 114, 123 with 4,096, 2,048, 1,024, 512).
   int64_t piece = 2 * kStepKeys;
   if (d.max_k_len > 0) {
     piece = (longest_k + pieces - 1) / pieces;

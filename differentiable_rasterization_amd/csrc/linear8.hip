@@ -9,9 +9,12 @@
 // border of two codes into either.
 //
 // What bounds it.  Few rows: reading the weights, and one launch or two.  Many: the
-// matrix unit, at work in 56% of the cycles, at 1.7 GHz under this load (16,384 rows of 4,096 by 8,192 in
-// 540 to 570 us, 1.9 to 2.0 POP/s, 50 us of it the codes; the products alone, without
-// loads or results, take 445).
+// matrix unit, at work in 56% of the cycles, at 1.7 to 1.9 GHz under this load (16,384 rows
+// of 4,096 by 8,192 in 550 to 562 us, 2.0 POP/s, 50 us of it the codes; the products
+// alone, without loads or results, take 445).
+//
+// The figures beside the rules below: bf16 with a bias, calls captured in a graph
+// over weights and rows of 600 MB that take turns, so that none come from a cache.
 #include "tokens.h"
 
 namespace gs {
@@ -120,11 +123,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(int64_t rows, int ch
 // memory straight into the operands of the 16x16x64 instruction (rows lane %
 // 16, 16 inputs a lane), and the wavefronts' sums meet in LDS.  Weights of
 // the first kAheadOfAll steps are on their way before anything else is looked at:
-// 16.8 MB of them, one row of 2,048 by 8,192, take 6.1 us with the call (2.8 TB/s; a
-// launch alone is about 3).
+// 16.8 MB of them, one row of 2,048 by 8,192, take 7.1 us (2.4 TB/s; a launch alone
+// is about 3), 6.2 where a few such calls take turns.
 // 16 wavefronts where there is a workgroup a compute unit or less, 8 where there
-// are more (us, 16 : 8; one row of 4,096 by 4,096 7.2 : 8.3, of 2,048 by 8,192
-// 9.2 : 8.6).
+// are more (us, 16 : 8; one row of 4,096 by 4,096 7.4 : 7.6, of 2,048 by 8,192
+// 9.5 : 7.1).
 //
 // kOwn: rows are brought to codes here, by every workgroup for itself while its
 // weights are on their way, which saves a launch: up to eight rows of at most
@@ -490,9 +493,10 @@ hipError_t many(LinearArgs a, hipStream_t s) {
 
 // Whether workgroups bring the rows to codes themselves: where that is little work
 // for all of them together (us with a launch for the codes : without; inputs by
-// outputs): one row of 4,096 by 4,096 10.6 : 7.6, of 16,384 by 4,096 25.0 : 17.0;
-// four of 4,096 by 4,096 10.0 : 8.7; eight of 1,024 by 1,024 10.4 : 7.5, of 4,096 by
-// 4,096 10.7 : 11.0, of 2,048 by 8,192 10.9 : 12.4.
+// outputs): one row of 4,096 by 4,096 9.8 : 7.3, of 16,384 by 4,096 26.3 : 18.9;
+// four of 4,096 by 4,096 10.3 : 9.0; eight of 1,024 by 1,024 6.1 : 4.7.  The limit is
+// where the two meet with weights from a cache (eight of 4,096 by 4,096 10.7 : 11.0, of
+// 2,048 by 8,192 10.9 : 12.4); from memory 10.8 : 10.7 and 12.2 : 10.1.
 bool own_codes(int64_t rows, int64_t inputs, int64_t outputs) {
   const int64_t shares = rows <= 2 ? rows : rows <= 4 ? 4 : 8;
   return rows <= 8 && shares * inputs <= (outputs <= kOutputsOf16 ? kOwnElems<16> : kOwnElems<8>) &&
@@ -507,26 +511,26 @@ hipError_t linear(const LinearArgs& a, hipStream_t s) {
   const auto tiles = [&](int64_t tall, int64_t wide) {
     return ((a.rows + tall - 1) / tall) * ((a.outputs + wide - 1) / wide);
   };
-  // us, few rows : tiles of 64 x 32 outputs: 16 rows of 8,192 by 2,048 14.0 : 15.4, of
-  // 4,096 by 4,096 11.4 : 11.3; with more outputs or rows every workgroup's reading
-  // of all rows weighs more (16 of 8,192 by 8,192 22.2 : 17.8, 33 of 4,096 by 4,096
-  // with three such groups of rows 13.4 : 11.7).
+  // us, few rows : tiles of 64 x 32 outputs: 16 rows of 8,192 by 2,048 15.7 : 18.3, of
+  // 4,096 by 4,096 11.7 : 13.3; with more outputs every workgroup's reading of all
+  // rows weighs more (16 of 8,192 by 8,192 26.5 : 21.7).
   if (a.rows <= 16 && of16) return few<T, 16, false>(a, s);
   // Small tiles while all run at a time and wait for memory and for each other's
   // steps: the steps shared by four groups of wavefronts, by two, by none (us of the
-  // three: 64 rows of 4,096 by 4,096 11.8, 12.9, 14.5; 200 of them 17.8, 13.3, 14.8;
-  // 1,024 of 2,048 by 2,048 24.3, 17.3, 14.6).
+  // three: 64 rows of 4,096 by 4,096 15.1, 17.2, 19.4; 200 of them 20.5, 15.9, 19.3;
+  // 1,024 of 2,048 by 2,048 28.6, 20.6, 17.7).
   if (tiles(64, 32) <= kUnits) return many<T, 64, 32, 2, 1, 3, 4>(a, s);
   if (tiles(64, 64) <= kUnits) return many<T, 64, 64, 2, 2, 3, 2>(a, s);
   if (tiles(64, 64) <= 2 * kUnits) return many<T, 64, 64, 2, 2, 3>(a, s);
   // A tile a compute unit: two steps on their way, or two workgroups with one each
-  // (2,048 by 2,048 20.5 : 21.6; with more tiles, 4,096 by 2,048, 33.3 : 30.3).
+  // (2,048 rows of 2,048 by 2,048 21.7 : 25.3; with more tiles, 4,096 such rows,
+  // 37.1 : 33.5).
   const int64_t n128 = tiles(128, 128);
   if (n128 <= kUnits) return many<T, 128, 128, 2, 2, 3>(a, s);
   // Else the form whose last tiles end first: a unit takes about 10, 25 and 32 us
   // for a tile of 128 x 128, 192 x 256 and 256 x 256 with 2,048 inputs (us of the
-  // three: 1,024 by 8,192 28.4, 30.5, 34.3; 1,500 by 8,192 38.6, 34.3, 36.7; 4,096 by
-  // 4,096 48.4, 55.8, 44.6; 9,000 by 4,096 109, 99, 112).
+  // three, rows by outputs: 1,024 by 8,192 30.5, 34.4, 39.4; 1,500 by 8,192 47.3, 37.3,
+  // 40.1; 4,096 by 4,096 55.4, 57.5, 46.5; 9,000 by 4,096 108, 101, 107).
   const auto turns = [](int64_t n) { return (n + kUnits - 1) / kUnits; };
   const int64_t t128 = 10 * turns(n128), t192 = 25 * turns(tiles(192, 256)),
                 t256 = 32 * turns(tiles(256, 256));

@@ -11,7 +11,10 @@ cached and the scan's state carried on.  ``Served`` is the layer as it is served
 8 bits: its products' weights and its cache are kept in 8 (the cache also in 4)
 bits, and a prompt that all requests share is in the cache once.
 
-    python examples/token_splats.py [steps]
+    python examples/token_splats.py [steps]      trains a layer
+
+A program that serves makes a ``Served`` of the trained layer, gives it the prompt
+with ``take_prompt`` and asks it for a token of every request with ``step``.
 
 In training the matrix products are torch's; everything else on the tokens is the
 library's, in serving in 8 bits its products too.
